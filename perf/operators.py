@@ -139,7 +139,8 @@ def _inputs_project(c, g):
     # weights in 8 bits with a scale for each output channel; the products come out near one
     wq = torch.randint(-127, 128, (N, D), generator=g, device="cuda", dtype=torch.int8)
     wscale = (0.5 + _rand(g, N)) / (127.0 * math.sqrt(D))
-    st = dict(wq=wq, wscale=wscale, y=e(T, N))
+    st = dict(wq=wq, wscale=wscale, y=e(T, N),
+              status=torch.zeros(1, dtype=torch.int32, device="cuda"))
     if c["kind"] == "project":
         st |= dict(x=_randn(g, T, D, dtype=dt), res=_hidden(g, T, D, dt),
                    w=1.0 + _randn(g, D, scale=0.1), s=e(T, D), q=e(T, D, d=torch.int8),
@@ -166,7 +167,7 @@ def _inputs_distill(c, g):
         weight = torch.where(_rand(g, T) < 0.125, torch.zeros_like(weight), weight)
     f = lambda *s: torch.empty(*s, dtype=torch.float32, device="cuda")  # noqa: E731
     return dict(z=z, ids=ids.contiguous(), teacher=teacher, weight=weight, tau=2.0,
-                loss=f(T), lse=f(T), dz=torch.empty_like(z),
+                loss=f(T), stats=f(T, 2), dz=torch.empty_like(z),
                 status=torch.zeros(1, dtype=torch.int32, device="cuda"))
 
 
@@ -230,10 +231,10 @@ def _plain_project(st):
 
 def _plain_distill(st):
     tau, ids = st["tau"], st["ids"].long()
-    z = st["z"].float() / tau
+    z = st["z"].float()
     top = z.amax(dim=1, keepdim=True)
-    e = torch.exp(z - top)
-    lse = top + torch.log(e.sum(dim=1, keepdim=True))
+    z = (z - top) / tau
+    lse = torch.log(torch.exp(z).sum(dim=1, keepdim=True))
     live, on = ids >= 0, st["weight"] != 0
     at = torch.where(live, ids, torch.zeros_like(ids))
     t = torch.where(live, st["teacher"] / tau, torch.full_like(st["teacher"], -math.inf))
@@ -247,8 +248,8 @@ def _plain_distill(st):
     loss = st["weight"] * tau * tau * kl
     g = torch.where(any_, st["weight"][:, None], torch.zeros_like(lse))
     dz = torch.exp(z - lse).scatter_add_(1, at, -p) * (tau * g)
-    return {"loss": loss, "lse": torch.where(on, lse[:, 0], torch.zeros_like(loss)),
-            "dz": dz.to(st["z"].dtype)}
+    stats = torch.cat([top, lse], dim=1) * on[:, None]
+    return {"loss": loss, "stats": stats, "dz": dz.to(st["z"].dtype)}
 
 
 PLAIN = {"embed": _plain_embed, "norm": _plain_norm, "project": _plain_project,
@@ -305,7 +306,7 @@ def _own_project(tw, st):
                                      st["q"], st["qscale"], None)
         out["s"] = st["s"]
     tw.twell_q8_matmul(st["q"], st["qscale"], st["wq"], st["wscale"], st.get("bias"), T, N, D, dt,
-                       st["y"], ws, st["nws"])
+                       st["y"], st["status"], ws, st["nws"])
     out["y"] = st["y"]
     return out
 
@@ -315,12 +316,12 @@ def _own_distill(tw, st):
     dt = tw.TWELL_BF16 if c["dtype"] == "bf16" else tw.TWELL_F32
     T, V, k = c["T"], c["V"], c["k"]
     tw.twell_distill_forward(st["z"], V, st["ids"], st["teacher"], st["weight"], T, V, k, dt,
-                             st["tau"], st["loss"], st["lse"], st["dz"] if c["fused"] else None,
+                             st["tau"], st["loss"], st["stats"], st["dz"] if c["fused"] else None,
                              st["status"])
     if not c["fused"]:
-        tw.twell_distill_backward(st["z"], V, st["ids"], st["teacher"], st["lse"], st["weight"], T,
-                                  V, k, dt, st["tau"], st["dz"], st["status"])
-    return {"loss": st["loss"], "lse": st["lse"], "dz": st["dz"]}
+        tw.twell_distill_backward(st["z"], V, st["ids"], st["teacher"], st["stats"], st["weight"],
+                                  T, V, k, dt, st["tau"], st["dz"], st["status"])
+    return {"loss": st["loss"], "stats": st["stats"], "dz": st["dz"]}
 
 
 OWN = {"embed": _own_embed, "norm": _own_norm, "project": _own_project, "q8": _own_project,
@@ -355,7 +356,7 @@ def work(case):
     V, k = c["V"], c["k"]
     live = 0.875 if c["masked"] else 1.0  # masked rows are not read
     reads = 1 if c["fused"] else 2        # as two calls the logits are read by each
-    return {"bytes": T * V * es * (live * reads + 1) + T * k * 8 * reads + 12 * T,
+    return {"bytes": T * V * es * (live * reads + 1) + T * k * 8 * reads + 16 * T,
             "flops": 8 * T * V}
 
 
@@ -416,9 +417,11 @@ def _exact_project(st):
 
 def _exact_distill(st):
     tau = st["tau"]
-    loss, lse, dz = [], [], []
+    loss, stats, dz = [], [], []
     for r in range(0, st["z"].shape[0], 1024):
-        z = st["z"][r:r + 1024].double() / tau
+        z = st["z"][r:r + 1024].double()
+        top = z.max(1).values
+        z /= tau
         w = st["weight"][r:r + 1024].double()
         ids = st["ids"][r:r + 1024].long()
         t = (st["teacher"][r:r + 1024].double() / tau).masked_fill(ids < 0, -math.inf)
@@ -430,9 +433,10 @@ def _exact_distill(st):
         has = (ids >= 0).any(1).double()
         logq = z.gather(1, ids.clamp_min(0)) - total[:, None]
         loss.append(w * tau * tau * torch.where(p > 0, p * (logp - logq), 0.0).sum(1))
-        lse.append(torch.where(w != 0, total, 0.0))
+        both = torch.stack([top, total - top / tau], dim=1)
+        stats.append(torch.where(w[:, None] != 0, both, 0.0))
         dz.append((w * has * tau)[:, None] * (torch.softmax(z, dim=1) - full))
-    return {"loss": torch.cat(loss), "lse": torch.cat(lse), "dz": torch.cat(dz)}
+    return {"loss": torch.cat(loss), "stats": torch.cat(stats), "dz": torch.cat(dz)}
 
 
 EXACT = {"embed": _exact_embed, "norm": _exact_norm, "project": _exact_project,
