@@ -11,7 +11,9 @@ Names follow the ABI: ``twell_workspace_size``, ``twell_pack_dense``,
 ``twell_get_status``, and the row-ELL comparison baseline
 ``twell_rowell_pack_dense`` / ``twell_rowell_forward``.  ``TwellBuffers`` and
 ``RowEllBuffers`` allocate the device buffers of a ``twell_t`` /
-``twell_rowell_t`` with torch.
+``twell_rowell_t`` with torch.  The operators around the FFN (embedding,
+residual norm, 8-bit product, distillation loss; include/twell_lm.h) are in
+``lm`` and available under the same names here.
 """
 from __future__ import annotations
 
@@ -35,6 +37,13 @@ TWELL_F32, TWELL_BF16 = 0, 1
 EXPORTS = ("twell_workspace_size", "twell_workspace_size_rows", "twell_pack_dense", "twell_pack",
            "twell_ffn_forward", "twell_ffn_backward", "twell_get_status", "twell_version",
            "twell_rowell_pack_dense", "twell_rowell_forward")
+# include/twell_lm.h (see __getattr__)
+LM_EXPORTS = ("twell_read_status", "twell_embed_forward", "twell_embed_backward",
+              "twell_embed_workspace_size", "twell_add_rmsnorm_forward",
+              "twell_add_rmsnorm_backward", "twell_add_rmsnorm_workspace_size",
+              "twell_q8_quantize", "twell_q8_matmul", "twell_q8_workspace_size",
+              "twell_distill_forward", "twell_distill_backward")
+EXPORTS += LM_EXPORTS
 
 
 class TwellError(RuntimeError):
@@ -97,9 +106,33 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     for name in ("twell_pack_dense", "twell_pack", "twell_ffn_forward", "twell_ffn_backward",
                  "twell_get_status", "twell_rowell_pack_dense", "twell_rowell_forward"):
         getattr(lib, name).restype = I
+    _declare_lm(lib)
     if path is None:
         _lib = lib
     return lib
+
+
+def _declare_lm(lib) -> None:
+    """Signatures of include/twell_lm.h."""
+    P, I, L, F32, S = (ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float,
+                       ctypes.c_size_t)
+    for name, args in (
+            ("twell_read_status", [P, P]),
+            ("twell_embed_forward", [P, I, P, I, I, I, I, F32, L, P, P, P]),
+            ("twell_embed_backward", [P, I, P, I, I, I, I, F32, L, P, P, P, S, P]),
+            ("twell_add_rmsnorm_forward", [P, P, P, I, I, I, F32, P, P, P, P, P, P]),
+            ("twell_add_rmsnorm_backward", [P, P, P, P, P, I, I, I, P, P, P, S, P]),
+            ("twell_q8_quantize", [P, I, I, I, P, P, P]),
+            ("twell_q8_matmul", [P, P, P, P, P, I, I, I, I, P, P, P, S, P]),
+            ("twell_distill_forward", [P, L, P, P, P, I, I, I, I, F32, P, P, P, P, P]),
+            ("twell_distill_backward", [P, L, P, P, P, P, I, I, I, I, F32, P, P, P])):
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = args, I
+    for name in ("twell_embed_workspace_size", "twell_q8_workspace_size"):
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = [I, I, I], S
+    lib.twell_add_rmsnorm_workspace_size.argtypes = [I, I]
+    lib.twell_add_rmsnorm_workspace_size.restype = S
 
 
 def _ptr(a) -> Optional[int]:
@@ -235,3 +268,13 @@ def workspace(T: int, D: int, F: int, C: int, K: int, dtype: int, train: bool, d
     if n == 0:
         raise TwellError(-1, "twell_workspace_size")
     return torch.empty((n,), dtype=torch.uint8, device=device), n
+
+
+
+def __getattr__(name):
+    """The operators around the FFN, from ``lm`` on first use (it needs torch)."""
+    if name not in LM_EXPORTS:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import lm
+    fn = globals()[name] = getattr(lm, name)
+    return fn

@@ -31,7 +31,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 
 SOURCES = ["twell_abi.cu", "pack.cu", "simt_gemm.cu", "updown.cu", "tc_gemm.cu", "backward.cu",
-           "rowell.cu", "static_split.cu"]
+           "rowell.cu", "static_split.cu", "lm_abi.cu", "embed.cu", "rmsnorm.cu", "distill.cu",
+           "q8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 # variant -> (library file, extra sources, extra nvcc flags)
@@ -56,7 +57,7 @@ def nvcc_path() -> str:
 
 def _deps():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "twell.h"))
+    files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     files.append(os.path.abspath(__file__))
     return files
 

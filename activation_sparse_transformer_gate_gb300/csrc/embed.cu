@@ -1,0 +1,390 @@
+// embed.cu -- token embedding with scaling, and its gradient by sorted tokens.
+//
+// forward   out[t] = scale E[tok_t]
+// gradient  dE[v]  = scale sum_{t: tok_t = v} dy[t]
+//
+// Both move rows and add; HBM bounds them.  The gradient writes the whole
+// [V][D] fp32 table once and reads dy once.  A gather per row in a fixed
+// order needs the positions grouped by token, so:
+//   1. one launch sorts (token, position) -- a stable radix sort by one
+//      thread-block cluster -- while every other cluster writes the zeros of
+//      the table;
+//   2. the sorted list is cut into equal chunks, so a token that fills half
+//      the batch costs what any other does: a run of equal tokens inside a
+//      chunk is summed and stored, a run that crosses a chunk's end leaves
+//      its part in the workspace;
+//   3. the parts of each crossing run are added in order.
+// No floating-point atomics: the grouping of every sum is fixed by T and the
+// tokens alone.
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+#include "lm_kernels.h"
+#include "vec16.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace twell {
+
+namespace {
+
+constexpr int SORT_CTAS = 8;       // CTAs of the sorting cluster (the portable maximum)
+constexpr int SORT_THREADS = 1024;
+constexpr int SORT_WARPS = SORT_THREADS / 32;
+constexpr int DIGIT_MAX = 9;       // bits per pass: 2 passes sort any vocabulary below 2^18
+constexpr int CHUNK = 16;          // sorted entries per chunk of step 2
+
+// The token at position t as a sort key: the token, or V for positions
+// without one (padding, or out of range: recorded).
+template <typename I>
+__device__ __forceinline__ uint32_t token_key(const I *tokens, int t, int V, long long pad_id,
+                                              int32_t *status) {
+  const long long v = (long long)tokens[t];
+  if (v == pad_id) return (uint32_t)V;
+  if (v < 0 || v >= V) {
+    set_status(status, TWELL_ERR_INDEX);
+    return (uint32_t)V;
+  }
+  return (uint32_t)v;
+}
+
+// One warp per 128 vectors (2 KB) of a row, four independent loads a lane.
+template <typename E, typename I>
+__global__ void __launch_bounds__(256)
+embed_forward_kernel(const I *tokens, const E *table, int T, int V, int nv, float scale,
+                     long long pad_id, E *out, int32_t *status) {
+  pdl_begin();
+  constexpr int N = VEC16<E>;
+  const int parts = (nv + 127) / 128;
+  const long long unit = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const long long t = unit / parts;
+  if (t >= T) return;
+  const int v0 = (int)(unit - t * parts) * 128 + (threadIdx.x & 31);
+  const uint32_t key = token_key(tokens, (int)t, V, pad_id, status);
+  const bool live = key < (uint32_t)V;
+  const uint4 *src = (const uint4 *)table + (size_t)(live ? key : 0) * nv;
+  uint4 *dst = (uint4 *)out + (size_t)t * nv;
+  uint4 r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r[i] = live && v0 + 32 * i < nv ? ldg_stream(src + v0 + 32 * i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (v0 + 32 * i >= nv) break;
+    float f[N];
+    unpack(r[i], f, (E *)nullptr);
+#pragma unroll
+    for (int j = 0; j < N; ++j) f[j] *= scale;
+    stg_stream(dst + v0 + 32 * i, live ? pack16(f, (E *)nullptr) : make_uint4(0, 0, 0, 0));
+  }
+}
+
+// ---- step 1: sort and zero ---------------------------------------------------
+// Cluster 0 sorts; the CTAs of the other clusters write zeros.  Least
+// significant digit first; each CTA owns a contiguous eighth of the list and
+// each warp a contiguous part of that, walked in order, so that (digit, CTA,
+// warp, place in the warp's walk) is the stable order.  Per pass: counts per
+// warp and digit in shared memory, the CTAs' totals exchanged through
+// distributed shared memory, then every key is stored at its place.
+struct SortSmem {
+  uint32_t hist[SORT_WARPS][1 << DIGIT_MAX];  // counts, then each warp's next place
+  uint32_t total[1 << DIGIT_MAX];             // this CTA's count per digit
+  uint32_t warp_sum[SORT_WARPS];
+};
+
+template <typename I>
+__global__ void __launch_bounds__(SORT_THREADS, 1)
+embed_sort_zero_kernel(const I *tokens, int T, int V, long long pad_id, uint32_t *key0,
+                       int32_t *pos0, uint32_t *key1, int32_t *pos1, int passes, int bits,
+                       uint4 *dtable, size_t table_vecs, int32_t *status) {
+  pdl_begin();
+  if (blockIdx.x >= SORT_CTAS) {
+    const size_t n = (size_t)(gridDim.x - SORT_CTAS) * SORT_THREADS;
+    for (size_t i = (size_t)(blockIdx.x - SORT_CTAS) * SORT_THREADS + threadIdx.x; i < table_vecs;
+         i += n)
+      stg_stream(dtable + i, make_uint4(0, 0, 0, 0));
+    return;
+  }
+  extern __shared__ uint8_t sort_smem_raw[];
+  SortSmem &sm = *(SortSmem *)sort_smem_raw;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bins = 1 << bits;
+  // this warp's part of the list, in groups of 32
+  const long long groups = ((long long)T + 31) / 32;
+  const long long warps = (long long)SORT_CTAS * SORT_WARPS;
+  const long long w = (long long)rank * SORT_WARPS + warp;
+  const long long g0 = groups * w / warps, g1 = groups * (w + 1) / warps;
+
+  for (int pass = 0; pass < passes; ++pass) {
+    // (the last pass ends in key0 / pos0 whatever their number)
+    const bool to0 = ((passes - 1 - pass) & 1) == 0;
+    const uint32_t *kin = to0 ? key1 : key0;
+    const int32_t *pin = to0 ? pos1 : pos0;
+    uint32_t *kout = to0 ? key0 : key1;
+    int32_t *pout = to0 ? pos0 : pos1;
+    const int shift = pass * bits;
+    auto load = [&](long long i) -> uint32_t {
+      if (i >= T) return 0xFFFFFFFFu;
+      return pass == 0 ? token_key(tokens, (int)i, V, pad_id, status) : __ldcg(kin + i);
+    };
+    for (int b = lane; b < bins; b += 32) sm.hist[warp][b] = 0;
+    __syncwarp();
+    for (long long g = g0; g < g1; ++g) {
+      const long long i = g * 32 + lane;
+      const uint32_t k = load(i);
+      const uint32_t d = i < T ? (k >> shift) & (bins - 1) : 0xFFFFFFFFu;
+      const uint32_t peers = __match_any_sync(0xFFFFFFFFu, d);
+      if (i < T && lane == __ffs(peers) - 1) sm.hist[warp][d] += __popc(peers);
+      __syncwarp();
+    }
+    __syncthreads();
+    // each digit: the warps' counts become offsets within the CTA
+    if (threadIdx.x < bins) {
+      uint32_t run = 0;
+      for (int i = 0; i < SORT_WARPS; ++i) {
+        const uint32_t c = sm.hist[i][threadIdx.x];
+        sm.hist[i][threadIdx.x] = run;
+        run += c;
+      }
+      sm.total[threadIdx.x] = run;
+    }
+    cluster.sync();
+    uint32_t before = 0, all = 0;
+    if (threadIdx.x < bins)
+      for (int c = 0; c < SORT_CTAS; ++c) {
+        const uint32_t n = *cluster.map_shared_rank(&sm.total[threadIdx.x], c);
+        if (c < rank) before += n;
+        all += n;
+      }
+    // exclusive scan of the digits' totals
+    uint32_t inc = all;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    if (lane == 31) sm.warp_sum[warp] = inc;
+    __syncthreads();
+    if (threadIdx.x < bins) {
+      uint32_t base = inc - all + before;
+      for (int i = 0; i < warp; ++i) base += sm.warp_sum[i];
+      for (int i = 0; i < SORT_WARPS; ++i) sm.hist[i][threadIdx.x] += base;
+    }
+    __syncthreads();
+    for (long long g = g0; g < g1; ++g) {
+      const long long i = g * 32 + lane;
+      const uint32_t k = load(i);
+      const uint32_t d = i < T ? (k >> shift) & (bins - 1) : 0xFFFFFFFFu;
+      const uint32_t peers = __match_any_sync(0xFFFFFFFFu, d);
+      if (i < T) {
+        const uint32_t to = sm.hist[warp][d] + __popc(peers & ((1u << lane) - 1));
+        kout[to] = k;
+        pout[to] = pass == 0 ? (int32_t)i : __ldcg(pin + i);
+      }
+      __syncwarp();
+      if (i < T && lane == __ffs(peers) - 1) sm.hist[warp][d] += __popc(peers);
+      __syncwarp();
+    }
+    // the pass's stores reach the other CTAs, and no CTA's totals are
+    // overwritten (or its shared memory freed) while another reads them
+    __threadfence();
+    cluster.sync();
+  }
+}
+
+// ---- step 2: runs of equal tokens --------------------------------------------
+// A group of `tpr` threads takes one chunk and one slab of tpr 16-byte
+// vectors; the rows are loaded four at a time ahead of their use.
+template <typename E>
+__global__ void __launch_bounds__(256)
+embed_runs_kernel(const uint32_t *key, const int32_t *pos, const E *dy, int T, int V, int nv,
+                  int tpr, int chunks, float scale, float *dtable, float *part) {
+  pdl_begin();
+  constexpr int N = VEC16<E>;
+  const int c = (int)blockIdx.x * (blockDim.x / tpr) + (int)threadIdx.x / tpr;
+  const int v = (int)blockIdx.y * tpr + (int)threadIdx.x % tpr;
+  if (c >= chunks || v >= nv) return;
+  const int i0 = c * CHUNK, i1 = min(T, i0 + CHUNK);
+  const int D = nv * N;
+  // the chunk's first run began before it / its last run goes on after it
+  const uint32_t first = key[i0];
+  const bool open_left = i0 > 0 && key[i0 - 1] == first;
+  const uint32_t last = key[i1 - 1];
+  const bool open_right = i1 < T && key[i1] == last;
+  float acc[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) acc[j] = 0.f;
+  bool left = open_left;  // the current run is the one open to the left
+  for (int i = i0; i < i1; i += 4) {
+    uint32_t k[5];
+    uint4 r[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      k[u] = i + u < i1 ? key[i + u] : 0xFFFFFFFFu;
+      r[u] = k[u] < (uint32_t)V ? ldg_stream((const uint4 *)dy + (size_t)pos[i + u] * nv + v)
+                                : make_uint4(0, 0, 0, 0);
+    }
+    k[4] = i + 4 < i1 ? key[i + 4] : 0xFFFFFFFFu;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (k[u] >= (uint32_t)V) continue;  // no token here, nor further on
+      float f[N];
+      unpack(r[u], f, (E *)nullptr);
+#pragma unroll
+      for (int j = 0; j < N; ++j) acc[j] += f[j];
+      if (k[u + 1] == k[u]) continue;
+      // the run ends with this entry (or the chunk does)
+      const bool right = open_right && i + u == i1 - 1;
+      float *dst = left    ? part + ((size_t)c * 2) * D
+                   : right ? part + ((size_t)c * 2 + 1) * D
+                           : dtable + (size_t)k[u] * D;
+      const float m = left || right ? 1.f : scale;
+#pragma unroll
+      for (int j = 0; j < N; j += 4)
+        stg_stream(dst + (size_t)v * N + j,
+                   make_uint4(__float_as_uint(acc[j] * m), __float_as_uint(acc[j + 1] * m),
+                              __float_as_uint(acc[j + 2] * m), __float_as_uint(acc[j + 3] * m)));
+#pragma unroll
+      for (int j = 0; j < N; ++j) acc[j] = 0.f;
+      left = false;
+    }
+  }
+}
+
+// ---- step 3: runs that cross chunk ends ----------------------------------------
+// CTA c acts if a run begins in chunk c and goes on into chunk c + 1: its
+// parts are [c][1] and [c+1][0], [c+2][0], ... up to the chunk it ends in.
+// Eight warps take consecutive eighths of the parts (128 columns a CTA) and
+// their sums are added in order.
+__global__ void __launch_bounds__(256)
+embed_join_kernel(const uint32_t *key, int T, int V, int D, int chunks, float scale,
+                  const float *part, float *dtable) {
+  pdl_begin();
+  const int c = (int)blockIdx.x;
+  const int end = min(T, (c + 1) * CHUNK);
+  if (end >= T) return;
+  const uint32_t k = key[end - 1];
+  if (k >= (uint32_t)V || key[end] != k) return;
+  if (key[c * CHUNK] == k && c > 0 && key[c * CHUNK - 1] == k) return;  // began earlier
+  // the last chunk of the run: binary search for the first entry above k
+  int lo = end, hi = T;  // key[lo] == k; key[hi] > k (or hi == T)
+  while (hi - lo > 1) {
+    const int mid = lo + (hi - lo) / 2;
+    if (key[mid] == k) lo = mid;
+    else hi = mid;
+  }
+  const int n = lo / CHUNK - c;  // parts [c+1][0] .. [c+n][0]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int col = (int)blockIdx.y * 128 + lane * 4;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (col < D) {
+    if (warp == 0) acc = *(const float4 *)(part + ((size_t)c * 2 + 1) * D + col);
+    const int a = (int)((long long)n * warp / 8), b = (int)((long long)n * (warp + 1) / 8);
+#pragma unroll 4
+    for (int i = a; i < b; ++i) {
+      const float4 p = *(const float4 *)(part + (size_t)(c + 1 + i) * 2 * D + col);
+      acc.x += p.x; acc.y += p.y; acc.z += p.z; acc.w += p.w;
+    }
+  }
+  __shared__ float4 sums[8][32];
+  sums[warp][lane] = acc;
+  __syncthreads();
+  if (warp != 0 || col >= D) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    const float4 p = sums[i][lane];
+    acc.x += p.x; acc.y += p.y; acc.z += p.z; acc.w += p.w;
+  }
+  *(float4 *)(dtable + (size_t)k * D + col) =
+      make_float4(acc.x * scale, acc.y * scale, acc.z * scale, acc.w * scale);
+}
+
+template <typename E, typename I>
+cudaError_t embed_forward_t(const EmbedArgs &a, const void *table, void *out, cudaStream_t s) {
+  const int nv = (int)((size_t)a.D * sizeof(E) / 16);
+  const long long units = (long long)a.T * ((nv + 127) / 128);
+  const long long grid = (units + 7) / 8;
+  if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  return launch_k(embed_forward_kernel<E, I>, dim3((unsigned)grid), dim3(256), 0, s,
+                  (const I *)a.tokens, (const E *)table, a.T, a.V, nv, a.scale, a.pad_id, (E *)out,
+                  a.status);
+}
+
+template <typename E, typename I>
+cudaError_t embed_backward_t(const EmbedArgs &a, const void *dy, float *dtable,
+                             const EmbedScratch &w, cudaStream_t s) {
+  // keys 0 .. V
+  int need = 1;
+  while (((long long)1 << need) <= a.V) ++need;
+  const int passes = (need + DIGIT_MAX - 1) / DIGIT_MAX;
+  const int bits = (need + passes - 1) / passes;
+  static const cudaError_t attr = cudaFuncSetAttribute(
+      embed_sort_zero_kernel<I>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(SortSmem));
+  if (attr != cudaSuccess) return attr;
+  // one CTA an SM: the sorting cluster beside the clusters that write zeros
+  const int clusters = num_sms() / SORT_CTAS > 1 ? num_sms() / SORT_CTAS : 2;
+  cudaError_t e = launch_clusters(
+      embed_sort_zero_kernel<I>, dim3(clusters * SORT_CTAS), dim3(SORT_THREADS), sizeof(SortSmem),
+      SORT_CTAS, s, (const I *)a.tokens, a.T, a.V, a.pad_id, w.key[0], w.pos[0], w.key[1], w.pos[1], passes, bits,
+                           (uint4 *)dtable, (size_t)a.V * a.D / 4, a.status);
+  if (e != cudaSuccess) return e;
+  prof_mark(KID_EMBED_SORT, s);
+  const int nv = (int)((size_t)a.D * sizeof(E) / 16);
+  const int chunks = (a.T + CHUNK - 1) / CHUNK;
+  int tpr = 32;
+  while (tpr < nv && tpr < 256) tpr *= 2;
+  const int per = 256 / tpr;
+  e = launch_k(embed_runs_kernel<E>, dim3((chunks + per - 1) / per, (nv + tpr - 1) / tpr),
+               dim3(256), 0, s, (const uint32_t *)w.key[0], (const int32_t *)w.pos[0],
+               (const E *)dy, a.T, a.V, nv, tpr, chunks, a.scale, dtable, w.part);
+  if (e != cudaSuccess) return e;
+  prof_mark(KID_EMBED_RUNS, s);
+  if (chunks > 1) {
+    e = launch_k(embed_join_kernel, dim3(chunks - 1, (a.D + 127) / 128), dim3(256), 0, s,
+                 (const uint32_t *)w.key[0], a.T, a.V, a.D, chunks, a.scale,
+                 (const float *)w.part, dtable);
+    prof_mark(KID_EMBED_JOIN, s);
+  }
+  return e;
+}
+
+}  // namespace
+
+EmbedScratch carve_embed(void *base, int T, int V, int D) {
+  EmbedScratch w;
+  (void)V;
+  size_t off = 0;
+  auto take = [&](size_t bytes) -> void * {
+    const size_t o = off;
+    off = (off + bytes + 255) / 256 * 256;
+    return base ? (void *)((char *)base + o) : nullptr;
+  };
+  for (int i = 0; i < 2; ++i) {
+    w.key[i] = (uint32_t *)take(4 * (size_t)T);
+    w.pos[i] = (int32_t *)take(4 * (size_t)T);
+  }
+  const size_t chunks = ((size_t)T + CHUNK - 1) / CHUNK;
+  w.part = (float *)take(chunks * 2 * (size_t)D * 4);
+  w.bytes = off;
+  return w;
+}
+
+cudaError_t launch_embed_forward(const EmbedArgs &a, const void *table, void *out, cudaStream_t s) {
+  if (a.dtype == TWELL_BF16)
+    return a.token_bytes == 8 ? embed_forward_t<bf16, long long>(a, table, out, s)
+                              : embed_forward_t<bf16, int32_t>(a, table, out, s);
+  return a.token_bytes == 8 ? embed_forward_t<float, long long>(a, table, out, s)
+                            : embed_forward_t<float, int32_t>(a, table, out, s);
+}
+
+cudaError_t launch_embed_backward(const EmbedArgs &a, const void *dy, float *dtable,
+                                  const EmbedScratch &w, cudaStream_t s) {
+  if (a.dtype == TWELL_BF16)
+    return a.token_bytes == 8 ? embed_backward_t<bf16, long long>(a, dy, dtable, w, s)
+                              : embed_backward_t<bf16, int32_t>(a, dy, dtable, w, s);
+  return a.token_bytes == 8 ? embed_backward_t<float, long long>(a, dy, dtable, w, s)
+                            : embed_backward_t<float, int32_t>(a, dy, dtable, w, s);
+}
+
+}  // namespace twell

@@ -80,6 +80,14 @@ struct BwdArgs {
 // counts are taken where dh is finished, one per TwELL slot).
 constexpr int TR_CHUNK = 1024;
 
+// Argument checks and the result of a launch, as the C entry points use them.
+inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+inline twell_status cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return TWELL_OK;
+  if (e == cudaErrorNotSupported) return TWELL_ERR_UNSUPPORTED;
+  return TWELL_ERR_CUDA;
+}
+
 // pack.cu
 // Streaming multiprocessors and L2 bytes of the current device (queried once).
 int num_sms();
@@ -195,7 +203,19 @@ enum KernelId {
   KID_ROWELL_UPDOWN = 19,
   KID_BWD_DH_GEMM = 20,
   KID_TO_F16 = 21,
-  KID_COUNT = 22
+  // the operators around the FFN (lm_kernels.h)
+  KID_EMBED_FWD = 22,
+  KID_EMBED_SORT = 23,
+  KID_EMBED_RUNS = 24,
+  KID_EMBED_JOIN = 25,
+  KID_RMSNORM_FWD = 26,
+  KID_RMSNORM_BWD = 27,
+  KID_RMSNORM_DW = 28,
+  KID_Q8_QUANTIZE = 29,
+  KID_Q8_MATMUL = 30,
+  KID_DISTILL_FWD = 31,
+  KID_DISTILL_BWD = 32,
+  KID_COUNT = 33
 };
 // Record a timing event after `launches` kernel launches of component `id`
 // (no-op unless enabled).

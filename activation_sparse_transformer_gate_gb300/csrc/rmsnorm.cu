@@ -1,0 +1,418 @@
+// rmsnorm.cu -- residual addition + root-mean-square norm, with an output in
+// the row's type or in 8 bits, and its backward.
+//
+// forward   s = x + r (stored),  rstd = (mean s^2 + eps)^(-1/2),  y = s rstd w
+//           8 bits: scale = max|y| / 127,  q = rint(y / scale)
+// backward  xhat = s rstd,  g = w dy
+//           dx = ds + rstd (g - xhat mean(g xhat)),  dw = sum_t dy xhat
+//
+// HBM bounds both: every operand is read or written once.  A row stays in
+// registers between the reduction and the output, spread over the fewest
+// warps that keep at most NV 16-byte vectors a lane.  max|y| = rstd max|s w|,
+// so the 8-bit output needs no second reduction.
+#include "common.cuh"
+#include "lm_kernels.h"
+#include "vec16.cuh"
+
+namespace twell {
+
+namespace {
+
+constexpr int WARPS = 8;  // per CTA
+
+// Sum and (bitwise) maximum over the W warps that share a row.  The maximum
+// of |v| is taken on the bit patterns: their order is the values' order, and
+// a NaN is above every number, so it is not lost.
+template <int W>
+__device__ __forceinline__ void reduce_row(float &sum, uint32_t &top, float (*s_sum)[WARPS],
+                                           uint32_t (*s_top)[WARPS], int buf) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  if (W == 1) return;
+  const int warp = threadIdx.x >> 5;
+  if ((threadIdx.x & 31) == 0) {
+    s_sum[buf][warp] = sum;
+    s_top[buf][warp] = top;
+  }
+  __syncthreads();
+  const int w0 = warp / W * W;
+  sum = 0.f;
+  top = 0;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    sum += s_sum[buf][w0 + i];
+    top = max(top, s_top[buf][w0 + i]);
+  }
+}
+
+// The 8-bit scale of a row whose largest magnitude is `top`, and the factors
+// (up, inv) with q = rint(v * up * inv): a row below 2^-60 is scaled up first
+// so that 127 / top stays finite.  Rows that hold an infinity or NaN get
+// scale NaN and q 0 (inv = 0, and fin = false).
+struct Q8Scale {
+  float scale, up, inv;
+  bool fin;
+};
+__device__ __forceinline__ Q8Scale q8_scale(uint32_t top_bits) {
+  Q8Scale r;
+  const float top = __uint_as_float(top_bits);
+  r.fin = top_bits < 0x7F800000u;
+  r.up = top < 0x1p-60f ? 0x1p+64f : 1.f;
+  r.scale = r.fin ? top / 127.f : __uint_as_float(0x7FC00000u);
+  r.inv = r.fin && top > 0.f ? 127.f / (top * r.up) : 0.f;
+  return r;
+}
+__device__ __forceinline__ uint32_t q8_of(float v, const Q8Scale &c) {
+  if (!c.fin) return 0;
+  const int q = __float2int_rn(v * c.up * c.inv);
+  return (uint32_t)max(-127, min(127, q)) & 0xFFu;
+}
+
+template <typename E> struct Q8Word;  // one vector's 8-bit values
+template <> struct Q8Word<float> { typedef uint32_t type; };
+template <> struct Q8Word<bf16> { typedef uint2 type; };
+__device__ __forceinline__ void q8_pack(const float (&f)[4], const Q8Scale &c, uint32_t &w) {
+  w = q8_of(f[0], c) | q8_of(f[1], c) << 8 | q8_of(f[2], c) << 16 | q8_of(f[3], c) << 24;
+}
+__device__ __forceinline__ void q8_pack(const float (&f)[8], const Q8Scale &c, uint2 &w) {
+  w.x = q8_of(f[0], c) | q8_of(f[1], c) << 8 | q8_of(f[2], c) << 16 | q8_of(f[3], c) << 24;
+  w.y = q8_of(f[4], c) | q8_of(f[5], c) << 8 | q8_of(f[6], c) << 16 | q8_of(f[7], c) << 24;
+}
+
+// N fp32 weights of vector v.
+template <int N>
+__device__ __forceinline__ void load_w(const float *w, int v, float (&f)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; j += 4) {
+    const float4 a = *(const float4 *)(w + (size_t)v * N + j);
+    f[j] = a.x; f[j + 1] = a.y; f[j + 2] = a.z; f[j + 3] = a.w;
+  }
+}
+
+// W warps a row, NV vectors a lane.
+template <typename E, int W, int NV>
+__global__ void __launch_bounds__(WARPS * 32)
+rmsnorm_forward_kernel(const uint4 *x, const uint4 *res, const float *weight, int T, int nv,
+                       float inv_d, float eps, uint4 *s_out, uint4 *y, int8_t *q, float *qscale,
+                       float *rstd_out) {
+  pdl_begin();
+  constexpr int N = VEC16<E>;
+  __shared__ float s_sum[1][WARPS];
+  __shared__ uint32_t s_top[1][WARPS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long t = (long long)blockIdx.x * (WARPS / W) + warp / W;
+  const bool row_ok = t < T;
+  const int v0 = (warp % W) * 32 + lane;
+  const size_t base = (size_t)(row_ok ? t : 0) * nv;
+  uint4 a[NV], b[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = v0 + i * W * 32;
+    const bool ok = row_ok && v < nv;
+    a[i] = ok ? ld_once(x + base + v) : make_uint4(0, 0, 0, 0);
+    b[i] = ok && res ? ld_once(res + base + v) : make_uint4(0, 0, 0, 0);
+  }
+  float sum = 0.f;
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = v0 + i * W * 32;
+    if (!row_ok || v >= nv) continue;
+    if (res) {
+      float f[N], g[N];
+      unpack(a[i], f, (E *)nullptr);
+      unpack(b[i], g, (E *)nullptr);
+#pragma unroll
+      for (int j = 0; j < N; ++j) f[j] += g[j];
+      a[i] = pack16(f, (E *)nullptr);  // the stored sum is what the norm reads
+    }
+    if (s_out) s_out[base + v] = a[i];
+    float f[N];
+    unpack(a[i], f, (E *)nullptr);
+#pragma unroll
+    for (int j = 0; j < N; ++j) sum += f[j] * f[j];
+    if (q) {
+      float w[N];
+      load_w(weight, v, w);
+#pragma unroll
+      for (int j = 0; j < N; ++j) top = max(top, __float_as_uint(fabsf(f[j] * w[j])));
+    }
+  }
+  reduce_row<W>(sum, top, s_sum, s_top, 0);
+  if (!row_ok) return;
+  const float rstd = rsqrtf(sum * inv_d + eps);
+  // (rstd is NaN, or 0 with an infinite sum, when s has a NaN or infinity:
+  // 0 * inf then makes the row's largest magnitude NaN too)
+  const Q8Scale sc = q8_scale(__float_as_uint(fabsf(__uint_as_float(top) * rstd)));
+  if (v0 == 0) {
+    if (rstd_out) rstd_out[t] = rstd;
+    if (q) qscale[t] = sc.scale;
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = v0 + i * W * 32;
+    if (v >= nv) break;
+    float f[N], w[N];
+    unpack(a[i], f, (E *)nullptr);
+    load_w(weight, v, w);
+#pragma unroll
+    for (int j = 0; j < N; ++j) f[j] = f[j] * rstd * w[j];
+    if (y) y[base + v] = pack16(f, (E *)nullptr);
+    if (q) {
+      typename Q8Word<E>::type word;
+      q8_pack(f, sc, word);
+      ((typename Q8Word<E>::type *)q)[base + v] = word;
+    }
+  }
+}
+
+// Backward.  CTAs walk the rows; each thread keeps its columns' part of dw
+// in registers over all its rows and writes it to the workspace at the end
+// (one row of `part` per row group of the grid).  The next row's loads are
+// issued before the current row's reduction.
+template <typename E, int W, int NV>
+__global__ void __launch_bounds__(WARPS * 32)
+rmsnorm_backward_kernel(const uint4 *s_in, const float *weight, const float *rstd_in,
+                        const uint4 *dy, const uint4 *ds, int T, int nv, float inv_d, uint4 *dx,
+                        float *part) {
+  pdl_begin();
+  constexpr int N = VEC16<E>;
+  __shared__ float s_sum[2][WARPS];
+  __shared__ uint32_t s_top[2][WARPS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = (int)blockIdx.x * (WARPS / W) + warp / W;
+  const int groups = (int)gridDim.x * (WARPS / W);
+  const int v0 = (warp % W) * 32 + lane;
+  float dw[NV][N];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < N; ++j) dw[i][j] = 0.f;
+  uint4 a[NV], b[NV], c[NV];
+  auto load = [&](long long t) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = v0 + i * W * 32;
+      const bool ok = t < T && v < nv;
+      const size_t o = (size_t)t * nv + v;
+      a[i] = ok ? ld_once(s_in + o) : make_uint4(0, 0, 0, 0);
+      b[i] = ok ? ld_once(dy + o) : make_uint4(0, 0, 0, 0);
+      c[i] = ok && ds ? ld_once(ds + o) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  load(group);
+  // every group makes the same number of rounds (the reduction's barrier is
+  // the CTA's)
+  const int rounds = (T + groups - 1) / groups;
+  for (int r = 0; r < rounds; ++r) {
+    const long long t = (long long)r * groups + group;
+    const bool row_ok = t < T;
+    const float rstd = row_ok ? rstd_in[t] : 0.f;
+    uint4 sa[NV], sb[NV], sc[NV];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      sa[i] = a[i]; sb[i] = b[i]; sc[i] = c[i];
+      const int v = v0 + i * W * 32;
+      if (!row_ok || v >= nv) continue;
+      float f[N], g[N], w[N];
+      unpack(a[i], f, (E *)nullptr);
+      unpack(b[i], g, (E *)nullptr);
+      load_w(weight, v, w);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const float xhat = f[j] * rstd;
+        dw[i][j] += g[j] * xhat;
+        sum += g[j] * w[j] * xhat;
+      }
+    }
+    load(t + groups);
+    uint32_t none = 0;
+    reduce_row<W>(sum, none, s_sum, s_top, r & 1);
+    const float mean = sum * inv_d;
+    if (!row_ok) continue;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = v0 + i * W * 32;
+      if (v >= nv) break;
+      float f[N], g[N], h[N], w[N];
+      unpack(sa[i], f, (E *)nullptr);
+      unpack(sb[i], g, (E *)nullptr);
+      unpack(sc[i], h, (E *)nullptr);
+      load_w(weight, v, w);
+#pragma unroll
+      for (int j = 0; j < N; ++j) h[j] += rstd * (g[j] * w[j] - f[j] * rstd * mean);
+      dx[(size_t)t * nv + v] = pack16(h, (E *)nullptr);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = v0 + i * W * 32;
+    if (v >= nv) break;
+    float *p = part + ((size_t)group * nv + v) * N;
+#pragma unroll
+    for (int j = 0; j < N; j += 4)
+      *(float4 *)(p + j) = make_float4(dw[i][j], dw[i][j + 1], dw[i][j + 2], dw[i][j + 3]);
+  }
+}
+
+// dw[d] = sum of the groups' rows, in order: 32 columns a CTA, 32 warps take
+// every 32nd group and are added in order.
+__global__ void __launch_bounds__(1024)
+rmsnorm_dw_kernel(const float *part, int groups, int D, float *dw) {
+  pdl_begin();
+  __shared__ float sums[32][33];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int d = blockIdx.x * 32 + lane;
+  float acc = 0.f;
+  if (d < D)
+#pragma unroll 4
+    for (int g = warp; g < groups; g += 32) acc += part[(size_t)g * D + d];
+  sums[warp][lane] = acc;
+  __syncthreads();
+  if (warp != 0 || d >= D) return;
+  acc = 0.f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) acc += sums[i][lane];
+  dw[d] = acc;
+}
+
+// Symmetric 8-bit rows of a matrix: a CTA per row, which is read twice (the
+// second time from L1 / L2).
+template <typename E>
+__global__ void __launch_bounds__(256)
+q8_quantize_kernel(const uint4 *a, int nv, int8_t *q, float *scale) {
+  pdl_begin();
+  constexpr int N = VEC16<E>;
+  __shared__ float s_sum[1][WARPS];
+  __shared__ uint32_t s_top[1][WARPS];
+  const size_t base = (size_t)blockIdx.x * nv;
+  uint32_t top = 0;
+  for (int v = threadIdx.x; v < nv; v += 256) {
+    float f[N];
+    unpack(a[base + v], f, (E *)nullptr);
+#pragma unroll
+    for (int j = 0; j < N; ++j) top = max(top, __float_as_uint(fabsf(f[j])));
+  }
+  float none = 0.f;
+  reduce_row<WARPS>(none, top, s_sum, s_top, 0);
+  const Q8Scale sc = q8_scale(top);
+  if (threadIdx.x == 0) scale[blockIdx.x] = sc.scale;
+  for (int v = threadIdx.x; v < nv; v += 256) {
+    float f[N];
+    unpack(a[base + v], f, (E *)nullptr);
+    typename Q8Word<E>::type word;
+    q8_pack(f, sc, word);
+    ((typename Q8Word<E>::type *)q)[base + v] = word;
+  }
+}
+
+// Warps a row: the fewest with at most `most` vectors a lane.
+int row_warps(int nv, int most) {
+  int w = 1;
+  while (w < WARPS && nv > w * 32 * most) w *= 2;
+  return w;
+}
+
+constexpr int FWD_NV = 2, BWD_NV = 2;  // vectors a lane before a row takes more warps
+
+int backward_grid(int T, int nv) {
+  const int per = WARPS / row_warps(nv, BWD_NV);
+  const int want = (T + per - 1) / per;
+  const int most = num_sms() * 2;
+  return want < most ? want : most;
+}
+
+template <typename E, int W, int NV>
+cudaError_t forward_t(const void *x, const void *residual, const float *weight, int T, int nv,
+                      float eps, void *s_out, void *y, int8_t *q, float *qscale, float *rstd,
+                      cudaStream_t s) {
+  const int per = WARPS / W;
+  return launch_k(rmsnorm_forward_kernel<E, W, NV>, dim3((T + per - 1) / per), dim3(WARPS * 32), 0,
+                  s, (const uint4 *)x, (const uint4 *)residual, weight, T, nv,
+                  1.f / (float)(nv * VEC16<E>), eps, (uint4 *)s_out, (uint4 *)y, q, qscale, rstd);
+}
+
+template <typename E, int W, int NV>
+cudaError_t backward_t(const void *s_in, const float *weight, const float *rstd, const void *dy,
+                       const void *ds, int T, int nv, void *dx, float *dweight, float *part,
+                       cudaStream_t s) {
+  const int grid = backward_grid(T, nv);
+  cudaError_t e = launch_k(rmsnorm_backward_kernel<E, W, NV>, dim3(grid), dim3(WARPS * 32), 0, s,
+                           (const uint4 *)s_in, weight, rstd, (const uint4 *)dy, (const uint4 *)ds,
+                           T, nv, 1.f / (float)(nv * VEC16<E>), (uint4 *)dx, part);
+  if (e != cudaSuccess) return e;
+  prof_mark(KID_RMSNORM_BWD, s);
+  const int D = nv * VEC16<E>;
+  e = launch_k(rmsnorm_dw_kernel, dim3((D + 31) / 32), dim3(1024), 0, s, (const float *)part,
+               grid * (WARPS / W), D, dweight);
+  prof_mark(KID_RMSNORM_DW, s);
+  return e;
+}
+
+// f<E, W, NV>(args...) for the row's width: at most FWD_NV / BWD_NV vectors a
+// lane up to eight warps, four beyond.
+#define TWELL_ROW_DISPATCH(F, E, nv, most, ...)             \
+  (nv <= 32 * most      ? F<E, 1, most>(__VA_ARGS__)        \
+   : nv <= 64 * most    ? F<E, 2, most>(__VA_ARGS__)        \
+   : nv <= 128 * most   ? F<E, 4, most>(__VA_ARGS__)        \
+   : nv <= 256 * most   ? F<E, 8, most>(__VA_ARGS__)        \
+                        : F<E, 8, 4>(__VA_ARGS__))
+
+}  // namespace
+
+cudaError_t launch_add_rmsnorm_forward(const void *x, const void *residual, const float *weight,
+                                       int T, int D, int dtype, float eps, void *s_out, void *y,
+                                       int8_t *q, float *qscale, float *rstd, cudaStream_t s) {
+  cudaError_t e;
+  if (dtype == TWELL_BF16) {
+    const int nv = D / VEC16<bf16>;
+    e = TWELL_ROW_DISPATCH(forward_t, bf16, nv, FWD_NV, x, residual, weight, T, nv, eps, s_out, y,
+                           q, qscale, rstd, s);
+  } else {
+    const int nv = D / VEC16<float>;
+    e = TWELL_ROW_DISPATCH(forward_t, float, nv, FWD_NV, x, residual, weight, T, nv, eps, s_out, y,
+                           q, qscale, rstd, s);
+  }
+  prof_mark(KID_RMSNORM_FWD, s);
+  return e;
+}
+
+size_t rmsnorm_scratch(int T, int D) {
+  // (the layout of either type: the finer one has the most row groups)
+  size_t groups = 0;
+  for (int n : {VEC16<bf16>, VEC16<float>}) {
+    const int nv = D / n;
+    const size_t g = (size_t)backward_grid(T, nv) * (WARPS / row_warps(nv, BWD_NV));
+    if (g > groups) groups = g;
+  }
+  return groups * (size_t)D * 4;
+}
+
+cudaError_t launch_add_rmsnorm_backward(const void *s_in, const float *weight, const float *rstd,
+                                        const void *dy, const void *ds, int T, int D, int dtype,
+                                        void *dx, float *dweight, float *part, cudaStream_t s) {
+  if (dtype == TWELL_BF16) {
+    const int nv = D / VEC16<bf16>;
+    return TWELL_ROW_DISPATCH(backward_t, bf16, nv, BWD_NV, s_in, weight, rstd, dy, ds, T, nv, dx,
+                              dweight, part, s);
+  }
+  const int nv = D / VEC16<float>;
+  return TWELL_ROW_DISPATCH(backward_t, float, nv, BWD_NV, s_in, weight, rstd, dy, ds, T, nv, dx,
+                            dweight, part, s);
+}
+
+cudaError_t launch_q8_quantize(const void *a, int rows, int cols, int dtype, int8_t *q,
+                               float *scale, cudaStream_t s) {
+  cudaError_t e =
+      dtype == TWELL_BF16
+          ? launch_k(q8_quantize_kernel<bf16>, dim3(rows), dim3(256), 0, s, (const uint4 *)a,
+                     cols / VEC16<bf16>, q, scale)
+          : launch_k(q8_quantize_kernel<float>, dim3(rows), dim3(256), 0, s, (const uint4 *)a,
+                     cols / VEC16<float>, q, scale);
+  prof_mark(KID_Q8_QUANTIZE, s);
+  return e;
+}
+
+}  // namespace twell

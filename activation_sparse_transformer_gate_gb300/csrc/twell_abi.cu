@@ -65,7 +65,9 @@ static const char *kKernelNames[KID_COUNT] = {
     "bwd_slots_sddmm",      "bwd_dx_spmm",      "twell_transpose",    "bwd_dw_gather",
     "bwd_dense_dh_gemm",    "fill_u_slots",     "assemble_fb_rows",   "bwd_dense_dx_gemm",
     "bwd_dense_dw_gemm",    "bwd_prep_rows",    "rowell_pack_dense",  "rowell_updown",
-    "bwd_dh_gemm_sampled", "weights_to_f16"};
+    "bwd_dh_gemm_sampled", "weights_to_f16", "embed_forward", "embed_sort_zero", "embed_runs",
+    "embed_join", "add_rmsnorm_forward", "add_rmsnorm_backward", "rmsnorm_dw", "q8_quantize",
+    "q8_matmul", "distill_forward", "distill_backward"};
 
 Workspace carve_workspace(void *base, int T, int D, int F, int C, int K, int dtype, int train,
                           int rows_cap) {
@@ -133,8 +135,6 @@ using namespace twell;
 
 namespace {
 
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-
 bool pow2_k(int K) { return K == 1 || K == 2 || K == 4 || K == 8 || K == 16 || K == 32; }
 
 twell_status check_shape(int T, int D, int F, int C, int K, int dtype) {
@@ -164,12 +164,6 @@ twell_status check_tw(const twell_t *tw, int train) {
     if (!aligned16(tw->u_val) || (tw->ovf_cap > 0 && !aligned16(tw->u_fb))) return TWELL_ERR_ALIGN;
   }
   return TWELL_OK;
-}
-
-twell_status cuda_status(cudaError_t e) {
-  if (e == cudaSuccess) return TWELL_OK;
-  if (e == cudaErrorNotSupported) return TWELL_ERR_UNSUPPORTED;
-  return TWELL_ERR_CUDA;
 }
 
 twell_status check_ws(void *ws, size_t ws_bytes, const Workspace &need) {

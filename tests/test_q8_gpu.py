@@ -1,0 +1,147 @@
+"""The 8-bit product against exact integer sums.
+
+Bounds, with u = 2^-24: for K <= 1024 every partial sum is an integer below
+2^24, so the accumulator is exact and the result has three fp32 roundings
+(two scales, the bias): 3 u of |sum sa sw| + |bias| in total, and its storage.
+Beyond, each of the at most K / 8 additions into the fp32 accumulator loses
+at most 2 u (rounding towards zero) of a partial sum of magnitude at most
+sum |a w|, and nothing where that stays below 2^24."""
+import pytest
+import torch
+
+import activation_sparse_transformer_gate_gb300 as tw
+from lm_testlib import DT, U, check, empty, gen, scratch, setup, status
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    setup()
+
+
+def run(a, w, sa, sw, bias, dtype):
+    (M, K), N = a.shape, w.shape[0]
+    tdt, dt = DT[dtype]
+    y, st = empty(M, N, dtype=tdt), status()
+    ws, n = scratch(tw.twell_q8_workspace_size(M, N, K))
+    tw.twell_q8_matmul(a.cuda(), sa.cuda(), w.cuda(), sw.cuda(),
+                       None if bias is None else bias.cuda(), M, N, K, dt, y, st, ws, n)
+    assert tw.twell_read_status(st) == 0
+    return y
+
+
+def verify(a, w, sa, sw, bias, dtype):
+    y = run(a, w, sa, sw, bias, dtype)
+    acc = a.cuda().double() @ w.cuda().double().t()        # integers, exact in 64 bits
+    mag = a.cuda().double().abs() @ w.cuda().double().abs().t()
+    K = a.shape[1]
+    eacc = torch.where(mag < 2.0 ** 24, 0.0, K / 8 * 2 * U * mag)
+    scale = sa.cuda().double()[:, None] * sw.cuda().double()
+    ref = acc * scale
+    bound = eacc * scale.abs() + 3 * U * ref.abs()
+    if bias is not None:
+        ref = ref + bias.cuda().double()
+        bound = bound + 3 * U * bias.cuda().double().abs()
+    check(y, ref.cpu(), bound.cpu(), dtype, "y")
+    assert torch.equal(run(a, w, sa, sw, bias, dtype), y)
+    return y
+
+
+def inputs(M, N, K, seed, lo=-127):
+    g = gen(seed)
+    a = torch.randint(lo, 128, (M, K), generator=g, dtype=torch.int8)
+    w = torch.randint(lo, 128, (N, K), generator=g, dtype=torch.int8)
+    return (a, w, torch.rand(M, generator=g) + 0.01, torch.rand(N, generator=g) + 0.01,
+            torch.randn(N, generator=g) * 100)
+
+
+SHAPES = [(1, 1, 16), (1, 64, 128), (1, 8192, 2048), (1, 50001, 512), (2, 33, 48), (3, 1000, 4096),
+          (4, 129, 8192), (5, 77, 1040), (8, 14336, 256), (9, 300, 2064), (16, 128, 64),
+          (17, 255, 1024), (31, 257, 528), (37, 4096, 1008), (64, 513, 2048), (65, 100, 80),
+          (100, 3001, 1024), (127, 128, 4096), (128, 256, 64), (129, 130, 144), (250, 1001, 768),
+          (256, 512, 128), (300, 2000, 2000), (513, 129, 16), (1001, 5001, 2048), (1500, 64, 7008),
+          (4096, 2048, 512)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("dtype,bias", [("bf16", False), ("f32", True)])
+def test_against_exact_sums(M, N, K, dtype, bias):
+    a, w, sa, sw, b = inputs(M, N, K, M + N + K)
+    verify(a, w, sa, sw, b if bias else None, dtype)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 200, 65536), (20, 130, 16384), (300, 300, 16384)])
+def test_largest_sums(M, N, K):
+    """All entries -128: the sums are the largest there can be."""
+    a = torch.full((M, K), -128, dtype=torch.int8)
+    w = torch.full((N, K), -128, dtype=torch.int8)
+    w[::2] = 127
+    w[1, K // 2:] = 127
+    verify(a, w, torch.ones(M), torch.ones(N), None, "f32")
+
+
+@pytest.mark.parametrize("M", [1, 7, 40, 300])
+def test_every_value_and_lane(M):
+    """Row m of a picks out column m's bytes: each product is a single entry of w, over all 256
+    values."""
+    K, N = 512, 300
+    w = (torch.arange(N * K) % 256 - 128).to(torch.int8).reshape(N, K)
+    a = torch.zeros(M, K, dtype=torch.int8)
+    at = torch.arange(M) * 37 % K
+    a[torch.arange(M), at] = 1
+    y = run(a, w, torch.ones(M), torch.ones(N), None, "f32")
+    assert torch.equal(y.cpu(), w.float().t()[at])
+
+
+@pytest.mark.parametrize("M", [1, 6, 50, 200])
+def test_scales_at_the_edges(M):
+    """Scales of zero, infinity and NaN reach their row or column only."""
+    a, w, sa, sw, _ = inputs(M, 140, 256, M)
+    sw[3], sw[70] = 0.0, float("nan")
+    sa[0] = float("nan")
+    y = run(a, w, sa, sw, None, "f32").cpu()
+    bad = torch.zeros(M, 140, dtype=torch.bool)
+    bad[0] = True
+    bad[:, 70] = True
+    assert torch.equal(torch.isnan(y), bad)
+    assert (y[1:, 3] == 0).all()
+
+
+def test_norm_feeds_the_product():
+    """The norm's 8-bit output through the product against the 64-bit chain: the rounding of q
+    (half a step, uniform) is the error that remains; 6 standard deviations of its sum."""
+    g = gen(77)
+    T, D, N = 50, 1024, 700
+    x = torch.randn(T, D, generator=g).bfloat16().cuda()
+    wn = (1 + 0.1 * torch.randn(D, generator=g)).cuda()
+    W = (torch.randn(N, D, generator=g) / 32).bfloat16().cuda()
+    q, qs = empty(T, D, dtype=torch.int8), empty(T)
+    wq, ws_ = empty(N, D, dtype=torch.int8), empty(N)
+    tw.twell_add_rmsnorm_forward(x, None, wn, T, D, tw.TWELL_BF16, 1e-6, None, None, q, qs, None)
+    tw.twell_q8_quantize(W, N, D, tw.TWELL_BF16, wq, ws_)
+    y = run(q.cpu(), wq.cpu(), qs.cpu(), ws_.cpu(), None, "f32").double()
+    xd = x.double()
+    h = xd / torch.sqrt((xd * xd).mean(1, keepdim=True) + 1e-6) * wn.double()
+    ref = h @ W.double().t()
+    sd = torch.sqrt((qs.double()[:, None] ** 2 / 12) * (W.double() ** 2).sum(1)
+                    + (ws_.double() ** 2 / 12) * (h ** 2).sum(1)[:, None])
+    assert ((y - ref).abs() <= 6 * sd).all()
+
+
+def test_other_stream_and_graph():
+    for M in (1, 200):
+        a, w, sa, sw, b = inputs(M, 600, 1024, 5)
+        want = run(a, w, sa, sw, b, "bf16")
+        a, w, sa, sw, b = (t.cuda() for t in (a, w, sa, sw, b))
+        y, st = empty(M, 600, dtype=torch.bfloat16), status()
+        ws, n = scratch(tw.twell_q8_workspace_size(M, 600, 1024))
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            tw.twell_q8_matmul(a, sa, w, sw, b, M, 600, 1024, tw.TWELL_BF16, y, st, ws, n)
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
