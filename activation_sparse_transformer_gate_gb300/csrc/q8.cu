@@ -1,63 +1,486 @@
-// q8.cu -- product of 8-bit rows: y[m][n] = sa[m] sw[n] sum_k a[m][k] w[n][k].
+// q8.cu -- product of 8-bit rows: y[m][n] = sa[m] sw[n] sum_k a[m][k] w[n][k]
+// (+ bias[n]).
+//
+// sm_103a has no fast 8-bit integer tensor path, but an 8-bit integer is
+// exact in fp16, its products are exact in fp32, and so is their sum while
+// it stays below 2^24: the fp16 tensor cores (tcgen05 kind::f16, fp32
+// accumulators in TMEM) do this product at twice the width and full speed.
+// The operands stay 8-bit in memory and are widened on their way through
+// shared memory.
+//
+//   M <= ROWS_MAX   q8_rows_kernel: the weights stream once through
+//                   registers, dp4a (exact int32 sums).
+//   else            q8_mma_kernel: TMA brings 8-bit tiles into a ring; eight
+//                   warps widen them into fp16 tiles in the 128B-swizzled
+//                   layout of the MMA; one lane issues tcgen05.mma; four
+//                   warps read TMEM, scale and store.
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 #include "lm_kernels.h"
+#include "tcgen05.cuh"
 #include "vec16.cuh"
 
 namespace twell {
 
 namespace {
 
-// 64 x 64 outputs a CTA, 64 bytes of K at a time through shared memory, 4 x 4
-// outputs a thread, dp4a: the integer sum is exact (K <= 65536).
-template <typename E>
+// ---- few rows ----------------------------------------------------------------
+constexpr int ROWS_MAX = 8;  // rows of a that q8_rows_kernel takes
+constexpr int ROWS_N = 4;    // weight rows a warp reads together
+
+// A group of KS warps takes ROWS_N weight rows and splits K; MT rows of a
+// (M <= MT) are read again by every warp, from L1.  Sums are integers, so
+// the split leaves no trace.
+template <typename E, int MT>
 __global__ void __launch_bounds__(256)
-q8_tile_kernel(const int8_t *a, const int8_t *w, const float *sa, const float *sw,
-               const float *bias, int M, int N, int K, E *y) {
+q8_rows_kernel(const int8_t *a, const int8_t *w, const float *sa, const float *sw,
+               const float *bias, int M, int N, int K, int ks, E *y) {
   pdl_begin();
-  __shared__ int ta[64][17], tw[64][17];
-  const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
-  const int r = threadIdx.x >> 2, c = threadIdx.x & 3;  // staging: row, 16-byte vector
-  const int tm = threadIdx.x >> 4, tn = threadIdx.x & 15;
-  int acc[4][4] = {};
-  for (int k0 = 0; k0 < K; k0 += 64) {
-    const bool kin = k0 + c * 16 < K;
-    const uint4 va = kin && m0 + r < M ? *(const uint4 *)(a + (size_t)(m0 + r) * K + k0 + c * 16)
-                                       : make_uint4(0, 0, 0, 0);
-    const uint4 vw = kin && n0 + r < N ? *(const uint4 *)(w + (size_t)(n0 + r) * K + k0 + c * 16)
-                                       : make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    ta[r][c * 4] = va.x; ta[r][c * 4 + 1] = va.y; ta[r][c * 4 + 2] = va.z; ta[r][c * 4 + 3] = va.w;
-    tw[r][c * 4] = vw.x; tw[r][c * 4 + 1] = vw.y; tw[r][c * 4 + 2] = vw.z; tw[r][c * 4 + 3] = vw.w;
-    __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n0 = ((int)blockIdx.x * (8 / ks) + warp / ks) * ROWS_N;
+  const int part = warp % ks;
+  const int nv = K / 16;
+  int acc[ROWS_N][MT];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      int x[4], v[4];
+  for (int r = 0; r < ROWS_N; ++r)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = ta[tm + 16 * i][k];
-        v[i] = tw[tn + 16 * i][k];
+    for (int m = 0; m < MT; ++m) acc[r][m] = 0;
+  if (n0 < N) {
+    const uint4 *wr[ROWS_N];
+#pragma unroll
+    for (int r = 0; r < ROWS_N; ++r)
+      wr[r] = (const uint4 *)w + (size_t)min(n0 + r, N - 1) * nv;
+#pragma unroll 2
+    for (int v = part * 32 + lane; v < nv; v += ks * 32) {
+      uint4 x[ROWS_N];
+#pragma unroll
+      for (int r = 0; r < ROWS_N; ++r) x[r] = ldg_stream(wr[r] + v);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const uint4 t = __ldg((const uint4 *)a + (size_t)min(m, M - 1) * nv + v);
+#pragma unroll
+        for (int r = 0; r < ROWS_N; ++r) {
+          int s = acc[r][m];
+          s = __dp4a((int)x[r].x, (int)t.x, s);
+          s = __dp4a((int)x[r].y, (int)t.y, s);
+          s = __dp4a((int)x[r].z, (int)t.z, s);
+          acc[r][m] = __dp4a((int)x[r].w, (int)t.w, s);
+        }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(x[i], v[j], acc[i][j]);
     }
   }
+  __shared__ int sums[8][ROWS_N * MT];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int r = 0; r < ROWS_N; ++r)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + tm + 16 * i, n = n0 + tn + 16 * j;
-      if (m < M && n < N)
-        y[(size_t)m * N + n] =
-            from_f<E>((float)acc[i][j] * sa[m] * sw[n] + (bias ? bias[n] : 0.f));
+    for (int m = 0; m < MT; ++m) {
+      const int s = __reduce_add_sync(0xFFFFFFFFu, acc[r][m]);
+      if (lane == 0) sums[warp][r * MT + m] = s;
     }
+  if (ks > 1) __syncthreads();
+  else __syncwarp();
+  if (part != 0 || lane >= ROWS_N * MT || n0 >= N) return;
+  int s = 0;
+  for (int i = 0; i < ks; ++i) s += sums[warp + i][lane];
+  const int n = n0 + lane / MT, m = lane % MT;
+  if (n < N && m < M)
+    y[(size_t)m * N + n] = from_f<E>((float)s * sa[m] * sw[n] + (bias ? bias[n] : 0.f));
+}
+
+// ---- tensor cores --------------------------------------------------------------
+constexpr int BM = 128, BK = 64;
+constexpr int CONV_WARPS = 8;
+constexpr int THREADS = 32 * (6 + CONV_WARPS);  // TMA, MMA, 4 epilogue, conversion
+constexpr int F16_STAGES_MAX = 4, RAW_STAGES_MAX = 8;
+constexpr int ACC_COLS = 256;                   // TMEM columns of one accumulator
+constexpr int EPI_PITCH = 33;                   // fp32 staging row of the scalar epilogue
+
+struct Q8Maps {
+  CUtensorMap a, w;
+};
+
+// Shape of the pipeline (the same for every CTA).
+struct Q8Plan {
+  int bn;         // output columns per tile (a multiple of 16, at most 256)
+  int ar;         // rows of a that a tile holds (a multiple of 16, at most 128)
+  int kr;         // 64-wide k-blocks per 8-bit stage
+  int raw, f16;   // stages
+  int raw_bytes, f16_bytes;
+};
+
+struct Q8Params {
+  int M, N, K;
+  const float *sa, *sw, *bias;
+  void *y;
+  int32_t *status;
+  Q8Plan pl;
+};
+
+// 16 8-bit integers as fp16: a byte b + 128 put under the exponent of 1024
+// is the fp16 number 1152 + b.
+__device__ __forceinline__ void widen16(const uint4 &v, uint4 &lo, uint4 &hi) {
+  const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+  uint32_t out[8];
+  const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t b = in[i] ^ 0x80808080u;
+    uint32_t p = __byte_perm(b, 0x64646464u, 0x4140), q = __byte_perm(b, 0x64646464u, 0x4342);
+    const __half2 hp = __hsub2(*(__half2 *)&p, off), hq = __hsub2(*(__half2 *)&q, off);
+    out[2 * i] = *(const uint32_t *)&hp;
+    out[2 * i + 1] = *(const uint32_t *)&hq;
+  }
+  lo = make_uint4(out[0], out[1], out[2], out[3]);
+  hi = make_uint4(out[4], out[5], out[6], out[7]);
+}
+
+__device__ __forceinline__ void fence_async_proxy() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+template <typename E>
+__global__ void __launch_bounds__(THREADS, 1)
+q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Params p) {
+  pdl_begin();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const Q8Plan pl = p.pl;
+  uint8_t *f16 = smem;                                   // [f16][A 128 rows, W bn rows] x 128 B
+  uint8_t *raw = smem + pl.f16 * pl.f16_bytes;           // [raw][kr][A ar rows, W bn rows] x 64 B
+  float *s_epi = (float *)(raw + pl.raw * pl.raw_bytes); // [4][32][EPI_PITCH]
+  float *s_sw = s_epi + 4 * 32 * EPI_PITCH;              // [2][256] scale, bias of the columns
+  __shared__ uint64_t bars[2 * RAW_STAGES_MAX + 2 * F16_STAGES_MAX + 5];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  volatile int *abort_flag = &s_abort;
+  const uint32_t rfull = smem_u32(bars), rempty = rfull + 8 * RAW_STAGES_MAX;
+  const uint32_t ffull = rempty + 8 * RAW_STAGES_MAX, fempty = ffull + 8 * F16_STAGES_MAX;
+  const uint32_t tfull = fempty + 8 * F16_STAGES_MAX, tempty = tfull + 16, mma_done = tempty + 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  const int mb = (p.M + BM - 1) / BM, nb = (p.N + pl.bn - 1) / pl.bn;
+  const int tiles = mb * nb;  // M-blocks innermost: the CTAs in flight share few weight tiles
+  const int KT = (p.K + BK - 1) / BK, KR = (KT + pl.kr - 1) / pl.kr;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < pl.raw; ++i) {
+      mbar_init(rfull + 8 * i, 1);
+      mbar_init(rempty + 8 * i, CONV_WARPS);
+    }
+    for (int i = 0; i < pl.f16; ++i) {
+      mbar_init(ffull + 8 * i, CONV_WARPS);
+      mbar_init(fempty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(tfull + 8 * i, 1);
+      mbar_init(tempty + 8 * i, 4);
+    }
+    mbar_init(mma_done, 1);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&s_tmem)),
+                 "r"(2 * ACC_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+
+  if (warp == 0) {
+    // ------------------------------------------------------ TMA producer --
+    if (lane == 0) {
+      int st = 0;
+      uint32_t ph = 0;
+      long issued = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        const int m0 = (t % mb) * BM, n0 = (t / mb) * pl.bn;
+        for (int g = 0; g < KR; ++g) {
+          if (!mbar_wait(rempty + 8 * st, ph ^ 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          const int sub = min(pl.kr, KT - g * pl.kr);
+          const uint32_t bar = rfull + 8 * st;
+          mbar_expect_tx(bar, (uint32_t)(sub * (pl.ar + pl.bn) * BK));
+          uint32_t dst = smem_u32(raw + st * pl.raw_bytes);
+          for (int i = 0; i < sub; ++i) {
+            const int k0 = (g * pl.kr + i) * BK;
+            tma_load_2d(dst, &maps.a, k0, m0, bar);
+            tma_load_2d(dst + pl.ar * BK, &maps.w, k0, n0, bar);
+            dst += (pl.ar + pl.bn) * BK;
+          }
+          ++issued;
+          if (++st == pl.raw) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      // after an abort: no copy may be in flight when the CTA exits
+      if (!ok) {
+        for (int s = 0; s < pl.raw && s < issued; ++s) {
+          const long last = s + (long)pl.raw * ((issued - 1 - s) / pl.raw);
+          const uint32_t par = (uint32_t)((last / pl.raw) & 1);
+          const uint64_t t0 = global_timer();
+          while (!mbar_try(rfull + 8 * s, par) && global_timer() - t0 < DRAIN_LIMIT_NS) {
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // --------------------------------------------------------- MMA issuer --
+    if (lane == 0) {
+      const uint32_t idesc = make_idesc(BM, pl.bn, false, false, true);
+      int st = 0, lt = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++lt) {
+        const int buf = lt & 1;
+        if (!mbar_wait(tempty + 8 * buf, ((uint32_t)(lt >> 1) & 1) ^ 1, abort_flag, p.status))
+          break;
+        tc_fence_after();
+        const uint32_t acc = tmem + (uint32_t)(buf * ACC_COLS);
+        for (int kt = 0; kt < KT; ++kt) {
+          if (!mbar_wait(ffull + 8 * st, ph, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t base = smem_u32(f16 + st * pl.f16_bytes);
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk)
+            mma_bf16(acc, sw128_desc(base + kk * 32, 16, 1024),
+                     sw128_desc(base + BM * 128 + kk * 32, 16, 1024), idesc,
+                     (kt > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(fempty + 8 * st);
+          if (++st == pl.f16) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+        if (!ok) break;
+        mma_commit(tfull + 8 * buf);
+      }
+      // all MMAs issued by this thread are complete before TMEM is freed
+      mma_commit(mma_done);
+      const uint64_t t0 = global_timer();
+      while (!mbar_try(mma_done, 0) && global_timer() - t0 < DRAIN_LIMIT_NS) {
+      }
+    }
+  } else if (warp < 6) {
+    // ------------------------------------------------------------ epilogue --
+    const int q = warp & 3;  // TMEM lane quadrant of this warp
+    const int et = threadIdx.x - 64;
+    float *stage = s_epi + q * 32 * EPI_PITCH;
+    const bool vec = (size_t)p.N * sizeof(E) % 16 == 0;  // rows of y are 16-byte aligned
+    int lt = 0;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++lt) {
+      const int m0 = (t % mb) * BM, n0 = (t / mb) * pl.bn;
+      const int buf = lt & 1;
+      const int m = m0 + q * 32 + lane;
+      epi_bar();
+      for (int c = et; c < pl.bn; c += 128) {
+        s_sw[c] = n0 + c < p.N ? p.sw[n0 + c] : 0.f;
+        s_sw[256 + c] = p.bias && n0 + c < p.N ? p.bias[n0 + c] : 0.f;
+      }
+      epi_bar();
+      const float sa = m < p.M ? p.sa[m] : 0.f;
+      const bool ok = epi_all(mbar_wait(tfull + 8 * buf, (uint32_t)(lt >> 1) & 1, abort_flag,
+                                        p.status));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * ACC_COLS);
+      if (m0 + q * 32 < p.M) {  // (uniform for the warp)
+        for (int c0 = 0; c0 < pl.bn; c0 += 32) {
+          float v[32];
+          tmem_ld32(acc + c0, v);
+          const int n = n0 + c0, cols = min(pl.bn - c0, min(32, p.N - n));
+          if (cols <= 0) break;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int c = (c0 + i) & 255;  // (past the tile: not stored)
+            v[i] = v[i] * sa * s_sw[c] + s_sw[256 + c];
+          }
+          if (vec && cols % VEC16<E> == 0) {
+            if (m < p.M) {
+              uint4 *dst = (uint4 *)((E *)p.y + (size_t)m * p.N + n);
+#pragma unroll
+              for (int i = 0; i < 32 / VEC16<E>; ++i) {
+                if (i * VEC16<E> >= cols) break;
+                float f[VEC16<E>];
+#pragma unroll
+                for (int j = 0; j < VEC16<E>; ++j) f[j] = v[i * VEC16<E> + j];
+                dst[i] = pack16(f, (E *)nullptr);
+              }
+            }
+          } else {  // through shared memory: a warp stores 32 columns of a row at a time
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) stage[lane * EPI_PITCH + i] = v[i];
+            __syncwarp();
+            const int rows = min(32, p.M - m0 - q * 32);
+            if (lane < cols) {
+              E *dst = (E *)p.y + (size_t)(m0 + q * 32) * p.N + n + lane;
+              for (int r = 0; r < rows; ++r)
+                dst[(size_t)r * p.N] = from_f<E>(stage[r * EPI_PITCH + lane]);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tempty + 8 * buf);
+    }
+  } else {
+    // ---------------------------------------------------------- conversion --
+    const int ct = threadIdx.x - 192;
+    const int vecs = (pl.ar + pl.bn) * (BK / 16);  // 16-byte vectors of a k-block
+    constexpr int CT = 32 * CONV_WARPS, NV = (BM + 256) * (BK / 16) / CT;
+    int rs = 0, fs = 0;
+    uint32_t rp = 0, fp = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      for (int kt = 0; kt < KT; ++kt) {
+        const int sub = kt % pl.kr;
+        if (sub == 0) ok = mbar_wait(rfull + 8 * rs, rp, abort_flag, p.status);
+        if (!ok) break;
+        const uint4 *src = (const uint4 *)(raw + rs * pl.raw_bytes + sub * (pl.ar + pl.bn) * BK);
+        uint4 x[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (ct + i * CT < vecs) x[i] = src[ct + i * CT];
+        ok = mbar_wait(fempty + 8 * fs, fp ^ 1, abort_flag, p.status);
+        if (!ok) break;
+        uint8_t *dst = f16 + fs * pl.f16_bytes;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int v = ct + i * CT;
+          if (v >= vecs) break;
+          const int r = v >> 2, c = (v & 3) * 2;
+          // row r of a, or row r - ar of w behind the tile of a
+          uint8_t *row = dst + (size_t)(r < pl.ar ? r : BM + r - pl.ar) * 128;
+          uint4 lo, hi;
+          widen16(x[i], lo, hi);
+          *(uint4 *)(row + ((c ^ (r & 7)) * 16)) = lo;
+          *(uint4 *)(row + (((c + 1) ^ (r & 7)) * 16)) = hi;
+        }
+        fence_async_proxy();  // the MMA reads through the async proxy
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(ffull + 8 * fs);
+          if (sub == pl.kr - 1 || kt == KT - 1) mbar_arrive(rempty + 8 * rs);
+        }
+        if (++fs == pl.f16) {
+          fs = 0;
+          fp ^= 1;
+        }
+        if ((sub == pl.kr - 1 || kt == KT - 1) && ++rs == pl.raw) {
+          rs = 0;
+          rp ^= 1;
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(2 * ACC_COLS)
+                 : "memory");
+  }
+}
+
+// [rows][K] 8-bit matrix, boxes of 64 columns and `box` rows.
+bool make_map8(CUtensorMap *m, const void *base, int rows, int K, int box) {
+  EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)K};
+  cuuint32_t bx[2] = {BK, (cuuint32_t)box};
+  cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, bx, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int SMEM_FIXED = 1024 + 4 * 32 * EPI_PITCH * 4 + 2 * 256 * 4;
+constexpr int SMEM_MAX = 225 * 1024;
+
+Q8Plan plan_of(int M, int N, int K) {
+  Q8Plan pl;
+  const int mb = (M + BM - 1) / BM, sms = num_sms();
+  pl.ar = mb > 1 ? BM : (M + 15) / 16 * 16;
+  // tile width: the least (rounds over the SMs) x (width + the a tile's share)
+  long best = 0;
+  pl.bn = 0;
+  for (int bn = 256; bn >= 16; bn -= 16) {
+    const long tiles = (long)mb * ((N + bn - 1) / bn);
+    const long cost = (tiles + sms - 1) / sms * (bn + 32);
+    if (pl.bn == 0 || cost < best) {
+      best = cost;
+      pl.bn = bn;
+    }
+  }
+  const int sub = (pl.ar + pl.bn) * BK, KT = (K + BK - 1) / BK;
+  pl.kr = 1;
+  while (pl.kr < 4 && pl.kr * 2 * sub <= 24 * 1024 && pl.kr * 2 <= KT) pl.kr *= 2;
+  pl.raw_bytes = pl.kr * sub;
+  pl.f16_bytes = BM * 128 + pl.bn * 128;
+  pl.f16 = 2;
+  const int left = SMEM_MAX - SMEM_FIXED - pl.f16 * pl.f16_bytes;
+  pl.raw = left / pl.raw_bytes;
+  if (pl.raw > RAW_STAGES_MAX) pl.raw = RAW_STAGES_MAX;
+  return pl;
+}
+
+template <typename E>
+cudaError_t mma_t(const Q8Args &a, cudaStream_t s) {
+  Q8Params p;
+  p.M = a.M; p.N = a.N; p.K = a.K; p.sa = a.ascale; p.sw = a.wscale; p.bias = a.bias; p.y = a.y;
+  p.status = a.status;
+  p.pl = plan_of(a.M, a.N, a.K);
+  Q8Maps maps;
+  if (!make_map8(&maps.a, a.aq, a.M, a.K, p.pl.ar) || !make_map8(&maps.w, a.wq, a.N, a.K, p.pl.bn))
+    return cudaErrorInvalidValue;
+  static const cudaError_t attr = cudaFuncSetAttribute(
+      q8_mma_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX);
+  if (attr != cudaSuccess) return attr;
+  const long long tiles =
+      (long long)((a.M + BM - 1) / BM) * ((a.N + p.pl.bn - 1) / p.pl.bn);
+  if (tiles > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  const int grid = tiles < num_sms() ? (int)tiles : num_sms();
+  const size_t smem =
+      SMEM_FIXED + (size_t)p.pl.f16 * p.pl.f16_bytes + (size_t)p.pl.raw * p.pl.raw_bytes;
+  return launch_k(q8_mma_kernel<E>, dim3(grid), dim3(THREADS), smem, s, maps, p);
+}
+
+template <typename E, int MT>
+cudaError_t rows_t(const Q8Args &a, cudaStream_t s) {
+  const int groups = (a.N + ROWS_N - 1) / ROWS_N;
+  // warps that share K: until 16 warps an SM, while each has 512 bytes a row
+  int ks = 1;
+  while (ks < 8 && (long long)groups * ks < 16ll * num_sms() && a.K >= ks * 2 * 512) ks *= 2;
+  const int per = 8 / ks;
+  return launch_k(q8_rows_kernel<E, MT>, dim3((groups + per - 1) / per), dim3(256), 0, s, a.aq,
+                  a.wq, a.ascale, a.wscale, a.bias, a.M, a.N, a.K, ks, (E *)a.y);
 }
 
 template <typename E>
 cudaError_t matmul_t(const Q8Args &a, cudaStream_t s) {
-  return launch_k(q8_tile_kernel<E>, dim3((a.N + 63) / 64, (a.M + 63) / 64), dim3(256), 0, s, a.aq,
-                  a.wq, a.ascale, a.wscale, a.bias, a.M, a.N, a.K, (E *)a.y);
+  if (a.M == 1) return rows_t<E, 1>(a, s);
+  if (a.M == 2) return rows_t<E, 2>(a, s);
+  if (a.M <= 4) return rows_t<E, 4>(a, s);
+  if (a.M <= ROWS_MAX) return rows_t<E, 8>(a, s);
+  return mma_t<E>(a, s);
 }
 
 }  // namespace

@@ -48,7 +48,6 @@
 // of its own) for the copies and MMAs it has in flight, frees its TMEM and
 // returns.  The four epilogue warps take the outcome of each wait together,
 // so they leave their loop at the same tile.
-#include <cuda.h>
 #include <cuda_fp16.h>
 #include <stdio.h>
 #include <string.h>
@@ -57,6 +56,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "tcgen05.cuh"
 #include "test_hooks.h"
 
 namespace twell {
@@ -67,137 +67,12 @@ constexpr int BM = 128, BK = 64, NTHREADS = 192;
 // bf16 elements per row of the EPI_U g staging: 32 columns, a spare element
 // for scattered slots outside the block, padding to 16 bytes
 constexpr int GZ_STRIDE = 40;
-// Limit of a pipeline wait (a build may shorten it to make the waits run out
-// on a sane input: the timeout path is then exercised without a fault).
-#ifndef TWELL_WAIT_LIMIT_NS
-#define TWELL_WAIT_LIMIT_NS 2000000000ull
-#endif
-constexpr uint64_t WAIT_LIMIT_NS = TWELL_WAIT_LIMIT_NS;
-// Limit of the waits for work already in flight before a CTA exits (TMA
-// copies into shared memory, MMAs writing TMEM): always long, since leaving
-// earlier would free memory that the hardware still writes.
-constexpr uint64_t DRAIN_LIMIT_NS = 2000000000ull;
-
 enum Epi { EPI_PACK = 0, EPI_GU = 1, EPI_DOWN = 2, EPI_F32 = 3, EPI_U = 4, EPI_DH = 5, EPI_DX = 6,
            EPI_DW = 7, EPI_DHS = 8 };
 // fp32 elements per row of the EPI_DHS accumulator staging (32 columns; the
 // 144-byte stride keeps the 16-byte stores of 8 consecutive rows on
 // distinct banks)
 constexpr int DHS_STRIDE = 36;
-
-// ---------------------------------------------------------------- PTX ----
-__device__ __forceinline__ uint32_t smem_u32(const void *p) {
-  return (uint32_t)__cvta_generic_to_shared(p);
-}
-__device__ __forceinline__ uint64_t global_timer() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-  return t;
-}
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// Bounded wait.  Returns false (and raises the CTA-wide abort flag and the
-// device status) when the limit expires or another role has aborted.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                          int32_t *status) {
-  if (mbar_try(bar, parity)) return true;
-  const uint64_t t0 = global_timer();
-  while (true) {
-    if (mbar_try(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (global_timer() - t0 > WAIT_LIMIT_NS) {
-      *abort_flag = 1;
-      set_status(status, TWELL_ERR_TIMEOUT);
-      return false;
-    }
-  }
-}
-
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int c0, int c1,
-                                            uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"((uint64_t)map), "r"(c0), "r"(c1), "r"(bar)
-      : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-
-// Shared-memory matrix descriptor of a 128B-swizzled operand tile.
-//  [0,14) start>>4  [16,30) LBO>>4  [32,46) SBO>>4  [46,48) version 1
-//  [61,64) layout 2 = SWIZZLE_128B
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
-}
-
-// Instruction descriptor, kind::f16: D=f32 (bits 4-5), A and B both bf16
-// (bits 7-9 and 10-12 = 1) or both fp16 (= 0), A and B each K- or MN-major
-// (bits 15 and 16), N>>3 at bit 17, M>>4 at bit 24.
-__host__ __device__ constexpr uint32_t make_idesc(int M, int N, bool a_mn, bool b_mn, bool f16) {
-  return (1u << 4) | ((f16 ? 0u : 1u) << 7) | ((f16 ? 0u : 1u) << 10) |
-         ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
-         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-__device__ __forceinline__ void mma_bf16(uint32_t dtmem, uint64_t adesc, uint64_t bdesc,
-                                         uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(dtmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-      : "memory");
-}
-
-// 32 consecutive fp32 accumulator columns of this thread's TMEM lane.  The
-// wait is inside the same asm statement, so no use of the outputs can be
-// scheduled before the load has completed.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      "tcgen05.wait::ld.sync.aligned;\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
 
 // The K slots of one (row, tile) with vector loads (K in {1,2,4,8,16,32}; a
 // slot row starts at a multiple of its own size, so each load is aligned):
@@ -275,25 +150,6 @@ __device__ __forceinline__ void store_f16x32(__half *dst, const float (&v)[32], 
 #pragma unroll
   for (int v4 = 0; v4 < 4; ++v4)
     d4[v4] = make_uint4(w[4 * v4], w[4 * v4 + 1], w[4 * v4 + 2], w[4 * v4 + 3]);
-}
-
-__device__ __forceinline__ void epi_bar() {  // named barrier of the 4 epilogue warps
-  asm volatile("bar.sync 1, 128;" ::: "memory");
-}
-
-// The same barrier with an AND of v over the 128 epilogue threads: every
-// thread gets the same answer, so a decision taken on it is uniform (the
-// warp-collective tcgen05.ld and the named barrier need all four warps on
-// the same path).
-__device__ __forceinline__ bool epi_all(bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred q, 1, 128, p;\n"
-      " selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"((uint32_t)v)
-      : "memory");
-  return r != 0;
 }
 
 // --------------------------------------------------------------- params --
@@ -1328,25 +1184,6 @@ int num_sms() {
 }
 
 namespace {
-
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                              const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                              const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn() {
-  static EncodeFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = (EncodeFn)f;
-  });
-  return fn;
-}
 
 // 2-D bf16 tensor map over a row-major [rows][cols] matrix, box {bc, br},
 // 128-byte swizzle (bc * 2 == 128).
