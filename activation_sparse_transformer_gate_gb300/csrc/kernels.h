@@ -215,7 +215,8 @@ enum KernelId {
   KID_Q8_MATMUL = 30,
   KID_DISTILL_FWD = 31,
   KID_DISTILL_BWD = 32,
-  KID_COUNT = 33
+  KID_Q8_WIDEN = 33,
+  KID_COUNT = 34
 };
 // Record a timing event after `launches` kernel launches of component `id`
 // (no-op unless enabled).

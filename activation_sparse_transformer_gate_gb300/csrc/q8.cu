@@ -15,6 +15,7 @@
 //                   layout of the MMA; one lane issues tcgen05.mma; four
 //                   warps read TMEM, scale and store.
 #include <cuda_fp16.h>
+#include <string.h>
 
 #include "common.cuh"
 #include "lm_kernels.h"
@@ -137,6 +138,81 @@ __device__ __forceinline__ void widen16(const uint4 &v, uint4 &lo, uint4 &hi) {
 
 __device__ __forceinline__ void fence_async_proxy() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// One warp's 32 accumulator rows (TMEM lane = row, from row m0 on) of a tile
+// of bn columns from n0 on: scaled, rounded and stored.  Rows of y that are
+// 16-byte aligned take vectors; otherwise the block goes through shared
+// memory and the warp stores 32 columns of a row at a time.
+template <typename E>
+__device__ __forceinline__ void store_tile(const Q8Params &p, uint32_t acc, int m0, int n0,
+                                           float sa, const float *s_sw, float *stage) {
+  if (m0 >= p.M) return;  // (uniform for the warp)
+  const int lane = threadIdx.x & 31, bn = p.pl.bn, m = m0 + lane;
+  const bool vec = (size_t)p.N * sizeof(E) % 16 == 0;
+  for (int c0 = 0; c0 < bn; c0 += 32) {
+    float v[32];
+    tmem_ld32(acc + c0, v);
+    const int n = n0 + c0, cols = min(bn - c0, min(32, p.N - n));
+    if (cols <= 0) break;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const int c = (c0 + i) & 255;  // (past the tile: not stored)
+      v[i] = v[i] * sa * s_sw[c] + s_sw[256 + c];
+    }
+    if (vec && cols % VEC16<E> == 0) {
+      if (m < p.M) {
+        uint4 *dst = (uint4 *)((E *)p.y + (size_t)m * p.N + n);
+#pragma unroll
+        for (int i = 0; i < 32 / VEC16<E>; ++i) {
+          if (i * VEC16<E> >= cols) break;
+          float f[VEC16<E>];
+#pragma unroll
+          for (int j = 0; j < VEC16<E>; ++j) f[j] = v[i * VEC16<E> + j];
+          dst[i] = pack16(f, (E *)nullptr);
+        }
+      }
+    } else {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) stage[lane * EPI_PITCH + i] = v[i];
+      __syncwarp();
+      const int rows = min(32, p.M - m0);
+      if (lane < cols) {
+        E *dst = (E *)p.y + (size_t)m0 * p.N + n + lane;
+        for (int r = 0; r < rows; ++r) dst[(size_t)r * p.N] = from_f<E>(stage[r * EPI_PITCH + lane]);
+      }
+    }
+  }
+}
+
+// Scale and bias of a tile's columns, staged by the 128 epilogue threads.
+__device__ __forceinline__ void stage_columns(const Q8Params &p, int n0, float *s_sw, int et) {
+  epi_bar();
+  for (int c = et; c < p.pl.bn; c += 128) {
+    s_sw[c] = n0 + c < p.N ? p.sw[n0 + c] : 0.f;
+    s_sw[256 + c] = p.bias && n0 + c < p.N ? p.bias[n0 + c] : 0.f;
+  }
+  epi_bar();
+}
+
+// Converts the `vecs` 16-byte vectors of a k-block (rows of 64 8-bit values
+// at src) that are thread ct's of CT into fp16 rows of 128 bytes, 128B
+// swizzle, at dst; rows from `gap_at` on lie `gap` rows further.
+template <int NV, int CT>
+__device__ __forceinline__ void widen_rows(const uint4 (&x)[NV], uint8_t *dst, int ct, int vecs,
+                                           int gap_at, int gap) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = ct + i * CT;
+    if (v >= vecs) break;
+    const int r = v >> 2, c = (v & 3) * 2;
+    uint8_t *row = dst + (size_t)(r < gap_at ? r : r + gap) * 128;
+    uint4 lo, hi;
+    widen16(x[i], lo, hi);
+    *(uint4 *)(row + ((c ^ (r & 7)) * 16)) = lo;
+    *(uint4 *)(row + (((c + 1) ^ (r & 7)) * 16)) = hi;
+  }
 }
 
 template <typename E>
@@ -279,61 +355,19 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
     const int q = warp & 3;  // TMEM lane quadrant of this warp
     const int et = threadIdx.x - 64;
     float *stage = s_epi + q * 32 * EPI_PITCH;
-    const bool vec = (size_t)p.N * sizeof(E) % 16 == 0;  // rows of y are 16-byte aligned
     int lt = 0;
     for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++lt) {
       const int m0 = (t % mb) * BM, n0 = (t / mb) * pl.bn;
       const int buf = lt & 1;
       const int m = m0 + q * 32 + lane;
-      epi_bar();
-      for (int c = et; c < pl.bn; c += 128) {
-        s_sw[c] = n0 + c < p.N ? p.sw[n0 + c] : 0.f;
-        s_sw[256 + c] = p.bias && n0 + c < p.N ? p.bias[n0 + c] : 0.f;
-      }
-      epi_bar();
+      stage_columns(p, n0, s_sw, et);
       const float sa = m < p.M ? p.sa[m] : 0.f;
       const bool ok = epi_all(mbar_wait(tfull + 8 * buf, (uint32_t)(lt >> 1) & 1, abort_flag,
                                         p.status));
       if (!ok) break;
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * ACC_COLS);
-      if (m0 + q * 32 < p.M) {  // (uniform for the warp)
-        for (int c0 = 0; c0 < pl.bn; c0 += 32) {
-          float v[32];
-          tmem_ld32(acc + c0, v);
-          const int n = n0 + c0, cols = min(pl.bn - c0, min(32, p.N - n));
-          if (cols <= 0) break;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int c = (c0 + i) & 255;  // (past the tile: not stored)
-            v[i] = v[i] * sa * s_sw[c] + s_sw[256 + c];
-          }
-          if (vec && cols % VEC16<E> == 0) {
-            if (m < p.M) {
-              uint4 *dst = (uint4 *)((E *)p.y + (size_t)m * p.N + n);
-#pragma unroll
-              for (int i = 0; i < 32 / VEC16<E>; ++i) {
-                if (i * VEC16<E> >= cols) break;
-                float f[VEC16<E>];
-#pragma unroll
-                for (int j = 0; j < VEC16<E>; ++j) f[j] = v[i * VEC16<E> + j];
-                dst[i] = pack16(f, (E *)nullptr);
-              }
-            }
-          } else {  // through shared memory: a warp stores 32 columns of a row at a time
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) stage[lane * EPI_PITCH + i] = v[i];
-            __syncwarp();
-            const int rows = min(32, p.M - m0 - q * 32);
-            if (lane < cols) {
-              E *dst = (E *)p.y + (size_t)(m0 + q * 32) * p.N + n + lane;
-              for (int r = 0; r < rows; ++r)
-                dst[(size_t)r * p.N] = from_f<E>(stage[r * EPI_PITCH + lane]);
-            }
-          }
-        }
-      }
+      store_tile<E>(p, acc, m0 + q * 32, n0, sa, s_sw, stage);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(tempty + 8 * buf);
@@ -358,19 +392,8 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
           if (ct + i * CT < vecs) x[i] = src[ct + i * CT];
         ok = mbar_wait(fempty + 8 * fs, fp ^ 1, abort_flag, p.status);
         if (!ok) break;
-        uint8_t *dst = f16 + fs * pl.f16_bytes;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int v = ct + i * CT;
-          if (v >= vecs) break;
-          const int r = v >> 2, c = (v & 3) * 2;
-          // row r of a, or row r - ar of w behind the tile of a
-          uint8_t *row = dst + (size_t)(r < pl.ar ? r : BM + r - pl.ar) * 128;
-          uint4 lo, hi;
-          widen16(x[i], lo, hi);
-          *(uint4 *)(row + ((c ^ (r & 7)) * 16)) = lo;
-          *(uint4 *)(row + (((c + 1) ^ (r & 7)) * 16)) = hi;
-        }
+        // rows of a, then rows of w behind the (128-row) tile of a
+        widen_rows<NV, CT>(x, f16 + fs * pl.f16_bytes, ct, vecs, pl.ar, BM - pl.ar);
         fence_async_proxy();  // the MMA reads through the async proxy
         __syncwarp();
         if (lane == 0) {
@@ -399,37 +422,318 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
   }
 }
 
-// [rows][K] 8-bit matrix, boxes of 64 columns and `box` rows.
-bool make_map8(CUtensorMap *m, const void *base, int rows, int K, int box) {
+// ---- tensor cores, CTA pairs ----------------------------------------------------
+// More than 128 rows of a: two CTAs (one cluster) share a 256 x bn tile.
+// Each holds 128 rows of a and bn / 2 rows of w, the leader issues
+// cta_group::2 MMAs over both, and each CTA stores its 128 rows.  a is
+// widened once by q8_widen_kernel and comes by TMA as fp16; w is widened
+// here, each row once per CTA pair: per k-block an SM then moves 64 KB through
+// shared memory (w in 8 bits twice and in fp16 once, a once, the MMA's reads)
+// where one CTA that widened both operands for its own 128 x 256 tile would
+// move 144 KB for the same multiplications, and shared memory, not the
+// tensor cores, was its bound.
+//
+// A conversion warp's stores, their fence and its arrival take about 2000
+// cycles from end to end, four times a k-block's MMAs, so four groups of
+// warps take the k-blocks in turn.  They arrive at a barrier of their own
+// CTA and one thread passes that on to the leader: a release across the
+// cluster by the storing warps themselves waits for their stores once more
+// (704 TFLOP/s at M 8192, N 14336, K 4096 with two groups that did).
+constexpr int P_AS = 5, P_BS = 4, P_RS = 6;     // stages: a, w in fp16, w in 8 bits
+constexpr int P_GROUPS = 4, P_GROUP = 2;        // conversion groups, warps of a group
+constexpr int P_THREADS = 32 * (8 + P_GROUPS * P_GROUP);
+constexpr int P_TILE = 128 * 128;               // bytes of an fp16 stage (a or w)
+constexpr int P_RAW = 128 * BK;
+constexpr int P_SMEM = 1024 + P_AS * P_TILE + P_BS * P_TILE + P_RS * P_RAW +
+                       4 * 32 * EPI_PITCH * 4 + 2 * 256 * 4;
+
+__global__ void __launch_bounds__(256)
+q8_widen_kernel(const uint4 *a, size_t vecs, uint4 *out) {
+  pdl_begin();
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= vecs) return;
+  uint4 lo, hi;
+  widen16(ldg_stream<L2_FIRST>(a + i), lo, hi);
+  out[2 * i] = lo;
+  out[2 * i + 1] = hi;
+}
+
+// Stage and phase of a ring after `it` uses.
+template <int S>
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == S) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+template <typename E>
+__global__ void __launch_bounds__(P_THREADS, 1)
+q8_pair_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Params p) {
+  pdl_begin();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t *sa16 = smem, *sw16 = sa16 + P_AS * P_TILE, *raw = sw16 + P_BS * P_TILE;
+  float *s_epi = (float *)(raw + P_RS * P_RAW);
+  float *s_sw = s_epi + 4 * 32 * EPI_PITCH;
+  // Barriers of this CTA: a stage is full, a stage is free again.  Barriers
+  // of the leader, at which both CTAs arrive: a k-block's operands are ready,
+  // an accumulator has been read (tempty).
+  __shared__ uint64_t bars[2 * P_AS + 3 * P_BS + 2 * P_RS + 5];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  volatile int *abort_flag = &s_abort;
+  const uint32_t afull = smem_u32(bars), aempty = afull + 8 * P_AS;
+  const uint32_t wfull = aempty + 8 * P_AS, wempty = wfull + 8 * P_BS, ready = wempty + 8 * P_BS;
+  const uint32_t rfull = ready + 8 * P_BS, rempty = rfull + 8 * P_RS;
+  const uint32_t tfull = rempty + 8 * P_RS, tempty = tfull + 16, mma_done = tempty + 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)(blockIdx.x & 1);  // in the pair (clusters are consecutive CTAs)
+  const int bn = p.pl.bn, half = bn / 2;
+
+  const int mb = (p.M + 2 * BM - 1) / (2 * BM), nb = (p.N + bn - 1) / bn;
+  const int tiles = mb * nb;  // M-blocks innermost: the pairs in flight share few weight tiles
+  const int KT = (p.K + BK - 1) / BK;
+  const int pair = (int)blockIdx.x >> 1, pairs = (int)gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < P_AS; ++i) {
+      mbar_init(afull + 8 * i, 1);
+      mbar_init(aempty + 8 * i, 1);
+    }
+    for (int i = 0; i < P_BS; ++i) {
+      mbar_init(wfull + 8 * i, P_GROUP);
+      mbar_init(wempty + 8 * i, 1);
+      mbar_init(ready + 8 * i, 2);
+    }
+    for (int i = 0; i < P_RS; ++i) {
+      mbar_init(rfull + 8 * i, 1);
+      mbar_init(rempty + 8 * i, P_GROUP);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(tfull + 8 * i, 1);
+      mbar_init(tempty + 8 * i, 8);
+    }
+    mbar_init(mma_done, 1);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&s_tmem)),
+                 "r"(2 * ACC_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+
+  if (warp == 0 || warp == 6) {
+    // ------------------------------- TMA producers: w in 8 bits; a in fp16 --
+    if (lane == 0) {
+      const bool is_w = warp == 0;
+      const uint32_t full = is_w ? rfull : afull, empty = is_w ? rempty : aempty;
+      const int S = is_w ? P_RS : P_AS, bytes = is_w ? half * BK : P_TILE;
+      int st = 0;
+      uint32_t ph = 0;
+      long issued = 0;
+      bool ok = true;
+      for (int t = pair; t < tiles && ok; t += pairs) {
+        const int row = is_w ? (t / mb) * bn + rank * half : (t % mb) * 2 * BM + rank * BM;
+        for (int kt = 0; kt < KT; ++kt) {
+          if (!mbar_wait(empty + 8 * st, ph ^ 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          mbar_expect_tx(full + 8 * st, (uint32_t)bytes);
+          tma_load_2d(smem_u32(is_w ? raw + st * P_RAW : sa16 + st * P_TILE),
+                      is_w ? &maps.w : &maps.a, kt * BK, row, full + 8 * st);
+          ++issued;
+          if (++st == S) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (!ok) {  // no copy may be in flight when the CTA exits
+        for (int s = 0; s < S && s < issued; ++s) {
+          const long last = s + (long)S * ((issued - 1 - s) / S);
+          const uint32_t par = (uint32_t)((last / S) & 1);
+          const uint64_t t0 = global_timer();
+          while (!mbar_try(full + 8 * s, par) && global_timer() - t0 < DRAIN_LIMIT_NS) {
+          }
+        }
+      }
+    }
+  } else if (warp == 7) {
+    // ------------- tells the leader that this CTA's operands have arrived --
+    if (lane == 0) {
+      const uint32_t to = cluster_addr(ready, 0);
+      Ring<P_AS> a;
+      Ring<P_BS> w;
+      bool ok = true;
+      for (int t = pair; t < tiles && ok; t += pairs)
+        for (int kt = 0; kt < KT; ++kt) {
+          ok = mbar_wait(afull + 8 * a.at, a.phase, abort_flag, p.status) &&
+               mbar_wait(wfull + 8 * w.at, w.phase, abort_flag, p.status);
+          if (!ok) break;
+          mbar_arrive_cluster(to + 8 * w.at);
+          a.next();
+          w.next();
+        }
+    }
+  } else if (warp == 1) {
+    // --------------------------------------------------------- MMA issuer --
+    if (lane == 0 && rank == 0) {
+      const uint32_t idesc = make_idesc(2 * BM, bn, false, false, true);
+      Ring<P_AS> a;
+      Ring<P_BS> w;
+      int lt = 0;
+      bool ok = true;
+      for (int t = pair; t < tiles && ok; t += pairs, ++lt) {
+        const int buf = lt & 1;
+        if (!mbar_wait(tempty + 8 * buf, ((uint32_t)(lt >> 1) & 1) ^ 1, abort_flag,
+                               p.status))
+          break;
+        tc_fence_after();
+        const uint32_t acc = tmem + (uint32_t)(buf * ACC_COLS);
+        for (int kt = 0; kt < KT; ++kt) {
+          ok = mbar_wait(ready + 8 * w.at, w.phase, abort_flag, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t ab = smem_u32(sa16 + a.at * P_TILE), wb = smem_u32(sw16 + w.at * P_TILE);
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk)
+            mma_f16_pair(acc, sw128_desc(ab + kk * 32, 16, 1024), sw128_desc(wb + kk * 32, 16, 1024),
+                         idesc, (kt > 0 || kk > 0) ? 1u : 0u);
+          mma_commit_pair(aempty + 8 * a.at);
+          mma_commit_pair(wempty + 8 * w.at);
+          a.next();
+          w.next();
+        }
+        if (!ok) break;
+        mma_commit_pair(tfull + 8 * buf);
+      }
+      // all MMAs issued by this thread are complete before TMEM is freed
+      mma_commit_pair(mma_done);
+      const uint64_t t0 = global_timer();
+      while (!mbar_try(mma_done, 0) && global_timer() - t0 < DRAIN_LIMIT_NS) {
+      }
+    }
+  } else if (warp < 6) {
+    // ------------------------------------------------------------ epilogue --
+    const int q = warp & 3;  // TMEM lane quadrant of this warp
+    float *stage = s_epi + q * 32 * EPI_PITCH;
+    const uint32_t free = cluster_addr(tempty, 0);
+    int lt = 0;
+    for (int t = pair; t < tiles; t += pairs, ++lt) {
+      const int m0 = (t % mb) * 2 * BM + rank * BM + q * 32, n0 = (t / mb) * bn;
+      const int buf = lt & 1;
+      stage_columns(p, n0, s_sw, threadIdx.x - 64);
+      const float sa = m0 + lane < p.M ? p.sa[m0 + lane] : 0.f;
+      const bool ok = epi_all(mbar_wait(tfull + 8 * buf, (uint32_t)(lt >> 1) & 1,
+                                                abort_flag, p.status));
+      if (!ok) break;
+      tc_fence_after();
+      store_tile<E>(p, tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * ACC_COLS), m0, n0, sa,
+                    s_sw, stage);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(free + 8 * buf);
+    }
+  } else {
+    // ---------------------------------------------------------- conversion --
+    const int group = (warp - 8) / P_GROUP, ct = (threadIdx.x - 256) % (32 * P_GROUP);
+    constexpr int CT = 32 * P_GROUP, NV = 128 * (BK / 16) / CT;
+    const int vecs = half * (BK / 16);
+    Ring<P_BS> w;
+    Ring<P_RS> r;
+    Ring<P_GROUPS> turn;
+    bool ok = true;
+    for (int t = pair; t < tiles && ok; t += pairs)
+      for (int kt = 0; kt < KT; ++kt) {
+        if (turn.at == group) {
+          ok = mbar_wait(rfull + 8 * r.at, r.phase, abort_flag, p.status);
+          if (!ok) break;
+          const uint4 *src = (const uint4 *)(raw + r.at * P_RAW);
+          uint4 x[NV];
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+            if (ct + i * CT < vecs) x[i] = src[ct + i * CT];
+          ok = mbar_wait(wempty + 8 * w.at, w.phase ^ 1, abort_flag, p.status);
+          if (!ok) break;
+          widen_rows<NV, CT>(x, sw16 + w.at * P_TILE, ct, vecs, 128, 0);
+          fence_async_proxy();  // the MMA reads through the async proxy
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(wfull + 8 * w.at);
+            mbar_arrive(rempty + 8 * r.at);
+          }
+        }
+        w.next();
+        r.next();
+        turn.next();
+      }
+  }
+
+  // neither CTA leaves while the other may reach its shared memory or TMEM
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(2 * ACC_COLS)
+                 : "memory");
+  }
+}
+
+// [rows][K] matrix of 8-bit or (f16) 16-bit elements, boxes of 64 columns and
+// `box` rows; 16-bit boxes 128B-swizzled, as the MMA reads them.
+bool make_map(CUtensorMap *m, const void *base, int rows, int K, int box, bool f16) {
   EncodeFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)K};
+  cuuint64_t strides[1] = {(cuuint64_t)K * (f16 ? 2 : 1)};
   cuuint32_t bx[2] = {BK, (cuuint32_t)box};
   cuuint32_t es[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, bx, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+  return fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+            const_cast<void *>(base), dims, strides, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            f16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 constexpr int SMEM_FIXED = 1024 + 4 * 32 * EPI_PITCH * 4 + 2 * 256 * 4;
 constexpr int SMEM_MAX = 225 * 1024;
 
-Q8Plan plan_of(int M, int N, int K) {
-  Q8Plan pl;
-  const int mb = (M + BM - 1) / BM, sms = num_sms();
-  pl.ar = mb > 1 ? BM : (M + 15) / 16 * 16;
-  // tile width: the least (rounds over the SMs) x (width + the a tile's share)
+// Tile width for `units` CTAs or pairs that work at once: the least (rounds)
+// x (width + `fixed`, a tile's cost apart from its width).
+int tile_width(int M, int N, int rows, int units, int step, int fixed) {
+  const long mb = (M + rows - 1) / rows;
   long best = 0;
-  pl.bn = 0;
-  for (int bn = 256; bn >= 16; bn -= 16) {
-    const long tiles = (long)mb * ((N + bn - 1) / bn);
-    const long cost = (tiles + sms - 1) / sms * (bn + 32);
-    if (pl.bn == 0 || cost < best) {
+  int width = 0;
+  for (int bn = 256; bn >= step; bn -= step) {
+    const long tiles = mb * ((N + bn - 1) / bn);
+    const long cost = (tiles + units - 1) / units * (bn + fixed);
+    if (width == 0 || cost < best) {
       best = cost;
-      pl.bn = bn;
+      width = bn;
     }
   }
+  return width;
+}
+
+Q8Plan plan_of(int M, int N, int K) {
+  Q8Plan pl;
+  pl.ar = M > BM ? BM : (M + 15) / 16 * 16;
+  pl.bn = tile_width(M, N, BM, num_sms(), 16, 32);
   const int sub = (pl.ar + pl.bn) * BK, KT = (K + BK - 1) / BK;
   pl.kr = 1;
   while (pl.kr < 4 && pl.kr * 2 * sub <= 24 * 1024 && pl.kr * 2 <= KT) pl.kr *= 2;
@@ -449,7 +753,8 @@ cudaError_t mma_t(const Q8Args &a, cudaStream_t s) {
   p.status = a.status;
   p.pl = plan_of(a.M, a.N, a.K);
   Q8Maps maps;
-  if (!make_map8(&maps.a, a.aq, a.M, a.K, p.pl.ar) || !make_map8(&maps.w, a.wq, a.N, a.K, p.pl.bn))
+  if (!make_map(&maps.a, a.aq, a.M, a.K, p.pl.ar, false) ||
+      !make_map(&maps.w, a.wq, a.N, a.K, p.pl.bn, false))
     return cudaErrorInvalidValue;
   static const cudaError_t attr = cudaFuncSetAttribute(
       q8_mma_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX);
@@ -461,6 +766,53 @@ cudaError_t mma_t(const Q8Args &a, cudaStream_t s) {
   const size_t smem =
       SMEM_FIXED + (size_t)p.pl.f16 * p.pl.f16_bytes + (size_t)p.pl.raw * p.pl.raw_bytes;
   return launch_k(q8_mma_kernel<E>, dim3(grid), dim3(THREADS), smem, s, maps, p);
+}
+
+// Rows of a from which CTA pairs are used.
+constexpr int PAIR_MIN = 129;
+
+template <typename E>
+cudaError_t pair_t(const Q8Args &a, cudaStream_t s) {
+  static int most = 0;  // pairs that the GPU runs at once (its SM clusters may have odd ones out)
+  static const cudaError_t attr = [] {
+    cudaError_t e = cudaFuncSetAttribute(q8_pair_kernel<E>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (num_sms() / 2));
+    cfg.blockDim = dim3(P_THREADS);
+    cfg.dynamicSmemBytes = P_SMEM;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&most, q8_pair_kernel<E>, &cfg);
+    return e == cudaSuccess && most < 1 ? cudaErrorInvalidConfiguration : e;
+  }();
+  if (attr != cudaSuccess) return attr;
+  const size_t vecs = (size_t)a.M * a.K / 16;
+  if ((vecs + 255) / 256 > 0x7FFFFFFFull) return cudaErrorInvalidValue;
+  cudaError_t e = launch_k(q8_widen_kernel, dim3((unsigned)((vecs + 255) / 256)), dim3(256), 0, s,
+                           (const uint4 *)a.aq, vecs, (uint4 *)a.ws);
+  if (e != cudaSuccess) return e;
+  prof_mark(KID_Q8_WIDEN, s);
+  Q8Params p;
+  memset(&p, 0, sizeof(p));
+  p.M = a.M; p.N = a.N; p.K = a.K; p.sa = a.ascale; p.sw = a.wscale; p.bias = a.bias; p.y = a.y;
+  p.status = a.status;
+  p.pl.bn = tile_width(a.M, a.N, 2 * BM, most, 32, 32);
+  Q8Maps maps;
+  if (!make_map(&maps.a, a.ws, a.M, a.K, BM, true) ||
+      !make_map(&maps.w, a.wq, a.N, a.K, p.pl.bn / 2, false))
+    return cudaErrorInvalidValue;
+  const long long tiles =
+      (long long)((a.M + 2 * BM - 1) / (2 * BM)) * ((a.N + p.pl.bn - 1) / p.pl.bn);
+  if (tiles > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  const int grid = 2 * (tiles < most ? (int)tiles : most);
+  return launch_clusters(q8_pair_kernel<E>, dim3(grid), dim3(P_THREADS), P_SMEM, 2, s, maps, p);
 }
 
 template <typename E, int MT>
@@ -480,14 +832,14 @@ cudaError_t matmul_t(const Q8Args &a, cudaStream_t s) {
   if (a.M == 2) return rows_t<E, 2>(a, s);
   if (a.M <= 4) return rows_t<E, 4>(a, s);
   if (a.M <= ROWS_MAX) return rows_t<E, 8>(a, s);
-  return mma_t<E>(a, s);
+  return a.M < PAIR_MIN ? mma_t<E>(a, s) : pair_t<E>(a, s);
 }
 
 }  // namespace
 
 size_t q8_scratch(int M, int N, int K) {
-  (void)M; (void)N; (void)K;
-  return 256;
+  (void)N;
+  return M < PAIR_MIN ? 0 : ((size_t)M * K * 2 + 255) / 256 * 256;  // a in fp16
 }
 
 cudaError_t launch_q8_matmul(const Q8Args &a, cudaStream_t s) {

@@ -67,7 +67,7 @@ static const char *kKernelNames[KID_COUNT] = {
     "bwd_dense_dw_gemm",    "bwd_prep_rows",    "rowell_pack_dense",  "rowell_updown",
     "bwd_dh_gemm_sampled", "weights_to_f16", "embed_forward", "embed_sort_zero", "embed_runs",
     "embed_join", "add_rmsnorm_forward", "add_rmsnorm_backward", "rmsnorm_dw", "q8_quantize",
-    "q8_matmul", "distill_forward", "distill_backward"};
+    "q8_matmul", "distill_forward", "distill_backward", "q8_widen"};
 
 Workspace carve_workspace(void *base, int T, int D, int F, int C, int K, int dtype, int train,
                           int rows_cap) {

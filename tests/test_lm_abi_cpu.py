@@ -75,8 +75,10 @@ def test_q8(lib):
         (2, OFF, ALIGN), (3, None, ARG), (3, ODD, ALIGN), (4, ODD, ALIGN), (5, 0, ARG), (6, 0, ARG),
         (7, 0, ARG), (7, 24, ALIGN), (7, 65552, ARG), (8, 4, DTYPE), (9, None, ARG), (9, OFF, ALIGN),
         (10, None, ARG), (10, ODD, ALIGN)])
-    if ws:
-        refused(lib.twell_q8_matmul, good, [(11, None, WS), (11, A + 64, WS), (12, ws - 1, WS)])
+    ws = tw.twell_q8_workspace_size(300, 20, 64)      # many rows: scratch for the widened rows
+    assert ws >= 300 * 64 * 2
+    good = [A, A, A, A, A, 300, 20, 64, 1, A, A, A, ws, None]
+    refused(lib.twell_q8_matmul, good, [(11, None, WS), (11, A + 64, WS), (12, ws - 1, WS)])
     for bad in ((0, 1, 16), (1, 0, 16), (1, 1, 0), (1, 1, 20), (1, 1, 65552)):
         assert tw.twell_q8_workspace_size(*bad) == 0
 
