@@ -89,11 +89,119 @@ q8_rows_kernel(const int8_t *a, const int8_t *w, const float *sa, const float *s
     y[(size_t)m * N + n] = from_f<E>((float)s * sa[m] * sw[n] + (bias ? bias[n] : 0.f));
 }
 
+// 16 8-bit integers as fp16: b + 128 under the exponent of 1024 is the fp16
+// number 1152 + b.  A word's bytes come out in the order 0, 2, 1, 3: the sum
+// over k does not mind, as both operands take the same order.
+__device__ __forceinline__ void widen16(const uint4 &v, uint4 &lo, uint4 &hi) {
+  const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+  uint32_t out[8];
+  const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t p = (in[i] & 0x00FF00FFu) ^ 0x64806480u;
+    const uint32_t q = ((in[i] >> 8) & 0x00FF00FFu) ^ 0x64806480u;
+    const __half2 hp = __hsub2(*(const __half2 *)&p, off), hq = __hsub2(*(const __half2 *)&q, off);
+    out[2 * i] = *(const uint32_t *)&hp;
+    out[2 * i + 1] = *(const uint32_t *)&hq;
+  }
+  lo = make_uint4(out[0], out[1], out[2], out[3]);
+  hi = make_uint4(out[4], out[5], out[6], out[7]);
+}
+
+// ---- a batch of decoded rows ---------------------------------------------------
+// The weights still stream once from HBM and are used up in registers: a
+// warp takes 16 weight rows as the M side of m16n8k16 and NT groups of eight
+// rows of a as its N side.  A lane loads 16 consecutive bytes of a row, which
+// serve as its part of four MMAs' k (both operands take the same order of k).
+// A tile's KS warps split K and are added in order through shared memory.
+constexpr int FRAG_N = 16;
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9},"
+      " {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The fp16 words of 16 8-bit integers in the order that widen16 gives them.
+__device__ __forceinline__ void widen_words(const uint4 &v, uint32_t (&o)[8]) {
+  uint4 lo, hi;
+  widen16(v, lo, hi);
+  o[0] = lo.x; o[1] = lo.y; o[2] = lo.z; o[3] = lo.w;
+  o[4] = hi.x; o[5] = hi.y; o[6] = hi.z; o[7] = hi.w;
+}
+
+template <typename E, int NT>
+__global__ void __launch_bounds__(256)
+q8_frag_kernel(const int8_t *a, const int8_t *w, const float *sa, const float *sw,
+               const float *bias, int M, int N, int K, int ks, E *y) {
+  pdl_begin();
+  __shared__ float sums[8][NT * 8][FRAG_N + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int tile = (int)blockIdx.x * (8 / ks) + warp / ks, part = warp % ks;
+  const int n0 = tile * FRAG_N;
+  const int chunks = (K + 63) / 64;
+  float acc[NT][4];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+  if (n0 < N) {
+    constexpr int U = 2;
+    const int8_t *w0 = w + (size_t)min(n0 + g, N - 1) * K, *w1 = w + (size_t)min(n0 + g + 8, N - 1) * K;
+    for (int c = part; c < chunks; c += U * ks) {
+      uint4 x0[U], x1[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = (c + u * ks) * 64 + t * 16;
+        x0[u] = k < K ? ldg_stream(w0 + k) : make_uint4(0, 0, 0, 0);
+        x1[u] = k < K ? ldg_stream(w1 + k) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = (c + u * ks) * 64 + t * 16;
+        uint32_t p[8], q[8];
+        widen_words(x0[u], p);
+        widen_words(x1[u], q);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const int m = min(j * 8 + g, M - 1);
+          uint32_t r[8];
+          widen_words(k < K ? __ldg((const uint4 *)(a + (size_t)m * K + k)) : make_uint4(0, 0, 0, 0),
+                      r);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mma_16816(acc[j], p[2 * i], q[2 * i], p[2 * i + 1], q[2 * i + 1], r[2 * i],
+                      r[2 * i + 1]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      sums[warp][j * 8 + 2 * t + (i & 1)][g + (i >> 1) * 8] = acc[j][i];
+  __syncthreads();
+  // the CTA's tiles: 16 columns of y for each row of a
+  const int cols = 8 / ks * FRAG_N;
+  for (int i = threadIdx.x; i < M * cols; i += 256) {
+    const int m = i / cols, c = i - m * cols, n = (int)blockIdx.x * cols + c;
+    if (n >= N) continue;
+    float s = 0.f;
+    for (int r = 0; r < ks; ++r) s += sums[c / FRAG_N * ks + r][m][c % FRAG_N];
+    y[(size_t)m * N + n] = from_f<E>(s * sa[m] * sw[n] + (bias ? bias[n] : 0.f));
+  }
+}
+
 // ---- tensor cores --------------------------------------------------------------
 constexpr int BM = 128, BK = 64;
-constexpr int CONV_WARPS = 8;
-constexpr int THREADS = 32 * (6 + CONV_WARPS);  // TMA, MMA, 4 epilogue, conversion
-constexpr int F16_STAGES_MAX = 4, RAW_STAGES_MAX = 8;
+constexpr int GROUPS = 4, GROUP = 4;            // conversion groups, warps of a group
+constexpr int THREADS = 32 * (6 + GROUPS * GROUP);  // TMA, MMA, 4 epilogue, conversion
+constexpr int F16_STAGES_MAX = 8, RAW_STAGES_MAX = 24;
 constexpr int ACC_COLS = 256;                   // TMEM columns of one accumulator
 constexpr int EPI_PITCH = 33;                   // fp32 staging row of the scalar epilogue
 
@@ -105,8 +213,7 @@ struct Q8Maps {
 struct Q8Plan {
   int bn;         // output columns per tile (a multiple of 16, at most 256)
   int ar;         // rows of a that a tile holds (a multiple of 16, at most 128)
-  int kr;         // 64-wide k-blocks per 8-bit stage
-  int raw, f16;   // stages
+  int raw, f16;   // stages (a k-block each)
   int raw_bytes, f16_bytes;
 };
 
@@ -117,24 +224,6 @@ struct Q8Params {
   int32_t *status;
   Q8Plan pl;
 };
-
-// 16 8-bit integers as fp16: a byte b + 128 put under the exponent of 1024
-// is the fp16 number 1152 + b.
-__device__ __forceinline__ void widen16(const uint4 &v, uint4 &lo, uint4 &hi) {
-  const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-  uint32_t out[8];
-  const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t b = in[i] ^ 0x80808080u;
-    uint32_t p = __byte_perm(b, 0x64646464u, 0x4140), q = __byte_perm(b, 0x64646464u, 0x4342);
-    const __half2 hp = __hsub2(*(__half2 *)&p, off), hq = __hsub2(*(__half2 *)&q, off);
-    out[2 * i] = *(const uint32_t *)&hp;
-    out[2 * i + 1] = *(const uint32_t *)&hq;
-  }
-  lo = make_uint4(out[0], out[1], out[2], out[3]);
-  hi = make_uint4(out[4], out[5], out[6], out[7]);
-}
 
 __device__ __forceinline__ void fence_async_proxy() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -196,24 +285,61 @@ __device__ __forceinline__ void stage_columns(const Q8Params &p, int n0, float *
   epi_bar();
 }
 
-// Converts the `vecs` 16-byte vectors of a k-block (rows of 64 8-bit values
-// at src) that are thread ct's of CT into fp16 rows of 128 bytes, 128B
-// swizzle, at dst; rows from `gap_at` on lie `gap` rows further.
-template <int NV, int CT>
-__device__ __forceinline__ void widen_rows(const uint4 (&x)[NV], uint8_t *dst, int ct, int vecs,
-                                           int gap_at, int gap) {
+// One k-block's conversion by CT threads: the `vecs` 16-byte vectors (a
+// multiple of 32) of rows of 64 8-bit values at src become fp16 rows of 128
+// bytes (128B swizzle) at dst.  Thread ct takes vectors ct, ct + CT, ...: the
+// same place in every (CT / 4)th row, so the addresses differ by constants.
+template <int CT>
+__device__ __forceinline__ void widen_rows(const uint8_t *src, uint8_t *dst, int ct, int vecs) {
+  static_assert(CT % 32 == 0, "the swizzle phase of a thread's rows is one");
+  constexpr int B = 4;  // vectors in flight
+  const int r = ct >> 2, c = (ct & 3) * 2;
+  uint8_t *row = dst + r * 128;
+  uint4 *lo = (uint4 *)(row + ((c ^ (r & 7)) * 16)), *hi = (uint4 *)(row + (((c + 1) ^ (r & 7)) * 16));
+  const uint4 *p = (const uint4 *)src + ct;
+  for (int v = ct; v < vecs; v += B * CT) {
+    uint4 x[B];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = ct + i * CT;
-    if (v >= vecs) break;
-    const int r = v >> 2, c = (v & 3) * 2;
-    uint8_t *row = dst + (size_t)(r < gap_at ? r : r + gap) * 128;
-    uint4 lo, hi;
-    widen16(x[i], lo, hi);
-    *(uint4 *)(row + ((c ^ (r & 7)) * 16)) = lo;
-    *(uint4 *)(row + (((c + 1) ^ (r & 7)) * 16)) = hi;
+    for (int i = 0; i < B; ++i)
+      if (v + i * CT < vecs) x[i] = p[i * CT];
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+      if (v + i * CT < vecs) widen16(x[i], lo[i * (CT * 2)], hi[i * (CT * 2)]);
+    p += B * CT;
+    lo += B * CT * 2;
+    hi += B * CT * 2;
   }
 }
+
+// Stage and phase of a ring of S stages, for a user of every STEP-th stage.
+struct Ring {
+  int at;
+  uint32_t phase;
+  __device__ __forceinline__ Ring(int first, int S) : at(first % S), phase((first / S) & 1) {}
+  template <int STEP = 1>
+  __device__ __forceinline__ void next(int S) {
+    at += STEP;
+    while (at >= S) {
+      at -= S;
+      phase ^= 1;
+    }
+  }
+};
+
+// After an abort no copy may be in flight when the CTA exits: waits (bounded)
+// for the last load that was issued into each stage of a ring.
+__device__ __forceinline__ void drain_ring(uint32_t full, int S, long issued) {
+  for (int s = 0; s < S && s < issued; ++s) {
+    const uint32_t par = (uint32_t)(((issued - 1 - s) / S) & 1);
+    const uint64_t t0 = global_timer();
+    while (!mbar_try(full + 8 * s, par) && global_timer() - t0 < DRAIN_LIMIT_NS) {
+    }
+  }
+}
+
+// Address part of the swizzled operand descriptors (sw128_desc): adding to
+// the low word moves the start, 16 bytes a unit.
+__device__ __forceinline__ uint64_t desc_at(uint32_t saddr) { return sw128_desc(saddr, 16, 1024); }
 
 template <typename E>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -222,8 +348,11 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const Q8Plan pl = p.pl;
-  uint8_t *f16 = smem;                                   // [f16][A 128 rows, W bn rows] x 128 B
-  uint8_t *raw = smem + pl.f16 * pl.f16_bytes;           // [raw][kr][A ar rows, W bn rows] x 64 B
+  // An fp16 stage holds the ar rows of a, then the bn rows of w; the MMA's
+  // 128 rows of a run into those of w when ar < 128 (accumulator rows that
+  // are not stored).
+  uint8_t *f16 = smem;                                   // [f16][A ar rows, W bn rows] x 128 B
+  uint8_t *raw = smem + pl.f16 * pl.f16_bytes;           // [raw][A ar rows, W bn rows] x 64 B
   float *s_epi = (float *)(raw + pl.raw * pl.raw_bytes); // [4][32][EPI_PITCH]
   float *s_sw = s_epi + 4 * 32 * EPI_PITCH;              // [2][256] scale, bias of the columns
   __shared__ uint64_t bars[2 * RAW_STAGES_MAX + 2 * F16_STAGES_MAX + 5];
@@ -233,19 +362,19 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
   const uint32_t rfull = smem_u32(bars), rempty = rfull + 8 * RAW_STAGES_MAX;
   const uint32_t ffull = rempty + 8 * RAW_STAGES_MAX, fempty = ffull + 8 * F16_STAGES_MAX;
   const uint32_t tfull = fempty + 8 * F16_STAGES_MAX, tempty = tfull + 16, mma_done = tempty + 16;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   const int mb = (p.M + BM - 1) / BM, nb = (p.N + pl.bn - 1) / pl.bn;
   const int tiles = mb * nb;  // M-blocks innermost: the CTAs in flight share few weight tiles
-  const int KT = (p.K + BK - 1) / BK, KR = (KT + pl.kr - 1) / pl.kr;
+  const int KT = (p.K + BK - 1) / BK;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < pl.raw; ++i) {
       mbar_init(rfull + 8 * i, 1);
-      mbar_init(rempty + 8 * i, CONV_WARPS);
+      mbar_init(rempty + 8 * i, GROUP);
     }
     for (int i = 0; i < pl.f16; ++i) {
-      mbar_init(ffull + 8 * i, CONV_WARPS);
+      mbar_init(ffull + 8 * i, GROUP);
       mbar_init(fempty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -270,82 +399,72 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
 
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer --
-    if (lane == 0) {
-      int st = 0;
-      uint32_t ph = 0;
-      long issued = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        const int m0 = (t % mb) * BM, n0 = (t / mb) * pl.bn;
-        for (int g = 0; g < KR; ++g) {
-          if (!mbar_wait(rempty + 8 * st, ph ^ 1, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
-          const int sub = min(pl.kr, KT - g * pl.kr);
-          const uint32_t bar = rfull + 8 * st;
-          mbar_expect_tx(bar, (uint32_t)(sub * (pl.ar + pl.bn) * BK));
-          uint32_t dst = smem_u32(raw + st * pl.raw_bytes);
-          for (int i = 0; i < sub; ++i) {
-            const int k0 = (g * pl.kr + i) * BK;
-            tma_load_2d(dst, &maps.a, k0, m0, bar);
-            tma_load_2d(dst + pl.ar * BK, &maps.w, k0, n0, bar);
-            dst += (pl.ar + pl.bn) * BK;
-          }
-          ++issued;
-          if (++st == pl.raw) {
-            st = 0;
-            ph ^= 1;
-          }
+    const bool issues = elect_one();
+    const uint32_t raw0 = smem_u32(raw);
+    int st = 0;
+    uint32_t ph = 0;
+    long issued = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      const int m0 = (t % mb) * BM, n0 = (t / mb) * pl.bn;
+      for (int kt = 0; kt < KT; ++kt) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(rempty + 8 * st, ph ^ 1, abort_flag, p.status));
+        if (!ok) break;
+        const uint32_t bar = rfull + 8 * st, dst = raw0 + st * pl.raw_bytes;
+        if (issues) {
+          mbar_expect_tx(bar, (uint32_t)pl.raw_bytes);
+          tma_load_2d(dst, &maps.a, kt * BK, m0, bar);
+          tma_load_2d(dst + pl.ar * BK, &maps.w, kt * BK, n0, bar);
         }
-      }
-      // after an abort: no copy may be in flight when the CTA exits
-      if (!ok) {
-        for (int s = 0; s < pl.raw && s < issued; ++s) {
-          const long last = s + (long)pl.raw * ((issued - 1 - s) / pl.raw);
-          const uint32_t par = (uint32_t)((last / pl.raw) & 1);
-          const uint64_t t0 = global_timer();
-          while (!mbar_try(rfull + 8 * s, par) && global_timer() - t0 < DRAIN_LIMIT_NS) {
-          }
+        __syncwarp();
+        ++issued;
+        if (++st == pl.raw) {
+          st = 0;
+          ph ^= 1;
         }
       }
     }
+    if (!ok) drain_ring(rfull, pl.raw, issued);
   } else if (warp == 1) {
     // --------------------------------------------------------- MMA issuer --
-    if (lane == 0) {
+    {
+      const bool issues = elect_one();
       const uint32_t idesc = make_idesc(BM, pl.bn, false, false, true);
+      const uint64_t ad0 = desc_at(smem_u32(f16));
+      const uint32_t w_off = (uint32_t)(pl.ar * 128) >> 4;
       int st = 0, lt = 0;
       uint32_t ph = 0;
       bool ok = true;
       for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++lt) {
         const int buf = lt & 1;
-        if (!mbar_wait(tempty + 8 * buf, ((uint32_t)(lt >> 1) & 1) ^ 1, abort_flag, p.status))
-          break;
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(tempty + 8 * buf, ((uint32_t)(lt >> 1) & 1) ^ 1,
+                                               abort_flag, p.status));
+        if (!ok) break;
         tc_fence_after();
         const uint32_t acc = tmem + (uint32_t)(buf * ACC_COLS);
         for (int kt = 0; kt < KT; ++kt) {
-          if (!mbar_wait(ffull + 8 * st, ph, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(ffull + 8 * st, ph, abort_flag, p.status));
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t base = smem_u32(f16 + st * pl.f16_bytes);
+          const uint64_t ad = ad0 + (uint32_t)(st * pl.f16_bytes >> 4), wd = ad + w_off;
+          if (issues) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk)
-            mma_bf16(acc, sw128_desc(base + kk * 32, 16, 1024),
-                     sw128_desc(base + BM * 128 + kk * 32, 16, 1024), idesc,
-                     (kt > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(fempty + 8 * st);
+            for (int kk = 0; kk < BK / 16; ++kk)  // 32 bytes of a row a step
+              mma_bf16(acc, ad + 2 * kk, wd + 2 * kk, idesc, (kt > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(fempty + 8 * st);
+          }
+          __syncwarp();
           if (++st == pl.f16) {
             st = 0;
             ph ^= 1;
           }
         }
         if (!ok) break;
-        mma_commit(tfull + 8 * buf);
+        if (issues) mma_commit(tfull + 8 * buf);
+        __syncwarp();
       }
       // all MMAs issued by this thread are complete before TMEM is freed
-      mma_commit(mma_done);
+      if (issues) mma_commit(mma_done);
       const uint64_t t0 = global_timer();
       while (!mbar_try(mma_done, 0) && global_timer() - t0 < DRAIN_LIMIT_NS) {
       }
@@ -374,41 +493,23 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
     }
   } else {
     // ---------------------------------------------------------- conversion --
-    const int ct = threadIdx.x - 192;
+    // Four groups of warps take the k-blocks in turn.
+    const int group = (warp - 6) / GROUP, ct = (threadIdx.x - 192) % (32 * GROUP);
     const int vecs = (pl.ar + pl.bn) * (BK / 16);  // 16-byte vectors of a k-block
-    constexpr int CT = 32 * CONV_WARPS, NV = (BM + 256) * (BK / 16) / CT;
-    int rs = 0, fs = 0;
-    uint32_t rp = 0, fp = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      for (int kt = 0; kt < KT; ++kt) {
-        const int sub = kt % pl.kr;
-        if (sub == 0) ok = mbar_wait(rfull + 8 * rs, rp, abort_flag, p.status);
-        if (!ok) break;
-        const uint4 *src = (const uint4 *)(raw + rs * pl.raw_bytes + sub * (pl.ar + pl.bn) * BK);
-        uint4 x[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-          if (ct + i * CT < vecs) x[i] = src[ct + i * CT];
-        ok = mbar_wait(fempty + 8 * fs, fp ^ 1, abort_flag, p.status);
-        if (!ok) break;
-        // rows of a, then rows of w behind the (128-row) tile of a
-        widen_rows<NV, CT>(x, f16 + fs * pl.f16_bytes, ct, vecs, pl.ar, BM - pl.ar);
-        fence_async_proxy();  // the MMA reads through the async proxy
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(ffull + 8 * fs);
-          if (sub == pl.kr - 1 || kt == KT - 1) mbar_arrive(rempty + 8 * rs);
-        }
-        if (++fs == pl.f16) {
-          fs = 0;
-          fp ^= 1;
-        }
-        if ((sub == pl.kr - 1 || kt == KT - 1) && ++rs == pl.raw) {
-          rs = 0;
-          rp ^= 1;
-        }
+    const int mine = (tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+    Ring f(group, pl.f16), r(group, pl.raw);
+    for (long it = group; it < (long)mine * KT; it += GROUPS) {
+      if (!mbar_wait(rfull + 8 * r.at, r.phase, abort_flag, p.status)) break;
+      if (!mbar_wait(fempty + 8 * f.at, f.phase ^ 1, abort_flag, p.status)) break;
+      widen_rows<32 * GROUP>(raw + r.at * pl.raw_bytes, f16 + f.at * pl.f16_bytes, ct, vecs);
+      fence_async_proxy();  // the MMA reads through the async proxy
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(ffull + 8 * f.at);
+        mbar_arrive(rempty + 8 * r.at);
       }
+      f.next<GROUPS>(pl.f16);
+      r.next<GROUPS>(pl.raw);
     }
   }
 
@@ -458,19 +559,6 @@ q8_widen_kernel(const uint4 *a, size_t vecs, uint4 *out) {
   out[2 * i + 1] = hi;
 }
 
-// Stage and phase of a ring after `it` uses.
-template <int S>
-struct Ring {
-  int at = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void next() {
-    if (++at == S) {
-      at = 0;
-      phase ^= 1;
-    }
-  }
-};
-
 template <typename E>
 __global__ void __launch_bounds__(P_THREADS, 1)
 q8_pair_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Params p) {
@@ -491,7 +579,7 @@ q8_pair_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Pa
   const uint32_t wfull = aempty + 8 * P_AS, wempty = wfull + 8 * P_BS, ready = wempty + 8 * P_BS;
   const uint32_t rfull = ready + 8 * P_BS, rempty = rfull + 8 * P_RS;
   const uint32_t tfull = rempty + 8 * P_RS, tempty = tfull + 16, mma_done = tempty + 16;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = (int)(blockIdx.x & 1);  // in the pair (clusters are consecutive CTAs)
   const int bn = p.pl.bn, half = bn / 2;
 
@@ -499,6 +587,7 @@ q8_pair_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Pa
   const int tiles = mb * nb;  // M-blocks innermost: the pairs in flight share few weight tiles
   const int KT = (p.K + BK - 1) / BK;
   const int pair = (int)blockIdx.x >> 1, pairs = (int)gridDim.x >> 1;
+  const long its = (long)((tiles - pair + pairs - 1) / pairs) * KT;  // k-blocks of this pair
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < P_AS; ++i) {
@@ -537,92 +626,87 @@ q8_pair_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Pa
 
   if (warp == 0 || warp == 6) {
     // ------------------------------- TMA producers: w in 8 bits; a in fp16 --
-    if (lane == 0) {
-      const bool is_w = warp == 0;
-      const uint32_t full = is_w ? rfull : afull, empty = is_w ? rempty : aempty;
-      const int S = is_w ? P_RS : P_AS, bytes = is_w ? half * BK : P_TILE;
-      int st = 0;
-      uint32_t ph = 0;
-      long issued = 0;
-      bool ok = true;
-      for (int t = pair; t < tiles && ok; t += pairs) {
-        const int row = is_w ? (t / mb) * bn + rank * half : (t % mb) * 2 * BM + rank * BM;
-        for (int kt = 0; kt < KT; ++kt) {
-          if (!mbar_wait(empty + 8 * st, ph ^ 1, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
+    const bool issues = elect_one();
+    const bool is_w = warp == 0;
+    const uint32_t full = is_w ? rfull : afull, empty = is_w ? rempty : aempty;
+    const uint32_t dst0 = smem_u32(is_w ? raw : sa16), step = is_w ? P_RAW : P_TILE;
+    const int S = is_w ? P_RS : P_AS, bytes = is_w ? half * BK : P_TILE;
+    const CUtensorMap *map = is_w ? &maps.w : &maps.a;
+    int st = 0;
+    uint32_t ph = 0;
+    long issued = 0;
+    bool ok = true;
+    for (int t = pair; t < tiles && ok; t += pairs) {
+      const int row = is_w ? (t / mb) * bn + rank * half : (t % mb) * 2 * BM + rank * BM;
+      for (int kt = 0; kt < KT; ++kt) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty + 8 * st, ph ^ 1, abort_flag, p.status));
+        if (!ok) break;
+        if (issues) {
           mbar_expect_tx(full + 8 * st, (uint32_t)bytes);
-          tma_load_2d(smem_u32(is_w ? raw + st * P_RAW : sa16 + st * P_TILE),
-                      is_w ? &maps.w : &maps.a, kt * BK, row, full + 8 * st);
-          ++issued;
-          if (++st == S) {
-            st = 0;
-            ph ^= 1;
-          }
+          tma_load_2d(dst0 + st * step, map, kt * BK, row, full + 8 * st);
         }
-      }
-      if (!ok) {  // no copy may be in flight when the CTA exits
-        for (int s = 0; s < S && s < issued; ++s) {
-          const long last = s + (long)S * ((issued - 1 - s) / S);
-          const uint32_t par = (uint32_t)((last / S) & 1);
-          const uint64_t t0 = global_timer();
-          while (!mbar_try(full + 8 * s, par) && global_timer() - t0 < DRAIN_LIMIT_NS) {
-          }
+        __syncwarp();
+        ++issued;
+        if (++st == S) {
+          st = 0;
+          ph ^= 1;
         }
       }
     }
+    if (!ok) drain_ring(full, S, issued);
   } else if (warp == 7) {
     // ------------- tells the leader that this CTA's operands have arrived --
     if (lane == 0) {
       const uint32_t to = cluster_addr(ready, 0);
-      Ring<P_AS> a;
-      Ring<P_BS> w;
-      bool ok = true;
-      for (int t = pair; t < tiles && ok; t += pairs)
-        for (int kt = 0; kt < KT; ++kt) {
-          ok = mbar_wait(afull + 8 * a.at, a.phase, abort_flag, p.status) &&
-               mbar_wait(wfull + 8 * w.at, w.phase, abort_flag, p.status);
-          if (!ok) break;
-          mbar_arrive_cluster(to + 8 * w.at);
-          a.next();
-          w.next();
-        }
+      Ring a(0, P_AS), w(0, P_BS);
+      for (long it = 0; it < its; ++it) {
+        if (!mbar_wait(afull + 8 * a.at, a.phase, abort_flag, p.status) ||
+            !mbar_wait(wfull + 8 * w.at, w.phase, abort_flag, p.status))
+          break;
+        mbar_arrive_cluster(to + 8 * w.at);
+        a.next(P_AS);
+        w.next(P_BS);
+      }
     }
   } else if (warp == 1) {
     // --------------------------------------------------------- MMA issuer --
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      const bool issues = elect_one();
       const uint32_t idesc = make_idesc(2 * BM, bn, false, false, true);
-      Ring<P_AS> a;
-      Ring<P_BS> w;
+      const uint64_t ad0 = desc_at(smem_u32(sa16)), wd0 = desc_at(smem_u32(sw16));
+      Ring a(0, P_AS), w(0, P_BS);
       int lt = 0;
       bool ok = true;
       for (int t = pair; t < tiles && ok; t += pairs, ++lt) {
         const int buf = lt & 1;
-        if (!mbar_wait(tempty + 8 * buf, ((uint32_t)(lt >> 1) & 1) ^ 1, abort_flag,
-                               p.status))
-          break;
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(tempty + 8 * buf, ((uint32_t)(lt >> 1) & 1) ^ 1,
+                                               abort_flag, p.status));
+        if (!ok) break;
         tc_fence_after();
         const uint32_t acc = tmem + (uint32_t)(buf * ACC_COLS);
         for (int kt = 0; kt < KT; ++kt) {
-          ok = mbar_wait(ready + 8 * w.at, w.phase, abort_flag, p.status);
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(ready + 8 * w.at, w.phase, abort_flag, p.status));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t ab = smem_u32(sa16 + a.at * P_TILE), wb = smem_u32(sw16 + w.at * P_TILE);
+          const uint64_t ad = ad0 + (uint32_t)(a.at * (P_TILE >> 4));
+          const uint64_t wd = wd0 + (uint32_t)(w.at * (P_TILE >> 4));
+          if (issues) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk)
-            mma_f16_pair(acc, sw128_desc(ab + kk * 32, 16, 1024), sw128_desc(wb + kk * 32, 16, 1024),
-                         idesc, (kt > 0 || kk > 0) ? 1u : 0u);
-          mma_commit_pair(aempty + 8 * a.at);
-          mma_commit_pair(wempty + 8 * w.at);
-          a.next();
-          w.next();
+            for (int kk = 0; kk < BK / 16; ++kk)
+              mma_f16_pair(acc, ad + 2 * kk, wd + 2 * kk, idesc, (kt > 0 || kk > 0) ? 1u : 0u);
+            mma_commit_pair(aempty + 8 * a.at);
+            mma_commit_pair(wempty + 8 * w.at);
+          }
+          __syncwarp();
+          a.next(P_AS);
+          w.next(P_BS);
         }
         if (!ok) break;
-        mma_commit_pair(tfull + 8 * buf);
+        if (issues) mma_commit_pair(tfull + 8 * buf);
+        __syncwarp();
       }
       // all MMAs issued by this thread are complete before TMEM is freed
-      mma_commit_pair(mma_done);
+      if (issues) mma_commit_pair(mma_done);
       const uint64_t t0 = global_timer();
       while (!mbar_try(mma_done, 0) && global_timer() - t0 < DRAIN_LIMIT_NS) {
       }
@@ -651,36 +735,21 @@ q8_pair_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Pa
   } else {
     // ---------------------------------------------------------- conversion --
     const int group = (warp - 8) / P_GROUP, ct = (threadIdx.x - 256) % (32 * P_GROUP);
-    constexpr int CT = 32 * P_GROUP, NV = 128 * (BK / 16) / CT;
     const int vecs = half * (BK / 16);
-    Ring<P_BS> w;
-    Ring<P_RS> r;
-    Ring<P_GROUPS> turn;
-    bool ok = true;
-    for (int t = pair; t < tiles && ok; t += pairs)
-      for (int kt = 0; kt < KT; ++kt) {
-        if (turn.at == group) {
-          ok = mbar_wait(rfull + 8 * r.at, r.phase, abort_flag, p.status);
-          if (!ok) break;
-          const uint4 *src = (const uint4 *)(raw + r.at * P_RAW);
-          uint4 x[NV];
-#pragma unroll
-          for (int i = 0; i < NV; ++i)
-            if (ct + i * CT < vecs) x[i] = src[ct + i * CT];
-          ok = mbar_wait(wempty + 8 * w.at, w.phase ^ 1, abort_flag, p.status);
-          if (!ok) break;
-          widen_rows<NV, CT>(x, sw16 + w.at * P_TILE, ct, vecs, 128, 0);
-          fence_async_proxy();  // the MMA reads through the async proxy
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(wfull + 8 * w.at);
-            mbar_arrive(rempty + 8 * r.at);
-          }
-        }
-        w.next();
-        r.next();
-        turn.next();
+    Ring w(group, P_BS), r(group, P_RS);
+    for (long it = group; it < its; it += P_GROUPS) {
+      if (!mbar_wait(rfull + 8 * r.at, r.phase, abort_flag, p.status)) break;
+      if (!mbar_wait(wempty + 8 * w.at, w.phase ^ 1, abort_flag, p.status)) break;
+      widen_rows<32 * P_GROUP>(raw + r.at * P_RAW, sw16 + w.at * P_TILE, ct, vecs);
+      fence_async_proxy();  // the MMA reads through the async proxy
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(wfull + 8 * w.at);
+        mbar_arrive(rempty + 8 * r.at);
       }
+      w.next<P_GROUPS>(P_BS);
+      r.next<P_GROUPS>(P_RS);
+    }
   }
 
   // neither CTA leaves while the other may reach its shared memory or TMEM
@@ -730,18 +799,19 @@ int tile_width(int M, int N, int rows, int units, int step, int fixed) {
   return width;
 }
 
-Q8Plan plan_of(int M, int N, int K) {
+Q8Plan plan_of(int M, int N) {
   Q8Plan pl;
   pl.ar = M > BM ? BM : (M + 15) / 16 * 16;
   pl.bn = tile_width(M, N, BM, num_sms(), 16, 32);
-  const int sub = (pl.ar + pl.bn) * BK, KT = (K + BK - 1) / BK;
-  pl.kr = 1;
-  while (pl.kr < 4 && pl.kr * 2 * sub <= 24 * 1024 && pl.kr * 2 <= KT) pl.kr *= 2;
-  pl.raw_bytes = pl.kr * sub;
-  pl.f16_bytes = BM * 128 + pl.bn * 128;
-  pl.f16 = 2;
-  const int left = SMEM_MAX - SMEM_FIXED - pl.f16 * pl.f16_bytes;
-  pl.raw = left / pl.raw_bytes;
+  pl.raw_bytes = (pl.ar + pl.bn) * BK;
+  pl.f16_bytes = (pl.ar + pl.bn) * 128;
+  // fp16 stages while the 8-bit stages keep a third of shared memory (the
+  // MMA's reach past the last fp16 stage stays inside it: a 128-row tile is
+  // 16 KB)
+  const int room = SMEM_MAX - SMEM_FIXED;
+  pl.f16 = F16_STAGES_MAX;
+  while (pl.f16 > 2 && room - pl.f16 * pl.f16_bytes < room / 3) --pl.f16;
+  pl.raw = (room - pl.f16 * pl.f16_bytes) / pl.raw_bytes;
   if (pl.raw > RAW_STAGES_MAX) pl.raw = RAW_STAGES_MAX;
   return pl;
 }
@@ -751,7 +821,7 @@ cudaError_t mma_t(const Q8Args &a, cudaStream_t s) {
   Q8Params p;
   p.M = a.M; p.N = a.N; p.K = a.K; p.sa = a.ascale; p.sw = a.wscale; p.bias = a.bias; p.y = a.y;
   p.status = a.status;
-  p.pl = plan_of(a.M, a.N, a.K);
+  p.pl = plan_of(a.M, a.N);
   Q8Maps maps;
   if (!make_map(&maps.a, a.aq, a.M, a.K, p.pl.ar, false) ||
       !make_map(&maps.w, a.wq, a.N, a.K, p.pl.bn, false))
@@ -826,8 +896,30 @@ cudaError_t rows_t(const Q8Args &a, cudaStream_t s) {
                   a.wq, a.ascale, a.wscale, a.bias, a.M, a.N, a.K, ks, (E *)a.y);
 }
 
+template <typename E, int NT>
+cudaError_t frag_t(const Q8Args &a, cudaStream_t s) {
+  const int tiles = (a.N + FRAG_N - 1) / FRAG_N;
+  // warps that share K: until 24 warps an SM, while each has two 64-byte steps
+  int ks = 1;
+  while (ks < 8 && (long long)tiles * ks < 24ll * num_sms() && a.K >= ks * 2 * 128) ks *= 2;
+  const int per = 8 / ks;
+  return launch_k(q8_frag_kernel<E, NT>, dim3((tiles + per - 1) / per), dim3(256), 0, s, a.aq,
+                  a.wq, a.ascale, a.wscale, a.bias, a.M, a.N, a.K, ks, (E *)a.y);
+}
+
 template <typename E>
 cudaError_t matmul_t(const Q8Args &a, cudaStream_t s) {
+  const char *force = getenv("Q8_FORCE");
+  const int f = force ? atoi(force) : 0;
+  if (f == 1) return mma_t<E>(a, s);
+  if (f == 2 && a.M <= 8) return frag_t<E, 1>(a, s);
+  if (f == 3 && a.M <= 2) return rows_t<E, 2>(a, s);
+  if (f == 3 && a.M <= 4) return rows_t<E, 4>(a, s);
+  if (f == 3 && a.M <= 8) return rows_t<E, 8>(a, s);
+  if (a.M > 8 && a.M <= 16) return frag_t<E, 2>(a, s);
+  if (a.M > 8 && a.M <= 32) return frag_t<E, 4>(a, s);
+  if (a.M > 8 && a.M <= 48) return frag_t<E, 6>(a, s);
+  if (a.M > 8 && a.M <= 64) return frag_t<E, 8>(a, s);
   if (a.M == 1) return rows_t<E, 1>(a, s);
   if (a.M == 2) return rows_t<E, 2>(a, s);
   if (a.M <= 4) return rows_t<E, 4>(a, s);

@@ -114,6 +114,18 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
       : "memory");
 }
 
+// One lane of a converged warp.  A warp that runs its role's loop with every
+// lane and lets one elected lane issue keeps descriptors and barrier addresses
+// in uniform registers; in a branch of a single lane each tcgen05.mma first
+// moves them there.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r));
+  return r != 0;
+}
+
 // ---- CTA pairs (cta_group::2: a cluster of two CTAs works on one tile) --------
 // Address of this CTA's shared-memory location in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {

@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (TWELL_BF16, TWELL_F32, TWELL_OK, TwellError, _stream, load)
+from . import TWELL_BF16, TWELL_F32, TWELL_OK, TwellError, load
 
 _TORCH = {TWELL_F32: torch.float32, TWELL_BF16: torch.bfloat16}
 _ARG, _DTYPE = -1, -3
@@ -20,11 +20,9 @@ def _arg(a, dtype, count, where):
     """The device pointer of an operand of `count` elements."""
     if a is None or isinstance(a, int):
         return a
-    if a.dtype is not dtype:
-        raise TwellError(_DTYPE, where)
-    if a.numel() != count or not a.is_cuda or not a.is_contiguous():
-        raise TwellError(_ARG, where)
-    return a.data_ptr()
+    if a.dtype is dtype and a.numel() == count and a.is_contiguous() and a.is_cuda:
+        return a.data_ptr()
+    raise TwellError(_ARG if a.dtype is dtype else _DTYPE, where)
 
 
 def _pitched(a, dtype, rows, cols, pitch, where):
@@ -61,6 +59,14 @@ def _scratch(workspace, nbytes, where):
     if not workspace.is_cuda or workspace.numel() * workspace.element_size() < nbytes:
         raise TwellError(-8, where)
     return workspace.data_ptr()
+
+
+def _stream(stream):
+    """Raw handle of a stream; None: the current one (as a handle, without the stream object that
+    torch.cuda.current_stream() makes, which takes as long as a launch)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _run(where, fn, *args):
