@@ -8,12 +8,14 @@
 // The operands stay 8-bit in memory and are widened on their way through
 // shared memory.
 //
-//   M <= ROWS_MAX   q8_rows_kernel: the weights stream once through
-//                   registers, dp4a (exact int32 sums).
-//   else            q8_mma_kernel: TMA brings 8-bit tiles into a ring; eight
-//                   warps widen them into fp16 tiles in the 128B-swizzled
-//                   layout of the MMA; one lane issues tcgen05.mma; four
-//                   warps read TMEM, scale and store.
+// By the rows of a (matmul_t has the rule and the measurements):
+//   a decoded row or four   q8_rows_kernel: dp4a, exact int32 sums
+//   a batch of them         q8_frag_kernel: the weights are widened in
+//                           registers and used up there (m16n8k16)
+//   up to 128 rows          q8_mma_kernel: TMA brings 8-bit tiles, warps
+//                           widen them into the MMA's shared-memory layout,
+//                           one lane issues tcgen05.mma, four warps read TMEM
+//   more                    q8_pair_kernel: the same over CTA pairs
 #include <cuda_fp16.h>
 #include <string.h>
 
@@ -27,7 +29,7 @@ namespace twell {
 namespace {
 
 // ---- few rows ----------------------------------------------------------------
-constexpr int ROWS_MAX = 8;  // rows of a that q8_rows_kernel takes
+constexpr int ROWS_MAX = 4;  // rows of a that q8_rows_kernel takes
 constexpr int ROWS_N = 4;    // weight rows a warp reads together
 
 // A group of KS warps takes ROWS_N weight rows and splits K; MT rows of a
@@ -110,12 +112,13 @@ __device__ __forceinline__ void widen16(const uint4 &v, uint4 &lo, uint4 &hi) {
 
 // ---- a batch of decoded rows ---------------------------------------------------
 // The weights still stream once from HBM and are used up in registers: a
-// warp takes 16 weight rows as the M side of m16n8k16 and NT groups of eight
-// rows of a as its N side.  A lane loads 16 consecutive bytes of a row, which
-// serve as its part of four MMAs' k (both operands take the same order of k).
-// A tile's KS warps split K and are added in order through shared memory.
-constexpr int FRAG_N = 16;
-
+// warp takes MT times 16 weight rows as the M side of m16n8k16 and NT groups
+// of eight rows of a as its N side.  A lane loads 16 consecutive bytes of a
+// row, which serve as its part of four MMAs' k (both operands take the same
+// order of k), and widens them in registers: rows of a again in every warp,
+// which is what bounds it from 32 rows on (reading them widened instead, from
+// L1, was slower: 47 against 33 us at 16 x 50001 x 2048).  A tile's KS warps
+// split K and are added in order through shared memory.
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -133,66 +136,74 @@ __device__ __forceinline__ void widen_words(const uint4 &v, uint32_t (&o)[8]) {
   o[4] = hi.x; o[5] = hi.y; o[6] = hi.z; o[7] = hi.w;
 }
 
-template <typename E, int NT>
-__global__ void __launch_bounds__(256)
-q8_frag_kernel(const int8_t *a, const int8_t *w, const float *sa, const float *sw,
+template <typename E, int NT, int MT, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32)
+q8_frag_kernel(const uint4 *a, const int8_t *w, const float *sa, const float *sw,
                const float *bias, int M, int N, int K, int ks, E *y) {
   pdl_begin();
-  __shared__ float sums[8][NT * 8][FRAG_N + 1];
+  constexpr int ROWS = MT * 16, U = 2;
+  __shared__ float sums[WARPS][NT * 8][ROWS + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int tile = (int)blockIdx.x * (8 / ks) + warp / ks, part = warp % ks;
-  const int n0 = tile * FRAG_N;
+  const int tile = (int)blockIdx.x * (WARPS / ks) + warp / ks, part = warp % ks;
+  const int n0 = tile * ROWS;
   const int chunks = (K + 63) / 64;
-  float acc[NT][4];
+  float acc[MT][NT][4];
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
+  for (int h = 0; h < MT; ++h)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[h][j][i] = 0.f;
   if (n0 < N) {
-    constexpr int U = 2;
-    const int8_t *w0 = w + (size_t)min(n0 + g, N - 1) * K, *w1 = w + (size_t)min(n0 + g + 8, N - 1) * K;
+    const int8_t *row[2 * MT];
+#pragma unroll
+    for (int h = 0; h < 2 * MT; ++h) row[h] = w + (size_t)min(n0 + g + 8 * h, N - 1) * K;
     for (int c = part; c < chunks; c += U * ks) {
-      uint4 x0[U], x1[U];
+      uint4 x[U][2 * MT];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int k = (c + u * ks) * 64 + t * 16;
-        x0[u] = k < K ? ldg_stream(w0 + k) : make_uint4(0, 0, 0, 0);
-        x1[u] = k < K ? ldg_stream(w1 + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int h = 0; h < 2 * MT; ++h)
+          x[u][h] = k < K ? ldg_stream(row[h] + k) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int k = (c + u * ks) * 64 + t * 16;
-        uint32_t p[8], q[8];
-        widen_words(x0[u], p);
-        widen_words(x1[u], q);
+        uint32_t p[2 * MT][8];
+#pragma unroll
+        for (int h = 0; h < 2 * MT; ++h) widen_words(x[u][h], p[h]);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          const int m = min(j * 8 + g, M - 1);
+          const size_t at = ((size_t)min(j * 8 + g, M - 1) * K + k) / 16;
           uint32_t r[8];
-          widen_words(k < K ? __ldg((const uint4 *)(a + (size_t)m * K + k)) : make_uint4(0, 0, 0, 0),
-                      r);
+          widen_words(k < K ? __ldg(a + at) : make_uint4(0, 0, 0, 0), r);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma_16816(acc[j], p[2 * i], q[2 * i], p[2 * i + 1], q[2 * i + 1], r[2 * i],
-                      r[2 * i + 1]);
+          for (int h = 0; h < MT; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mma_16816(acc[h][j], p[2 * h][2 * i], p[2 * h + 1][2 * i], p[2 * h][2 * i + 1],
+                        p[2 * h + 1][2 * i + 1], r[2 * i], r[2 * i + 1]);
         }
       }
     }
   }
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
+  for (int h = 0; h < MT; ++h)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      sums[warp][j * 8 + 2 * t + (i & 1)][g + (i >> 1) * 8] = acc[j][i];
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        sums[warp][j * 8 + 2 * t + (i & 1)][h * 16 + g + (i >> 1) * 8] = acc[h][j][i];
   __syncthreads();
-  // the CTA's tiles: 16 columns of y for each row of a
-  const int cols = 8 / ks * FRAG_N;
-  for (int i = threadIdx.x; i < M * cols; i += 256) {
+  // the CTA's tiles: `cols` columns of y for each row of a
+  const int cols = WARPS / ks * ROWS;
+  for (int i = threadIdx.x; i < M * cols; i += WARPS * 32) {
     const int m = i / cols, c = i - m * cols, n = (int)blockIdx.x * cols + c;
     if (n >= N) continue;
     float s = 0.f;
-    for (int r = 0; r < ks; ++r) s += sums[c / FRAG_N * ks + r][m][c % FRAG_N];
+    for (int r = 0; r < ks; ++r) s += sums[c / ROWS * ks + r][m][c % ROWS];
     y[(size_t)m * N + n] = from_f<E>(s * sa[m] * sw[n] + (bias ? bias[n] : 0.f));
   }
 }
@@ -203,7 +214,7 @@ constexpr int GROUPS = 4, GROUP = 4;            // conversion groups, warps of a
 constexpr int THREADS = 32 * (6 + GROUPS * GROUP);  // TMA, MMA, 4 epilogue, conversion
 constexpr int F16_STAGES_MAX = 8, RAW_STAGES_MAX = 24;
 constexpr int ACC_COLS = 256;                   // TMEM columns of one accumulator
-constexpr int EPI_PITCH = 33;                   // fp32 staging row of the scalar epilogue
+constexpr int EPI_PITCH = 33;                   // 32-bit words of an epilogue staging row
 
 struct Q8Maps {
   CUtensorMap a, w;
@@ -230,49 +241,103 @@ __device__ __forceinline__ void fence_async_proxy() {
 }
 
 // One warp's 32 accumulator rows (TMEM lane = row, from row m0 on) of a tile
-// of bn columns from n0 on: scaled, rounded and stored.  Rows of y that are
-// 16-byte aligned take vectors; otherwise the block goes through shared
-// memory and the warp stores 32 columns of a row at a time.
-template <typename E>
-__device__ __forceinline__ void store_tile(const Q8Params &p, uint32_t acc, int m0, int n0,
-                                           float sa, const float *s_sw, float *stage) {
-  if (m0 >= p.M) return;  // (uniform for the warp)
-  const int lane = threadIdx.x & 31, bn = p.pl.bn, m = m0 + lane;
-  const bool vec = (size_t)p.N * sizeof(E) % 16 == 0;
-  for (int c0 = 0; c0 < bn; c0 += 32) {
+// of bn columns from n0 on: scaled, rounded, and stored through shared memory
+// so that one instruction writes 128 consecutive bytes of a row whatever its
+// alignment.
+__device__ __forceinline__ void scale32(float *v, float sa, const float *sw, const float *bias) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    const float4 s = *(const float4 *)(sw + i), b = *(const float4 *)(bias + i);
+    v[i] = v[i] * sa * s.x + b.x;
+    v[i + 1] = v[i + 1] * sa * s.y + b.y;
+    v[i + 2] = v[i + 2] * sa * s.z + b.z;
+    v[i + 3] = v[i + 3] * sa * s.w + b.w;
+  }
+}
+
+__device__ __forceinline__ void store_tile(const Q8Params &p, float *y, uint32_t acc, int m0,
+                                           int n0, float sa, const float *s_sw, float *stage) {
+  const int lane = threadIdx.x & 31, cols = min(p.pl.bn, p.N - n0), rows = min(32, p.M - m0);
+  for (int c0 = 0; c0 < cols; c0 += 32) {
     float v[32];
     tmem_ld32(acc + c0, v);
-    const int n = n0 + c0, cols = min(bn - c0, min(32, p.N - n));
-    if (cols <= 0) break;
+    scale32(v, sa, s_sw + c0, s_sw + 256 + c0);
+    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const int c = (c0 + i) & 255;  // (past the tile: not stored)
-      v[i] = v[i] * sa * s_sw[c] + s_sw[256 + c];
+    for (int i = 0; i < 32; ++i) stage[lane * EPI_PITCH + i] = v[i];
+    __syncwarp();
+    float *dst = y + (size_t)m0 * p.N + n0 + c0 + lane;
+    if (c0 + lane < cols)
+#pragma unroll 4
+      for (int r = 0; r < rows; ++r) dst[(size_t)r * p.N] = stage[r * EPI_PITCH + lane];
+  }
+}
+
+// bf16: pairs of elements as they lie in aligned 4-byte words of y.  With an
+// odd N every other row starts in the upper half of a word; such a row's
+// pairs are (-1, 0), (1, 2), ...: its thread packs them so, carrying one
+// element from block to block, and only a tile's first and last words are
+// stored by halves.
+__device__ __forceinline__ void store_tile(const Q8Params &p, bf16 *y, uint32_t acc, int m0,
+                                           int n0, float sa, const float *s_sw, float *stage_f) {
+  uint32_t *stage = (uint32_t *)stage_f;
+  const int lane = threadIdx.x & 31, cols = min(p.pl.bn, p.N - n0), rows = min(32, p.M - m0);
+  const int odd_n = p.N & 1;                  // (n0 is even)
+  const bool odd = (odd_n & (m0 + lane)) != 0;
+  float carry = 0.f;
+  if (p.N % 8 == 0) {
+    // 16-byte aligned rows: each thread stores its own (a last tile's epilogue
+    // is over sooner: 18.7 against 21.6 us at 300 x 8192 x 2048)
+    for (int c0 = 0; c0 < cols; c0 += 32) {
+      float v[32];
+      tmem_ld32(acc + c0, v);
+      scale32(v, sa, s_sw + c0, s_sw + 256 + c0);
+      uint4 *dst = (uint4 *)(y + (size_t)(m0 + lane) * p.N + n0 + c0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (lane < rows && c0 + 8 * i < cols)
+          dst[i] = make_uint4(pack_bf2(v[8 * i], v[8 * i + 1]), pack_bf2(v[8 * i + 2], v[8 * i + 3]),
+                              pack_bf2(v[8 * i + 4], v[8 * i + 5]),
+                              pack_bf2(v[8 * i + 6], v[8 * i + 7]));
     }
-    if (vec && cols % VEC16<E> == 0) {
-      if (m < p.M) {
-        uint4 *dst = (uint4 *)((E *)p.y + (size_t)m * p.N + n);
+    return;
+  }
+  for (int c0 = 0; c0 < cols; c0 += 64) {
+    float v[64];
+    tmem_ld32(acc + c0, *(float(*)[32])v);
+    if (c0 + 32 < p.pl.bn) tmem_ld32(acc + c0 + 32, *(float(*)[32])(v + 32));
+    scale32(v, sa, s_sw + c0, s_sw + 256 + c0);
+    scale32(v + 32, sa, s_sw + c0 + 32, s_sw + 256 + c0 + 32);
+    __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 32 / VEC16<E>; ++i) {
-          if (i * VEC16<E> >= cols) break;
-          float f[VEC16<E>];
-#pragma unroll
-          for (int j = 0; j < VEC16<E>; ++j) f[j] = v[i * VEC16<E> + j];
-          dst[i] = pack16(f, (E *)nullptr);
-        }
-      }
+    for (int j = 0; j < 32; ++j)
+      stage[lane * EPI_PITCH + j] = pack_bf2(odd ? (j ? v[2 * j - 1] : carry) : v[2 * j],
+                                             odd ? v[2 * j] : v[2 * j + 1]);
+    carry = v[63];
+    __syncwarp();
+    bf16 *dst = y + (size_t)m0 * p.N + n0 + c0 + 2 * lane;
+    if (c0 > 0 && c0 + 64 < cols) {
+#pragma unroll 4
+      for (int r = 0; r < rows; ++r)
+        *(uint32_t *)(dst + (size_t)r * p.N - (odd_n & (m0 + r))) = stage[r * EPI_PITCH + lane];
     } else {
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 32; ++i) stage[lane * EPI_PITCH + i] = v[i];
-      __syncwarp();
-      const int rows = min(32, p.M - m0);
-      if (lane < cols) {
-        E *dst = (E *)p.y + (size_t)m0 * p.N + n + lane;
-        for (int r = 0; r < rows; ++r) dst[(size_t)r * p.N] = from_f<E>(stage[r * EPI_PITCH + lane]);
+      for (int r = 0; r < rows; ++r) {
+        const int o = odd_n & (m0 + r), c = c0 + 2 * lane - o;  // column of the word's lower half
+        const uint32_t w = stage[r * EPI_PITCH + lane];
+        bf16 *d = dst + (size_t)r * p.N - o;
+        if (c >= 0 && c + 1 < cols) {
+          *(uint32_t *)d = w;
+        } else if (c >= 0 && c < cols) {
+          *(uint16_t *)d = (uint16_t)w;
+        } else if (c == -1) {
+          *(uint16_t *)(d + 1) = (uint16_t)(w >> 16);
+        }
       }
     }
   }
+  // the last element of a shifted row whose columns fill the last block
+  if (odd && lane < rows && cols % 64 == 0)
+    y[(size_t)(m0 + lane) * p.N + n0 + cols - 1] = __float2bfloat16_rn(carry);
 }
 
 // Scale and bias of a tile's columns, staged by the 128 epilogue threads.
@@ -486,7 +551,8 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
       if (!ok) break;
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * ACC_COLS);
-      store_tile<E>(p, acc, m0 + q * 32, n0, sa, s_sw, stage);
+      if (m0 + q * 32 < p.M)  // (uniform for the warp)
+        store_tile(p, (E *)p.y, acc, m0 + q * 32, n0, sa, s_sw, stage);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(tempty + 8 * buf);
@@ -548,6 +614,7 @@ constexpr int P_RAW = 128 * BK;
 constexpr int P_SMEM = 1024 + P_AS * P_TILE + P_BS * P_TILE + P_RS * P_RAW +
                        4 * 32 * EPI_PITCH * 4 + 2 * 256 * 4;
 
+// fp16 copy of a.
 __global__ void __launch_bounds__(256)
 q8_widen_kernel(const uint4 *a, size_t vecs, uint4 *out) {
   pdl_begin();
@@ -726,8 +793,9 @@ q8_pair_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Pa
                                                 abort_flag, p.status));
       if (!ok) break;
       tc_fence_after();
-      store_tile<E>(p, tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * ACC_COLS), m0, n0, sa,
-                    s_sw, stage);
+      if (m0 < p.M)  // (uniform for the warp)
+        store_tile(p, (E *)p.y, tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * ACC_COLS), m0,
+                   n0, sa, s_sw, stage);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(free + 8 * buf);
@@ -865,8 +933,9 @@ cudaError_t pair_t(const Q8Args &a, cudaStream_t s) {
   if (attr != cudaSuccess) return attr;
   const size_t vecs = (size_t)a.M * a.K / 16;
   if ((vecs + 255) / 256 > 0x7FFFFFFFull) return cudaErrorInvalidValue;
-  cudaError_t e = launch_k(q8_widen_kernel, dim3((unsigned)((vecs + 255) / 256)), dim3(256), 0, s,
-                           (const uint4 *)a.aq, vecs, (uint4 *)a.ws);
+  const cudaError_t e =
+      launch_k(q8_widen_kernel, dim3((unsigned)((vecs + 255) / 256)), dim3(256), 0, s,
+               (const uint4 *)a.aq, vecs, (uint4 *)a.ws);
   if (e != cudaSuccess) return e;
   prof_mark(KID_Q8_WIDEN, s);
   Q8Params p;
@@ -896,34 +965,43 @@ cudaError_t rows_t(const Q8Args &a, cudaStream_t s) {
                   a.wq, a.ascale, a.wscale, a.bias, a.M, a.N, a.K, ks, (E *)a.y);
 }
 
-template <typename E, int NT>
-cudaError_t frag_t(const Q8Args &a, cudaStream_t s) {
-  const int tiles = (a.N + FRAG_N - 1) / FRAG_N;
-  // warps that share K: until 24 warps an SM, while each has two 64-byte steps
+template <typename E, int NT, int MT>
+cudaError_t frag_mt(const Q8Args &a, cudaStream_t s) {
+  constexpr int WARPS = MT == 2 ? 4 : 8;
+  const int tiles = (a.N + MT * 16 - 1) / (MT * 16);
+  // warps that share K: until 16 warps an SM, while each has two 64-byte steps
   int ks = 1;
-  while (ks < 8 && (long long)tiles * ks < 24ll * num_sms() && a.K >= ks * 2 * 128) ks *= 2;
-  const int per = 8 / ks;
-  return launch_k(q8_frag_kernel<E, NT>, dim3((tiles + per - 1) / per), dim3(256), 0, s, a.aq,
-                  a.wq, a.ascale, a.wscale, a.bias, a.M, a.N, a.K, ks, (E *)a.y);
+  while (ks < WARPS && (long long)tiles * ks < 16ll * num_sms() && a.K >= ks * 2 * 128) ks *= 2;
+  const int per = WARPS / ks;
+  return launch_k(q8_frag_kernel<E, NT, MT, WARPS>, dim3((tiles + per - 1) / per),
+                  dim3(WARPS * 32), 0, s, (const uint4 *)a.aq, a.wq, a.ascale, a.wscale, a.bias,
+                  a.M, a.N, a.K, ks, (E *)a.y);
 }
 
+template <typename E, int NT>
+cudaError_t frag_t(const Q8Args &a, cudaStream_t s) {
+  // 32 weight rows a warp where that leaves eight warps an SM (rows of a are
+  // widened half as often: 22.6 against 28.4 us at 1 x 50001 x 2048)
+  return a.N >= 64 * num_sms() ? frag_mt<E, NT, 2>(a, s) : frag_mt<E, NT, 1>(a, s);
+}
+
+// Measured, us at N x K = 14336 x 4096 | 8192 x 2048 | 2048 x 2048 | 50001 x
+// 2048 (weights from HBM):
+//   M 1    rows 14.4 | 5.6 | 2.8 | 22.7    frag 15.9 | 6.5 | 3.9 | 22.6
+//   M 4    rows 12.4 | 6.9 | 2.9 | 24.1    frag 16.5 | 6.6 | 3.9 | 23.6
+//   M 8    rows 22.9 | 11.9 | 4.9 | 47.2   frag 16.8 | 6.6 | 3.9 | 24.8
+//   M 16   frag 17.9 | 8.3 | 4.8 | 33.1    mma 19.7 | 11.4 | 10.2 | 30.6
+//   M 32   frag 23.7 | 12.4 | 5.7 | 49.6   mma 19.8 | 11.4 | 10.3 | 35.7
+//   M 128  mma 27.1 | 14.0 | 11.7 | 49.2
+//   M 129  pair 28.3 | 16.2 | 13.6 | 52.5
 template <typename E>
 cudaError_t matmul_t(const Q8Args &a, cudaStream_t s) {
-  const char *force = getenv("Q8_FORCE");
-  const int f = force ? atoi(force) : 0;
-  if (f == 1) return mma_t<E>(a, s);
-  if (f == 2 && a.M <= 8) return frag_t<E, 1>(a, s);
-  if (f == 3 && a.M <= 2) return rows_t<E, 2>(a, s);
-  if (f == 3 && a.M <= 4) return rows_t<E, 4>(a, s);
-  if (f == 3 && a.M <= 8) return rows_t<E, 8>(a, s);
-  if (a.M > 8 && a.M <= 16) return frag_t<E, 2>(a, s);
-  if (a.M > 8 && a.M <= 32) return frag_t<E, 4>(a, s);
-  if (a.M > 8 && a.M <= 48) return frag_t<E, 6>(a, s);
-  if (a.M > 8 && a.M <= 64) return frag_t<E, 8>(a, s);
   if (a.M == 1) return rows_t<E, 1>(a, s);
   if (a.M == 2) return rows_t<E, 2>(a, s);
-  if (a.M <= 4) return rows_t<E, 4>(a, s);
-  if (a.M <= ROWS_MAX) return rows_t<E, 8>(a, s);
+  if (a.M <= ROWS_MAX) return rows_t<E, 4>(a, s);
+  if (a.M <= 8) return frag_t<E, 1>(a, s);
+  if (a.M <= 16) return frag_t<E, 2>(a, s);
+  if (a.M <= 32 && a.N <= 4096) return frag_mt<E, 4, 1>(a, s);
   return a.M < PAIR_MIN ? mma_t<E>(a, s) : pair_t<E>(a, s);
 }
 
