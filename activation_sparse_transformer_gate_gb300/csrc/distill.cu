@@ -12,9 +12,15 @@
 // teacher's list are then patched by the CTA whose slice holds them, so p is
 // never spread over the vocabulary.
 //
-// Exponentials are ex2((z - max z) * log2(e) / tau): the difference first, so
-// that logits of the type's lowest value neither overflow nor, in a row of
-// nothing else, lose the uniform q.
+// One warp of each CTA deals with the teacher's list while the others stream
+// the logits: its softmax, repeated ids, the student's logits there, the loss,
+// and at the end the list's entries of the gradient.
+//
+// Exponentials are 2^(z c - ref), c = log2(e) / tau, one fma before the ex2:
+// ref is max z * c rounded, and as the same ref stands in the sum and in the
+// gradient, its rounding cancels.  Where the maximum is so large that z c
+// would overflow (rows masked with the type's lowest value and nothing else),
+// the difference z - max z is taken first.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -27,8 +33,8 @@ namespace twell {
 
 namespace {
 
-constexpr float LOG2E = 1.4426950408889634f;
-constexpr int MAX_WARPS = 32;
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr int MAX_WARPS = 7;     // streaming warps of a CTA (8 with the list's)
 constexpr int MAX_CLUSTER = 8;
 
 __device__ __forceinline__ float ex2(float v) {
@@ -37,73 +43,76 @@ __device__ __forceinline__ float ex2(float v) {
   return r;
 }
 
-// The reference that exponentials of a row (or part) with maximum m are taken
-// against: m, or 0 where everything is -inf.
-__device__ __forceinline__ float ref_of(float m) { return m == -INFINITY ? 0.f : m; }
+// The reference that the exponentials of a row (or part of one) with maximum
+// m are taken against.
+struct Ref {
+  float m, mc;  // m (0 where everything is -inf), and max * c rounded
+  bool wide;    // z c may overflow beside it
+  __device__ __forceinline__ Ref(float max, float c) {
+    m = max == -INFINITY ? 0.f : max;
+    mc = __fmul_rn(max, c);  // (one rounding everywhere: not to be fused)
+    wide = !(fabsf(mc) < 1e30f);
+  }
+  // log2 of an exponential against this reference
+  __device__ __forceinline__ float operator()(float z, float c) const {
+    return wide ? (z - m) * c : fmaf(z, c, -mc);
+  }
+};
 
-// (m, l) += (m2, l2): l counts exponentials against ref_of(m).
+// What a sum of exponentials against the reference of maximum `max` is
+// multiplied by to count against `to`.
+__device__ __forceinline__ float rescale(float max, const Ref &to, float c) {
+  const Ref from(max, c);
+  return ex2(from.wide || to.wide ? (max - to.m) * c : from.mc - to.mc);
+}
+
+// (m, l) += (m2, l2): l counts exponentials against the reference of m.
 __device__ __forceinline__ void merge(float &m, float &l, float m2, float l2, float c) {
   const float top = fmaxf(m, m2);
-  const float r = ref_of(top);
-  l = l * ex2((m - r) * c) + l2 * ex2((m2 - r) * c);
+  const Ref to(top, c);
+  l = l * rescale(m, to, c) + l2 * rescale(m2, to, c);
   m = top;
 }
 
 // A row as aligned 16-byte vectors: vector j holds the elements
-// j*N - lead .. j*N - lead + N - 1.  Only vectors wholly inside the row are
-// read or written as vectors (the others are shared with the rows beside it).
+// j*N - lead .. j*N - lead + N - 1.  The vectors wholly inside the row,
+// [w0, w1), are split among the CTAs; the elements before and behind them (at
+// most N - 1 each) are its ends, single elements of the row's first CTA.
 template <typename E>
 struct Row {
-  const E *z;   // element 0
-  int lead;     // elements between the aligned address below z and z
-  int V, nvec;
-  __device__ Row(const E *p, int V_) : z(p), V(V_) {
+  const uint4 *base;  // vector 0
+  int lead;           // elements between the aligned address below the row and the row
+  int V, w0, w1;
+  int head, tail;     // ends: [0, head) and [tail, V)
+  __device__ __forceinline__ Row(const E *p, int V_) : V(V_) {
     lead = (int)(((uintptr_t)p & 15u) / sizeof(E));
-    nvec = (int)(((long long)V + lead + VEC16<E> - 1) / VEC16<E>);
+    base = (const uint4 *)(p - lead);
+    w0 = lead ? 1 : 0;
+    w1 = max(w0, (int)((V + (unsigned)lead) / VEC16<E>));
+    head = min(V, lead ? VEC16<E> - lead : 0);
+    tail = max(head, min(V, w1 * VEC16<E> - lead));
   }
-  __device__ long long first(int j) const { return (long long)j * VEC16<E> - lead; }
-  __device__ bool whole(int j) const { return first(j) >= 0 && first(j) + VEC16<E> <= V; }
+  // end element i, or -1
+  __device__ __forceinline__ int end(int i) const {
+    return i < head ? i : i < head + V - tail ? tail + i - head : -1;
+  }
+  // whether the CTA of vectors [ja, jb) has element e
+  __device__ __forceinline__ bool owns(int e, int ja, int jb, bool first) const {
+    if (e < head || e >= tail) return first;
+    const int j = (int)(((unsigned)e + lead) / VEC16<E>);
+    return j >= ja && j < jb;
+  }
 };
 
-template <typename E> __device__ __forceinline__ E lowest();
-template <> __device__ __forceinline__ float lowest<float>() { return -INFINITY; }
-template <> __device__ __forceinline__ bf16 lowest<bf16>() {
-  return __ushort_as_bfloat16((unsigned short)0xFF80);
-}
-
-// Vector j of a row; elements outside it are -inf.
+// Zeros in a row of the gradient (its alignment is the logits'): vectors
+// [ja, jb), and the ends for the row's first CTA; by the first `threads`.
 template <typename E>
-__device__ __forceinline__ uint4 load_vec(const Row<E> &row, int j) {
-  const long long e0 = row.first(j);
-  if (row.whole(j)) return ld_once(row.z + e0);
-  E e[VEC16<E>];
-#pragma unroll
-  for (int i = 0; i < VEC16<E>; ++i)
-    e[i] = e0 + i >= 0 && e0 + i < row.V ? row.z[e0 + i] : lowest<E>();
-  uint4 r;
-  memcpy(&r, e, 16);
-  return r;
-}
-
-template <typename E>
-__device__ __forceinline__ void store_vec(const Row<E> &row, E *out, int j,
-                                          const float (&f)[VEC16<E>]) {
-  const long long e0 = row.first(j);
-  if (row.whole(j)) {
-    stg_stream(out + e0, pack16(f, (E *)nullptr));
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < VEC16<E>; ++i)
-    if (e0 + i >= 0 && e0 + i < row.V) out[e0 + i] = from_f<E>(f[i]);
-}
-
-template <typename E>
-__device__ __forceinline__ void store_zeros(const Row<E> &row, E *out, int j0, int j1) {
-  float f[VEC16<E>];
-#pragma unroll
-  for (int i = 0; i < VEC16<E>; ++i) f[i] = 0.f;
-  for (int j = j0 + (int)threadIdx.x; j < j1; j += blockDim.x) store_vec(row, out, j, f);
+__device__ __forceinline__ void store_zeros(const Row<E> &row, E *out, int ja, int jb, bool first,
+                                            int threads) {
+  for (int j = ja + (int)threadIdx.x; j < jb; j += threads)
+    stg_stream((uint4 *)(out - row.lead) + j, make_uint4(0, 0, 0, 0));
+  const int e = row.end(threadIdx.x);
+  if (first && e >= 0) out[e] = from_f<E>(0.f);
 }
 
 struct DistillParams {
@@ -118,239 +127,482 @@ struct DistillParams {
   int32_t *status;
 };
 
-// The teacher's list of a row in shared memory.
+// The teacher's list of a row in shared memory, kept by one warp.
 struct Teacher {
-  int id[DISTILL_MAX_K];     // -1: unused
-  float t[DISTILL_MAX_K];    // teacher logit, then p
+  int4 id4[DISTILL_MAX_K / 4];  // ids; -1: unused
+  float p[DISTILL_MAX_K];       // teacher logit, then probability
   float logp[DISTILL_MAX_K];
-  float z[DISTILL_MAX_K];    // the student's logit there
+  float z[DISTILL_MAX_K];       // the student's logit there
+  float sum[DISTILL_MAX_K];     // of the probabilities with this id; -1: not the id's first entry
+  int4 seen4[DISTILL_MAX_K / 2];  // hash table of the ids (twice their number, -1: free)
+  __device__ __forceinline__ int *id() { return (int *)id4; }
 };
 
-// Thread i < k takes entry i; returns whether it is used.  An entry whose
-// teacher logit is -inf has p = 0 and counts as unused.
+// The list and the student's logits there, by one warp; z: the row.  Entries
+// whose teacher logit is -inf have p = 0 and count as unused.  Returns whether
+// any entry is used.
 template <typename E>
-__device__ __forceinline__ bool load_entry(Teacher &te, const DistillParams &p, const E *z,
-                                           size_t t) {
-  const int i = threadIdx.x;
-  if (i >= p.k) return false;
-  int id = p.ids[t * p.k + i];
-  const float v = p.teacher[t * p.k + i];
-  if (id >= p.V) {
-    set_status(p.status, TWELL_ERR_INDEX);
-    id = -1;
+__device__ __forceinline__ bool load_list(Teacher &te, const DistillParams &p, const E *z,
+                                          size_t t) {
+  const int lane = threadIdx.x & 31;
+  bool any = false;
+  for (int i = lane; i < (p.k + 3) / 4 * 4; i += 32) {
+    int id = i < p.k ? p.ids[t * p.k + i] : -1;
+    const float v = i < p.k ? p.teacher[t * p.k + i] : 0.f;
+    if (id >= p.V) {
+      set_status(p.status, TWELL_ERR_INDEX);
+      id = -1;
+    }
+    if (v == -INFINITY) id = -1;
+    te.id()[i] = id < 0 ? -1 : id;
+    te.p[i] = v;
+    te.z[i] = id >= 0 ? to_f(z[id]) : 0.f;
+    any |= id >= 0;
   }
-  if (v == -INFINITY) id = -1;
-  te.id[i] = id < 0 ? -1 : id;
-  te.t[i] = v;
-  te.z[i] = id < 0 ? 0.f : to_f(z[id]);
-  return id >= 0;
+  for (int i = lane; i < DISTILL_MAX_K / 2; i += 32) te.seen4[i] = make_int4(-1, -1, -1, -1);
+  return __any_sync(0xFFFFFFFFu, any);  // (orders the list before its readers)
 }
 
-// p and log p of the list, by one warp (ends with a warp barrier).
-__device__ __forceinline__ void teacher_softmax(Teacher &te, const DistillParams &p) {
+// Its softmax, and for each id its first entry's sum, by the same warp.
+__device__ __forceinline__ void list_softmax(Teacher &te, const DistillParams &p) {
   const int lane = threadIdx.x & 31;
   float m = -INFINITY;
   for (int i = lane; i < p.k; i += 32)
-    if (te.id[i] >= 0) m = fmaxf(m, te.t[i]);
+    if (te.id()[i] >= 0) m = fmaxf(m, te.p[i]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
   float sum = 0.f;
   for (int i = lane; i < p.k; i += 32)
-    if (te.id[i] >= 0) sum += ex2((te.t[i] - m) * p.c);
+    if (te.id()[i] >= 0) sum += ex2((te.p[i] - m) * p.c);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
   const float inv = 1.f / sum, ln = logf(sum);
+  __syncwarp();
   for (int i = lane; i < p.k; i += 32) {
-    const bool on = te.id[i] >= 0;
-    const float d = te.t[i] - m;
-    te.t[i] = on ? ex2(d * p.c) * inv : 0.f;
+    const bool on = te.id()[i] >= 0;
+    const float d = te.p[i] - m;
+    te.p[i] = on ? ex2(d * p.c) * inv : 0.f;
     te.logp[i] = on ? d * p.inv_tau - ln : 0.f;
+  }
+  __syncwarp();
+  // repeated ids (rare) are found by hashing, summed in order
+  bool again = false;
+  for (int i = lane; i < p.k; i += 32) {
+    const int id = te.id()[i];
+    te.sum[i] = te.p[i];
+    if (id < 0) continue;
+    int *seen = (int *)te.seen4;
+    unsigned h = ((unsigned)id * 2654435761u) >> 23;
+    static_assert(DISTILL_MAX_K * 2 == 1 << (32 - 23), "the hash fills the table");
+    for (;;) {
+      const int old = atomicCAS(&seen[h], -1, id);
+      again |= old == id;
+      if (old == -1 || old == id) break;
+      h = (h + 1) % (2 * DISTILL_MAX_K);
+    }
+  }
+  if (!__any_sync(0xFFFFFFFFu, again)) return;
+  for (int i = lane; i < p.k; i += 32) {
+    const int id = te.id()[i];
+    float s = 0.f;
+    for (int o = 0; o < p.k; ++o) {
+      if (te.id()[o] != id) continue;
+      if (o < i) {
+        s = -1.f;
+        break;
+      }
+      s += te.p[o];
+    }
+    te.sum[i] = s;
   }
   __syncwarp();
 }
 
-// Gradient at the list's entries that lie in vectors [j0, j1) of the row:
-// entry i patches its element if it is the first with that id, with the
-// probabilities of all of them.
-template <typename E>
-__device__ __forceinline__ void patch_entries(const Teacher &te, const DistillParams &p,
-                                              const Row<E> &row, E *out, int j0, int j1, float ref,
-                                              float nl, float g) {
-  const int i = threadIdx.x;
-  if (i >= p.k) return;
-  const int id = te.id[i];
-  const long long j = ((long long)id + row.lead) / VEC16<E>;
-  if (id < 0 || j < j0 || j >= j1) return;
+// The row's loss and statistics, by the same warp: m, l the maximum and the
+// sum of exponentials, w the row's weight.
+__device__ __forceinline__ void store_loss(Teacher &te, const DistillParams &p, size_t t, bool any,
+                                           float w, float m, float l) {
+  const int lane = threadIdx.x & 31;
+  const Ref ref(m, p.c);
+  const float log2l = log2f(l);
   float sum = 0.f;
-  for (int o = 0; o < p.k; ++o) {
-    if (te.id[o] != id) continue;
-    if (o < i) return;
-    sum += te.t[o];
-  }
-  out[id] = from_f<E>(g * (ex2((te.z[i] - ref) * p.c + nl) - sum));
+  if (any)
+    for (int i = lane; i < p.k; i += 32)
+      if (te.id()[i] >= 0 && te.p[i] != 0.f)
+        sum += te.p[i] * (te.logp[i] - (ref(te.z[i], p.c) - log2l) * LN2);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if (lane != 0) return;
+  p.loss[t] = any ? w * p.tau * p.tau * sum : 0.f;
+  p.stats[t] = make_float2(m, logf(l) - (ref.wide ? 0.f : LN2 * fmaf(m, p.c, -ref.mc)));
 }
 
-// One cluster a row, CTA r of it the vectors [r * per, (r + 1) * per).  GRAD:
-// the first `cap` of them stay in shared memory (all of them unless the row
-// is longer than the cluster's shared memory; the rest is read again).
+// Gradient at the list's entries that the CTA owns, by the same warp after
+// everything else there is written; gl = g / (sum of the exponentials).
+template <typename E>
+__device__ __forceinline__ void patch_entries(Teacher &te, const DistillParams &p,
+                                              const Row<E> &row, E *out, int ja, int jb, bool first,
+                                              const Ref &ref, float gl, float g) {
+  for (int i = threadIdx.x & 31; i < p.k; i += 32) {
+    const int id = te.id()[i];
+    if (id >= 0 && row.owns(id, ja, jb, first) && !(te.sum[i] == -1.f))
+      out[id] = from_f<E>(gl * ex2(ref(te.z[i], p.c)) - g * te.sum[i]);
+  }
+}
+
+// Gradient of a vector where no entry is.
+template <typename E>
+__device__ __forceinline__ void grad_vec(const uint4 &r, const Ref &ref, float c, float gl,
+                                         float (&f)[VEC16<E>]) {
+  unpack(r, f, (E *)nullptr);
+  if (!ref.wide) {
+#pragma unroll
+    for (int i = 0; i < VEC16<E>; ++i) f[i] = gl * ex2(fmaf(f[i], c, -ref.mc));
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC16<E>; ++i) f[i] = gl * ex2(ref(f[i], c));
+  }
+}
+
+__device__ __forceinline__ float max_of(const uint4 &r, float *) {
+  return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)),
+               fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+}
+__device__ __forceinline__ float max_of(const uint4 &r, bf16 *) {
+  const __nv_bfloat162 *p = (const __nv_bfloat162 *)&r;
+  const __nv_bfloat162 m = __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3]));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+
+// Running maximum and sum of exponentials.
+template <typename E>
+struct Running {
+  float m = -INFINITY, l = 0.f;
+  Ref ref;
+  float c;
+  __device__ __forceinline__ explicit Running(float c_) : ref(-INFINITY, c_), c(c_) {}
+  __device__ __forceinline__ void raise(float top) {
+    if (top > m) {
+      ref = Ref(top, c);
+      l *= rescale(m, ref, c);
+      m = top;
+    }
+  }
+  // U vectors, of which the i with i * step < n count.  Their maximum first:
+  // raising the reference costs as much as a vector, and some lane of a warp
+  // would raise it at nearly every vector of a short slice.
+  template <int U>
+  __device__ __forceinline__ void add(const uint4 (&r)[U], int n, int step) {
+    constexpr int N = VEC16<E>;
+    float top = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (u * step < n) top = fmaxf(top, max_of(r[u], (E *)nullptr));
+    raise(top);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (u * step >= n) break;
+      float f[N];
+      unpack(r[u], f, (E *)nullptr);
+      if (!ref.wide) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) l += ex2(fmaf(f[i], c, -ref.mc));
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) l += ex2(ref(f[i], c));
+      }
+    }
+  }
+  __device__ __forceinline__ void add(float z) {
+    raise(z);
+    l += ex2(ref(z, c));
+  }
+};
+
+// (m, l) of a warp's lanes, the same bits in each of them (additions over
+// exchanged lanes commute).
+__device__ __forceinline__ void merge_warp(float &m, float &l, float c) {
+  float top = m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  l *= rescale(m, Ref(top, c), c);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+  m = top;
+}
+
+// 16 bytes from global to shared memory, asynchronously.
+__device__ __forceinline__ void copy16_async(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src)
+               : "memory");
+}
+
+// One cluster a row, each CTA a slice of `per` of its whole vectors (the first
+// one the row's ends too).  The last warp keeps the teacher's list, the others
+// stream.  GRAD: the first `cap` vectors of a slice stay in shared memory (all
+// of them unless the row is longer than the cluster's shared memory; the rest
+// is read again).
 template <typename E, bool GRAD>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(32 * (MAX_WARPS + 1), 3)
 distill_forward_kernel(const E *z, E *dz, DistillParams p, int cap) {
   pdl_begin();
-  constexpr int N = VEC16<E>, U = 4;
+  constexpr int U = 4;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const size_t t = blockIdx.x / C;
-  const Row<E> row(z + t * p.ldz, p.V);
+  const E *zr = z + t * p.ldz;
+  const Row<E> row(zr, p.V);
   E *out = GRAD ? dz + t * p.ldz : nullptr;
-  const int per = (row.nvec + C - 1) / C;
-  const int j0 = min(row.nvec, rank * per), j1 = min(row.nvec, j0 + per);
+  const int per = (row.w1 - row.w0 + C - 1) / C;
+  const int ja = min(row.w1, row.w0 + rank * per), jb = min(row.w1, ja + per);
+  const bool first = rank == 0;
+  // [ja, js) go to shared memory, asynchronously and in two parts, before
+  // anything is waited for (js: where it ends; jh: a multiple of the streaming
+  // threads from ja on)
+  extern __shared__ uint4 slice[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int SW = (int)blockDim.x / 32 - 1, ST = SW * 32;  // streaming warps, threads
+  const int js = GRAD ? min(jb, ja + cap) : ja;
+  const int jh = min(js, ja + ((js - ja) / 2 + ST - 1) / ST * ST);
+  if (GRAD && warp < SW) {
+    for (int j = ja + (int)threadIdx.x; j < jh; j += ST) copy16_async(slice + (j - ja), row.base + j);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    for (int j = jh + (int)threadIdx.x; j < js; j += ST) copy16_async(slice + (j - ja), row.base + j);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
   const float w = p.w ? p.w[t] : 1.f;
-  if (w == 0.f) {  // a masked row (uniform for the cluster): nothing is read
-    if (GRAD) store_zeros(row, out, j0, j1);
-    if (rank == 0 && threadIdx.x == 0) {
+  if (w == 0.f) {  // a masked row (uniform for the cluster): its logits are not used
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (GRAD) store_zeros(row, out, ja, jb, first, blockDim.x);
+    if (first && threadIdx.x == 0) {
       p.loss[t] = 0.f;
       p.stats[t] = make_float2(0.f, 0.f);
     }
     return;
   }
-  extern __shared__ uint4 slice[];
+  // (this CTA runs: its shared memory may be written by the others)
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
   __shared__ Teacher te;
-  __shared__ float s_m[MAX_WARPS], s_l[MAX_WARPS];
-  __shared__ float2 s_part;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool used = load_entry(te, p, row.z, t);
+  __shared__ float2 s_part[MAX_CLUSTER * MAX_WARPS];  // (m, l) of the cluster's streaming warps
+  __shared__ int s_any;
+  const int e = first && warp < SW ? row.end(threadIdx.x) : -1;
+  float ze = 0.f;  // this thread's end element
 
   float m = -INFINITY, l = 0.f;
-  for (int j = j0 + (int)threadIdx.x; j < j1; j += U * blockDim.x) {
-    uint4 r[U];
+  if (warp == SW) {
+    const bool any = load_list(te, p, zr, t);
+    if (lane == 0) s_any = any;
+  } else {
+    Running<E> sum(p.c);
+    if (e >= 0) ze = to_f(zr[e]);
+    // what shared memory does not hold
+    for (int j = js + (int)threadIdx.x; j < jb; j += U * ST) {
+      uint4 r[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (j + u * (int)blockDim.x < j1) r[u] = load_vec(row, j + u * blockDim.x);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int at = j + u * (int)blockDim.x;
-      if (at >= j1) break;
-      if (GRAD && at - j0 < cap) slice[at - j0] = r[u];
-      float f[N];
-      unpack(r[u], f, (E *)nullptr);
-      float top = f[0];
-#pragma unroll
-      for (int i = 1; i < N; ++i) top = fmaxf(top, f[i]);
-      if (top > m) {
-        l *= ex2((m - top) * p.c);
-        m = top;
-      }
-      const float ref = ref_of(m);
-#pragma unroll
-      for (int i = 0; i < N; ++i) l += ex2((f[i] - ref) * p.c);
+      for (int u = 0; u < U; ++u)
+        if (j + u * ST < jb) r[u] = ld_once(row.base + j + u * ST);
+      sum.add(r, jb - j, ST);
     }
-  }
+    if (GRAD) {  // (each thread reads back only what it copied)
+      auto held = [&](int from, int to) {
+        for (int j = from + (int)threadIdx.x; j < to; j += U * ST) {
+          uint4 r[U];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    merge(m, l, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, l, o), p.c);
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-  const bool any = __syncthreads_or(used) != 0;
-  if (warp == 0) {
-    m = lane < (int)blockDim.x / 32 ? s_m[lane] : -INFINITY;
-    l = lane < (int)blockDim.x / 32 ? s_l[lane] : 0.f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      merge(m, l, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, l, o), p.c);
-    if (lane == 0) s_part = make_float2(m, l);
-  } else if (warp == 1 && any) {
-    teacher_softmax(te, p);
-  }
-  cluster.sync();
-  m = -INFINITY;
-  l = 0.f;
-  for (int i = 0; i < C; ++i) {
-    const float2 o = *cluster.map_shared_rank(&s_part, i);
-    merge(m, l, o.x, o.y, p.c);
-  }
-  // (the CTAs' shared memory is read no more: the matching wait is at the end)
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-  const float ref = ref_of(m);
-  if (rank == 0 && warp == 0) {
-    const float lnl = logf(l);
-    float sum = 0.f;
-    if (any)
-      for (int i = lane; i < p.k; i += 32)
-        if (te.id[i] >= 0 && te.t[i] != 0.f)
-          sum += te.t[i] * (te.logp[i] - ((te.z[i] - ref) * p.inv_tau - lnl));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (lane == 0) {
-      p.loss[t] = any ? w * p.tau * p.tau * sum : 0.f;
-      p.stats[t] = make_float2(m, lnl);
+          for (int u = 0; u < U; ++u)
+            if (j + u * ST < to) r[u] = slice[j + u * ST - ja];
+          sum.add(r, to - j, ST);
+        }
+      };
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      held(ja, jh);
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      held(jh, js);
     }
-  }
-  if (GRAD) {
-    if (!any) {
-      store_zeros(row, out, j0, j1);
-    } else {
-      const float g = w * p.tau, nl = -log2f(l);
-      for (int j = j0 + (int)threadIdx.x; j < j1; j += blockDim.x) {
-        const uint4 r = j - j0 < cap ? slice[j - j0] : load_vec(row, j);
-        float f[N];
-        unpack(r, f, (E *)nullptr);
-#pragma unroll
-        for (int i = 0; i < N; ++i) f[i] = g * ex2((f[i] - ref) * p.c + nl);
-        store_vec(row, out, j, f);
-      }
-      __syncthreads();  // the vectors are written before their entries are patched
-      patch_entries(te, p, row, out, j0, j1, ref, nl, g);
-    }
+    if (e >= 0) sum.add(ze);
+    m = sum.m;
+    l = sum.l;
+    merge_warp(m, l, p.c);
   }
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+  if (warp < SW && lane < C)
+    *cluster.map_shared_rank(&s_part[rank * SW + warp], lane) = make_float2(m, l);
+  // (the last time that a CTA reaches into another, and, with a gradient in
+  // place, that the row's logits are read by any but their owner)
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  if (warp == SW) list_softmax(te, p);
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+  m = -INFINITY;
+  l = 0.f;
+  for (int i = lane; i < C * SW; i += 32) merge(m, l, s_part[i].x, s_part[i].y, p.c);
+  merge_warp(m, l, p.c);
+  const Ref ref(m, p.c);
+  const bool any = s_any != 0;
+  const float g = w * p.tau, gl = g / l;
+  if (warp == SW) {
+    if (first) store_loss(te, p, t, any, w, m, l);
+  } else if (GRAD) {
+    if (any) {
+      uint4 *dst = (uint4 *)(out - row.lead);
+      for (int j = ja + (int)threadIdx.x; j < jb; j += ST) {
+        float f[VEC16<E>];
+        grad_vec<E>(j < js ? slice[j - ja] : ld_once(row.base + j), ref, p.c, gl, f);
+        stg_stream(dst + j, pack16(f, (E *)nullptr));
+      }
+      if (e >= 0) out[e] = from_f<E>(gl * ex2(ref(ze, p.c)));
+    } else {
+      store_zeros(row, out, ja, jb, first, ST);
+    }
+  }
+  if (GRAD && any) {
+    __syncthreads();  // all is written before the list's entries
+    if (warp == SW) patch_entries(te, p, row, out, ja, jb, first, ref, gl, g);
+  }
 }
 
-// The gradient from the forward's statistics: a CTA per row and 2048 vectors.
-constexpr int BWD_SLAB = 2048;
+// The gradient from the forward's statistics: a row's slab of `slab_vecs`
+// vectors a CTA, eight warps that stream and one for the list.
+constexpr int BWD_THREADS = 256;
 
 template <typename E>
-__global__ void __launch_bounds__(256)
-distill_backward_kernel(const E *z, E *dz, DistillParams p, int slabs) {
+__global__ void __launch_bounds__(BWD_THREADS + 32)
+distill_backward_kernel(const E *z, E *dz, DistillParams p, int slabs, int slab_vecs) {
   pdl_begin();
   constexpr int N = VEC16<E>, U = 4;
   const size_t t = blockIdx.x / slabs;
-  const Row<E> row(z + t * p.ldz, p.V);
+  const E *zr = z + t * p.ldz;
+  const Row<E> row(zr, p.V);
   E *out = dz + t * p.ldz;
-  const int j0 = (int)(blockIdx.x % slabs) * BWD_SLAB, j1 = min(row.nvec, j0 + BWD_SLAB);
+  const int slab = (int)(blockIdx.x % slabs);
+  const int ja = min(row.w1, row.w0 + slab * slab_vecs);
+  const int jb = min(row.w1, ja + slab_vecs);
+  const bool first = slab == 0;
   const float w = p.w[t];
   if (w == 0.f) {
-    store_zeros(row, out, j0, j1);
+    store_zeros(row, out, ja, jb, first, blockDim.x);
     return;
   }
   __shared__ Teacher te;
-  const bool used = load_entry(te, p, row.z, t);
-  if (!__syncthreads_or(used)) {
-    store_zeros(row, out, j0, j1);
-    return;
+  const bool lists = threadIdx.x >= BWD_THREADS;
+  // the row's list may be empty, so every warp looks at it
+  bool used = false;
+  for (int i = threadIdx.x & 31; i < p.k; i += 32) {
+    const int id = p.ids[t * p.k + i];
+    used |= id >= 0 && id < p.V && p.teacher[t * p.k + i] != -INFINITY;
   }
+  const bool any = __any_sync(0xFFFFFFFFu, used);
   const float2 st = p.stats[t];
-  const float ref = ref_of(st.x), nl = -st.y * LOG2E, g = w * p.tau;
-  for (int j = j0 + (int)threadIdx.x; j < j1; j += U * blockDim.x) {
+  const Ref ref(st.x, p.c);
+  const float g = w * p.tau;
+  const float gl = g * ex2(-st.y * LOG2E - (ref.wide ? 0.f : fmaf(st.x, p.c, -ref.mc)));
+  if (lists) {
+    // (with a gradient in place, the list's logits are read before the
+    // barrier and overwritten after it; other CTAs write elsewhere, but may
+    // be done with an entry's element already: only what this CTA owns is used)
+    load_list(te, p, zr, t);
+    __syncthreads();
+    list_softmax(te, p);
+  } else {
+    uint4 *dst = (uint4 *)(out - row.lead);
     uint4 r[U];
+    int j = ja + (int)threadIdx.x;
+    auto load = [&] {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (j + u * 256 < j1) r[u] = load_vec(row, j + u * 256);
+      for (int u = 0; u < U; ++u)
+        if (j + u * BWD_THREADS < jb) r[u] = ld_once(row.base + j + u * BWD_THREADS);
+    };
+    if (any) load();
+    __syncthreads();
+    if (any) {
+      while (j < jb) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (j + u * 256 >= j1) break;
-      float f[N];
-      unpack(r[u], f, (E *)nullptr);
-#pragma unroll
-      for (int i = 0; i < N; ++i) f[i] = g * ex2((f[i] - ref) * p.c + nl);
-      store_vec(row, out, j + u * 256, f);
+        for (int u = 0; u < U; ++u) {
+          if (j + u * BWD_THREADS >= jb) break;
+          float f[N];
+          grad_vec<E>(r[u], ref, p.c, gl, f);
+          stg_stream(dst + j + u * BWD_THREADS, pack16(f, (E *)nullptr));
+        }
+        j += U * BWD_THREADS;
+        load();
+      }
+      const int e = row.end(threadIdx.x);
+      if (first && e >= 0) out[e] = from_f<E>(gl * ex2(ref(to_f(zr[e]), p.c)));
+    } else {
+      store_zeros(row, out, ja, jb, first, BWD_THREADS);
     }
   }
-  if (threadIdx.x < 32) teacher_softmax(te, p);
   __syncthreads();
-  patch_entries(te, p, row, out, j0, j1, ref, nl, g);
+  if (lists && any) patch_entries(te, p, row, out, ja, jb, first, ref, gl, g);
+}
+
+// Short rows: a warp each, which does it all; the second pass reads the row
+// again from L1.
+enum Pass { LOSS = 0, LOSS_GRAD = 1, GRAD_ONLY = 2 };
+constexpr int SHORT_VECS = 256, SHORT_WARPS = 4;
+
+template <typename E, int PASS>
+__global__ void __launch_bounds__(SHORT_WARPS * 32)
+distill_short_kernel(const E *z, E *dz, DistillParams p, int T) {
+  pdl_begin();
+  constexpr int N = VEC16<E>, U = 4;
+  __shared__ Teacher lists[SHORT_WARPS];
+  Teacher &te = lists[threadIdx.x >> 5];
+  const int lane = threadIdx.x & 31;
+  const size_t t = (size_t)blockIdx.x * SHORT_WARPS + (threadIdx.x >> 5);
+  if (t >= (size_t)T) return;
+  const E *zr = z + t * p.ldz;
+  const Row<E> row(zr, p.V);
+  E *out = PASS == LOSS ? nullptr : dz + t * p.ldz;
+  uint4 *dst = PASS == LOSS ? nullptr : (uint4 *)(out - row.lead);
+  const int e = row.end(lane);
+  const float w = p.w ? p.w[t] : 1.f;
+  const bool any = w != 0.f && load_list(te, p, zr, t);
+  if (w == 0.f && PASS != GRAD_ONLY && lane == 0) {
+    p.loss[t] = 0.f;
+    p.stats[t] = make_float2(0.f, 0.f);
+  }
+  const float ze = w != 0.f && e >= 0 ? to_f(zr[e]) : 0.f;
+  float m = -INFINITY, l = 0.f, gl = 0.f;
+  const float g = w * p.tau;
+  if (w != 0.f && PASS != GRAD_ONLY) {
+    Running<E> sum(p.c);
+    for (int j = row.w0 + lane; j < row.w1; j += U * 32) {
+      uint4 r[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (j + u * 32 < row.w1) r[u] = row.base[j + u * 32];
+      sum.add(r, row.w1 - j, 32);
+    }
+    if (e >= 0) sum.add(ze);
+    m = sum.m;
+    l = sum.l;
+    merge_warp(m, l, p.c);
+    gl = g / l;
+  }
+  if (any) list_softmax(te, p);
+  if (w != 0.f && PASS != GRAD_ONLY) store_loss(te, p, t, any, w, m, l);
+  if (PASS == LOSS) return;
+  if (!any) {  // masked, or a list of nothing
+    for (int j = row.w0 + lane; j < row.w1; j += 32) dst[j] = make_uint4(0, 0, 0, 0);
+    if (e >= 0) out[e] = from_f<E>(0.f);
+    return;
+  }
+  if (PASS == GRAD_ONLY) {
+    const float2 st = p.stats[t];
+    const Ref ref(st.x, p.c);
+    m = st.x;
+    gl = g * ex2(-st.y * LOG2E - (ref.wide ? 0.f : fmaf(st.x, p.c, -ref.mc)));
+  }
+  const Ref ref(m, p.c);
+  for (int j = row.w0 + lane; j < row.w1; j += 32) {
+    float f[N];
+    grad_vec<E>(row.base[j], ref, p.c, gl, f);
+    dst[j] = pack16(f, (E *)nullptr);
+  }
+  if (e >= 0) out[e] = from_f<E>(gl * ex2(ref(ze, p.c)));
+  __syncwarp();
+  patch_entries(te, p, row, out, row.w0, row.w1, true, ref, gl, g);
 }
 
 DistillParams params_of(const DistillArgs &a) {
@@ -365,9 +617,17 @@ DistillParams params_of(const DistillArgs &a) {
 // the other writes.
 constexpr int SLICE_VECS = 108 * 1024 / 16, SLICE_MAX = 200 * 1024 / 16;
 
+template <typename E, int PASS>
+cudaError_t short_t(const DistillArgs &a, cudaStream_t s) {
+  return launch_k(distill_short_kernel<E, PASS>,
+                  dim3((unsigned)(((long long)a.T + SHORT_WARPS - 1) / SHORT_WARPS)),
+                  dim3(SHORT_WARPS * 32), 0, s, (const E *)a.z, (E *)a.dz, params_of(a), a.T);
+}
+
 template <typename E, bool GRAD>
 cudaError_t forward_t(const DistillArgs &a, cudaStream_t s) {
-  const int nvec = (int)(((long long)a.V + 2 * VEC16<E> - 2) / VEC16<E>);  // (any alignment)
+  if (a.V / VEC16<E> <= SHORT_VECS) return short_t<E, GRAD ? LOSS_GRAD : LOSS>(a, s);
+  const int nvec = (int)((size_t)a.V / VEC16<E>);  // at most so many whole vectors
   int C = 1;
   if (GRAD)
     while (C < MAX_CLUSTER && (nvec + C - 1) / C > SLICE_VECS) C *= 2;
@@ -382,17 +642,22 @@ cudaError_t forward_t(const DistillArgs &a, cudaStream_t s) {
            : cudaSuccess;
   if (attr != cudaSuccess) return attr;
   if ((long long)a.T * C > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-  return launch_clusters(kern, dim3((unsigned)(a.T * C)), dim3(per <= 1024 ? 256 : 512),
+  return launch_clusters(kern, dim3((unsigned)(a.T * C)), dim3(32 * (MAX_WARPS + 1)),
                          (size_t)cap * 16, C, s, (const E *)a.z, (E *)a.dz, params_of(a), cap);
 }
 
 template <typename E>
 cudaError_t backward_t(const DistillArgs &a, cudaStream_t s) {
-  const int nvec = (int)(((long long)a.V + 2 * VEC16<E> - 2) / VEC16<E>);
-  const int slabs = (nvec + BWD_SLAB - 1) / BWD_SLAB;
+  if (a.V / VEC16<E> <= SHORT_VECS) return short_t<E, GRAD_ONLY>(a, s);
+  const int nvec = a.V / VEC16<E>;
+  // whole rows (the list is worked through once), in slabs of at least 1024
+  // vectors while there are not four CTAs an SM
+  int slabs = 1;
+  while ((long long)a.T * slabs < 4 * num_sms() && nvec / (2 * slabs) >= 1024) slabs *= 2;
+  const int slab_vecs = (nvec + slabs - 1) / slabs;
   if ((long long)a.T * slabs > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-  return launch_k(distill_backward_kernel<E>, dim3((unsigned)((long long)a.T * slabs)), dim3(256),
-                  0, s, (const E *)a.z, (E *)a.dz, params_of(a), slabs);
+  return launch_k(distill_backward_kernel<E>, dim3((unsigned)((long long)a.T * slabs)),
+                  dim3(BWD_THREADS + 32), 0, s, (const E *)a.z, (E *)a.dz, params_of(a), slabs, slab_vecs);
 }
 
 }  // namespace
