@@ -4,13 +4,16 @@
 //   loss = w tau^2 sum_i p_i (log p_i - log q_{id_i}),  dz = w tau (q - p)
 //
 // The logits are the whole cost: 2 bytes in and 2 out per entry in bf16, and
-// one exponential for the sum and one for the gradient.  The forward with
-// the gradient reads each logit once: a thread-block cluster takes a row,
-// every CTA keeps its slice in shared memory while it forms the running
-// maximum and sum, the CTAs exchange those through distributed shared
-// memory, and the slice is written out as the gradient.  The entries of the
-// teacher's list are then patched by the CTA whose slice holds them, so p is
-// never spread over the vocabulary.
+// one exponential for the sum and one for the gradient.  HBM bounds it, then
+// the exponentials (16 a clock an SM).  The forward with the gradient reads
+// each logit from HBM once; by the shape, a row belongs to
+//   a warp            up to 256 vectors of 16 bytes
+//   a CTA             many rows: it streams the row twice, the second time
+//                     from L2
+//   a cluster of CTAs few rows: each keeps its slice in shared memory, and
+//                     maxima and sums go through distributed shared memory
+// p is never spread over the vocabulary: the list's entries of the gradient
+// are written over what the stream left there.
 //
 // One warp of each CTA deals with the teacher's list while the others stream
 // the logits: its softmax, repeated ids, the student's logits there, the loss,
@@ -331,16 +334,83 @@ __device__ __forceinline__ void merge_warp(float &m, float &l, float c) {
   m = top;
 }
 
-// 16 bytes from global to shared memory, asynchronously.
-__device__ __forceinline__ void copy16_async(void *dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+// 16 bytes from global to shared memory, asynchronously, with an L2 policy.
+__device__ __forceinline__ void copy16_async(void *dst, const void *src, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(
                    (uint32_t)__cvta_generic_to_shared(dst)),
-               "l"(src)
+               "l"(src), "l"(policy)
                : "memory");
 }
+__device__ __forceinline__ uint64_t keep_policy() {
+  uint64_t pol;
+  asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
 
-// One cluster a row, each CTA a slice of `per` of its whole vectors (the first
-// one the row's ends too).  The last warp keeps the teacher's list, the others
+// A thread's own stream through shared memory: vectors first, first + step,
+// ... below `end` of a row, RING of them in flight (registers would hold half
+// as many), taken two at a time: f(two vectors, how many of them, index of the
+// first).
+constexpr int RING = 8;
+template <typename F>
+__device__ __forceinline__ void stream_vectors(const uint4 *base, int first, int end, int step,
+                                               uint4 *ring, int threads, uint64_t policy, F f) {
+  uint4 *mine = ring + threadIdx.x;
+  const uint4 *src = base + first;
+#pragma unroll
+  for (int s = 0; s < RING; s += 2) {
+#pragma unroll
+    for (int i = s; i < s + 2; ++i)
+      if (first + i * step < end) copy16_async(mine + i * threads, src + i * step, policy);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  for (int j = first; j < end; j += RING * step) {
+    src += RING * step;
+#pragma unroll
+    for (int s = 0; s < RING; s += 2) {
+      if (j + s * step >= end) break;
+      asm volatile("cp.async.wait_group %0;" ::"n"(RING / 2 - 1) : "memory");
+      const uint4 r[2] = {mine[s * threads], mine[(s + 1) * threads]};
+      const int n = j + (s + 1) * step < end ? 2 : 1;
+#pragma unroll
+      for (int i = s; i < s + 2; ++i)
+        if (j + (RING + i) * step < end)
+          copy16_async(mine + i * threads, src + i * step, policy);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      f(r, n, j + s * step);
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// Adds a row's vectors [ja, jb), streamed by the first `threads` threads.
+template <typename E>
+__device__ __forceinline__ void sum_vectors(Running<E> &sum, const Row<E> &row, int ja, int jb,
+                                            uint4 *ring, int threads, uint64_t policy) {
+  stream_vectors(row.base, ja + (int)threadIdx.x, jb, threads, ring, threads, policy,
+                 [&](const uint4 (&r)[2], int n, int) { sum.add(r, n, 1); });
+}
+
+// Writes the gradient at a row's vectors [ja, jb), entries apart, in the same
+// way.
+template <typename E>
+__device__ __forceinline__ void grad_vectors(const Row<E> &row, E *out, int ja, int jb, uint4 *ring,
+                                             int threads, const Ref &ref, float c, float gl) {
+  uint4 *dst = (uint4 *)(out - row.lead);
+  stream_vectors(row.base, ja + (int)threadIdx.x, jb, threads, ring, threads,
+                 gather_policy<L2_FIRST>(), [&](const uint4 (&r)[2], int n, int j) {
+#pragma unroll
+                   for (int i = 0; i < 2; ++i) {
+                     if (i == n) break;
+                     float f[VEC16<E>];
+                     grad_vec<E>(r[i], ref, c, gl, f);
+                     stg_stream(dst + j + i * threads, pack16(f, (E *)nullptr));
+                   }
+                 });
+}
+
+// Few rows: one cluster a row, each CTA a slice of `per` of its whole vectors
+// (the first one the row's ends too).  The last warp keeps the teacher's list, the others
 // stream.  GRAD: the first `cap` vectors of a slice stay in shared memory (all
 // of them unless the row is longer than the cluster's shared memory; the rest
 // is read again).
@@ -366,10 +436,11 @@ distill_forward_kernel(const E *z, E *dz, DistillParams p, int cap) {
   const int SW = (int)blockDim.x / 32 - 1, ST = SW * 32;  // streaming warps, threads
   const int js = GRAD ? min(jb, ja + cap) : ja;
   const int jh = min(js, ja + ((js - ja) / 2 + ST - 1) / ST * ST);
+  const uint64_t once = gather_policy<L2_FIRST>();
   if (GRAD && warp < SW) {
-    for (int j = ja + (int)threadIdx.x; j < jh; j += ST) copy16_async(slice + (j - ja), row.base + j);
+    for (int j = ja + (int)threadIdx.x; j < jh; j += ST) copy16_async(slice + (j - ja), row.base + j, once);
     asm volatile("cp.async.commit_group;" ::: "memory");
-    for (int j = jh + (int)threadIdx.x; j < js; j += ST) copy16_async(slice + (j - ja), row.base + j);
+    for (int j = jh + (int)threadIdx.x; j < js; j += ST) copy16_async(slice + (j - ja), row.base + j, once);
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
   const float w = p.w ? p.w[t] : 1.f;
@@ -397,13 +468,16 @@ distill_forward_kernel(const E *z, E *dz, DistillParams p, int cap) {
   } else {
     Running<E> sum(p.c);
     if (e >= 0) ze = to_f(zr[e]);
-    // what shared memory does not hold
-    for (int j = js + (int)threadIdx.x; j < jb; j += U * ST) {
-      uint4 r[U];
+    if (!GRAD) {
+      sum_vectors(sum, row, ja, jb, slice, ST, once);
+    } else {  // what shared memory does not hold
+      for (int j = js + (int)threadIdx.x; j < jb; j += U * ST) {
+        uint4 r[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (j + u * ST < jb) r[u] = ld_once(row.base + j + u * ST);
-      sum.add(r, jb - j, ST);
+        for (int u = 0; u < U; ++u)
+          if (j + u * ST < jb) r[u] = ld_once(row.base + j + u * ST);
+        sum.add(r, jb - j, ST);
+      }
     }
     if (GRAD) {  // (each thread reads back only what it copied)
       auto held = [&](int from, int to) {
@@ -461,6 +535,74 @@ distill_forward_kernel(const E *z, E *dz, DistillParams p, int cap) {
   }
 }
 
+// Many rows: a CTA each, and with the gradient two streamed passes, the second
+// one's reads from L2: at most 1024 streaming threads an SM keep 304 of the
+// longest rows in flight (80 MB at 131072 bf16 logits; L2 has 126), and the
+// first pass asks L2 to keep what it reads until the second has read it
+// (0.80 against 0.85 ms).  8192 x 131072, k 128: 0.77 ms, 5.5 TB/s, where the
+// cluster kernel below 2 CTAs an SM takes 1.10 ms: its CTAs stand still
+// between reading and writing, and three of them an SM do not cover that.
+template <typename E, int ROW_WARPS, bool GRAD>
+__global__ void __launch_bounds__(32 * ROW_WARPS + 32, 1024 / (32 * ROW_WARPS))
+distill_row_kernel(const E *z, E *dz, DistillParams p) {
+  pdl_begin();
+  constexpr int ROW_THREADS = 32 * ROW_WARPS;
+  extern __shared__ uint4 slice[];  // the streaming threads' rings
+  __shared__ Teacher te;
+  __shared__ float2 s_part[ROW_WARPS];
+  __shared__ int s_any;
+  const size_t t = blockIdx.x;
+  const E *zr = z + t * p.ldz;
+  E *out = GRAD ? dz + t * p.ldz : nullptr;
+  const Row<E> row(zr, p.V);
+  const float w = p.w ? p.w[t] : 1.f;
+  if (w == 0.f) {  // a masked row: nothing is read
+    if (GRAD) store_zeros(row, out, row.w0, row.w1, true, blockDim.x);
+    if (threadIdx.x == 0) {
+      p.loss[t] = 0.f;
+      p.stats[t] = make_float2(0.f, 0.f);
+    }
+    return;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool lists = warp == ROW_WARPS;
+  const int e = lists ? -1 : row.end(threadIdx.x);
+  float ze = 0.f;
+  if (lists) {
+    const bool any = load_list(te, p, zr, t);
+    if (lane == 0) s_any = any;
+  } else {
+    Running<E> sum(p.c);
+    if (e >= 0) {
+      ze = to_f(zr[e]);
+      sum.add(ze);
+    }
+    sum_vectors(sum, row, row.w0, row.w1, slice, ROW_THREADS,
+                GRAD ? keep_policy() : gather_policy<L2_FIRST>());
+    merge_warp(sum.m, sum.l, p.c);
+    if (lane == 0) s_part[warp] = make_float2(sum.m, sum.l);
+  }
+  __syncthreads();
+  float m = lane < ROW_WARPS ? s_part[lane].x : -INFINITY;
+  float l = lane < ROW_WARPS ? s_part[lane].y : 0.f;
+  merge_warp(m, l, p.c);
+  const Ref ref(m, p.c);
+  const bool any = s_any != 0;
+  const float g = w * p.tau, gl = g / l;
+  if (lists) {
+    if (any) list_softmax(te, p);
+    store_loss(te, p, t, any, w, m, l);
+  } else if (GRAD && any) {
+    grad_vectors(row, out, row.w0, row.w1, slice, ROW_THREADS, ref, p.c, gl);
+    if (e >= 0) out[e] = from_f<E>(gl * ex2(ref(ze, p.c)));
+  } else if (GRAD) {
+    store_zeros(row, out, row.w0, row.w1, true, ROW_THREADS);
+  }
+  if (!GRAD || !any) return;
+  __syncthreads();  // all is written before the list's entries
+  if (lists) patch_entries(te, p, row, out, row.w0, row.w1, true, ref, gl, g);
+}
+
 // The gradient from the forward's statistics: a row's slab of `slab_vecs`
 // vectors a CTA, eight warps that stream and one for the list.
 constexpr int BWD_THREADS = 256;
@@ -469,7 +611,6 @@ template <typename E>
 __global__ void __launch_bounds__(BWD_THREADS + 32)
 distill_backward_kernel(const E *z, E *dz, DistillParams p, int slabs, int slab_vecs) {
   pdl_begin();
-  constexpr int N = VEC16<E>, U = 4;
   const size_t t = blockIdx.x / slabs;
   const E *zr = z + t * p.ldz;
   const Row<E> row(zr, p.V);
@@ -484,6 +625,7 @@ distill_backward_kernel(const E *z, E *dz, DistillParams p, int slabs, int slab_
     return;
   }
   __shared__ Teacher te;
+  __shared__ uint4 ring[RING * BWD_THREADS];
   const bool lists = threadIdx.x >= BWD_THREADS;
   // the row's list may be empty, so every warp looks at it
   bool used = false;
@@ -504,28 +646,9 @@ distill_backward_kernel(const E *z, E *dz, DistillParams p, int slabs, int slab_
     __syncthreads();
     list_softmax(te, p);
   } else {
-    uint4 *dst = (uint4 *)(out - row.lead);
-    uint4 r[U];
-    int j = ja + (int)threadIdx.x;
-    auto load = [&] {
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (j + u * BWD_THREADS < jb) r[u] = ld_once(row.base + j + u * BWD_THREADS);
-    };
-    if (any) load();
     __syncthreads();
     if (any) {
-      while (j < jb) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (j + u * BWD_THREADS >= jb) break;
-          float f[N];
-          grad_vec<E>(r[u], ref, p.c, gl, f);
-          stg_stream(dst + j + u * BWD_THREADS, pack16(f, (E *)nullptr));
-        }
-        j += U * BWD_THREADS;
-        load();
-      }
+      grad_vectors(row, out, ja, jb, ring, BWD_THREADS, ref, p.c, gl);
       const int e = row.end(threadIdx.x);
       if (first && e >= 0) out[e] = from_f<E>(gl * ex2(ref(to_f(zr[e]), p.c)));
     } else {
@@ -624,17 +747,37 @@ cudaError_t short_t(const DistillArgs &a, cudaStream_t s) {
                   dim3(SHORT_WARPS * 32), 0, s, (const E *)a.z, (E *)a.dz, params_of(a), a.T);
 }
 
+template <typename E, int ROW_WARPS, bool GRAD>
+cudaError_t row_t(const DistillArgs &a, cudaStream_t s) {
+  auto kern = distill_row_kernel<E, ROW_WARPS, GRAD>;
+  constexpr int RING_BYTES = RING * 32 * ROW_WARPS * 16;
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_BYTES);
+  if (attr != cudaSuccess) return attr;
+  return launch_k(kern, dim3((unsigned)a.T), dim3(32 * ROW_WARPS + 32), RING_BYTES, s,
+                  (const E *)a.z, (E *)a.dz, params_of(a));
+}
+
 template <typename E, bool GRAD>
 cudaError_t forward_t(const DistillArgs &a, cudaStream_t s) {
   if (a.V / VEC16<E> <= SHORT_VECS) return short_t<E, GRAD ? LOSS_GRAD : LOSS>(a, s);
   const int nvec = (int)((size_t)a.V / VEC16<E>);  // at most so many whole vectors
+  // Streaming warps of a CTA, us at 8192 rows of 5001 | 12000 | 32000 | 80000 |
+  // 131072 logits: 4 warps 53 | 101 | 233 | 642 | 1072; 8 warps 80 | 144 | 215 |
+  // 616 | 1057; 16 warps 133 | 214 | 275 | 486 | 851 (cluster kernel: 89 | - |
+  // 240 | - | 1126).
+  if (a.T >= 2 * num_sms())
+    return nvec <= 2048   ? row_t<E, 4, GRAD>(a, s)
+           : nvec <= 7680 ? row_t<E, 8, GRAD>(a, s)
+                          : row_t<E, 16, GRAD>(a, s);
   int C = 1;
   if (GRAD)
     while (C < MAX_CLUSTER && (nvec + C - 1) / C > SLICE_VECS) C *= 2;
   // few rows: split them until every SM has two CTAs or a slice is 16 KB
   while (C < MAX_CLUSTER && (long long)a.T * C < 2 * num_sms() && nvec / C >= 1024) C *= 2;
   const int per = (nvec + C - 1) / C;
-  const int cap = !GRAD ? 0 : per < SLICE_MAX ? per : SLICE_MAX;
+  // (without a gradient: the ring of each streaming thread)
+  const int cap = !GRAD ? RING * 32 * MAX_WARPS : per < SLICE_MAX ? per : SLICE_MAX;
   auto kern = distill_forward_kernel<E, GRAD>;
   static const cudaError_t attr =
       GRAD ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
