@@ -29,9 +29,10 @@ namespace twell {
 namespace {
 
 constexpr int SORT_CTAS = 8;       // CTAs of the sorting cluster (the portable maximum)
-constexpr int SORT_THREADS = 1024;
+constexpr int SORT_THREADS = 512;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int DIGIT_MAX = 9;       // bits per pass: 2 passes sort any vocabulary below 2^18
+constexpr int ZERO_VECS = 2048;    // 16-byte vectors that a CTA zeroes
 constexpr int CHUNK = 16;          // sorted entries per chunk of step 2
 
 // The token at position t as a sort key: the token, or V for positions
@@ -80,7 +81,9 @@ embed_forward_kernel(const I *tokens, const E *table, int T, int V, int nv, floa
 }
 
 // ---- step 1: sort and zero ---------------------------------------------------
-// Cluster 0 sorts; the CTAs of the other clusters write zeros.  Least
+// Cluster 0 sorts; each CTA of the other clusters zeroes one 32 KB piece (as
+// few long-lived CTAs, of which not all fitted at once, the zeros took 492
+// where they now take 275 us for 2.1 GB).  Least
 // significant digit first; each CTA owns a contiguous eighth of the list and
 // each warp a contiguous part of that, walked in order, so that (digit, CTA,
 // warp, place in the warp's walk) is the stable order.  Per pass: counts per
@@ -93,16 +96,16 @@ struct SortSmem {
 };
 
 template <typename I>
-__global__ void __launch_bounds__(SORT_THREADS, 1)
+__global__ void __launch_bounds__(SORT_THREADS, 2)
 embed_sort_zero_kernel(const I *tokens, int T, int V, long long pad_id, uint32_t *key0,
                        int32_t *pos0, uint32_t *key1, int32_t *pos1, int passes, int bits,
                        uint4 *dtable, size_t table_vecs, int32_t *status) {
   pdl_begin();
   if (blockIdx.x >= SORT_CTAS) {
-    const size_t n = (size_t)(gridDim.x - SORT_CTAS) * SORT_THREADS;
-    for (size_t i = (size_t)(blockIdx.x - SORT_CTAS) * SORT_THREADS + threadIdx.x; i < table_vecs;
-         i += n)
-      stg_stream(dtable + i, make_uint4(0, 0, 0, 0));
+    const size_t i0 = (size_t)(blockIdx.x - SORT_CTAS) * ZERO_VECS + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < ZERO_VECS; i += SORT_THREADS)
+      if (i0 + i < table_vecs) dtable[i0 + i] = make_uint4(0, 0, 0, 0);
     return;
   }
   extern __shared__ uint8_t sort_smem_raw[];
@@ -194,57 +197,63 @@ embed_sort_zero_kernel(const I *tokens, int T, int V, long long pad_id, uint32_t
 }
 
 // ---- step 2: runs of equal tokens --------------------------------------------
-// A group of `tpr` threads takes one chunk and one slab of tpr 16-byte
-// vectors; the rows are loaded four at a time ahead of their use.
+// A group of `tpr` threads (whole warps) takes one chunk and one slab of tpr
+// 16-byte vectors.  Every warp holds the chunk's keys and positions a lane
+// each; rows are loaded eight at a time ahead of their use.
 template <typename E>
 __global__ void __launch_bounds__(256)
 embed_runs_kernel(const uint32_t *key, const int32_t *pos, const E *dy, int T, int V, int nv,
                   int tpr, int chunks, float scale, float *dtable, float *part) {
   pdl_begin();
-  constexpr int N = VEC16<E>;
+  constexpr int N = VEC16<E>, U = 8;
+  static_assert(CHUNK + 2 <= 32, "a warp holds a chunk and its neighbours");
   const int c = (int)blockIdx.x * (blockDim.x / tpr) + (int)threadIdx.x / tpr;
   const int v = (int)blockIdx.y * tpr + (int)threadIdx.x % tpr;
-  if (c >= chunks || v >= nv) return;
-  const int i0 = c * CHUNK, i1 = min(T, i0 + CHUNK);
+  if (c >= chunks) return;  // (uniform for the warp)
+  const int lane = threadIdx.x & 31;
+  const int i0 = c * CHUNK, n = min(T - i0, CHUNK);
   const int D = nv * N;
+  // lane 0: the entry before the chunk; 1 .. n: the chunk; n + 1: the next
+  const int at = i0 + lane - 1;
+  const uint32_t NONE = 0xFFFFFFFFu;
+  const uint32_t k_of = at >= 0 && at < T && lane <= n + 1 ? key[at] : NONE;
+  const int p_of = lane >= 1 && lane <= n ? pos[at] : 0;
   // the chunk's first run began before it / its last run goes on after it
-  const uint32_t first = key[i0];
-  const bool open_left = i0 > 0 && key[i0 - 1] == first;
-  const uint32_t last = key[i1 - 1];
-  const bool open_right = i1 < T && key[i1] == last;
+  bool left = __shfl_sync(NONE, k_of, 0) == __shfl_sync(NONE, k_of, 1);
+  const bool open_right = __shfl_sync(NONE, k_of, n) == __shfl_sync(NONE, k_of, n + 1);
   float acc[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) acc[j] = 0.f;
-  bool left = open_left;  // the current run is the one open to the left
-  for (int i = i0; i < i1; i += 4) {
-    uint32_t k[5];
-    uint4 r[4];
+  for (int i = 0; i < n; i += U) {
+    uint4 r[U];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      k[u] = i + u < i1 ? key[i + u] : 0xFFFFFFFFu;
-      r[u] = k[u] < (uint32_t)V ? ldg_stream((const uint4 *)dy + (size_t)pos[i + u] * nv + v)
-                                : make_uint4(0, 0, 0, 0);
+    for (int u = 0; u < U; ++u) {
+      const uint32_t k = __shfl_sync(NONE, k_of, min(i + u, CHUNK) + 1);
+      const int p = __shfl_sync(NONE, p_of, min(i + u, CHUNK) + 1);
+      r[u] = i + u < n && k < (uint32_t)V && v < nv ? ldg_stream((const uint4 *)dy + (size_t)p * nv + v)
+                                                    : make_uint4(0, 0, 0, 0);
     }
-    k[4] = i + 4 < i1 ? key[i + 4] : 0xFFFFFFFFu;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (k[u] >= (uint32_t)V) continue;  // no token here, nor further on
+    for (int u = 0; u < U; ++u) {
+      const uint32_t k = __shfl_sync(NONE, k_of, min(i + u, CHUNK) + 1);
+      const uint32_t next = __shfl_sync(NONE, k_of, min(i + u + 1, CHUNK) + 1);
+      if (i + u >= n || k >= (uint32_t)V) continue;  // no token here, nor further on
       float f[N];
       unpack(r[u], f, (E *)nullptr);
 #pragma unroll
       for (int j = 0; j < N; ++j) acc[j] += f[j];
-      if (k[u + 1] == k[u]) continue;
+      if (i + u + 1 < n && next == k) continue;
       // the run ends with this entry (or the chunk does)
-      const bool right = open_right && i + u == i1 - 1;
+      const bool right = open_right && i + u == n - 1;
       float *dst = left    ? part + ((size_t)c * 2) * D
                    : right ? part + ((size_t)c * 2 + 1) * D
-                           : dtable + (size_t)k[u] * D;
+                           : dtable + (size_t)k * D;
       const float m = left || right ? 1.f : scale;
+      if (v < nv)
 #pragma unroll
-      for (int j = 0; j < N; j += 4)
-        stg_stream(dst + (size_t)v * N + j,
-                   make_uint4(__float_as_uint(acc[j] * m), __float_as_uint(acc[j + 1] * m),
-                              __float_as_uint(acc[j + 2] * m), __float_as_uint(acc[j + 3] * m)));
+        for (int j = 0; j < N; j += 4)
+          *(float4 *)(dst + (size_t)v * N + j) =
+              make_float4(acc[j] * m, acc[j + 1] * m, acc[j + 2] * m, acc[j + 3] * m);
 #pragma unroll
       for (int j = 0; j < N; ++j) acc[j] = 0.f;
       left = false;
@@ -253,51 +262,75 @@ embed_runs_kernel(const uint32_t *key, const int32_t *pos, const E *dy, int T, i
 }
 
 // ---- step 3: runs that cross chunk ends ----------------------------------------
-// CTA c acts if a run begins in chunk c and goes on into chunk c + 1: its
-// parts are [c][1] and [c+1][0], [c+2][0], ... up to the chunk it ends in.
-// Eight warps take consecutive eighths of the parts (128 columns a CTA) and
-// their sums are added in order.
+// A run that begins in chunk c and goes on into chunk c + 1 has the parts
+// [c][1] and [c+1][0], [c+2][0], ... up to the chunk it ends in.  A CTA looks
+// at eight chunks, a warp each, and adds up those runs' parts for 256 columns:
+// four groups of 64 threads take consecutive quarters of the parts, whose sums
+// are added in order.
 __global__ void __launch_bounds__(256)
 embed_join_kernel(const uint32_t *key, int T, int V, int D, int chunks, float scale,
                   const float *part, float *dtable) {
   pdl_begin();
-  const int c = (int)blockIdx.x;
-  const int end = min(T, (c + 1) * CHUNK);
-  if (end >= T) return;
-  const uint32_t k = key[end - 1];
-  if (k >= (uint32_t)V || key[end] != k) return;
-  if (key[c * CHUNK] == k && c > 0 && key[c * CHUNK - 1] == k) return;  // began earlier
-  // the last chunk of the run: binary search for the first entry above k
-  int lo = end, hi = T;  // key[lo] == k; key[hi] > k (or hi == T)
-  while (hi - lo > 1) {
-    const int mid = lo + (hi - lo) / 2;
-    if (key[mid] == k) lo = mid;
-    else hi = mid;
-  }
-  const int n = lo / CHUNK - c;  // parts [c+1][0] .. [c+n][0]
+  __shared__ int s_parts[8];  // parts after the first; 0: nothing begins here and goes on
+  __shared__ uint32_t s_key[8];
+  __shared__ float4 s_sum[4][64];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int col = (int)blockIdx.y * 128 + lane * 4;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (col < D) {
-    if (warp == 0) acc = *(const float4 *)(part + ((size_t)c * 2 + 1) * D + col);
-    const int a = (int)((long long)n * warp / 8), b = (int)((long long)n * (warp + 1) / 8);
-#pragma unroll 4
-    for (int i = a; i < b; ++i) {
-      const float4 p = *(const float4 *)(part + (size_t)(c + 1 + i) * 2 * D + col);
-      acc.x += p.x; acc.y += p.y; acc.z += p.z; acc.w += p.w;
+  {
+    const int c = (int)blockIdx.x * 8 + warp;
+    int n = 0;
+    uint32_t k = 0;
+    if (c < chunks - 1) {
+      const int end = (c + 1) * CHUNK;
+      k = key[end - 1];
+      if (k < (uint32_t)V && key[end] == k &&
+          !(c > 0 && key[c * CHUNK] == k && key[c * CHUNK - 1] == k)) {
+        // the last entry with this key: 32 probes a step
+        int lo = end, hi = T;  // key[lo] == k; key[hi] > k (or hi == T)
+        while (hi - lo > 1) {
+          const int step = (hi - lo + 31) / 32;
+          const int at = lo + lane * step;
+          const uint32_t same = __ballot_sync(0xFFFFFFFFu, at < hi && key[at] == k);
+          const int last = 31 - __clz(same);  // (lane 0 holds)
+          hi = min(hi, lo + (last + 1) * step);
+          lo = lo + last * step;
+        }
+        n = lo / CHUNK - c;
+      }
+    }
+    if (lane == 0) {
+      s_parts[warp] = n;
+      s_key[warp] = k;
     }
   }
-  __shared__ float4 sums[8][32];
-  sums[warp][lane] = acc;
   __syncthreads();
-  if (warp != 0 || col >= D) return;
+  const int g = threadIdx.x >> 6, t = threadIdx.x & 63;
+  const int col = (int)blockIdx.y * 256 + t * 4;
+  for (int w = 0; w < 8; ++w) {
+    const int n = s_parts[w], c = (int)blockIdx.x * 8 + w;
+    if (n == 0) continue;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (col < D) {
+      if (g == 0) acc = *(const float4 *)(part + ((size_t)c * 2 + 1) * D + col);
+      const int a = (int)((long long)n * g / 4), b = (int)((long long)n * (g + 1) / 4);
+#pragma unroll 8
+      for (int i = a; i < b; ++i) {
+        const float4 p = *(const float4 *)(part + (size_t)(c + 1 + i) * 2 * D + col);
+        acc.x += p.x; acc.y += p.y; acc.z += p.z; acc.w += p.w;
+      }
+    }
+    s_sum[g][t] = acc;
+    __syncthreads();
+    if (g == 0 && col < D) {
 #pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    const float4 p = sums[i][lane];
-    acc.x += p.x; acc.y += p.y; acc.z += p.z; acc.w += p.w;
+      for (int i = 1; i < 4; ++i) {
+        const float4 p = s_sum[i][t];
+        acc.x += p.x; acc.y += p.y; acc.z += p.z; acc.w += p.w;
+      }
+      *(float4 *)(dtable + (size_t)s_key[w] * D + col) =
+          make_float4(acc.x * scale, acc.y * scale, acc.z * scale, acc.w * scale);
+    }
+    __syncthreads();
   }
-  *(float4 *)(dtable + (size_t)k * D + col) =
-      make_float4(acc.x * scale, acc.y * scale, acc.z * scale, acc.w * scale);
 }
 
 template <typename E, typename I>
@@ -322,12 +355,14 @@ cudaError_t embed_backward_t(const EmbedArgs &a, const void *dy, float *dtable,
   static const cudaError_t attr = cudaFuncSetAttribute(
       embed_sort_zero_kernel<I>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(SortSmem));
   if (attr != cudaSuccess) return attr;
-  // one CTA an SM: the sorting cluster beside the clusters that write zeros
-  const int clusters = num_sms() / SORT_CTAS > 1 ? num_sms() / SORT_CTAS : 2;
+  const size_t table_vecs = (size_t)a.V * a.D / 4;
+  const size_t zero_ctas = (table_vecs + ZERO_VECS - 1) / ZERO_VECS;
+  const size_t grid = SORT_CTAS + (zero_ctas + SORT_CTAS - 1) / SORT_CTAS * SORT_CTAS;
+  if (grid > 0x7FFFFFFFull) return cudaErrorInvalidValue;
   cudaError_t e = launch_clusters(
-      embed_sort_zero_kernel<I>, dim3(clusters * SORT_CTAS), dim3(SORT_THREADS), sizeof(SortSmem),
-      SORT_CTAS, s, (const I *)a.tokens, a.T, a.V, a.pad_id, w.key[0], w.pos[0], w.key[1], w.pos[1], passes, bits,
-                           (uint4 *)dtable, (size_t)a.V * a.D / 4, a.status);
+      embed_sort_zero_kernel<I>, dim3((unsigned)grid), dim3(SORT_THREADS), sizeof(SortSmem),
+      SORT_CTAS, s, (const I *)a.tokens, a.T, a.V, a.pad_id, w.key[0], w.pos[0], w.key[1],
+      w.pos[1], passes, bits, (uint4 *)dtable, table_vecs, a.status);
   if (e != cudaSuccess) return e;
   prof_mark(KID_EMBED_SORT, s);
   const int nv = (int)((size_t)a.D * sizeof(E) / 16);
@@ -341,7 +376,7 @@ cudaError_t embed_backward_t(const EmbedArgs &a, const void *dy, float *dtable,
   if (e != cudaSuccess) return e;
   prof_mark(KID_EMBED_RUNS, s);
   if (chunks > 1) {
-    e = launch_k(embed_join_kernel, dim3(chunks - 1, (a.D + 127) / 128), dim3(256), 0, s,
+    e = launch_k(embed_join_kernel, dim3((chunks + 7) / 8, (a.D + 255) / 256), dim3(256), 0, s,
                  (const uint32_t *)w.key[0], a.T, a.V, a.D, chunks, a.scale,
                  (const float *)w.part, dtable);
     prof_mark(KID_EMBED_JOIN, s);

@@ -23,13 +23,13 @@ twell_status check_scratch(const void *ws, size_t bytes, size_t need) {
   return TWELL_OK;
 }
 
-constexpr int EMBED_MAX_D = 65536;
+constexpr int EMBED_MAX_D = 65536, EMBED_MAX_T = 1 << 30;
 
 twell_status check_embed(const EmbedArgs &a) {
   twell_status st = check_dtype(a.dtype);
   if (st != TWELL_OK) return st;
   if (a.token_bytes != 4 && a.token_bytes != 8) return TWELL_ERR_DTYPE;
-  if (a.T < 1 || a.V < 1 || a.V == 0x7FFFFFFF || a.D < 1 || a.D > EMBED_MAX_D || !a.tokens ||
+  if (a.T < 1 || a.T > EMBED_MAX_T || a.V < 1 || a.V == 0x7FFFFFFF || a.D < 1 || a.D > EMBED_MAX_D || !a.tokens ||
       !a.status)
     return TWELL_ERR_ARG;
   if ((size_t)a.D * elem_size(a.dtype) % 16 != 0) return TWELL_ERR_ALIGN;
@@ -86,7 +86,7 @@ twell_status twell_embed_forward(const void *tokens, int token_bytes, const void
 }
 
 size_t twell_embed_workspace_size(int T, int V, int D) {
-  if (T < 1 || V < 1 || V == 0x7FFFFFFF || D < 1 || D > EMBED_MAX_D || D % 4 != 0) return 0;
+  if (T < 1 || T > EMBED_MAX_T || V < 1 || V == 0x7FFFFFFF || D < 1 || D > EMBED_MAX_D || D % 4 != 0) return 0;
   return carve_embed(nullptr, T, V, D).bytes;
 }
 

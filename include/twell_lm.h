@@ -37,7 +37,8 @@ twell_status twell_read_status(int32_t *status, void *stream);
  * tokens [T]: int32 (token_bytes 4) or int64 (8).  A position whose token is
  * pad_id gives a zero row and takes no gradient (pad_id = -1 pads nothing but
  * -1).  Any other token outside [0, V) is treated the same way and records
- * TWELL_ERR_INDEX.  1 <= T, V < 2^31 - 1; D*elem_size a multiple of 16. */
+ * TWELL_ERR_INDEX.  1 <= T <= 2^30, 1 <= V < 2^31 - 1, D <= 65536;
+ * D*elem_size a multiple of 16. */
 twell_status twell_embed_forward(const void *tokens, int token_bytes, const void *table, int T,
                                  int V, int D, int dtype, float scale, long long pad_id,
                                  void *out, int32_t *status, void *stream);
