@@ -334,13 +334,7 @@ __device__ __forceinline__ void merge_warp(float &m, float &l, float c) {
   m = top;
 }
 
-// 16 bytes from global to shared memory, asynchronously, with an L2 policy.
-__device__ __forceinline__ void copy16_async(void *dst, const void *src, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(
-                   (uint32_t)__cvta_generic_to_shared(dst)),
-               "l"(src), "l"(policy)
-               : "memory");
-}
+// L2 policy of what is read again soon.
 __device__ __forceinline__ uint64_t keep_policy() {
   uint64_t pol;
   asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));

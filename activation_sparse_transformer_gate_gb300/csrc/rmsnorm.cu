@@ -167,115 +167,153 @@ rmsnorm_forward_kernel(const uint4 *x, const uint4 *res, const float *weight, in
   }
 }
 
-// Backward.  CTAs walk the rows; each thread keeps its columns' part of dw
-// in registers over all its rows and writes it to the workspace at the end
-// (one row of `part` per row group of the grid).  The next row's loads are
-// issued before the current row's reduction.
+// Backward.  CTAs walk the rows; each thread keeps its columns' weights and
+// its part of dw in registers over all its rows and writes the latter to the
+// workspace at the end (one row of `part` a CTA, the row groups of a CTA
+// added).  BWD_STAGES rows of each thread's operands are on their way through
+// shared memory at any time: 16 warps an SM, all that the registers leave
+// room for, do not keep enough of HBM busy with loads to registers (16384 x
+// 4096 bf16: 100 us so).
+constexpr int BWD_STAGES = 4;
+
+template <int NV>
+constexpr int bwd_ring_bytes() {
+  return BWD_STAGES * 3 * NV * WARPS * 32 * 16;
+}
+
 template <typename E, int W, int NV>
 __global__ void __launch_bounds__(WARPS * 32)
 rmsnorm_backward_kernel(const uint4 *s_in, const float *weight, const float *rstd_in,
                         const uint4 *dy, const uint4 *ds, int T, int nv, float inv_d, uint4 *dx,
                         float *part) {
   pdl_begin();
-  constexpr int N = VEC16<E>;
+  constexpr int N = VEC16<E>, THREADS = WARPS * 32;
+  extern __shared__ uint4 ring[];  // [stage][operand][NV][thread]
   __shared__ float s_sum[2][WARPS];
   __shared__ uint32_t s_top[2][WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = (int)blockIdx.x * (WARPS / W) + warp / W;
   const int groups = (int)gridDim.x * (WARPS / W);
   const int v0 = (warp % W) * 32 + lane;
-  float dw[NV][N];
+  float dw[NV][N], w[NV][N];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
+    if (v0 + i * W * 32 < nv) load_w(weight, v0 + i * W * 32, w[i]);
 #pragma unroll
     for (int j = 0; j < N; ++j) dw[i][j] = 0.f;
-  uint4 a[NV], b[NV], c[NV];
-  auto load = [&](long long t) {
+  }
+  auto slot = [&](int st, int op, int i) { return ring + ((st * 3 + op) * NV + i) * THREADS + threadIdx.x; };
+  auto fetch = [&](long long t, int st) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = v0 + i * W * 32;
-      const bool ok = t < T && v < nv;
-      const size_t o = (size_t)t * nv + v;
-      a[i] = ok ? ld_once(s_in + o) : make_uint4(0, 0, 0, 0);
-      b[i] = ok ? ld_once(dy + o) : make_uint4(0, 0, 0, 0);
-      c[i] = ok && ds ? ld_once(ds + o) : make_uint4(0, 0, 0, 0);
+      if (t < T && v < nv) {
+        const size_t o = (size_t)t * nv + v;
+        copy16_async(slot(st, 0, i), s_in + o);
+        copy16_async(slot(st, 1, i), dy + o);
+        if (ds) copy16_async(slot(st, 2, i), ds + o);
+      }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  load(group);
+#pragma unroll
+  for (int st = 0; st < BWD_STAGES; ++st) fetch(group + (long long)st * groups, st);
+  float rstd_next = group < T ? rstd_in[group] : 0.f;
   // every group makes the same number of rounds (the reduction's barrier is
   // the CTA's)
   const int rounds = (T + groups - 1) / groups;
+  int st = 0;
   for (int r = 0; r < rounds; ++r) {
     const long long t = (long long)r * groups + group;
     const bool row_ok = t < T;
-    const float rstd = row_ok ? rstd_in[t] : 0.f;
-    uint4 sa[NV], sb[NV], sc[NV];
+    const float rstd = rstd_next;
+    rstd_next = t + groups < T ? rstd_in[t + groups] : 0.f;
+    asm volatile("cp.async.wait_group %0;" ::"n"(BWD_STAGES - 1) : "memory");
+    uint4 a[NV], b[NV], c[NV];
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      sa[i] = a[i]; sb[i] = b[i]; sc[i] = c[i];
-      const int v = v0 + i * W * 32;
-      if (!row_ok || v >= nv) continue;
-      float f[N], g[N], w[N];
+      if (!row_ok || v0 + i * W * 32 >= nv) continue;
+      a[i] = *slot(st, 0, i);
+      b[i] = *slot(st, 1, i);
+      c[i] = ds ? *slot(st, 2, i) : make_uint4(0, 0, 0, 0);
+      float f[N], g[N];
       unpack(a[i], f, (E *)nullptr);
       unpack(b[i], g, (E *)nullptr);
-      load_w(weight, v, w);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         const float xhat = f[j] * rstd;
         dw[i][j] += g[j] * xhat;
-        sum += g[j] * w[j] * xhat;
+        sum += g[j] * w[i][j] * xhat;
       }
     }
-    load(t + groups);
+    fetch(t + (long long)BWD_STAGES * groups, st);
+    st = st + 1 == BWD_STAGES ? 0 : st + 1;
     uint32_t none = 0;
     reduce_row<W>(sum, none, s_sum, s_top, r & 1);
     const float mean = sum * inv_d;
-    if (!row_ok) continue;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = v0 + i * W * 32;
-      if (v >= nv) break;
-      float f[N], g[N], h[N], w[N];
-      unpack(sa[i], f, (E *)nullptr);
-      unpack(sb[i], g, (E *)nullptr);
-      unpack(sc[i], h, (E *)nullptr);
-      load_w(weight, v, w);
+      if (!row_ok || v >= nv) continue;
+      float f[N], g[N], h[N];
+      unpack(a[i], f, (E *)nullptr);
+      unpack(b[i], g, (E *)nullptr);
+      unpack(c[i], h, (E *)nullptr);
 #pragma unroll
-      for (int j = 0; j < N; ++j) h[j] += rstd * (g[j] * w[j] - f[j] * rstd * mean);
-      dx[(size_t)t * nv + v] = pack16(h, (E *)nullptr);
+      for (int j = 0; j < N; ++j) h[j] += rstd * (g[j] * w[i][j] - f[j] * rstd * mean);
+      stg_stream(dx + (size_t)t * nv + v, pack16(h, (E *)nullptr));
     }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  // the CTA's row groups in order, through the ring's memory
+  float *sums = (float *)ring;  // [groups of the CTA][nv * N]
+  const int D = nv * N;
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = v0 + i * W * 32;
     if (v >= nv) break;
-    float *p = part + ((size_t)group * nv + v) * N;
+    float *p = WARPS / W > 1 ? sums + (size_t)(warp / W) * D + (size_t)v * N
+                             : part + (size_t)blockIdx.x * D + (size_t)v * N;
 #pragma unroll
     for (int j = 0; j < N; j += 4)
       *(float4 *)(p + j) = make_float4(dw[i][j], dw[i][j + 1], dw[i][j + 2], dw[i][j + 3]);
   }
+  if (WARPS / W == 1) return;
+  __syncthreads();
+  for (int d = threadIdx.x; d < D; d += THREADS) {
+    float acc = sums[d];
+#pragma unroll
+    for (int i = 1; i < WARPS / W; ++i) acc += sums[(size_t)i * D + d];
+    part[(size_t)blockIdx.x * D + d] = acc;
+  }
 }
 
-// dw[d] = sum of the groups' rows, in order: 32 columns a CTA, 32 warps take
-// every 32nd group and are added in order.
-__global__ void __launch_bounds__(1024)
-rmsnorm_dw_kernel(const float *part, int groups, int D, float *dw) {
+// dw[d] = sum of the CTAs' rows of `part`: 32 columns a CTA, four a thread; 32
+// threads take every 32nd row, and are added in order.
+__global__ void __launch_bounds__(256)
+rmsnorm_dw_kernel(const float *part, int rows, int D, float *dw) {
   pdl_begin();
-  __shared__ float sums[32][33];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int d = blockIdx.x * 32 + lane;
-  float acc = 0.f;
+  __shared__ float4 sums[32][8];
+  const int c = threadIdx.x & 7, g = threadIdx.x >> 3;
+  const int d = blockIdx.x * 32 + c * 4;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   if (d < D)
-#pragma unroll 4
-    for (int g = warp; g < groups; g += 32) acc += part[(size_t)g * D + d];
-  sums[warp][lane] = acc;
+#pragma unroll 10
+    for (int r = g; r < rows; r += 32) {
+      const float4 p = *(const float4 *)(part + (size_t)r * D + d);
+      acc.x += p.x; acc.y += p.y; acc.z += p.z; acc.w += p.w;
+    }
+  sums[g][c] = acc;
   __syncthreads();
-  if (warp != 0 || d >= D) return;
-  acc = 0.f;
+  if (g != 0 || d >= D) return;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) acc += sums[i][lane];
-  dw[d] = acc;
+  for (int i = 1; i < 32; ++i) {
+    const float4 p = sums[i][c];
+    acc.x += p.x; acc.y += p.y; acc.z += p.z; acc.w += p.w;
+  }
+  dw[d] = acc.x; dw[d + 1] = acc.y; dw[d + 2] = acc.z; dw[d + 3] = acc.w;
 }
 
 // Symmetric 8-bit rows of a matrix: a CTA per row, which is read twice (the
@@ -339,14 +377,21 @@ cudaError_t backward_t(const void *s_in, const float *weight, const float *rstd,
                        const void *ds, int T, int nv, void *dx, float *dweight, float *part,
                        cudaStream_t s) {
   const int grid = backward_grid(T, nv);
-  cudaError_t e = launch_k(rmsnorm_backward_kernel<E, W, NV>, dim3(grid), dim3(WARPS * 32), 0, s,
-                           (const uint4 *)s_in, weight, rstd, (const uint4 *)dy, (const uint4 *)ds,
+  // (the ring holds the row groups' sums at the end too: WARPS / W rows of
+  // at most W * 32 * NV vectors in fp32)
+  static_assert(bwd_ring_bytes<NV>() >= WARPS * 32 * NV * VEC16<E> * 4, "the sums fit");
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(rmsnorm_backward_kernel<E, W, NV>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, bwd_ring_bytes<NV>());
+  if (attr != cudaSuccess) return attr;
+  cudaError_t e = launch_k(rmsnorm_backward_kernel<E, W, NV>, dim3(grid), dim3(WARPS * 32),
+                           bwd_ring_bytes<NV>(), s, (const uint4 *)s_in, weight, rstd, (const uint4 *)dy, (const uint4 *)ds,
                            T, nv, 1.f / (float)(nv * VEC16<E>), (uint4 *)dx, part);
   if (e != cudaSuccess) return e;
   prof_mark(KID_RMSNORM_BWD, s);
   const int D = nv * VEC16<E>;
-  e = launch_k(rmsnorm_dw_kernel, dim3((D + 31) / 32), dim3(1024), 0, s, (const float *)part,
-               grid * (WARPS / W), D, dweight);
+  e = launch_k(rmsnorm_dw_kernel, dim3((D + 31) / 32), dim3(256), 0, s, (const float *)part, grid,
+               D, dweight);
   prof_mark(KID_RMSNORM_DW, s);
   return e;
 }
@@ -380,14 +425,12 @@ cudaError_t launch_add_rmsnorm_forward(const void *x, const void *residual, cons
 }
 
 size_t rmsnorm_scratch(int T, int D) {
-  // (the layout of either type: the finer one has the most row groups)
-  size_t groups = 0;
+  int grid = 0;  // of either type
   for (int n : {VEC16<bf16>, VEC16<float>}) {
-    const int nv = D / n;
-    const size_t g = (size_t)backward_grid(T, nv) * (WARPS / row_warps(nv, BWD_NV));
-    if (g > groups) groups = g;
+    const int g = backward_grid(T, (D + n - 1) / n);
+    if (g > grid) grid = g;
   }
-  return groups * (size_t)D * 4;
+  return (size_t)grid * (size_t)D * 4;
 }
 
 cudaError_t launch_add_rmsnorm_backward(const void *s_in, const float *weight, const float *rstd,

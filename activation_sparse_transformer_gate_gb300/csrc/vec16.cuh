@@ -18,6 +18,21 @@ __device__ __forceinline__ uint4 ld_once(const void *p) {
   return r;
 }
 
+// 16 bytes from global to shared memory, asynchronously, past L1.
+__device__ __forceinline__ void copy16_async(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src)
+               : "memory");
+}
+// The same with an L2 policy.
+__device__ __forceinline__ void copy16_async(void *dst, const void *src, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src), "l"(policy)
+               : "memory");
+}
+
 template <typename E> constexpr int VEC16 = 16 / (int)sizeof(E);
 
 __device__ __forceinline__ void unpack(const uint4 &u, float (&f)[4], float *) {
