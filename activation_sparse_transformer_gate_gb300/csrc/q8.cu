@@ -391,6 +391,13 @@ struct Ring {
   }
 };
 
+// A wait that a whole warp takes together: all lanes go on or all give up, so
+// that the warp stays whole for what follows.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+                                          int32_t *status) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, status));
+}
+
 // After an abort no copy may be in flight when the CTA exits: waits (bounded)
 // for the last load that was issued into each stage of a ring.
 __device__ __forceinline__ void drain_ring(uint32_t full, int S, long issued) {
@@ -473,7 +480,7 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
     for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
       const int m0 = (t % mb) * BM, n0 = (t / mb) * pl.bn;
       for (int kt = 0; kt < KT; ++kt) {
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(rempty + 8 * st, ph ^ 1, abort_flag, p.status));
+        ok = warp_wait(rempty + 8 * st, ph ^ 1, abort_flag, p.status);
         if (!ok) break;
         const uint32_t bar = rfull + 8 * st, dst = raw0 + st * pl.raw_bytes;
         if (issues) {
@@ -502,13 +509,12 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
       bool ok = true;
       for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++lt) {
         const int buf = lt & 1;
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(tempty + 8 * buf, ((uint32_t)(lt >> 1) & 1) ^ 1,
-                                               abort_flag, p.status));
+        ok = warp_wait(tempty + 8 * buf, ((uint32_t)(lt >> 1) & 1) ^ 1, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
         const uint32_t acc = tmem + (uint32_t)(buf * ACC_COLS);
         for (int kt = 0; kt < KT; ++kt) {
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(ffull + 8 * st, ph, abort_flag, p.status));
+          ok = warp_wait(ffull + 8 * st, ph, abort_flag, p.status);
           if (!ok) break;
           tc_fence_after();
           const uint64_t ad = ad0 + (uint32_t)(st * pl.f16_bytes >> 4), wd = ad + w_off;
@@ -565,8 +571,8 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
     const int mine = (tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
     Ring f(group, pl.f16), r(group, pl.raw);
     for (long it = group; it < (long)mine * KT; it += GROUPS) {
-      if (!mbar_wait(rfull + 8 * r.at, r.phase, abort_flag, p.status)) break;
-      if (!mbar_wait(fempty + 8 * f.at, f.phase ^ 1, abort_flag, p.status)) break;
+      if (!warp_wait(rfull + 8 * r.at, r.phase, abort_flag, p.status)) break;
+      if (!warp_wait(fempty + 8 * f.at, f.phase ^ 1, abort_flag, p.status)) break;
       widen_rows<32 * GROUP>(raw + r.at * pl.raw_bytes, f16 + f.at * pl.f16_bytes, ct, vecs);
       fence_async_proxy();  // the MMA reads through the async proxy
       __syncwarp();
@@ -706,7 +712,7 @@ q8_pair_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Pa
     for (int t = pair; t < tiles && ok; t += pairs) {
       const int row = is_w ? (t / mb) * bn + rank * half : (t % mb) * 2 * BM + rank * BM;
       for (int kt = 0; kt < KT; ++kt) {
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty + 8 * st, ph ^ 1, abort_flag, p.status));
+        ok = warp_wait(empty + 8 * st, ph ^ 1, abort_flag, p.status);
         if (!ok) break;
         if (issues) {
           mbar_expect_tx(full + 8 * st, (uint32_t)bytes);
@@ -746,13 +752,12 @@ q8_pair_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Pa
       bool ok = true;
       for (int t = pair; t < tiles && ok; t += pairs, ++lt) {
         const int buf = lt & 1;
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(tempty + 8 * buf, ((uint32_t)(lt >> 1) & 1) ^ 1,
-                                               abort_flag, p.status));
+        ok = warp_wait(tempty + 8 * buf, ((uint32_t)(lt >> 1) & 1) ^ 1, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
         const uint32_t acc = tmem + (uint32_t)(buf * ACC_COLS);
         for (int kt = 0; kt < KT; ++kt) {
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(ready + 8 * w.at, w.phase, abort_flag, p.status));
+          ok = warp_wait(ready + 8 * w.at, w.phase, abort_flag, p.status);
           if (!ok) break;
           tc_fence_after();
           const uint64_t ad = ad0 + (uint32_t)(a.at * (P_TILE >> 4));
@@ -806,8 +811,8 @@ q8_pair_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Pa
     const int vecs = half * (BK / 16);
     Ring w(group, P_BS), r(group, P_RS);
     for (long it = group; it < its; it += P_GROUPS) {
-      if (!mbar_wait(rfull + 8 * r.at, r.phase, abort_flag, p.status)) break;
-      if (!mbar_wait(wempty + 8 * w.at, w.phase ^ 1, abort_flag, p.status)) break;
+      if (!warp_wait(rfull + 8 * r.at, r.phase, abort_flag, p.status)) break;
+      if (!warp_wait(wempty + 8 * w.at, w.phase ^ 1, abort_flag, p.status)) break;
       widen_rows<32 * P_GROUP>(raw + r.at * P_RAW, sw16 + w.at * P_TILE, ct, vecs);
       fence_async_proxy();  // the MMA reads through the async proxy
       __syncwarp();

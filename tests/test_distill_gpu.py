@@ -143,10 +143,26 @@ def test_pitch_ragged_lists_and_masked_rows(dtype):
     assert (dz[4] == 0).all() and loss[4] == 0
 
 
+@pytest.mark.parametrize("V,dtype", [(70003, "bf16"), (5003, "f32"), (3001, "f32"), (20011, "bf16")])
+def test_a_cta_a_row(V, dtype):
+    """Enough rows for a CTA each, in every width of that kernel: ragged lists, masked rows of NaN,
+    and the gradient in place of the logits, the same bits as beside them."""
+    z, ids, t, w = inputs(308, V, 9, dtype, V, ragged=True)
+    w[::5] = 0
+    z[::5] = float("nan")
+    assert verify(z, ids, t, w, 1.5, dtype) == 0
+    for fused in (True, False):
+        a = run(z, ids, t, w, 1.5, dtype, fused=fused)
+        b = run(z, ids, t, w, 1.5, dtype, fused=fused, in_place=True)
+        for u, v in zip(a[:3], b[:3]):
+            assert torch.equal(u, v)
+
+
+@pytest.mark.parametrize("T,V", [(40, 777), (9, 40001), (1, 131075)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("fused", [True, False])
-def test_in_place(dtype, fused):
-    z, ids, t, w = inputs(40, 777, 9, dtype, 6)
+def test_in_place(dtype, fused, T, V):
+    z, ids, t, w = inputs(T, V, 9, dtype, 6)
     a = run(z, ids, t, w, 1.0, dtype, fused=fused)
     b = run(z, ids, t, w, 1.0, dtype, fused=fused, in_place=True)
     for u, v in zip(a[:3], b[:3]):
@@ -154,12 +170,12 @@ def test_in_place(dtype, fused):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_masked_logits(dtype):
+@pytest.mark.parametrize("V,rows", [(300, 8), (30011, 8), (6007, 312)])
+def test_masked_logits(dtype, V, rows):
     """Vocabulary masked with -inf or with the type's lowest value, also in a row of nothing
     else; large logits; a teacher entry that the student excludes has infinite loss."""
     tdt = DT[dtype][0]
-    V = 300
-    z, ids, t, _ = inputs(8, V, 6, dtype, 12)
+    z, ids, t, _ = inputs(rows, V, 6, dtype, 12)
     low = torch.finfo(tdt).min
     z[0, ::2] = -math.inf
     z[1, ::2] = low
@@ -167,6 +183,7 @@ def test_masked_logits(dtype):
     z[3] = z[3] * 1e4
     z[4] = 3e38
     z[5, 5:] = -math.inf
+    z[5, 77] = -math.inf
     for r in (0, 1):  # keep the teacher on what is left
         ids[r] = ids[r] // 2 * 2 + 1
         ids[r][ids[r] >= V] = 1
@@ -178,9 +195,10 @@ def test_masked_logits(dtype):
 
 
 @pytest.mark.parametrize("bad", [math.inf, math.nan])
-def test_bad_rows_stay_alone(bad):
+@pytest.mark.parametrize("V", [400, 20011])
+def test_bad_rows_stay_alone(bad, V):
     """A row with NaN or +inf has NaN outputs; the others are untouched."""
-    z, ids, t, w = inputs(6, 400, 5, "f32", 2)
+    z, ids, t, w = inputs(6, V, 5, "f32", 2)
     z[2, 31] = bad
     z[4] = -math.inf
     for fused in (True, False):
@@ -189,7 +207,7 @@ def test_bad_rows_stay_alone(bad):
         for r in (2, 4):
             assert torch.isnan(loss[r]) and torch.isnan(dz[r]).all()
         ok = [0, 1, 3, 5]
-        ref = reference(z[ok], ids[ok], t[ok], w[ok], 1.0, 400)
+        ref = reference(z[ok], ids[ok], t[ok], w[ok], 1.0, V)
         check(loss[ok], ref[0], ref[3], "f32", "loss")
         check(dz[ok], ref[2], ref[4], "f32", "dz")
 

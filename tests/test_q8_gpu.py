@@ -145,3 +145,49 @@ def test_other_stream_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+TIMEOUT_CHILD = """
+import sys
+import torch
+sys.path.insert(0, sys.argv[1])
+import activation_sparse_transformer_gate_gb300 as tw
+from activation_sparse_transformer_gate_gb300 import _build
+lib = tw.load(_build.lib_path("timeout"))
+sh = torch.cuda.current_stream().cuda_stream
+for M, N, K in ((100, 2000, 1024), (700, 2000, 1024), (100, 20000, 8192), (128, 50000, 4096),
+                (1000, 20000, 4096)):
+    a = torch.ones(M, K, dtype=torch.int8, device="cuda")
+    w = torch.ones(N, K, dtype=torch.int8, device="cuda")
+    sa, sw = torch.ones(M, device="cuda"), torch.ones(N, device="cuda")
+    y = torch.zeros(M, N, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    n = lib.twell_q8_workspace_size(M, N, K)
+    ws = torch.zeros(max(n, 1), dtype=torch.uint8, device="cuda")
+    P = lambda t: t.data_ptr()
+    rc = lib.twell_q8_matmul(P(a), P(sa), P(w), P(sw), None, M, N, K, 0, P(y), P(st), P(ws), n, sh)
+    print("RESULT", rc, lib.twell_read_status(P(st), sh), lib.twell_read_status(P(st), sh),
+          int((a.float().sum(1) == K).all()), int((y == K).all()))
+"""
+
+
+def test_waits_that_run_out():
+    """With the waits' limit at 1 ns (the test-only build) both tensor-core kernels return, record
+    TWELL_ERR_TIMEOUT and leave the context usable.  (A wait whose first try lasts until it is
+    satisfied does not run out: a call may also come through, and is then right.)"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    tw._build.build(variants=("timeout",))
+    r = subprocess.run([sys.executable, "-c", TIMEOUT_CHILD, root], capture_output=True, text=True,
+                       timeout=300, cwd=root)
+    assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-2000:]
+    got = [ln.split()[1:] for ln in r.stdout.splitlines() if ln.startswith("RESULT")]
+    assert len(got) == 5
+    for rc, first, second, usable, right in got:
+        assert rc == "0" and second == "0" and usable == "1", got
+        assert first == "-6" or (first == "0" and right == "1"), got
+    ran_out = [g[1] == "-6" for g in got]
+    assert ran_out[0] or ran_out[2] or ran_out[3], got      # up to 128 rows
+    assert ran_out[1] or ran_out[4], got                    # CTA pairs
