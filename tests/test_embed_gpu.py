@@ -69,6 +69,10 @@ CASES = [  # kind, T, V, D, dtype, token type
     ("uniform", 20000, 300000, 8, "bf16", torch.int32),   # three sort passes
     ("uniform", 70001, 300, 16, "bf16", torch.int64),
     ("uniform", 2000, 100, 4096, "f32", torch.int64),
+    ("same", 512, 3, 40, "bf16", torch.int32),            # the most tokens of the one-launch form
+    ("zipf", 512, 70001, 8, "bf16", torch.int64),
+    ("uniform", 511, 20, 1032, "f32", torch.int64),
+    ("zipf", 513, 300, 136, "bf16", torch.int64),         # the fewest of the sort
 ]
 
 
