@@ -99,6 +99,13 @@ __device__ __forceinline__ void stg_stream(void *p, const uint4 &v) {
 // TWELL_PDL=0 in the environment launches plainly.
 __device__ __forceinline__ void pdl_begin() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// The one exception: a kernel that only prepares an operand for the next one
+// lets it start (after pdl_begin, so that all before both is complete); the
+// next one calls pdl_begin where it first touches that operand.
+__device__ __forceinline__ void pdl_trigger() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 inline bool pdl_enabled() {
   static const bool on = [] {
     const char *e = getenv("TWELL_PDL");

@@ -210,30 +210,33 @@ q8_frag_kernel(const uint4 *a, const int8_t *w, const float *sa, const float *sw
 
 // ---- tensor cores --------------------------------------------------------------
 constexpr int BM = 128, BK = 64;
-constexpr int GROUPS = 4, GROUP = 4;            // conversion groups, warps of a group
-constexpr int THREADS = 32 * (6 + GROUPS * GROUP);  // TMA, MMA, 4 epilogue, conversion
-constexpr int F16_STAGES_MAX = 8, RAW_STAGES_MAX = 24;
-constexpr int ACC_COLS = 256;                   // TMEM columns of one accumulator
-constexpr int EPI_PITCH = 33;                   // 32-bit words of an epilogue staging row
+constexpr int ACC_COLS = 256;  // TMEM columns of one accumulator
+constexpr int EPI_PITCH = 33;  // 32-bit words of an epilogue staging row
+constexpr int GROUPS = 4;      // conversion groups, which take the k-blocks in turn
+
+// One CTA, or a pair of CTAs, per tile: rows of a, stages of a (fp16), of w in
+// fp16 and in 8 bits, warps of a conversion group.  Stages hold 128 rows.
+template <bool PAIR>
+struct Shape {
+  static constexpr int ROWS = PAIR ? 2 * BM : BM;
+  static constexpr int AS = PAIR ? 5 : 4, WS = 4, RS = PAIR ? 6 : 8;
+  static constexpr int GROUP = PAIR ? 2 : 4;
+  static constexpr int THREADS = 32 * (8 + GROUPS * GROUP);
+  static constexpr int TILE = BM * BK * 2, RAW = BM * BK;  // bytes of a stage
+  static constexpr int SMEM = 1024 + (AS + WS) * TILE + RS * RAW + 4 * 32 * EPI_PITCH * 4 + 2 * 256 * 4;
+};
 
 struct Q8Maps {
   CUtensorMap a, w;
 };
 
-// Shape of the pipeline (the same for every CTA).
-struct Q8Plan {
-  int bn;         // output columns per tile (a multiple of 16, at most 256)
-  int ar;         // rows of a that a tile holds (a multiple of 16, at most 128)
-  int raw, f16;   // stages (a k-block each)
-  int raw_bytes, f16_bytes;
-};
-
 struct Q8Params {
   int M, N, K;
+  int bn;   // output columns of a tile
+  int box;  // rows of a that a TMA box holds
   const float *sa, *sw, *bias;
   void *y;
   int32_t *status;
-  Q8Plan pl;
 };
 
 __device__ __forceinline__ void fence_async_proxy() {
@@ -257,7 +260,7 @@ __device__ __forceinline__ void scale32(float *v, float sa, const float *sw, con
 
 __device__ __forceinline__ void store_tile(const Q8Params &p, float *y, uint32_t acc, int m0,
                                            int n0, float sa, const float *s_sw, float *stage) {
-  const int lane = threadIdx.x & 31, cols = min(p.pl.bn, p.N - n0), rows = min(32, p.M - m0);
+  const int lane = threadIdx.x & 31, cols = min(p.bn, p.N - n0), rows = min(32, p.M - m0);
   for (int c0 = 0; c0 < cols; c0 += 32) {
     float v[32];
     tmem_ld32(acc + c0, v);
@@ -281,7 +284,7 @@ __device__ __forceinline__ void store_tile(const Q8Params &p, float *y, uint32_t
 __device__ __forceinline__ void store_tile(const Q8Params &p, bf16 *y, uint32_t acc, int m0,
                                            int n0, float sa, const float *s_sw, float *stage_f) {
   uint32_t *stage = (uint32_t *)stage_f;
-  const int lane = threadIdx.x & 31, cols = min(p.pl.bn, p.N - n0), rows = min(32, p.M - m0);
+  const int lane = threadIdx.x & 31, cols = min(p.bn, p.N - n0), rows = min(32, p.M - m0);
   const int odd_n = p.N & 1;                  // (n0 is even)
   const bool odd = (odd_n & (m0 + lane)) != 0;
   float carry = 0.f;
@@ -305,7 +308,7 @@ __device__ __forceinline__ void store_tile(const Q8Params &p, bf16 *y, uint32_t 
   for (int c0 = 0; c0 < cols; c0 += 64) {
     float v[64];
     tmem_ld32(acc + c0, *(float(*)[32])v);
-    if (c0 + 32 < p.pl.bn) tmem_ld32(acc + c0 + 32, *(float(*)[32])(v + 32));
+    if (c0 + 32 < p.bn) tmem_ld32(acc + c0 + 32, *(float(*)[32])(v + 32));
     scale32(v, sa, s_sw + c0, s_sw + 256 + c0);
     scale32(v + 32, sa, s_sw + c0 + 32, s_sw + 256 + c0 + 32);
     __syncwarp();
@@ -343,7 +346,7 @@ __device__ __forceinline__ void store_tile(const Q8Params &p, bf16 *y, uint32_t 
 // Scale and bias of a tile's columns, staged by the 128 epilogue threads.
 __device__ __forceinline__ void stage_columns(const Q8Params &p, int n0, float *s_sw, int et) {
   epi_bar();
-  for (int c = et; c < p.pl.bn; c += 128) {
+  for (int c = et; c < p.bn; c += 128) {
     s_sw[c] = n0 + c < p.N ? p.sw[n0 + c] : 0.f;
     s_sw[256 + c] = p.bias && n0 + c < p.N ? p.bias[n0 + c] : 0.f;
   }
@@ -413,217 +416,27 @@ __device__ __forceinline__ void drain_ring(uint32_t full, int S, long issued) {
 // the low word moves the start, 16 bytes a unit.
 __device__ __forceinline__ uint64_t desc_at(uint32_t saddr) { return sw128_desc(saddr, 16, 1024); }
 
-template <typename E>
-__global__ void __launch_bounds__(THREADS, 1)
-q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Params p) {
-  pdl_begin();
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  const Q8Plan pl = p.pl;
-  // An fp16 stage holds the ar rows of a, then the bn rows of w; the MMA's
-  // 128 rows of a run into those of w when ar < 128 (accumulator rows that
-  // are not stored).
-  uint8_t *f16 = smem;                                   // [f16][A ar rows, W bn rows] x 128 B
-  uint8_t *raw = smem + pl.f16 * pl.f16_bytes;           // [raw][A ar rows, W bn rows] x 64 B
-  float *s_epi = (float *)(raw + pl.raw * pl.raw_bytes); // [4][32][EPI_PITCH]
-  float *s_sw = s_epi + 4 * 32 * EPI_PITCH;              // [2][256] scale, bias of the columns
-  __shared__ uint64_t bars[2 * RAW_STAGES_MAX + 2 * F16_STAGES_MAX + 5];
-  __shared__ uint32_t s_tmem;
-  __shared__ int s_abort;
-  volatile int *abort_flag = &s_abort;
-  const uint32_t rfull = smem_u32(bars), rempty = rfull + 8 * RAW_STAGES_MAX;
-  const uint32_t ffull = rempty + 8 * RAW_STAGES_MAX, fempty = ffull + 8 * F16_STAGES_MAX;
-  const uint32_t tfull = fempty + 8 * F16_STAGES_MAX, tempty = tfull + 16, mma_done = tempty + 16;
-  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-
-  const int mb = (p.M + BM - 1) / BM, nb = (p.N + pl.bn - 1) / pl.bn;
-  const int tiles = mb * nb;  // M-blocks innermost: the CTAs in flight share few weight tiles
-  const int KT = (p.K + BK - 1) / BK;
-
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < pl.raw; ++i) {
-      mbar_init(rfull + 8 * i, 1);
-      mbar_init(rempty + 8 * i, GROUP);
-    }
-    for (int i = 0; i < pl.f16; ++i) {
-      mbar_init(ffull + 8 * i, GROUP);
-      mbar_init(fempty + 8 * i, 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(tfull + 8 * i, 1);
-      mbar_init(tempty + 8 * i, 4);
-    }
-    mbar_init(mma_done, 1);
-    s_abort = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(&s_tmem)),
-                 "r"(2 * ACC_COLS)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = s_tmem;
-
-  if (warp == 0) {
-    // ------------------------------------------------------ TMA producer --
-    const bool issues = elect_one();
-    const uint32_t raw0 = smem_u32(raw);
-    int st = 0;
-    uint32_t ph = 0;
-    long issued = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const int m0 = (t % mb) * BM, n0 = (t / mb) * pl.bn;
-      for (int kt = 0; kt < KT; ++kt) {
-        ok = warp_wait(rempty + 8 * st, ph ^ 1, abort_flag, p.status);
-        if (!ok) break;
-        const uint32_t bar = rfull + 8 * st, dst = raw0 + st * pl.raw_bytes;
-        if (issues) {
-          mbar_expect_tx(bar, (uint32_t)pl.raw_bytes);
-          tma_load_2d(dst, &maps.a, kt * BK, m0, bar);
-          tma_load_2d(dst + pl.ar * BK, &maps.w, kt * BK, n0, bar);
-        }
-        __syncwarp();
-        ++issued;
-        if (++st == pl.raw) {
-          st = 0;
-          ph ^= 1;
-        }
-      }
-    }
-    if (!ok) drain_ring(rfull, pl.raw, issued);
-  } else if (warp == 1) {
-    // --------------------------------------------------------- MMA issuer --
-    {
-      const bool issues = elect_one();
-      const uint32_t idesc = make_idesc(BM, pl.bn, false, false, true);
-      const uint64_t ad0 = desc_at(smem_u32(f16));
-      const uint32_t w_off = (uint32_t)(pl.ar * 128) >> 4;
-      int st = 0, lt = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++lt) {
-        const int buf = lt & 1;
-        ok = warp_wait(tempty + 8 * buf, ((uint32_t)(lt >> 1) & 1) ^ 1, abort_flag, p.status);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t acc = tmem + (uint32_t)(buf * ACC_COLS);
-        for (int kt = 0; kt < KT; ++kt) {
-          ok = warp_wait(ffull + 8 * st, ph, abort_flag, p.status);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t ad = ad0 + (uint32_t)(st * pl.f16_bytes >> 4), wd = ad + w_off;
-          if (issues) {
-#pragma unroll
-            for (int kk = 0; kk < BK / 16; ++kk)  // 32 bytes of a row a step
-              mma_bf16(acc, ad + 2 * kk, wd + 2 * kk, idesc, (kt > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(fempty + 8 * st);
-          }
-          __syncwarp();
-          if (++st == pl.f16) {
-            st = 0;
-            ph ^= 1;
-          }
-        }
-        if (!ok) break;
-        if (issues) mma_commit(tfull + 8 * buf);
-        __syncwarp();
-      }
-      // all MMAs issued by this thread are complete before TMEM is freed
-      if (issues) mma_commit(mma_done);
-      const uint64_t t0 = global_timer();
-      while (!mbar_try(mma_done, 0) && global_timer() - t0 < DRAIN_LIMIT_NS) {
-      }
-    }
-  } else if (warp < 6) {
-    // ------------------------------------------------------------ epilogue --
-    const int q = warp & 3;  // TMEM lane quadrant of this warp
-    const int et = threadIdx.x - 64;
-    float *stage = s_epi + q * 32 * EPI_PITCH;
-    int lt = 0;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++lt) {
-      const int m0 = (t % mb) * BM, n0 = (t / mb) * pl.bn;
-      const int buf = lt & 1;
-      const int m = m0 + q * 32 + lane;
-      stage_columns(p, n0, s_sw, et);
-      const float sa = m < p.M ? p.sa[m] : 0.f;
-      const bool ok = epi_all(mbar_wait(tfull + 8 * buf, (uint32_t)(lt >> 1) & 1, abort_flag,
-                                        p.status));
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * ACC_COLS);
-      if (m0 + q * 32 < p.M)  // (uniform for the warp)
-        store_tile(p, (E *)p.y, acc, m0 + q * 32, n0, sa, s_sw, stage);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(tempty + 8 * buf);
-    }
-  } else {
-    // ---------------------------------------------------------- conversion --
-    // Four groups of warps take the k-blocks in turn.
-    const int group = (warp - 6) / GROUP, ct = (threadIdx.x - 192) % (32 * GROUP);
-    const int vecs = (pl.ar + pl.bn) * (BK / 16);  // 16-byte vectors of a k-block
-    const int mine = (tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
-    Ring f(group, pl.f16), r(group, pl.raw);
-    for (long it = group; it < (long)mine * KT; it += GROUPS) {
-      if (!warp_wait(rfull + 8 * r.at, r.phase, abort_flag, p.status)) break;
-      if (!warp_wait(fempty + 8 * f.at, f.phase ^ 1, abort_flag, p.status)) break;
-      widen_rows<32 * GROUP>(raw + r.at * pl.raw_bytes, f16 + f.at * pl.f16_bytes, ct, vecs);
-      fence_async_proxy();  // the MMA reads through the async proxy
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(ffull + 8 * f.at);
-        mbar_arrive(rempty + 8 * r.at);
-      }
-      f.next<GROUPS>(pl.f16);
-      r.next<GROUPS>(pl.raw);
-    }
-  }
-
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(2 * ACC_COLS)
-                 : "memory");
-  }
-}
-
-// ---- tensor cores, CTA pairs ----------------------------------------------------
-// More than 128 rows of a: two CTAs (one cluster) share a 256 x bn tile.
-// Each holds 128 rows of a and bn / 2 rows of w, the leader issues
-// cta_group::2 MMAs over both, and each CTA stores its 128 rows.  a is
-// widened once by q8_widen_kernel and comes by TMA as fp16; w is widened
-// here, each row once per CTA pair: per k-block an SM then moves 64 KB through
-// shared memory (w in 8 bits twice and in fp16 once, a once, the MMA's reads)
-// where one CTA that widened both operands for its own 128 x 256 tile would
-// move 144 KB for the same multiplications, and shared memory, not the
-// tensor cores, was its bound.
+// a is widened once by q8_widen_kernel and comes by TMA as fp16; w comes by
+// TMA in 8 bits and is widened here, between two stages of shared memory.
 //
-// A conversion warp's stores, their fence and its arrival take about 2000
-// cycles from end to end, four times a k-block's MMAs, so four groups of
-// warps take the k-blocks in turn.  They arrive at a barrier of their own
-// CTA and one thread passes that on to the leader: a release across the
-// cluster by the storing warps themselves waits for their stores once more
-// (704 TFLOP/s at M 8192, N 14336, K 4096 with two groups that did).
-constexpr int P_AS = 5, P_BS = 4, P_RS = 6;     // stages: a, w in fp16, w in 8 bits
-constexpr int P_GROUPS = 4, P_GROUP = 2;        // conversion groups, warps of a group
-constexpr int P_THREADS = 32 * (8 + P_GROUPS * P_GROUP);
-constexpr int P_TILE = 128 * 128;               // bytes of an fp16 stage (a or w)
-constexpr int P_RAW = 128 * BK;
-constexpr int P_SMEM = 1024 + P_AS * P_TILE + P_BS * P_TILE + P_RS * P_RAW +
-                       4 * 32 * EPI_PITCH * 4 + 2 * 256 * 4;
-
+// Above 128 rows of a, two CTAs (one cluster) share a 256 x bn tile: each holds
+// 128 rows of a and bn / 2 rows of w, the leader issues cta_group::2 MMAs over
+// both, and each CTA stores its 128 rows.  Per k-block an SM then moves 64 KB
+// through shared memory (w in 8 bits twice and in fp16 once, a once, the MMA's
+// reads) where one CTA that widened both operands for its own 128 x 256 tile
+// would move 144 KB for the same multiplications, and shared memory, not the
+// tensor cores, was its bound (770 TFLOP/s at M 8192, N 14336, K 4096; pairs:
+// 1.7 PFLOP/s).
+//
+// A conversion warp's loads, stores, their fence and its arrival take about
+// 2000 cycles from end to end, four times a k-block's MMAs, so four groups of
+// warps take the k-blocks in turn.  They arrive at a barrier of their own CTA
+// and, in a pair, one thread passes that on to the leader.
 // fp16 copy of a.
 __global__ void __launch_bounds__(256)
 q8_widen_kernel(const uint4 *a, size_t vecs, uint4 *out) {
   pdl_begin();
+  pdl_trigger();  // (the product's weights are under way meanwhile)
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= vecs) return;
   uint4 lo, hi;
@@ -632,68 +445,70 @@ q8_widen_kernel(const uint4 *a, size_t vecs, uint4 *out) {
   out[2 * i + 1] = hi;
 }
 
-template <typename E>
-__global__ void __launch_bounds__(P_THREADS, 1)
-q8_pair_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Params p) {
-  pdl_begin();
+template <typename E, bool PAIR>
+__global__ void __launch_bounds__(Shape<PAIR>::THREADS, 1)
+q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Params p) {
+  // (everything but the fp16 rows of a was complete before q8_widen_kernel:
+  // only their producer waits for it)
+  using S = Shape<PAIR>;
+  constexpr int AS = S::AS, WS = S::WS, RS = S::RS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t *sa16 = smem, *sw16 = sa16 + P_AS * P_TILE, *raw = sw16 + P_BS * P_TILE;
-  float *s_epi = (float *)(raw + P_RS * P_RAW);
+  uint8_t *sa16 = smem, *sw16 = sa16 + AS * S::TILE, *raw = sw16 + WS * S::TILE;
+  float *s_epi = (float *)(raw + RS * S::RAW);
   float *s_sw = s_epi + 4 * 32 * EPI_PITCH;
-  // Barriers of this CTA: a stage is full, a stage is free again.  Barriers
-  // of the leader, at which both CTAs arrive: a k-block's operands are ready,
-  // an accumulator has been read (tempty).
-  __shared__ uint64_t bars[2 * P_AS + 3 * P_BS + 2 * P_RS + 5];
+  // Barriers of this CTA: a stage is full, a stage is free again.  In a pair,
+  // barriers of the leader, at which both CTAs arrive: a k-block's operands
+  // are ready, an accumulator has been read (tempty).
+  __shared__ uint64_t bars[2 * AS + 3 * WS + 2 * RS + 5];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   volatile int *abort_flag = &s_abort;
-  const uint32_t afull = smem_u32(bars), aempty = afull + 8 * P_AS;
-  const uint32_t wfull = aempty + 8 * P_AS, wempty = wfull + 8 * P_BS, ready = wempty + 8 * P_BS;
-  const uint32_t rfull = ready + 8 * P_BS, rempty = rfull + 8 * P_RS;
-  const uint32_t tfull = rempty + 8 * P_RS, tempty = tfull + 16, mma_done = tempty + 16;
+  // (where both rings have as many stages, one barrier frees a stage of each)
+  constexpr bool JOINT = AS == WS;
+  const uint32_t afull = smem_u32(bars);
+  const uint32_t wfull = afull + 8 * 2 * AS, wempty = wfull + 8 * WS, ready = wempty + 8 * WS;
+  const uint32_t aempty = JOINT ? wempty : afull + 8 * AS;
+  const uint32_t rfull = ready + 8 * WS, rempty = rfull + 8 * RS;
+  const uint32_t tfull = rempty + 8 * RS, tempty = tfull + 16, mma_done = tempty + 16;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int rank = (int)(blockIdx.x & 1);  // in the pair (clusters are consecutive CTAs)
-  const int bn = p.pl.bn, half = bn / 2;
+  const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;  // (a pair's CTAs are consecutive)
+  const int bn = p.bn, half = PAIR ? bn / 2 : bn;      // columns of the tile; rows of w here
 
-  const int mb = (p.M + 2 * BM - 1) / (2 * BM), nb = (p.N + bn - 1) / bn;
-  const int tiles = mb * nb;  // M-blocks innermost: the pairs in flight share few weight tiles
+  const int mb = (p.M + S::ROWS - 1) / S::ROWS, nb = (p.N + bn - 1) / bn;
+  const int tiles = mb * nb;  // M-blocks innermost: the tiles in flight share few weight tiles
   const int KT = (p.K + BK - 1) / BK;
-  const int pair = (int)blockIdx.x >> 1, pairs = (int)gridDim.x >> 1;
-  const long its = (long)((tiles - pair + pairs - 1) / pairs) * KT;  // k-blocks of this pair
+  // this CTA's or pair's tiles: unit, unit + units, ...; their k-blocks
+  const int unit = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
+  const int units = PAIR ? (int)gridDim.x >> 1 : (int)gridDim.x;
+  const long its = (long)((tiles - unit + units - 1) / units) * KT;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < P_AS; ++i) {
+    for (int i = 0; i < AS; ++i) {
       mbar_init(afull + 8 * i, 1);
-      mbar_init(aempty + 8 * i, 1);
+      if (!JOINT) mbar_init(aempty + 8 * i, 1);
     }
-    for (int i = 0; i < P_BS; ++i) {
-      mbar_init(wfull + 8 * i, P_GROUP);
+    for (int i = 0; i < WS; ++i) {
+      mbar_init(wfull + 8 * i, S::GROUP);
       mbar_init(wempty + 8 * i, 1);
       mbar_init(ready + 8 * i, 2);
     }
-    for (int i = 0; i < P_RS; ++i) {
+    for (int i = 0; i < RS; ++i) {
       mbar_init(rfull + 8 * i, 1);
-      mbar_init(rempty + 8 * i, P_GROUP);
+      mbar_init(rempty + 8 * i, S::GROUP);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(tfull + 8 * i, 1);
-      mbar_init(tempty + 8 * i, 8);
+      mbar_init(tempty + 8 * i, PAIR ? 8 : 4);
     }
     mbar_init(mma_done, 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(&s_tmem)),
-                 "r"(2 * ACC_COLS)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-  }
+  if (warp == 1) tmem_alloc<PAIR>(smem_u32(&s_tmem), 2 * ACC_COLS);
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();
+  if (PAIR) cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
 
@@ -701,16 +516,17 @@ q8_pair_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Pa
     // ------------------------------- TMA producers: w in 8 bits; a in fp16 --
     const bool issues = elect_one();
     const bool is_w = warp == 0;
+    if (!is_w) pdl_begin();
     const uint32_t full = is_w ? rfull : afull, empty = is_w ? rempty : aempty;
-    const uint32_t dst0 = smem_u32(is_w ? raw : sa16), step = is_w ? P_RAW : P_TILE;
-    const int S = is_w ? P_RS : P_AS, bytes = is_w ? half * BK : P_TILE;
+    const uint32_t dst0 = smem_u32(is_w ? raw : sa16), step = is_w ? S::RAW : S::TILE;
+    const int stages = is_w ? RS : AS, bytes = is_w ? half * BK : p.box * BK * 2;
     const CUtensorMap *map = is_w ? &maps.w : &maps.a;
     int st = 0;
     uint32_t ph = 0;
     long issued = 0;
     bool ok = true;
-    for (int t = pair; t < tiles && ok; t += pairs) {
-      const int row = is_w ? (t / mb) * bn + rank * half : (t % mb) * 2 * BM + rank * BM;
+    for (int t = unit; t < tiles && ok; t += units) {
+      const int row = is_w ? (t / mb) * bn + rank * half : (t % mb) * S::ROWS + rank * BM;
       for (int kt = 0; kt < KT; ++kt) {
         ok = warp_wait(empty + 8 * st, ph ^ 1, abort_flag, p.status);
         if (!ok) break;
@@ -720,65 +536,76 @@ q8_pair_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Pa
         }
         __syncwarp();
         ++issued;
-        if (++st == S) {
+        if (++st == stages) {
           st = 0;
           ph ^= 1;
         }
       }
     }
-    if (!ok) drain_ring(full, S, issued);
+    if (!ok) drain_ring(full, stages, issued);
   } else if (warp == 7) {
     // ------------- tells the leader that this CTA's operands have arrived --
-    if (lane == 0) {
+    if (PAIR && lane == 0) {
       const uint32_t to = cluster_addr(ready, 0);
-      Ring a(0, P_AS), w(0, P_BS);
+      Ring a(0, AS), w(0, WS);
       for (long it = 0; it < its; ++it) {
         if (!mbar_wait(afull + 8 * a.at, a.phase, abort_flag, p.status) ||
             !mbar_wait(wfull + 8 * w.at, w.phase, abort_flag, p.status))
           break;
         mbar_arrive_cluster(to + 8 * w.at);
-        a.next(P_AS);
-        w.next(P_BS);
+        a.next(AS);
+        w.next(WS);
       }
     }
   } else if (warp == 1) {
     // --------------------------------------------------------- MMA issuer --
     if (rank == 0) {
       const bool issues = elect_one();
-      const uint32_t idesc = make_idesc(2 * BM, bn, false, false, true);
+      const uint32_t idesc = make_idesc(S::ROWS, bn, false, false, true);
       const uint64_t ad0 = desc_at(smem_u32(sa16)), wd0 = desc_at(smem_u32(sw16));
-      Ring a(0, P_AS), w(0, P_BS);
+      // a k-block's operands: one barrier in a pair, one for a and one for w else
+      auto look = [&](const Ring &a, const Ring &w) {
+        return PAIR ? mbar_test(ready + 8 * w.at, w.phase)
+                    : mbar_test(wfull + 8 * w.at, w.phase) && mbar_test(afull + 8 * a.at, a.phase);
+      };
+      Ring a(0, AS), w(0, WS);
       int lt = 0;
-      bool ok = true;
-      for (int t = pair; t < tiles && ok; t += pairs, ++lt) {
+      bool ok = true, seen = false;
+      for (int t = unit; t < tiles && ok; t += units, ++lt) {
         const int buf = lt & 1;
         ok = warp_wait(tempty + 8 * buf, ((uint32_t)(lt >> 1) & 1) ^ 1, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
         const uint32_t acc = tmem + (uint32_t)(buf * ACC_COLS);
         for (int kt = 0; kt < KT; ++kt) {
-          ok = warp_wait(ready + 8 * w.at, w.phase, abort_flag, p.status);
-          if (!ok) break;
+          if (!__all_sync(0xFFFFFFFFu, seen)) {
+            ok = PAIR ? warp_wait(ready + 8 * w.at, w.phase, abort_flag, p.status)
+                      : warp_wait(wfull + 8 * w.at, w.phase, abort_flag, p.status) &&
+                            warp_wait(afull + 8 * a.at, a.phase, abort_flag, p.status);
+            if (!ok) break;
+          }
           tc_fence_after();
-          const uint64_t ad = ad0 + (uint32_t)(a.at * (P_TILE >> 4));
-          const uint64_t wd = wd0 + (uint32_t)(w.at * (P_TILE >> 4));
+          const uint64_t ad = ad0 + (uint32_t)(a.at * (S::TILE >> 4));
+          const uint64_t wd = wd0 + (uint32_t)(w.at * (S::TILE >> 4));
+          const uint32_t a_free = aempty + 8 * a.at, w_free = wempty + 8 * w.at;
+          a.next(AS);
+          w.next(WS);
+          seen = look(a, w);  // of the next k-block, under this one's issue
           if (issues) {
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk)
-              mma_f16_pair(acc, ad + 2 * kk, wd + 2 * kk, idesc, (kt > 0 || kk > 0) ? 1u : 0u);
-            mma_commit_pair(aempty + 8 * a.at);
-            mma_commit_pair(wempty + 8 * w.at);
+              mma_f16<PAIR>(acc, ad + 2 * kk, wd + 2 * kk, idesc, (kt > 0 || kk > 0) ? 1u : 0u);
+            if (!JOINT) mma_commit_to<PAIR>(a_free);
+            mma_commit_to<PAIR>(w_free);
           }
           __syncwarp();
-          a.next(P_AS);
-          w.next(P_BS);
         }
         if (!ok) break;
-        if (issues) mma_commit_pair(tfull + 8 * buf);
+        if (issues) mma_commit_to<PAIR>(tfull + 8 * buf);
         __syncwarp();
       }
       // all MMAs issued by this thread are complete before TMEM is freed
-      if (issues) mma_commit_pair(mma_done);
+      if (issues) mma_commit_to<PAIR>(mma_done);
       const uint64_t t0 = global_timer();
       while (!mbar_try(mma_done, 0) && global_timer() - t0 < DRAIN_LIMIT_NS) {
       }
@@ -787,10 +614,10 @@ q8_pair_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Pa
     // ------------------------------------------------------------ epilogue --
     const int q = warp & 3;  // TMEM lane quadrant of this warp
     float *stage = s_epi + q * 32 * EPI_PITCH;
-    const uint32_t free = cluster_addr(tempty, 0);
+    const uint32_t free = PAIR ? cluster_addr(tempty, 0) : tempty;
     int lt = 0;
-    for (int t = pair; t < tiles; t += pairs, ++lt) {
-      const int m0 = (t % mb) * 2 * BM + rank * BM + q * 32, n0 = (t / mb) * bn;
+    for (int t = unit; t < tiles; t += units, ++lt) {
+      const int m0 = (t % mb) * S::ROWS + rank * BM + q * 32, n0 = (t / mb) * bn;
       const int buf = lt & 1;
       stage_columns(p, n0, s_sw, threadIdx.x - 64);
       const float sa = m0 + lane < p.M ? p.sa[m0 + lane] : 0.f;
@@ -803,37 +630,39 @@ q8_pair_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Pa
                    n0, sa, s_sw, stage);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(free + 8 * buf);
+      if (lane == 0) {
+        if (PAIR) mbar_arrive_cluster(free + 8 * buf);
+        else mbar_arrive(free + 8 * buf);
+      }
     }
   } else {
     // ---------------------------------------------------------- conversion --
-    const int group = (warp - 8) / P_GROUP, ct = (threadIdx.x - 256) % (32 * P_GROUP);
+    const int group = (warp - 8) / S::GROUP, ct = (threadIdx.x - 256) % (32 * S::GROUP);
     const int vecs = half * (BK / 16);
-    Ring w(group, P_BS), r(group, P_RS);
-    for (long it = group; it < its; it += P_GROUPS) {
+    Ring w(group, WS), r(group, RS);
+    for (long it = group; it < its; it += GROUPS) {
       if (!warp_wait(rfull + 8 * r.at, r.phase, abort_flag, p.status)) break;
       if (!warp_wait(wempty + 8 * w.at, w.phase ^ 1, abort_flag, p.status)) break;
-      widen_rows<32 * P_GROUP>(raw + r.at * P_RAW, sw16 + w.at * P_TILE, ct, vecs);
+      widen_rows<32 * S::GROUP>(raw + r.at * S::RAW, sw16 + w.at * S::TILE, ct, vecs);
       fence_async_proxy();  // the MMA reads through the async proxy
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(wfull + 8 * w.at);
         mbar_arrive(rempty + 8 * r.at);
       }
-      w.next<P_GROUPS>(P_BS);
-      r.next<P_GROUPS>(P_RS);
+      w.next<GROUPS>(WS);
+      r.next<GROUPS>(RS);
     }
   }
 
-  // neither CTA leaves while the other may reach its shared memory or TMEM
+  // neither CTA of a pair leaves while the other may reach its shared memory
+  // or TMEM
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();
+  if (PAIR) cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(2 * ACC_COLS)
-                 : "memory");
+    tmem_free<PAIR>(tmem, 2 * ACC_COLS);
   }
 }
 
@@ -852,18 +681,18 @@ bool make_map(CUtensorMap *m, const void *base, int rows, int K, int box, bool f
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int SMEM_FIXED = 1024 + 4 * 32 * EPI_PITCH * 4 + 2 * 256 * 4;
-constexpr int SMEM_MAX = 225 * 1024;
+// Rows of a from which CTA pairs are used.
+constexpr int PAIR_MIN = 129;
 
 // Tile width for `units` CTAs or pairs that work at once: the least (rounds)
-// x (width + `fixed`, a tile's cost apart from its width).
-int tile_width(int M, int N, int rows, int units, int step, int fixed) {
+// x (width + 32, a tile's cost apart from its width).
+int tile_width(int M, int N, int rows, int units, int step, int most) {
   const long mb = (M + rows - 1) / rows;
   long best = 0;
   int width = 0;
-  for (int bn = 256; bn >= step; bn -= step) {
+  for (int bn = most; bn >= step; bn -= step) {
     const long tiles = mb * ((N + bn - 1) / bn);
-    const long cost = (tiles + units - 1) / units * (bn + fixed);
+    const long cost = (tiles + units - 1) / units * (bn + 32);
     if (width == 0 || cost < best) {
       best = cost;
       width = bn;
@@ -872,59 +701,21 @@ int tile_width(int M, int N, int rows, int units, int step, int fixed) {
   return width;
 }
 
-Q8Plan plan_of(int M, int N) {
-  Q8Plan pl;
-  pl.ar = M > BM ? BM : (M + 15) / 16 * 16;
-  pl.bn = tile_width(M, N, BM, num_sms(), 16, 32);
-  pl.raw_bytes = (pl.ar + pl.bn) * BK;
-  pl.f16_bytes = (pl.ar + pl.bn) * 128;
-  // fp16 stages while the 8-bit stages keep a third of shared memory (the
-  // MMA's reach past the last fp16 stage stays inside it: a 128-row tile is
-  // 16 KB)
-  const int room = SMEM_MAX - SMEM_FIXED;
-  pl.f16 = F16_STAGES_MAX;
-  while (pl.f16 > 2 && room - pl.f16 * pl.f16_bytes < room / 3) --pl.f16;
-  pl.raw = (room - pl.f16 * pl.f16_bytes) / pl.raw_bytes;
-  if (pl.raw > RAW_STAGES_MAX) pl.raw = RAW_STAGES_MAX;
-  return pl;
-}
-
-template <typename E>
+template <typename E, bool PAIR>
 cudaError_t mma_t(const Q8Args &a, cudaStream_t s) {
-  Q8Params p;
-  p.M = a.M; p.N = a.N; p.K = a.K; p.sa = a.ascale; p.sw = a.wscale; p.bias = a.bias; p.y = a.y;
-  p.status = a.status;
-  p.pl = plan_of(a.M, a.N);
-  Q8Maps maps;
-  if (!make_map(&maps.a, a.aq, a.M, a.K, p.pl.ar, false) ||
-      !make_map(&maps.w, a.wq, a.N, a.K, p.pl.bn, false))
-    return cudaErrorInvalidValue;
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      q8_mma_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX);
-  if (attr != cudaSuccess) return attr;
-  const long long tiles =
-      (long long)((a.M + BM - 1) / BM) * ((a.N + p.pl.bn - 1) / p.pl.bn);
-  if (tiles > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-  const int grid = tiles < num_sms() ? (int)tiles : num_sms();
-  const size_t smem =
-      SMEM_FIXED + (size_t)p.pl.f16 * p.pl.f16_bytes + (size_t)p.pl.raw * p.pl.raw_bytes;
-  return launch_k(q8_mma_kernel<E>, dim3(grid), dim3(THREADS), smem, s, maps, p);
-}
-
-// Rows of a from which CTA pairs are used.
-constexpr int PAIR_MIN = 129;
-
-template <typename E>
-cudaError_t pair_t(const Q8Args &a, cudaStream_t s) {
-  static int most = 0;  // pairs that the GPU runs at once (its SM clusters may have odd ones out)
+  using S = Shape<PAIR>;
+  constexpr int CTAS = PAIR ? 2 : 1;
+  static int most = 0;  // CTAs or pairs that the GPU runs at once
   static const cudaError_t attr = [] {
-    cudaError_t e = cudaFuncSetAttribute(q8_pair_kernel<E>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM);
-    if (e != cudaSuccess) return e;
+    cudaError_t e = cudaFuncSetAttribute(q8_mma_kernel<E, PAIR>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    most = num_sms();
+    if (e != cudaSuccess || !PAIR) return e;
+    // (its SM clusters may have odd ones out)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (num_sms() / 2));
-    cfg.blockDim = dim3(P_THREADS);
-    cfg.dynamicSmemBytes = P_SMEM;
+    cfg.blockDim = dim3(S::THREADS);
+    cfg.dynamicSmemBytes = S::SMEM;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = 2;
@@ -932,7 +723,7 @@ cudaError_t pair_t(const Q8Args &a, cudaStream_t s) {
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&most, q8_pair_kernel<E>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&most, q8_mma_kernel<E, PAIR>, &cfg);
     return e == cudaSuccess && most < 1 ? cudaErrorInvalidConfiguration : e;
   }();
   if (attr != cudaSuccess) return attr;
@@ -947,16 +738,18 @@ cudaError_t pair_t(const Q8Args &a, cudaStream_t s) {
   memset(&p, 0, sizeof(p));
   p.M = a.M; p.N = a.N; p.K = a.K; p.sa = a.ascale; p.sw = a.wscale; p.bias = a.bias; p.y = a.y;
   p.status = a.status;
-  p.pl.bn = tile_width(a.M, a.N, 2 * BM, most, 32, 32);
+  p.bn = tile_width(a.M, a.N, S::ROWS, most, 16 * CTAS, 128 * CTAS);
+  p.box = a.M >= BM ? BM : (a.M + 7) / 8 * 8;
   Q8Maps maps;
-  if (!make_map(&maps.a, a.ws, a.M, a.K, BM, true) ||
-      !make_map(&maps.w, a.wq, a.N, a.K, p.pl.bn / 2, false))
+  if (!make_map(&maps.a, a.ws, a.M, a.K, p.box, true) ||
+      !make_map(&maps.w, a.wq, a.N, a.K, p.bn / CTAS, false))
     return cudaErrorInvalidValue;
-  const long long tiles =
-      (long long)((a.M + 2 * BM - 1) / (2 * BM)) * ((a.N + p.pl.bn - 1) / p.pl.bn);
+  const long long tiles = (long long)((a.M + S::ROWS - 1) / S::ROWS) * ((a.N + p.bn - 1) / p.bn);
   if (tiles > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-  const int grid = 2 * (tiles < most ? (int)tiles : most);
-  return launch_clusters(q8_pair_kernel<E>, dim3(grid), dim3(P_THREADS), P_SMEM, 2, s, maps, p);
+  const int grid = CTAS * (tiles < most ? (int)tiles : most);
+  return PAIR ? launch_clusters(q8_mma_kernel<E, PAIR>, dim3(grid), dim3(S::THREADS), S::SMEM, 2, s,
+                                maps, p)
+              : launch_k(q8_mma_kernel<E, PAIR>, dim3(grid), dim3(S::THREADS), S::SMEM, s, maps, p);
 }
 
 template <typename E, int MT>
@@ -991,14 +784,17 @@ cudaError_t frag_t(const Q8Args &a, cudaStream_t s) {
 }
 
 // Measured, us at N x K = 14336 x 4096 | 8192 x 2048 | 2048 x 2048 | 50001 x
-// 2048 (weights from HBM):
+// 2048 (weights from HBM; the floors, N x K bytes, are 8.6 | 2.5 | 0.6 | 15):
 //   M 1    rows 14.4 | 5.6 | 2.8 | 22.7    frag 15.9 | 6.5 | 3.9 | 22.6
 //   M 4    rows 12.4 | 6.9 | 2.9 | 24.1    frag 16.5 | 6.6 | 3.9 | 23.6
-//   M 8    rows 22.9 | 11.9 | 4.9 | 47.2   frag 16.8 | 6.6 | 3.9 | 24.8
-//   M 16   frag 17.9 | 8.3 | 4.8 | 33.1    mma 19.7 | 11.4 | 10.2 | 30.6
-//   M 32   frag 23.7 | 12.4 | 5.7 | 49.6   mma 19.8 | 11.4 | 10.3 | 35.7
-//   M 128  mma 27.1 | 14.0 | 11.7 | 49.2
-//   M 129  pair 28.3 | 16.2 | 13.6 | 52.5
+//   M 8    rows 22.9 | 11.9 | 4.9 | 47.2   frag 16.7 | 6.6 | 3.9 | 24.2
+//   M 16   frag 17.7 | 8.4 | 4.8 | 33.1    mma 21.6 | 13.1 | 11.6 | 37.7
+//   M 32   frag 23.7 | 12.4 | 5.7 | 49.6   mma 21.6 | 13.1 | 11.6 | 37.7
+//   M 64   mma 21.9 | 13.1 | 11.7 | 38.3
+//   M 128  mma 23.2 | 13.7 | 12.1 | 41.0
+//   M 129  pair 27.3 | 15.1 | 12.5 | 48.7
+// The mma kernels take about 440 cycles a k-block however narrow the tile:
+// the issuing warp's wait, four MMAs and commit.
 template <typename E>
 cudaError_t matmul_t(const Q8Args &a, cudaStream_t s) {
   if (a.M == 1) return rows_t<E, 1>(a, s);
@@ -1006,15 +802,15 @@ cudaError_t matmul_t(const Q8Args &a, cudaStream_t s) {
   if (a.M <= ROWS_MAX) return rows_t<E, 4>(a, s);
   if (a.M <= 8) return frag_t<E, 1>(a, s);
   if (a.M <= 16) return frag_t<E, 2>(a, s);
-  if (a.M <= 32 && a.N <= 4096) return frag_mt<E, 4, 1>(a, s);
-  return a.M < PAIR_MIN ? mma_t<E>(a, s) : pair_t<E>(a, s);
+  if (a.M <= 32 && a.N <= 8192) return frag_mt<E, 4, 1>(a, s);
+  return a.M < PAIR_MIN ? mma_t<E, false>(a, s) : mma_t<E, true>(a, s);
 }
 
 }  // namespace
 
 size_t q8_scratch(int M, int N, int K) {
-  (void)N;
-  return M < PAIR_MIN ? 0 : ((size_t)M * K * 2 + 255) / 256 * 256;  // a in fp16
+  // a in fp16
+  return M <= 16 || (M <= 32 && N <= 8192) ? 0 : ((size_t)M * K * 2 + 255) / 256 * 256;
 }
 
 cudaError_t launch_q8_matmul(const Q8Args &a, cudaStream_t s) {
