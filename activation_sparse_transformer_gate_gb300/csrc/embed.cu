@@ -4,7 +4,8 @@
 // gradient  dE[v]  = scale sum_{t: tok_t = v} dy[t]
 //
 // Both move rows and add; HBM bounds them.  The gradient writes the whole
-// [V][D] fp32 table once and reads dy once.  A gather per row in a fixed
+// [V][D] fp32 table once and reads dy once (V 131072, D 4096, 16384 tokens:
+// 332 us, 6.9 TB/s).  A gather per row in a fixed
 // order needs the positions grouped by token, so:
 //   1. one launch sorts (token, position) -- a stable radix sort by one
 //      thread-block cluster -- while every other cluster writes the zeros of
@@ -14,8 +15,9 @@
 //      chunk is summed and stored, a run that crosses a chunk's end leaves
 //      its part in the workspace;
 //   3. the parts of each crossing run are added in order.
-// No floating-point atomics: the grouping of every sum is fixed by T and the
-// tokens alone.
+// Up to 512 tokens one launch compares the positions instead.  No
+// floating-point atomics: the grouping of every sum is fixed by T and the tokens
+// alone.
 #include <cooperative_groups.h>
 
 #include "common.cuh"

