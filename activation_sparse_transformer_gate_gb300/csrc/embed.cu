@@ -355,7 +355,7 @@ embed_few_kernel(const I *tokens, const E *dy, int T, int V, int nv, float scale
   const size_t D = (size_t)nv * N;
   if ((int)blockIdx.x >= sum_ctas) {  // zeros
     __shared__ uint8_t named[FEW_ROWS];
-    const int v0 = ((int)blockIdx.x - sum_ctas) * rows_per, v1 = min(V, v0 + rows_per);
+    const int v0 = ((int)blockIdx.x - sum_ctas) * rows_per, v1 = v0 + min(rows_per, V - v0);
     for (int i = threadIdx.x; i < v1 - v0; i += 256) named[i] = 0;
     __syncthreads();
     for (int t = threadIdx.x; t < T; t += 256) {

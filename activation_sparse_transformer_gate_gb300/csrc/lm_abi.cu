@@ -11,6 +11,8 @@ namespace {
 
 bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
 
+constexpr int MAX_ROWS = 1 << 30;  // tokens, rows, output columns: sums of two stay in int32
+
 size_t elem_size(int dtype) { return dtype == TWELL_BF16 ? 2 : 4; }
 
 twell_status check_dtype(int dtype) {
@@ -23,14 +25,14 @@ twell_status check_scratch(const void *ws, size_t bytes, size_t need) {
   return TWELL_OK;
 }
 
-constexpr int EMBED_MAX_D = 65536, EMBED_MAX_T = 1 << 30;
+constexpr int EMBED_MAX_D = 65536;
 
 twell_status check_embed(const EmbedArgs &a) {
   twell_status st = check_dtype(a.dtype);
   if (st != TWELL_OK) return st;
   if (a.token_bytes != 4 && a.token_bytes != 8) return TWELL_ERR_DTYPE;
-  if (a.T < 1 || a.T > EMBED_MAX_T || a.V < 1 || a.V == 0x7FFFFFFF || a.D < 1 || a.D > EMBED_MAX_D || !a.tokens ||
-      !a.status)
+  if (a.T < 1 || a.T > MAX_ROWS || a.V < 1 || a.V == 0x7FFFFFFF || a.D < 1 ||
+      a.D > EMBED_MAX_D || !a.tokens || !a.status)
     return TWELL_ERR_ARG;
   if ((size_t)a.D * elem_size(a.dtype) % 16 != 0) return TWELL_ERR_ALIGN;
   if (((uintptr_t)a.tokens & (uintptr_t)(a.token_bytes - 1)) != 0 || !aligned4(a.status))
@@ -50,7 +52,7 @@ EmbedArgs embed_args(const void *tokens, int token_bytes, int T, int V, int D, i
 twell_status check_rows(int T, int D, int dtype) {
   twell_status st = check_dtype(dtype);
   if (st != TWELL_OK) return st;
-  if (T < 1 || D < 1) return TWELL_ERR_ARG;
+  if (T < 1 || T > MAX_ROWS || D < 1) return TWELL_ERR_ARG;
   const size_t bytes = (size_t)D * elem_size(dtype);
   if (bytes > 16384) return TWELL_ERR_ARG;
   return bytes % 16 == 0 ? TWELL_OK : TWELL_ERR_ALIGN;
@@ -86,7 +88,7 @@ twell_status twell_embed_forward(const void *tokens, int token_bytes, const void
 }
 
 size_t twell_embed_workspace_size(int T, int V, int D) {
-  if (T < 1 || T > EMBED_MAX_T || V < 1 || V == 0x7FFFFFFF || D < 1 || D > EMBED_MAX_D || D % 4 != 0) return 0;
+  if (T < 1 || T > MAX_ROWS || V < 1 || V == 0x7FFFFFFF || D < 1 || D > EMBED_MAX_D || D % 4 != 0) return 0;
   return carve_embed(nullptr, T, V, D).bytes;
 }
 
@@ -124,7 +126,7 @@ twell_status twell_add_rmsnorm_forward(const void *x, const void *residual, cons
 }
 
 size_t twell_add_rmsnorm_workspace_size(int T, int D) {
-  if (T < 1 || D < 4 || D > 8192 || D % 4 != 0) return 0;
+  if (T < 1 || T > MAX_ROWS || D < 4 || D > 8192 || D % 4 != 0) return 0;
   return rmsnorm_scratch(T, D);
 }
 
@@ -150,7 +152,8 @@ twell_status twell_q8_quantize(const void *a, int rows, int cols, int dtype, int
                                float *scale, void *stream) {
   const twell_status st = check_dtype(dtype);
   if (st != TWELL_OK) return st;
-  if (!a || !q || !scale || rows < 1 || cols < 1) return TWELL_ERR_ARG;
+  if (!a || !q || !scale || rows < 1 || rows > MAX_ROWS || cols < 1 || cols > MAX_ROWS)
+    return TWELL_ERR_ARG;
   if (cols % 16 != 0 || !aligned16(a) || !aligned16(q) || !aligned4(scale)) return TWELL_ERR_ALIGN;
   cudaStream_t s = (cudaStream_t)stream;
   prof_mark(KID_START, s);
@@ -158,7 +161,8 @@ twell_status twell_q8_quantize(const void *a, int rows, int cols, int dtype, int
 }
 
 size_t twell_q8_workspace_size(int M, int N, int K) {
-  if (M < 1 || N < 1 || K < 16 || K % 16 != 0 || K > Q8_MAX_K) return 0;
+  if (M < 1 || M > MAX_ROWS || N < 1 || N > MAX_ROWS || K < 16 || K % 16 != 0 || K > Q8_MAX_K)
+    return 0;
   return q8_scratch(M, N, K);
 }
 
@@ -168,7 +172,8 @@ twell_status twell_q8_matmul(const int8_t *aq, const float *ascale, const int8_t
                              size_t workspace_bytes, void *stream) {
   twell_status st = check_dtype(dtype);
   if (st != TWELL_OK) return st;
-  if (!aq || !ascale || !wq || !wscale || !y || !status || M < 1 || N < 1 || K < 1 || K > Q8_MAX_K)
+  if (!aq || !ascale || !wq || !wscale || !y || !status || M < 1 || M > MAX_ROWS || N < 1 ||
+      N > MAX_ROWS || K < 1 || K > Q8_MAX_K)
     return TWELL_ERR_ARG;
   if (K % 16 != 0 || !aligned16(aq) || !aligned16(wq) || !aligned16(y) || !aligned4(ascale) ||
       !aligned4(wscale) || !aligned4(bias) || !aligned4(status))
@@ -186,8 +191,8 @@ twell_status twell_q8_matmul(const int8_t *aq, const float *ascale, const int8_t
 static twell_status check_distill(const DistillArgs &a) {
   const twell_status st = check_dtype(a.dtype);
   if (st != TWELL_OK) return st;
-  if (!a.z || !a.ids || !a.teacher || !a.stats || !a.status || a.T < 1 || a.V < 1 ||
-      a.ldz < a.V || a.k < 1 || a.k > DISTILL_MAX_K || !(a.tau >= 1e-4f) || !(a.tau <= 1e4f))
+  if (!a.z || !a.ids || !a.teacher || !a.stats || !a.status || a.T < 1 || a.T > MAX_ROWS ||
+      a.V < 1 || a.V > MAX_ROWS || a.ldz < a.V || a.k < 1 || a.k > DISTILL_MAX_K || !(a.tau >= 1e-4f) || !(a.tau <= 1e4f))
     return TWELL_ERR_ARG;
   if (!aligned16(a.z) || !aligned16(a.dz) || !aligned4(a.ids) || !aligned4(a.teacher) ||
       !aligned4(a.row_weight) || !aligned4(a.loss) || ((uintptr_t)a.stats & 7u) != 0 ||

@@ -17,7 +17,9 @@
  * type `dtype`: TWELL_F32 or TWELL_BF16.  Sums, maxima, statistics and norms
  * are held in fp32 (8-bit products: exact in fp32, see twell_q8_matmul), each
  * output is rounded once (to nearest even), and every result is independent
- * of scheduling: the same call gives the same bits.
+ * of scheduling: the same call gives the same bits.  Numbers of tokens, rows
+ * and output columns are at most 2^30 (element offsets are 64-bit throughout);
+ * sizes beyond what an entry states return TWELL_ERR_ARG.
  */
 #ifndef TWELL_LM_H
 #define TWELL_LM_H
@@ -37,8 +39,8 @@ twell_status twell_read_status(int32_t *status, void *stream);
  * tokens [T]: int32 (token_bytes 4) or int64 (8).  A position whose token is
  * pad_id gives a zero row and takes no gradient (pad_id = -1 pads nothing but
  * -1).  Any other token outside [0, V) is treated the same way and records
- * TWELL_ERR_INDEX.  1 <= T <= 2^30, 1 <= V < 2^31 - 1, D <= 65536;
- * D*elem_size a multiple of 16. */
+ * TWELL_ERR_INDEX.  1 <= T, 1 <= V < 2^31 - 1, D <= 65536; D*elem_size a
+ * multiple of 16. */
 twell_status twell_embed_forward(const void *tokens, int token_bytes, const void *table, int T,
                                  int V, int D, int dtype, float scale, long long pad_id,
                                  void *out, int32_t *status, void *stream);
