@@ -48,7 +48,8 @@ def test_rmsnorm(lib):
     f = lib.twell_add_rmsnorm_forward
     refused(f, good, [
         (0, None, ARG), (0, OFF, ALIGN), (1, OFF, ALIGN), (2, None, ARG), (2, OFF, ALIGN),
-        (3, 0, ARG), (3, (1 << 30) + 1, ARG), (4, 0, ARG), (4, 130, ALIGN), (4, 8192, ARG), (5, 2, DTYPE), (6, -1.0, ARG),
+        (3, 0, ARG), (3, (1 << 30) + 1, ARG), (4, 0, ARG), (4, 130, ALIGN), (4, 8192, ARG),
+        (5, 2, DTYPE), (6, -1.0, ARG),
         (6, float("nan"), ARG), (7, None, ARG), (7, OFF, ALIGN), (8, OFF, ALIGN), (9, OFF, ALIGN),
         (10, None, ARG), (10, ODD, ALIGN), (11, ODD, ALIGN)])
     assert f(A, A, A, 64, 128, 0, 1e-6, A, None, None, A, A, None) == ARG   # no output
@@ -74,7 +75,8 @@ def test_q8(lib):
     refused(lib.twell_q8_matmul, good, [
         (0, None, ARG), (0, OFF, ALIGN), (1, None, ARG), (1, ODD, ALIGN), (2, None, ARG),
         (2, OFF, ALIGN), (3, None, ARG), (3, ODD, ALIGN), (4, ODD, ALIGN), (5, 0, ARG), (6, 0, ARG),
-        (5, (1 << 30) + 1, ARG), (6, (1 << 30) + 1, ARG), (7, 0, ARG), (7, 24, ALIGN), (7, 65552, ARG), (8, 4, DTYPE), (9, None, ARG), (9, OFF, ALIGN),
+        (5, (1 << 30) + 1, ARG), (6, (1 << 30) + 1, ARG), (7, 0, ARG), (7, 24, ALIGN),
+        (7, 65552, ARG), (8, 4, DTYPE), (9, None, ARG), (9, OFF, ALIGN),
         (10, None, ARG), (10, ODD, ALIGN)])
     ws = tw.twell_q8_workspace_size(300, 20, 64)      # many rows: scratch for the widened rows
     assert ws >= 300 * 64 * 2
@@ -88,7 +90,8 @@ def test_distill(lib):
     good = [A, 512, A, A, A, 4, 500, 8, 0, 1.0, A, A, A, A, None]
     refused(lib.twell_distill_forward, good, [
         (0, None, ARG), (0, OFF, ALIGN), (1, 499, ARG), (2, None, ARG), (2, ODD, ALIGN),
-        (3, None, ARG), (4, ODD, ALIGN), (5, 0, ARG), (5, (1 << 30) + 1, ARG), (6, 0, ARG), (7, 0, ARG), (7, 257, ARG),
+        (3, None, ARG), (4, ODD, ALIGN), (5, 0, ARG), (5, (1 << 30) + 1, ARG), (6, 0, ARG),
+        (7, 0, ARG), (7, 257, ARG),
         (8, 7, DTYPE), (9, 0.0, ARG), (9, -1.0, ARG), (9, float("nan"), ARG), (9, float("inf"), ARG),
         (10, None, ARG), (11, None, ARG), (11, A + 4, ALIGN), (12, OFF, ALIGN), (13, None, ARG)])
     back = [A, 512, A, A, A, A, 4, 500, 8, 0, 1.0, A, A, None]
