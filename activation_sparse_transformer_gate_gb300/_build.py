@@ -19,10 +19,12 @@ entry points):
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -42,6 +44,9 @@ VARIANTS = {
     "timeout": ("libtwell_timeout.so", [], ["-DTWELL_WAIT_LIMIT_NS=1ull"]),
 }
 LIB = os.path.join(PKG, VARIANTS[""][0])
+# Python's argument marshalling of the operators around the FFN (csrc/lm_bind.cpp), a CPython
+# extension against torch's headers, beside libtwell.so and linked to it
+BINDING = os.path.join(PKG, "_lm.so")
 
 
 def lib_path(variant: str = "") -> str:
@@ -76,10 +81,26 @@ def _jobs(variant: str):
             for src in SOURCES + extra_src], objdir, os.path.join(PKG, name)
 
 
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("torch not found: its headers are required to build the binding")
+    return list(spec.submodule_search_locations)[0]
+
+
+def _binding_flags(torch_dir: str, nvcc: str):
+    dirs = [os.path.join(torch_dir, "include"),
+            os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+            os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include"),
+            sysconfig.get_paths()["include"]]
+    return [a for d in dirs for a in ("-isystem", d)]
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(), variants=("",)) -> str:
     """Build the requested library variants ("" = libtwell.so); returns the
     path of the first one."""
-    todo = [v for v in variants if force or _stale(lib_path(v))]
+    todo = [v for v in variants
+            if force or _stale(lib_path(v)) or (v == "" and _stale(BINDING))]
     if not todo:
         return lib_path(variants[0])
     nvcc = nvcc_path()
@@ -88,10 +109,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), variants=(
 
     def compile_one(job):
         src, obj, flags = job
-        cmd = [nvcc, "-c", os.path.join(CSRC, src), "-o", obj] + common + flags
+        if src.endswith(".cpp"):
+            cmd = ["g++", "-c", os.path.join(CSRC, src), "-o", obj, "-O2", "-std=c++17", "-fPIC",
+                   "-I", INCLUDE] + flags
+        else:
+            cmd = [nvcc, "-c", os.path.join(CSRC, src), "-o", obj] + common + flags
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{cmd[0]} failed for {src}:\n{r.stdout}\n{r.stderr}")
         if verbose and (r.stdout or r.stderr):
             print(r.stdout + r.stderr, file=sys.stderr)
         return obj
@@ -103,6 +128,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), variants=(
         os.makedirs(objdir, exist_ok=True)
         plans.append((js, lib))
         jobs += js
+    torch_dir = _torch_dir()
+    bind_obj = os.path.join(OBJDIR, "lib", "lm_bind.o")
+    if "" in todo:
+        jobs.insert(0, ("lm_bind.cpp", bind_obj, _binding_flags(torch_dir, nvcc)))
     workers = max(1, min(len(jobs), os.cpu_count() or 8))
     with cf.ThreadPoolExecutor(max_workers=workers) as ex:
         list(ex.map(compile_one, jobs))
@@ -113,6 +142,15 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), variants=(
         if r.returncode != 0:
             raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, lib)
+    if "" in todo:
+        tmp = BINDING + f".tmp{os.getpid()}"
+        libs = os.path.join(torch_dir, "lib")
+        cmd = ["g++", "-shared", "-o", tmp, bind_obj, "-L", PKG, "-l:libtwell.so", "-L", libs,
+               "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, BINDING)
     return lib_path(variants[0])
 
 

@@ -668,7 +668,7 @@ def kernel_source_hash() -> str:
     the operators around the FFN (which no captured kernel is built from)."""
     import re
     around = ("lm_abi.cu", "lm_kernels.h", "vec16.cuh", "embed.cu", "rmsnorm.cu", "distill.cu",
-              "q8.cu")
+              "q8.cu", "lm_bind.cpp")
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "activation_sparse_transformer_gate_gb300", "csrc")
     for f in sorted(os.listdir(csrc)):

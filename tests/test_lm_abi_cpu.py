@@ -104,7 +104,7 @@ def test_read_status(lib):
     assert lib.twell_read_status(None, None) == ARG
 
 
-def test_binding_checks_tensors():
+def test_binding_checks_tensors(lib):
     """Type, size and place of a tensor are checked before the call."""
     cpu = torch.zeros(64, 128)
 
@@ -125,3 +125,11 @@ def test_binding_checks_tensors():
                 fn=tw.twell_embed_forward) == DTYPE
     with pytest.raises(AttributeError):
         tw.no_such_operator
+    # what is neither a tensor, nor a pointer, nor a number raises as such
+    with pytest.raises(TypeError):
+        tw.twell_add_rmsnorm_forward("x", A, *rest, stream=0)
+    with pytest.raises(TypeError):
+        tw.twell_add_rmsnorm_forward(A, A, A, 64, 128, tw.TWELL_F32, "eps", A, A, A, A, A, stream=0)
+    assert code(A, A, A, 1 << 40, 128, tw.TWELL_F32, 1e-6, A, A, A, A, A) == ARG
+    assert code(A, A, A, A, A, 64, 128, tw.TWELL_F32, A, A, torch.zeros(10), 1 << 20,
+                fn=tw.twell_add_rmsnorm_backward) == WS
