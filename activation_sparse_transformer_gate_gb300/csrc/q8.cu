@@ -565,13 +565,16 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
       const uint32_t idesc = make_idesc(S::ROWS, bn, false, false, true);
       const uint64_t ad0 = desc_at(smem_u32(sa16)), wd0 = desc_at(smem_u32(sw16));
       // a k-block's operands: one barrier in a pair, one for a and one for w else
-      auto look = [&](const Ring &a, const Ring &w) {
-        return PAIR ? mbar_test(ready + 8 * w.at, w.phase)
-                    : mbar_test(wfull + 8 * w.at, w.phase) && mbar_test(afull + 8 * a.at, a.phase);
+      auto look = [&](const Ring &a, const Ring &w) -> int {
+        if (PAIR) return mbar_test(ready + 8 * w.at, w.phase);
+        const bool has_w = mbar_test(wfull + 8 * w.at, w.phase);
+        const bool has_a = mbar_test(afull + 8 * a.at, a.phase);  // (not one after the other)
+        return (int)has_w & (int)has_a;
       };
       Ring a(0, AS), w(0, WS);
       int lt = 0;
-      bool ok = true, seen = false;
+      bool ok = true;
+      int seen = 0;
       for (int t = unit; t < tiles && ok; t += units, ++lt) {
         const int buf = lt & 1;
         ok = warp_wait(tempty + 8 * buf, ((uint32_t)(lt >> 1) & 1) ^ 1, abort_flag, p.status);
