@@ -10,7 +10,7 @@
 // registers between the reduction and the output, spread over the fewest
 // warps that keep at most NV 16-byte vectors a lane.  max|y| = rstd max|s w|,
 // so the 8-bit output needs no second reduction.  16384 x 4096 bf16: forward
-// 78 us (6.9 TB/s), with 8 bits out 77, backward 84 (6.4 TB/s).
+// 78 us (6.9 TB/s), with 8 bits out 77, backward 81 (6.6 TB/s).
 #include "common.cuh"
 #include "lm_kernels.h"
 #include "vec16.cuh"
@@ -19,7 +19,8 @@ namespace twell {
 
 namespace {
 
-constexpr int WARPS = 8;  // per CTA
+constexpr int WARPS = 8;       // per CTA
+constexpr int BWD_WARPS = 16;  // of the backward, one CTA an SM
 
 // Sum and (bitwise) maximum over the W warps that share a row.  The maximum
 // of |v| is taken on the bit patterns: their order is the values' order, and
@@ -168,33 +169,48 @@ rmsnorm_forward_kernel(const uint4 *x, const uint4 *res, const float *weight, in
   }
 }
 
-// Backward.  CTAs walk the rows; each thread keeps its columns' weights and
-// its part of dw in registers over all its rows and writes the latter to the
-// workspace at the end (one row of `part` a CTA, the row groups of a CTA
-// added).  BWD_STAGES rows of each thread's operands are on their way through
-// shared memory at any time: 16 warps an SM, all that the registers leave
-// room for, do not keep enough of HBM busy with loads to registers (16384 x
-// 4096 bf16: 100 us so).
-constexpr int BWD_STAGES = 4;
+// Backward.  The row groups (W warps each) of one CTA an SM walk the rows; each
+// thread keeps its columns' weights and its part of dw in registers over all
+// its rows, and the CTA's sum of the latter goes to the workspace at the end.
+// BWD_STAGES rows of each thread's operands are on their way through shared
+// memory at any time: 16 warps an SM, all that the registers leave room for, do
+// not keep enough of HBM busy with loads to registers (16384 x 4096 bf16: 100
+// us so).  A row group meets at a barrier of its own, so that the groups of a
+// CTA drift apart and their reductions hide under each other's copies: two CTAs
+// of 8 warps an SM whose groups share the CTA's barrier take 84 us there and
+// 57 us at 4096 x 8192, these 81 and 48.5.
+constexpr int BWD_STAGES = 4, BWD_NV = 2;
 
-template <int NV>
-constexpr int bwd_ring_bytes() {
-  return BWD_STAGES * 3 * NV * WARPS * 32 * 16;
+constexpr int BWD_RING = BWD_STAGES * 3 * BWD_NV * BWD_WARPS * 32 * 16;  // bytes
+
+// Sum over the W warps of a row group; the group's threads meet at a barrier
+// of their own.
+template <int W>
+__device__ __forceinline__ float sum_group(float sum, float *s_sum) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if (W == 1) return sum;
+  const int warp = threadIdx.x >> 5, w0 = warp / W * W;
+  if ((threadIdx.x & 31) == 0) s_sum[warp] = sum;
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / W), "n"(W * 32) : "memory");
+  sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < W; ++i) sum += s_sum[w0 + i];
+  return sum;
 }
 
-template <typename E, int W, int NV>
-__global__ void __launch_bounds__(WARPS * 32)
+template <typename E, int W>
+__global__ void __launch_bounds__(BWD_WARPS * 32)
 rmsnorm_backward_kernel(const uint4 *s_in, const float *weight, const float *rstd_in,
                         const uint4 *dy, const uint4 *ds, int T, int nv, float inv_d, uint4 *dx,
                         float *part) {
   pdl_begin();
-  constexpr int N = VEC16<E>, THREADS = WARPS * 32;
+  constexpr int N = VEC16<E>, NV = BWD_NV, THREADS = BWD_WARPS * 32, GROUPS = BWD_WARPS / W;
   extern __shared__ uint4 ring[];  // [stage][operand][NV][thread]
-  __shared__ float s_sum[2][WARPS];
-  __shared__ uint32_t s_top[2][WARPS];
+  __shared__ float s_sum[2][BWD_WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int group = (int)blockIdx.x * (WARPS / W) + warp / W;
-  const int groups = (int)gridDim.x * (WARPS / W);
+  const int group = (int)blockIdx.x * GROUPS + warp / W;
+  const int groups = (int)gridDim.x * GROUPS;
   const int v0 = (warp % W) * 32 + lane;
   float dw[NV][N], w[NV][N];
 #pragma unroll
@@ -220,13 +236,8 @@ rmsnorm_backward_kernel(const uint4 *s_in, const float *weight, const float *rst
 #pragma unroll
   for (int st = 0; st < BWD_STAGES; ++st) fetch(group + (long long)st * groups, st);
   float rstd_next = group < T ? rstd_in[group] : 0.f;
-  // every group makes the same number of rounds (the reduction's barrier is
-  // the CTA's)
-  const int rounds = (T + groups - 1) / groups;
-  int st = 0;
-  for (int r = 0; r < rounds; ++r) {
-    const long long t = (long long)r * groups + group;
-    const bool row_ok = t < T;
+  int st = 0, r = 0;
+  for (long long t = group; t < T; t += groups, ++r) {
     const float rstd = rstd_next;
     rstd_next = t + groups < T ? rstd_in[t + groups] : 0.f;
     asm volatile("cp.async.wait_group %0;" ::"n"(BWD_STAGES - 1) : "memory");
@@ -234,7 +245,7 @@ rmsnorm_backward_kernel(const uint4 *s_in, const float *weight, const float *rst
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (!row_ok || v0 + i * W * 32 >= nv) continue;
+      if (v0 + i * W * 32 >= nv) continue;
       a[i] = *slot(st, 0, i);
       b[i] = *slot(st, 1, i);
       c[i] = ds ? *slot(st, 2, i) : make_uint4(0, 0, 0, 0);
@@ -250,13 +261,11 @@ rmsnorm_backward_kernel(const uint4 *s_in, const float *weight, const float *rst
     }
     fetch(t + (long long)BWD_STAGES * groups, st);
     st = st + 1 == BWD_STAGES ? 0 : st + 1;
-    uint32_t none = 0;
-    reduce_row<W>(sum, none, s_sum, s_top, r & 1);
-    const float mean = sum * inv_d;
+    const float mean = sum_group<W>(sum, s_sum[r & 1]) * inv_d;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = v0 + i * W * 32;
-      if (!row_ok || v >= nv) continue;
+      if (v >= nv) continue;
       float f[N], g[N], h[N];
       unpack(a[i], f, (E *)nullptr);
       unpack(b[i], g, (E *)nullptr);
@@ -268,26 +277,27 @@ rmsnorm_backward_kernel(const uint4 *s_in, const float *weight, const float *rst
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   // the CTA's row groups in order, through the ring's memory
-  float *sums = (float *)ring;  // [groups of the CTA][nv * N]
+  float *sums = (float *)ring;  // [GROUPS][nv * N]
   const int D = nv * N;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = v0 + i * W * 32;
     if (v >= nv) break;
-    float *p = WARPS / W > 1 ? sums + (size_t)(warp / W) * D + (size_t)v * N
-                             : part + (size_t)blockIdx.x * D + (size_t)v * N;
+    float *p = sums + (size_t)(warp / W) * D + (size_t)v * N;
 #pragma unroll
     for (int j = 0; j < N; j += 4)
       *(float4 *)(p + j) = make_float4(dw[i][j], dw[i][j + 1], dw[i][j + 2], dw[i][j + 3]);
   }
-  if (WARPS / W == 1) return;
   __syncthreads();
-  for (int d = threadIdx.x; d < D; d += THREADS) {
-    float acc = sums[d];
+  for (int d = threadIdx.x * 4; d < D; d += THREADS * 4) {
+    float4 acc = *(const float4 *)(sums + d);
 #pragma unroll
-    for (int i = 1; i < WARPS / W; ++i) acc += sums[(size_t)i * D + d];
-    part[(size_t)blockIdx.x * D + d] = acc;
+    for (int i = 1; i < GROUPS; ++i) {
+      const float4 p = *(const float4 *)(sums + (size_t)i * D + d);
+      acc.x += p.x; acc.y += p.y; acc.z += p.z; acc.w += p.w;
+    }
+    *(float4 *)(part + (size_t)blockIdx.x * D + d) = acc;
   }
 }
 
@@ -347,20 +357,15 @@ q8_quantize_kernel(const uint4 *a, int nv, int8_t *q, float *scale) {
   }
 }
 
-// Warps a row: the fewest with at most `most` vectors a lane.
-int row_warps(int nv, int most) {
-  int w = 1;
-  while (w < WARPS && nv > w * 32 * most) w *= 2;
-  return w;
-}
+constexpr int FWD_NV = 2;  // vectors a lane before a row takes more warps
 
-constexpr int FWD_NV = 2, BWD_NV = 2;  // vectors a lane before a row takes more warps
-
+// The backward's CTAs: one an SM, fewer where their row groups cover the rows.
 int backward_grid(int T, int nv) {
-  const int per = WARPS / row_warps(nv, BWD_NV);
+  int w = 1;  // warps of a row
+  while (w < BWD_WARPS && nv > w * 32 * BWD_NV) w *= 2;
+  const int per = BWD_WARPS / w;
   const int want = (T + per - 1) / per;
-  const int most = num_sms() * 2;
-  return want < most ? want : most;
+  return want < num_sms() ? want : num_sms();
 }
 
 template <typename E, int W, int NV>
@@ -373,21 +378,22 @@ cudaError_t forward_t(const void *x, const void *residual, const float *weight, 
                   1.f / (float)(nv * VEC16<E>), eps, (uint4 *)s_out, (uint4 *)y, q, qscale, rstd);
 }
 
-template <typename E, int W, int NV>
+template <typename E, int W>
 cudaError_t backward_t(const void *s_in, const float *weight, const float *rstd, const void *dy,
                        const void *ds, int T, int nv, void *dx, float *dweight, float *part,
                        cudaStream_t s) {
   const int grid = backward_grid(T, nv);
-  // (the ring holds the row groups' sums at the end too: WARPS / W rows of
-  // at most W * 32 * NV vectors in fp32)
-  static_assert(bwd_ring_bytes<NV>() >= WARPS * 32 * NV * VEC16<E> * 4, "the sums fit");
+  // (the ring holds the row groups' sums at the end too: BWD_WARPS / W rows of
+  // at most W * 32 * BWD_NV vectors in fp32)
+  static_assert(BWD_RING >= BWD_WARPS * 32 * BWD_NV * VEC16<E> * 4, "the sums fit");
   static const cudaError_t attr =
-      cudaFuncSetAttribute(rmsnorm_backward_kernel<E, W, NV>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, bwd_ring_bytes<NV>());
+      cudaFuncSetAttribute(rmsnorm_backward_kernel<E, W>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, BWD_RING);
   if (attr != cudaSuccess) return attr;
-  cudaError_t e = launch_k(rmsnorm_backward_kernel<E, W, NV>, dim3(grid), dim3(WARPS * 32),
-                           bwd_ring_bytes<NV>(), s, (const uint4 *)s_in, weight, rstd, (const uint4 *)dy, (const uint4 *)ds,
-                           T, nv, 1.f / (float)(nv * VEC16<E>), (uint4 *)dx, part);
+  cudaError_t e = launch_k(rmsnorm_backward_kernel<E, W>, dim3(grid), dim3(BWD_WARPS * 32),
+                           BWD_RING, s, (const uint4 *)s_in, weight, rstd, (const uint4 *)dy,
+                           (const uint4 *)ds, T, nv, 1.f / (float)(nv * VEC16<E>), (uint4 *)dx,
+                           part);
   if (e != cudaSuccess) return e;
   prof_mark(KID_RMSNORM_BWD, s);
   const int D = nv * VEC16<E>;
@@ -397,8 +403,22 @@ cudaError_t backward_t(const void *s_in, const float *weight, const float *rstd,
   return e;
 }
 
-// f<E, W, NV>(args...) for the row's width: at most FWD_NV / BWD_NV vectors a
-// lane up to eight warps, four beyond.
+template <typename E>
+cudaError_t backward_rows(const void *s_in, const float *weight, const float *rstd, const void *dy,
+                          const void *ds, int T, int D, void *dx, float *dweight, float *part,
+                          cudaStream_t s) {
+  const int nv = D / VEC16<E>;
+  auto f = nv <= 64    ? backward_t<E, 1>
+           : nv <= 128 ? backward_t<E, 2>
+           : nv <= 256 ? backward_t<E, 4>
+           : nv <= 512 ? backward_t<E, 8>
+                       : backward_t<E, 16>;
+  static_assert(BWD_NV == 2 && BWD_WARPS == 16, "rows of up to 1024 vectors");
+  return f(s_in, weight, rstd, dy, ds, T, nv, dx, dweight, part, s);
+}
+
+// f<E, W, NV>(args...) for the row's width: at most FWD_NV vectors a lane up to
+// eight warps, four beyond.
 #define TWELL_ROW_DISPATCH(F, E, nv, most, ...)             \
   (nv <= 32 * most      ? F<E, 1, most>(__VA_ARGS__)        \
    : nv <= 64 * most    ? F<E, 2, most>(__VA_ARGS__)        \
@@ -437,14 +457,9 @@ size_t rmsnorm_scratch(int T, int D) {
 cudaError_t launch_add_rmsnorm_backward(const void *s_in, const float *weight, const float *rstd,
                                         const void *dy, const void *ds, int T, int D, int dtype,
                                         void *dx, float *dweight, float *part, cudaStream_t s) {
-  if (dtype == TWELL_BF16) {
-    const int nv = D / VEC16<bf16>;
-    return TWELL_ROW_DISPATCH(backward_t, bf16, nv, BWD_NV, s_in, weight, rstd, dy, ds, T, nv, dx,
-                              dweight, part, s);
-  }
-  const int nv = D / VEC16<float>;
-  return TWELL_ROW_DISPATCH(backward_t, float, nv, BWD_NV, s_in, weight, rstd, dy, ds, T, nv, dx,
-                            dweight, part, s);
+  return dtype == TWELL_BF16
+             ? backward_rows<bf16>(s_in, weight, rstd, dy, ds, T, D, dx, dweight, part, s)
+             : backward_rows<float>(s_in, weight, rstd, dy, ds, T, D, dx, dweight, part, s);
 }
 
 cudaError_t launch_q8_quantize(const void *a, int rows, int cols, int dtype, int8_t *q,
