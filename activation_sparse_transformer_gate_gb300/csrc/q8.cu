@@ -402,8 +402,10 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, status));
 }
 
-// After an abort no copy may be in flight when the CTA exits: waits (bounded)
-// for the last load that was issued into each stage of a ring.
+// No copy may be in flight when the CTA exits: waits (bounded) for the last
+// load that was issued into each stage of a ring.  That the issuing warp has
+// come to its end does not say that the loads were waited for: another role may
+// have given up since.
 __device__ __forceinline__ void drain_ring(uint32_t full, int S, long issued) {
   for (int s = 0; s < S && s < issued; ++s) {
     const uint32_t par = (uint32_t)(((issued - 1 - s) / S) & 1);
@@ -543,7 +545,7 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
         }
       }
     }
-    if (!ok) drain_ring(full, stages, issued);
+    drain_ring(full, stages, issued);
   } else if (warp == 7) {
     // ------------- tells the leader that this CTA's operands have arrived --
     if (PAIR && lane == 0) {
@@ -645,8 +647,11 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
     const int vecs = half * (BK / 16);
     Ring w(group, WS), r(group, RS);
     for (long it = group; it < its; it += GROUPS) {
-      if (!warp_wait(rfull + 8 * r.at, r.phase, abort_flag, p.status)) break;
+      // w's stage first: when it is free, the k-blocks up to it - GROUPS have been
+      // multiplied, so the 8-bit stage's last load before this one (it - RS, of
+      // another group) has been seen and the phase's parity means this one
       if (!warp_wait(wempty + 8 * w.at, w.phase ^ 1, abort_flag, p.status)) break;
+      if (!warp_wait(rfull + 8 * r.at, r.phase, abort_flag, p.status)) break;
       widen_rows<32 * S::GROUP>(raw + r.at * S::RAW, sw16 + w.at * S::TILE, ct, vecs);
       fence_async_proxy();  // the MMA reads through the async proxy
       __syncwarp();

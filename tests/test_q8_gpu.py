@@ -147,6 +147,15 @@ def test_other_stream_and_graph():
         assert torch.equal(y, want)
 
 
+@pytest.mark.parametrize("M,N,K", [(128, 50000, 4096), (40, 30001, 4112), (100, 20000, 8192),
+                                   (300, 40001, 4096), (700, 9000, 8208)])
+def test_many_tiles(M, N, K):
+    """Several tiles a CTA or pair, every ring of stages used many times over."""
+    a, w, sa, sw, _ = inputs(M, N, K, M + N + K)
+    for _ in range(3):
+        verify(a, w, sa, sw, None, "bf16")
+
+
 TIMEOUT_CHILD = """
 import sys
 import torch
