@@ -541,15 +541,15 @@ tc_gemm_kernel(const __grid_constant__ TcMaps maps, TcParams p) {
           }
         }
       }
-      // Drain after an abort: wait (bounded) until the last load issued into
-      // each stage has landed, so no copy is in flight when the CTA exits.
-      if (!ok) {
-        for (int s = 0; s < S && s < issued; ++s) {
-          const long last = s + (long)S * ((issued - 1 - s) / S);
-          const uint32_t par = (uint32_t)((last / S) & 1);
-          const uint64_t t0 = global_timer();
-          while (!mbar_try(full0 + 8 * s, par) && global_timer() - t0 < DRAIN_LIMIT_NS) {
-          }
+      // Drain: wait (bounded) until the last load issued into each stage has
+      // landed, so that no copy is in flight when the CTA exits.  (Also where
+      // this warp came to its end: another role may have given up since, with
+      // the last loads still on their way.)
+      for (int s = 0; s < S && s < issued; ++s) {
+        const long last = s + (long)S * ((issued - 1 - s) / S);
+        const uint32_t par = (uint32_t)((last / S) & 1);
+        const uint64_t t0 = global_timer();
+        while (!mbar_try(full0 + 8 * s, par) && global_timer() - t0 < DRAIN_LIMIT_NS) {
         }
       }
     }
