@@ -10,11 +10,12 @@
 //   a decoded row or four   q8_rows_kernel: dp4a, exact int32 sums
 //   a batch of them         q8_frag_kernel: the weights are widened in
 //                           registers and used up there (m16n8k16)
-//   more                    q8_mma_kernel: TMA brings 8-bit weights, warps
-//                           widen them into the layout of tcgen05.mma, one
-//                           lane issues, four warps read TMEM; up to 128 rows
-//                           a CTA a tile, above that a pair of CTAs
-// The first two are bound by the weights' bytes, the pairs by the tensor
+//   up to 128               q8_few_kernel: TMA brings 8-bit weights, warps
+//                           widen them into TMEM, where they are the M side
+//                           of tcgen05.mma; clusters share k
+//   more                    q8_mma_kernel: warps widen the weights into shared
+//                           memory, pairs of CTAs (cta_group::2) multiply
+// The first three are bound by the weights' bytes, the pairs by the tensor
 // cores: 8192 x 14336 x 4096 in 0.57 ms, 1.7 PFLOP/s with the launch that
 // widens a.
 #include <cuda_fp16.h>
@@ -215,17 +216,14 @@ constexpr int ACC_COLS = 256;  // TMEM columns of one accumulator
 constexpr int EPI_PITCH = 33;  // 32-bit words of an epilogue staging row
 constexpr int GROUPS = 4;      // conversion groups, which take the k-blocks in turn
 
-// One CTA, or a pair of CTAs, per tile: rows of a, stages of a (fp16), of w in
-// fp16 and in 8 bits, warps of a conversion group.  Stages hold 128 rows.
-template <bool PAIR>
-struct Shape {
-  static constexpr int ROWS = PAIR ? 2 * BM : BM;
-  static constexpr int AS = PAIR ? 5 : 4, WS = 4, RS = PAIR ? 6 : 8;
-  static constexpr int GROUP = PAIR ? 2 : 4;
-  static constexpr int THREADS = 32 * (8 + GROUPS * GROUP);
-  static constexpr int TILE = BM * BK * 2, RAW = BM * BK;  // bytes of a stage
-  static constexpr int SMEM = 1024 + (AS + WS) * TILE + RS * RAW + 4 * 32 * EPI_PITCH * 4 + 2 * 256 * 4;
-};
+// A pair of CTAs per tile: rows of a; stages of a (fp16), of w in fp16 and in 8
+// bits, with 128 rows each; warps of a conversion group.
+constexpr int ROWS = 2 * BM;
+constexpr int AS = 5, WS = 4, RS = 6;
+constexpr int GROUP = 2;
+constexpr int THREADS = 32 * (8 + GROUPS * GROUP);
+constexpr int TILE = BM * BK * 2, RAW = BM * BK;  // bytes of a stage
+constexpr int SMEM = 1024 + (AS + WS) * TILE + RS * RAW + 4 * 32 * EPI_PITCH * 4 + 2 * 256 * 4;
 
 struct Q8Maps {
   CUtensorMap a, w;
@@ -234,7 +232,6 @@ struct Q8Maps {
 struct Q8Params {
   int M, N, K;
   int bn;   // output columns of a tile
-  int box;  // rows of a that a TMA box holds
   const float *sa, *sw, *bias;
   void *y;
   int32_t *status;
@@ -419,22 +416,23 @@ __device__ __forceinline__ void drain_ring(uint32_t full, int S, long issued) {
 // the low word moves the start, 16 bytes a unit.
 __device__ __forceinline__ uint64_t desc_at(uint32_t saddr) { return sw128_desc(saddr, 16, 1024); }
 
+// ---- more than 128 rows of a ---------------------------------------------------
 // a is widened once by q8_widen_kernel and comes by TMA as fp16; w comes by
 // TMA in 8 bits and is widened here, between two stages of shared memory.
 //
-// Above 128 rows of a, two CTAs (one cluster) share a 256 x bn tile: each holds
-// 128 rows of a and bn / 2 rows of w, the leader issues cta_group::2 MMAs over
-// both, and each CTA stores its 128 rows.  Per k-block an SM then moves 64 KB
-// through shared memory (w in 8 bits twice and in fp16 once, a once, the MMA's
-// reads) where one CTA that widened both operands for its own 128 x 256 tile
-// would move 144 KB for the same multiplications, and shared memory, not the
-// tensor cores, was its bound (770 TFLOP/s at M 8192, N 14336, K 4096; pairs:
-// 1.7 PFLOP/s).
+// Two CTAs (one cluster) share a 256 x bn tile: each holds 128 rows of a and bn
+// / 2 rows of w, the leader issues cta_group::2 MMAs over both, and each CTA
+// stores its 128 rows.  Per k-block an SM then moves 64 KB through shared memory
+// (w in 8 bits twice and in fp16 once, a once, the MMA's reads) where one CTA
+// that widened both operands for its own 128 x 256 tile would move 144 KB for
+// the same multiplications, and shared memory, not the tensor cores, was its
+// bound (770 TFLOP/s at M 8192, N 14336, K 4096; pairs: 1.7 PFLOP/s).
 //
 // A conversion warp's loads, stores, their fence and its arrival take about
 // 2000 cycles from end to end, four times a k-block's MMAs, so four groups of
 // warps take the k-blocks in turn.  They arrive at a barrier of their own CTA
-// and, in a pair, one thread passes that on to the leader.
+// and one thread passes that on to the leader.
+
 // fp16 copy of a.
 __global__ void __launch_bounds__(256)
 q8_widen_kernel(const uint4 *a, size_t vecs, uint4 *out) {
@@ -448,70 +446,64 @@ q8_widen_kernel(const uint4 *a, size_t vecs, uint4 *out) {
   out[2 * i + 1] = hi;
 }
 
-template <typename E, bool PAIR>
-__global__ void __launch_bounds__(Shape<PAIR>::THREADS, 1)
+template <typename E>
+__global__ void __launch_bounds__(THREADS, 1)
 q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Params p) {
   // (everything but the fp16 rows of a was complete before q8_widen_kernel:
   // only their producer waits for it)
-  using S = Shape<PAIR>;
-  constexpr int AS = S::AS, WS = S::WS, RS = S::RS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t *sa16 = smem, *sw16 = sa16 + AS * S::TILE, *raw = sw16 + WS * S::TILE;
-  float *s_epi = (float *)(raw + RS * S::RAW);
+  uint8_t *sa16 = smem, *sw16 = sa16 + AS * TILE, *raw = sw16 + WS * TILE;
+  float *s_epi = (float *)(raw + RS * RAW);
   float *s_sw = s_epi + 4 * 32 * EPI_PITCH;
-  // Barriers of this CTA: a stage is full, a stage is free again.  In a pair,
-  // barriers of the leader, at which both CTAs arrive: a k-block's operands
-  // are ready, an accumulator has been read (tempty).
+  // Barriers of this CTA: a stage is full, a stage is free again.  Barriers of
+  // the leader, at which both CTAs arrive: a k-block's operands are ready, an
+  // accumulator has been read (tempty).
   __shared__ uint64_t bars[2 * AS + 3 * WS + 2 * RS + 5];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   volatile int *abort_flag = &s_abort;
-  // (where both rings have as many stages, one barrier frees a stage of each)
-  constexpr bool JOINT = AS == WS;
-  const uint32_t afull = smem_u32(bars);
-  const uint32_t wfull = afull + 8 * 2 * AS, wempty = wfull + 8 * WS, ready = wempty + 8 * WS;
-  const uint32_t aempty = JOINT ? wempty : afull + 8 * AS;
+  const uint32_t afull = smem_u32(bars), aempty = afull + 8 * AS;
+  const uint32_t wfull = aempty + 8 * AS, wempty = wfull + 8 * WS, ready = wempty + 8 * WS;
   const uint32_t rfull = ready + 8 * WS, rempty = rfull + 8 * RS;
   const uint32_t tfull = rempty + 8 * RS, tempty = tfull + 16, mma_done = tempty + 16;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;  // (a pair's CTAs are consecutive)
-  const int bn = p.bn, half = PAIR ? bn / 2 : bn;      // columns of the tile; rows of w here
+  const int rank = (int)(blockIdx.x & 1);  // (a pair's CTAs are consecutive)
+  const int bn = p.bn, half = bn / 2;      // columns of the tile; rows of w here
 
-  const int mb = (p.M + S::ROWS - 1) / S::ROWS, nb = (p.N + bn - 1) / bn;
+  const int mb = (p.M + ROWS - 1) / ROWS, nb = (p.N + bn - 1) / bn;
   const int tiles = mb * nb;  // M-blocks innermost: the tiles in flight share few weight tiles
   const int KT = (p.K + BK - 1) / BK;
-  // this CTA's or pair's tiles: unit, unit + units, ...; their k-blocks
-  const int unit = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
-  const int units = PAIR ? (int)gridDim.x >> 1 : (int)gridDim.x;
+  // this pair's tiles: unit, unit + units, ...; their k-blocks
+  const int unit = (int)blockIdx.x >> 1, units = (int)gridDim.x >> 1;
   const long its = (long)((tiles - unit + units - 1) / units) * KT;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < AS; ++i) {
       mbar_init(afull + 8 * i, 1);
-      if (!JOINT) mbar_init(aempty + 8 * i, 1);
+      mbar_init(aempty + 8 * i, 1);
     }
     for (int i = 0; i < WS; ++i) {
-      mbar_init(wfull + 8 * i, S::GROUP);
+      mbar_init(wfull + 8 * i, GROUP);
       mbar_init(wempty + 8 * i, 1);
       mbar_init(ready + 8 * i, 2);
     }
     for (int i = 0; i < RS; ++i) {
       mbar_init(rfull + 8 * i, 1);
-      mbar_init(rempty + 8 * i, S::GROUP);
+      mbar_init(rempty + 8 * i, GROUP);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(tfull + 8 * i, 1);
-      mbar_init(tempty + 8 * i, PAIR ? 8 : 4);
+      mbar_init(tempty + 8 * i, 8);
     }
     mbar_init(mma_done, 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) tmem_alloc<PAIR>(smem_u32(&s_tmem), 2 * ACC_COLS);
+  if (warp == 1) tmem_alloc<true>(smem_u32(&s_tmem), 2 * ACC_COLS);
   tc_fence_before();
   __syncthreads();
-  if (PAIR) cluster_sync_all();
+  cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
 
@@ -521,15 +513,15 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
     const bool is_w = warp == 0;
     if (!is_w) pdl_begin();
     const uint32_t full = is_w ? rfull : afull, empty = is_w ? rempty : aempty;
-    const uint32_t dst0 = smem_u32(is_w ? raw : sa16), step = is_w ? S::RAW : S::TILE;
-    const int stages = is_w ? RS : AS, bytes = is_w ? half * BK : p.box * BK * 2;
+    const uint32_t dst0 = smem_u32(is_w ? raw : sa16), step = is_w ? RAW : TILE;
+    const int stages = is_w ? RS : AS, bytes = is_w ? half * BK : BM * BK * 2;
     const CUtensorMap *map = is_w ? &maps.w : &maps.a;
     int st = 0;
     uint32_t ph = 0;
     long issued = 0;
     bool ok = true;
     for (int t = unit; t < tiles && ok; t += units) {
-      const int row = is_w ? (t / mb) * bn + rank * half : (t % mb) * S::ROWS + rank * BM;
+      const int row = is_w ? (t / mb) * bn + rank * half : (t % mb) * ROWS + rank * BM;
       for (int kt = 0; kt < KT; ++kt) {
         ok = warp_wait(empty + 8 * st, ph ^ 1, abort_flag, p.status);
         if (!ok) break;
@@ -548,7 +540,7 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
     drain_ring(full, stages, issued);
   } else if (warp == 7) {
     // ------------- tells the leader that this CTA's operands have arrived --
-    if (PAIR && lane == 0) {
+    if (lane == 0) {
       const uint32_t to = cluster_addr(ready, 0);
       Ring a(0, AS), w(0, WS);
       for (long it = 0; it < its; ++it) {
@@ -564,15 +556,8 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
     // --------------------------------------------------------- MMA issuer --
     if (rank == 0) {
       const bool issues = elect_one();
-      const uint32_t idesc = make_idesc(S::ROWS, bn, false, false, true);
+      const uint32_t idesc = make_idesc(ROWS, bn, false, false, true);
       const uint64_t ad0 = desc_at(smem_u32(sa16)), wd0 = desc_at(smem_u32(sw16));
-      // a k-block's operands: one barrier in a pair, one for a and one for w else
-      auto look = [&](const Ring &a, const Ring &w) -> int {
-        if (PAIR) return mbar_test(ready + 8 * w.at, w.phase);
-        const bool has_w = mbar_test(wfull + 8 * w.at, w.phase);
-        const bool has_a = mbar_test(afull + 8 * a.at, a.phase);  // (not one after the other)
-        return (int)has_w & (int)has_a;
-      };
       Ring a(0, AS), w(0, WS);
       int lt = 0;
       bool ok = true;
@@ -585,33 +570,31 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
         const uint32_t acc = tmem + (uint32_t)(buf * ACC_COLS);
         for (int kt = 0; kt < KT; ++kt) {
           if (!__all_sync(0xFFFFFFFFu, seen)) {
-            ok = PAIR ? warp_wait(ready + 8 * w.at, w.phase, abort_flag, p.status)
-                      : warp_wait(wfull + 8 * w.at, w.phase, abort_flag, p.status) &&
-                            warp_wait(afull + 8 * a.at, a.phase, abort_flag, p.status);
+            ok = warp_wait(ready + 8 * w.at, w.phase, abort_flag, p.status);
             if (!ok) break;
           }
           tc_fence_after();
-          const uint64_t ad = ad0 + (uint32_t)(a.at * (S::TILE >> 4));
-          const uint64_t wd = wd0 + (uint32_t)(w.at * (S::TILE >> 4));
+          const uint64_t ad = ad0 + (uint32_t)(a.at * (TILE >> 4));
+          const uint64_t wd = wd0 + (uint32_t)(w.at * (TILE >> 4));
           const uint32_t a_free = aempty + 8 * a.at, w_free = wempty + 8 * w.at;
           a.next(AS);
           w.next(WS);
-          seen = look(a, w);  // of the next k-block, under this one's issue
+          seen = mbar_test(ready + 8 * w.at, w.phase);  // of the next one, under this one's issue
           if (issues) {
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk)
-              mma_f16<PAIR>(acc, ad + 2 * kk, wd + 2 * kk, idesc, (kt > 0 || kk > 0) ? 1u : 0u);
-            if (!JOINT) mma_commit_to<PAIR>(a_free);
-            mma_commit_to<PAIR>(w_free);
+              mma_f16<true>(acc, ad + 2 * kk, wd + 2 * kk, idesc, (kt > 0 || kk > 0) ? 1u : 0u);
+            mma_commit_to<true>(a_free);
+            mma_commit_to<true>(w_free);
           }
           __syncwarp();
         }
         if (!ok) break;
-        if (issues) mma_commit_to<PAIR>(tfull + 8 * buf);
+        if (issues) mma_commit_to<true>(tfull + 8 * buf);
         __syncwarp();
       }
       // all MMAs issued by this thread are complete before TMEM is freed
-      if (issues) mma_commit_to<PAIR>(mma_done);
+      if (issues) mma_commit_to<true>(mma_done);
       const uint64_t t0 = global_timer();
       while (!mbar_try(mma_done, 0) && global_timer() - t0 < DRAIN_LIMIT_NS) {
       }
@@ -620,10 +603,10 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
     // ------------------------------------------------------------ epilogue --
     const int q = warp & 3;  // TMEM lane quadrant of this warp
     float *stage = s_epi + q * 32 * EPI_PITCH;
-    const uint32_t free = PAIR ? cluster_addr(tempty, 0) : tempty;
+    const uint32_t free = cluster_addr(tempty, 0);
     int lt = 0;
     for (int t = unit; t < tiles; t += units, ++lt) {
-      const int m0 = (t % mb) * S::ROWS + rank * BM + q * 32, n0 = (t / mb) * bn;
+      const int m0 = (t % mb) * ROWS + rank * BM + q * 32, n0 = (t / mb) * bn;
       const int buf = lt & 1;
       stage_columns(p, n0, s_sw, threadIdx.x - 64);
       const float sa = m0 + lane < p.M ? p.sa[m0 + lane] : 0.f;
@@ -636,14 +619,11 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
                    n0, sa, s_sw, stage);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        if (PAIR) mbar_arrive_cluster(free + 8 * buf);
-        else mbar_arrive(free + 8 * buf);
-      }
+      if (lane == 0) mbar_arrive_cluster(free + 8 * buf);
     }
   } else {
     // ---------------------------------------------------------- conversion --
-    const int group = (warp - 8) / S::GROUP, ct = (threadIdx.x - 256) % (32 * S::GROUP);
+    const int group = (warp - 8) / GROUP, ct = (threadIdx.x - 256) % (32 * GROUP);
     const int vecs = half * (BK / 16);
     Ring w(group, WS), r(group, RS);
     for (long it = group; it < its; it += GROUPS) {
@@ -652,7 +632,7 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
       // another group) has been seen and the phase's parity means this one
       if (!warp_wait(wempty + 8 * w.at, w.phase ^ 1, abort_flag, p.status)) break;
       if (!warp_wait(rfull + 8 * r.at, r.phase, abort_flag, p.status)) break;
-      widen_rows<32 * S::GROUP>(raw + r.at * S::RAW, sw16 + w.at * S::TILE, ct, vecs);
+      widen_rows<32 * GROUP>(raw + r.at * RAW, sw16 + w.at * TILE, ct, vecs);
       fence_async_proxy();  // the MMA reads through the async proxy
       __syncwarp();
       if (lane == 0) {
@@ -668,38 +648,430 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
   // or TMEM
   tc_fence_before();
   __syncthreads();
-  if (PAIR) cluster_sync_all();
+  cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
-    tmem_free<PAIR>(tmem, 2 * ACC_COLS);
+    tmem_free<true>(tmem, 2 * ACC_COLS);
   }
 }
 
-// [rows][K] matrix of 8-bit or (f16) 16-bit elements, boxes of 64 columns and
-// `box` rows; 16-bit boxes 128B-swizzled, as the MMA reads them.
-bool make_map(CUtensorMap *m, const void *base, int rows, int K, int box, bool f16) {
+// ---- up to 128 rows of a ------------------------------------------------------
+// The product is turned round: 128 rows of w are the M side of tcgen05.mma and
+// the rows of a its N side, so an MMA is as wide as there are rows.  w is read
+// from TMEM, into which the conversion warps write it as they widen it: in
+// shared memory it is only ever in 8 bits.  With w widened there too, and 128
+// rows of a read for however few there are, a k-block of 64 for 96 columns moved
+// 57 KB through shared memory, which at its 128 bytes a cycle took the 420 cycles
+// that were measured (37 x 14336 x 4096: 20.2 us); here 128 k of 128 columns move
+// 52 KB and take 620 (16.0 us).
+//
+// A tile is 128 columns of y.  Where the tiles leave SMs idle, a cluster of ks
+// CTAs shares a tile's k and adds the parts through distributed shared memory,
+// each CTA for its share of the rows of a (37 x 8192 x 2048: 11.4 us).
+//
+// What is left above the weights' bytes: the launch of q8_widen_kernel, about
+// 9000 cycles from the first load to the first MMA (all SMs fill their rings at
+// once), 2100 of the epilogue, and 112 of 152 SMs at N = 14336.  The epilogue's
+// stores count by their number: 32 of 64 bytes a warp took 4200 cycles for 37
+// rows, the same bytes in stores of 16 a lane 2100.
+constexpr int FEW_MOST = 128;              // rows of a
+constexpr int FN = 128, FK = 128;          // columns of y a tile, k of a k-block
+constexpr int FEW_STAGES = 6;              // of w in TMEM and of a in shared memory: the most
+constexpr int FEW_RAW = 12;                // of w in 8 bits: the most
+constexpr int FEW_RINGS = 4 * FEW_MOST * FK * 2 + 6 * FN * FK;
+constexpr int FEW_SMEM = 1024 + FEW_RINGS;
+constexpr int FEW_THREADS = 32 * (8 + 4 * GROUPS);
+constexpr int FEW_KS = 8;                  // CTAs that share a tile: the most
+
+struct FewParams {
+  int M, N, K;
+  int box;         // rows of a that a TMA box holds
+  int ks;          // CTAs that share a tile
+  int cols;        // rows of a in MMAs: TMEM columns of an accumulator
+  int stages, raw_stages;
+  const float *sa, *sw, *bias;
+  void *y;
+  int32_t *status;
+};
+
+// 32 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+// The MMA with its first operand in TMEM.
+__device__ __forceinline__ void mma_tmem(uint32_t dtmem, uint32_t atmem, uint64_t bdesc,
+                                         uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(dtmem),
+      "r"(atmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// 32 rows of y from row m0 on; this lane holds column n of them (of `rows` rows
+// where the column exists).
+__device__ __forceinline__ void store_columns(const FewParams &p, float *y, int n, int m0,
+                                              int rows, const float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (m0 + i < rows) y[(size_t)(m0 + i) * p.N] = v[i];
+}
+__device__ __forceinline__ void store_columns(const FewParams &p, bf16 *y, int n, int m0, int rows,
+                                              const float (&v)[32]) {
+  if (p.N % 8 != 0) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (m0 + i < rows) y[(size_t)(m0 + i) * p.N] = __float2bfloat16_rn(v[i]);
+    return;
+  }
+  // 8 x 8 blocks change places between eight lanes, which then hold eight
+  // columns of one row each
+  const int lane = threadIdx.x & 31;
+  const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
+  uint32_t h[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t own = pack_bf2(v[2 * i], v[2 * i + 1]);
+    const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
+    h[i] = b0 ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+  }
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    const uint32_t keep = b1 ? h[i + 1] : h[i];
+    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, b1 ? h[i] : h[i + 1], 2);
+    h[i] = b1 ? got : keep;
+    h[i + 1] = b1 ? keep : got;
+  }
+  const int m = m0 + (lane & 7), c = n - lane + (lane >> 3) * 8;
+  bf16 *row = (bf16 *)p.y + (size_t)m * p.N + c;
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    uint32_t keep[2], got[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      keep[j] = b2 ? h[i + 2 + j] : h[i + j];
+      got[j] = __shfl_xor_sync(0xFFFFFFFFu, b2 ? h[i + j] : h[i + 2 + j], 4);
+    }
+    if (m + 2 * i < p.M && c < p.N)
+      *(uint4 *)(row + (size_t)(2 * i) * p.N) =
+          b2 ? make_uint4(got[0], got[1], keep[0], keep[1])
+             : make_uint4(keep[0], keep[1], got[0], got[1]);
+  }
+}
+
+template <typename E>
+__global__ void __launch_bounds__(FEW_THREADS, 1)
+q8_few_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ FewParams p) {
+  // (everything but the fp16 rows of a was complete before q8_widen_kernel:
+  // only their producer waits for it)
+  constexpr int RAW = FN * FK;           // bytes of a stage of w in 8 bits
+  const int WS = p.stages, RS = p.raw_stages;
+  const int half = p.box * 128, a_step = 2 * half;  // bytes: 64 k of a's rows; a stage
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t *raw = smem + WS * a_step;  // (behind a: an MMA may read past a stage's rows)
+  __shared__ uint64_t bars[3 * FEW_STAGES + 2 * FEW_RAW + 5];
+  __shared__ __align__(16) float s_sa[FEW_MOST];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  volatile int *abort_flag = &s_abort;
+  const uint32_t afull = smem_u32(bars), wfull = afull + 8 * FEW_STAGES;
+  const uint32_t empty = wfull + 8 * FEW_STAGES;  // frees a stage of a and one of w
+  const uint32_t rfull = empty + 8 * FEW_STAGES, rempty = rfull + 8 * FEW_RAW;
+  const uint32_t tfull = rempty + 8 * FEW_RAW, tempty = tfull + 16, mma_done = tempty + 16;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int tiles = (p.N + FN - 1) / FN, KT = (p.K + FK - 1) / FK;
+  // this CTA's tiles: unit, unit + units, ... (one where a tile is shared);
+  // its k-blocks of each: [k0, k1)
+  const int rank = (int)blockIdx.x % p.ks, unit = (int)blockIdx.x / p.ks;
+  const int units = (int)gridDim.x / p.ks;
+  const int k0 = (int)((long)KT * rank / p.ks), k1 = (int)((long)KT * (rank + 1) / p.ks);
+
+  const int early = min(RS, k1 - k0);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < WS; ++i) {
+      mbar_init(afull + 8 * i, 1);
+      mbar_init(wfull + 8 * i, 4);
+      mbar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < RS; ++i) {
+      mbar_init(rfull + 8 * i, 1);
+      mbar_init(rempty + 8 * i, 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(tfull + 8 * i, 1);
+      mbar_init(tempty + 8 * i, 4);
+    }
+    mbar_init(mma_done, 1);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    // the first tile's w under way before the others are ready
+    for (int i = 0; i < early; ++i) {
+      mbar_expect_tx(rfull + 8 * i, RAW);
+      tma_load_2d(smem_u32(raw) + i * RAW, &maps.w, (k0 + i) * FK, unit * FN, rfull + 8 * i);
+    }
+  }
+  if (warp == 1) tmem_alloc<false>(smem_u32(&s_tmem), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem, w16 = tmem + 2 * p.cols;  // two accumulators; the stages of w
+
+  if (warp == 0 || warp == 6) {
+    // ------------------------------- TMA producers: w in 8 bits; a in fp16 --
+    const bool issues = elect_one();
+    const bool is_w = warp == 0;
+    if (!is_w) pdl_begin();
+    const uint32_t full = is_w ? rfull : afull, free = is_w ? rempty : empty;
+    const uint32_t dst0 = smem_u32(is_w ? raw : smem), step = is_w ? RAW : a_step;
+    const int stages = is_w ? RS : WS;
+    const int first = is_w ? early : 0;  // (loads that are on their way)
+    Ring r(first, stages);
+    long issued = first;
+    bool ok = true;
+    for (int t = unit; t < tiles && ok; t += units) {
+      for (int kt = t == unit ? k0 + first : k0; kt < k1; ++kt) {
+        ok = warp_wait(free + 8 * r.at, r.phase ^ 1, abort_flag, p.status);
+        if (!ok) break;
+        if (issues) {
+          const uint32_t bar = full + 8 * r.at, dst = dst0 + r.at * step;
+          mbar_expect_tx(bar, step);
+          if (is_w) {
+            tma_load_2d(dst, &maps.w, kt * FK, t * FN, bar);
+          } else {
+            tma_load_2d(dst, &maps.a, kt * FK, 0, bar);
+            tma_load_2d(dst + half, &maps.a, kt * FK + 64, 0, bar);
+          }
+        }
+        __syncwarp();
+        ++issued;
+        r.next(stages);
+      }
+    }
+    drain_ring(full, stages, issued);
+  } else if (warp == 1) {
+    // --------------------------------------------------------- MMA issuer --
+    const bool issues = elect_one();
+    const uint32_t idesc = make_idesc(FN, p.cols, false, false, true);
+    const uint64_t ad0 = desc_at(smem_u32(smem));
+    auto look = [&](const Ring &w) -> int {  // (not one after the other)
+      const bool has_w = mbar_test(wfull + 8 * w.at, w.phase);
+      const bool has_a = mbar_test(afull + 8 * w.at, w.phase);
+      return (int)has_w & (int)has_a;
+    };
+    Ring w(0, WS);
+    int lt = 0, seen = 0;
+    bool ok = true;
+    for (int t = unit; t < tiles && ok; t += units, ++lt) {
+      const int buf = lt & 1;
+      ok = warp_wait(tempty + 8 * buf, ((uint32_t)(lt >> 1) & 1) ^ 1, abort_flag, p.status);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + (uint32_t)(buf * p.cols);
+      for (int kt = k0; kt < k1; ++kt) {
+        if (!__all_sync(0xFFFFFFFFu, seen)) {
+          ok = warp_wait(wfull + 8 * w.at, w.phase, abort_flag, p.status) &&
+               warp_wait(afull + 8 * w.at, w.phase, abort_flag, p.status);
+          if (!ok) break;
+        }
+        tc_fence_after();
+        const uint32_t wt = w16 + (uint32_t)(w.at * (FK / 2));
+        const uint64_t ad = ad0 + (uint32_t)(w.at * (a_step >> 4));
+        const uint32_t done = empty + 8 * w.at;
+        w.next(WS);
+        seen = look(w);  // of the next k-block, under this one's issue
+        __syncwarp();
+        if (issues) {
+#pragma unroll
+          for (int kk = 0; kk < FK / 16; ++kk)
+            mma_tmem(acc, wt + 8 * kk, ad + (uint32_t)((kk >> 2) * (half >> 4) + 2 * (kk & 3)),
+                     idesc, (kt > k0 || kk > 0) ? 1u : 0u);
+          mma_commit(done);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (issues) mma_commit(tfull + 8 * buf);
+      __syncwarp();
+    }
+    // all MMAs issued by this thread are complete before TMEM is freed
+    if (issues) mma_commit(mma_done);
+    __syncwarp();
+    const uint64_t t0 = global_timer();
+    while (!mbar_try(mma_done, 0) && global_timer() - t0 < DRAIN_LIMIT_NS) {
+    }
+  } else if (warp < 6) {
+    // ------------------------ epilogue: a lane is a column of y, n0 + lane --
+    const int q = warp & 3;  // TMEM lane quadrant of this warp
+    float *part = (float *)smem + q * 32 + lane;  // [row of a][FN]; the rings are done with
+    const int e = q * 32 + lane;
+    s_sa[e] = e < p.M ? p.sa[e] : 0.f;
+    epi_bar();
+    int lt = 0;
+    for (int t = unit; t < tiles; t += units, ++lt) {
+      const int n = t * FN + q * 32 + lane, buf = lt & 1;
+      const float sw = n < p.N ? p.sw[n] : 0.f, bias = p.bias && n < p.N ? p.bias[n] : 0.f;
+      const bool ok = epi_all(mbar_wait(tfull + 8 * buf, (uint32_t)(lt >> 1) & 1, abort_flag,
+                                        p.status));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * p.cols);
+      E *y = (E *)p.y + n;
+      const int rows = n < p.N ? p.M : 0;
+      for (int m0 = 0; m0 < p.M; m0 += 32) {
+        float v[32];
+        __syncwarp();  // (tcgen05.ld takes the whole warp)
+        tmem_ld32(acc + m0, v);
+        if (p.ks > 1) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (m0 + i < p.M) part[(m0 + i) * FN] = v[i];
+        } else {
+          // (all scales before the first store, behind which they would wait)
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 sa = *(const float4 *)(s_sa + m0 + i);
+            v[i] = v[i] * sa.x * sw + bias;
+            v[i + 1] = v[i + 1] * sa.y * sw + bias;
+            v[i + 2] = v[i + 2] * sa.z * sw + bias;
+            v[i + 3] = v[i + 3] * sa.w * sw + bias;
+          }
+          store_columns(p, y, n, m0, rows, v);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tempty + 8 * buf);
+    }
+  } else if (warp >= 8) {
+    // ---------------------------------------------------------- conversion --
+    const int group = (warp - 8) >> 2, row = (warp & 3) * 32 + lane;
+    const long its = (long)((tiles - unit + units - 1) / units) * (k1 - k0);
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    Ring w(group, WS), r(group, RS);
+    for (long it = group; it < its; it += GROUPS) {
+      // w's stage first: when it is free, the k-blocks up to it - WS have been
+      // multiplied, so the 8-bit stage's last load before this one (it - RS, of
+      // another group) has been seen and the phase's parity means this one (so
+      // it does for w's stage: MMAs complete in order, and this group has seen
+      // those up to it - 4 - WS)
+      if (!warp_wait(empty + 8 * w.at, w.phase ^ 1, abort_flag, p.status)) break;
+      if (!warp_wait(rfull + 8 * r.at, r.phase, abort_flag, p.status)) break;
+      __syncwarp();  // (tcgen05.st takes the whole warp)
+      tc_fence_after();
+      const uint8_t *src = raw + r.at * RAW + row * FK;  // (128B swizzle)
+      const uint32_t dst = w16 + lanes + (uint32_t)(w.at * (FK / 2));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint4 x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = *(const uint4 *)(src + (((h * 4 + j) ^ (row & 7)) * 16));
+        uint32_t f[32];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint4 lo, hi;
+          widen16(x[j], lo, hi);
+          f[8 * j] = lo.x; f[8 * j + 1] = lo.y; f[8 * j + 2] = lo.z; f[8 * j + 3] = lo.w;
+          f[8 * j + 4] = hi.x; f[8 * j + 5] = hi.y; f[8 * j + 6] = hi.z; f[8 * j + 7] = hi.w;
+        }
+        tmem_st32(dst + h * 32, f);
+      }
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(wfull + 8 * w.at);
+        mbar_arrive(rempty + 8 * r.at);
+      }
+      w.next<GROUPS>(WS);
+      r.next<GROUPS>(RS);
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_free<false>(tmem, 512);
+  }
+  if (p.ks == 1) return;
+  // the parts of this CTA's share of the rows, in the order of the ranks
+  cluster_sync_all();
+  const int m0 = p.M * rank / p.ks, m1 = p.M * (rank + 1) / p.ks;
+  const uint32_t parts = smem_u32(smem);
+  for (int i = threadIdx.x; i < (m1 - m0) * (FN / 8); i += FEW_THREADS) {
+    const int m = m0 + i / (FN / 8), c = i % (FN / 8) * 8, n = unit * FN + c;
+    if (n >= p.N) continue;
+    float v[8] = {};
+    for (int r = 0; r < p.ks; ++r) {
+      const uint32_t from = cluster_addr(parts + (uint32_t)(m * FN + c) * 4, r);
+      const float4 lo = ld_cluster4(from), hi = ld_cluster4(from + 16);
+      v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+      v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+    }
+    const float sa = s_sa[m];
+    const int cols = min(8, p.N - n);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < cols) v[j] = v[j] * sa * p.sw[n + j] + (p.bias ? p.bias[n + j] : 0.f);
+    E *y = (E *)p.y + (size_t)m * p.N + n;
+    if (p.N % 8 == 0) {
+#pragma unroll
+      for (int j = 0; j < 8; j += VEC16<E>) {
+        float f[VEC16<E>];
+#pragma unroll
+        for (int k = 0; k < VEC16<E>; ++k) f[k] = v[j + k];
+        *(uint4 *)(y + j) = pack16(f, (E *)nullptr);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < cols) y[j] = from_f<E>(v[j]);
+    }
+  }
+  cluster_sync_all();  // no CTA leaves while another may read its part
+}
+
+// [rows][K] matrix of 8-bit or (f16) 16-bit elements, boxes of `cols` columns
+// and `box` rows, 128B-swizzled or not.
+bool make_map(CUtensorMap *m, const void *base, int rows, int K, int cols, int box, bool f16,
+              bool swizzle) {
   EncodeFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)K * (f16 ? 2 : 1)};
-  cuuint32_t bx[2] = {BK, (cuuint32_t)box};
+  cuuint32_t bx[2] = {(cuuint32_t)cols, (cuuint32_t)box};
   cuuint32_t es[2] = {1, 1};
   return fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
             const_cast<void *>(base), dims, strides, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            f16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of a from which CTA pairs are used.
-constexpr int PAIR_MIN = 129;
-
-// Tile width for `units` CTAs or pairs that work at once: the least (rounds)
-// x (width + 32, a tile's cost apart from its width).
-int tile_width(int M, int N, int rows, int units, int step, int most) {
-  const long mb = (M + rows - 1) / rows;
+// Tile width for `units` pairs that work at once: the least (rounds) x (width +
+// 32, a tile's cost apart from its width).
+int tile_width(int M, int N, int units) {
+  const long mb = (M + ROWS - 1) / ROWS;
   long best = 0;
   int width = 0;
-  for (int bn = most; bn >= step; bn -= step) {
+  for (int bn = 256; bn >= 32; bn -= 32) {
     const long tiles = mb * ((N + bn - 1) / bn);
     const long cost = (tiles + units - 1) / units * (bn + 32);
     if (width == 0 || cost < best) {
@@ -710,55 +1082,104 @@ int tile_width(int M, int N, int rows, int units, int step, int most) {
   return width;
 }
 
-template <typename E, bool PAIR>
-cudaError_t mma_t(const Q8Args &a, cudaStream_t s) {
-  using S = Shape<PAIR>;
-  constexpr int CTAS = PAIR ? 2 : 1;
-  static int most = 0;  // CTAs or pairs that the GPU runs at once
-  static const cudaError_t attr = [] {
-    cudaError_t e = cudaFuncSetAttribute(q8_mma_kernel<E, PAIR>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
-    most = num_sms();
-    if (e != cudaSuccess || !PAIR) return e;
-    // (its SM clusters may have odd ones out)
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * (num_sms() / 2));
-    cfg.blockDim = dim3(S::THREADS);
-    cfg.dynamicSmemBytes = S::SMEM;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 2;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&most, q8_mma_kernel<E, PAIR>, &cfg);
-    return e == cudaSuccess && most < 1 ? cudaErrorInvalidConfiguration : e;
-  }();
-  if (attr != cudaSuccess) return attr;
+// CTAs, in clusters of `cluster`, that the GPU runs of a kernel at once.
+template <typename Kernel>
+cudaError_t ctas_at_once(Kernel kernel, int threads, int smem, int cluster, int *ctas) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(num_sms() / cluster * cluster);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cluster;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  int n = 0;
+  const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+  *ctas = n * cluster;
+  return e;
+}
+
+cudaError_t launch_widen(const Q8Args &a, cudaStream_t s) {
   const size_t vecs = (size_t)a.M * a.K / 16;
   if ((vecs + 255) / 256 > 0x7FFFFFFFull) return cudaErrorInvalidValue;
   const cudaError_t e =
       launch_k(q8_widen_kernel, dim3((unsigned)((vecs + 255) / 256)), dim3(256), 0, s,
                (const uint4 *)a.aq, vecs, (uint4 *)a.ws);
-  if (e != cudaSuccess) return e;
   prof_mark(KID_Q8_WIDEN, s);
+  return e;
+}
+
+template <typename E>
+cudaError_t mma_t(const Q8Args &a, cudaStream_t s) {
+  static int pairs = 0;  // that the GPU runs at once (its SM clusters may have odd ones out)
+  static const cudaError_t attr = [] {
+    cudaError_t e = cudaFuncSetAttribute(q8_mma_kernel<E>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e == cudaSuccess) e = ctas_at_once(q8_mma_kernel<E>, THREADS, SMEM, 2, &pairs);
+    pairs /= 2;
+    return e == cudaSuccess && pairs < 1 ? cudaErrorInvalidConfiguration : e;
+  }();
+  if (attr != cudaSuccess) return attr;
+  const cudaError_t e = launch_widen(a, s);
+  if (e != cudaSuccess) return e;
   Q8Params p;
   memset(&p, 0, sizeof(p));
   p.M = a.M; p.N = a.N; p.K = a.K; p.sa = a.ascale; p.sw = a.wscale; p.bias = a.bias; p.y = a.y;
   p.status = a.status;
-  p.bn = tile_width(a.M, a.N, S::ROWS, most, 16 * CTAS, 128 * CTAS);
-  p.box = a.M >= BM ? BM : (a.M + 7) / 8 * 8;
+  p.bn = tile_width(a.M, a.N, pairs);
   Q8Maps maps;
-  if (!make_map(&maps.a, a.ws, a.M, a.K, p.box, true) ||
-      !make_map(&maps.w, a.wq, a.N, a.K, p.bn / CTAS, false))
+  if (!make_map(&maps.a, a.ws, a.M, a.K, BK, BM, true, true) ||
+      !make_map(&maps.w, a.wq, a.N, a.K, BK, p.bn / 2, false, false))
     return cudaErrorInvalidValue;
-  const long long tiles = (long long)((a.M + S::ROWS - 1) / S::ROWS) * ((a.N + p.bn - 1) / p.bn);
+  const long long tiles = (long long)((a.M + ROWS - 1) / ROWS) * ((a.N + p.bn - 1) / p.bn);
   if (tiles > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-  const int grid = CTAS * (tiles < most ? (int)tiles : most);
-  return PAIR ? launch_clusters(q8_mma_kernel<E, PAIR>, dim3(grid), dim3(S::THREADS), S::SMEM, 2, s,
-                                maps, p)
-              : launch_k(q8_mma_kernel<E, PAIR>, dim3(grid), dim3(S::THREADS), S::SMEM, s, maps, p);
+  const int grid = 2 * (tiles < pairs ? (int)tiles : pairs);
+  return launch_clusters(q8_mma_kernel<E>, dim3(grid), dim3(THREADS), SMEM, 2, s, maps, p);
+}
+
+template <typename E>
+cudaError_t few_t(const Q8Args &a, cudaStream_t s) {
+  static int at_once[4];  // CTAs in clusters of (1,) 2, 4, 8 that the GPU runs at once
+  static const cudaError_t attr = [] {
+    cudaError_t e = cudaFuncSetAttribute(q8_few_kernel<E>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, FEW_SMEM);
+    for (int i = 1; i < 4 && e == cudaSuccess; ++i)
+      e = ctas_at_once(q8_few_kernel<E>, FEW_THREADS, FEW_SMEM, 1 << i, &at_once[i]);
+    return e;
+  }();
+  if (attr != cudaSuccess) return attr;
+  cudaError_t e = launch_widen(a, s);
+  if (e != cudaSuccess) return e;
+  FewParams p;
+  memset(&p, 0, sizeof(p));
+  p.M = a.M; p.N = a.N; p.K = a.K; p.sa = a.ascale; p.sw = a.wscale; p.bias = a.bias; p.y = a.y;
+  p.status = a.status;
+  p.box = (a.M + 7) / 8 * 8;
+  // the 512 TMEM columns hold two accumulators and four to six stages, the
+  // rings in shared memory as many of a and six (no fewer than of the others:
+  // the conversion's order of waits) to twelve of w
+  p.cols = (a.M + 15) / 16 * 16;
+  p.stages = (512 - 2 * p.cols) / (FK / 2);
+  if (p.stages > FEW_STAGES) p.stages = FEW_STAGES;
+  const int raw = (FEW_RINGS - p.stages * p.box * FK * 2) / (FN * FK);
+  p.raw_stages = raw < FEW_RAW ? raw : FEW_RAW;
+  // CTAs that share a tile: while all of them run at once and each has two
+  // k-blocks
+  const int tiles = (a.N + FN - 1) / FN, KT = (a.K + FK - 1) / FK;
+  p.ks = 1;
+  for (int i = 1; i < 4; ++i)
+    if (((long long)tiles << i) <= at_once[i] && KT >= 2 << i) p.ks = 1 << i;
+  Q8Maps maps;
+  if (!make_map(&maps.a, a.ws, a.M, a.K, 64, p.box, true, true) ||
+      !make_map(&maps.w, a.wq, a.N, a.K, FK, FN, false, true))
+    return cudaErrorInvalidValue;
+  const int grid = p.ks > 1 ? tiles * p.ks : tiles < num_sms() ? tiles : num_sms();
+  return p.ks > 1 ? launch_clusters(q8_few_kernel<E>, dim3(grid), dim3(FEW_THREADS), FEW_SMEM,
+                                    p.ks, s, maps, p)
+                  : launch_k(q8_few_kernel<E>, dim3(grid), dim3(FEW_THREADS), FEW_SMEM, s, maps, p);
 }
 
 template <typename E, int MT>
@@ -792,34 +1213,43 @@ cudaError_t frag_t(const Q8Args &a, cudaStream_t s) {
   return a.N >= 64 * num_sms() ? frag_mt<E, NT, 2>(a, s) : frag_mt<E, NT, 1>(a, s);
 }
 
-// Measured, us at N x K = 14336 x 4096 | 8192 x 2048 | 2048 x 2048 | 50001 x
-// 2048 (weights from HBM; the floors, N x K bytes, are 8.6 | 2.5 | 0.6 | 15):
-//   M 1    rows 14.4 | 5.6 | 2.8 | 22.7    frag 15.9 | 6.5 | 3.9 | 22.6
-//   M 4    rows 12.4 | 6.9 | 2.9 | 24.1    frag 16.5 | 6.6 | 3.9 | 23.6
-//   M 8    rows 22.9 | 11.9 | 4.9 | 47.2   frag 16.7 | 6.6 | 3.9 | 24.2
-//   M 16   frag 17.7 | 8.4 | 4.8 | 33.1    mma 21.6 | 13.1 | 11.6 | 37.7
-//   M 32   frag 23.7 | 12.4 | 5.7 | 49.6   mma 21.6 | 13.1 | 11.6 | 37.7
-//   M 64   mma 21.9 | 13.1 | 11.7 | 38.3
-//   M 128  mma 23.2 | 13.7 | 12.1 | 41.0
-//   M 129  pair 27.3 | 15.1 | 12.5 | 48.7
-// The mma kernels take about 440 cycles a k-block however narrow the tile:
-// the issuing warp's wait, four MMAs and commit.
+// Whether a batch of decoded rows is multiplied in fragments: few kernel cycles
+// where the weights are small, but their rows of a are widened again in every
+// warp.  Measured, us at N x K = 2048 x 2048 | 8192 x 2048 | 8192 x 4096 | 14336 x
+// 4096 | 50001 x 2048 | 14336 x 16384 (weights from HBM; the floors, N x K bytes,
+// are 0.6 | 2.5 | 4.9 | 8.6 | 15 | 35):
+//   M 1    rows 2.8 | 5.6 | - | 13.4 | 22.0 | 47   few - | - | - | 15.4 | 25.2 | 45
+//   M 4    rows 2.9 | 6.9 | - | 12.7 | 24.1 | 51   few - | - | - | 15.5 | 24.8 | 44
+//   M 8    frag 4.0 | 6.7 | 10.6 | 16.9 | 24.7 | 62   few 8.5 | 10.7 | 13.4 | 15.5 | 24.2 | 43
+//   M 16   frag 4.8 | 8.4 | 13.6 | 18.1 | 32.8 | 60   few 8.6 | 10.8 | 13.6 | 15.5 | 24.5 | 44
+//   M 32   frag 5.8 | 12.4 | 20.5 | 36.6 | 68 | 153   few 9.1 | 11.3 | 14.1 | 16.0 | 24.8 | 44
+//   M 64   few 10.3 | 12.3 | - | 16.8 | 25.9 | 49   pair 12.2 | 14.2 | - | 25.5 | 45 | 76
+//   M 128  few 12.9 | 14.7 | - | 19.8 | 31.0 | 59   pair 12.6 | 15.1 | - | 27.5 | 48 | 82
+// (the rows' kernel is the simplest, and keeps up to four rows at any size; the
+// other way round, 50001 x 256 in 17 to 32 rows takes the fragments 17.9 us, few
+// 10.7, 8192 x 1024 8.6 and 9.7)
+bool in_fragments(int M, int N, int K) {
+  const long long bytes = (long long)N * K;
+  return M <= 16 ? bytes < 3ll << 24 : M <= 32 && N <= 8192 && bytes < 1ll << 24;
+}
+
 template <typename E>
 cudaError_t matmul_t(const Q8Args &a, cudaStream_t s) {
   if (a.M == 1) return rows_t<E, 1>(a, s);
   if (a.M == 2) return rows_t<E, 2>(a, s);
   if (a.M <= ROWS_MAX) return rows_t<E, 4>(a, s);
-  if (a.M <= 8) return frag_t<E, 1>(a, s);
-  if (a.M <= 16) return frag_t<E, 2>(a, s);
-  if (a.M <= 32 && a.N <= 8192) return frag_mt<E, 4, 1>(a, s);
-  return a.M < PAIR_MIN ? mma_t<E, false>(a, s) : mma_t<E, true>(a, s);
+  if (in_fragments(a.M, a.N, a.K))
+    return a.M <= 8    ? frag_t<E, 1>(a, s)
+           : a.M <= 16 ? frag_t<E, 2>(a, s)
+                       : frag_mt<E, 4, 1>(a, s);
+  return a.M <= FEW_MOST ? few_t<E>(a, s) : mma_t<E>(a, s);
 }
 
 }  // namespace
 
 size_t q8_scratch(int M, int N, int K) {
   // a in fp16
-  return M <= 16 || (M <= 32 && N <= 8192) ? 0 : ((size_t)M * K * 2 + 255) / 256 * 256;
+  return M <= ROWS_MAX || in_fragments(M, N, K) ? 0 : ((size_t)M * K * 2 + 255) / 256 * 256;
 }
 
 cudaError_t launch_q8_matmul(const Q8Args &a, cudaStream_t s) {

@@ -156,6 +156,17 @@ def test_many_tiles(M, N, K):
         verify(a, w, sa, sw, None, "bf16")
 
 
+@pytest.mark.parametrize("M,N,K", [(5, 14336, 4096), (9, 25001, 2064), (16, 50000, 1040),
+                                   (33, 1, 16), (40, 129, 4112), (97, 1030, 2064),
+                                   (128, 2048, 8192), (128, 4104, 528)])
+@pytest.mark.parametrize("dtype,bias", [("bf16", True), ("f32", True), ("bf16", False)])
+def test_few_rows(M, N, K, dtype, bias):
+    """Up to 128 rows: MMAs as wide as the rows, tiles alone or shared by a cluster, columns that
+    end inside a tile, a warp or a vector of eight."""
+    a, w, sa, sw, b = inputs(M, N, K, M + N + K)
+    verify(a, w, sa, sw, b if bias else None, dtype)
+
+
 TIMEOUT_CHILD = """
 import sys
 import torch
