@@ -213,17 +213,16 @@ q8_frag_kernel(const uint4 *a, const int8_t *w, const float *sa, const float *sw
 // ---- tensor cores --------------------------------------------------------------
 constexpr int BM = 128, BK = 64;
 constexpr int ACC_COLS = 256;  // TMEM columns of one accumulator
-constexpr int EPI_PITCH = 33;  // 32-bit words of an epilogue staging row
 constexpr int GROUPS = 4;      // conversion groups, which take the k-blocks in turn
 
 // A pair of CTAs per tile: rows of a; stages of a (fp16), of w in fp16 and in 8
 // bits, with 128 rows each; warps of a conversion group.
 constexpr int ROWS = 2 * BM;
-constexpr int AS = 5, WS = 4, RS = 6;
+constexpr int AS = 5, WS = 4, RS = 8;
 constexpr int GROUP = 2;
 constexpr int THREADS = 32 * (8 + GROUPS * GROUP);
 constexpr int TILE = BM * BK * 2, RAW = BM * BK;  // bytes of a stage
-constexpr int SMEM = 1024 + (AS + WS) * TILE + RS * RAW + 4 * 32 * EPI_PITCH * 4 + 2 * 256 * 4;
+constexpr int SMEM = 1024 + (AS + WS) * TILE + RS * RAW + 2 * 256 * 4;
 
 struct Q8Maps {
   CUtensorMap a, w;
@@ -241,10 +240,6 @@ __device__ __forceinline__ void fence_async_proxy() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// One warp's 32 accumulator rows (TMEM lane = row, from row m0 on) of a tile
-// of bn columns from n0 on: scaled, rounded, and stored through shared memory
-// so that one instruction writes 128 consecutive bytes of a row whatever its
-// alignment.
 __device__ __forceinline__ void scale32(float *v, float sa, const float *sw, const float *bias) {
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
@@ -256,89 +251,112 @@ __device__ __forceinline__ void scale32(float *v, float sa, const float *sw, con
   }
 }
 
-__device__ __forceinline__ void store_tile(const Q8Params &p, float *y, uint32_t acc, int m0,
-                                           int n0, float sa, const float *s_sw, float *stage) {
-  const int lane = threadIdx.x & 31, cols = min(p.bn, p.N - n0), rows = min(32, p.M - m0);
-  for (int c0 = 0; c0 < cols; c0 += 32) {
-    float v[32];
-    tmem_ld32(acc + c0, v);
-    scale32(v, sa, s_sw + c0, s_sw + 256 + c0);
-    __syncwarp();
+// 32 values of a row, rounded, as the words behind e[0 .. 3].
+__device__ __forceinline__ void row_words(const float (&v)[32], uint32_t (&e)[36], float *) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) stage[lane * EPI_PITCH + i] = v[i];
-    __syncwarp();
-    float *dst = y + (size_t)m0 * p.N + n0 + c0 + lane;
-    if (c0 + lane < cols)
-#pragma unroll 4
-      for (int r = 0; r < rows; ++r) dst[(size_t)r * p.N] = stage[r * EPI_PITCH + lane];
+  for (int i = 0; i < 32; ++i) e[4 + i] = __float_as_uint(v[i]);
+}
+__device__ __forceinline__ void row_words(const float (&v)[32], uint32_t (&e)[20], bf16 *) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) e[4 + i] = pack_bf2(v[2 * i], v[2 * i + 1]);
+}
+// e[4 ..] becomes what stands r elements before it.
+__device__ __forceinline__ void move_words(uint32_t (&e)[36], int r, float *) {
+  const bool r1 = r & 1, r2 = r & 2;
+#pragma unroll
+  for (int i = 35; i >= 1; --i) e[i] = r1 ? e[i - 1] : e[i];
+#pragma unroll
+  for (int i = 35; i >= 4; --i) e[i] = r2 ? e[i - 2] : e[i];
+}
+__device__ __forceinline__ void move_words(uint32_t (&e)[20], int r, bf16 *) {
+  const uint32_t r1 = r & 1 ? 0x5432 : 0x7654;
+  const bool r2 = r & 2, r4 = r & 4;
+#pragma unroll
+  for (int i = 19; i >= 1; --i) e[i] = __byte_perm(e[i - 1], e[i], r1);
+#pragma unroll
+  for (int i = 19; i >= 2; --i) e[i] = r2 ? e[i - 1] : e[i];
+#pragma unroll
+  for (int i = 19; i >= 4; --i) e[i] = r4 ? e[i - 2] : e[i];
+}
+// Elements lo <= j < hi of a vector.
+__device__ __forceinline__ void store_some(float *dst, const uint32_t *w, int lo, int hi) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j >= lo && j < hi) dst[j] = __uint_as_float(w[j]);
+}
+__device__ __forceinline__ void store_some(bf16 *dst, const uint32_t *w, int lo, int hi) {
+  // from lo up to what is aligned to 2, 4, 8 elements, and from there down to hi
+  auto word = [&](int i) { return i & 2 ? i & 1 ? w[3] : w[2] : i & 1 ? w[1] : w[0]; };
+  if ((lo & 1) && lo < hi) {
+    ((uint16_t *)dst)[lo] = (uint16_t)(word(lo >> 1) >> 16);
+    ++lo;
   }
+  if ((lo & 2) && lo + 2 <= hi) {
+    *(uint32_t *)(dst + lo) = word(lo >> 1);
+    lo += 2;
+  }
+  if (lo + 4 <= hi) {
+    *(uint2 *)(dst + lo) = lo ? make_uint2(w[2], w[3]) : make_uint2(w[0], w[1]);
+    lo += 4;
+  }
+  if (lo + 2 <= hi) {
+    *(uint32_t *)(dst + lo) = word(lo >> 1);
+    lo += 2;
+  }
+  if (lo < hi) ((uint16_t *)dst)[lo] = (uint16_t)word(lo >> 1);
 }
 
-// bf16: pairs of elements as they lie in aligned 4-byte words of y.  With an
-// odd N every other row starts in the upper half of a word; such a row's
-// pairs are (-1, 0), (1, 2), ...: its thread packs them so, carrying one
-// element from block to block, and only a tile's first and last words are
-// stored by halves.
-__device__ __forceinline__ void store_tile(const Q8Params &p, bf16 *y, uint32_t acc, int m0,
-                                           int n0, float sa, const float *s_sw, float *stage_f) {
-  uint32_t *stage = (uint32_t *)stage_f;
-  const int lane = threadIdx.x & 31, cols = min(p.bn, p.N - n0), rows = min(32, p.M - m0);
-  const int odd_n = p.N & 1;                  // (n0 is even)
-  const bool odd = (odd_n & (m0 + lane)) != 0;
-  float carry = 0.f;
-  if (p.N % 8 == 0) {
-    // 16-byte aligned rows: each thread stores its own (a last tile's epilogue
-    // is over sooner: 18.7 against 21.6 us at 300 x 8192 x 2048)
-    for (int c0 = 0; c0 < cols; c0 += 32) {
-      float v[32];
-      tmem_ld32(acc + c0, v);
-      scale32(v, sa, s_sw + c0, s_sw + 256 + c0);
-      uint4 *dst = (uint4 *)(y + (size_t)(m0 + lane) * p.N + n0 + c0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (lane < rows && c0 + 8 * i < cols)
-          dst[i] = make_uint4(pack_bf2(v[8 * i], v[8 * i + 1]), pack_bf2(v[8 * i + 2], v[8 * i + 3]),
-                              pack_bf2(v[8 * i + 4], v[8 * i + 5]),
-                              pack_bf2(v[8 * i + 6], v[8 * i + 7]));
-    }
-    return;
-  }
-  for (int c0 = 0; c0 < cols; c0 += 64) {
-    float v[64];
-    tmem_ld32(acc + c0, *(float(*)[32])v);
-    if (c0 + 32 < p.bn) tmem_ld32(acc + c0 + 32, *(float(*)[32])(v + 32));
+// One warp's 32 accumulator rows (TMEM lane = row, from row m0 on) of a tile of
+// bn columns from n0 on: scaled, rounded, and stored by each thread for its own
+// row, in 16 bytes at a time whatever the row's alignment: its elements move by
+// as many places as the row starts behind a 16-byte boundary, and the first and
+// the last few are stored alone, in the widest pieces.  (Stores count by
+// their number: 1001 x 50001 x 512, where rows of y start at odd elements and
+// the epilogue is all there is, takes 70 us, with 50000 columns 64; through
+// shared memory, in words that a warp stores for one row, it took 118, and 1001
+// x 50001 x 2048 151 us instead of 144.)
+template <typename E>
+__device__ __forceinline__ void store_tile(const Q8Params &p, E *y, uint32_t acc, int m0, int n0,
+                                           float sa, const float *s_sw) {
+  constexpr int N = VEC16<E>, WORDS = 32 * (int)sizeof(E) / 4;  // of 32 columns
+  const int lane = threadIdx.x & 31, cols = min(p.bn, p.N - n0);
+  E *row = y + (size_t)(m0 + lane) * p.N + n0;
+  const int r = (int)((uintptr_t)row / sizeof(E)) & (N - 1);
+  row -= r;
+  const int end = m0 + lane < p.M ? r + cols : 0;
+  // the vector from element `at` on
+  auto store = [&](const uint32_t *w, int at) {
+    const int lo = at == 0 ? r : 0, hi = end - at;
+    if (lo == 0 && hi >= N)
+      *(uint4 *)(row + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if (hi > lo)
+      store_some(row + at, w, lo, hi);
+  };
+  uint32_t e[4 + WORDS], last[4] = {};
+  int c0 = 0;
+  for (; c0 < cols; c0 += 32) {
+    float v[32];
+    __syncwarp();  // (tcgen05.ld takes the whole warp)
+    tmem_ld32(acc + c0, v);
     scale32(v, sa, s_sw + c0, s_sw + 256 + c0);
-    scale32(v + 32, sa, s_sw + c0 + 32, s_sw + 256 + c0 + 32);
-    __syncwarp();
+    row_words(v, e, (E *)nullptr);
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      stage[lane * EPI_PITCH + j] = pack_bf2(odd ? (j ? v[2 * j - 1] : carry) : v[2 * j],
-                                             odd ? v[2 * j] : v[2 * j + 1]);
-    carry = v[63];
-    __syncwarp();
-    bf16 *dst = y + (size_t)m0 * p.N + n0 + c0 + 2 * lane;
-    if (c0 > 0 && c0 + 64 < cols) {
-#pragma unroll 4
-      for (int r = 0; r < rows; ++r)
-        *(uint32_t *)(dst + (size_t)r * p.N - (odd_n & (m0 + r))) = stage[r * EPI_PITCH + lane];
-    } else {
-      for (int r = 0; r < rows; ++r) {
-        const int o = odd_n & (m0 + r), c = c0 + 2 * lane - o;  // column of the word's lower half
-        const uint32_t w = stage[r * EPI_PITCH + lane];
-        bf16 *d = dst + (size_t)r * p.N - o;
-        if (c >= 0 && c + 1 < cols) {
-          *(uint32_t *)d = w;
-        } else if (c >= 0 && c < cols) {
-          *(uint16_t *)d = (uint16_t)w;
-        } else if (c == -1) {
-          *(uint16_t *)(d + 1) = (uint16_t)(w >> 16);
-        }
-      }
+    for (int i = 0; i < 4; ++i) {
+      e[i] = last[i];
+      last[i] = e[WORDS + i];
     }
+    move_words(e, r, (E *)nullptr);
+#pragma unroll
+    for (int j = 0; j < 32; j += N) store(e + 4 + j * (int)sizeof(E) / 4, c0 + j);
   }
-  // the last element of a shifted row whose columns fill the last block
-  if (odd && lane < rows && cols % 64 == 0)
-    y[(size_t)(m0 + lane) * p.N + n0 + cols - 1] = __float2bfloat16_rn(carry);
+  // what has moved past the last 32 columns
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    e[i] = last[i];
+    e[4 + i] = 0;
+  }
+  move_words(e, r, (E *)nullptr);
+  store(e + 4, c0);
 }
 
 // Scale and bias of a tile's columns, staged by the 128 epilogue threads.
@@ -454,8 +472,7 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t *sa16 = smem, *sw16 = sa16 + AS * TILE, *raw = sw16 + WS * TILE;
-  float *s_epi = (float *)(raw + RS * RAW);
-  float *s_sw = s_epi + 4 * 32 * EPI_PITCH;
+  float *s_sw = (float *)(raw + RS * RAW);
   // Barriers of this CTA: a stage is full, a stage is free again.  Barriers of
   // the leader, at which both CTAs arrive: a k-block's operands are ready, an
   // accumulator has been read (tempty).
@@ -602,7 +619,6 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
   } else if (warp < 6) {
     // ------------------------------------------------------------ epilogue --
     const int q = warp & 3;  // TMEM lane quadrant of this warp
-    float *stage = s_epi + q * 32 * EPI_PITCH;
     const uint32_t free = cluster_addr(tempty, 0);
     int lt = 0;
     for (int t = unit; t < tiles; t += units, ++lt) {
@@ -616,7 +632,7 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
       tc_fence_after();
       if (m0 < p.M)  // (uniform for the warp)
         store_tile(p, (E *)p.y, tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * ACC_COLS), m0,
-                   n0, sa, s_sw, stage);
+                   n0, sa, s_sw);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(free + 8 * buf);
