@@ -697,7 +697,7 @@ constexpr int FEW_RAW = 12;                // of w in 8 bits: the most
 constexpr int FEW_RINGS = 4 * FEW_MOST * FK * 2 + 6 * FN * FK;
 constexpr int FEW_SMEM = 1024 + FEW_RINGS;
 constexpr int FEW_THREADS = 32 * (8 + 4 * GROUPS);
-constexpr int FEW_KS = 8;                  // CTAs that share a tile: the most
+constexpr int FEW_BARS = 3 * FEW_STAGES + 2 * FEW_RAW + 5;
 
 struct FewParams {
   int M, N, K;
@@ -802,7 +802,7 @@ q8_few_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ FewPa
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t *raw = smem + WS * a_step;  // (behind a: an MMA may read past a stage's rows)
-  __shared__ uint64_t bars[3 * FEW_STAGES + 2 * FEW_RAW + 5];
+  __shared__ uint64_t bars[FEW_BARS];
   __shared__ __align__(16) float s_sa[FEW_MOST];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
@@ -819,35 +819,28 @@ q8_few_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ FewPa
   const int units = (int)gridDim.x / p.ks;
   const int k0 = (int)((long)KT * rank / p.ks), k1 = (int)((long)KT * (rank + 1) / p.ks);
 
-  const int early = min(RS, k1 - k0);
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < WS; ++i) {
-      mbar_init(afull + 8 * i, 1);
-      mbar_init(wfull + 8 * i, 4);
-      mbar_init(empty + 8 * i, 1);
+  // The loads of w begin as soon as their barriers stand: warp 0 only arrives
+  // where the others wait for the barriers and for TMEM.
+  uint32_t tmem = 0;
+  if (warp == 0) {
+    for (int i = lane; i < FEW_BARS; i += 32) {
+      const uint32_t bar = afull + 8 * i;  // four warps arrive at these, one thread at the others
+      const bool four = (bar >= wfull && bar < empty) || (bar >= rempty && bar < tfull) ||
+                        (bar >= tempty && bar < mma_done);
+      mbar_init(bar, four ? 4 : 1);
     }
-    for (int i = 0; i < RS; ++i) {
-      mbar_init(rfull + 8 * i, 1);
-      mbar_init(rempty + 8 * i, 4);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(tfull + 8 * i, 1);
-      mbar_init(tempty + 8 * i, 4);
-    }
-    mbar_init(mma_done, 1);
-    s_abort = 0;
+    if (lane == 0) s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    // the first tile's w under way before the others are ready
-    for (int i = 0; i < early; ++i) {
-      mbar_expect_tx(rfull + 8 * i, RAW);
-      tma_load_2d(smem_u32(raw) + i * RAW, &maps.w, (k0 + i) * FK, unit * FN, rfull + 8 * i);
-    }
+    __syncwarp();
+    asm volatile("bar.arrive 2, %0;" ::"n"(FEW_THREADS) : "memory");
+  } else {
+    if (warp == 1) tmem_alloc<false>(smem_u32(&s_tmem), 512);
+    tc_fence_before();
+    asm volatile("bar.sync 2, %0;" ::"n"(FEW_THREADS) : "memory");
+    tc_fence_after();
+    tmem = s_tmem;
   }
-  if (warp == 1) tmem_alloc<false>(smem_u32(&s_tmem), 512);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = s_tmem, w16 = tmem + 2 * p.cols;  // two accumulators; the stages of w
+  const uint32_t w16 = tmem + 2 * p.cols;  // behind two accumulators: the stages of w
 
   if (warp == 0 || warp == 6) {
     // ------------------------------- TMA producers: w in 8 bits; a in fp16 --
@@ -857,12 +850,11 @@ q8_few_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ FewPa
     const uint32_t full = is_w ? rfull : afull, free = is_w ? rempty : empty;
     const uint32_t dst0 = smem_u32(is_w ? raw : smem), step = is_w ? RAW : a_step;
     const int stages = is_w ? RS : WS;
-    const int first = is_w ? early : 0;  // (loads that are on their way)
-    Ring r(first, stages);
-    long issued = first;
+    Ring r(0, stages);
+    long issued = 0;
     bool ok = true;
     for (int t = unit; t < tiles && ok; t += units) {
-      for (int kt = t == unit ? k0 + first : k0; kt < k1; ++kt) {
+      for (int kt = k0; kt < k1; ++kt) {
         ok = warp_wait(free + 8 * r.at, r.phase ^ 1, abort_flag, p.status);
         if (!ok) break;
         if (issues) {
