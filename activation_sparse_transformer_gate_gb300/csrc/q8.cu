@@ -679,17 +679,19 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
 // rows of a read for however few there are, a k-block of 64 for 96 columns moved
 // 57 KB through shared memory, which at its 128 bytes a cycle took the 420 cycles
 // that were measured (37 x 14336 x 4096: 20.2 us); here 128 k of 128 columns move
-// 52 KB and take 620 (16.0 us).
+// 52 KB and take 600 (15.4 us).
 //
 // A tile is 128 columns of y.  Where the tiles leave SMs idle, a cluster of ks
 // CTAs shares a tile's k and adds the parts through distributed shared memory,
-// each CTA for its share of the rows of a (37 x 8192 x 2048: 11.4 us).
+// each CTA for its share of the rows of a (37 x 2048 x 2048: 9.0 us).
 //
-// What is left above the weights' bytes: the launch of q8_widen_kernel, about
-// 9000 cycles from the first load to the first MMA (all SMs fill their rings at
-// once), 2100 of the epilogue, and 112 of 152 SMs at N = 14336.  The epilogue's
-// stores count by their number: 32 of 64 bytes a warp took 4200 cycles for 37
-// rows, the same bytes in stores of 16 a lane 2100.
+// What is left above the weights' bytes: an MMA takes 75 cycles however few rows
+// of a there are (128 x 16 of w come from TMEM at about 64 bytes a cycle), 600
+// a k-block, so 112 tiles keep 112 of 152 SMs below HBM's rate (narrower tiles on
+// more SMs take the same time: their MMAs are as high); some 9000 cycles from
+// the first load to the first MMA, when all SMs fill their rings at once; 2000
+// of the epilogue.  Its stores count by their number: 32 of 64 bytes a warp took
+// 4200 cycles for 37 rows, the same bytes in stores of 16 a lane 2100.
 constexpr int FEW_MOST = 128;              // rows of a
 constexpr int FN = 128, FK = 128;          // columns of y a tile, k of a k-block
 constexpr int FEW_STAGES = 6;              // of w in TMEM and of a in shared memory: the most
@@ -1020,41 +1022,62 @@ q8_few_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ FewPa
     tmem_free<false>(tmem, 512);
   }
   if (p.ks == 1) return;
-  // the parts of this CTA's share of the rows, in the order of the ranks
-  cluster_sync_all();
+  // The parts of this CTA's share of the rows, in the order of the ranks: eight
+  // columns a thread, in at most ITEMS rows.  The CTAs part as soon as all have
+  // read, with their stores to come.
+  constexpr int ITEMS = (FEW_MOST / 2 * (FN / 8) + FEW_THREADS - 1) / FEW_THREADS;
+  static_assert(FEW_THREADS % (FN / 8) == 0, "a thread's rows share its columns");
   const int m0 = p.M * rank / p.ks, m1 = p.M * (rank + 1) / p.ks;
-  const uint32_t parts = smem_u32(smem);
-  for (int i = threadIdx.x; i < (m1 - m0) * (FN / 8); i += FEW_THREADS) {
-    const int m = m0 + i / (FN / 8), c = i % (FN / 8) * 8, n = unit * FN + c;
-    if (n >= p.N) continue;
-    float v[8] = {};
-    for (int r = 0; r < p.ks; ++r) {
-      const uint32_t from = cluster_addr(parts + (uint32_t)(m * FN + c) * 4, r);
-      const float4 lo = ld_cluster4(from), hi = ld_cluster4(from + 16);
-      v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
-      v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
-    }
-    const float sa = s_sa[m];
-    const int cols = min(8, p.N - n);
+  const int c = threadIdx.x % (FN / 8) * 8, n = unit * FN + c;
+  const int cols = min(8, p.N - n);
+  float sw[8], bias[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < cols) v[j] = v[j] * sa * p.sw[n + j] + (p.bias ? p.bias[n + j] : 0.f);
+  for (int j = 0; j < 8; ++j) {
+    sw[j] = j < cols ? p.sw[n + j] : 0.f;
+    bias[j] = p.bias && j < cols ? p.bias[n + j] : 0.f;
+  }
+  cluster_sync_all();
+  float v[ITEMS][8] = {};
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    const int m = m0 + (int)(threadIdx.x + k * FEW_THREADS) / (FN / 8);
+    if (m >= m1 || cols <= 0) continue;
+    const uint32_t at = smem_u32(smem) + (uint32_t)(m * FN + c) * 4;
+    for (int r = 0; r < p.ks; r += 2) {
+      const uint32_t one = cluster_addr(at, r), two = cluster_addr(at, r + 1);
+      const float4 a = ld_cluster4(one), b = ld_cluster4(one + 16);
+      const float4 d = ld_cluster4(two), e = ld_cluster4(two + 16);
+      v[k][0] += a.x; v[k][1] += a.y; v[k][2] += a.z; v[k][3] += a.w;
+      v[k][4] += b.x; v[k][5] += b.y; v[k][6] += b.z; v[k][7] += b.w;
+      v[k][0] += d.x; v[k][1] += d.y; v[k][2] += d.z; v[k][3] += d.w;
+      v[k][4] += e.x; v[k][5] += e.y; v[k][6] += e.z; v[k][7] += e.w;
+    }
+  }
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    const int m = m0 + (int)(threadIdx.x + k * FEW_THREADS) / (FN / 8);
+    if (m >= m1 || cols <= 0) continue;
+    const float sa = s_sa[m];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[k][j] = v[k][j] * sa * sw[j] + bias[j];
     E *y = (E *)p.y + (size_t)m * p.N + n;
     if (p.N % 8 == 0) {
 #pragma unroll
       for (int j = 0; j < 8; j += VEC16<E>) {
         float f[VEC16<E>];
 #pragma unroll
-        for (int k = 0; k < VEC16<E>; ++k) f[k] = v[j + k];
+        for (int i = 0; i < VEC16<E>; ++i) f[i] = v[k][j + i];
         *(uint4 *)(y + j) = pack16(f, (E *)nullptr);
       }
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (j < cols) y[j] = from_f<E>(v[j]);
+        if (j < cols) y[j] = from_f<E>(v[k][j]);
     }
   }
-  cluster_sync_all();  // no CTA leaves while another may read its part
+  // no CTA leaves while another may read its part
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // [rows][K] matrix of 8-bit or (f16) 16-bit elements, boxes of `cols` columns
@@ -1174,12 +1197,20 @@ cudaError_t few_t(const Q8Args &a, cudaStream_t s) {
   if (p.stages > FEW_STAGES) p.stages = FEW_STAGES;
   const int raw = (FEW_RINGS - p.stages * p.box * FK * 2) / (FN * FK);
   p.raw_stages = raw < FEW_RAW ? raw : FEW_RAW;
-  // CTAs that share a tile: while all of them run at once and each has two
-  // k-blocks
+  // CTAs that share a tile, while all of them run at once: a k-block takes about
+  // 600 cycles, the clusters' meetings and the join 5500 (in us, 8 rows and N x K
+  // = 2048 x 2048: 9.9 for one CTA a tile, 9.0 for two, 8.4 for four; 8192 x 2048:
+  // 10.2 and 10.6; 9728 x 4096: 14.9 and 14.1)
   const int tiles = (a.N + FN - 1) / FN, KT = (a.K + FK - 1) / FK;
   p.ks = 1;
-  for (int i = 1; i < 4; ++i)
-    if (((long long)tiles << i) <= at_once[i] && KT >= 2 << i) p.ks = 1 << i;
+  int best = KT * 600;
+  for (int i = 1; i < 4; ++i) {
+    const int cost = (KT + (1 << i) - 1) / (1 << i) * 600 + 5500;
+    if (((long long)tiles << i) <= at_once[i] && KT >= 1 << i && cost < best) {
+      best = cost;
+      p.ks = 1 << i;
+    }
+  }
   Q8Maps maps;
   if (!make_map(&maps.a, a.ws, a.M, a.K, 64, p.box, true, true) ||
       !make_map(&maps.w, a.wq, a.N, a.K, FK, FN, false, true))
@@ -1221,24 +1252,32 @@ cudaError_t frag_t(const Q8Args &a, cudaStream_t s) {
   return a.N >= 64 * num_sms() ? frag_mt<E, NT, 2>(a, s) : frag_mt<E, NT, 1>(a, s);
 }
 
-// Whether a batch of decoded rows is multiplied in fragments: few kernel cycles
-// where the weights are small, but their rows of a are widened again in every
-// warp.  Measured, us at N x K = 2048 x 2048 | 8192 x 2048 | 8192 x 4096 | 14336 x
-// 4096 | 50001 x 2048 | 14336 x 16384 (weights from HBM; the floors, N x K bytes,
-// are 0.6 | 2.5 | 4.9 | 8.6 | 15 | 35):
-//   M 1    rows 2.8 | 5.6 | - | 13.4 | 22.0 | 47   few - | - | - | 15.4 | 25.2 | 45
-//   M 4    rows 2.9 | 6.9 | - | 12.7 | 24.1 | 51   few - | - | - | 15.5 | 24.8 | 44
-//   M 8    frag 4.0 | 6.7 | 10.6 | 16.9 | 24.7 | 62   few 8.5 | 10.7 | 13.4 | 15.5 | 24.2 | 43
-//   M 16   frag 4.8 | 8.4 | 13.6 | 18.1 | 32.8 | 60   few 8.6 | 10.8 | 13.6 | 15.5 | 24.5 | 44
-//   M 32   frag 5.8 | 12.4 | 20.5 | 36.6 | 68 | 153   few 9.1 | 11.3 | 14.1 | 16.0 | 24.8 | 44
-//   M 64   few 10.3 | 12.3 | - | 16.8 | 25.9 | 49   pair 12.2 | 14.2 | - | 25.5 | 45 | 76
-//   M 128  few 12.9 | 14.7 | - | 19.8 | 31.0 | 59   pair 12.6 | 15.1 | - | 27.5 | 48 | 82
-// (the rows' kernel is the simplest, and keeps up to four rows at any size; the
-// other way round, 50001 x 256 in 17 to 32 rows takes the fragments 17.9 us, few
-// 10.7, 8192 x 1024 8.6 and 9.7)
+// Whether a batch of decoded rows is multiplied in fragments: it starts and ends
+// sooner, but rows of a are widened again in every warp.  Measured, us at N x K =
+// 2048 x 2048 | 8192 x 2048 | 4096 x 4096 | 8192 x 4096 | 14336 x 4096 | 50001 x
+// 2048 | 14336 x 16384 (weights from HBM; the floors, N x K bytes, are 0.6 | 2.5 |
+// 2.5 | 4.9 | 8.6 | 15 | 35):
+//   M 1    rows 2.4 | 5.1 | 5.1 | 8.4 | 13.5 | 21.6 | 46
+//          few  7.8 | 9.7 | 10.0 | 12.8 | 15.1 | 24.1 | 43
+//   M 4    rows 2.9 | 7.1 | 7.4 | 11.1 | 12.4 | 24.7 | 54
+//          few  7.9 | 9.7 | 10.1 | 12.8 | 15.1 | 23.5 | 43
+//   M 8    frag 4.0 | 6.6 | 7.3 | 10.7 | 16.8 | 24.3 | 64
+//          few  7.9 | 9.8 | 10.3 | 12.6 | 15.5 | 23.7 | 43
+//   M 16   frag 4.9 | 8.4 | 9.2 | 13.5 | 18.0 | 33.0 | 61
+//          few  8.1 | 9.9 | 10.5 | 12.9 | 15.5 | 24.2 | 44
+//   M 32   frag 5.7 | 12.5 | 11.3 | 20.6 | 36.5 | 68 | 151
+//          few  8.6 | 10.1 | 11.0 | 13.5 | 15.4 | 24.2 | 45
+//   M 64   few  9.8 | 10.8 | 12.5 | 13.9 | 16.5 | 25.5 | 49
+//          pair 12.3 | 14.3 | 19.8 | 21.2 | 26.7 | 39.4 | 80
+//   M 128  few  12.6 | 12.7 | 15.5 | 16.9 | 19.1 | 31.5 | 58
+//          pair 12.2 | 14.8 | 20.1 | 21.8 | 28.0 | 43.0 | 82
+// (Up to four rows stay with the simplest kernel.  Columns count too: 17 to 32
+// rows of 50001 x 256 take the fragments 16 to 18 us, few 10.5.)
 bool in_fragments(int M, int N, int K) {
   const long long bytes = (long long)N * K;
-  return M <= 16 ? bytes < 3ll << 24 : M <= 32 && N <= 8192 && bytes < 1ll << 24;
+  return M <= 8    ? bytes < 3ll << 24
+         : M <= 16 ? bytes < 1ll << 25
+                   : M <= 32 && N <= 8192 && bytes < 1ll << 24;
 }
 
 template <typename E>
