@@ -92,6 +92,28 @@ def test_against_64_bits(kind, T, V, D, dtype, itype):
     assert torch.equal(again, dtable)  # the same bits
 
 
+@pytest.mark.parametrize("kind,T,V,D", [
+    ("uniform", 600, 5, 16), ("zipf", 2047, 511, 72), ("uniform", 2048, 512, 16),
+    ("same", 2048, 40000, 8), ("distinct", 2048, 262143, 8), ("zipf", 2049, 50001, 24),
+    ("uniform", 700, 262144, 8), ("zipf", 1537, 9000, 520)])
+@pytest.mark.parametrize("itype", [torch.int32, torch.int64])
+def test_sort_forms(kind, T, V, D, itype):
+    """One, two and three passes, by one CTA (up to 2048 tokens below 2^18) and by the cluster;
+    some tokens are padding, some out of range."""
+    g = gen(T + V)
+    tok = tokens_of(kind, T, V, g).to(itype)
+    tok[5::11] = -7
+    tok[9::17] = V
+    table = torch.randn(V, D, generator=g).bfloat16()
+    dy = torch.randn(T, D, generator=g).bfloat16()
+    out, dtable, code = run(tok, table, dy, V, D, "bf16", 1.5, -7)
+    assert code == -5
+    ref, grad, bound = reference(tok, table, dy, V, 1.5, -7)
+    assert torch.equal(out.cpu(), ref)
+    check(dtable, grad, bound, "f32", "dtable")
+    assert torch.equal(run(tok, table, dy, V, D, "bf16", 1.5, -7)[1], dtable)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_padding_and_out_of_range(dtype):
     """Padded positions give zero rows and take no gradient, whatever dy holds there; a token
