@@ -188,8 +188,10 @@ __device__ __forceinline__ void list_softmax(Teacher &te, const DistillParams &p
     te.logp[i] = on ? d * p.inv_tau - ln : 0.f;
   }
   __syncwarp();
-  // repeated ids (rare) are found by hashing, summed in order
-  bool again = false;
+  // repeated ids (rare) are found by hashing; the warp sums each one's entries
+  // in order (loss and gradient, 64 rows of 131072, k 128, one in a few rows: 12
+  // us; where a lane went through the list for each of its entries 41)
+  uint32_t again = 0;  // this lane's entries, one bit each
   for (int i = lane; i < p.k; i += 32) {
     const int id = te.id()[i];
     te.sum[i] = te.p[i];
@@ -199,26 +201,32 @@ __device__ __forceinline__ void list_softmax(Teacher &te, const DistillParams &p
     static_assert(DISTILL_MAX_K * 2 == 1 << (32 - 23), "the hash fills the table");
     for (;;) {
       const int old = atomicCAS(&seen[h], -1, id);
-      again |= old == id;
+      if (old == id) again |= 1u << (i >> 5);
       if (old == -1 || old == id) break;
       h = (h + 1) % (2 * DISTILL_MAX_K);
     }
   }
-  if (!__any_sync(0xFFFFFFFFu, again)) return;
-  for (int i = lane; i < p.k; i += 32) {
-    const int id = te.id()[i];
-    float s = 0.f;
-    for (int o = 0; o < p.k; ++o) {
-      if (te.id()[o] != id) continue;
-      if (o < i) {
-        s = -1.f;
-        break;
+  if (!__any_sync(0xFFFFFFFFu, again != 0)) return;
+  for (int i0 = 0; i0 < p.k; i0 += 32) {
+    uint32_t found = __ballot_sync(0xFFFFFFFFu, again >> (i0 >> 5) & 1);
+    while (found) {
+      const int i = i0 + __ffs(found) - 1, id = te.id()[i];
+      found &= found - 1;
+      if (te.sum[i] == -1.f) continue;  // (summed with another of its entries)
+      float s = 0.f;
+      int first = -1;
+      for (int o = lane; o - lane < p.k; o += 32) {
+        const bool same = o < p.k && te.id()[o] == id;
+        uint32_t m = __ballot_sync(0xFFFFFFFFu, same);
+        if (first < 0 && m) first = o - lane + __ffs(m) - 1;
+        for (; m; m &= m - 1) s += te.p[o - lane + __ffs(m) - 1];
+        if (same) te.sum[o] = -1.f;
       }
-      s += te.p[o];
+      __syncwarp();
+      if (lane == 0) te.sum[first] = s;
+      __syncwarp();
     }
-    te.sum[i] = s;
   }
-  __syncwarp();
 }
 
 // The row's loss and statistics, by the same warp: m, l the maximum and the

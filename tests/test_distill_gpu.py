@@ -222,6 +222,20 @@ def test_repeated_and_out_of_range_ids():
     assert verify(z, ids, t, w, 1.0, "f32") == -5
 
 
+@pytest.mark.parametrize("T,V,k,dtype", [(9, 40, 256, "f32"), (7, 300, 256, "bf16"),
+                                         (5, 3000, 130, "f32"), (310, 3000, 97, "bf16"),
+                                         (6, 20000, 256, "bf16")])
+def test_many_repeated_ids(T, V, k, dtype):
+    """Lists in which most ids occur several times, in one group of 32 entries and across groups,
+    one list of a single id, one of a single id but for unused entries."""
+    z, _, t, w = inputs(T, V, k, dtype, T + V + k)
+    g = gen(T * k)
+    ids = torch.randint(0, min(V, k // 3), (T, k), generator=g).int()
+    ids[1] = V - 1
+    ids[2] = torch.where(torch.arange(k) % 3 == 1, 5, -1).int()
+    assert verify(z, ids, t, w, 1.3, dtype) == 0
+
+
 def test_gradient_against_differences():
     """Central differences of the summed loss in 64 bits, step h: the third derivative of the loss
     is below w tau^2 / tau^3, its h^2 / 6 below 1e-9; and the kernel's fp32 bound."""
