@@ -36,9 +36,12 @@ constexpr int ROWS_N = 4;    // weight rows a warp reads together
 
 // A group of KS warps takes ROWS_N weight rows and splits K; MT rows of a
 // (M <= MT) are read again by every warp, from L1.  Sums are integers, so
-// the split leaves no trace.
+// the split leaves no trace.  Loads in flight bound it: four CTAs an SM and two
+// steps ahead for one or two rows, two and four for more (1 x 14336 x 4096 11.8
+// us, and 13.4 where the compiler took fewer registers; 4 x 14336 x 16384 42 us,
+// three CTAs and two steps 54).
 template <typename E, int MT>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, MT <= 2 ? 4 : 2)
 q8_rows_kernel(const int8_t *a, const int8_t *w, const float *sa, const float *sw,
                const float *bias, int M, int N, int K, int ks, E *y) {
   pdl_begin();
@@ -56,7 +59,8 @@ q8_rows_kernel(const int8_t *a, const int8_t *w, const float *sa, const float *s
 #pragma unroll
     for (int r = 0; r < ROWS_N; ++r)
       wr[r] = (const uint4 *)w + (size_t)min(n0 + r, N - 1) * nv;
-#pragma unroll 2
+    constexpr int STEPS = MT <= 2 ? 2 : 4;
+#pragma unroll STEPS
     for (int v = part * 32 + lane; v < nv; v += ks * 32) {
       uint4 x[ROWS_N];
 #pragma unroll
@@ -1257,9 +1261,9 @@ cudaError_t frag_t(const Q8Args &a, cudaStream_t s) {
 // 2048 x 2048 | 8192 x 2048 | 4096 x 4096 | 8192 x 4096 | 14336 x 4096 | 50001 x
 // 2048 | 14336 x 16384 (weights from HBM; the floors, N x K bytes, are 0.6 | 2.5 |
 // 2.5 | 4.9 | 8.6 | 15 | 35):
-//   M 1    rows 2.4 | 5.1 | 5.1 | 8.4 | 13.5 | 21.6 | 46
+//   M 1    rows 2.4 | 4.5 | 4.6 | 7.3 | 11.8 | 19.0 | 41
 //          few  7.8 | 9.7 | 10.0 | 12.8 | 15.1 | 24.1 | 43
-//   M 4    rows 2.9 | 7.1 | 7.4 | 11.1 | 12.4 | 24.7 | 54
+//   M 4    rows 3.1 | 6.8 | 6.9 | 9.1 | 13.1 | 22.2 | 42
 //          few  7.9 | 9.7 | 10.1 | 12.8 | 15.1 | 23.5 | 43
 //   M 8    frag 4.0 | 6.6 | 7.3 | 10.7 | 16.8 | 24.3 | 64
 //          few  7.9 | 9.8 | 10.3 | 12.6 | 15.5 | 23.7 | 43
