@@ -143,7 +143,7 @@ __device__ __forceinline__ void widen_words(const uint4 &v, uint32_t (&o)[8]) {
 }
 
 template <typename E, int NT, int MT, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32)
+__global__ void __launch_bounds__(WARPS * 32, 2)
 q8_frag_kernel(const uint4 *a, const int8_t *w, const float *sa, const float *sw,
                const float *bias, int M, int N, int K, int ks, E *y) {
   pdl_begin();
@@ -1265,11 +1265,11 @@ cudaError_t frag_t(const Q8Args &a, cudaStream_t s) {
 //          few  7.8 | 9.7 | 10.0 | 12.8 | 15.1 | 24.1 | 43
 //   M 4    rows 3.1 | 6.8 | 6.9 | 9.1 | 13.1 | 22.2 | 42
 //          few  7.9 | 9.7 | 10.1 | 12.8 | 15.1 | 23.5 | 43
-//   M 8    frag 4.0 | 6.6 | 7.3 | 10.7 | 16.8 | 24.3 | 64
+//   M 8    frag 3.6 | 6.4 | 7.0 | 10.4 | 16.8 | 24.3 | 64
 //          few  7.9 | 9.8 | 10.3 | 12.6 | 15.5 | 23.7 | 43
-//   M 16   frag 4.9 | 8.4 | 9.2 | 13.5 | 18.0 | 33.0 | 61
+//   M 16   frag 4.3 | 8.6 | 8.1 | 12.8 | 18.0 | 33.0 | 61
 //          few  8.1 | 9.9 | 10.5 | 12.9 | 15.5 | 24.2 | 44
-//   M 32   frag 5.7 | 12.5 | 11.3 | 20.6 | 36.5 | 68 | 151
+//   M 32   frag 5.3 | 12.5 | 11.3 | 20.6 | 36.5 | 68 | 151
 //          few  8.6 | 10.1 | 11.0 | 13.5 | 15.4 | 24.2 | 45
 //   M 64   few  9.8 | 10.8 | 12.5 | 13.9 | 16.5 | 25.5 | 49
 //          pair 12.3 | 14.3 | 19.8 | 21.2 | 26.7 | 39.4 | 80
