@@ -1276,12 +1276,16 @@ cudaError_t frag_t(const Q8Args &a, cudaStream_t s) {
 //   M 128  few  12.6 | 12.7 | 15.5 | 16.9 | 19.1 | 31.5 | 58
 //          pair 12.2 | 14.8 | 20.1 | 21.8 | 28.0 | 43.0 | 82
 // (Up to four rows stay with the simplest kernel.  Columns count too: 17 to 32
-// rows of 50001 x 256 take the fragments 16 to 18 us, few 10.5.)
+// rows of 50001 x 256 take the fragments 16 to 18 us, few 10.5.  And 33 to 64
+// rows at 1000 x 1024 | 2048 x 2048 | 4096 x 2048 | 2048 x 4096 | 8192 x 1024: 48
+// rows in fragments 3.9 | 6.4 | 8.6 | 10.0 | 10.6, few 6.8 | 9.3 | 10.4 | 10.7 |
+// 8.4; 64 rows 4.9 | 7.5 | 10.5 | 11.9 | 12.9 and 7.0 | 9.9 | 11.0 | 11.3 | 8.6.)
 bool in_fragments(int M, int N, int K) {
   const long long bytes = (long long)N * K;
   return M <= 8    ? bytes < 3ll << 24
          : M <= 16 ? bytes < 1ll << 25
-                   : M <= 32 && N <= 8192 && bytes < 1ll << 24;
+         : M <= 32 ? N <= 8192 && bytes < 1ll << 24
+                   : M <= 64 && N <= 4096 && bytes <= 1ll << 23;
 }
 
 template <typename E>
@@ -1292,7 +1296,9 @@ cudaError_t matmul_t(const Q8Args &a, cudaStream_t s) {
   if (in_fragments(a.M, a.N, a.K))
     return a.M <= 8    ? frag_t<E, 1>(a, s)
            : a.M <= 16 ? frag_t<E, 2>(a, s)
-                       : frag_mt<E, 4, 1>(a, s);
+           : a.M <= 32 ? frag_mt<E, 4, 1>(a, s)
+           : a.M <= 48 ? frag_mt<E, 6, 1>(a, s)
+                       : frag_mt<E, 8, 1>(a, s);
   return a.M <= FEW_MOST ? few_t<E>(a, s) : mma_t<E>(a, s);
 }
 

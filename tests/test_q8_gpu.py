@@ -167,6 +167,14 @@ def test_few_rows(M, N, K, dtype, bias):
     verify(a, w, sa, sw, b if bias else None, dtype)
 
 
+@pytest.mark.parametrize("M,N,K", [(33, 1000, 1024), (48, 4096, 2048), (49, 301, 2064),
+                                   (63, 4095, 1040), (64, 128, 64), (64, 4097, 528)])
+def test_fragments_of_many_rows(M, N, K):
+    """33 to 64 rows of small weights, up to where they leave the fragments."""
+    a, w, sa, sw, b = inputs(M, N, K, M + N + K)
+    verify(a, w, sa, sw, b, "bf16")
+
+
 TIMEOUT_CHILD = """
 import sys
 import torch
