@@ -8,10 +8,11 @@ Besides the product library, two variants of the same sources serve the tests
 and the benchmark only (they are never loaded by the Python binding's
 entry points):
 
-* ``libtwell_hooks.so`` -- adds two measurement hooks (``TWELL_TEST_HOOKS``):
+* ``libtwell_hooks.so`` -- adds three hooks (``TWELL_TEST_HOOKS``):
   the tensor-core GEMM engine with a plain fp32 epilogue, and the random-row
-  gather probe that the benchmark reads the gather kernels against.
-* ``libtwell_timeout.so`` -- the pipeline waits of the tensor-core kernels
+  gather probe that the benchmark reads the gather kernels against; and a count
+  of CTA pairs that end before their last commits have arrived.
+* ``libtwell_timeout.so`` -- the same hooks of the kernels, and the pipeline waits of the tensor-core kernels
   limited to 1 ns, so that every wait that is not satisfied at once runs out
   on a sane input and the timeout path (status, drain, exit) can be tested
   without a fault.
@@ -41,7 +42,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 VARIANTS = {
     "": ("libtwell.so", [], []),
     "hooks": ("libtwell_hooks.so", ["probe.cu"], ["-DTWELL_TEST_HOOKS"]),
-    "timeout": ("libtwell_timeout.so", [], ["-DTWELL_WAIT_LIMIT_NS=1ull"]),
+    "timeout": ("libtwell_timeout.so", [], ["-DTWELL_WAIT_LIMIT_NS=1ull", "-DTWELL_TEST_HOOKS"]),
 }
 LIB = os.path.join(PKG, VARIANTS[""][0])
 # Python's argument marshalling of the operators around the FFN (csrc/lm_bind.cpp), a CPython

@@ -24,6 +24,7 @@
 #include "common.cuh"
 #include "lm_kernels.h"
 #include "tcgen05.cuh"
+#include "test_hooks.h"
 #include "vec16.cuh"
 
 namespace twell {
@@ -424,7 +425,8 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 // No copy may be in flight when the CTA exits: waits (bounded) for the last
 // load that was issued into each stage of a ring.  That the issuing warp has
 // come to its end does not say that the loads were waited for: another role may
-// have given up since.
+// have given up since.  (So for commits, where `full` are the barriers at which
+// they arrive.)
 __device__ __forceinline__ void drain_ring(uint32_t full, int S, long issued) {
   for (int s = 0; s < S && s < issued; ++s) {
     const uint32_t par = (uint32_t)(((issued - 1 - s) / S) & 1);
@@ -433,6 +435,17 @@ __device__ __forceinline__ void drain_ring(uint32_t full, int S, long issued) {
     }
   }
 }
+
+#ifdef TWELL_TEST_HOOKS
+// CTAs of pairs that have ended, and those among them that left while an
+// arrival at one of their barriers was still to come.
+__device__ unsigned test_pairs[2];
+__device__ __forceinline__ bool ring_drained(uint32_t full, int S, long issued) {
+  for (int s = 0; s < S && s < issued; ++s)
+    if (!mbar_test(full + 8 * s, (uint32_t)(((issued - 1 - s) / S) & 1))) return false;
+  return true;
+}
+#endif
 
 // Address part of the swizzled operand descriptors (sw128_desc): adding to
 // the low word moves the start, 16 bytes a unit.
@@ -483,6 +496,7 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
   __shared__ uint64_t bars[2 * AS + 3 * WS + 2 * RS + 5];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
+  __shared__ uint32_t s_committed[2];  // k-blocks and tiles that the leader has committed
   volatile int *abort_flag = &s_abort;
   const uint32_t afull = smem_u32(bars), aempty = afull + 8 * AS;
   const uint32_t wfull = aempty + 8 * AS, wempty = wfull + 8 * WS, ready = wempty + 8 * WS;
@@ -583,6 +597,7 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
       int lt = 0;
       bool ok = true;
       int seen = 0;
+      uint32_t blocks = 0, done = 0;  // committed k-blocks, tiles
       for (int t = unit; t < tiles && ok; t += units, ++lt) {
         const int buf = lt & 1;
         ok = warp_wait(tempty + 8 * buf, ((uint32_t)(lt >> 1) & 1) ^ 1, abort_flag, p.status);
@@ -608,16 +623,18 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
             mma_commit_to<true>(a_free);
             mma_commit_to<true>(w_free);
           }
+          ++blocks;
           __syncwarp();
         }
         if (!ok) break;
         if (issues) mma_commit_to<true>(tfull + 8 * buf);
+        ++done;
         __syncwarp();
       }
-      // all MMAs issued by this thread are complete before TMEM is freed
       if (issues) mma_commit_to<true>(mma_done);
-      const uint64_t t0 = global_timer();
-      while (!mbar_try(mma_done, 0) && global_timer() - t0 < DRAIN_LIMIT_NS) {
+      if (lane < 2) {  // (read behind the cluster's barrier)
+        st_cluster(cluster_addr(smem_u32(s_committed), lane), blocks);
+        st_cluster(cluster_addr(smem_u32(s_committed + 1), lane), done);
       }
     }
   } else if (warp < 6) {
@@ -664,12 +681,26 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
     }
   }
 
-  // neither CTA of a pair leaves while the other may reach its shared memory
-  // or TMEM
+  // Neither CTA of a pair leaves while something may still reach its shared
+  // memory or TMEM.  The other's threads: the barrier.  The leader's MMAs, which
+  // read both CTAs, and its commits, which arrive in both: each CTA waits
+  // (bounded) for the last arrival at each of its own barriers that take commits,
+  // also where roles have given up, which is why their number is passed on.
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();
   if (warp == 1) {
+    const long blocks = s_committed[0], done = s_committed[1];
+    drain_ring(mma_done, 1, 1);
+    drain_ring(aempty, AS, blocks);
+    drain_ring(wempty, WS, blocks);
+    drain_ring(tfull, 2, done);
+#ifdef TWELL_TEST_HOOKS
+    if (lane == 0 && (!ring_drained(mma_done, 1, 1) || !ring_drained(aempty, AS, blocks) ||
+                      !ring_drained(wempty, WS, blocks) || !ring_drained(tfull, 2, done)))
+      atomicAdd(&test_pairs[1], 1u);
+    if (lane == 0) atomicAdd(&test_pairs[0], 1u);
+#endif
     tc_fence_after();
     tmem_free<true>(tmem, 2 * ACC_COLS);
   }
@@ -1316,3 +1347,16 @@ cudaError_t launch_q8_matmul(const Q8Args &a, cudaStream_t s) {
 }
 
 }  // namespace twell
+
+#ifdef TWELL_TEST_HOOKS
+extern "C" int twell_test_q8_pairs(unsigned *ended, unsigned *early) {
+  unsigned n[2] = {0, 0};
+  const unsigned zero[2] = {0, 0};
+  if (cudaMemcpyFromSymbol(n, twell::test_pairs, sizeof(n)) != cudaSuccess ||
+      cudaMemcpyToSymbol(twell::test_pairs, zero, sizeof(zero)) != cudaSuccess)
+    return TWELL_ERR_CUDA;
+  *ended = n[0];
+  *early = n[1];
+  return TWELL_OK;
+}
+#endif

@@ -145,6 +145,9 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
+__device__ __forceinline__ void st_cluster(uint32_t cluster_ptr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_ptr), "r"(v) : "memory");
+}
 // Arrival at another CTA's barrier.  It releases no memory across the cluster
 // (that costs a fence of about 2000 cycles): what it announces are operands
 // which the MMA reads through the async proxy of the SM that holds them,

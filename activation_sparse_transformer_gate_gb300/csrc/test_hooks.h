@@ -13,6 +13,11 @@
 // row count of W, checked by the caller) of row_bytes each from W with
 // `blocks` CTAs of 256 threads; out receives blocks * 8 checksums.
 // Asynchronous on stream.
+//
+// twell_test_q8_pairs: CTAs of the 8-bit product over CTA pairs that have ended
+// since the last call, and those among them that ended before the last arrival at
+// one of their barriers.  Synchronises the device; compiled into both test-only
+// variants.
 #pragma once
 #include <stdint.h>
 #ifdef __cplusplus
@@ -22,6 +27,7 @@ int twell_test_tc_gemm(const void *A, const void *B, float *C, int M, int N, int
                        int32_t *status, void *stream);
 int twell_test_gather_probe(const void *W, int row_bytes, const int32_t *rows, int n_rows,
                             int blocks, uint32_t *out, void *stream);
+int twell_test_q8_pairs(unsigned *ended, unsigned *early);
 #ifdef __cplusplus
 }
 #endif
