@@ -163,7 +163,8 @@ __device__ __forceinline__ bool load_list(Teacher &te, const DistillParams &p, c
     any |= id >= 0;
   }
   for (int i = lane; i < DISTILL_MAX_K / 2; i += 32) te.seen4[i] = make_int4(-1, -1, -1, -1);
-  return __any_sync(0xFFFFFFFFu, any);  // (orders the list before its readers)
+  __syncwarp();  // the list and the table before their readers (a vote orders no memory)
+  return __any_sync(0xFFFFFFFFu, any);
 }
 
 // Its softmax, and for each id its first entry's sum, by the same warp.
@@ -207,12 +208,14 @@ __device__ __forceinline__ void list_softmax(Teacher &te, const DistillParams &p
     }
   }
   if (!__any_sync(0xFFFFFFFFu, again != 0)) return;
+  __syncwarp();  // the lanes' sums before the other lanes read and change them
   for (int i0 = 0; i0 < p.k; i0 += 32) {
     uint32_t found = __ballot_sync(0xFFFFFFFFu, again >> (i0 >> 5) & 1);
     while (found) {
       const int i = i0 + __ffs(found) - 1, id = te.id()[i];
       found &= found - 1;
       if (te.sum[i] == -1.f) continue;  // (summed with another of its entries)
+      __syncwarp();                     // (all have read it)
       float s = 0.f;
       int first = -1;
       for (int o = lane; o - lane < p.k; o += 32) {

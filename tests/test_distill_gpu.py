@@ -269,3 +269,19 @@ def test_other_stream_and_graph():
     torch.cuda.synchronize()
     for a, b in zip((loss, stats, dz), want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("V,dtype", [(97, "f32"), (4200, "bf16")])
+def test_one_id_twice_in_any_two_places(V, dtype):
+    """A row for every two of 66 places: the id at both has one sum, kept at the first."""
+    k = 66
+    first, second = torch.triu_indices(k, k, offset=1)
+    T = len(first)
+    z, _, t, w = inputs(T, V, k, dtype, V)
+    ids = torch.arange(k, dtype=torch.int32).repeat(T, 1)
+    ids[torch.arange(T), second] = first.int()
+    assert verify(z, ids, t, w, 1.0, dtype) == 0
+    a = run(z, ids, t, w, 1.0, dtype)
+    for _ in range(20):
+        for u, v in zip(run(z, ids, t, w, 1.0, dtype)[:3], a):
+            assert torch.equal(u, v)
