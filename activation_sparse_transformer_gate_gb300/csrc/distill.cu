@@ -21,9 +21,10 @@
 //
 // Exponentials are 2^(z c - ref), c = log2(e) / tau, one fma before the ex2:
 // ref is max z * c rounded, and as the same ref stands in the sum and in the
-// gradient, its rounding cancels.  Where the maximum is so large that z c
-// would overflow (rows masked with the type's lowest value and nothing else),
-// the difference z - max z is taken first.
+// gradient, its rounding cancels.  Where the maximum is so large that this
+// rounding is no longer a fraction of a power of two, or z c would overflow (rows
+// masked with a huge negative value and nothing else), the difference z - max z is
+// taken first.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -50,11 +51,13 @@ __device__ __forceinline__ float ex2(float v) {
 // m are taken against.
 struct Ref {
   float m, mc;  // m (0 where everything is -inf), and max * c rounded
-  bool wide;    // z c may overflow beside it
+  bool wide;    // taken against m itself instead of mc
   __device__ __forceinline__ Ref(float max, float c) {
     m = max == -INFINITY ? 0.f : max;
     mc = __fmul_rn(max, c);  // (one rounding everywhere: not to be fused)
-    wide = !(fabsf(mc) < 1e30f);
+    // (below 2^24 the largest exponential is within 2^(1/2) of 1; from 2^32 on the
+    // rounding of mc alone could take it out of fp32's range)
+    wide = !(fabsf(mc) < 0x1p24f);
   }
   // log2 of an exponential against this reference
   __device__ __forceinline__ float operator()(float z, float c) const {
@@ -66,7 +69,9 @@ struct Ref {
 // multiplied by to count against `to`.
 __device__ __forceinline__ float rescale(float max, const Ref &to, float c) {
   const Ref from(max, c);
-  return ex2(from.wide || to.wide ? (max - to.m) * c : from.mc - to.mc);
+  // (one of each kind may be neighbours: max c and its rounding are told apart)
+  if (from.wide) return ex2(to.wide ? (max - to.m) * c : fmaf(max, c, -to.mc));
+  return ex2(to.wide ? fmaf(-to.m, c, from.mc) : from.mc - to.mc);
 }
 
 // (m, l) += (m2, l2): l counts exponentials against the reference of m.

@@ -285,3 +285,25 @@ def test_one_id_twice_in_any_two_places(V, dtype):
     for _ in range(20):
         for u, v in zip(run(z, ids, t, w, 1.0, dtype)[:3], a):
             assert torch.equal(u, v)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,rows", [(300, 12), (30011, 12), (6007, 312), (90001, 312)])
+@pytest.mark.parametrize("tau", [1.0, 0.5, 1e-3])
+def test_logits_of_any_size(dtype, V, rows, tau):
+    """Rows of one huge value of either sign (a mask and nothing else), rows of values that differ by
+    their last place there, huge values beside ordinary ones, and steps across the size from which
+    differences are taken first."""
+    z, ids, t, _ = inputs(rows, V, 6, dtype, V)
+    big = [1e6, 1.2e7, -1e9, 2.5e9, -1e10, 1e14, -1e20, 1e30]
+    for r, b in enumerate(big):
+        z[r] = b * tau
+    near = torch.tensor(2.0 ** 24 / 1.4426950408889634 * tau)
+    z[8] = near * (1 + (torch.arange(V) % 9 - 4) * 2.0 ** (-23 if dtype == "f32" else -7))
+    z[9] = -near * (1 + (torch.arange(V) % 9 - 4) * 2.0 ** (-23 if dtype == "f32" else -7))
+    z[10, ::3] = -1e9
+    z[11, ::3] = 1e9
+    for r in range(12):   # a teacher on what the student does not exclude: the row's largest
+        top = torch.nonzero(z[r] == z[r].max())[:, 0]
+        ids[r] = top[torch.arange(6) % len(top)].int()
+    assert verify(z, ids, t, None, tau, dtype) == 0
