@@ -11,6 +11,8 @@
 // warps that keep at most NV 16-byte vectors a lane.  max|y| = rstd max|s w|,
 // so the 8-bit output needs no second reduction.  16384 x 4096 bf16: forward
 // 78 us (6.9 TB/s), with 8 bits out 77, backward 81 (6.6 TB/s).
+#include <float.h>
+
 #include "common.cuh"
 #include "lm_kernels.h"
 #include "vec16.cuh"
@@ -143,7 +145,10 @@ rmsnorm_forward_kernel(const uint4 *x, const uint4 *res, const float *weight, in
   }
   reduce_row<W>(sum, top, s_sum, s_top, 0);
   if (!row_ok) return;
-  const float rstd = rsqrtf(sum * inv_d + eps);
+  // (below the normal range, which with eps 0 a row of zeros reaches, rstd is 0: y
+  // and the backward's terms are then 0 and not 0 * inf)
+  const float var = sum * inv_d + eps;
+  const float rstd = var < FLT_MIN ? 0.f : rsqrtf(var);
   // (rstd is NaN, or 0 with an infinite sum, when s has a NaN or infinity:
   // 0 * inf then makes the row's largest magnitude NaN too)
   const Q8Scale sc = q8_scale(__float_as_uint(fabsf(__uint_as_float(top) * rstd)));

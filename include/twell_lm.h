@@ -70,8 +70,9 @@ size_t twell_embed_workspace_size(int T, int V, int D);
  * 8-bit output: q [T][D] int8, qscale [T] fp32: qscale = max|y| / 127 over
  * the row, q = y / qscale rounded to nearest even, so y ~ q * qscale (y in
  * fp32, not rounded to dtype first).  A row of zeros has qscale 0; a row with
- * an infinity or NaN has q 0 and qscale NaN; a row whose sum of squares
- * leaves the fp32 range has y 0.
+ * an infinity or NaN has q 0 and qscale NaN.  A finite row whose mean(s^2) + eps
+ * leaves the normal fp32 range, upwards or (with eps below 2^-126, 0 among them)
+ * downwards, as a row of zeros does, has rstd 0, y 0, q 0 and qscale 0.
  * 16 <= D*elem_size <= 16384, a multiple of 16 (TWELL_BF16 with q: D a
  * multiple of 16). */
 twell_status twell_add_rmsnorm_forward(const void *x, const void *residual, const float *weight,

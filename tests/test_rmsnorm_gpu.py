@@ -207,3 +207,41 @@ def test_quantize(rows, cols, dtype):
             assert abs(sc[i].item() - top[i].item() / 127) <= 2 * U * top[i].item() / 127 + 2.0 ** -149
             off = (q[i].double().cpu() - a[i].double() * 127 / top[i]).abs().max().item()
             assert off <= 0.5 + 127 * 4 * U, (i, off)
+
+
+@pytest.mark.parametrize("D", [64, 2048, 4096])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_that_leave_the_range(dtype, D):
+    """Zeros and values whose squares vanish, with eps 0, and values whose squares overflow: rstd, y,
+    q and qscale are 0, the gradient is what reaches the sum past the norm, and the row leaves no
+    trace in the weight's gradient; the rows beside them are as ever."""
+    tdt = DT[dtype][0]
+    x = torch.randn(7, D, generator=gen(D))
+    x[1] = 0
+    x[2] *= 1e-30
+    x[3] = 0
+    x[3, 3] = 1e-38
+    x[4] = 2e19                    # (squares beyond fp32)
+    x[6] = -0.0
+    x = x.to(tdt)
+    w = 1 + 0.2 * torch.randn(D, generator=gen(2))
+    gone, ok = [1, 2, 3, 4, 6], [0, 5]
+    s, y, q, qs, r = forward(x, None, w, dtype, eps=0.0)
+    for v in (y, q, qs, r):
+        assert (v[gone] == 0).all()
+    rstd, yr = ref_norm(x, w, 0.0)
+    check(y[ok], yr[ok], 32 * U * yr[ok].abs(), dtype, "y")
+    check(r[ok], rstd[ok][:, 0], 32 * U * rstd[ok][:, 0], "f32", "rstd")
+    dy, ds = torch.randn(7, D, generator=gen(3)).to(tdt), torch.randn(7, D, generator=gen(4)).to(tdt)
+    dx, dw = backward(s, w, r, dy, ds, dtype)
+    assert torch.equal(dx.cpu()[gone], ds[gone])
+    # (dw: the sums of the two rows, in whatever order the zeros are added)
+    hat = x[ok].double() * r.double().cpu()[ok][:, None]
+    check(dw, (dy[ok].double() * hat).sum(0), (7 + 64) * U * (dy[ok].double() * hat).abs().sum(0),
+          "f32", "dw")
+    # with eps, zeros are zeros and the small rows count
+    _, y, q, qs, r = forward(x, None, w, dtype)
+    rstd, yr = ref_norm(x, w)
+    some = [0, 1, 2, 3, 5, 6]
+    check(y[some], yr[some], 32 * U * yr[some].abs(), dtype, "y")
+    assert (y[4] == 0).all() and qs[4] == 0 and qs[1] == 0 and (q[1] == 0).all()
