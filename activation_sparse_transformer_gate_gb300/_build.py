@@ -26,6 +26,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -48,6 +49,7 @@ LIB = os.path.join(PKG, VARIANTS[""][0])
 # Python's argument marshalling of the operators around the FFN (csrc/lm_bind.cpp), a CPython
 # extension against torch's headers, beside libtwell.so and linked to it
 BINDING = os.path.join(PKG, "_lm.so")
+STAMP = os.path.join(OBJDIR, "lib", "lm_bind.for")  # the Python and torch that it was built for
 
 
 def lib_path(variant: str = "") -> str:
@@ -82,11 +84,31 @@ def _jobs(variant: str):
             for src in SOURCES + extra_src], objdir, os.path.join(PKG, name)
 
 
-def _torch_dir() -> str:
+def _torch_dir() -> Optional[str]:
+    """Where the torch is that a binding can be built against; None without one, or without a C++
+    compiler (the C library needs only nvcc)."""
     spec = importlib.util.find_spec("torch")
-    if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("torch not found: its headers are required to build the binding")
-    return list(spec.submodule_search_locations)[0]
+    if spec is None or not spec.submodule_search_locations or not shutil.which("g++"):
+        return None
+    path = list(spec.submodule_search_locations)[0]
+    return path if os.path.exists(os.path.join(path, "lib", "libc10_cuda.so")) else None
+
+
+def _binding_tag(torch_dir: str) -> str:
+    """What a binding is good for: this Python and this torch."""
+    with open(os.path.join(torch_dir, "version.py"), encoding="utf-8") as f:
+        version = f.read()
+    return f"{sysconfig.get_config_var('SOABI')}\n{torch_dir}\n{version}"
+
+
+def _binding_stale() -> bool:
+    torch_dir = _torch_dir()
+    if torch_dir is None:
+        return False
+    if _stale(BINDING) or not os.path.exists(STAMP):
+        return True
+    with open(STAMP, encoding="utf-8") as f:
+        return f.read() != _binding_tag(torch_dir)
 
 
 def _binding_flags(torch_dir: str, nvcc: str):
@@ -101,7 +123,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), variants=(
     """Build the requested library variants ("" = libtwell.so); returns the
     path of the first one."""
     todo = [v for v in variants
-            if force or _stale(lib_path(v)) or (v == "" and _stale(BINDING))]
+            if force or _stale(lib_path(v)) or (v == "" and _binding_stale())]
     if not todo:
         return lib_path(variants[0])
     nvcc = nvcc_path()
@@ -129,9 +151,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), variants=(
         os.makedirs(objdir, exist_ok=True)
         plans.append((js, lib))
         jobs += js
-    torch_dir = _torch_dir()
+    torch_dir = _torch_dir() if "" in todo else None
     bind_obj = os.path.join(OBJDIR, "lib", "lm_bind.o")
-    if "" in todo:
+    if torch_dir:
         jobs.insert(0, ("lm_bind.cpp", bind_obj, _binding_flags(torch_dir, nvcc)))
     workers = max(1, min(len(jobs), os.cpu_count() or 8))
     with cf.ThreadPoolExecutor(max_workers=workers) as ex:
@@ -143,7 +165,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), variants=(
         if r.returncode != 0:
             raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, lib)
-    if "" in todo:
+    if torch_dir:
         tmp = BINDING + f".tmp{os.getpid()}"
         libs = os.path.join(torch_dir, "lib")
         cmd = ["g++", "-shared", "-o", tmp, bind_obj, "-L", PKG, "-l:libtwell.so", "-L", libs,
@@ -152,6 +174,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), variants=(
         if r.returncode != 0:
             raise RuntimeError(f"g++ link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, BINDING)
+        with open(STAMP, "w", encoding="utf-8") as f:
+            f.write(_binding_tag(torch_dir))
+    elif "" in todo:
+        print("no torch with CUDA, or no g++: the operators around the FFN have no Python binding",
+              file=sys.stderr)
     return lib_path(variants[0])
 
 
