@@ -438,6 +438,19 @@ distill_forward_kernel(const E *z, E *dz, DistillParams p, int cap) {
   const int per = (row.w1 - row.w0 + C - 1) / C;
   const int ja = min(row.w1, row.w0 + rank * per), jb = min(row.w1, ja + per);
   const bool first = rank == 0;
+  // a masked row (uniform for the cluster) is not read: the weight is looked at
+  // before the copies are issued, which costs the other rows nothing that shows
+  // (us, with it first | behind the copies: 148 x 131072 bf16 25.1 | 24.5, 64 x
+  // 131072 11.7 | 12.0; half the rows masked 17.0 | 19.3, 11.2 | 11.8)
+  const float w = p.w ? p.w[t] : 1.f;
+  if (w == 0.f) {
+    if (GRAD) store_zeros(row, out, ja, jb, first, blockDim.x);
+    if (first && threadIdx.x == 0) {
+      p.loss[t] = 0.f;
+      p.stats[t] = make_float2(0.f, 0.f);
+    }
+    return;
+  }
   // [ja, js) go to shared memory, asynchronously and in two parts, before
   // anything is waited for (js: where it ends; jh: a multiple of the streaming
   // threads from ja on)
@@ -452,16 +465,6 @@ distill_forward_kernel(const E *z, E *dz, DistillParams p, int cap) {
     asm volatile("cp.async.commit_group;" ::: "memory");
     for (int j = jh + (int)threadIdx.x; j < js; j += ST) copy16_async(slice + (j - ja), row.base + j, once);
     asm volatile("cp.async.commit_group;" ::: "memory");
-  }
-  const float w = p.w ? p.w[t] : 1.f;
-  if (w == 0.f) {  // a masked row (uniform for the cluster): its logits are not used
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (GRAD) store_zeros(row, out, ja, jb, first, blockDim.x);
-    if (first && threadIdx.x == 0) {
-      p.loss[t] = 0.f;
-      p.stats[t] = make_float2(0.f, 0.f);
-    }
-    return;
   }
   // (this CTA runs: its shared memory may be written by the others)
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");

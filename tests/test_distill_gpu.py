@@ -307,3 +307,23 @@ def test_logits_of_any_size(dtype, V, rows, tau):
         top = torch.nonzero(z[r] == z[r].max())[:, 0]
         ids[r] = top[torch.arange(6) % len(top)].int()
     assert verify(z, ids, t, None, tau, dtype) == 0
+
+
+@pytest.mark.parametrize("fused", [True, False])
+@pytest.mark.parametrize("T,V,ldz", [(9, 40001, 40001), (61, 20011, 20016), (300, 9001, 9001)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_masked_rows_of_long_rows(dtype, T, V, ldz, fused):
+    """Masked rows between others where a cluster has a row, in place too: zeros, whatever stood
+    there, and the others have the bits that they have beside rows that count."""
+    z, ids, t, w = inputs(T, V, 9, dtype, T)
+    rest = torch.arange(T) % 3 != 1
+    want = [a[rest] for a in run(z, ids, t, w, 1.0, dtype, ldz=ldz, fused=fused)[:3]]
+    z[~rest] = float("nan")
+    w[~rest] = 0
+    for in_place in (False, True):
+        got = run(z, ids, t, w, 1.0, dtype, ldz=ldz, fused=fused, in_place=in_place)
+        for a, b in zip(got[:3], want):
+            assert (a[~rest] == 0).all() and torch.equal(a[rest], b)
+    w[:] = 0
+    got = run(z, ids, t, w, 1.0, dtype, ldz=ldz, fused=fused)
+    assert all((a == 0).all() for a in got[:3])
