@@ -1309,14 +1309,21 @@ cudaError_t frag_t(const Q8Args &a, cudaStream_t s) {
 // (Up to four rows stay with the simplest kernel.  Columns count too: 17 to 32
 // rows of 50001 x 256 take the fragments 16 to 18 us, few 10.5.  And 33 to 64
 // rows at 1000 x 1024 | 2048 x 2048 | 4096 x 2048 | 2048 x 4096 | 8192 x 1024: 48
-// rows in fragments 3.9 | 6.4 | 8.6 | 10.0 | 10.6, few 6.8 | 9.3 | 10.4 | 10.7 |
-// 8.4; 64 rows 4.9 | 7.5 | 10.5 | 11.9 | 12.9 and 7.0 | 9.9 | 11.0 | 11.3 | 8.6.)
+// rows in fragments 3.9 | 6.5 | 8.6 | 10.1 | 10.7, few 6.9 | 9.2 | 10.5 | 10.8 |
+// 8.4; 64 rows 4.9 | 7.8 | 10.5 | 12.0 | 13.0 and 7.0 | 9.8 | 11.1 | 11.4 | 8.7.)
+// And k: at most eight warps of one CTA share it in the fragments, clusters of
+// eight CTAs in few.  N x K = 1000 x 3584 | 2048 x 8192 | 1000 x 8192 | 1000 x 16384 |
+// 128 x 65536, fragments and few: 8 rows 5.7 | 10.4 | 10.1 | 18.7 | 66 and 8.0 |
+// 11.3 | 9.6 | 11.6 | 22; 16 rows 6.1 | 11.2 | 10.9 | 19.5 | 71 and 7.9 | 11.5 | 9.8 |
+// 11.8 | 23; 32 rows 7.5 | 13.8 | 13.6 | 24.5 | 89 and 8.7 | 12.0 | 10.5 | 12.7 | 24;
+// 48 rows 9.1 | 16.6 | 16.3 | 29 | 107 and 9.5 | 12.9 | 11.5 | 13.8 | 26; 64 rows
+// 11.4 | 20.3 | 20.1 | 37 | 131 and 10.3 | 13.8 | 12.5 | 14.8 | 27.
 bool in_fragments(int M, int N, int K) {
   const long long bytes = (long long)N * K;
-  return M <= 8    ? bytes < 3ll << 24
-         : M <= 16 ? bytes < 1ll << 25
-         : M <= 32 ? N <= 8192 && bytes < 1ll << 24
-                   : M <= 64 && N <= 4096 && bytes <= 1ll << 23;
+  return M <= 8    ? K <= 8192 && bytes < 3ll << 24
+         : M <= 16 ? K <= 8192 && bytes < 1ll << 25
+         : M <= 32 ? K <= 4096 && N <= 8192 && bytes < 1ll << 24
+                   : M <= 64 && K <= (M <= 48 ? 4096 : 2048) && N <= 4096 && bytes <= 1ll << 23;
 }
 
 template <typename E>

@@ -133,3 +133,13 @@ def test_binding_checks_tensors(lib):
     assert code(A, A, A, 1 << 40, 128, tw.TWELL_F32, 1e-6, A, A, A, A, A) == ARG
     assert code(A, A, A, A, A, 64, 128, tw.TWELL_F32, A, A, torch.zeros(10), 1 << 20,
                 fn=tw.twell_add_rmsnorm_backward) == WS
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 1000, 16384), (8, 128, 65536), (16, 512, 16384),
+                                   (32, 1000, 8192), (48, 1024, 8192), (64, 1024, 8192),
+                                   (64, 2048, 4096), (64, 128, 65536)])
+def test_long_sums_of_few_columns_leave_the_fragments(lib, M, N, K):
+    """Few columns with a long k are multiplied where clusters share k, which needs the widened rows
+    of a as scratch."""
+    assert tw.twell_q8_workspace_size(M, N, K) >= M * K * 2
+    assert tw.twell_q8_workspace_size(M, N, 1024) == 0

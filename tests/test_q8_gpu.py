@@ -175,6 +175,15 @@ def test_fragments_of_many_rows(M, N, K):
     verify(a, w, sa, sw, b, "bf16")
 
 
+@pytest.mark.parametrize("M,N,K", [(5, 130, 16384), (16, 257, 8208), (17, 1000, 8192),
+                                   (33, 128, 4112), (48, 300, 16384), (49, 1000, 2064),
+                                   (64, 1024, 8192), (64, 100, 65536)])
+def test_long_sums_of_few_columns(M, N, K):
+    """Where few columns leave the fragments for their long k."""
+    a, w, sa, sw, b = inputs(M, N, K, M + N + K)
+    verify(a, w, sa, sw, b, "f32")
+
+
 TIMEOUT_CHILD = """
 import sys
 import torch
