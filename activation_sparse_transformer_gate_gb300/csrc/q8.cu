@@ -619,19 +619,19 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
           if (issues) {
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk)
-              mma_f16<true>(acc, ad + 2 * kk, wd + 2 * kk, idesc, (kt > 0 || kk > 0) ? 1u : 0u);
-            mma_commit_to<true>(a_free);
-            mma_commit_to<true>(w_free);
+              mma_f16_pair(acc, ad + 2 * kk, wd + 2 * kk, idesc, (kt > 0 || kk > 0) ? 1u : 0u);
+            mma_commit_pair(a_free);
+            mma_commit_pair(w_free);
           }
           ++blocks;
           __syncwarp();
         }
         if (!ok) break;
-        if (issues) mma_commit_to<true>(tfull + 8 * buf);
+        if (issues) mma_commit_pair(tfull + 8 * buf);
         ++done;
         __syncwarp();
       }
-      if (issues) mma_commit_to<true>(mma_done);
+      if (issues) mma_commit_pair(mma_done);
       if (lane < 2) {  // (read behind the cluster's barrier)
         st_cluster(cluster_addr(smem_u32(s_committed), lane), blocks);
         st_cluster(cluster_addr(smem_u32(s_committed + 1), lane), done);

@@ -156,27 +156,17 @@ __device__ __forceinline__ void st_cluster(uint32_t cluster_ptr, uint32_t v) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
-// fp16 operands; PAIR: over both CTAs' shared memory and TMEM.
-template <bool PAIR>
-__device__ __forceinline__ void mma_f16(uint32_t dtmem, uint64_t adesc, uint64_t bdesc,
-                                        uint32_t idesc, uint32_t accumulate) {
-  if (!PAIR) {
-    mma_bf16(dtmem, adesc, bdesc, idesc, accumulate);  // (the types are the descriptor's)
-    return;
-  }
+// fp16 operands over both CTAs' shared memory and TMEM.
+__device__ __forceinline__ void mma_f16_pair(uint32_t dtmem, uint64_t adesc, uint64_t bdesc,
+                                             uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(dtmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// PAIR: arrives at `bar` in both CTAs.
-template <bool PAIR>
-__device__ __forceinline__ void mma_commit_to(uint32_t bar) {
-  if (!PAIR) {
-    mma_commit(bar);
-    return;
-  }
+// Arrives at `bar` in both CTAs.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
       " [%0], %1;" ::"r"(bar),
