@@ -551,10 +551,10 @@ distill_forward_kernel(const E *z, E *dz, DistillParams p, int cap) {
 // Many rows: a CTA each, and with the gradient two streamed passes, the second
 // one's reads from L2: at most 1024 streaming threads an SM keep 304 of the
 // longest rows in flight (80 MB at 131072 bf16 logits; L2 has 126), and the
-// first pass asks L2 to keep what it reads until the second has read it
-// (0.80 against 0.85 ms).  8192 x 131072, k 128: 0.77 ms, 5.5 TB/s, where the
-// cluster kernel below 2 CTAs an SM takes 1.10 ms: its CTAs stand still
-// between reading and writing, and three of them an SM do not cover that.
+// first pass asks L2 to keep what it reads until the second has read it (206.5
+// against 208 us at 2048 x 131072).  8192 x 131072, k 128: 0.75 ms, 5.7 TB/s, where
+// the cluster kernel takes 1.04 ms: its CTAs stand still between reading and
+// writing, and three of them an SM do not cover that.
 template <typename E, int ROW_WARPS, bool GRAD>
 __global__ void __launch_bounds__(32 * ROW_WARPS + 32, 1024 / (32 * ROW_WARPS))
 distill_row_kernel(const E *z, E *dz, DistillParams p) {
@@ -750,7 +750,8 @@ DistillParams params_of(const DistillArgs &a) {
 }
 
 // Slices of at most 108 KB let two CTAs share an SM, so that one loads while
-// the other writes.
+// the other writes (290 rows of 131072 | 200000 bf16 logits, us: 54 KB 45.1 | 68.5,
+// 108 KB 43.4 | 67.2, 200 KB 59 | 82).
 constexpr int SLICE_VECS = 108 * 1024 / 16, SLICE_MAX = 200 * 1024 / 16;
 
 template <typename E, int PASS>
@@ -775,10 +776,17 @@ template <typename E, bool GRAD>
 cudaError_t forward_t(const DistillArgs &a, cudaStream_t s) {
   if (a.V / VEC16<E> <= SHORT_VECS) return short_t<E, GRAD ? LOSS_GRAD : LOSS>(a, s);
   const int nvec = (int)((size_t)a.V / VEC16<E>);  // at most so many whole vectors
-  // Streaming warps of a CTA, us at 8192 rows of 5001 | 12000 | 32000 | 80000 |
-  // 131072 logits: 4 warps 53 | 101 | 233 | 642 | 1072; 8 warps 80 | 144 | 215 |
-  // 616 | 1057; 16 warps 133 | 214 | 275 | 486 | 851 (cluster kernel: 89 | - |
-  // 240 | - | 1126).
+  // Streaming warps of a CTA, with the gradient, us at 8192 rows of 5001 | 12000 |
+  // 32000 | 50001 | 80000 | 131072 bf16 logits, k 64: 4 warps 58 | 96 | 210 | 346 | 653
+  // | 1072; 8 warps 88 | 118 | 206 | 280 | 536 | 1034; 16 warps 159 | 181 | 259 | 339 |
+  // 472 | 743 (cluster kernel 102 | 139 | 263 | 413 | 706 | 1041).  The loss alone: 4
+  // warps 39 | 52 | 87 | 123 | 203 | 327; 8 warps 56 | 67 | 99 | 133 | 205 | 325; 16 warps
+  // 124 | 132 | 167 | 204 | 246 | 326 (cluster kernel 81 | 94 | 119 | 146 | 214 | 330): it
+  // takes the same widths, which are not its best from 12000 to 100000 logits.
+  // By rows, us at 5001 | 32000 | 131072 logits, cluster kernel and this rule's width:
+  // 76 rows 6.9 | 7.5 | 15 and 6.0 | 8.2 | 17; 152 rows 6.7 | 8.2 | 26 and 6.5 | 8.4 | 17.5;
+  // 256 rows 7.0 | 11.7 | 37 and 6.7 | 11.7 | 34; 304 rows 7.2 | 12.1 | 45 and 6.7 | 11.7 |
+  // 37; 608 rows 8.8 | 22 | 84 and 7.4 | 18 | 73.
   if (a.T >= 2 * num_sms())
     return nvec <= 2048   ? row_t<E, 4, GRAD>(a, s)
            : nvec <= 7680 ? row_t<E, 8, GRAD>(a, s)
@@ -786,7 +794,9 @@ cudaError_t forward_t(const DistillArgs &a, cudaStream_t s) {
   int C = 1;
   if (GRAD)
     while (C < MAX_CLUSTER && (nvec + C - 1) / C > SLICE_VECS) C *= 2;
-  // few rows: split them until every SM has two CTAs or a slice is 16 KB
+  // few rows: split them until every SM has two CTAs or a slice is 16 KB (64 rows
+  // of 50001, us: slices of 4 to 16 KB 8.8, 32 KB 7.4, 64 KB 7.8; one CTA an SM 7.3, four
+  // 8.7; 64 and 148 rows of 131072 are the same within 2% throughout)
   while (C < MAX_CLUSTER && (long long)a.T * C < 2 * num_sms() && nvec / C >= 1024) C *= 2;
   const int per = (nvec + C - 1) / C;
   // (without a gradient: the ring of each streaming thread)
@@ -807,7 +817,10 @@ cudaError_t backward_t(const DistillArgs &a, cudaStream_t s) {
   if (a.V / VEC16<E> <= SHORT_VECS) return short_t<E, GRAD_ONLY>(a, s);
   const int nvec = a.V / VEC16<E>;
   // whole rows (the list is worked through once), in slabs of at least 1024
-  // vectors while there are not four CTAs an SM
+  // vectors while there are not four CTAs an SM (us, two | four | eight: 8 x 131072
+  // 4.5 | 4.5 | 4.6, 64 x 131072 7.8 | 10.5 | 10.2, 300 x 50001 11.1 | 13.5 | 13.5, 600 x
+  // 131072 53.8 | 52.3 | 52.0, 2048 x 50001 70 | 70 | 70; slabs of at least 512 and 2048
+  // vectors: 8 x 50001 4.3 and 5.2, here 4.5)
   int slabs = 1;
   while ((long long)a.T * slabs < 4 * num_sms() && nvec / (2 * slabs) >= 1024) slabs *= 2;
   const int slab_vecs = (nvec + slabs - 1) / slabs;

@@ -8,16 +8,18 @@
 //
 // By the rows of a (matmul_t has the rule and the measurements):
 //   a decoded row or four   q8_rows_kernel: dp4a, exact int32 sums
-//   a batch of them         q8_frag_kernel: the weights are widened in
-//                           registers and used up there (m16n8k16)
+//   a batch of them, small  q8_frag_kernel: the weights are widened in
+//   weights                 registers and used up there (m16n8k16)
 //   up to 128               q8_few_kernel: TMA brings 8-bit weights, warps
 //                           widen them into TMEM, where they are the M side
 //                           of tcgen05.mma; clusters share k
 //   more                    q8_mma_kernel: warps widen the weights into shared
 //                           memory, pairs of CTAs (cta_group::2) multiply
-// The first three are bound by the weights' bytes, the pairs by the tensor
-// cores: 8192 x 14336 x 4096 in 0.57 ms, 1.7 PFLOP/s with the launch that
-// widens a.
+// The rows kernel is bound by the weights' bytes, fragments by the widening of a
+// in every warp, few by its MMAs' reading of the weights from TMEM and by its start
+// (by the weights' bytes where all SMs have several tiles), the pairs by the tensor
+// cores: 8192 x 14336 x 4096 in 0.61 to 0.63 ms, 1.55 PFLOP/s under the power limit
+// with the launch that widens a.
 #include <cuda_fp16.h>
 #include <string.h>
 
@@ -124,7 +126,7 @@ __device__ __forceinline__ void widen16(const uint4 &v, uint4 &lo, uint4 &hi) {
 // row, which serve as its part of four MMAs' k (both operands take the same
 // order of k), and widens them in registers: rows of a again in every warp,
 // which is what bounds it from 32 rows on (reading them widened instead, from
-// L1, was slower: 47 against 33 us at 16 x 50001 x 2048).  A tile's KS warps
+// L1, was slower: 47 against 33 us at 16 x 50001 x 2048, a size that few has now).  A tile's KS warps
 // split K and are added in order through shared memory.
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -317,7 +319,7 @@ __device__ __forceinline__ void store_some(bf16 *dst, const uint32_t *w, int lo,
 // as many places as the row starts behind a 16-byte boundary, and the first and
 // the last few are stored alone, in the widest pieces.  (Stores count by
 // their number: 1001 x 50001 x 512, where rows of y start at odd elements and
-// the epilogue is all there is, takes 70 us, with 50000 columns 64; through
+// the epilogue is all there is, takes 71 us, with 50000 columns 65; through
 // shared memory, in words that a warp stores for one row, it took 118, and 1001
 // x 50001 x 2048 151 us instead of 144.)
 template <typename E>
@@ -714,11 +716,11 @@ q8_mma_kernel(const __grid_constant__ Q8Maps maps, const __grid_constant__ Q8Par
 // rows of a read for however few there are, a k-block of 64 for 96 columns moved
 // 57 KB through shared memory, which at its 128 bytes a cycle took the 420 cycles
 // that were measured (37 x 14336 x 4096: 20.2 us); here 128 k of 128 columns move
-// 52 KB and take 600 (15.4 us).
+// 52 KB and take 600 (16.3 us).
 //
 // A tile is 128 columns of y.  Where the tiles leave SMs idle, a cluster of ks
 // CTAs shares a tile's k and adds the parts through distributed shared memory,
-// each CTA for its share of the rows of a (37 x 2048 x 2048: 9.0 us).
+// each CTA for its share of the rows of a (100 x 2048 x 2048: 11.5 us).
 //
 // What is left above the weights' bytes: an MMA takes 75 cycles however few rows
 // of a there are (128 x 16 of w come from TMEM at about 64 bytes a cycle), 600
@@ -1282,8 +1284,11 @@ cudaError_t frag_mt(const Q8Args &a, cudaStream_t s) {
 
 template <typename E, int NT>
 cudaError_t frag_t(const Q8Args &a, cudaStream_t s) {
-  // 32 weight rows a warp where that leaves eight warps an SM (rows of a are
-  // widened half as often: 22.6 against 28.4 us at 1 x 50001 x 2048)
+  // 32 weight rows a warp where that leaves eight warps an SM: rows of a are
+  // widened half as often, in half as many warps (us, 16 and 32 weight rows, at
+  // 8192 x 2048 | 9728 x 2048 | 14336 x 2048 | 16000 x 1024 | 50001 x 512: 8 rows 6.3 |
+  // 7.1 | 8.8 | 6.6 | 9.6 and 7.6 | 8.0 | 9.0 | 6.4 | 8.8; 16 rows 8.6 | 8.5 | 11.1 |
+  // 9.1 | 12.6 and 9.0 | 9.3 | 10.6 | 7.6 | 13.9: the two cross about there)
   return a.N >= 64 * num_sms() ? frag_mt<E, NT, 2>(a, s) : frag_mt<E, NT, 1>(a, s);
 }
 

@@ -10,7 +10,8 @@
 // registers between the reduction and the output, spread over the fewest
 // warps that keep at most NV 16-byte vectors a lane.  max|y| = rstd max|s w|,
 // so the 8-bit output needs no second reduction.  16384 x 4096 bf16: forward
-// 78 us (6.9 TB/s), with 8 bits out 77, backward 81 (6.6 TB/s).
+// 80 us (6.7 TB/s), with 8 bits out 78, backward 85 (6.3 TB/s; 81 right behind
+// the forward, which leaves some of s in L2).
 #include <float.h>
 
 #include "common.cuh"
@@ -181,9 +182,8 @@ rmsnorm_forward_kernel(const uint4 *x, const uint4 *res, const float *weight, in
 // memory at any time: 16 warps an SM, all that the registers leave room for, do
 // not keep enough of HBM busy with loads to registers (16384 x 4096 bf16: 100
 // us so).  A row group meets at a barrier of its own, so that the groups of a
-// CTA drift apart and their reductions hide under each other's copies: two CTAs
-// of 8 warps an SM whose groups share the CTA's barrier take 84 us there and
-// 57 us at 4096 x 8192, these 81 and 48.5.
+// CTA drift apart and their reductions hide under each other's copies (4096 x 8192:
+// 49.5 us; two CTAs of 8 warps an SM whose groups share the CTA's barrier 57).
 constexpr int BWD_STAGES = 4, BWD_NV = 2;
 
 constexpr int BWD_RING = BWD_STAGES * 3 * BWD_NV * BWD_WARPS * 32 * 16;  // bytes
@@ -333,7 +333,8 @@ rmsnorm_dw_kernel(const float *part, int rows, int D, float *dw) {
 }
 
 // Symmetric 8-bit rows of a matrix: a CTA per row, which is read twice (the
-// second time from L1 / L2).
+// second time from L1 / L2).  For weights, once, so it is left plain: 14336 x 4096
+// bf16 42 us (4.2 TB/s), 131072 x 4096 346 us (4.7 TB/s).
 template <typename E>
 __global__ void __launch_bounds__(256)
 q8_quantize_kernel(const uint4 *a, int nv, int8_t *q, float *scale) {

@@ -13,7 +13,9 @@
  * word (device int32, 0 before the first call, the first error wins;
  * twell_read_status reads and clears it).  Row-major contiguous operands
  * unless a row pitch is given; pointers 16-byte aligned except the per-row
- * and per-column vectors, which take their type's own alignment.  Element
+ * and per-column vectors, which take their type's own alignment (the norm's
+ * weight 16 bytes, a pair of stats 8).  Operands, stream and current device are
+ * one GPU's, the same for all calls of a process.  Element
  * type `dtype`: TWELL_F32 or TWELL_BF16.  Sums, maxima, statistics and norms
  * are held in fp32 (8-bit products: exact in fp32, see twell_q8_matmul), each
  * output is rounded once (to nearest even), and every result is independent
