@@ -106,3 +106,23 @@ def test_what_follows_reads_all_of_it(M, N, K):
     tw.twell_add_rmsnorm_forward(want[2], None, ones, M, N, BF16, 1e-6, None, None, q3, qs3, None)
     torch.cuda.synchronize()
     assert torch.equal(q2, q3) and torch.equal(qs2, qs3)
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_weights_written_right_before(M, N, K):
+    """Weights quantised on the stream just before the product that reads them."""
+    c = Chain(M, N, K, sets=1)
+    g = gen(K)
+    W = [torch.randn(N, K, generator=g).bfloat16().cuda() for _ in range(2)]
+    c.call(0)
+    want = []
+    for w in W:
+        tw.twell_q8_quantize(w, N, K, BF16, c.w, c.sw)
+        torch.cuda.synchronize()
+        want.append(((c.q.double() @ c.w.double().t()).float() * c.qs[:, None] * c.sw).bfloat16())
+    y = [torch.empty_like(c.y[0]) for _ in range(6)]
+    for i in range(6):
+        tw.twell_q8_quantize(W[i & 1], N, K, BF16, c.w, c.sw)
+        tw.twell_q8_matmul(c.q, c.qs, c.w, c.sw, None, M, N, K, BF16, y[i], c.st, c.ws, c.n)
+    for i in range(6):
+        assert torch.equal(y[i], want[i & 1])
