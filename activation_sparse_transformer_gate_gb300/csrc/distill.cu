@@ -782,7 +782,7 @@ cudaError_t forward_t(const DistillArgs &a, cudaStream_t s) {
   // 472 | 743 (cluster kernel 102 | 139 | 263 | 413 | 706 | 1041).  The loss alone: 4
   // warps 39 | 52 | 87 | 123 | 203 | 327; 8 warps 56 | 67 | 99 | 133 | 205 | 325; 16 warps
   // 124 | 132 | 167 | 204 | 246 | 326 (cluster kernel 81 | 94 | 119 | 146 | 214 | 330): it
-  // takes the same widths, which are not its best from 12000 to 100000 logits.
+  // takes the same widths, which are not its best from 16384 to about 100000.
   // By rows, us at 5001 | 32000 | 131072 logits, cluster kernel and this rule's width:
   // 76 rows 6.9 | 7.5 | 15 and 6.0 | 8.2 | 17; 152 rows 6.7 | 8.2 | 26 and 6.5 | 8.4 | 17.5;
   // 256 rows 7.0 | 11.7 | 37 and 6.7 | 11.7 | 34; 304 rows 7.2 | 12.1 | 45 and 6.7 | 11.7 |
