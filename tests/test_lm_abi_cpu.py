@@ -143,3 +143,10 @@ def test_long_sums_of_few_columns_leave_the_fragments(lib, M, N, K):
     of a as scratch."""
     assert tw.twell_q8_workspace_size(M, N, K) >= M * K * 2
     assert tw.twell_q8_workspace_size(M, N, 1024) == 0
+
+
+def test_pair_counts_are_in_the_test_variants_only(lib):
+    assert not hasattr(lib, "twell_test_q8_pairs")
+    _build.build(variants=("hooks", "timeout"))
+    for variant in ("hooks", "timeout"):
+        assert hasattr(tw.load(_build.lib_path(variant)), "twell_test_q8_pairs")
