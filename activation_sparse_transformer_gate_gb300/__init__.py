@@ -12,8 +12,8 @@ Names follow the ABI: ``twell_workspace_size``, ``twell_pack_dense``,
 ``twell_rowell_pack_dense`` / ``twell_rowell_forward``.  ``TwellBuffers`` and
 ``RowEllBuffers`` allocate the device buffers of a ``twell_t`` /
 ``twell_rowell_t`` with torch.  The operators around the FFN (embedding,
-residual norm, 8-bit product, distillation loss; include/twell_lm.h) are in
-``lm`` and available under the same names here.
+residual norm, recurrence, 8-bit product, distillation and policy loss, AdamW;
+include/twell_lm.h) are in ``lm`` and available under the same names here.
 """
 from __future__ import annotations
 
@@ -42,8 +42,12 @@ LM_EXPORTS = ("twell_read_status", "twell_embed_forward", "twell_embed_backward"
               "twell_embed_workspace_size", "twell_add_rmsnorm_forward",
               "twell_add_rmsnorm_backward", "twell_add_rmsnorm_workspace_size",
               "twell_q8_quantize", "twell_q8_matmul", "twell_q8_workspace_size",
-              "twell_distill_forward", "twell_distill_backward")
+              "twell_distill_forward", "twell_distill_backward",
+              "twell_recur_forward", "twell_recur_backward", "twell_recur_states",
+              "twell_policy_forward", "twell_policy_backward", "twell_adamw_step")
 EXPORTS += LM_EXPORTS
+# what the binding has beside them
+LM_HELPERS = ("AdamWTensors", "adamw_dynamic")
 
 
 class TwellError(RuntimeError):
@@ -125,7 +129,15 @@ def _declare_lm(lib) -> None:
             ("twell_q8_quantize", [P, I, I, I, P, P, P]),
             ("twell_q8_matmul", [P, P, P, P, P, I, I, I, I, P, P, P, S, P]),
             ("twell_distill_forward", [P, L, P, P, P, I, I, I, I, F32, P, P, P, P, P]),
-            ("twell_distill_backward", [P, L, P, P, P, P, I, I, I, I, F32, P, P, P])):
+            ("twell_distill_backward", [P, L, P, P, P, P, I, I, I, I, F32, P, P, P]),
+            ("twell_recur_forward", [P, P, L, P, P, I, P, I, I, I, P, P, P, P, P]),
+            ("twell_recur_backward", [P, P, L, P, P, I, P, P, P, P, I, I, I, P, P, P, P, P, P]),
+            ("twell_recur_states", [I]),
+            ("twell_policy_forward", [P, L, P, I, P, P, P, P, I, I, I, F32, F32, F32, F32, P, P, P,
+                                      P, P, P]),
+            ("twell_policy_backward", [P, L, P, I, P, P, P, P, P, P, I, I, I, F32, F32, F32, F32, P,
+                                       P, P]),
+            ("twell_adamw_step", [P, I, I, I, F32, F32, F32, F32, L, ctypes.c_uint32, P, P, P])):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, I
     for name in ("twell_embed_workspace_size", "twell_q8_workspace_size"):
@@ -273,7 +285,7 @@ def workspace(T: int, D: int, F: int, C: int, K: int, dtype: int, train: bool, d
 
 def __getattr__(name):
     """The operators around the FFN, from ``lm`` on first use (it needs torch)."""
-    if name not in LM_EXPORTS:
+    if name not in LM_EXPORTS + LM_HELPERS:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
     from . import lm
     fn = globals()[name] = getattr(lm, name)

@@ -216,7 +216,12 @@ enum KernelId {
   KID_DISTILL_FWD = 31,
   KID_DISTILL_BWD = 32,
   KID_Q8_WIDEN = 33,
-  KID_COUNT = 34
+  KID_RECUR_FWD = 34,
+  KID_RECUR_BWD = 35,
+  KID_POLICY_FWD = 36,
+  KID_POLICY_BWD = 37,
+  KID_ADAMW = 38,
+  KID_COUNT = 39
 };
 // Record a timing event after `launches` kernel launches of component `id`
 // (no-op unless enabled).

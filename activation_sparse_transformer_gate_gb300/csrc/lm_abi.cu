@@ -25,7 +25,7 @@ twell_status check_scratch(const void *ws, size_t bytes, size_t need) {
   return TWELL_OK;
 }
 
-constexpr int EMBED_MAX_D = 65536;
+constexpr int EMBED_MAX_D = 65536, RECUR_MAX_D = 65536;
 
 twell_status check_embed(const EmbedArgs &a) {
   twell_status st = check_dtype(a.dtype);
@@ -241,6 +241,152 @@ twell_status twell_distill_backward(const void *z, long long ldz, const int32_t 
   prof_mark(KID_START, s);
   const cudaError_t e = launch_distill_backward(a, s);
   prof_mark(KID_DISTILL_BWD, s);
+  return cuda_status(e);
+}
+
+static twell_status check_recur(const RecurArgs &a) {
+  const twell_status st = check_dtype(a.dtype);
+  if (st != TWELL_OK) return st;
+  if (!a.x || !a.gate || !a.status || a.T < 1 || a.T > MAX_ROWS || a.B < 1 || a.B > MAX_ROWS ||
+      a.D < 1 || a.D > RECUR_MAX_D || a.ld < a.D || a.ld > (1ll << 40))
+    return TWELL_ERR_ARG;
+  if (!a.starts && a.T % a.B != 0) return TWELL_ERR_ARG;
+  const size_t es = elem_size(a.dtype);
+  if ((size_t)a.D * es % 16 != 0 || (size_t)a.ld * es % 16 != 0) return TWELL_ERR_ALIGN;
+  if (!aligned16(a.x) || !aligned16(a.gate) || !aligned16(a.bias) || !aligned4(a.starts) ||
+      !aligned16(a.h0) || !aligned4(a.status) || !aligned16(a.h) || !aligned16(a.hT) ||
+      !aligned16(a.states) || !aligned16(a.dh) || !aligned16(a.dhT) || !aligned16(a.dx) ||
+      !aligned16(a.dgate) || !aligned16(a.dbias) || !aligned16(a.dh0))
+    return TWELL_ERR_ALIGN;
+  return TWELL_OK;
+}
+
+int twell_recur_states(int T) {
+  return T < 1 || T > MAX_ROWS ? 0 : (T + RECUR_KEEP - 1) / RECUR_KEEP;
+}
+
+twell_status twell_recur_forward(const void *x, const void *gate, long long ld, const float *bias,
+                                 const int32_t *starts, int B, const float *h0, int T, int D,
+                                 int dtype, void *h, float *hT, float *states, int32_t *status,
+                                 void *stream) {
+  RecurArgs a = {};
+  a.x = x; a.gate = gate; a.ld = ld; a.bias = bias; a.starts = starts; a.B = B; a.h0 = h0;
+  a.T = T; a.D = D; a.dtype = dtype; a.h = h; a.hT = hT; a.states = states; a.status = status;
+  const twell_status st = check_recur(a);
+  if (st != TWELL_OK) return st;
+  if (!h) return TWELL_ERR_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  prof_mark(KID_START, s);
+  const cudaError_t e = launch_recur_forward(a, s);
+  prof_mark(KID_RECUR_FWD, s);
+  return cuda_status(e);
+}
+
+twell_status twell_recur_backward(const void *x, const void *gate, long long ld,
+                                  const float *bias, const int32_t *starts, int B,
+                                  const float *h0, const float *states, const void *dh,
+                                  const float *dhT, int T, int D, int dtype, void *dx,
+                                  void *dgate, float *dbias, float *dh0, int32_t *status,
+                                  void *stream) {
+  RecurArgs a = {};
+  a.x = x; a.gate = gate; a.ld = ld; a.bias = bias; a.starts = starts; a.B = B; a.h0 = h0;
+  a.states = const_cast<float *>(states); a.dh = dh; a.dhT = dhT; a.T = T; a.D = D;
+  a.dtype = dtype; a.dx = dx; a.dgate = dgate; a.dbias = dbias; a.dh0 = dh0; a.status = status;
+  const twell_status st = check_recur(a);
+  if (st != TWELL_OK) return st;
+  if (!states || !dh || !dx || !dgate) return TWELL_ERR_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  prof_mark(KID_START, s);
+  const cudaError_t e = launch_recur_backward(a, s);
+  prof_mark(KID_RECUR_BWD, s);
+  return cuda_status(e);
+}
+
+static twell_status check_policy(const PolicyArgs &a) {
+  const twell_status st = check_dtype(a.dtype);
+  if (st != TWELL_OK) return st;
+  if (a.token_bytes != 4 && a.token_bytes != 8) return TWELL_ERR_DTYPE;
+  if (!a.z || !a.tokens || !a.logp || !a.stats || !a.status || a.T < 1 || a.T > MAX_ROWS ||
+      a.V < 1 || a.V > MAX_ROWS || a.ldz < a.V || !(a.tau >= 1e-4f) || !(a.tau <= 1e4f) ||
+      !(a.clip_low >= 0.f) || !(a.clip_low <= 1.f) || !(a.clip_high >= 0.f) ||
+      !isfinite(a.clip_high) || !(a.beta >= 0.f) || !isfinite(a.beta))
+    return TWELL_ERR_ARG;
+  if (((uintptr_t)a.tokens & (uintptr_t)(a.token_bytes - 1)) != 0 || !aligned16(a.z) ||
+      !aligned16(a.dz) || !aligned4(a.old_logp) || !aligned4(a.ref_logp) ||
+      !aligned4(a.advantage) || !aligned4(a.row_weight) || !aligned4(a.loss) ||
+      !aligned4(a.logp) || ((uintptr_t)a.stats & 7u) != 0 || !aligned4(a.status))
+    return TWELL_ERR_ALIGN;
+  return TWELL_OK;
+}
+
+twell_status twell_policy_forward(const void *z, long long ldz, const void *tokens,
+                                  int token_bytes, const float *old_logp, const float *ref_logp,
+                                  const float *advantage, const float *row_weight, int T, int V,
+                                  int dtype, float tau, float clip_low, float clip_high,
+                                  float beta, float *loss, float *logp, float *stats, void *dz,
+                                  int32_t *status, void *stream) {
+  const PolicyArgs a = {z, ldz, tokens, token_bytes, old_logp, ref_logp, advantage, row_weight, T,
+                        V, dtype, tau, clip_low, clip_high, beta, loss, logp, stats, dz, status};
+  const twell_status st = check_policy(a);
+  if (st != TWELL_OK) return st;
+  if (advantage ? !loss : loss || dz) return TWELL_ERR_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  prof_mark(KID_START, s);
+  const cudaError_t e = launch_policy_forward(a, s);
+  prof_mark(KID_POLICY_FWD, s);
+  return cuda_status(e);
+}
+
+twell_status twell_policy_backward(const void *z, long long ldz, const void *tokens,
+                                   int token_bytes, const float *old_logp, const float *ref_logp,
+                                   const float *advantage, const float *logp, const float *stats,
+                                   const float *row_grad, int T, int V, int dtype, float tau,
+                                   float clip_low, float clip_high, float beta, void *dz,
+                                   int32_t *status, void *stream) {
+  const PolicyArgs a = {z, ldz, tokens, token_bytes, old_logp, ref_logp, advantage, row_grad, T,
+                        V, dtype, tau, clip_low, clip_high, beta, nullptr,
+                        const_cast<float *>(logp), const_cast<float *>(stats), dz, status};
+  const twell_status st = check_policy(a);
+  if (st != TWELL_OK) return st;
+  if (!row_grad || !advantage || !dz) return TWELL_ERR_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  prof_mark(KID_START, s);
+  const cudaError_t e = launch_policy_backward(a, s);
+  prof_mark(KID_POLICY_BWD, s);
+  return cuda_status(e);
+}
+
+twell_status twell_adamw_step(const twell_adamw_tensor *tensors, int count, int grad_dtype,
+                              int state_bits, float lr, float beta1, float beta2, float eps,
+                              long long step, uint32_t seed, const float *grad_scale,
+                              const twell_adamw_dynamic *dynamic, void *stream) {
+  twell_status st = check_dtype(grad_dtype);
+  if (st != TWELL_OK) return st;
+  if (state_bits != 8 && state_bits != 32) return TWELL_ERR_DTYPE;
+  if (!tensors || count < 1 || !isfinite(lr) || !(beta1 >= 0.f) || !(beta1 < 1.f) ||
+      !(beta2 >= 0.f) || !(beta2 < 1.f) || !(eps >= 0.f) || !isfinite(eps) || step < 1)
+    return TWELL_ERR_ARG;
+  if (!aligned4(grad_scale) || !aligned16(dynamic)) return TWELL_ERR_ALIGN;
+  for (int i = 0; i < count; ++i) {
+    const twell_adamw_tensor &t = tensors[i];
+    if (t.n < 0 || t.n > (1ll << 40) || t.first < 0 || !isfinite(t.decay)) return TWELL_ERR_ARG;
+    if (t.n == 0) continue;
+    if (!t.param || !t.grad || !t.m || !t.v || (state_bits == 8 && (!t.mscale || !t.vscale)))
+      return TWELL_ERR_ARG;
+    if (!aligned16(t.param) || !aligned16(t.grad) || !aligned16(t.m) || !aligned16(t.v) ||
+        !aligned4(t.mscale) || !aligned4(t.vscale) || !aligned16(t.copy))
+      return TWELL_ERR_ALIGN;
+  }
+  AdamwArgs a;
+  a.tensors = tensors; a.count = count; a.grad_dtype = grad_dtype; a.state_bits = state_bits;
+  a.lr = lr; a.beta1 = beta1; a.beta2 = beta2; a.eps = eps; a.seed = seed;
+  a.correction1 = 1.0 - pow((double)beta1, (double)step);
+  a.correction2 = 1.0 - pow((double)beta2, (double)step);
+  a.grad_scale = grad_scale; a.dynamic = dynamic;
+  cudaStream_t s = (cudaStream_t)stream;
+  prof_mark(KID_START, s);
+  const cudaError_t e = launch_adamw(a, s);
+  prof_mark(KID_ADAMW, s);
   return cuda_status(e);
 }
 

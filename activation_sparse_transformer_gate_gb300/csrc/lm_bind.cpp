@@ -282,6 +282,115 @@ PyObject *distill_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
   });
 }
 
+// x, gate, ld, bias, starts, B, h0, T, D, dtype, h, hT, states, status, stream
+PyObject *recur_forward(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  Args a(args, n);
+  const long long L = a.ahead(2), B = a.ahead(5), T = a.ahead(7), D = a.ahead(8);
+  const at::ScalarType t = a.type((int)a.ahead(9));
+  const void *x = a.pitched(t, T, D, L), *gate = a.pitched(t, T, D, L);
+  const long long ld = a.integer();
+  const void *bias = a.tensor(F32, D), *starts = a.tensor(I32, B + 1);
+  const int iB = a.small();
+  const void *h0 = a.tensor(F32, B * D);
+  const int iT = a.small(), iD = a.small(), dt = a.small();
+  void *h = a.tensor(t, T * D), *hT = a.tensor(F32, B * D);
+  void *states = a.tensor(F32, twell_recur_states((int)T) * D), *st = a.tensor(I32, 1);
+  void *s = a.stream();
+  return finish(a, [&] {
+    return twell_recur_forward(x, gate, ld, (const float *)bias, (const int32_t *)starts, iB,
+                               (const float *)h0, iT, iD, dt, h, (float *)hT, (float *)states,
+                               (int32_t *)st, s);
+  });
+}
+
+// x, gate, ld, bias, starts, B, h0, states, dh, dhT, T, D, dtype, dx, dgate, dbias, dh0, status,
+// stream
+PyObject *recur_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  Args a(args, n);
+  const long long L = a.ahead(2), B = a.ahead(5), T = a.ahead(10), D = a.ahead(11);
+  const at::ScalarType t = a.type((int)a.ahead(12));
+  const void *x = a.pitched(t, T, D, L), *gate = a.pitched(t, T, D, L);
+  const long long ld = a.integer();
+  const void *bias = a.tensor(F32, D), *starts = a.tensor(I32, B + 1);
+  const int iB = a.small();
+  const void *h0 = a.tensor(F32, B * D);
+  const void *states = a.tensor(F32, twell_recur_states((int)T) * D);
+  const void *dh = a.tensor(t, T * D), *dhT = a.tensor(F32, B * D);
+  const int iT = a.small(), iD = a.small(), dt = a.small();
+  void *dx = a.pitched(t, T, D, L), *dgate = a.pitched(t, T, D, L);
+  void *dbias = a.tensor(F32, D), *dh0 = a.tensor(F32, B * D), *st = a.tensor(I32, 1);
+  void *s = a.stream();
+  return finish(a, [&] {
+    return twell_recur_backward(x, gate, ld, (const float *)bias, (const int32_t *)starts, iB,
+                                (const float *)h0, (const float *)states, dh, (const float *)dhT,
+                                iT, iD, dt, dx, dgate, (float *)dbias, (float *)dh0, (int32_t *)st,
+                                s);
+  });
+}
+
+// z, ldz, tokens, old_logp, ref_logp, advantage, row_weight, T, V, dtype, tau, clip_low, clip_high,
+// beta, loss, logp, stats, dz, status, stream
+PyObject *policy_forward(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  Args a(args, n);
+  const long long L = a.ahead(1), T = a.ahead(7), V = a.ahead(8);
+  const at::ScalarType t = a.type((int)a.ahead(9));
+  int bytes;
+  const void *z = a.pitched(t, T, V, L);
+  const long long ldz = a.integer();
+  const void *tok = a.tokens(T, &bytes), *old = a.tensor(F32, T), *ref = a.tensor(F32, T);
+  const void *adv = a.tensor(F32, T), *w = a.tensor(F32, T);
+  const int iT = a.small(), iV = a.small(), dt = a.small();
+  const float tau = a.real(), low = a.real(), high = a.real(), beta = a.real();
+  void *loss = a.tensor(F32, T), *logp = a.tensor(F32, T), *stats = a.tensor(F32, 2 * T);
+  void *dz = a.pitched(t, T, V, L), *st = a.tensor(I32, 1), *s = a.stream();
+  return finish(a, [&] {
+    return twell_policy_forward(z, ldz, tok, bytes, (const float *)old, (const float *)ref,
+                                (const float *)adv, (const float *)w, iT, iV, dt, tau, low, high,
+                                beta, (float *)loss, (float *)logp, (float *)stats, dz,
+                                (int32_t *)st, s);
+  });
+}
+
+// z, ldz, tokens, old_logp, ref_logp, advantage, logp, stats, row_grad, T, V, dtype, tau, clip_low,
+// clip_high, beta, dz, status, stream
+PyObject *policy_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  Args a(args, n);
+  const long long L = a.ahead(1), T = a.ahead(9), V = a.ahead(10);
+  const at::ScalarType t = a.type((int)a.ahead(11));
+  int bytes;
+  const void *z = a.pitched(t, T, V, L);
+  const long long ldz = a.integer();
+  const void *tok = a.tokens(T, &bytes), *old = a.tensor(F32, T), *ref = a.tensor(F32, T);
+  const void *adv = a.tensor(F32, T), *logp = a.tensor(F32, T), *stats = a.tensor(F32, 2 * T);
+  const void *g = a.tensor(F32, T);
+  const int iT = a.small(), iV = a.small(), dt = a.small();
+  const float tau = a.real(), low = a.real(), high = a.real(), beta = a.real();
+  void *dz = a.pitched(t, T, V, L), *st = a.tensor(I32, 1), *s = a.stream();
+  return finish(a, [&] {
+    return twell_policy_backward(z, ldz, tok, bytes, (const float *)old, (const float *)ref,
+                                 (const float *)adv, (const float *)logp, (const float *)stats,
+                                 (const float *)g, iT, iV, dt, tau, low, high, beta, dz,
+                                 (int32_t *)st, s);
+  });
+}
+
+// tensors (address of the host's array), count, grad_dtype, state_bits, lr, beta1, beta2, eps, step,
+// seed, grad_scale, dynamic, stream
+PyObject *adamw_step(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  Args a(args, n);
+  const void *list = (const void *)a.integer();
+  const int count = a.small(), gt = a.small(), bits = a.small();
+  const float lr = a.real(), b1 = a.real(), b2 = a.real(), eps = a.real();
+  const long long step = a.integer(), seed = a.integer();
+  const void *scale = a.tensor(F32, 1), *dyn = a.tensor(I32, 4);
+  void *s = a.stream();
+  return finish(a, [&] {
+    return twell_adamw_step((const twell_adamw_tensor *)list, count, gt, bits, lr, b1, b2, eps, step,
+                            (uint32_t)seed, (const float *)scale, (const twell_adamw_dynamic *)dyn,
+                            s);
+  });
+}
+
 using Method = PyObject *(PyObject *, PyObject *const *, Py_ssize_t);
 
 // No C++ exception leaves through Python's C frames.
@@ -302,7 +411,9 @@ PyMethodDef methods[] = {
     TWELL_METHOD(add_rmsnorm_forward), TWELL_METHOD(add_rmsnorm_backward),
     TWELL_METHOD(q8_quantize),         TWELL_METHOD(q8_matmul),
     TWELL_METHOD(distill_forward),     TWELL_METHOD(distill_backward),
-    {nullptr, nullptr, 0, nullptr}};
+    TWELL_METHOD(recur_forward),       TWELL_METHOD(recur_backward),
+    TWELL_METHOD(policy_forward),      TWELL_METHOD(policy_backward),
+    TWELL_METHOD(adamw_step),          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lm",
                       "Argument marshalling of the operators around the FFN.", -1, methods,

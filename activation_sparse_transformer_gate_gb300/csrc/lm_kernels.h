@@ -69,4 +69,55 @@ constexpr int Q8_MAX_K = 65536;
 size_t q8_scratch(int M, int N, int K);
 cudaError_t launch_q8_matmul(const Q8Args &a, cudaStream_t s);
 
+// recur.cu
+constexpr int RECUR_KEEP = 64;   // rows from one kept state to the next
+struct RecurArgs {
+  const void *x, *gate;
+  long long ld;
+  const float *bias;
+  const int32_t *starts;    // NULL: B sequences of T / B rows
+  int B, T, D, dtype;
+  const float *h0;
+  int32_t *status;
+  // forward
+  void *h;
+  float *hT, *states;
+  // backward (reads states)
+  const void *dh;
+  const float *dhT;
+  void *dx, *dgate;
+  float *dbias, *dh0;
+};
+cudaError_t launch_recur_forward(const RecurArgs &a, cudaStream_t s);
+cudaError_t launch_recur_backward(const RecurArgs &a, cudaStream_t s);
+
+// policy.cu
+struct PolicyArgs {
+  const void *z;
+  long long ldz;
+  const void *tokens;
+  int token_bytes;          // 4 or 8
+  const float *old_logp, *ref_logp, *advantage;
+  const float *row_weight;  // forward: NULL = all 1; backward: row_grad
+  int T, V, dtype;
+  float tau, clip_low, clip_high, beta;
+  float *loss, *logp, *stats;  // backward: loss NULL, the others read
+  void *dz;
+  int32_t *status;
+};
+cudaError_t launch_policy_forward(const PolicyArgs &a, cudaStream_t s);
+cudaError_t launch_policy_backward(const PolicyArgs &a, cudaStream_t s);
+
+// adamw.cu
+struct AdamwArgs {
+  const twell_adamw_tensor *tensors;
+  int count, grad_dtype, state_bits;
+  float lr, beta1, beta2, eps;
+  double correction1, correction2;
+  uint32_t seed;
+  const float *grad_scale;
+  const twell_adamw_dynamic *dynamic;
+};
+cudaError_t launch_adamw(const AdamwArgs &a, cudaStream_t s);
+
 }  // namespace twell

@@ -2,9 +2,11 @@
  * twell_lm.h -- the operators that stand around the activation-sparse FFN in
  * a language model (same library, libtwell.so; one GB300, sm_103a):
  *
- *   token ids -> twell_embed_* -> twell_add_rmsnorm_* -> twell_ffn_* -> ...
- *     -> twell_add_rmsnorm_* -> output product -> twell_distill_*   (training)
- *     -> twell_add_rmsnorm_* (8-bit output) -> twell_q8_matmul      (serving)
+ *   token ids -> twell_embed_* -> twell_add_rmsnorm_* -> twell_recur_*
+ *     -> twell_add_rmsnorm_* -> twell_ffn_* -> ...
+ *     -> twell_add_rmsnorm_* -> output product
+ *          -> twell_distill_* or twell_policy_*, back, twell_adamw_step (training)
+ *     -> twell_add_rmsnorm_* (8-bit output) -> twell_q8_matmul        (serving)
  *
  * The conventions of twell.h hold for every call: device pointers owned by
  * the caller, asynchronous on `stream`, errors the host can see are returned
@@ -146,6 +148,131 @@ twell_status twell_distill_backward(const void *z, long long ldz, const int32_t 
                                     const float *teacher, const float *stats,
                                     const float *row_grad, int T, int V, int k, int dtype,
                                     float tau, void *dz, int32_t *status, void *stream);
+
+/* ---- gated linear recurrence over packed sequences ------------------------------
+ * a_t = sigmoid(gate_t + bias),  c_t = 1 - a_t   (channel by channel)
+ * h_t = a_t h_{t-1} + c_t x_t,   h_{-1} = h0 of the sequence
+ *   x, gate [T][D] dtype, row pitch ld elements (the halves of one projection's
+ *   rows, or matrices of their own); bias [D] fp32 or NULL; h [T][D] dtype.
+ *   starts [B + 1] int32 on the device, ascending: sequence s is the rows
+ *   starts[s] .. starts[s + 1] - 1 (none: an empty sequence).  Rows before the
+ *   first and behind the last sequence are not read, and their outputs are left
+ *   as they were.  starts NULL: B sequences of T / B rows each.  Values that
+ *   descend or leave [0, T] record TWELL_ERR_INDEX; the outputs are then undefined.
+ *   h0 [B][D] fp32: the states before the sequences (NULL: 0); hT [B][D] fp32 or
+ *   NULL: the states behind them (of an empty sequence: h0).  hT may be h0.
+ *   states [twell_recur_states(T)][D] fp32 or NULL: what the backward needs.
+ * The state is held in fp32, h is its rounding.  B = T without starts is the step
+ * of a decoded token for each of T sequences.
+ * 1 <= T, 1 <= B, D <= 65536, ld >= D; D*elem_size and ld*elem_size multiples
+ * of 16. */
+twell_status twell_recur_forward(const void *x, const void *gate, long long ld, const float *bias,
+                                 const int32_t *starts, int B, const float *h0, int T, int D,
+                                 int dtype, void *h, float *hT, float *states, int32_t *status,
+                                 void *stream);
+
+/* G_t = dh_t + a_{t+1} G_{t+1} within the sequence (a_{t+1} G_{t+1} = dhT at its last row)
+ * dx = c G,  dgate = G (h_{t-1} - x) a c,  dbias = sum over rows of dgate
+ * dh0 = a G at the sequence's first row (an empty sequence: dhT)
+ *   dh [T][D] dtype, dhT [B][D] fp32 (NULL: 0); dx, dgate [T][D] dtype, row pitch
+ *   ld; dbias [D] and dh0 [B][D] fp32, overwritten, each may be NULL.
+ * x, gate, bias, starts, h0 and states as in the forward (whose fp32 states the
+ * backward takes up again, so that h and its rounding do not matter).  The outputs
+ * may not be the inputs' buffers. */
+twell_status twell_recur_backward(const void *x, const void *gate, long long ld,
+                                  const float *bias, const int32_t *starts, int B,
+                                  const float *h0, const float *states, const void *dh,
+                                  const float *dhT, int T, int D, int dtype, void *dx,
+                                  void *dgate, float *dbias, float *dh0, int32_t *status,
+                                  void *stream);
+
+/* Rows of `states` (0 for an invalid T). */
+int twell_recur_states(int T);
+
+/* ---- clipped policy loss with a KL term -----------------------------------------
+ * z [T][V] (row pitch ldz elements) dtype: the policy's logits.  tokens [T] int32
+ * (token_bytes 4) or int64 (8): the sampled ones.
+ *   logp = z[token] / tau - log sum exp(z / tau)
+ *   r = exp(logp - old_logp)       (old_logp NULL: old_logp = logp, r = 1)
+ *   d = ref_logp - logp            (ref_logp NULL: no KL term)
+ *   loss[t] = row_weight[t] * (-min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *                              + beta (exp(d) - d - 1)),  A = advantage[t]
+ *   slope   = row_weight[t] * (-(r A, or 0 where the clipped side is the smaller)
+ *                              + beta (1 - exp(d)))        d loss / d logp
+ *   dz[t]   = slope / tau * (onehot(token) - softmax(z / tau))
+ *   stats[t] = {max z, log sum exp((z - max z) / tau)}
+ * old_logp, ref_logp, advantage, row_weight (NULL: all 1), loss, logp [T] fp32.
+ * A row of weight 0 or with a token < 0 is not read: its loss, logp, stats and dz
+ * are 0.  A token >= V records TWELL_ERR_INDEX, and its row is treated the same.
+ * Logits of -inf have probability 0; a row with NaN, +inf or nothing but -inf has
+ * loss, logp and dz NaN (with advantage 0 and no KL term: loss and dz 0 or NaN).
+ * advantage NULL: the log-probabilities alone (loss and dz NULL), as for old_logp
+ * and ref_logp themselves.  dz (else NULL: not computed) has z's type and pitch and
+ * may be z itself.
+ * 1 <= T, 1 <= V <= ldz, 1e-4 <= tau <= 1e4, 0 <= clip_low <= 1, 0 <= clip_high,
+ * 0 <= beta, all finite. */
+twell_status twell_policy_forward(const void *z, long long ldz, const void *tokens,
+                                  int token_bytes, const float *old_logp, const float *ref_logp,
+                                  const float *advantage, const float *row_weight, int T, int V,
+                                  int dtype, float tau, float clip_low, float clip_high,
+                                  float beta, float *loss, float *logp, float *stats, void *dz,
+                                  int32_t *status, void *stream);
+
+/* dz from the forward's logp and stats; row_grad in the place of row_weight:
+ * row_weight * (gradient that reaches the row's loss).  dz may be z itself. */
+twell_status twell_policy_backward(const void *z, long long ldz, const void *tokens,
+                                   int token_bytes, const float *old_logp, const float *ref_logp,
+                                   const float *advantage, const float *logp, const float *stats,
+                                   const float *row_grad, int T, int V, int dtype, float tau,
+                                   float clip_low, float clip_high, float beta, void *dz,
+                                   int32_t *status, void *stream);
+
+/* ---- AdamW over many tensors ------------------------------------------------------
+ * For every element of every tensor, with g = grad (* *grad_scale):
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   param = param (1 - lr decay)
+ *           - lr / correction1 * m / (sqrt(v) / sqrt(correction2) + eps)
+ *   copy = param in bf16 (where there is a copy)
+ * correction = 1 - beta^step.
+ * state_bits 32: m, v [n] fp32.  state_bits 8: m and r = sqrt(v) are kept in blocks
+ * of 256 elements as e4m3 codes times a scale, the block's largest magnitude (at
+ * least 1e-30) / 448; [n] codes, ceil(n / 256) scales.  The step itself uses m and
+ * v before that rounding.  Rounding is stochastic: up with the chance of what
+ * rounding down would leave, from 16 bits for each of m and r that follow from
+ * `seed` and first + i (element i's number) alone:
+ *   u = (first + i) * 0x9E3779B9 + ((first + i) >> 32) * 0x3C6EF373 + seed,
+ *   u = (u ^ u >> 16) * 0x6A09E667,  u = (u ^ u >> 15) * 0xBB67AE85,  u ^= u >> 16
+ * (32 bits), m's in the low half, r's in the high half; another seed for every
+ * step.  An r > 0 is not rounded to 0.  A block with an infinity or NaN gets codes
+ * 0 and a scale of NaN.
+ * param, m, v, scales and copies are updated in place; they are 16-byte aligned, as
+ * grad is, the scales 4, and no two of them may overlap.  n 0: left out. */
+typedef struct {
+  float *param;             /* [n]                                            */
+  const void *grad;         /* [n] of grad_dtype                              */
+  void *m, *v;              /* [n] fp32, or codes                             */
+  float *mscale, *vscale;   /* [ceil(n / 256)] (state_bits 8)                 */
+  void *copy;               /* [n] bf16, or NULL                              */
+  long long n;              /* 0 <= n <= 2^40                                 */
+  long long first;          /* number of element 0, >= 0 (state_bits 8)       */
+  float decay;              /* weight decay                                   */
+} twell_adamw_tensor;
+
+/* What changes from step to step, in device memory (16-byte aligned), for a step
+ * that is captured once and replayed: the caller writes it before each replay. */
+typedef struct {
+  float lr, correction1, correction2;
+  uint32_t seed;
+} twell_adamw_dynamic;
+
+/* tensors: [count] in host memory, read before the call returns.  grad_scale: a
+ * device scalar or NULL (1); where it is not finite, nothing is changed.  dynamic:
+ * NULL, or in the place of lr, step and seed.  0 <= beta < 1, eps >= 0, 1 <= step,
+ * all finite. */
+twell_status twell_adamw_step(const twell_adamw_tensor *tensors, int count, int grad_dtype,
+                              int state_bits, float lr, float beta1, float beta2, float eps,
+                              long long step, uint32_t seed, const float *grad_scale,
+                              const twell_adamw_dynamic *dynamic, void *stream);
 
 #ifdef __cplusplus
 }
