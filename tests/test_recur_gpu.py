@@ -195,6 +195,22 @@ def test_states_of_long_decoding():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,D,starts", [(1000, 136, ragged(1000, 17, 1)), (600, 2048, 20), (4100, 72, [0, 4099, 4100]),
+                                        (300, 64, 150), (2049, 256, ragged(2049, 40, 5))])
+def test_states_in_place(T, D, starts, dtype):
+    """hT in the place of h0: the bits of two buffers."""
+    c = Case(T, D, starts, dtype, fused=False)
+    want = c.run(backward=False)
+    x, gate, bias = c.x.cuda(), c.gate.cuda(), c.bias.cuda()
+    s = torch.tensor(c.starts, dtype=torch.int32).cuda() if isinstance(c.starts, list) else None
+    h, st = empty(T, D, dtype=DT[dtype][0]), status()
+    for _ in range(20):
+        state = c.h0.cuda()
+        tw.twell_recur_forward(x, gate, D, bias, s, c.B, state, T, D, DT[dtype][1], h, state, None, st)
+        assert torch.equal(state, want["hT"]) and torch.equal(torch.nan_to_num(h), torch.nan_to_num(want["h"]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_nothing_passes_from_sequence_to_sequence(dtype):
     """NaN and infinities in one sequence, in rows outside and in unused states stay there."""
     starts = [10, 50, 50, 130, 131, 400, 690]
