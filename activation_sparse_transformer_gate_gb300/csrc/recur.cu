@@ -23,9 +23,13 @@
 // itself is not read (5 values an element instead of 6), and its rounding does not
 // enter the gradient.
 #include <cooperative_groups.h>
+#include <limits.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "lm_kernels.h"
+#include "tcgen05.cuh"
 #include "vec16.cuh"
 
 namespace cg = cooperative_groups;
@@ -34,9 +38,8 @@ namespace twell {
 
 namespace {
 
-constexpr int NT = 128;             // threads of a CTA
+constexpr int WARPS = 4;            // of a CTA
 constexpr int MAX_CLUSTER = 8;
-constexpr int FWD_STEPS = 8, BWD_STEPS = 4;  // rows of a thread in a tile
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float CUT = 2.f;          // a C that stands for: nothing comes through
 
@@ -84,32 +87,32 @@ __device__ __forceinline__ void then(float &C, float &H, float C2, float H2) {
   C = !CLEAN && (C == CUT || C2 == CUT) ? CUT : r;
 }
 
-// Geometry of a slab of CX threads of channels: NT / CX groups of S rows a tile.
-// For the scan over the groups a channel has PARTS threads, lanes of one warp, with
-// N consecutive groups each.
-template <typename E, int CX, int S>
+// A warp's slab: 16 channels (32 or 64 bytes of a row), as CX lanes across; GROUPS of
+// lanes take S rows of a tile each.  In the scan over the groups a channel has PARTS
+// lanes with N consecutive groups each.
+template <typename E, int S_>
 struct Geo {
-  static constexpr int N = VEC16<E>, SLAB = CX * N, GROUPS = NT / CX, R = GROUPS * S;
-  static constexpr int PARTS = NT / SLAB, ACROSS = 32 / PARTS;  // a warp's channels in the scan
+  static constexpr int N = VEC16<E>, SLAB = 16, CX = SLAB / N, GROUPS = 32 / CX, S = S_, R = GROUPS * S;
+  static constexpr int PARTS = 32 / SLAB, ACROSS = SLAB;
+  static constexpr uint32_t ALL = (1u << S) - 1;
   static_assert(R % RECUR_KEEP == 0 && RECUR_KEEP % S == 0, "states stand at a group's first row");
-  static_assert(PARTS * N == GROUPS && PARTS <= 32, "a warp holds a channel's groups");
-  static_assert(SLAB >= 16, "columns are exchanged within 16");
+  static_assert(PARTS * N == GROUPS && 32 % S == 0, "lanes hold a channel's groups");
   // Where the step of group q's channel n * CX + cx stands: rows of SLAB pairs, whose
-  // columns are exchanged so that neither the threads of the rows (q and cx vary, n
-  // does not) nor those of the scan (channels and parts vary) meet in a bank.
+  // columns are exchanged so that lanes that differ in q and cx do not meet in a bank
+  // (nor do those of the scan, which differ in channel and part).
   __device__ static __forceinline__ int at(int q, int ch) {
-    return q * SLAB + (ch ^ (((q / N * ACROSS) ^ (q % (16 / CX) * CX)) & 15));
+    return q * SLAB + (ch ^ (q % (SLAB / CX) * CX));
   }
 };
+template <typename E> using Fwd = Geo<E, 8>;
+template <typename E> using Bwd = Geo<E, sizeof(E) == 2 ? 4 : 8>;
 
-// Where sequences begin and end in a tile's rows.  With starts, the CTA marks the
-// rows in shared memory (three tiles' worth, so that marking needs no barrier of
-// its own); without, it follows from the row.
+// Where sequences begin and end in a warp's tile, by rows.  (Without starts it
+// follows from the row.)
 template <int R>
 struct Marks {
-  uint32_t firsts[3][R / 32], lasts[3][R / 32];  // bits of the rows
-  int first[3][R], last[3][R];  // the sequence that begins / ends with a marked row
-  int from[3];                  // the first entry of starts that is not before the tile
+  uint32_t firsts[R / 32], lasts[R / 32];  // bits of the rows
+  int first[R], last[R];                   // the sequence that begins / ends with a marked row
 };
 
 // The first entry of starts[0 .. B] that is >= row (B + 1: none), by one warp.
@@ -129,41 +132,37 @@ __device__ __forceinline__ int first_entry(const RecurParams &p, int row) {
   return lo;
 }
 
-// What has to be done before the barrier that marking stands behind.
+// An open interval of rows that no entry of starts lies in.
+struct Gap {
+  int lo = INT_MAX, hi = INT_MIN;
+};
+
+// Marks a tile's rows; returns whether there are any.  Most tiles lie within a gap
+// that is known already, and cost no look at starts.
 template <int R>
-__device__ __forceinline__ void begin_marks(const RecurParams &p, Marks<R> &m, int buf, int r0) {
-  if (!p.starts) return;
-  if (threadIdx.x < R / 32) m.firsts[buf][threadIdx.x] = m.lasts[buf][threadIdx.x] = 0;
-  static_assert(R / 32 <= NT, "a word a thread");
-  if (threadIdx.x >= NT - 32) {
-    const int s = first_entry(p, r0);
-    if (threadIdx.x == NT - 1) m.from[buf] = s;
-  }
-}
-// Marks a tile's rows.
-template <int R>
-__device__ __forceinline__ void mark(const RecurParams &p, Marks<R> &m, int buf, int r0) {
-  if (!p.starts) return;
-  for (int s = m.from[buf] + (int)threadIdx.x; s <= p.B; s += NT) {
+__device__ __forceinline__ bool mark(const RecurParams &p, Marks<R> &m, Gap &gap, int r0) {
+  if (gap.lo < r0 && gap.hi > r0 + R) return false;
+  const int lane = threadIdx.x & 31;
+  const int from = first_entry(p, r0);
+  gap.lo = from > 0 ? p.starts[from - 1] : INT_MIN;
+  gap.hi = from <= p.B ? p.starts[from] : INT_MAX;
+  __syncwarp();  // (the last tile's marks have been read)
+  if (lane < R / 32) m.firsts[lane] = m.lasts[lane] = 0;
+  __syncwarp();
+  for (int s = from + lane; s <= p.B; s += 32) {
     const int v = p.starts[s], k = v - r0;
     if (v > r0 + R || v < r0) break;  // (below: entries that descend)
     if (s < p.B && k < R && p.starts[s + 1] > v) {
-      m.first[buf][k] = s;
-      atomicOr(&m.firsts[buf][k / 32], 1u << (k & 31));
+      m.first[k] = s;
+      atomicOr(&m.firsts[k / 32], 1u << (k & 31));
     }
     if (s > 0 && k > 0 && p.starts[s - 1] < v) {
-      m.last[buf][k - 1] = s - 1;
-      atomicOr(&m.lasts[buf][(k - 1) / 32], 1u << ((k - 1) & 31));
+      m.last[k - 1] = s - 1;
+      atomicOr(&m.lasts[(k - 1) / 32], 1u << ((k - 1) & 31));
     }
   }
-}
-template <int R>
-__device__ __forceinline__ void first_marks(const RecurParams &p, Marks<R> &m, int r0) {
-  if (!p.starts) return;
-  begin_marks(p, m, 0, r0);
-  __syncthreads();
-  mark(p, m, 0, r0);
-  __syncthreads();
+  __syncwarp();
+  return true;
 }
 
 // Bits of a thread's S rows of a tile.
@@ -178,16 +177,18 @@ __device__ __forceinline__ uint32_t live_rows(int row, int lo, int hi) {
   return (ALL << below) & ALL & ((1u << upto) - 1);
 }
 template <int S, int R>
-__device__ __forceinline__ RowBits row_bits(const RecurParams &p, const Marks<R> &m, int buf, int row,
-                                            int q, uint32_t live) {
+__device__ __forceinline__ RowBits row_bits(const RecurParams &p, Marks<R> &m, Gap &gap, int r0, int q,
+                                            uint32_t live) {
   constexpr uint32_t ALL = (1u << S) - 1;
   RowBits b{0, 0, live};
   if (p.starts) {
-    const int k = q * S;  // (S divides 32: a thread's rows are of one word)
-    b.first = m.firsts[buf][k / 32] >> (k & 31) & ALL;
-    b.last = m.lasts[buf][k / 32] >> (k & 31) & ALL;
-  } else {
-    int at = row % p.len;
+    if (mark(p, m, gap, r0)) {
+      const int k = q * S;  // (S divides 32: a lane's rows are of one word)
+      b.first = m.firsts[k / 32] >> (k & 31) & ALL;
+      b.last = m.lasts[k / 32] >> (k & 31) & ALL;
+    }
+  } else if (p.len < p.T) {
+    int at = (r0 + q * S) % p.len;
     if (at == 0 || at + S >= p.len) {
 #pragma unroll
       for (int i = 0; i < S; ++i) {
@@ -196,18 +197,22 @@ __device__ __forceinline__ RowBits row_bits(const RecurParams &p, const Marks<R>
         b.last |= (uint32_t)(at == 0) << i;
       }
     }
+  } else {
+    const int row = r0 + q * S;
+    b.first = row == 0;
+    if (row < p.T && row + S >= p.T) b.last = 1u << (p.T - 1 - row);
   }
   b.first &= live;
   b.last &= live;
   return b;
 }
 template <int R>
-__device__ __forceinline__ int first_of(const RecurParams &p, const Marks<R> &m, int buf, int r0, int k) {
-  return p.starts ? m.first[buf][k] : (r0 + k) / p.len;
+__device__ __forceinline__ int first_of(const RecurParams &p, const Marks<R> &m, int r0, int k) {
+  return p.starts ? m.first[k] : (r0 + k) / p.len;
 }
 template <int R>
-__device__ __forceinline__ int last_of(const RecurParams &p, const Marks<R> &m, int buf, int r0, int k) {
-  return p.starts ? m.last[buf][k] : (r0 + k) / p.len;
+__device__ __forceinline__ int last_of(const RecurParams &p, const Marks<R> &m, int r0, int k) {
+  return p.starts ? m.last[k] : (r0 + k) / p.len;
 }
 
 // N values of an fp32 [B][D] matrix (zeros without one).
@@ -226,12 +231,12 @@ __device__ __forceinline__ void store_state(float *v, size_t s, int D, int d, co
     *(float4 *)(v + s * D + d + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
 }
 
-// Empty sequences pass `from` on to `to` (zeros without one); the slab's channels
-// [d0, d1), by the cluster's CTAs.  The first slab checks starts.
+// Empty sequences pass `from` on to `to` (zeros without one): the slab's channels from
+// d0 on, by the warps of the cluster's CTAs.  The first slab checks starts.
 __device__ __forceinline__ void empty_sequences(const RecurParams &p, const float *from, float *to,
                                                 int d0, int d1, int rank, int C) {
   if (!p.starts) return;
-  for (long long s = rank * NT + (int)threadIdx.x; s < p.B; s += C * NT) {
+  for (long long s = rank * 32 + (int)(threadIdx.x & 31); s < p.B; s += C * 32) {
     const int a = p.starts[s], b = p.starts[s + 1];
     if (d0 == 0 && (a < 0 || b > p.T || a > b)) set_status(p.status, TWELL_ERR_INDEX);
     if (a == b && to)
@@ -250,16 +255,20 @@ __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
-// A thread's rows of a tile on their way to shared memory: row i to slot[i * NT],
+// A thread's rows of a tile on their way to shared memory: row i to slot[i * 32],
 // which the same thread reads back.
 template <int S, typename E>
 __device__ __forceinline__ void fetch(uint4 *slot, const E *src, long long pitch, int row,
                                       uint32_t live) {
   const uint64_t once = gather_policy<L2_FIRST>();
   const E *at = src + (size_t)row * pitch;
+  if (live == (1u << S) - 1) {
 #pragma unroll
-  for (int i = 0; i < S; ++i, at += pitch)
-    if (live >> i & 1) copy16_async(slot + i * NT, at, once);
+    for (int i = 0; i < S; ++i, at += pitch) copy16_async(slot + i * 32, at, once);
+  } else if (live) {
+    for (int i = 0; i < S; ++i, at += pitch)
+      if (live >> i & 1) copy16_async(slot + i * 32, at, once);
+  }
 }
 
 // The scan over a tile's groups, from the tile's first row on (BACK: from its last):
@@ -269,7 +278,7 @@ template <typename G, bool BACK, bool CLEAN, typename F>
 __device__ __forceinline__ void scan_groups(float2 *steps, F exchange) {
   constexpr int N = G::N, P = G::PARTS, W = G::ACROSS;
   constexpr uint32_t FULL = 0xFFFFFFFFu;
-  const int lane = threadIdx.x & 31, part = lane / W, ch = (int)(threadIdx.x >> 5) * W + lane % W;
+  const int lane = threadIdx.x & 31, part = lane / W, ch = lane % W;
   float2 v[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) v[j] = steps[G::at(part * N + j, ch)];
@@ -303,32 +312,84 @@ __device__ __forceinline__ void scan_groups(float2 *steps, F exchange) {
   }
 }
 
-// What reaches this CTA's tile, from the cluster's tiles' steps in the order of the
-// rows (BACK: against it); `carry` is what reaches the cluster's first one, and then
-// the first one of its next round.  Steps of CTAs that the cluster does not have are
-// (0, 0).
+// The exchange of a slab's steps among the cluster's CTAs: in each round every warp
+// sends its tile's step to the warps of the other CTAs that have the slab, whose
+// barrier counts the bytes.  Two rounds' worth: a warp sends the steps of the round
+// after next only when all have sent, and so have read, the one between.
+struct Exchange {
+  float2 total[2][MAX_CLUSTER][16];  // (0, 0) for CTAs that the cluster does not have
+  uint64_t bar[2];
+};
+
+__device__ __forceinline__ uint32_t peer(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+__device__ __forceinline__ bool arrived(uint32_t bar, uint32_t parity, uint64_t limit) {
+  uint64_t t0 = 0;
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    if (ok) return true;
+    const uint64_t now = global_timer();
+    if (!t0) t0 = now;
+    else if (now - t0 > limit) return false;
+  }
+}
+
+// What reaches this warp's tile of round i, from the cluster's tiles' steps in the
+// order of the rows (BACK: against it); `carry` is what reaches the cluster's first
+// one, and then the first one of its next round.
 template <typename G, bool BACK>
-__device__ __forceinline__ float exchange_totals(cg::cluster_group &cluster, int n, int rank,
-                                                 float2 (*total)[G::SLAB], int ch, int part, float C,
-                                                 float H, float &carry) {
+__device__ __forceinline__ float exchange_totals(Exchange &x, int n, int rank, int i, int ch, int part,
+                                                 float C, float H, float &carry, bool &lost,
+                                                 int32_t *status) {
   if (n == 1) {
     const float in = carry;
     carry = apply(C, H, carry);
     return in;
   }
-  for (int r = part; r < n; r += G::PARTS)
-    *cluster.map_shared_rank(&total[rank][ch], r) = make_float2(C, H);
-  cluster_arrive();
-  cluster_wait();
+  const uint32_t bar = smem_u32(&x.bar[i & 1]), mine = smem_u32(&x.total[i & 1][rank][ch]);
+  if (!lost) {
+    if ((threadIdx.x & 31) == 0) mbar_expect_tx(bar, (uint32_t)n * G::SLAB * sizeof(float2));
+    for (int r = part; r < n; r += G::PARTS)
+      asm volatile(
+          "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+              peer(mine, r)),
+          "f"(C), "f"(H), "r"(peer(bar, r))
+          : "memory");
+    const uint32_t parity = (uint32_t)i >> 1 & 1;
+    if (!arrived(bar, parity, WAIT_LIMIT_NS)) {
+      set_status(status, TWELL_ERR_TIMEOUT);
+      // (what is on its way has to come in before the barrier is used again)
+      lost = !arrived(bar, parity, DRAIN_LIMIT_NS);
+    }
+    lost = __any_sync(0xFFFFFFFFu, lost);
+  }
   float in = carry;
 #pragma unroll
   for (int k = 0; k < MAX_CLUSTER; ++k) {
     const int r = BACK ? MAX_CLUSTER - 1 - k : k;
     if (r == rank) in = carry;
-    const float2 v = total[r][ch];
+    const float2 v = x.total[i & 1][r][ch];
     carry = apply(v.x, v.y, carry);
   }
   return in;
+}
+
+// Before the first exchange, by the whole cluster.
+__device__ __forceinline__ void open_exchange(Exchange &x, int C) {
+  const int lane = threadIdx.x & 31;
+  for (int k = lane; k < 2 * MAX_CLUSTER * 16; k += 32) (&x.total[0][0][0])[k] = make_float2(0.f, 0.f);
+  if (lane < 2) mbar_init(smem_u32(&x.bar[lane]), 1);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  __syncwarp();
+  if (C > 1) cluster_arrive();  // (from here on the others may write here)
 }
 
 // Rounds of a cluster's tiles.
@@ -342,163 +403,182 @@ struct Rounds {
   }
 };
 
-template <typename E, int CX>
-__global__ void __launch_bounds__(NT, 3)
+// What a warp of the forward has in shared memory.
+template <typename E>
+struct FwdShared {
+  using G = Fwd<E>;
+  uint4 x[2][G::S][32], gate[G::S][32];  // x of two tiles, gates of one
+  float2 steps[G::GROUPS * G::SLAB];     // the groups' steps, then what reaches them
+  Exchange exchange;
+  // h0 of the last sequence that begins in each lane's rows: hT may be h0, and who
+  // comes to that sequence's end first is open (the others end with the same lane)
+  float4 held[G::N / 4][32];
+  Marks<G::R> marks;
+};
+
+template <typename E>
+__global__ void __launch_bounds__(32 * WARPS, 3)
 recur_forward_kernel(const E *x, const E *gate, E *h, RecurParams p) {
   pdl_begin();
-  using G = Geo<E, CX, FWD_STEPS>;
-  constexpr int N = G::N, R = G::R, SLAB = G::SLAB, S = FWD_STEPS;
-  constexpr uint32_t ALL = (1u << S) - 1;
-  extern __shared__ uint4 stages[];                  // x of two tiles, gates of one
-  __shared__ Marks<R> marks;
-  __shared__ float2 steps[G::GROUPS * SLAB];         // the groups' steps, then what reaches them
-  __shared__ float2 total[2][MAX_CLUSTER][SLAB];     // the CTAs' steps
-  // h0 of the last sequence that begins in each thread's rows: hT may be h0, and who
-  // comes to that sequence's end first is open (the others end in the same thread)
-  __shared__ float4 held[N / 4][NT];
+  using G = Fwd<E>;
+  constexpr int N = G::N, R = G::R, S = G::S, CX = G::CX;
+  extern __shared__ __align__(16) char shared[];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const int tid = threadIdx.x;
-  for (int k = tid; k < 2 * MAX_CLUSTER * SLAB; k += NT) (&total[0][0][0])[k] = make_float2(0.f, 0.f);
-  __syncthreads();
-  if (C > 1) cluster_arrive();  // (from here on the others may write to this CTA's memory)
-  const int q = tid / CX, cx = tid % CX;
-  const int d0 = (int)(blockIdx.x / C) * SLAB, d = d0 + cx * N;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q = lane / CX, cx = lane % CX;
+  FwdShared<E> &sh = ((FwdShared<E> *)shared)[warp];
+  open_exchange(sh.exchange, C);
+  const int d0 = (int)(blockIdx.x / C * WARPS + warp) * G::SLAB, d = d0 + cx * N;
   const bool on = d < p.D;
-  const int lo = p.starts ? max(0, p.starts[0]) : 0, hi = p.starts ? min(p.T, max(0, p.starts[p.B])) : p.T;
+  const int lo = p.starts ? max(0, p.starts[0]) : 0;
+  const int hi = p.starts ? min(p.T, max(0, p.starts[p.B])) : p.T;
   const Rounds rounds(C, rank, R, p.T);
-  uint4 *const xs = stages + tid, *const gs = stages + 2 * S * NT + tid;
   auto live_of = [&](int i) { return live_rows<S>(rounds.row(i, p.T) + q * S, lo, hi); };
   uint32_t live = live_of(0);
   if (on) {
-    fetch<S>(xs, x + d, p.ld, rounds.row(0, p.T) + q * S, live);
-    fetch<S>(gs, gate + d, p.ld, rounds.row(0, p.T) + q * S, live);
+    fetch<S>(&sh.x[0][0][lane], x + d, p.ld, rounds.row(0, p.T) + q * S, live);
+    fetch<S>(&sh.gate[0][lane], gate + d, p.ld, rounds.row(0, p.T) + q * S, live);
   }
-  empty_sequences(p, p.h0, p.hT, d0, min(p.D, d0 + SLAB), rank, C);
+  empty_sequences(p, p.h0, p.hT, d0, min(p.D, d0 + G::SLAB), rank, C);
   float bias[N];
   load_state(on ? p.bias : nullptr, 0, 0, d, bias);
 #pragma unroll
   for (int n = 0; n < N; ++n) bias[n] *= LOG2E;
-  first_marks(p, marks, rounds.row(0, p.T));
   float carry = 0.f;  // the state before the cluster's next rows, of the scan's channel
+  bool lost = false;
   if (C > 1) cluster_wait();
-  for (int i = 0; i < rounds.n; ++i) {
-    const int r0 = rounds.row(i, p.T), buf = i % 3, row = r0 + q * S;
-    uint4 *const st = xs + (i & 1) * S * NT;
-    const bool more = i + 1 < rounds.n;
+  Gap gap;
+  const int count = d0 < p.D ? rounds.n : 0;
+  for (int i = 0; i < count; ++i) {
+    const int r0 = rounds.row(i, p.T), row = r0 + q * S, b = i & 1;
+    const bool more = i + 1 < count;
     const int r1 = more ? rounds.row(i + 1, p.T) : p.T;
     const uint32_t next = more ? live_of(i + 1) : 0, wanted = on ? next : 0;
+    const RowBits bits = row_bits<S>(p, sh.marks, gap, r0, q, live);
     asm volatile("cp.async.wait_all;" ::: "memory");
-    fetch<S>(xs + (~i & 1) * S * NT, x + d, p.ld, r1 + q * S, wanted);
-    if (more) begin_marks(p, marks, (i + 1) % 3, r1);
-    const RowBits bits = row_bits<S>(p, marks, buf, row, q, live);
-    // this thread's rows as one step
-    float c[S][N], Cs[N], Hs[N];
+    fetch<S>(&sh.x[b ^ 1][0][lane], x + d, p.ld, r1 + q * S, wanted);
+    // Plain: no sequence begins or ends in the warp's tile, and all of its rows are
+    // some sequence's (a row's branches cost as much as its arithmetic).
+    auto round = [&](auto plain) {
+      constexpr bool PLAIN = decltype(plain)::value;
+      // this lane's rows as one step
+      float c[S][N], Cs[N], Hs[N];
 #pragma unroll
-    for (int k = 0; k < S; ++k) {
-      if (k == 0) {
+      for (int n = 0; n < N; ++n) Cs[n] = Hs[n] = 0.f;
 #pragma unroll
-        for (int n = 0; n < N; ++n) Cs[n] = Hs[n] = 0.f;
+      for (int k = 0; k < S; ++k) {
+        if (!PLAIN && (bits.first >> k & 1)) {
+          load_state(on ? p.h0 : nullptr, first_of(p, sh.marks, r0, q * S + k), p.D, d, Hs);
+#pragma unroll
+          for (int n = 0; n < N; n += 4)
+            sh.held[n / 4][lane] = make_float4(Hs[n], Hs[n + 1], Hs[n + 2], Hs[n + 3]);
+        }
+        float xv[N], gv[N];
+        unpack(sh.x[b][k][lane], xv, (E *)nullptr);
+        unpack(sh.gate[k][lane], gv, (E *)nullptr);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          c[k][n] = taken(ex2_approx(fmaf(gv[n], LOG2E, bias[n])));
+          Hs[n] = fmaf(c[k][n], xv[n] - Hs[n], Hs[n]);
+          Cs[n] = fmaf(-Cs[n], c[k][n], Cs[n]) + c[k][n];
+        }
+        if (!PLAIN && !(live >> k & 1)) {  // (what was not read may be anything)
+#pragma unroll
+          for (int n = 0; n < N; ++n) Hs[n] = 0.f;
+        }
       }
-      if (bits.first >> k & 1) {
-        load_state(on ? p.h0 : nullptr, first_of(p, marks, buf, r0, q * S + k), p.D, d, Hs);
+      fetch<S>(&sh.gate[0][lane], gate + d, p.ld, r1 + q * S, wanted);
+      const bool cut = !PLAIN && (bits.first != 0 || live != G::ALL);
 #pragma unroll
-        for (int n = 0; n < N; n += 4)
-          held[n / 4][tid] = make_float4(Hs[n], Hs[n + 1], Hs[n + 2], Hs[n + 3]);
-      }
-      float xv[N], gv[N];
-      unpack(st[k * NT], xv, (E *)nullptr);
-      unpack(gs[k * NT], gv, (E *)nullptr);
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        c[k][n] = taken(ex2_approx(fmaf(gv[n], LOG2E, bias[n])));
-        Hs[n] = fmaf(c[k][n], xv[n] - Hs[n], Hs[n]);
-        Cs[n] = fmaf(-Cs[n], c[k][n], Cs[n]) + c[k][n];
-      }
-      if (!(live >> k & 1)) {  // (what was not read may be anything)
-#pragma unroll
-        for (int n = 0; n < N; ++n) Hs[n] = 0.f;
-      }
-    }
-    fetch<S>(gs, gate + d, p.ld, r1 + q * S, wanted);
-    const bool cut = bits.first != 0 || live != ALL;
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-      steps[G::at(q, n * CX + cx)] = make_float2(cut ? CUT : Cs[n], Hs[n]);
-    const bool cuts = __syncthreads_or(cut);
-    if (more) mark(p, marks, (i + 1) % 3, r1);
-    auto exchange = [&](int ch, int part, float Ct, float Ht) {
-      return exchange_totals<G, false>(cluster, C, rank, total[i & 1], ch, part, Ct, Ht, carry);
-    };
-    if (cuts) scan_groups<G, false, false>(steps, exchange);
-    else scan_groups<G, false, true>(steps, exchange);
-    __syncthreads();
-    // the rows once more, from the state before them
-    if (on) {
+      for (int n = 0; n < N; ++n)
+        sh.steps[G::at(q, n * CX + cx)] = make_float2(cut ? CUT : Cs[n], Hs[n]);
+      __syncwarp();
+      scan_groups<G, false, PLAIN>(sh.steps, [&](int ch, int part, float Ct, float Ht) {
+        return exchange_totals<G, false>(sh.exchange, C, rank, i, ch, part, Ct, Ht, carry, lost,
+                                         p.status);
+      });
+      __syncwarp();
+      // the rows once more, from the state before them
       float y[N];
 #pragma unroll
-      for (int n = 0; n < N; ++n) y[n] = steps[G::at(q, n * CX + cx)].x;
+      for (int n = 0; n < N; ++n) y[n] = sh.steps[G::at(q, n * CX + cx)].x;
+      if (!on) return;
       if (p.states && row % RECUR_KEEP == 0 && row < p.T)
         store_state(p.states, row / RECUR_KEEP, p.D, d, y);
       E *out = h + (size_t)row * p.D + d;
 #pragma unroll
       for (int k = 0; k < S; ++k, out += p.D) {
         float xv[N];
-        unpack(st[k * NT], xv, (E *)nullptr);
-        if (!(live >> k & 1)) continue;
-        if (bits.first >> k == 1) {
+        unpack(sh.x[b][k][lane], xv, (E *)nullptr);
+        if (!PLAIN) {
+          if (!(live >> k & 1)) continue;
+          if (bits.first >> k == 1) {
 #pragma unroll
-          for (int n = 0; n < N; n += 4) {
-            const float4 v = held[n / 4][tid];
-            y[n] = v.x; y[n + 1] = v.y; y[n + 2] = v.z; y[n + 3] = v.w;
+            for (int n = 0; n < N; n += 4) {
+              const float4 v = sh.held[n / 4][lane];
+              y[n] = v.x; y[n + 1] = v.y; y[n + 2] = v.z; y[n + 3] = v.w;
+            }
+          } else if (bits.first >> k & 1) {
+            load_state(p.h0, first_of(p, sh.marks, r0, q * S + k), p.D, d, y);
           }
-        } else if (bits.first >> k & 1) {
-          load_state(p.h0, first_of(p, marks, buf, r0, q * S + k), p.D, d, y);
         }
 #pragma unroll
         for (int n = 0; n < N; ++n) y[n] = fmaf(c[k][n], xv[n] - y[n], y[n]);
         *(uint4 *)out = pack16(y, (E *)nullptr);
-        if ((bits.last >> k & 1) && p.hT)
-          store_state(p.hT, last_of(p, marks, buf, r0, q * S + k), p.D, d, y);
+        if (!PLAIN && (bits.last >> k & 1) && p.hT)
+          store_state(p.hT, last_of(p, sh.marks, r0, q * S + k), p.D, d, y);
       }
-    }
+    };
+    if (__all_sync(0xFFFFFFFFu, (bits.first | bits.last) == 0 && live == G::ALL))
+      round(std::true_type{});
+    else
+      round(std::false_type{});
     live = next;
+  }
+  // (nothing is on its way to this CTA any more, unless a wait has given up)
+  if (C > 1) {
+    cluster_arrive();
+    cluster_wait();
   }
 }
 
-template <typename E, int CX>
-__global__ void __launch_bounds__(NT, 3)
+// What a warp of the backward has in shared memory.
+template <typename E>
+struct BwdShared {
+  using G = Bwd<E>;
+  uint4 x[2][G::S][32], dh[2][G::S][32], gate[G::S][32];
+  float2 steps[2][G::GROUPS * G::SLAB];  // the groups' steps: h forward, a G back
+  Exchange exchange;
+  float bias[MAX_CLUSTER][G::SLAB];      // the CTAs' sums of dgate
+  Marks<G::R> marks;
+};
+
+template <typename E>
+__global__ void __launch_bounds__(32 * WARPS, 3)
 recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, RecurParams p) {
   pdl_begin();
-  using G = Geo<E, CX, BWD_STEPS>;
-  constexpr int N = G::N, R = G::R, SLAB = G::SLAB, S = BWD_STEPS;
-  constexpr uint32_t ALL = (1u << S) - 1;
-  extern __shared__ uint4 stages[];                  // x and dh of two tiles, gates of one
-  __shared__ Marks<R> marks;
-  __shared__ float2 steps[2][G::GROUPS * SLAB];      // the groups' steps: h forward, a G back
-  __shared__ float2 total[2][MAX_CLUSTER][SLAB];     // the CTAs' steps back
+  using G = Bwd<E>;
+  constexpr int N = G::N, R = G::R, S = G::S, CX = G::CX;
+  extern __shared__ __align__(16) char shared[];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int k = tid; k < 2 * MAX_CLUSTER * SLAB; k += NT) (&total[0][0][0])[k] = make_float2(0.f, 0.f);
-  __syncthreads();
-  if (C > 1) cluster_arrive();
-  const int q = tid / CX, cx = tid % CX;
-  const int d0 = (int)(blockIdx.x / C) * SLAB, d = d0 + cx * N;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q = lane / CX, cx = lane % CX;
+  BwdShared<E> &sh = ((BwdShared<E> *)shared)[warp];
+  open_exchange(sh.exchange, C);
+  const int d0 = (int)(blockIdx.x / C * WARPS + warp) * G::SLAB, d = d0 + cx * N;
   const bool on = d < p.D;
-  const int lo = p.starts ? max(0, p.starts[0]) : 0, hi = p.starts ? min(p.T, max(0, p.starts[p.B])) : p.T;
+  const int lo = p.starts ? max(0, p.starts[0]) : 0;
+  const int hi = p.starts ? min(p.T, max(0, p.starts[p.B])) : p.T;
   const Rounds rounds(C, rank, R, p.T);
   auto first_row = [&](int i) { return rounds.row(rounds.n - 1 - i, p.T); };  // from the last on
-  uint4 *const xs = stages + tid, *const ds = stages + 2 * S * NT + tid,
-        *const gs = stages + 4 * S * NT + tid;
   auto live_of = [&](int i) { return live_rows<S>(first_row(i) + q * S, lo, hi); };
   uint32_t live = live_of(0);
   if (on) {
-    fetch<S>(xs, x + d, p.ld, first_row(0) + q * S, live);
-    fetch<S>(ds, dh + d, p.D, first_row(0) + q * S, live);
-    fetch<S>(gs, gate + d, p.ld, first_row(0) + q * S, live);
+    fetch<S>(&sh.x[0][0][lane], x + d, p.ld, first_row(0) + q * S, live);
+    fetch<S>(&sh.dh[0][0][lane], dh + d, p.D, first_row(0) + q * S, live);
+    fetch<S>(&sh.gate[0][lane], gate + d, p.ld, first_row(0) + q * S, live);
   }
-  empty_sequences(p, p.dhT, p.dh0, d0, min(p.D, d0 + SLAB), rank, C);
+  empty_sequences(p, p.dhT, p.dh0, d0, min(p.D, d0 + G::SLAB), rank, C);
   float bias[N], db[N];
   load_state(on ? p.bias : nullptr, 0, 0, d, bias);
 #pragma unroll
@@ -506,97 +586,92 @@ recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, R
     bias[n] *= LOG2E;
     db[n] = 0.f;
   }
-  first_marks(p, marks, first_row(0));
   float carry = 0.f;  // a G behind the cluster's next rows, of the scan's channel
-  const int sc = warp * G::ACROSS + lane % G::ACROSS, sd = d0 + sc % CX * N + sc / CX;
+  bool lost = false;
+  const int sc = lane % G::ACROSS, sd = d0 + sc % CX * N + sc / CX;  // that channel
   if (C > 1) cluster_wait();
-  for (int i = 0; i < rounds.n; ++i) {
-    const int r0 = first_row(i), buf = i % 3, row = r0 + q * S;
-    uint4 *const xt = xs + (i & 1) * S * NT, *const dt = ds + (i & 1) * S * NT;
-    const bool more = i + 1 < rounds.n;
+  Gap gap;
+  const int count = d0 < p.D ? rounds.n : 0;
+  for (int i = 0; i < count; ++i) {
+    const int r0 = first_row(i), row = r0 + q * S, b = i & 1;
+    const bool more = i + 1 < count;
     const int r1 = more ? first_row(i + 1) : p.T;
     const uint32_t next = more ? live_of(i + 1) : 0, wanted = on ? next : 0;
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    fetch<S>(xs + (~i & 1) * S * NT, x + d, p.ld, r1 + q * S, wanted);
-    fetch<S>(ds + (~i & 1) * S * NT, dh + d, p.D, r1 + q * S, wanted);
-    if (more) begin_marks(p, marks, (i + 1) % 3, r1);
     // (the state before the tile; where its first row begins a sequence it is not used)
     const float before = sd < p.D && r0 > 0 && r0 < p.T
                              ? p.states[(size_t)(r0 / RECUR_KEEP) * p.D + sd] : 0.f;
-    const RowBits bits = row_bits<S>(p, marks, buf, row, q, live);
-    float e[S][N], Cs[N], Hs[N], c[S][N];
+    const RowBits bits = row_bits<S>(p, sh.marks, gap, r0, q, live);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    fetch<S>(&sh.x[b ^ 1][0][lane], x + d, p.ld, r1 + q * S, wanted);
+    fetch<S>(&sh.dh[b ^ 1][0][lane], dh + d, p.D, r1 + q * S, wanted);
+    auto round = [&](auto plain) {  // (as in the forward)
+      constexpr bool PLAIN = decltype(plain)::value;
+      float e[S][N], Cs[N], Hs[N], c[S][N];
 #pragma unroll
-    for (int n = 0; n < N; ++n) Cs[n] = Hs[n] = 0.f;
+      for (int n = 0; n < N; ++n) Cs[n] = Hs[n] = 0.f;
 #pragma unroll
-    for (int k = 0; k < S; ++k) {
-      if (bits.first >> k & 1)
-        load_state(on ? p.h0 : nullptr, first_of(p, marks, buf, r0, q * S + k), p.D, d, Hs);
-      float xv[N], gv[N];
-      unpack(xt[k * NT], xv, (E *)nullptr);
-      unpack(gs[k * NT], gv, (E *)nullptr);
+      for (int k = 0; k < S; ++k) {
+        if (!PLAIN && (bits.first >> k & 1))
+          load_state(on ? p.h0 : nullptr, first_of(p, sh.marks, r0, q * S + k), p.D, d, Hs);
+        float xv[N], gv[N];
+        unpack(sh.x[b][k][lane], xv, (E *)nullptr);
+        unpack(sh.gate[k][lane], gv, (E *)nullptr);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          e[k][n] = ex2_held(fmaf(gv[n], LOG2E, bias[n]));
+          c[k][n] = taken(e[k][n]);
+          Hs[n] = fmaf(c[k][n], xv[n] - Hs[n], Hs[n]);
+          Cs[n] = fmaf(-Cs[n], c[k][n], Cs[n]) + c[k][n];
+        }
+        if (!PLAIN && !(live >> k & 1)) {
+#pragma unroll
+          for (int n = 0; n < N; ++n) Hs[n] = 0.f;
+        }
+      }
+      fetch<S>(&sh.gate[0][lane], gate + d, p.ld, r1 + q * S, wanted);
+      const bool dead = !PLAIN && live != G::ALL;
+      const bool cutF = !PLAIN && (dead || bits.first), cutB = !PLAIN && (dead || bits.last);
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        e[k][n] = ex2_held(fmaf(gv[n], LOG2E, bias[n]));
-        c[k][n] = taken(e[k][n]);
-        Hs[n] = fmaf(c[k][n], xv[n] - Hs[n], Hs[n]);
-        Cs[n] = fmaf(-Cs[n], c[k][n], Cs[n]) + c[k][n];
+        sh.steps[0][G::at(q, n * CX + cx)] = make_float2(cutF ? CUT : Cs[n], Hs[n]);
+        Hs[n] = 0.f;
       }
-      if (!(live >> k & 1)) {
 #pragma unroll
-        for (int n = 0; n < N; ++n) Hs[n] = 0.f;
+      for (int k = S - 1; k >= 0; --k) {
+        if (!PLAIN && (bits.last >> k & 1))
+          load_state(on ? p.dhT : nullptr, last_of(p, sh.marks, r0, q * S + k), p.D, d, Hs);
+        float dv[N];
+        unpack(sh.dh[b][k][lane], dv, (E *)nullptr);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          const float g = dv[n] + Hs[n];
+          Hs[n] = fmaf(-c[k][n], g, g);
+        }
+        if (!PLAIN && !(live >> k & 1)) {
+#pragma unroll
+          for (int n = 0; n < N; ++n) Hs[n] = 0.f;
+        }
       }
-    }
-    fetch<S>(gs, gate + d, p.ld, r1 + q * S, wanted);
-    const bool gap = live != ALL, cutF = gap || bits.first, cutB = gap || bits.last;
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      steps[0][G::at(q, n * CX + cx)] = make_float2(cutF ? CUT : Cs[n], Hs[n]);
-      Hs[n] = 0.f;
-    }
-#pragma unroll
-    for (int k = S - 1; k >= 0; --k) {
-      if (bits.last >> k & 1)
-        load_state(on ? p.dhT : nullptr, last_of(p, marks, buf, r0, q * S + k), p.D, d, Hs);
-      float dv[N];
-      unpack(dt[k * NT], dv, (E *)nullptr);
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const float g = dv[n] + Hs[n];
-        Hs[n] = fmaf(-c[k][n], g, g);
-      }
-      if (!(live >> k & 1)) {
-#pragma unroll
-        for (int n = 0; n < N; ++n) Hs[n] = 0.f;
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-      steps[1][G::at(q, n * CX + cx)] = make_float2(cutB ? CUT : Cs[n], Hs[n]);
-    const bool cuts = __syncthreads_or(cutF || cutB);
-    if (more) mark(p, marks, (i + 1) % 3, r1);
-    auto forward = [&](int, int, float, float) { return before; };
-    auto exchange = [&](int ch, int part, float Ct, float Ht) {
-      return exchange_totals<G, true>(cluster, C, rank, total[i & 1], ch, part, Ct, Ht, carry);
-    };
-    if (cuts) {
-      scan_groups<G, false, false>(steps[0], forward);
-      scan_groups<G, true, false>(steps[1], exchange);
-    } else {
-      scan_groups<G, false, true>(steps[0], forward);
-      scan_groups<G, true, true>(steps[1], exchange);
-    }
-    __syncthreads();
-    if (on) {
+      for (int n = 0; n < N; ++n)
+        sh.steps[1][G::at(q, n * CX + cx)] = make_float2(cutB ? CUT : Cs[n], Hs[n]);
+      __syncwarp();
+      scan_groups<G, false, PLAIN>(sh.steps[0], [&](int, int, float, float) { return before; });
+      scan_groups<G, true, PLAIN>(sh.steps[1], [&](int ch, int part, float Ct, float Ht) {
+        return exchange_totals<G, true>(sh.exchange, C, rank, i, ch, part, Ct, Ht, carry, lost,
+                                        p.status);
+      });
+      __syncwarp();
       float y[N];
 #pragma unroll
-      for (int n = 0; n < N; ++n) y[n] = steps[0][G::at(q, n * CX + cx)].x;
+      for (int n = 0; n < N; ++n) y[n] = sh.steps[0][G::at(q, n * CX + cx)].x;
       // e := (h_{t-1} - x_t) a c
 #pragma unroll
       for (int k = 0; k < S; ++k) {
-        if (bits.first >> k & 1)
-          load_state(p.h0, first_of(p, marks, buf, r0, q * S + k), p.D, d, y);
+        if (!PLAIN && on && (bits.first >> k & 1))
+          load_state(p.h0, first_of(p, sh.marks, r0, q * S + k), p.D, d, y);
         float xv[N];
-        unpack(xt[k * NT], xv, (E *)nullptr);
+        unpack(sh.x[b][k][lane], xv, (E *)nullptr);
 #pragma unroll
         for (int n = 0; n < N; ++n) {
           const float took = (y[n] - xv[n]) * c[k][n];
@@ -605,15 +680,18 @@ recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, R
         }
       }
 #pragma unroll
-      for (int n = 0; n < N; ++n) y[n] = steps[1][G::at(q, n * CX + cx)].x;
+      for (int n = 0; n < N; ++n) y[n] = sh.steps[1][G::at(q, n * CX + cx)].x;
+      if (!on) return;
       E *px = dx + (size_t)row * p.ld + d, *pg = dgate + (size_t)row * p.ld + d;
 #pragma unroll
       for (int k = S - 1; k >= 0; --k) {
-        if (!(live >> k & 1)) continue;
-        if (bits.last >> k & 1)
-          load_state(p.dhT, last_of(p, marks, buf, r0, q * S + k), p.D, d, y);
+        if (!PLAIN) {
+          if (!(live >> k & 1)) continue;
+          if (bits.last >> k & 1)
+            load_state(p.dhT, last_of(p, sh.marks, r0, q * S + k), p.D, d, y);
+        }
         float dv[N], gv[N];
-        unpack(dt[k * NT], dv, (E *)nullptr);
+        unpack(sh.dh[b][k][lane], dv, (E *)nullptr);
 #pragma unroll
         for (int n = 0; n < N; ++n) {
           const float g = dv[n] + y[n];
@@ -624,48 +702,41 @@ recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, R
         }
         *(uint4 *)(px + k * p.ld) = pack16(dv, (E *)nullptr);
         *(uint4 *)(pg + k * p.ld) = pack16(gv, (E *)nullptr);
-        if ((bits.first >> k & 1) && p.dh0)
-          store_state(p.dh0, first_of(p, marks, buf, r0, q * S + k), p.D, d, y);
+        if (!PLAIN && (bits.first >> k & 1) && p.dh0)
+          store_state(p.dh0, first_of(p, sh.marks, r0, q * S + k), p.D, d, y);
       }
-    }
+    };
+    if (__all_sync(0xFFFFFFFFu, (bits.first | bits.last) == 0 && live == G::ALL))
+      round(std::true_type{});
+    else
+      round(std::false_type{});
     live = next;
   }
-  if (!p.dbias) return;
-  // the bias' gradient: groups of a warp, warps, CTAs, each in order (by way of the
-  // totals that the last round does not read)
-  __shared__ float warps[NT / 32][SLAB];
+  // the bias' gradient: the warp's groups, then the CTAs, in order
 #pragma unroll
   for (int n = 0; n < N; ++n) {
 #pragma unroll
     for (int o = 16; o >= CX; o /= 2) db[n] += __shfl_down_sync(0xFFFFFFFFu, db[n], o);
-    if (lane < CX) warps[warp][cx * N + n] = db[n];
+    if (lane < CX) *cluster.map_shared_rank(&sh.bias[rank][cx * N + n], 0) = db[n];
   }
-  __syncthreads();
+  cluster_arrive();
+  cluster_wait();
+  if (rank != 0 || !p.dbias || lane >= G::SLAB || d0 + lane >= p.D) return;
   float sum = 0.f;
-  if (tid < SLAB) {
-#pragma unroll
-    for (int w = 0; w < NT / 32; ++w) sum += warps[w][tid];
-    if (C > 1) cluster.map_shared_rank(&total[rounds.n & 1][rank][tid], 0)->x = sum;
-  }
-  if (C > 1) {
-    cluster_arrive();
-    cluster_wait();
-    if (rank != 0) return;
-    sum = 0.f;
-    if (tid < SLAB)
-      for (int r = 0; r < C; ++r) sum += total[rounds.n & 1][r][tid].x;
-  }
-  if (tid < SLAB && d0 + tid < p.D) p.dbias[d0 + tid] = sum;
+  for (int r = 0; r < C; ++r) sum += sh.bias[r][lane];
+  p.dbias[d0 + lane] = sum;
 }
 
 // Sequences of one row (a decoded token each): a thread for 16 bytes.
+constexpr int STEP_THREADS = 128;
+
 template <typename E>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(STEP_THREADS)
 recur_step_kernel(const E *x, const E *gate, E *h, RecurParams p) {
   pdl_begin();
   constexpr int N = VEC16<E>;
   const int per = p.D / N;
-  const long long k = (long long)blockIdx.x * NT + threadIdx.x;
+  const long long k = (long long)blockIdx.x * STEP_THREADS + threadIdx.x;
   const int row = (int)(k / per), d = (int)(k % per) * N;
   if (row >= p.T) return;
   float xv[N], gv[N], y[N], bias[N];
@@ -695,7 +766,7 @@ template <typename K>
 int resident_clusters(K kern, size_t smem, int C) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)C);
-  cfg.blockDim = dim3(NT);
+  cfg.blockDim = dim3(32 * WARPS);
   cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -726,76 +797,52 @@ struct Shape {
     int C = 1;
     for (int k = 2; k <= MAX_CLUSTER && k <= tiles; ++k)
       if (fit[k] >= slabs) C = k;
-    if (const char *e = getenv("RECUR_CL")) C = min(tiles, atoi(e));
+    if (const char *e = getenv("RECUR_CL")) C = tiles < atoi(e) ? tiles : atoi(e);
     return C;
   }
 };
 
-template <typename E, int CX>
+template <typename E>
 cudaError_t forward_t(const RecurArgs &a, cudaStream_t s) {
-  using G = Geo<E, CX, FWD_STEPS>;
-  constexpr int SMEM = 3 * FWD_STEPS * NT * 16;
-  auto kern = recur_forward_kernel<E, CX>;
-  static const Shape<decltype(kern)> shape(kern, SMEM);
-  if (shape.attr != cudaSuccess) return shape.attr;
-  const int slabs = (a.D + G::SLAB - 1) / G::SLAB, C = shape.cluster(slabs, (a.T + G::R - 1) / G::R);
-  return launch_clusters(kern, dim3((unsigned)(slabs * C)), dim3(NT), SMEM, C, s, (const E *)a.x,
-                         (const E *)a.gate, (E *)a.h, params_of(a));
-}
-
-template <typename E, int CX>
-cudaError_t backward_t(const RecurArgs &a, cudaStream_t s) {
-  using G = Geo<E, CX, BWD_STEPS>;
-  constexpr int SMEM = 5 * BWD_STEPS * NT * 16;
-  auto kern = recur_backward_kernel<E, CX>;
-  static const Shape<decltype(kern)> shape(kern, SMEM);
-  if (shape.attr != cudaSuccess) return shape.attr;
-  const int slabs = (a.D + G::SLAB - 1) / G::SLAB, C = shape.cluster(slabs, (a.T + G::R - 1) / G::R);
-  return launch_clusters(kern, dim3((unsigned)(slabs * C)), dim3(NT), SMEM, C, s, (const E *)a.x,
-                         (const E *)a.gate, (const E *)a.dh, (E *)a.dx, (E *)a.dgate, params_of(a));
-}
-
-// Channels of a slab: 128 bytes of a row, or less where the grid would not fill the SMs.
-template <typename E>
-int threads_across(const RecurArgs &a) {
-  const int vecs = a.D / VEC16<E>;
-  int cx = 8;
-  const int least = 16 / VEC16<E>;  // (a slab has 16 channels at least)
-  while (cx > least && (vecs + cx - 1) / cx * MAX_CLUSTER < num_sms()) cx /= 2;
-  if (const char *e = getenv("RECUR_CX")) cx = atoi(e);
-  if (cx < least) cx = least;
-  return cx;
-}
-
-template <typename E>
-cudaError_t forward_e(const RecurArgs &a, cudaStream_t s) {
   if (!a.starts && a.B == a.T) {
     const long long vecs = (long long)a.T * (a.D / VEC16<E>);
-    return launch_k(recur_step_kernel<E>, dim3((unsigned)((vecs + NT - 1) / NT)), dim3(NT), 0, s,
-                    (const E *)a.x, (const E *)a.gate, (E *)a.h, params_of(a));
+    return launch_k(recur_step_kernel<E>, dim3((unsigned)((vecs + STEP_THREADS - 1) / STEP_THREADS)),
+                    dim3(STEP_THREADS), 0, s, (const E *)a.x, (const E *)a.gate, (E *)a.h,
+                    params_of(a));
   }
-  const int cx = threads_across<E>(a);
-  if constexpr (VEC16<E> == 8)
-    if (cx == 2) return forward_t<E, 2>(a, s);
-  return cx == 8 ? forward_t<E, 8>(a, s) : forward_t<E, 4>(a, s);
+  using G = Fwd<E>;
+  constexpr int SMEM = WARPS * sizeof(FwdShared<E>);
+  auto kern = recur_forward_kernel<E>;
+  static const Shape<decltype(kern)> shape(kern, SMEM);
+  if (shape.attr != cudaSuccess) return shape.attr;
+  const int wide = WARPS * G::SLAB, ctas = (a.D + wide - 1) / wide;
+  const int C = shape.cluster(ctas, (a.T + G::R - 1) / G::R);
+  return launch_clusters(kern, dim3((unsigned)(ctas * C)), dim3(32 * WARPS), SMEM, C, s,
+                         (const E *)a.x, (const E *)a.gate, (E *)a.h, params_of(a));
 }
 
 template <typename E>
-cudaError_t backward_e(const RecurArgs &a, cudaStream_t s) {
-  const int cx = threads_across<E>(a);
-  if constexpr (VEC16<E> == 8)
-    if (cx == 2) return backward_t<E, 2>(a, s);
-  return cx == 8 ? backward_t<E, 8>(a, s) : backward_t<E, 4>(a, s);
+cudaError_t backward_t(const RecurArgs &a, cudaStream_t s) {
+  using G = Bwd<E>;
+  constexpr int SMEM = WARPS * sizeof(BwdShared<E>);
+  auto kern = recur_backward_kernel<E>;
+  static const Shape<decltype(kern)> shape(kern, SMEM);
+  if (shape.attr != cudaSuccess) return shape.attr;
+  const int wide = WARPS * G::SLAB, ctas = (a.D + wide - 1) / wide;
+  const int C = shape.cluster(ctas, (a.T + G::R - 1) / G::R);
+  return launch_clusters(kern, dim3((unsigned)(ctas * C)), dim3(32 * WARPS), SMEM, C, s,
+                         (const E *)a.x, (const E *)a.gate, (const E *)a.dh, (E *)a.dx, (E *)a.dgate,
+                         params_of(a));
 }
 
 }  // namespace
 
 cudaError_t launch_recur_forward(const RecurArgs &a, cudaStream_t s) {
-  return a.dtype == TWELL_BF16 ? forward_e<bf16>(a, s) : forward_e<float>(a, s);
+  return a.dtype == TWELL_BF16 ? forward_t<bf16>(a, s) : forward_t<float>(a, s);
 }
 
 cudaError_t launch_recur_backward(const RecurArgs &a, cudaStream_t s) {
-  return a.dtype == TWELL_BF16 ? backward_e<bf16>(a, s) : backward_e<float>(a, s);
+  return a.dtype == TWELL_BF16 ? backward_t<bf16>(a, s) : backward_t<float>(a, s);
 }
 
 }  // namespace twell
