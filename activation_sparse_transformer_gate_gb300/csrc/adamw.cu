@@ -58,14 +58,20 @@ __device__ __forceinline__ uint32_t noise_of(unsigned long long i, uint32_t seed
 }
 
 // y in [0, 448] (a rounding above at most) as e4m3, rounded down after the noise
-// has been added below the three mantissa bits: up with the chance of what is cut
-// off, to 2^-16.  Below 2^-6 the code's step is 2^-9, which is the mantissa's step
-// from 2^-6 to 2^-5.
+// (16 bits, in place) has been added below the three mantissa bits: up with the
+// chance of what is cut off, to 2^-16.  Below 2^-6 the code's step is 2^-9, which is
+// the mantissa's step from 2^-6 to 2^-5.
 __device__ __forceinline__ uint32_t to_code(float y, uint32_t noise) {
   const bool small = y < 0x1p-6f;
-  const float z = small ? __fadd_rn(y, 0x1p-6f) : y;
-  const int code = (int)((__float_as_uint(z) + (noise << 4)) >> 20) - (small ? 968 : 960);
-  return (uint32_t)min(code, 126);
+  if (small) y = __fadd_rn(y, 0x1p-6f);
+  return (__float_as_uint(y) + noise - (small ? 968u << 20 : 960u << 20)) >> 20;
+}
+
+// The larger magnitude; NaN if there is one.
+__device__ __forceinline__ float top_of(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
 }
 
 // Four codes as values.
@@ -93,12 +99,12 @@ struct Step {
     m = __fadd_rn(__fmul_rn(m, b1), __fmul_rn(g, o1));
     v = __fadd_rn(__fmul_rn(v, b2), __fmul_rn(__fmul_rn(g, g), o2));
     r = __fsqrt_rn(v);
-    p = fmaf(-step, __fdiv_rn(m, fmaf(r, isq, eps)), fmaf(-shrink, p, p));
+    p = fmaf(-step, __fdividef(m, fmaf(r, isq, eps)), fmaf(-shrink, p, p));
   }
 };
 
 template <typename G, int BITS, int N>
-__global__ void __launch_bounds__(32 * WARPS)
+__global__ void __launch_bounds__(32 * WARPS, 4)
 adamw_kernel(const __grid_constant__ Table<N> table, const Scalars sc) {
   pdl_begin();
   // the tensor of this CTA's chunk of WARPS blocks
@@ -135,8 +141,7 @@ adamw_kernel(const __grid_constant__ Table<N> table, const Scalars sc) {
     vs = e.vs[block];
   }
   float P[2][4], M[2][4], R[2][4];  // (R: v for fp32 states, sqrt(v) for 8 bits)
-  uint32_t topm = 0, topr = 0;      // largest magnitudes, as bits (NaN is the largest)
-  bool positive[2][4];
+  float topm = 0.f, topr = 0.f;     // largest magnitudes
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int at = h * 128 + lane * 4;
@@ -181,35 +186,39 @@ adamw_kernel(const __grid_constant__ Table<N> table, const Scalars sc) {
       float r;
       st(P[h][i], gr[i], M[h][i], v[i], r);
       R[h][i] = BITS == 32 ? v[i] : r;
-      positive[h][i] = v[i] > 0.f;
-      if (BITS == 8 && at + i < left) {
-        topm = max(topm, __float_as_uint(M[h][i]) & 0x7FFFFFFFu);
-        topr = max(topr, __float_as_uint(r) & 0x7FFFFFFFu);
+      if (BITS == 8) {  // (elements that the tensor does not have are 0)
+        topm = top_of(topm, M[h][i]);
+        topr = top_of(topr, r);
       }
     }
   }
   uint32_t cm[2] = {0, 0}, cr[2] = {0, 0};
   if (BITS == 8) {
-    topm = __reduce_max_sync(0xFFFFFFFFu, topm);
-    topr = __reduce_max_sync(0xFFFFFFFFu, topr);
-    const bool okm = topm < 0x7F800000u, okr = topr < 0x7F800000u;
-    const float tm = fmaxf(__uint_as_float(topm), 1e-30f), tr = fmaxf(__uint_as_float(topr), 1e-30f);
+    // (as bits, magnitudes are ordered, with NaN above infinity)
+    const uint32_t bm = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(topm) & 0x7FFFFFFFu);
+    const uint32_t br = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(topr) & 0x7FFFFFFFu);
+    const bool okm = bm < 0x7F800000u, okr = br < 0x7F800000u;
+    const float tm = fmaxf(__uint_as_float(bm), 1e-30f), tr = fmaxf(__uint_as_float(br), 1e-30f);
     const float im = __fdiv_rn(448.f, tm), ir = __fdiv_rn(448.f, tr);
     if (lane == 0) {
       e.ms[block] = okm ? __fmul_rn(tm, 1.f / 448.f) : NAN;
       e.vs[block] = okr ? __fmul_rn(tr, 1.f / 448.f) : NAN;
     }
+    const unsigned long long first = (unsigned long long)(e.first + i0 + lane * 4);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t u = noise_of((unsigned long long)(e.first + i0 + h * 128 + lane * 4 + i), seed);
-        const uint32_t a = to_code(__fmul_rn(fabsf(M[h][i]), im), u & 0xFFFFu) |
-                           (M[h][i] < 0.f ? 0x80u : 0u);
-        const uint32_t b = max(to_code(__fmul_rn(R[h][i], ir), u >> 16), positive[h][i] ? 1u : 0u);
-        cm[h] |= (okm ? a : 0u) << (8 * i);
-        cr[h] |= (okr ? b : 0u) << (8 * i);
+        const uint32_t u = noise_of(first + h * 128 + i, seed);
+        const uint32_t a = to_code(__fmul_rn(fabsf(M[h][i]), im), u << 4 & 0xFFFF0u);
+        const uint32_t b = to_code(__fmul_rn(R[h][i], ir), u >> 12 & 0xFFFF0u);
+        // (r > 0 exactly where its bits are not 0)
+        cr[h] |= max(b, min(__float_as_uint(R[h][i]), 1u)) << (8 * i);
+        cm[h] |= (a | (__float_as_uint(M[h][i]) >> 24 & 0x80u)) << (8 * i);
       }
+      if (!okm) cm[h] = 0;
+      if (!okr) cr[h] = 0;
+    }
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {

@@ -797,7 +797,6 @@ struct Shape {
     int C = 1;
     for (int k = 2; k <= MAX_CLUSTER && k <= tiles; ++k)
       if (fit[k] >= slabs) C = k;
-    if (const char *e = getenv("RECUR_CL")) C = tiles < atoi(e) ? tiles : atoi(e);
     return C;
   }
 };
