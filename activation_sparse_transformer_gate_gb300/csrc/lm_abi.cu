@@ -369,7 +369,7 @@ twell_status twell_adamw_step(const twell_adamw_tensor *tensors, int count, int 
   if (!aligned4(grad_scale) || !aligned16(dynamic)) return TWELL_ERR_ALIGN;
   for (int i = 0; i < count; ++i) {
     const twell_adamw_tensor &t = tensors[i];
-    if (t.n < 0 || t.n > (1ll << 40) || t.first < 0 || !isfinite(t.decay)) return TWELL_ERR_ARG;
+    if (t.n < 0 || t.n > (1ll << 39) || t.first < 0 || !isfinite(t.decay)) return TWELL_ERR_ARG;
     if (t.n == 0) continue;
     if (!t.param || !t.grad || !t.m || !t.v || (state_bits == 8 && (!t.mscale || !t.vscale)))
       return TWELL_ERR_ARG;

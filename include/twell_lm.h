@@ -253,7 +253,7 @@ typedef struct {
   void *m, *v;              /* [n] fp32, or codes                             */
   float *mscale, *vscale;   /* [ceil(n / 256)] (state_bits 8)                 */
   void *copy;               /* [n] bf16, or NULL                              */
-  long long n;              /* 0 <= n <= 2^40                                 */
+  long long n;              /* 0 <= n <= 2^39                                 */
   long long first;          /* number of element 0, >= 0 (state_bits 8)       */
   float decay;              /* weight decay                                   */
 } twell_adamw_tensor;

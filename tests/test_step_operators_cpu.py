@@ -83,7 +83,7 @@ def test_adamw(lib):
                      (ARG, dict(b1=1.0)), (ARG, dict(b1=-0.1)), (ARG, dict(b2=1.0)),
                      (ARG, dict(b2=NAN)), (ARG, dict(eps=-1.0)), (ARG, dict(eps=INF)),
                      (ARG, dict(step=0)), (ALIGN, dict(scale=ODD)), (ALIGN, dict(dyn=OFF)),
-                     (ARG, dict(n=-1)), (ARG, dict(n=(1 << 40) + 1)), (ARG, dict(first=-1)),
+                     (ARG, dict(n=-1)), (ARG, dict(n=(1 << 39) + 1)), (ARG, dict(first=-1)),
                      (ARG, dict(decay=INF)), (ARG, dict(param=None)), (ARG, dict(grad=None)),
                      (ARG, dict(m=None)), (ARG, dict(v=None)), (ARG, dict(bits=8, mscale=None)),
                      (ARG, dict(bits=8, vscale=None)), (ALIGN, dict(param=OFF)),
