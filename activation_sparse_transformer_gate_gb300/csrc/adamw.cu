@@ -1,14 +1,24 @@
 // adamw.cu -- one AdamW step over many tensors, states in 32 or 8 bits.
 //
-// Nothing but bytes: 30 a parameter with fp32 states and gradients and a bf16
-// copy, 18 with states in 8 bits.  The tensors' addresses travel in the launch's
-// parameters, so a step is one launch for up to MAX_TENSORS of them, captures as
-// it is, and reads no list from memory.  A warp takes blocks of 256 elements; the
-// block's largest magnitudes, which the 8-bit codes are scaled by, stay within it.
+//   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2
+//   p = p - lr decay p - lr / c1 m / (sqrt(v) / sqrt(c2) + eps)
 //
-// The state's arithmetic is rounded operation by operation (no fused
-// multiply-add), and the square root is IEEE's, so that the stochastic rounding to
-// 8 bits falls the same way wherever the formula is evaluated in fp32.
+// Bytes bound it: 30 a parameter with fp32 states and gradients and a bf16 copy, 18
+// with states in 8 bits, where the instructions (106 an element before the copies
+// ahead) come close: 0.41e9 parameters 1.34 ms of a floor of 1.10 by bytes, issue
+// slots 82% busy; fp32 states at the floor (1.43e9 parameters 6.1 ms, 6.4 by the
+// copy rate).  The tensors' addresses travel in the launch's parameters, so a step is
+// one launch for up to MAX_TENSORS of them, captures as it is, and reads no list from
+// memory.  A warp takes blocks of 256 elements; the block's largest magnitudes, which
+// the 8-bit codes are scaled by, stay within it.
+//
+// 8 bits: e4m3 codes hold m and sqrt(v), whose range is half of v's in octaves.  A
+// step moves an average by a fraction 1 - beta of the difference, 1e-3 and less for
+// v, where half a code's distance is 2^-5 to 2^-4 of the value: rounded to nearest it
+// would never move.  Rounded up with the chance of what is cut off, it moves as much
+// in the mean.  The state's arithmetic is rounded operation by operation (no fused
+// multiply-add), and the square root is IEEE's, so that this rounding falls the same
+// way wherever the formula is evaluated in fp32.
 #include <cuda_fp8.h>
 #include <math.h>
 #include <string.h>
@@ -167,12 +177,11 @@ __device__ __forceinline__ void update_block(const Entry &e, const Step &st, lon
     const uint32_t bm = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(topm) & 0x7FFFFFFFu);
     const uint32_t br = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(topr) & 0x7FFFFFFFu);
     const bool okm = bm < 0x7F800000u, okr = br < 0x7F800000u;
-    const float tm = fmaxf(__uint_as_float(bm), 1e-30f), tr = fmaxf(__uint_as_float(br), 1e-30f);
-    const float im = __fdiv_rn(448.f, tm), ir = __fdiv_rn(448.f, tr);
-    if (lane == 0) {
-      e.ms[i0 / BLOCK] = okm ? __fmul_rn(tm, 1.f / 448.f) : NAN;
-      e.vs[i0 / BLOCK] = okr ? __fmul_rn(tr, 1.f / 448.f) : NAN;
-    }
+    // (one division: m's in the even lanes, r's in the odd ones)
+    const float top = fmaxf(__uint_as_float(lane & 1 ? br : bm), 1e-30f), inv = __fdiv_rn(448.f, top);
+    const float im = __shfl_sync(0xFFFFFFFFu, inv, 0), ir = __shfl_sync(0xFFFFFFFFu, inv, 1);
+    if (lane < 2)
+      (lane ? e.vs : e.ms)[i0 / BLOCK] = (lane ? okr : okm) ? __fmul_rn(top, 1.f / 448.f) : NAN;
     const unsigned long long first = (unsigned long long)(e.first + i0 + lane * 4);
     const uint32_t low = (uint32_t)first;
     const uint32_t u0 = low * NOISE_K1 + (uint32_t)(first >> 32) * NOISE_K3 + seed;
@@ -266,10 +275,22 @@ __device__ __forceinline__ void load_some(const bf16 *p, long long at, long long
   }
 }
 
-// States in 32 bits: a warp a block, straight from global memory.
-template <typename G, int N>
+__device__ __forceinline__ void load_some(const uint8_t *p, long long at, long long n, float (&f)[4]) {
+  uint32_t w = 0;
+  if (at + 4 <= n) {
+    w = *(const uint32_t *)(p + at);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (at + i < n) w |= (uint32_t)p[at + i] << (8 * i);
+  }
+  from_codes(w, f);
+}
+
+// A warp a block, straight from global memory.
+template <typename G, int BITS, int N>
 __global__ void __launch_bounds__(32 * WARPS, 4)
-adamw32_kernel(const __grid_constant__ Table<N> table, const Scalars sc) {
+adamw_direct_kernel(const __grid_constant__ Table<N> table, const Scalars sc) {
   pdl_begin();
   const long long b = (long long)blockIdx.x * WARPS + (threadIdx.x >> 5);
   int lo = 0, hi = table.count - 1;
@@ -292,14 +313,21 @@ adamw32_kernel(const __grid_constant__ Table<N> table, const Scalars sc) {
     const long long at = i0 + h * 128 + (threadIdx.x & 31) * 4;
     load_some(e.p, at, e.n, P[h]);
     load_some((const G *)e.g, at, e.n, Gr[h]);
-    load_some((const float *)e.m, at, e.n, M[h]);
-    load_some((const float *)e.v, at, e.n, R[h]);
+    if (BITS == 32) {
+      load_some((const float *)e.m, at, e.n, M[h]);
+      load_some((const float *)e.v, at, e.n, R[h]);
+    } else {
+      load_some((const uint8_t *)e.m, at, e.n, M[h]);
+      load_some((const uint8_t *)e.v, at, e.n, R[h]);
+    }
   }
-  update_block<32>(e, st, i0, seed, P, Gr, M, R, 0.f, 0.f);
+  const float ms = BITS == 8 ? e.ms[i0 / BLOCK] : 0.f, vs = BITS == 8 ? e.vs[i0 / BLOCK] : 0.f;
+  update_block<BITS>(e, st, i0, seed, P, Gr, M, R, ms, vs);
 }
 
 // States in 8 bits: warps go over the blocks in strides of the grid, two of them on
-// their way while one is worked on.
+// their way to shared memory while one is worked on (registers would hold one; a warp
+// a block took 1577 us where this takes 1340).
 template <typename G, int N>
 __global__ void __launch_bounds__(32 * WARPS, CTAS8)
 adamw8_kernel(const __grid_constant__ Table<N> table, const Scalars sc) {
@@ -378,10 +406,10 @@ adamw8_kernel(const __grid_constant__ Table<N> table, const Scalars sc) {
   }
 }
 
-template <typename G, int N>
-cudaError_t launch32(const Table<N> &t, const Scalars &sc, cudaStream_t s) {
+template <typename G, int BITS, int N>
+cudaError_t launch_direct(const Table<N> &t, const Scalars &sc, cudaStream_t s) {
   const long long ctas = (t.end[t.count - 1] + (long long)WARPS - 1) / WARPS;
-  return launch_k(adamw32_kernel<G, N>, dim3((unsigned)ctas), dim3(32 * WARPS), 0, s, t, sc);
+  return launch_k(adamw_direct_kernel<G, BITS, N>, dim3((unsigned)ctas), dim3(32 * WARPS), 0, s, t, sc);
 }
 
 template <typename G, int N>
@@ -393,6 +421,9 @@ cudaError_t launch8(const Table<N> &t, const Scalars &sc, cudaStream_t s) {
   if (attr != cudaSuccess) return attr;
   const long long ctas = (t.end[t.count - 1] + (long long)WARPS - 1) / WARPS;
   const long long most = (long long)num_sms() * CTAS8;
+  // Fetching ahead pays from about two blocks a warp (us, ahead | direct: 0.53e6
+  // parameters 5.4 | 3.9, 2.1e6 10.6 | 9.8, 5.1e6 21.6 | 24.9, 16.7e6 61 | 76, 255e6 824 | 1028).
+  if (ctas <= 2 * most) return launch_direct<G, 8>(t, sc, s);
   return launch_k(kern, dim3((unsigned)(ctas < most ? ctas : most)), dim3(32 * WARPS), SMEM, s, t, sc);
 }
 
@@ -405,9 +436,9 @@ cudaError_t launch_t(const AdamwArgs &a, const Scalars &sc, cudaStream_t s) {
     if (t.count == 0) return cudaSuccess;
     const cudaError_t e =
         a.grad_dtype == TWELL_BF16
-            ? a.state_bits == 8 ? launch8<bf16>(t, sc, s) : launch32<bf16>(t, sc, s)
+            ? a.state_bits == 8 ? launch8<bf16>(t, sc, s) : launch_direct<bf16, 32>(t, sc, s)
         : a.state_bits == 8 ? launch8<float>(t, sc, s)
-                            : launch32<float>(t, sc, s);
+                            : launch_direct<float, 32>(t, sc, s);
     t.count = 0;
     blocks = 0;
     return e;

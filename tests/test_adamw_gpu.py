@@ -150,6 +150,20 @@ def test_steps(bits, grad):
 
 
 @pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("grad", [torch.float32, torch.bfloat16])
+def test_large_tensors(bits, grad):
+    """Enough blocks for warps to go over several, across tensors and their partial blocks."""
+    ts = [Tensor(n, bits, grad, decay=0.1, first=7 * n) for n in (3000001, 5, 70001, 256, 2000000, 300)]
+    lst = tw.AdamWTensors(bits)
+    for t in ts:
+        t.add(lst)
+    for step in (1, 2):
+        tw.twell_adamw_step(lst, LR, B1, B2, EPS, step, seed=31 * step)
+        for t in ts:
+            t.compare(*t.step(step, 31 * step))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
 def test_more_tensors_than_a_launch_takes(bits):
     ts = [Tensor(1 + 37 * i % 700, bits, seed=i, first=i << 20) for i in range(1000)]
     lst = tw.AdamWTensors(bits)
@@ -176,18 +190,19 @@ def test_empty_tensors_are_left_out():
     tw.twell_adamw_step(lst, LR, B1, B2, EPS, 1)
 
 
-def test_rounding_goes_by_the_elements_number():
+@pytest.mark.parametrize("n", [70001, 5000001])
+def test_rounding_goes_by_the_elements_number(n):
     """Tensors cut into pieces (of whole blocks) have the bits of the whole, and those around the
     number 2^32."""
-    n, cut, first = 70001, 256 * 100, 2 ** 32 - 30000
+    cut, first = 256 * 100, 2 ** 32 - 30000
     whole = Tensor(n, 8, first=first)
     a = Tensor(n, 8, first=first)
     p, g, m, v, ms, vs, copy = a.dev
-    lst = tw.AdamWTensors(8)
     for lo, hi in ((0, cut), (cut, n)):
         s, b = slice(lo, hi), slice(lo // 256, -(-hi // 256))
+        lst = tw.AdamWTensors(8)
         lst.add(p[s], g[s], m[s], v[s], ms[b], vs[b], copy=copy[s], first=first + lo)
-    tw.twell_adamw_step(lst, LR, B1, B2, EPS, 3, seed=5)
+        tw.twell_adamw_step(lst, LR, B1, B2, EPS, 3, seed=5)
     lst = tw.AdamWTensors(8)
     whole.add(lst)
     tw.twell_adamw_step(lst, LR, B1, B2, EPS, 3, seed=5)
