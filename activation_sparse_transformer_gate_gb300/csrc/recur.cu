@@ -25,8 +25,6 @@
 #include <cooperative_groups.h>
 #include <limits.h>
 
-#include <type_traits>
-
 #include "common.cuh"
 #include "lm_kernels.h"
 #include "tcgen05.cuh"
@@ -271,11 +269,14 @@ __device__ __forceinline__ void fetch(uint4 *slot, const E *src, long long pitch
   }
 }
 
-// The scan over a tile's groups, from the tile's first row on (BACK: from its last):
-// replaces each group's step in `steps` by the value that reaches the group;
-// `exchange` gives what reaches the tile, from the tile's own step.
-template <typename G, bool BACK, bool CLEAN, typename F>
-__device__ __forceinline__ void scan_groups(float2 *steps, F exchange) {
+// The scan over a tile's groups, from the tile's first row on (BACK: from its last).
+// What a lane keeps of it between its halves: the step of the parts before its own,
+// and the tile's.
+struct Scan {
+  float C, H, tileC, tileH;
+};
+template <typename G, bool BACK, bool CLEAN>
+__device__ __forceinline__ Scan scan_up(const float2 *steps) {
   constexpr int N = G::N, P = G::PARTS, W = G::ACROSS;
   constexpr uint32_t FULL = 0xFFFFFFFFu;
   const int lane = threadIdx.x & 31, part = lane / W, ch = lane % W;
@@ -300,10 +301,24 @@ __device__ __forceinline__ void scan_groups(float2 *steps, F exchange) {
     }
   }
   const int whole = (BACK ? 0 : 32 - W) + lane % W;  // the lane that has the tile's step
-  float h = exchange(ch, part, __shfl_sync(FULL, C, whole), __shfl_sync(FULL, H, whole));
-  const float C1 = BACK ? __shfl_down_sync(FULL, C, W) : __shfl_up_sync(FULL, C, W);
-  const float H1 = BACK ? __shfl_down_sync(FULL, H, W) : __shfl_up_sync(FULL, H, W);
-  if (behind > 0) h = apply<CLEAN>(C1, H1, h);
+  Scan s;
+  s.tileC = __shfl_sync(FULL, C, whole);
+  s.tileH = __shfl_sync(FULL, H, whole);
+  s.C = BACK ? __shfl_down_sync(FULL, C, W) : __shfl_up_sync(FULL, C, W);
+  s.H = BACK ? __shfl_down_sync(FULL, H, W) : __shfl_up_sync(FULL, H, W);
+  if (behind == 0) s.C = s.H = 0.f;
+  return s;
+}
+// Replaces each group's step by the value that reaches the group, from the one that
+// reaches the tile.
+template <typename G, bool BACK, bool CLEAN>
+__device__ __forceinline__ void scan_down(float2 *steps, const Scan &s, float h) {
+  constexpr int N = G::N, W = G::ACROSS;
+  const int lane = threadIdx.x & 31, part = lane / W, ch = lane % W;
+  float2 v[N];  // (all read before any is written: the compiler would keep the order)
+#pragma unroll
+  for (int j = 0; j < N; ++j) v[j] = steps[G::at(part * N + j, ch)];
+  h = apply<CLEAN>(s.C, s.H, h);
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     const int j = BACK ? N - 1 - k : k;
@@ -313,12 +328,14 @@ __device__ __forceinline__ void scan_groups(float2 *steps, F exchange) {
 }
 
 // The exchange of a slab's steps among the cluster's CTAs: in each round every warp
-// sends its tile's step to the warps of the other CTAs that have the slab, whose
-// barrier counts the bytes.  Two rounds' worth: a warp sends the steps of the round
-// after next only when all have sent, and so have read, the one between.
+// sends its tile's step to the warps of the CTAs that have the slab, whose barrier
+// counts the bytes.  A warp sends round i + 1's before it waits for round i's, so
+// that they travel while it works.  It sends those of round i + 4 after all have
+// sent round i + 2's, and so have read round i's: four rounds' worth of room.
+constexpr int ROOM = 4;
 struct Exchange {
-  float2 total[2][MAX_CLUSTER][16];  // (0, 0) for CTAs that the cluster does not have
-  uint64_t bar[2];
+  float2 total[ROOM][MAX_CLUSTER][16];  // (0, 0) for CTAs that the cluster does not have
+  uint64_t bar[ROOM];
 };
 
 __device__ __forceinline__ uint32_t peer(uint32_t addr, int rank) {
@@ -342,28 +359,33 @@ __device__ __forceinline__ bool arrived(uint32_t bar, uint32_t parity, uint64_t 
   }
 }
 
+template <typename G>
+__device__ __forceinline__ void send_step(Exchange &x, int n, int rank, int i, const Scan &s, bool lost) {
+  if (n == 1 || lost) return;
+  const int lane = threadIdx.x & 31, ch = lane % G::ACROSS, part = lane / G::ACROSS;
+  const uint32_t bar = smem_u32(&x.bar[i % ROOM]), mine = smem_u32(&x.total[i % ROOM][rank][ch]);
+  if (lane == 0) mbar_expect_tx(bar, (uint32_t)n * G::SLAB * sizeof(float2));
+  for (int r = part; r < n; r += G::PARTS)
+    asm volatile(
+        "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+            peer(mine, r)),
+        "f"(s.tileC), "f"(s.tileH), "r"(peer(bar, r))
+        : "memory");
+}
+
 // What reaches this warp's tile of round i, from the cluster's tiles' steps in the
 // order of the rows (BACK: against it); `carry` is what reaches the cluster's first
 // one, and then the first one of its next round.
 template <typename G, bool BACK>
-__device__ __forceinline__ float exchange_totals(Exchange &x, int n, int rank, int i, int ch, int part,
-                                                 float C, float H, float &carry, bool &lost,
-                                                 int32_t *status) {
+__device__ __forceinline__ float receive_steps(Exchange &x, int n, int rank, int i, const Scan &s,
+                                               float &carry, bool &lost, int32_t *status) {
   if (n == 1) {
     const float in = carry;
-    carry = apply(C, H, carry);
+    carry = apply(s.tileC, s.tileH, carry);
     return in;
   }
-  const uint32_t bar = smem_u32(&x.bar[i & 1]), mine = smem_u32(&x.total[i & 1][rank][ch]);
   if (!lost) {
-    if ((threadIdx.x & 31) == 0) mbar_expect_tx(bar, (uint32_t)n * G::SLAB * sizeof(float2));
-    for (int r = part; r < n; r += G::PARTS)
-      asm volatile(
-          "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
-              peer(mine, r)),
-          "f"(C), "f"(H), "r"(peer(bar, r))
-          : "memory");
-    const uint32_t parity = (uint32_t)i >> 1 & 1;
+    const uint32_t bar = smem_u32(&x.bar[i % ROOM]), parity = (uint32_t)i / ROOM & 1;
     if (!arrived(bar, parity, WAIT_LIMIT_NS)) {
       set_status(status, TWELL_ERR_TIMEOUT);
       // (what is on its way has to come in before the barrier is used again)
@@ -371,12 +393,13 @@ __device__ __forceinline__ float exchange_totals(Exchange &x, int n, int rank, i
     }
     lost = __any_sync(0xFFFFFFFFu, lost);
   }
+  const int ch = (threadIdx.x & 31) % G::ACROSS;
   float in = carry;
 #pragma unroll
   for (int k = 0; k < MAX_CLUSTER; ++k) {
     const int r = BACK ? MAX_CLUSTER - 1 - k : k;
     if (r == rank) in = carry;
-    const float2 v = x.total[i & 1][r][ch];
+    const float2 v = x.total[i % ROOM][r][ch];
     carry = apply(v.x, v.y, carry);
   }
   return in;
@@ -385,8 +408,8 @@ __device__ __forceinline__ float exchange_totals(Exchange &x, int n, int rank, i
 // Before the first exchange, by the whole cluster.
 __device__ __forceinline__ void open_exchange(Exchange &x, int C) {
   const int lane = threadIdx.x & 31;
-  for (int k = lane; k < 2 * MAX_CLUSTER * 16; k += 32) (&x.total[0][0][0])[k] = make_float2(0.f, 0.f);
-  if (lane < 2) mbar_init(smem_u32(&x.bar[lane]), 1);
+  for (int k = lane; k < ROOM * MAX_CLUSTER * 16; k += 32) (&x.total[0][0][0])[k] = make_float2(0.f, 0.f);
+  if (lane < ROOM) mbar_init(smem_u32(&x.bar[lane]), 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __syncwarp();
   if (C > 1) cluster_arrive();  // (from here on the others may write here)
@@ -403,137 +426,181 @@ struct Rounds {
   }
 };
 
+// A tile between its two halves.
+struct Tile {
+  int r0;
+  RowBits bits;
+  bool plain;  // no sequence begins or ends in the warp's tile, and all of its rows are
+               // some sequence's (a row's branches cost as much as its arithmetic)
+  Scan scan;
+};
+
 // What a warp of the forward has in shared memory.
 template <typename E>
 struct FwdShared {
   using G = Fwd<E>;
-  uint4 x[2][G::S][32], gate[G::S][32];  // x of two tiles, gates of one
-  float2 steps[G::GROUPS * G::SLAB];     // the groups' steps, then what reaches them
+  uint4 x[3][G::S][32], gate[G::S][32];  // x of the tiles in both halves and the next one
+  float2 steps[2][G::GROUPS * G::SLAB];  // the groups' steps, then what reaches them
   Exchange exchange;
   // h0 of the last sequence that begins in each lane's rows: hT may be h0, and who
   // comes to that sequence's end first is open (the others end with the same lane)
-  float4 held[G::N / 4][32];
-  Marks<G::R> marks;
+  float4 held[2][G::N / 4][32];
+  Marks<G::R> marks[2];
+};
+
+// A warp of the forward.
+template <typename E>
+struct ForwardWarp {
+  using G = Fwd<E>;
+  static constexpr int N = G::N, S = G::S, CX = G::CX;
+  const E *x, *gate;
+  E *h;
+  const RecurParams &p;
+  FwdShared<E> &sh;
+  Rounds rounds;
+  int C, rank, lane, q, cx, d, count, lo, hi;
+  bool on, lost;
+  float bias[N];
+  float carry;  // the state before the cluster's next rows, of the scan's channel
+  Gap gap;
+
+  __device__ __forceinline__ uint32_t live_of(int i) const {
+    return live_rows<S>(rounds.row(i, p.T) + q * S, lo, hi);
+  }
+  __device__ __forceinline__ void fetch_x(int i) {
+    if (i < count && on)
+      fetch<S>(&sh.x[i % 3][0][lane], x + d, p.ld, rounds.row(i, p.T) + q * S, live_of(i));
+  }
+  __device__ __forceinline__ void fetch_gate(int i) {
+    if (i < count && on)
+      fetch<S>(&sh.gate[0][lane], gate + d, p.ld, rounds.row(i, p.T) + q * S, live_of(i));
+  }
+  // The first half of tile i: its rows as one step a lane, scanned and sent.
+  template <bool PLAIN>
+  __device__ __forceinline__ void first_half(int i, Tile &t, float (&c)[S][N]) {
+    float Cs[N], Hs[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) Cs[n] = Hs[n] = 0.f;
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      if (!PLAIN && (t.bits.first >> k & 1)) {
+        load_state(on ? p.h0 : nullptr, first_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, Hs);
+#pragma unroll
+        for (int n = 0; n < N; n += 4)
+          sh.held[i & 1][n / 4][lane] = make_float4(Hs[n], Hs[n + 1], Hs[n + 2], Hs[n + 3]);
+      }
+      float xv[N], gv[N];
+      unpack(sh.x[i % 3][k][lane], xv, (E *)nullptr);
+      unpack(sh.gate[k][lane], gv, (E *)nullptr);
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        c[k][n] = taken(ex2_approx(fmaf(gv[n], LOG2E, bias[n])));
+        Hs[n] = fmaf(c[k][n], xv[n] - Hs[n], Hs[n]);
+        Cs[n] = fmaf(-Cs[n], c[k][n], Cs[n]) + c[k][n];
+      }
+      if (!PLAIN && !(t.bits.live >> k & 1)) {  // (what was not read may be anything)
+#pragma unroll
+        for (int n = 0; n < N; ++n) Hs[n] = 0.f;
+      }
+    }
+    fetch_gate(i + 1);
+    const bool cut = !PLAIN && (t.bits.first != 0 || t.bits.live != G::ALL);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      sh.steps[i & 1][G::at(q, n * CX + cx)] = make_float2(cut ? CUT : Cs[n], Hs[n]);
+    __syncwarp();
+    t.scan = scan_up<G, false, PLAIN>(sh.steps[i & 1]);
+    send_step<G>(sh.exchange, C, rank, i, t.scan, lost);
+  }
+  // The second half: the rows once more, from the state before them.
+  template <bool PLAIN>
+  __device__ __forceinline__ void second_half(int i, const Tile &t, const float (&c)[S][N]) {
+    const float in = receive_steps<G, false>(sh.exchange, C, rank, i, t.scan, carry, lost, p.status);
+    scan_down<G, false, PLAIN>(sh.steps[i & 1], t.scan, in);
+    __syncwarp();
+    float y[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) y[n] = sh.steps[i & 1][G::at(q, n * CX + cx)].x;
+    if (!on) return;
+    const int row = t.r0 + q * S;
+    if (p.states && row % RECUR_KEEP == 0 && row < p.T)
+      store_state(p.states, row / RECUR_KEEP, p.D, d, y);
+    E *out = h + (size_t)row * p.D + d;
+    uint4 rows[S];  // (read before the first store, which the reads could not pass)
+#pragma unroll
+    for (int k = 0; k < S; ++k) rows[k] = sh.x[i % 3][k][lane];
+#pragma unroll
+    for (int k = 0; k < S; ++k, out += p.D) {
+      float xv[N];
+      unpack(rows[k], xv, (E *)nullptr);
+      if (!PLAIN) {
+        if (!(t.bits.live >> k & 1)) continue;
+        if (t.bits.first >> k == 1) {
+#pragma unroll
+          for (int n = 0; n < N; n += 4) {
+            const float4 v = sh.held[i & 1][n / 4][lane];
+            y[n] = v.x; y[n + 1] = v.y; y[n + 2] = v.z; y[n + 3] = v.w;
+          }
+        } else if (t.bits.first >> k & 1) {
+          load_state(p.h0, first_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, y);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < N; ++n) y[n] = fmaf(c[k][n], xv[n] - y[n], y[n]);
+      *(uint4 *)out = pack16(y, (E *)nullptr);
+      if (!PLAIN && (t.bits.last >> k & 1) && p.hT)
+        store_state(p.hT, last_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, y);
+    }
+  }
 };
 
 template <typename E>
-__global__ void __launch_bounds__(32 * WARPS, 3)
+__global__ void __launch_bounds__(32 * WARPS, 2)
 recur_forward_kernel(const E *x, const E *gate, E *h, RecurParams p) {
   pdl_begin();
   using G = Fwd<E>;
-  constexpr int N = G::N, R = G::R, S = G::S, CX = G::CX;
   extern __shared__ __align__(16) char shared[];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q = lane / CX, cx = lane % CX;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   FwdShared<E> &sh = ((FwdShared<E> *)shared)[warp];
   open_exchange(sh.exchange, C);
-  const int d0 = (int)(blockIdx.x / C * WARPS + warp) * G::SLAB, d = d0 + cx * N;
-  const bool on = d < p.D;
+  const int d0 = (int)(blockIdx.x / C * WARPS + warp) * G::SLAB;
+  const Rounds rounds(C, rank, G::R, p.T);
+  const int q = lane / G::CX, cx = lane % G::CX, d = d0 + cx * G::N, count = d0 < p.D ? rounds.n : 0;
   const int lo = p.starts ? max(0, p.starts[0]) : 0;
   const int hi = p.starts ? min(p.T, max(0, p.starts[p.B])) : p.T;
-  const Rounds rounds(C, rank, R, p.T);
-  auto live_of = [&](int i) { return live_rows<S>(rounds.row(i, p.T) + q * S, lo, hi); };
-  uint32_t live = live_of(0);
-  if (on) {
-    fetch<S>(&sh.x[0][0][lane], x + d, p.ld, rounds.row(0, p.T) + q * S, live);
-    fetch<S>(&sh.gate[0][lane], gate + d, p.ld, rounds.row(0, p.T) + q * S, live);
-  }
+  ForwardWarp<E> w{x, gate, h, p, sh, rounds, C, rank, lane, q, cx, d, count, lo, hi, d < p.D, false};
+  w.fetch_x(0);
+  w.fetch_gate(0);
   empty_sequences(p, p.h0, p.hT, d0, min(p.D, d0 + G::SLAB), rank, C);
-  float bias[N];
-  load_state(on ? p.bias : nullptr, 0, 0, d, bias);
+  load_state(w.on ? p.bias : nullptr, 0, 0, d, w.bias);
 #pragma unroll
-  for (int n = 0; n < N; ++n) bias[n] *= LOG2E;
-  float carry = 0.f;  // the state before the cluster's next rows, of the scan's channel
-  bool lost = false;
+  for (int n = 0; n < G::N; ++n) w.bias[n] *= LOG2E;
+  w.carry = 0.f;
   if (C > 1) cluster_wait();
-  Gap gap;
-  const int count = d0 < p.D ? rounds.n : 0;
-  for (int i = 0; i < count; ++i) {
-    const int r0 = rounds.row(i, p.T), row = r0 + q * S, b = i & 1;
-    const bool more = i + 1 < count;
-    const int r1 = more ? rounds.row(i + 1, p.T) : p.T;
-    const uint32_t next = more ? live_of(i + 1) : 0, wanted = on ? next : 0;
-    const RowBits bits = row_bits<S>(p, sh.marks, gap, r0, q, live);
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    fetch<S>(&sh.x[b ^ 1][0][lane], x + d, p.ld, r1 + q * S, wanted);
-    // Plain: no sequence begins or ends in the warp's tile, and all of its rows are
-    // some sequence's (a row's branches cost as much as its arithmetic).
-    auto round = [&](auto plain) {
-      constexpr bool PLAIN = decltype(plain)::value;
-      // this lane's rows as one step
-      float c[S][N], Cs[N], Hs[N];
+  Tile now, next;
+  float c[G::S][G::N], cn[G::S][G::N];
+  for (int i = count > 0 ? -1 : 0; i < count; ++i) {
+    const int j = i + 1;
+    if (j < count) {
+      next.r0 = rounds.row(j, p.T);
+      next.bits = row_bits<G::S>(p, sh.marks[j & 1], w.gap, next.r0, q, w.live_of(j));
+      next.plain = __all_sync(0xFFFFFFFFu, (next.bits.first | next.bits.last) == 0 && next.bits.live == G::ALL);
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      w.fetch_x(j + 1);
+      if (next.plain) w.template first_half<true>(j, next, cn);
+      else w.template first_half<false>(j, next, cn);
+    }
+    if (i >= 0) {
+      if (now.plain) w.template second_half<true>(i, now, c);
+      else w.template second_half<false>(i, now, c);
+    }
+    now = next;
 #pragma unroll
-      for (int n = 0; n < N; ++n) Cs[n] = Hs[n] = 0.f;
+    for (int k = 0; k < G::S; ++k)
 #pragma unroll
-      for (int k = 0; k < S; ++k) {
-        if (!PLAIN && (bits.first >> k & 1)) {
-          load_state(on ? p.h0 : nullptr, first_of(p, sh.marks, r0, q * S + k), p.D, d, Hs);
-#pragma unroll
-          for (int n = 0; n < N; n += 4)
-            sh.held[n / 4][lane] = make_float4(Hs[n], Hs[n + 1], Hs[n + 2], Hs[n + 3]);
-        }
-        float xv[N], gv[N];
-        unpack(sh.x[b][k][lane], xv, (E *)nullptr);
-        unpack(sh.gate[k][lane], gv, (E *)nullptr);
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-          c[k][n] = taken(ex2_approx(fmaf(gv[n], LOG2E, bias[n])));
-          Hs[n] = fmaf(c[k][n], xv[n] - Hs[n], Hs[n]);
-          Cs[n] = fmaf(-Cs[n], c[k][n], Cs[n]) + c[k][n];
-        }
-        if (!PLAIN && !(live >> k & 1)) {  // (what was not read may be anything)
-#pragma unroll
-          for (int n = 0; n < N; ++n) Hs[n] = 0.f;
-        }
-      }
-      fetch<S>(&sh.gate[0][lane], gate + d, p.ld, r1 + q * S, wanted);
-      const bool cut = !PLAIN && (bits.first != 0 || live != G::ALL);
-#pragma unroll
-      for (int n = 0; n < N; ++n)
-        sh.steps[G::at(q, n * CX + cx)] = make_float2(cut ? CUT : Cs[n], Hs[n]);
-      __syncwarp();
-      scan_groups<G, false, PLAIN>(sh.steps, [&](int ch, int part, float Ct, float Ht) {
-        return exchange_totals<G, false>(sh.exchange, C, rank, i, ch, part, Ct, Ht, carry, lost,
-                                         p.status);
-      });
-      __syncwarp();
-      // the rows once more, from the state before them
-      float y[N];
-#pragma unroll
-      for (int n = 0; n < N; ++n) y[n] = sh.steps[G::at(q, n * CX + cx)].x;
-      if (!on) return;
-      if (p.states && row % RECUR_KEEP == 0 && row < p.T)
-        store_state(p.states, row / RECUR_KEEP, p.D, d, y);
-      E *out = h + (size_t)row * p.D + d;
-#pragma unroll
-      for (int k = 0; k < S; ++k, out += p.D) {
-        float xv[N];
-        unpack(sh.x[b][k][lane], xv, (E *)nullptr);
-        if (!PLAIN) {
-          if (!(live >> k & 1)) continue;
-          if (bits.first >> k == 1) {
-#pragma unroll
-            for (int n = 0; n < N; n += 4) {
-              const float4 v = sh.held[n / 4][lane];
-              y[n] = v.x; y[n + 1] = v.y; y[n + 2] = v.z; y[n + 3] = v.w;
-            }
-          } else if (bits.first >> k & 1) {
-            load_state(p.h0, first_of(p, sh.marks, r0, q * S + k), p.D, d, y);
-          }
-        }
-#pragma unroll
-        for (int n = 0; n < N; ++n) y[n] = fmaf(c[k][n], xv[n] - y[n], y[n]);
-        *(uint4 *)out = pack16(y, (E *)nullptr);
-        if (!PLAIN && (bits.last >> k & 1) && p.hT)
-          store_state(p.hT, last_of(p, sh.marks, r0, q * S + k), p.D, d, y);
-      }
-    };
-    if (__all_sync(0xFFFFFFFFu, (bits.first | bits.last) == 0 && live == G::ALL))
-      round(std::true_type{});
-    else
-      round(std::false_type{});
-    live = next;
+      for (int n = 0; n < G::N; ++n) c[k][n] = cn[k][n];
   }
   // (nothing is on its way to this CTA any more, unless a wait has given up)
   if (C > 1) {
@@ -546,172 +613,225 @@ recur_forward_kernel(const E *x, const E *gate, E *h, RecurParams p) {
 template <typename E>
 struct BwdShared {
   using G = Bwd<E>;
-  uint4 x[2][G::S][32], dh[2][G::S][32], gate[G::S][32];
-  float2 steps[2][G::GROUPS * G::SLAB];  // the groups' steps: h forward, a G back
+  uint4 x[2][G::S][32], dh[3][G::S][32], gate[G::S][32];
+  float2 stepsF[G::GROUPS * G::SLAB];     // the groups' steps forward
+  float2 stepsB[2][G::GROUPS * G::SLAB];  // and back, then what reaches them
   Exchange exchange;
-  float bias[MAX_CLUSTER][G::SLAB];      // the CTAs' sums of dgate
-  Marks<G::R> marks;
+  float bias[MAX_CLUSTER][G::SLAB];       // the CTAs' sums of dgate
+  Marks<G::R> marks[2];
+};
+
+// A warp of the backward, which goes from the last tile to the first.
+template <typename E>
+struct BackwardWarp {
+  using G = Bwd<E>;
+  static constexpr int N = G::N, S = G::S, CX = G::CX;
+  const E *x, *gate, *dh;
+  E *dx, *dgate;
+  const RecurParams &p;
+  BwdShared<E> &sh;
+  Rounds rounds;
+  int C, rank, lane, q, cx, d, sd, count, lo, hi;  // sd: the scan's channel
+  bool on, lost;
+  float bias[N], db[N];
+  float carry;   // a G behind the cluster's next rows, of the scan's channel
+  float before;  // the state before the next tile
+  Gap gap;
+
+  __device__ __forceinline__ int first_row(int i) const { return rounds.row(rounds.n - 1 - i, p.T); }
+  __device__ __forceinline__ uint32_t live_of(int i) const {
+    return live_rows<S>(first_row(i) + q * S, lo, hi);
+  }
+  __device__ __forceinline__ void fetch_xd(int i) {
+    if (i >= count || !on) return;
+    const uint32_t live = live_of(i);
+    fetch<S>(&sh.x[i & 1][0][lane], x + d, p.ld, first_row(i) + q * S, live);
+    fetch<S>(&sh.dh[i % 3][0][lane], dh + d, p.D, first_row(i) + q * S, live);
+  }
+  __device__ __forceinline__ void fetch_gate(int i) {
+    if (i < count && on)
+      fetch<S>(&sh.gate[0][lane], gate + d, p.ld, first_row(i) + q * S, live_of(i));
+  }
+  // (where a tile's first row begins a sequence it is not used)
+  __device__ __forceinline__ float state_before(int i) const {
+    const int r0 = i < count ? first_row(i) : p.T;
+    return sd < p.D && r0 > 0 && r0 < p.T ? p.states[(size_t)(r0 / RECUR_KEEP) * p.D + sd] : 0.f;
+  }
+  // The first half of tile i: its rows as one step forward and one back; h within the
+  // tile needs no other, and of the gates there stays e := (h_{t-1} - x_t) a c.
+  template <bool PLAIN>
+  __device__ __forceinline__ void first_half(int i, Tile &t, float (&e)[S][N], float (&c)[S][N]) {
+    float Cs[N], Hs[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) Cs[n] = Hs[n] = 0.f;
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      if (!PLAIN && (t.bits.first >> k & 1))
+        load_state(on ? p.h0 : nullptr, first_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, Hs);
+      float xv[N], gv[N];
+      unpack(sh.x[i & 1][k][lane], xv, (E *)nullptr);
+      unpack(sh.gate[k][lane], gv, (E *)nullptr);
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        e[k][n] = ex2_held(fmaf(gv[n], LOG2E, bias[n]));
+        c[k][n] = taken(e[k][n]);
+        Hs[n] = fmaf(c[k][n], xv[n] - Hs[n], Hs[n]);
+        Cs[n] = fmaf(-Cs[n], c[k][n], Cs[n]) + c[k][n];
+      }
+      if (!PLAIN && !(t.bits.live >> k & 1)) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) Hs[n] = 0.f;
+      }
+    }
+    fetch_gate(i + 1);
+    const bool dead = !PLAIN && t.bits.live != G::ALL;
+    const bool cutF = !PLAIN && (dead || t.bits.first), cutB = !PLAIN && (dead || t.bits.last);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      sh.stepsF[G::at(q, n * CX + cx)] = make_float2(cutF ? CUT : Cs[n], Hs[n]);
+      Hs[n] = 0.f;
+    }
+#pragma unroll
+    for (int k = S - 1; k >= 0; --k) {
+      if (!PLAIN && (t.bits.last >> k & 1))
+        load_state(on ? p.dhT : nullptr, last_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, Hs);
+      float dv[N];
+      unpack(sh.dh[i % 3][k][lane], dv, (E *)nullptr);
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const float g = dv[n] + Hs[n];
+        Hs[n] = fmaf(-c[k][n], g, g);
+      }
+      if (!PLAIN && !(t.bits.live >> k & 1)) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) Hs[n] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      sh.stepsB[i & 1][G::at(q, n * CX + cx)] = make_float2(cutB ? CUT : Cs[n], Hs[n]);
+    __syncwarp();
+    t.scan = scan_up<G, true, PLAIN>(sh.stepsB[i & 1]);
+    send_step<G>(sh.exchange, C, rank, i, t.scan, lost);
+    scan_down<G, false, PLAIN>(sh.stepsF, scan_up<G, false, PLAIN>(sh.stepsF), before);
+    before = state_before(i + 1);
+    __syncwarp();
+    float y[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) y[n] = sh.stepsF[G::at(q, n * CX + cx)].x;
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      if (!PLAIN && on && (t.bits.first >> k & 1))
+        load_state(p.h0, first_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, y);
+      float xv[N];
+      unpack(sh.x[i & 1][k][lane], xv, (E *)nullptr);
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const float took = (y[n] - xv[n]) * c[k][n];
+        y[n] -= took;
+        e[k][n] = took * (e[k][n] * c[k][n]);
+      }
+    }
+  }
+  // The second half: G, from the last row on.
+  template <bool PLAIN>
+  __device__ __forceinline__ void second_half(int i, const Tile &t, const float (&e)[S][N],
+                                              const float (&c)[S][N]) {
+    const float in = receive_steps<G, true>(sh.exchange, C, rank, i, t.scan, carry, lost, p.status);
+    scan_down<G, true, PLAIN>(sh.stepsB[i & 1], t.scan, in);
+    __syncwarp();
+    float y[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) y[n] = sh.stepsB[i & 1][G::at(q, n * CX + cx)].x;
+    if (!on) return;
+    const int row = t.r0 + q * S;
+    E *px = dx + (size_t)row * p.ld + d, *pg = dgate + (size_t)row * p.ld + d;
+    uint4 rows[S];
+#pragma unroll
+    for (int k = 0; k < S; ++k) rows[k] = sh.dh[i % 3][k][lane];
+#pragma unroll
+    for (int k = S - 1; k >= 0; --k) {
+      if (!PLAIN) {
+        if (!(t.bits.live >> k & 1)) continue;
+        if (t.bits.last >> k & 1)
+          load_state(p.dhT, last_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, y);
+      }
+      float dv[N], gv[N];
+      unpack(rows[k], dv, (E *)nullptr);
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const float g = dv[n] + y[n];
+        gv[n] = g * e[k][n];
+        db[n] += gv[n];
+        dv[n] = c[k][n] * g;
+        y[n] = g - dv[n];
+      }
+      *(uint4 *)(px + k * p.ld) = pack16(dv, (E *)nullptr);
+      *(uint4 *)(pg + k * p.ld) = pack16(gv, (E *)nullptr);
+      if (!PLAIN && (t.bits.first >> k & 1) && p.dh0)
+        store_state(p.dh0, first_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, y);
+    }
+  }
 };
 
 template <typename E>
-__global__ void __launch_bounds__(32 * WARPS, 3)
+__global__ void __launch_bounds__(32 * WARPS, 2)
 recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, RecurParams p) {
   pdl_begin();
   using G = Bwd<E>;
-  constexpr int N = G::N, R = G::R, S = G::S, CX = G::CX;
+  constexpr int N = G::N, CX = G::CX;
   extern __shared__ __align__(16) char shared[];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q = lane / CX, cx = lane % CX;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   BwdShared<E> &sh = ((BwdShared<E> *)shared)[warp];
   open_exchange(sh.exchange, C);
-  const int d0 = (int)(blockIdx.x / C * WARPS + warp) * G::SLAB, d = d0 + cx * N;
-  const bool on = d < p.D;
+  const int d0 = (int)(blockIdx.x / C * WARPS + warp) * G::SLAB;
+  const Rounds rounds(C, rank, G::R, p.T);
+  const int q = lane / CX, cx = lane % CX, d = d0 + cx * N, count = d0 < p.D ? rounds.n : 0;
+  const int sc = lane % G::ACROSS, sd = d0 + sc % CX * N + sc / CX;
   const int lo = p.starts ? max(0, p.starts[0]) : 0;
   const int hi = p.starts ? min(p.T, max(0, p.starts[p.B])) : p.T;
-  const Rounds rounds(C, rank, R, p.T);
-  auto first_row = [&](int i) { return rounds.row(rounds.n - 1 - i, p.T); };  // from the last on
-  auto live_of = [&](int i) { return live_rows<S>(first_row(i) + q * S, lo, hi); };
-  uint32_t live = live_of(0);
-  if (on) {
-    fetch<S>(&sh.x[0][0][lane], x + d, p.ld, first_row(0) + q * S, live);
-    fetch<S>(&sh.dh[0][0][lane], dh + d, p.D, first_row(0) + q * S, live);
-    fetch<S>(&sh.gate[0][lane], gate + d, p.ld, first_row(0) + q * S, live);
-  }
+  BackwardWarp<E> w{x, gate, dh, dx, dgate, p, sh, rounds, C, rank, lane, q, cx, d, sd, count, lo, hi, d < p.D, false};
+  w.fetch_xd(0);
+  w.fetch_gate(0);
+  w.before = w.state_before(0);
   empty_sequences(p, p.dhT, p.dh0, d0, min(p.D, d0 + G::SLAB), rank, C);
-  float bias[N], db[N];
-  load_state(on ? p.bias : nullptr, 0, 0, d, bias);
+  load_state(w.on ? p.bias : nullptr, 0, 0, d, w.bias);
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    bias[n] *= LOG2E;
-    db[n] = 0.f;
+    w.bias[n] *= LOG2E;
+    w.db[n] = 0.f;
   }
-  float carry = 0.f;  // a G behind the cluster's next rows, of the scan's channel
-  bool lost = false;
-  const int sc = lane % G::ACROSS, sd = d0 + sc % CX * N + sc / CX;  // that channel
+  w.carry = 0.f;
   if (C > 1) cluster_wait();
-  Gap gap;
-  const int count = d0 < p.D ? rounds.n : 0;
-  for (int i = 0; i < count; ++i) {
-    const int r0 = first_row(i), row = r0 + q * S, b = i & 1;
-    const bool more = i + 1 < count;
-    const int r1 = more ? first_row(i + 1) : p.T;
-    const uint32_t next = more ? live_of(i + 1) : 0, wanted = on ? next : 0;
-    // (the state before the tile; where its first row begins a sequence it is not used)
-    const float before = sd < p.D && r0 > 0 && r0 < p.T
-                             ? p.states[(size_t)(r0 / RECUR_KEEP) * p.D + sd] : 0.f;
-    const RowBits bits = row_bits<S>(p, sh.marks, gap, r0, q, live);
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    fetch<S>(&sh.x[b ^ 1][0][lane], x + d, p.ld, r1 + q * S, wanted);
-    fetch<S>(&sh.dh[b ^ 1][0][lane], dh + d, p.D, r1 + q * S, wanted);
-    auto round = [&](auto plain) {  // (as in the forward)
-      constexpr bool PLAIN = decltype(plain)::value;
-      float e[S][N], Cs[N], Hs[N], c[S][N];
+  Tile now, next;
+  float c[G::S][N], e[G::S][N], cn[G::S][N], en[G::S][N];
+  for (int i = count > 0 ? -1 : 0; i < count; ++i) {
+    const int j = i + 1;
+    if (j < count) {
+      next.r0 = w.first_row(j);
+      next.bits = row_bits<G::S>(p, sh.marks[j & 1], w.gap, next.r0, q, w.live_of(j));
+      next.plain = __all_sync(0xFFFFFFFFu, (next.bits.first | next.bits.last) == 0 && next.bits.live == G::ALL);
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      w.fetch_xd(j + 1);
+      if (next.plain) w.template first_half<true>(j, next, en, cn);
+      else w.template first_half<false>(j, next, en, cn);
+    }
+    if (i >= 0) {
+      if (now.plain) w.template second_half<true>(i, now, e, c);
+      else w.template second_half<false>(i, now, e, c);
+    }
+    now = next;
 #pragma unroll
-      for (int n = 0; n < N; ++n) Cs[n] = Hs[n] = 0.f;
-#pragma unroll
-      for (int k = 0; k < S; ++k) {
-        if (!PLAIN && (bits.first >> k & 1))
-          load_state(on ? p.h0 : nullptr, first_of(p, sh.marks, r0, q * S + k), p.D, d, Hs);
-        float xv[N], gv[N];
-        unpack(sh.x[b][k][lane], xv, (E *)nullptr);
-        unpack(sh.gate[k][lane], gv, (E *)nullptr);
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-          e[k][n] = ex2_held(fmaf(gv[n], LOG2E, bias[n]));
-          c[k][n] = taken(e[k][n]);
-          Hs[n] = fmaf(c[k][n], xv[n] - Hs[n], Hs[n]);
-          Cs[n] = fmaf(-Cs[n], c[k][n], Cs[n]) + c[k][n];
-        }
-        if (!PLAIN && !(live >> k & 1)) {
-#pragma unroll
-          for (int n = 0; n < N; ++n) Hs[n] = 0.f;
-        }
-      }
-      fetch<S>(&sh.gate[0][lane], gate + d, p.ld, r1 + q * S, wanted);
-      const bool dead = !PLAIN && live != G::ALL;
-      const bool cutF = !PLAIN && (dead || bits.first), cutB = !PLAIN && (dead || bits.last);
+    for (int k = 0; k < G::S; ++k)
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        sh.steps[0][G::at(q, n * CX + cx)] = make_float2(cutF ? CUT : Cs[n], Hs[n]);
-        Hs[n] = 0.f;
+        c[k][n] = cn[k][n];
+        e[k][n] = en[k][n];
       }
-#pragma unroll
-      for (int k = S - 1; k >= 0; --k) {
-        if (!PLAIN && (bits.last >> k & 1))
-          load_state(on ? p.dhT : nullptr, last_of(p, sh.marks, r0, q * S + k), p.D, d, Hs);
-        float dv[N];
-        unpack(sh.dh[b][k][lane], dv, (E *)nullptr);
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-          const float g = dv[n] + Hs[n];
-          Hs[n] = fmaf(-c[k][n], g, g);
-        }
-        if (!PLAIN && !(live >> k & 1)) {
-#pragma unroll
-          for (int n = 0; n < N; ++n) Hs[n] = 0.f;
-        }
-      }
-#pragma unroll
-      for (int n = 0; n < N; ++n)
-        sh.steps[1][G::at(q, n * CX + cx)] = make_float2(cutB ? CUT : Cs[n], Hs[n]);
-      __syncwarp();
-      scan_groups<G, false, PLAIN>(sh.steps[0], [&](int, int, float, float) { return before; });
-      scan_groups<G, true, PLAIN>(sh.steps[1], [&](int ch, int part, float Ct, float Ht) {
-        return exchange_totals<G, true>(sh.exchange, C, rank, i, ch, part, Ct, Ht, carry, lost,
-                                        p.status);
-      });
-      __syncwarp();
-      float y[N];
-#pragma unroll
-      for (int n = 0; n < N; ++n) y[n] = sh.steps[0][G::at(q, n * CX + cx)].x;
-      // e := (h_{t-1} - x_t) a c
-#pragma unroll
-      for (int k = 0; k < S; ++k) {
-        if (!PLAIN && on && (bits.first >> k & 1))
-          load_state(p.h0, first_of(p, sh.marks, r0, q * S + k), p.D, d, y);
-        float xv[N];
-        unpack(sh.x[b][k][lane], xv, (E *)nullptr);
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-          const float took = (y[n] - xv[n]) * c[k][n];
-          y[n] -= took;
-          e[k][n] = took * (e[k][n] * c[k][n]);
-        }
-      }
-#pragma unroll
-      for (int n = 0; n < N; ++n) y[n] = sh.steps[1][G::at(q, n * CX + cx)].x;
-      if (!on) return;
-      E *px = dx + (size_t)row * p.ld + d, *pg = dgate + (size_t)row * p.ld + d;
-#pragma unroll
-      for (int k = S - 1; k >= 0; --k) {
-        if (!PLAIN) {
-          if (!(live >> k & 1)) continue;
-          if (bits.last >> k & 1)
-            load_state(p.dhT, last_of(p, sh.marks, r0, q * S + k), p.D, d, y);
-        }
-        float dv[N], gv[N];
-        unpack(sh.dh[b][k][lane], dv, (E *)nullptr);
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-          const float g = dv[n] + y[n];
-          gv[n] = g * e[k][n];
-          db[n] += gv[n];
-          dv[n] = c[k][n] * g;
-          y[n] = g - dv[n];
-        }
-        *(uint4 *)(px + k * p.ld) = pack16(dv, (E *)nullptr);
-        *(uint4 *)(pg + k * p.ld) = pack16(gv, (E *)nullptr);
-        if (!PLAIN && (bits.first >> k & 1) && p.dh0)
-          store_state(p.dh0, first_of(p, sh.marks, r0, q * S + k), p.D, d, y);
-      }
-    };
-    if (__all_sync(0xFFFFFFFFu, (bits.first | bits.last) == 0 && live == G::ALL))
-      round(std::true_type{});
-    else
-      round(std::false_type{});
-    live = next;
   }
+  float (&db)[N] = w.db;
   // the bias' gradient: the warp's groups, then the CTAs, in order
 #pragma unroll
   for (int n = 0; n < N; ++n) {
