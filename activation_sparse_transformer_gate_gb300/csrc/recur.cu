@@ -9,19 +9,30 @@
 // that stays: where little is taken at each of many rows, 1 - C would lose it to
 // rounding.  A sequence's first row forgets what stood before it ("cut").
 //
-// HBM bounds it: 3 values an element forward, 5 backward.  To read each value once
-// without a wait of CTA on CTA through memory, a cluster of up to 8 CTAs owns a
-// slab of channels and goes through all rows: each CTA takes a tile of the rows,
-//   a thread composes its rows' steps, a warp its threads' (shuffles), the CTA
-//   its warps' (shared memory), the cluster its CTAs' (distributed shared memory),
-// and with the state that comes in from the left every thread goes over its rows
-// once more, from shared memory, and writes them.  The grouping of the sums follows
-// from the sizes alone.  The next tiles' rows are on their way meanwhile.
+// To read each value once without a wait of CTA on CTA through memory, a cluster of
+// up to 8 CTAs owns a slab of channels and goes through all rows in rounds.  A warp
+// has 16 channels and works by itself (lanes: 2 across, 16 groups of rows; fp32 4 and
+// 8): its tile of a round is 128 rows (backward 64; fp32 64), of which
+//   a lane composes its rows' steps, the warp its groups' (shared memory), the cluster
+//   its CTAs' (asynchronous stores to distributed shared memory, which an mbarrier
+//   counts),
+// and with the state that comes in from the left the lanes go over their rows once
+// more, from shared memory and registers, and write them.  Tile and tile overlap: while a
+// tile's step is on its way to the other CTAs, the next one is composed.  The grouping
+// of the sums follows from the sizes alone.
 //
 // The backward runs the same over the rows in reverse for G, and forward within a
 // tile for h, from the fp32 states that the forward kept every RECUR_KEEP rows: h
 // itself is not read (5 values an element instead of 6), and its rounding does not
 // enter the gradient.
+//
+// HBM would bound it (3 values an element forward, 5 backward: 60 and 101 us at 16384 x
+// 4096 bf16), but what bounds it now is latency: the gates stay in registers from one
+// pass over a tile to the other, for two tiles, which leaves room for 8 warps an SM, and
+// a round takes a warp 4250 cycles alone and 5700 beside the others (107 and 186 us).
+// Measured on the way: CTAs in step with barriers, 150 and 430 us; warps by themselves,
+// 120 and 187; gates computed again in the second pass (24 warps an SM, inputs of a
+// round from L2), 120 and 258.
 #include <cooperative_groups.h>
 #include <limits.h>
 
@@ -36,7 +47,7 @@ namespace twell {
 
 namespace {
 
-constexpr int WARPS = 4;            // of a CTA
+constexpr int SM_WARPS = 8;         // resident, by registers and shared memory
 constexpr int MAX_CLUSTER = 8;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float CUT = 2.f;          // a C that stands for: nothing comes through
@@ -171,6 +182,7 @@ struct RowBits {
 template <int S>
 __device__ __forceinline__ uint32_t live_rows(int row, int lo, int hi) {
   constexpr uint32_t ALL = (1u << S) - 1;
+  if (row >= lo && row + S <= hi) return ALL;
   const int below = min(max(lo - row, 0), S), upto = min(max(hi - row, 0), S);
   return (ALL << below) & ALL & ((1u << upto) - 1);
 }
@@ -421,9 +433,8 @@ struct Rounds {
   __device__ __forceinline__ Rounds(int C_, int rank_, int R_, int T)
       : C(C_), rank(rank_), R(R_), n(((T + R_ - 1) / R_ + C_ - 1) / C_) {}
   // first row of this CTA's tile in the i-th of them (T where it has none)
-  __device__ __forceinline__ int row(int i, int T) const {
-    return (int)min((long long)T, ((long long)i * C + rank) * R);
-  }
+  // (T <= 2^30 and C R <= 1024: below T + C R, which fits)
+  __device__ __forceinline__ int row(int i, int T) const { return min(T, (i * C + rank) * R); }
 };
 
 // A tile between its two halves.
@@ -554,8 +565,8 @@ struct ForwardWarp {
   }
 };
 
-template <typename E>
-__global__ void __launch_bounds__(32 * WARPS, 2)
+template <typename E, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, SM_WARPS / WARPS)
 recur_forward_kernel(const E *x, const E *gate, E *h, RecurParams p) {
   pdl_begin();
   using G = Fwd<E>;
@@ -774,8 +785,8 @@ struct BackwardWarp {
   }
 };
 
-template <typename E>
-__global__ void __launch_bounds__(32 * WARPS, 2)
+template <typename E, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, SM_WARPS / WARPS)
 recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, RecurParams p) {
   pdl_begin();
   using G = Bwd<E>;
@@ -883,10 +894,10 @@ RecurParams params_of(const RecurArgs &a) {
 
 // Clusters of C CTAs of a kernel that are resident at once (0: cannot be told).
 template <typename K>
-int resident_clusters(K kern, size_t smem, int C) {
+int resident_clusters(K kern, int threads, size_t smem, int C) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)C);
-  cfg.blockDim = dim3(32 * WARPS);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -908,18 +919,36 @@ template <typename K>
 struct Shape {
   cudaError_t attr;
   int fit[MAX_CLUSTER + 1];  // clusters that are resident, by their CTAs
-  Shape(K kern, size_t smem)
+  Shape(K kern, int threads, size_t smem)
       : attr(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) {
     for (int C = 1; C <= MAX_CLUSTER; ++C)
-      fit[C] = attr == cudaSuccess ? resident_clusters(kern, smem, C) : 0;
+      fit[C] = attr == cudaSuccess ? resident_clusters(kern, threads, smem, C) : 0;
   }
-  int cluster(int slabs, int tiles) const {
+  int cluster(int ctas, int tiles) const {
     int C = 1;
     for (int k = 2; k <= MAX_CLUSTER && k <= tiles; ++k)
-      if (fit[k] >= slabs) C = k;
+      if (fit[k] >= ctas) C = k;
     return C;
   }
 };
+
+// Four warps a CTA, or two where they leave SMs without one (us, forward and backward,
+// two | four: 2048 x 1024 fp32 13 + 21 | 15 + 24, 131072 x 1024 forward 270 | 354, 4096 x
+// 2048 34 + 40 | 25 + 37, 16384 x 4096 129 + 189 | 107 + 186).
+bool narrow(int D) { return (long long)((D + 63) / 64) * MAX_CLUSTER < num_sms(); }
+
+template <typename E, int WARPS>
+cudaError_t forward_w(const RecurArgs &a, cudaStream_t s) {
+  using G = Fwd<E>;
+  constexpr int SMEM = WARPS * sizeof(FwdShared<E>);
+  auto kern = recur_forward_kernel<E, WARPS>;
+  static const Shape<decltype(kern)> shape(kern, 32 * WARPS, SMEM);
+  if (shape.attr != cudaSuccess) return shape.attr;
+  const int wide = WARPS * G::SLAB, ctas = (a.D + wide - 1) / wide;
+  const int C = shape.cluster(ctas, (a.T + G::R - 1) / G::R);
+  return launch_clusters(kern, dim3((unsigned)(ctas * C)), dim3(32 * WARPS), SMEM, C, s,
+                         (const E *)a.x, (const E *)a.gate, (E *)a.h, params_of(a));
+}
 
 template <typename E>
 cudaError_t forward_t(const RecurArgs &a, cudaStream_t s) {
@@ -929,29 +958,26 @@ cudaError_t forward_t(const RecurArgs &a, cudaStream_t s) {
                     dim3(STEP_THREADS), 0, s, (const E *)a.x, (const E *)a.gate, (E *)a.h,
                     params_of(a));
   }
-  using G = Fwd<E>;
-  constexpr int SMEM = WARPS * sizeof(FwdShared<E>);
-  auto kern = recur_forward_kernel<E>;
-  static const Shape<decltype(kern)> shape(kern, SMEM);
-  if (shape.attr != cudaSuccess) return shape.attr;
-  const int wide = WARPS * G::SLAB, ctas = (a.D + wide - 1) / wide;
-  const int C = shape.cluster(ctas, (a.T + G::R - 1) / G::R);
-  return launch_clusters(kern, dim3((unsigned)(ctas * C)), dim3(32 * WARPS), SMEM, C, s,
-                         (const E *)a.x, (const E *)a.gate, (E *)a.h, params_of(a));
+  return narrow(a.D) ? forward_w<E, 2>(a, s) : forward_w<E, 4>(a, s);
 }
 
-template <typename E>
-cudaError_t backward_t(const RecurArgs &a, cudaStream_t s) {
+template <typename E, int WARPS>
+cudaError_t backward_w(const RecurArgs &a, cudaStream_t s) {
   using G = Bwd<E>;
   constexpr int SMEM = WARPS * sizeof(BwdShared<E>);
-  auto kern = recur_backward_kernel<E>;
-  static const Shape<decltype(kern)> shape(kern, SMEM);
+  auto kern = recur_backward_kernel<E, WARPS>;
+  static const Shape<decltype(kern)> shape(kern, 32 * WARPS, SMEM);
   if (shape.attr != cudaSuccess) return shape.attr;
   const int wide = WARPS * G::SLAB, ctas = (a.D + wide - 1) / wide;
   const int C = shape.cluster(ctas, (a.T + G::R - 1) / G::R);
   return launch_clusters(kern, dim3((unsigned)(ctas * C)), dim3(32 * WARPS), SMEM, C, s,
                          (const E *)a.x, (const E *)a.gate, (const E *)a.dh, (E *)a.dx, (E *)a.dgate,
                          params_of(a));
+}
+
+template <typename E>
+cudaError_t backward_t(const RecurArgs &a, cudaStream_t s) {
+  return narrow(a.D) ? backward_w<E, 2>(a, s) : backward_w<E, 4>(a, s);
 }
 
 }  // namespace

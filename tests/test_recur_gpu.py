@@ -162,7 +162,7 @@ def test_optional_outputs():
     want = c.run()
     D, T, B = c.D, c.T, c.B
     x, gate, starts = c.x.cuda(), c.gate.cuda(), torch.tensor(c.starts, dtype=torch.int32).cuda()
-    h, kept, st = empty(T, D, dtype=torch.bfloat16), empty(4, D), status()
+    h, kept, st = empty(T, D, dtype=torch.bfloat16), empty(tw.twell_recur_states(T), D), status()
     args = (x, gate, D, c.bias.cuda(), starts, B, c.h0.cuda())
     tw.twell_recur_forward(*args, T, D, 1, h, None, None, st)
     assert torch.equal(h[:180], want["h"][:180])
@@ -305,7 +305,7 @@ def test_repeats_streams_and_graph():
 def test_malformed_starts_are_recorded(starts):
     T, D, B = 100, 64, len(starts) - 1
     x = torch.zeros(T, D, device="cuda")
-    h, hT, kept, st = empty(T, D), empty(B, D), empty(2, D), status()
+    h, hT, kept, st = empty(T, D), empty(B, D), empty(tw.twell_recur_states(T), D), status()
     s = torch.tensor(starts, dtype=torch.int32).cuda()
     tw.twell_recur_forward(x, x, D, None, s, B, hT, T, D, 0, h, hT, kept, st)
     assert tw.twell_read_status(st) == -5
