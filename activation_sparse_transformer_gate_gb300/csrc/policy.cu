@@ -5,11 +5,13 @@
 //   loss = w (-min(r A, clip(r) A) + beta (exp(d) - d - 1)),  slope = d loss / d logp
 //   dz = slope / tau (onehot - softmax(z / tau))
 //
-// As in the distillation loss the logits are the whole cost, and a row belongs to
-// a warp (up to 256 vectors of 16 bytes), to a CTA that streams it twice (many
-// rows), or to a cluster of CTAs that keep it in shared memory (few rows).  What
-// the row's scalars give is computed by every thread: the row's slope is known
-// before its gradient is written, so no pass depends on another launch.
+// As in the distillation loss the logits are the whole cost, and HBM bounds it: a row
+// belongs to a warp (up to 256 vectors of 16 bytes), to a CTA that streams it twice, the
+// second time from L2 (many rows: 8192 x 131072 bf16 with the gradient 708 us, 6.1 TB/s; the
+// log-probabilities of 8192 x 50001 123 us, 6.7 TB/s), or to a cluster of CTAs that keep
+// it in shared memory (few long rows).  What the row's scalars give is computed by every
+// thread: the row's slope is known before its gradient is written, so no pass depends
+// on another launch.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -362,6 +364,8 @@ PolicyParams params_of(const PolicyArgs &a) {
   return p;
 }
 
+// Slices of at most 108 KB let two CTAs share an SM, so that one loads while the
+// other writes.
 constexpr int SLICE_VECS = 108 * 1024 / 16, SLICE_MAX = 200 * 1024 / 16;
 
 template <typename E, int PASS>
@@ -382,14 +386,43 @@ cudaError_t row_t(const PolicyArgs &a, cudaStream_t s) {
                   (E *)a.dz, params_of(a));
 }
 
+// Warps of a row's CTA, 0 for clusters.  us of the cluster kernel | 4 | 8 | 16 warps,
+// with the gradient, at 12000, 50001 and 131072 bf16 logits:
+//   8192 rows  105|71|93|151    387|351|274|336   834|930|894|709
+//   2048        30|23|25|38     105|92|80|91      216|244|226|187
+//   304        7.0|6.1|5.6|6.2   18|18|17|17       39|39|34|32
+//   152        5.6|5.4|4.5|4.5   11|14|12|11       24|29|20|18
+//   64         5.0|5.0|4.1|4.2  8.8|13|10|9.3      12|28|19|15
+// and the log-probabilities alone:
+//   8192        70|39|47|71     145|123|130|149   305|306|300|312
+//   2048        20|13|14|20      41|40|37|41       84|92|82|84
+//   304        4.6|4.0|3.6|4.1  9.6|9.7|8.6|9.2    17|19|15|16
+//   152        3.9|3.4|2.9|2.9  7.2|8.5|6.5|6.1    11|17|12|9.7
+//   64         3.6|3.3|2.8|2.8  5.6|8.1|6.0|5.4   8.4|16|11|8.6
+// (With few rows, a row's latency counts; with many, that the rows in flight fit into L2
+// and the warps into the SMs.)
+int row_warps(long long rows, int nvec, bool grad) {
+  const int sms = num_sms();
+  const bool short_ = nvec <= 2048;  // 32 KB
+  if (rows >= 2 * sms) {
+    if (short_) return rows >= 4 * sms ? 4 : 8;
+    if (grad) return nvec <= 7680 ? 8 : 16;
+    return rows >= 48 * sms && nvec <= 10240 ? 4 : 8;
+  }
+  if (short_) return 8;
+  if (rows >= sms) return 16;
+  return !grad && rows >= sms / 4 && nvec <= 10240 ? 16 : 0;
+}
+
 template <typename E, bool GRAD>
 cudaError_t forward_t(const PolicyArgs &a, cudaStream_t s) {
   if (a.V / VEC16<E> <= SHORT_VECS) return short_t<E, GRAD ? LOSS_GRAD : LOSS>(a, s);
   const int nvec = (int)((size_t)a.V / VEC16<E>);  // at most so many whole vectors
-  if (a.T >= 2 * num_sms())
-    return nvec <= 2048   ? row_t<E, 4, GRAD>(a, s)
-           : nvec <= 7680 ? row_t<E, 8, GRAD>(a, s)
-                          : row_t<E, 16, GRAD>(a, s);
+  switch (row_warps(a.T, nvec, GRAD)) {
+    case 4: return row_t<E, 4, GRAD>(a, s);
+    case 8: return row_t<E, 8, GRAD>(a, s);
+    case 16: return row_t<E, 16, GRAD>(a, s);
+  }
   int C = 1;
   if (GRAD)
     while (C < MAX_CLUSTER && (nvec + C - 1) / C > SLICE_VECS) C *= 2;
@@ -412,6 +445,9 @@ template <typename E>
 cudaError_t backward_t(const PolicyArgs &a, cudaStream_t s) {
   if (a.V / VEC16<E> <= SHORT_VECS) return short_t<E, GRAD_ONLY>(a, s);
   const int nvec = a.V / VEC16<E>;
+  // whole rows, in slabs of at least 1024 vectors while there are not four CTAs an SM (us,
+  // two | four | eight: 64 x 131072 7.0 | 7.5 | 7.5, 152 x 131072 14.1 | 13.6 | 13.6, 304 x
+  // 50001 11.7 | 11.5 | 11.6, 2048 rows and more the same)
   int slabs = 1;
   while ((long long)a.T * slabs < 4 * num_sms() && nvec / (2 * slabs) >= 1024) slabs *= 2;
   const int slab_vecs = (nvec + slabs - 1) / slabs;
