@@ -68,18 +68,57 @@ __device__ __forceinline__ float ex2_approx(float t) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
   return e;
 }
-// c from exp(f), to a few units of its own last place on either side (0 where exp(f)
-// has overflowed).
-__device__ __forceinline__ float taken(float e) {
-  float c;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(c) : "f"(1.f + e));
-  return c;
+__device__ __forceinline__ float rcp_approx(float t) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
+  return r;
+}
+
+// Pairs of channels: additions, products and fmas of two in one instruction.
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 less2(float2 a, float2 b) { return fma2(b, both(-1.f), a); }  // a - b
+
+// exp(f), and -c = -1 / (1 + exp(f)) from it, to a few units of its own last place on
+// either side (0 where exp(f) has overflowed).
+__device__ __forceinline__ float2 exp2_of(float2 t) { return make_float2(ex2_approx(t.x), ex2_approx(t.y)); }
+__device__ __forceinline__ float2 minus_c(float2 e) {
+  const float2 u = fma2(e, both(-1.f), both(-1.f));
+  return make_float2(rcp_approx(u.x), rcp_approx(u.y));
 }
 // exp(f) held below 2^127.5, where c has been flushed to 0 and e c is a number.
-__device__ __forceinline__ float ex2_held(float t) {
-  float m;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(t), "f"(127.5f));
-  return ex2_approx(m);
+__device__ __forceinline__ float2 exp2_held(float2 t) {
+  float2 m;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(m.x) : "f"(t.x), "f"(127.5f));
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(m.y) : "f"(t.y), "f"(127.5f));
+  return exp2_of(m);
+}
+// h + c (x - h), and the share taken after c more is.
+__device__ __forceinline__ float2 row_step(float2 mc, float2 x, float2 h) { return fma2(mc, less2(h, x), h); }
+__device__ __forceinline__ float2 share(float2 mc, float2 C) { return fma2(mc, add2(C, both(-1.f)), C); }
+
+// 16 bytes of a row as pairs, and back (SIGN: negated).
+__device__ __forceinline__ void pairs(const uint4 &u, float2 (&f)[4], bf16 *) {
+  f[0] = make_float2(bf_lo(u.x), bf_hi(u.x)); f[1] = make_float2(bf_lo(u.y), bf_hi(u.y));
+  f[2] = make_float2(bf_lo(u.z), bf_hi(u.z)); f[3] = make_float2(bf_lo(u.w), bf_hi(u.w));
+}
+__device__ __forceinline__ void pairs(const uint4 &u, float2 (&f)[2], float *) {
+  f[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+  f[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+}
+template <bool NEGATED = false>
+__device__ __forceinline__ uint4 packed(const float2 (&f)[4], bf16 *) {
+  const uint32_t s = NEGATED ? 0x80008000u : 0u;
+  return make_uint4(pack_bf2(f[0].x, f[0].y) ^ s, pack_bf2(f[1].x, f[1].y) ^ s,
+                    pack_bf2(f[2].x, f[2].y) ^ s, pack_bf2(f[3].x, f[3].y) ^ s);
+}
+template <bool NEGATED = false>
+__device__ __forceinline__ uint4 packed(const float2 (&f)[2], float *) {
+  const uint32_t s = NEGATED ? 0x80000000u : 0u;
+  return make_uint4(__float_as_uint(f[0].x) ^ s, __float_as_uint(f[0].y) ^ s,
+                    __float_as_uint(f[1].x) ^ s, __float_as_uint(f[1].y) ^ s);
 }
 
 // What a step (C, H) makes of h.  CLEAN: where no step is cut.
@@ -225,20 +264,21 @@ __device__ __forceinline__ int last_of(const RecurParams &p, const Marks<R> &m, 
   return p.starts ? m.last[k] : (r0 + k) / p.len;
 }
 
-// N values of an fp32 [B][D] matrix (zeros without one).
-template <int N>
-__device__ __forceinline__ void load_state(const float *v, int s, int D, int d, float (&f)[N]) {
+// M pairs of an fp32 [B][D] matrix (zeros without one).
+template <int M>
+__device__ __forceinline__ void load_state(const float *v, size_t s, int D, int d, float2 (&f)[M]) {
 #pragma unroll
-  for (int i = 0; i < N; i += 4) {
-    const float4 r = v ? *(const float4 *)(v + (size_t)s * D + d + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-    f[i] = r.x; f[i + 1] = r.y; f[i + 2] = r.z; f[i + 3] = r.w;
+  for (int i = 0; i < M; i += 2) {
+    const float4 r = v ? *(const float4 *)(v + s * D + d + 2 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+    f[i] = make_float2(r.x, r.y);
+    f[i + 1] = make_float2(r.z, r.w);
   }
 }
-template <int N>
-__device__ __forceinline__ void store_state(float *v, size_t s, int D, int d, const float (&f)[N]) {
+template <int M>
+__device__ __forceinline__ void store_state(float *v, size_t s, int D, int d, const float2 (&f)[M]) {
 #pragma unroll
-  for (int i = 0; i < N; i += 4)
-    *(float4 *)(v + s * D + d + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+  for (int i = 0; i < M; i += 2)
+    *(float4 *)(v + s * D + d + 2 * i) = make_float4(f[i].x, f[i].y, f[i + 1].x, f[i + 1].y);
 }
 
 // Empty sequences pass `from` on to `to` (zeros without one): the slab's channels from
@@ -251,8 +291,8 @@ __device__ __forceinline__ void empty_sequences(const RecurParams &p, const floa
     if (d0 == 0 && (a < 0 || b > p.T || a > b)) set_status(p.status, TWELL_ERR_INDEX);
     if (a == b && to)
       for (int d = d0; d < d1; d += 4) {
-        float f[4];
-        load_state(from, (int)s, p.D, d, f);
+        float2 f[2];
+        load_state(from, s, p.D, d, f);
         store_state(to, s, p.D, d, f);
       }
   }
@@ -463,7 +503,7 @@ struct FwdShared {
 template <typename E>
 struct ForwardWarp {
   using G = Fwd<E>;
-  static constexpr int N = G::N, S = G::S, CX = G::CX;
+  static constexpr int M = G::N / 2, S = G::S, CX = G::CX;  // M pairs of channels a lane
   const E *x, *gate;
   E *h;
   const RecurParams &p;
@@ -471,7 +511,7 @@ struct ForwardWarp {
   Rounds rounds;
   int C, rank, lane, q, cx, d, count, lo, hi;
   bool on, lost;
-  float bias[N];
+  float2 bias[M];  // times log2(e)
   float carry;  // the state before the cluster's next rows, of the scan's channel
   Gap gap;
 
@@ -488,50 +528,54 @@ struct ForwardWarp {
   }
   // The first half of tile i: its rows as one step a lane, scanned and sent.
   template <bool PLAIN>
-  __device__ __forceinline__ void first_half(int i, Tile &t, float (&c)[S][N]) {
-    float Cs[N], Hs[N];
+  __device__ __forceinline__ void first_half(int i, Tile &t, float2 (&mc)[S][M]) {
+    float2 Cs[M], Hs[M];
 #pragma unroll
-    for (int n = 0; n < N; ++n) Cs[n] = Hs[n] = 0.f;
+    for (int n = 0; n < M; ++n) Cs[n] = Hs[n] = both(0.f);
 #pragma unroll
     for (int k = 0; k < S; ++k) {
       if (!PLAIN && (t.bits.first >> k & 1)) {
         load_state(on ? p.h0 : nullptr, first_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, Hs);
 #pragma unroll
-        for (int n = 0; n < N; n += 4)
-          sh.held[i & 1][n / 4][lane] = make_float4(Hs[n], Hs[n + 1], Hs[n + 2], Hs[n + 3]);
+        for (int n = 0; n < M; n += 2)
+          sh.held[i & 1][n / 2][lane] = make_float4(Hs[n].x, Hs[n].y, Hs[n + 1].x, Hs[n + 1].y);
       }
-      float xv[N], gv[N];
-      unpack(sh.x[i % 3][k][lane], xv, (E *)nullptr);
-      unpack(sh.gate[k][lane], gv, (E *)nullptr);
+      float2 xv[M], gv[M];
+      pairs(sh.x[i % 3][k][lane], xv, (E *)nullptr);
+      pairs(sh.gate[k][lane], gv, (E *)nullptr);
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        c[k][n] = taken(ex2_approx(fmaf(gv[n], LOG2E, bias[n])));
-        Hs[n] = fmaf(c[k][n], xv[n] - Hs[n], Hs[n]);
-        Cs[n] = fmaf(-Cs[n], c[k][n], Cs[n]) + c[k][n];
+      for (int n = 0; n < M; ++n) {
+        mc[k][n] = minus_c(exp2_of(fma2(gv[n], both(LOG2E), bias[n])));
+        Hs[n] = row_step(mc[k][n], xv[n], Hs[n]);
+        Cs[n] = share(mc[k][n], Cs[n]);
       }
       if (!PLAIN && !(t.bits.live >> k & 1)) {  // (what was not read may be anything)
 #pragma unroll
-        for (int n = 0; n < N; ++n) Hs[n] = 0.f;
+        for (int n = 0; n < M; ++n) Hs[n] = both(0.f);
       }
     }
     fetch_gate(i + 1);
     const bool cut = !PLAIN && (t.bits.first != 0 || t.bits.live != G::ALL);
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-      sh.steps[i & 1][G::at(q, n * CX + cx)] = make_float2(cut ? CUT : Cs[n], Hs[n]);
+    for (int n = 0; n < M; ++n) {
+      sh.steps[i & 1][G::at(q, 2 * n * CX + cx)] = make_float2(cut ? CUT : Cs[n].x, Hs[n].x);
+      sh.steps[i & 1][G::at(q, (2 * n + 1) * CX + cx)] = make_float2(cut ? CUT : Cs[n].y, Hs[n].y);
+    }
     __syncwarp();
     t.scan = scan_up<G, false, PLAIN>(sh.steps[i & 1]);
     send_step<G>(sh.exchange, C, rank, i, t.scan, lost);
   }
   // The second half: the rows once more, from the state before them.
   template <bool PLAIN>
-  __device__ __forceinline__ void second_half(int i, const Tile &t, const float (&c)[S][N]) {
+  __device__ __forceinline__ void second_half(int i, const Tile &t, const float2 (&mc)[S][M]) {
     const float in = receive_steps<G, false>(sh.exchange, C, rank, i, t.scan, carry, lost, p.status);
     scan_down<G, false, PLAIN>(sh.steps[i & 1], t.scan, in);
     __syncwarp();
-    float y[N];
+    float2 y[M];
 #pragma unroll
-    for (int n = 0; n < N; ++n) y[n] = sh.steps[i & 1][G::at(q, n * CX + cx)].x;
+    for (int n = 0; n < M; ++n)
+      y[n] = make_float2(sh.steps[i & 1][G::at(q, 2 * n * CX + cx)].x,
+                         sh.steps[i & 1][G::at(q, (2 * n + 1) * CX + cx)].x);
     if (!on) return;
     const int row = t.r0 + q * S;
     if (p.states && row % RECUR_KEEP == 0 && row < p.T)
@@ -542,23 +586,24 @@ struct ForwardWarp {
     for (int k = 0; k < S; ++k) rows[k] = sh.x[i % 3][k][lane];
 #pragma unroll
     for (int k = 0; k < S; ++k, out += p.D) {
-      float xv[N];
-      unpack(rows[k], xv, (E *)nullptr);
+      float2 xv[M];
+      pairs(rows[k], xv, (E *)nullptr);
       if (!PLAIN) {
         if (!(t.bits.live >> k & 1)) continue;
         if (t.bits.first >> k == 1) {
 #pragma unroll
-          for (int n = 0; n < N; n += 4) {
-            const float4 v = sh.held[i & 1][n / 4][lane];
-            y[n] = v.x; y[n + 1] = v.y; y[n + 2] = v.z; y[n + 3] = v.w;
+          for (int n = 0; n < M; n += 2) {
+            const float4 v = sh.held[i & 1][n / 2][lane];
+            y[n] = make_float2(v.x, v.y);
+            y[n + 1] = make_float2(v.z, v.w);
           }
         } else if (t.bits.first >> k & 1) {
           load_state(p.h0, first_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, y);
         }
       }
 #pragma unroll
-      for (int n = 0; n < N; ++n) y[n] = fmaf(c[k][n], xv[n] - y[n], y[n]);
-      *(uint4 *)out = pack16(y, (E *)nullptr);
+      for (int n = 0; n < M; ++n) y[n] = row_step(mc[k][n], xv[n], y[n]);
+      *(uint4 *)out = packed(y, (E *)nullptr);
       if (!PLAIN && (t.bits.last >> k & 1) && p.hT)
         store_state(p.hT, last_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, y);
     }
@@ -587,11 +632,11 @@ recur_forward_kernel(const E *x, const E *gate, E *h, RecurParams p) {
   empty_sequences(p, p.h0, p.hT, d0, min(p.D, d0 + G::SLAB), rank, C);
   load_state(w.on ? p.bias : nullptr, 0, 0, d, w.bias);
 #pragma unroll
-  for (int n = 0; n < G::N; ++n) w.bias[n] *= LOG2E;
+  for (int n = 0; n < G::N / 2; ++n) w.bias[n] = mul2(w.bias[n], both(LOG2E));
   w.carry = 0.f;
   if (C > 1) cluster_wait();
   Tile now, next;
-  float c[G::S][G::N], cn[G::S][G::N];
+  float2 c[G::S][G::N / 2], cn[G::S][G::N / 2];
   for (int i = count > 0 ? -1 : 0; i < count; ++i) {
     const int j = i + 1;
     if (j < count) {
@@ -611,7 +656,7 @@ recur_forward_kernel(const E *x, const E *gate, E *h, RecurParams p) {
 #pragma unroll
     for (int k = 0; k < G::S; ++k)
 #pragma unroll
-      for (int n = 0; n < G::N; ++n) c[k][n] = cn[k][n];
+      for (int n = 0; n < G::N / 2; ++n) c[k][n] = cn[k][n];
   }
   // (nothing is on its way to this CTA any more, unless a wait has given up)
   if (C > 1) {
@@ -636,7 +681,7 @@ struct BwdShared {
 template <typename E>
 struct BackwardWarp {
   using G = Bwd<E>;
-  static constexpr int N = G::N, S = G::S, CX = G::CX;
+  static constexpr int M = G::N / 2, S = G::S, CX = G::CX;
   const E *x, *gate, *dh;
   E *dx, *dgate;
   const RecurParams &p;
@@ -644,7 +689,7 @@ struct BackwardWarp {
   Rounds rounds;
   int C, rank, lane, q, cx, d, sd, count, lo, hi;  // sd: the scan's channel
   bool on, lost;
-  float bias[N], db[N];
+  float2 bias[M], db[M];
   float carry;   // a G behind the cluster's next rows, of the scan's channel
   float before;  // the state before the next tile
   Gap gap;
@@ -669,91 +714,97 @@ struct BackwardWarp {
     return sd < p.D && r0 > 0 && r0 < p.T ? p.states[(size_t)(r0 / RECUR_KEEP) * p.D + sd] : 0.f;
   }
   // The first half of tile i: its rows as one step forward and one back; h within the
-  // tile needs no other, and of the gates there stays e := (h_{t-1} - x_t) a c.
+  // tile needs no other, and of the gates there stay -c and e := (h_{t-1} - x_t) a c.
   template <bool PLAIN>
-  __device__ __forceinline__ void first_half(int i, Tile &t, float (&e)[S][N], float (&c)[S][N]) {
-    float Cs[N], Hs[N];
+  __device__ __forceinline__ void first_half(int i, Tile &t, float2 (&e)[S][M], float2 (&mc)[S][M]) {
+    float2 Cs[M], Hs[M];
 #pragma unroll
-    for (int n = 0; n < N; ++n) Cs[n] = Hs[n] = 0.f;
+    for (int n = 0; n < M; ++n) Cs[n] = Hs[n] = both(0.f);
 #pragma unroll
     for (int k = 0; k < S; ++k) {
       if (!PLAIN && (t.bits.first >> k & 1))
         load_state(on ? p.h0 : nullptr, first_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, Hs);
-      float xv[N], gv[N];
-      unpack(sh.x[i & 1][k][lane], xv, (E *)nullptr);
-      unpack(sh.gate[k][lane], gv, (E *)nullptr);
+      float2 xv[M], gv[M];
+      pairs(sh.x[i & 1][k][lane], xv, (E *)nullptr);
+      pairs(sh.gate[k][lane], gv, (E *)nullptr);
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        e[k][n] = ex2_held(fmaf(gv[n], LOG2E, bias[n]));
-        c[k][n] = taken(e[k][n]);
-        Hs[n] = fmaf(c[k][n], xv[n] - Hs[n], Hs[n]);
-        Cs[n] = fmaf(-Cs[n], c[k][n], Cs[n]) + c[k][n];
+      for (int n = 0; n < M; ++n) {
+        e[k][n] = exp2_held(fma2(gv[n], both(LOG2E), bias[n]));
+        mc[k][n] = minus_c(e[k][n]);
+        Hs[n] = row_step(mc[k][n], xv[n], Hs[n]);
+        Cs[n] = share(mc[k][n], Cs[n]);
       }
       if (!PLAIN && !(t.bits.live >> k & 1)) {
 #pragma unroll
-        for (int n = 0; n < N; ++n) Hs[n] = 0.f;
+        for (int n = 0; n < M; ++n) Hs[n] = both(0.f);
       }
     }
     fetch_gate(i + 1);
     const bool dead = !PLAIN && t.bits.live != G::ALL;
     const bool cutF = !PLAIN && (dead || t.bits.first), cutB = !PLAIN && (dead || t.bits.last);
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      sh.stepsF[G::at(q, n * CX + cx)] = make_float2(cutF ? CUT : Cs[n], Hs[n]);
-      Hs[n] = 0.f;
+    for (int n = 0; n < M; ++n) {
+      sh.stepsF[G::at(q, 2 * n * CX + cx)] = make_float2(cutF ? CUT : Cs[n].x, Hs[n].x);
+      sh.stepsF[G::at(q, (2 * n + 1) * CX + cx)] = make_float2(cutF ? CUT : Cs[n].y, Hs[n].y);
+      Hs[n] = both(0.f);
     }
 #pragma unroll
     for (int k = S - 1; k >= 0; --k) {
       if (!PLAIN && (t.bits.last >> k & 1))
         load_state(on ? p.dhT : nullptr, last_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, Hs);
-      float dv[N];
-      unpack(sh.dh[i % 3][k][lane], dv, (E *)nullptr);
+      float2 dv[M];
+      pairs(sh.dh[i % 3][k][lane], dv, (E *)nullptr);
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const float g = dv[n] + Hs[n];
-        Hs[n] = fmaf(-c[k][n], g, g);
+      for (int n = 0; n < M; ++n) {
+        const float2 g = add2(dv[n], Hs[n]);
+        Hs[n] = fma2(mc[k][n], g, g);
       }
       if (!PLAIN && !(t.bits.live >> k & 1)) {
 #pragma unroll
-        for (int n = 0; n < N; ++n) Hs[n] = 0.f;
+        for (int n = 0; n < M; ++n) Hs[n] = both(0.f);
       }
     }
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-      sh.stepsB[i & 1][G::at(q, n * CX + cx)] = make_float2(cutB ? CUT : Cs[n], Hs[n]);
+    for (int n = 0; n < M; ++n) {
+      sh.stepsB[i & 1][G::at(q, 2 * n * CX + cx)] = make_float2(cutB ? CUT : Cs[n].x, Hs[n].x);
+      sh.stepsB[i & 1][G::at(q, (2 * n + 1) * CX + cx)] = make_float2(cutB ? CUT : Cs[n].y, Hs[n].y);
+    }
     __syncwarp();
     t.scan = scan_up<G, true, PLAIN>(sh.stepsB[i & 1]);
     send_step<G>(sh.exchange, C, rank, i, t.scan, lost);
     scan_down<G, false, PLAIN>(sh.stepsF, scan_up<G, false, PLAIN>(sh.stepsF), before);
     before = state_before(i + 1);
     __syncwarp();
-    float y[N];
+    float2 y[M];
 #pragma unroll
-    for (int n = 0; n < N; ++n) y[n] = sh.stepsF[G::at(q, n * CX + cx)].x;
+    for (int n = 0; n < M; ++n)
+      y[n] = make_float2(sh.stepsF[G::at(q, 2 * n * CX + cx)].x, sh.stepsF[G::at(q, (2 * n + 1) * CX + cx)].x);
 #pragma unroll
     for (int k = 0; k < S; ++k) {
       if (!PLAIN && on && (t.bits.first >> k & 1))
         load_state(p.h0, first_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, y);
-      float xv[N];
-      unpack(sh.x[i & 1][k][lane], xv, (E *)nullptr);
+      float2 xv[M];
+      pairs(sh.x[i & 1][k][lane], xv, (E *)nullptr);
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const float took = (y[n] - xv[n]) * c[k][n];
-        y[n] -= took;
-        e[k][n] = took * (e[k][n] * c[k][n]);
+      for (int n = 0; n < M; ++n) {
+        const float2 minus_took = mul2(less2(y[n], xv[n]), mc[k][n]);
+        y[n] = add2(y[n], minus_took);
+        e[k][n] = mul2(minus_took, mul2(e[k][n], mc[k][n]));
       }
     }
   }
   // The second half: G, from the last row on.
   template <bool PLAIN>
-  __device__ __forceinline__ void second_half(int i, const Tile &t, const float (&e)[S][N],
-                                              const float (&c)[S][N]) {
+  __device__ __forceinline__ void second_half(int i, const Tile &t, const float2 (&e)[S][M],
+                                              const float2 (&mc)[S][M]) {
     const float in = receive_steps<G, true>(sh.exchange, C, rank, i, t.scan, carry, lost, p.status);
     scan_down<G, true, PLAIN>(sh.stepsB[i & 1], t.scan, in);
     __syncwarp();
-    float y[N];
+    float2 y[M];
 #pragma unroll
-    for (int n = 0; n < N; ++n) y[n] = sh.stepsB[i & 1][G::at(q, n * CX + cx)].x;
+    for (int n = 0; n < M; ++n)
+      y[n] = make_float2(sh.stepsB[i & 1][G::at(q, 2 * n * CX + cx)].x,
+                         sh.stepsB[i & 1][G::at(q, (2 * n + 1) * CX + cx)].x);
     if (!on) return;
     const int row = t.r0 + q * S;
     E *px = dx + (size_t)row * p.ld + d, *pg = dgate + (size_t)row * p.ld + d;
@@ -767,18 +818,18 @@ struct BackwardWarp {
         if (t.bits.last >> k & 1)
           load_state(p.dhT, last_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, y);
       }
-      float dv[N], gv[N];
-      unpack(rows[k], dv, (E *)nullptr);
+      float2 dv[M], gv[M];
+      pairs(rows[k], dv, (E *)nullptr);
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const float g = dv[n] + y[n];
-        gv[n] = g * e[k][n];
-        db[n] += gv[n];
-        dv[n] = c[k][n] * g;
-        y[n] = g - dv[n];
+      for (int n = 0; n < M; ++n) {
+        const float2 g = add2(dv[n], y[n]);
+        gv[n] = mul2(g, e[k][n]);
+        db[n] = add2(db[n], gv[n]);
+        dv[n] = mul2(g, mc[k][n]);  // -dx
+        y[n] = add2(g, dv[n]);
       }
-      *(uint4 *)(px + k * p.ld) = pack16(dv, (E *)nullptr);
-      *(uint4 *)(pg + k * p.ld) = pack16(gv, (E *)nullptr);
+      *(uint4 *)(px + k * p.ld) = packed<true>(dv, (E *)nullptr);
+      *(uint4 *)(pg + k * p.ld) = packed(gv, (E *)nullptr);
       if (!PLAIN && (t.bits.first >> k & 1) && p.dh0)
         store_state(p.dh0, first_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, y);
     }
@@ -810,14 +861,14 @@ recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, R
   empty_sequences(p, p.dhT, p.dh0, d0, min(p.D, d0 + G::SLAB), rank, C);
   load_state(w.on ? p.bias : nullptr, 0, 0, d, w.bias);
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    w.bias[n] *= LOG2E;
-    w.db[n] = 0.f;
+  for (int n = 0; n < N / 2; ++n) {
+    w.bias[n] = mul2(w.bias[n], both(LOG2E));
+    w.db[n] = both(0.f);
   }
   w.carry = 0.f;
   if (C > 1) cluster_wait();
   Tile now, next;
-  float c[G::S][N], e[G::S][N], cn[G::S][N], en[G::S][N];
+  float2 c[G::S][N / 2], e[G::S][N / 2], cn[G::S][N / 2], en[G::S][N / 2];
   for (int i = count > 0 ? -1 : 0; i < count; ++i) {
     const int j = i + 1;
     if (j < count) {
@@ -837,12 +888,14 @@ recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, R
 #pragma unroll
     for (int k = 0; k < G::S; ++k)
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
+      for (int n = 0; n < N / 2; ++n) {
         c[k][n] = cn[k][n];
         e[k][n] = en[k][n];
       }
   }
-  float (&db)[N] = w.db;
+  float db[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) db[n] = n & 1 ? w.db[n / 2].y : w.db[n / 2].x;
   // the bias' gradient: the warp's groups, then the CTAs, in order
 #pragma unroll
   for (int n = 0; n < N; ++n) {
@@ -870,17 +923,18 @@ recur_step_kernel(const E *x, const E *gate, E *h, RecurParams p) {
   const long long k = (long long)blockIdx.x * STEP_THREADS + threadIdx.x;
   const int row = (int)(k / per), d = (int)(k % per) * N;
   if (row >= p.T) return;
-  float xv[N], gv[N], y[N], bias[N];
-  unpack(*(const uint4 *)(x + (size_t)row * p.ld + d), xv, (E *)nullptr);
-  unpack(*(const uint4 *)(gate + (size_t)row * p.ld + d), gv, (E *)nullptr);
+  constexpr int M = N / 2;
+  float2 xv[M], gv[M], y[M], bias[M];
+  pairs(*(const uint4 *)(x + (size_t)row * p.ld + d), xv, (E *)nullptr);
+  pairs(*(const uint4 *)(gate + (size_t)row * p.ld + d), gv, (E *)nullptr);
   load_state(p.bias, 0, 0, d, bias);
   load_state(p.h0, row, p.D, d, y);
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    const float c = taken(ex2_approx(fmaf(gv[n], LOG2E, bias[n] * LOG2E)));
-    y[n] = fmaf(c, xv[n] - y[n], y[n]);
+  for (int n = 0; n < M; ++n) {
+    const float2 t = fma2(gv[n], both(LOG2E), mul2(bias[n], both(LOG2E)));
+    y[n] = row_step(minus_c(exp2_of(t)), xv[n], y[n]);
   }
-  *(uint4 *)(h + (size_t)row * p.D + d) = pack16(y, (E *)nullptr);
+  *(uint4 *)(h + (size_t)row * p.D + d) = packed(y, (E *)nullptr);
   if (p.hT) store_state(p.hT, row, p.D, d, y);
 }
 
