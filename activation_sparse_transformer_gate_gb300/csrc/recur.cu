@@ -255,6 +255,13 @@ __device__ __forceinline__ RowBits row_bits(const RecurParams &p, Marks<R> &m, G
   b.last &= live;
   return b;
 }
+// Whether no sequence begins or ends in the tile from r0 on and all of its rows are some
+// sequence's, as far as can be told without a look at starts.
+template <int R>
+__device__ __forceinline__ bool plain_tile(const RecurParams &p, const Gap &gap, int r0, int lo, int hi) {
+  if (!p.starts || r0 < lo || r0 + R > hi) return false;
+  return gap.lo < r0 && gap.hi > r0 + R;
+}
 template <int R>
 __device__ __forceinline__ int first_of(const RecurParams &p, const Marks<R> &m, int r0, int k) {
   return p.starts ? m.first[k] : (r0 + k) / p.len;
@@ -305,19 +312,44 @@ __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
-// A thread's rows of a tile on their way to shared memory: row i to slot[i * 32],
-// which the same thread reads back.
-template <int S, typename E>
-__device__ __forceinline__ void fetch(uint4 *slot, const E *src, long long pitch, int row,
-                                      uint32_t live) {
+// All warps of the CTA, wherever each of them stands.
+template <int W>
+__device__ __forceinline__ void cta_barrier() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory");
+}
+
+// A CTA's tile of one matrix in shared memory: the channels of W warps, 16-byte chunks.
+// The chunks of a group's rows are exchanged so that a warp's lanes, which read one row
+// of every group, do not meet in a bank.
+template <typename G, int W>
+struct Slot {
+  static constexpr int CH = W * G::CX;  // chunks of a row
+  uint4 v[G::R * CH];
+  __device__ static __forceinline__ int at(int q, int k, int chunk) {
+    const int swap = CH >= 8 ? q * G::CX & 7 : (q >> 1) * G::CX & 3;
+    return (k * G::GROUPS + q) * CH + (chunk ^ swap);
+  }
+};
+
+// Copies the rows in [lo, hi) of a tile from r0 on, asynchronously, by the whole CTA:
+// consecutive lanes take consecutive chunks of a row, so that rows go in whole lines
+// (lanes that copied what they read themselves, 32 bytes of each of 16 rows, kept the
+// load unit busy for half the time).
+template <typename G, int W, typename E>
+__device__ __forceinline__ void fetch(Slot<G, W> &slot, const E *src, long long pitch, int r0, int lo,
+                                      int hi, int d0, int D) {
+  constexpr int CH = Slot<G, W>::CH, STEP = 32 * W / CH, S = G::S;  // rows of a pass
+  static_assert(STEP % S == 0 && G::R % STEP == 0, "a pass is whole groups");
+  const int chunk = threadIdx.x % CH, first = threadIdx.x / CH, d = d0 + chunk * G::N;
+  if (d >= D) return;
   const uint64_t once = gather_policy<L2_FIRST>();
-  const E *at = src + (size_t)row * pitch;
-  if (live == (1u << S) - 1) {
+  const E *at = src + (size_t)(r0 + first) * pitch + d;
+  const bool whole = r0 >= lo && r0 + G::R <= hi;
 #pragma unroll
-    for (int i = 0; i < S; ++i, at += pitch) copy16_async(slot + i * 32, at, once);
-  } else if (live) {
-    for (int i = 0; i < S; ++i, at += pitch)
-      if (live >> i & 1) copy16_async(slot + i * 32, at, once);
+  for (int m = 0; m < G::R / STEP; ++m, at += STEP * pitch) {
+    const int row = r0 + first + m * STEP;
+    if (whole || (row >= lo && row < hi))
+      copy16_async(&slot.v[Slot<G, W>::at(first / S + m * (STEP / S), first % S, chunk)], at, once);
   }
 }
 
@@ -490,7 +522,6 @@ struct Tile {
 template <typename E>
 struct FwdShared {
   using G = Fwd<E>;
-  uint4 x[3][G::S][32], gate[G::S][32];  // x of the tiles in both halves and the next one
   float2 steps[2][G::GROUPS * G::SLAB];  // the groups' steps, then what reaches them
   Exchange exchange;
   // h0 of the last sequence that begins in each lane's rows: hT may be h0, and who
@@ -499,17 +530,25 @@ struct FwdShared {
   Marks<G::R> marks[2];
 };
 
+// And a CTA: x of the tiles in both halves and the next one, gates of one.
+template <typename E, int W>
+struct FwdCta {
+  Slot<Fwd<E>, W> x[3], gate;
+  FwdShared<E> warps[W];
+};
+
 // A warp of the forward.
-template <typename E>
+template <typename E, int W>
 struct ForwardWarp {
   using G = Fwd<E>;
   static constexpr int M = G::N / 2, S = G::S, CX = G::CX;  // M pairs of channels a lane
   const E *x, *gate;
   E *h;
   const RecurParams &p;
+  FwdCta<E, W> &cta;
   FwdShared<E> &sh;
   Rounds rounds;
-  int C, rank, lane, q, cx, d, count, lo, hi;
+  int C, rank, lane, q, cx, chunk, d0, d, count, lo, hi;  // d0: the CTA's first channel
   bool on, lost;
   float2 bias[M];  // times log2(e)
   float carry;  // the state before the cluster's next rows, of the scan's channel
@@ -518,14 +557,13 @@ struct ForwardWarp {
   __device__ __forceinline__ uint32_t live_of(int i) const {
     return live_rows<S>(rounds.row(i, p.T) + q * S, lo, hi);
   }
-  __device__ __forceinline__ void fetch_x(int i) {
-    if (i < count && on)
-      fetch<S>(&sh.x[i % 3][0][lane], x + d, p.ld, rounds.row(i, p.T) + q * S, live_of(i));
+  __device__ __forceinline__ void fetch_tile(int i) {
+    if (i >= count) return;
+    const int r0 = rounds.row(i, p.T);
+    fetch(cta.x[i % 3], x, p.ld, r0, lo, hi, d0, p.D);
+    fetch(cta.gate, gate, p.ld, r0, lo, hi, d0, p.D);
   }
-  __device__ __forceinline__ void fetch_gate(int i) {
-    if (i < count && on)
-      fetch<S>(&sh.gate[0][lane], gate + d, p.ld, rounds.row(i, p.T) + q * S, live_of(i));
-  }
+  __device__ __forceinline__ int slot(int k) const { return Slot<G, W>::at(q, k, chunk); }
   // The first half of tile i: its rows as one step a lane, scanned and sent.
   template <bool PLAIN>
   __device__ __forceinline__ void first_half(int i, Tile &t, float2 (&mc)[S][M]) {
@@ -541,8 +579,8 @@ struct ForwardWarp {
           sh.held[i & 1][n / 2][lane] = make_float4(Hs[n].x, Hs[n].y, Hs[n + 1].x, Hs[n + 1].y);
       }
       float2 xv[M], gv[M];
-      pairs(sh.x[i % 3][k][lane], xv, (E *)nullptr);
-      pairs(sh.gate[k][lane], gv, (E *)nullptr);
+      pairs(cta.x[i % 3].v[slot(k)], xv, (E *)nullptr);
+      pairs(cta.gate.v[slot(k)], gv, (E *)nullptr);
 #pragma unroll
       for (int n = 0; n < M; ++n) {
         mc[k][n] = minus_c(exp2_of(fma2(gv[n], both(LOG2E), bias[n])));
@@ -554,7 +592,8 @@ struct ForwardWarp {
         for (int n = 0; n < M; ++n) Hs[n] = both(0.f);
       }
     }
-    fetch_gate(i + 1);
+    cta_barrier<W>();  // (all warps are done with the gates, and with tile i - 2)
+    fetch_tile(i + 1);
     const bool cut = !PLAIN && (t.bits.first != 0 || t.bits.live != G::ALL);
 #pragma unroll
     for (int n = 0; n < M; ++n) {
@@ -583,7 +622,7 @@ struct ForwardWarp {
     E *out = h + (size_t)row * p.D + d;
     uint4 rows[S];  // (read before the first store, which the reads could not pass)
 #pragma unroll
-    for (int k = 0; k < S; ++k) rows[k] = sh.x[i % 3][k][lane];
+    for (int k = 0; k < S; ++k) rows[k] = cta.x[i % 3].v[slot(k)];
 #pragma unroll
     for (int k = 0; k < S; ++k, out += p.D) {
       float2 xv[M];
@@ -615,20 +654,20 @@ __global__ void __launch_bounds__(32 * WARPS, SM_WARPS / WARPS)
 recur_forward_kernel(const E *x, const E *gate, E *h, RecurParams p) {
   pdl_begin();
   using G = Fwd<E>;
-  extern __shared__ __align__(16) char shared[];
+  extern __shared__ __align__(128) char shared[];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  FwdShared<E> &sh = ((FwdShared<E> *)shared)[warp];
+  FwdCta<E, WARPS> &cta = *(FwdCta<E, WARPS> *)shared;
+  FwdShared<E> &sh = cta.warps[warp];
   open_exchange(sh.exchange, C);
-  const int d0 = (int)(blockIdx.x / C * WARPS + warp) * G::SLAB;
+  const int base = (int)(blockIdx.x / C) * WARPS * G::SLAB, d0 = base + warp * G::SLAB;
   const Rounds rounds(C, rank, G::R, p.T);
-  const int q = lane / G::CX, cx = lane % G::CX, d = d0 + cx * G::N, count = d0 < p.D ? rounds.n : 0;
+  const int q = lane / G::CX, cx = lane % G::CX, d = d0 + cx * G::N, count = rounds.n;
   const int lo = p.starts ? max(0, p.starts[0]) : 0;
   const int hi = p.starts ? min(p.T, max(0, p.starts[p.B])) : p.T;
-  ForwardWarp<E> w{x, gate, h, p, sh, rounds, C, rank, lane, q, cx, d, count, lo, hi, d < p.D, false};
-  w.fetch_x(0);
-  w.fetch_gate(0);
+  ForwardWarp<E, WARPS> w{x, gate, h, p, cta, sh, rounds, C, rank, lane, q, cx, warp * G::CX + cx, base, d, count, lo, hi, d < p.D, false};
+  w.fetch_tile(0);
   empty_sequences(p, p.h0, p.hT, d0, min(p.D, d0 + G::SLAB), rank, C);
   load_state(w.on ? p.bias : nullptr, 0, 0, d, w.bias);
 #pragma unroll
@@ -637,14 +676,18 @@ recur_forward_kernel(const E *x, const E *gate, E *h, RecurParams p) {
   if (C > 1) cluster_wait();
   Tile now, next;
   float2 c[G::S][G::N / 2], cn[G::S][G::N / 2];
-  for (int i = count > 0 ? -1 : 0; i < count; ++i) {
+  for (int i = -1; i < count; ++i) {
     const int j = i + 1;
     if (j < count) {
       next.r0 = rounds.row(j, p.T);
-      next.bits = row_bits<G::S>(p, sh.marks[j & 1], w.gap, next.r0, q, w.live_of(j));
-      next.plain = __all_sync(0xFFFFFFFFu, (next.bits.first | next.bits.last) == 0 && next.bits.live == G::ALL);
+      next.plain = plain_tile<G::R>(p, w.gap, next.r0, lo, hi);
+      if (!next.plain) {
+        next.bits = row_bits<G::S>(p, sh.marks[j & 1], w.gap, next.r0, q, w.live_of(j));
+        next.plain = (next.bits.first | next.bits.last) == 0 && next.bits.live == G::ALL;
+      }
+      next.plain = __all_sync(0xFFFFFFFFu, next.plain);
       asm volatile("cp.async.wait_all;" ::: "memory");
-      w.fetch_x(j + 1);
+      cta_barrier<WARPS>();  // (the whole tile is there)
       if (next.plain) w.template first_half<true>(j, next, cn);
       else w.template first_half<false>(j, next, cn);
     }
@@ -669,7 +712,6 @@ recur_forward_kernel(const E *x, const E *gate, E *h, RecurParams p) {
 template <typename E>
 struct BwdShared {
   using G = Bwd<E>;
-  uint4 x[2][G::S][32], dh[3][G::S][32], gate[G::S][32];
   float2 stepsF[G::GROUPS * G::SLAB];     // the groups' steps forward
   float2 stepsB[2][G::GROUPS * G::SLAB];  // and back, then what reaches them
   Exchange exchange;
@@ -677,17 +719,24 @@ struct BwdShared {
   Marks<G::R> marks[2];
 };
 
+template <typename E, int W>
+struct BwdCta {
+  Slot<Bwd<E>, W> x[2], dh[3], gate;
+  BwdShared<E> warps[W];
+};
+
 // A warp of the backward, which goes from the last tile to the first.
-template <typename E>
+template <typename E, int W>
 struct BackwardWarp {
   using G = Bwd<E>;
   static constexpr int M = G::N / 2, S = G::S, CX = G::CX;
   const E *x, *gate, *dh;
   E *dx, *dgate;
   const RecurParams &p;
+  BwdCta<E, W> &cta;
   BwdShared<E> &sh;
   Rounds rounds;
-  int C, rank, lane, q, cx, d, sd, count, lo, hi;  // sd: the scan's channel
+  int C, rank, lane, q, cx, chunk, d0, d, sd, count, lo, hi;  // d0: the CTA's first channel, sd: the scan's
   bool on, lost;
   float2 bias[M], db[M];
   float carry;   // a G behind the cluster's next rows, of the scan's channel
@@ -698,16 +747,14 @@ struct BackwardWarp {
   __device__ __forceinline__ uint32_t live_of(int i) const {
     return live_rows<S>(first_row(i) + q * S, lo, hi);
   }
-  __device__ __forceinline__ void fetch_xd(int i) {
-    if (i >= count || !on) return;
-    const uint32_t live = live_of(i);
-    fetch<S>(&sh.x[i & 1][0][lane], x + d, p.ld, first_row(i) + q * S, live);
-    fetch<S>(&sh.dh[i % 3][0][lane], dh + d, p.D, first_row(i) + q * S, live);
+  __device__ __forceinline__ void fetch_tile(int i) {
+    if (i >= count) return;
+    const int r0 = first_row(i);
+    fetch(cta.x[i & 1], x, p.ld, r0, lo, hi, d0, p.D);
+    fetch(cta.gate, gate, p.ld, r0, lo, hi, d0, p.D);
+    fetch(cta.dh[i % 3], dh, (long long)p.D, r0, lo, hi, d0, p.D);
   }
-  __device__ __forceinline__ void fetch_gate(int i) {
-    if (i < count && on)
-      fetch<S>(&sh.gate[0][lane], gate + d, p.ld, first_row(i) + q * S, live_of(i));
-  }
+  __device__ __forceinline__ int slot(int k) const { return Slot<G, W>::at(q, k, chunk); }
   // (where a tile's first row begins a sequence it is not used)
   __device__ __forceinline__ float state_before(int i) const {
     const int r0 = i < count ? first_row(i) : p.T;
@@ -725,8 +772,8 @@ struct BackwardWarp {
       if (!PLAIN && (t.bits.first >> k & 1))
         load_state(on ? p.h0 : nullptr, first_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, Hs);
       float2 xv[M], gv[M];
-      pairs(sh.x[i & 1][k][lane], xv, (E *)nullptr);
-      pairs(sh.gate[k][lane], gv, (E *)nullptr);
+      pairs(cta.x[i & 1].v[slot(k)], xv, (E *)nullptr);
+      pairs(cta.gate.v[slot(k)], gv, (E *)nullptr);
 #pragma unroll
       for (int n = 0; n < M; ++n) {
         e[k][n] = exp2_held(fma2(gv[n], both(LOG2E), bias[n]));
@@ -739,7 +786,8 @@ struct BackwardWarp {
         for (int n = 0; n < M; ++n) Hs[n] = both(0.f);
       }
     }
-    fetch_gate(i + 1);
+    cta_barrier<W>();  // (all warps are done with the gates, and with what stood in the other slots)
+    fetch_tile(i + 1);
     const bool dead = !PLAIN && t.bits.live != G::ALL;
     const bool cutF = !PLAIN && (dead || t.bits.first), cutB = !PLAIN && (dead || t.bits.last);
 #pragma unroll
@@ -753,7 +801,7 @@ struct BackwardWarp {
       if (!PLAIN && (t.bits.last >> k & 1))
         load_state(on ? p.dhT : nullptr, last_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, Hs);
       float2 dv[M];
-      pairs(sh.dh[i % 3][k][lane], dv, (E *)nullptr);
+      pairs(cta.dh[i % 3].v[slot(k)], dv, (E *)nullptr);
 #pragma unroll
       for (int n = 0; n < M; ++n) {
         const float2 g = add2(dv[n], Hs[n]);
@@ -784,7 +832,7 @@ struct BackwardWarp {
       if (!PLAIN && on && (t.bits.first >> k & 1))
         load_state(p.h0, first_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, y);
       float2 xv[M];
-      pairs(sh.x[i & 1][k][lane], xv, (E *)nullptr);
+      pairs(cta.x[i & 1].v[slot(k)], xv, (E *)nullptr);
 #pragma unroll
       for (int n = 0; n < M; ++n) {
         const float2 minus_took = mul2(less2(y[n], xv[n]), mc[k][n]);
@@ -810,7 +858,7 @@ struct BackwardWarp {
     E *px = dx + (size_t)row * p.ld + d, *pg = dgate + (size_t)row * p.ld + d;
     uint4 rows[S];
 #pragma unroll
-    for (int k = 0; k < S; ++k) rows[k] = sh.dh[i % 3][k][lane];
+    for (int k = 0; k < S; ++k) rows[k] = cta.dh[i % 3].v[slot(k)];
 #pragma unroll
     for (int k = S - 1; k >= 0; --k) {
       if (!PLAIN) {
@@ -842,21 +890,21 @@ recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, R
   pdl_begin();
   using G = Bwd<E>;
   constexpr int N = G::N, CX = G::CX;
-  extern __shared__ __align__(16) char shared[];
+  extern __shared__ __align__(128) char shared[];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  BwdShared<E> &sh = ((BwdShared<E> *)shared)[warp];
+  BwdCta<E, WARPS> &cta = *(BwdCta<E, WARPS> *)shared;
+  BwdShared<E> &sh = cta.warps[warp];
   open_exchange(sh.exchange, C);
-  const int d0 = (int)(blockIdx.x / C * WARPS + warp) * G::SLAB;
+  const int base = (int)(blockIdx.x / C) * WARPS * G::SLAB, d0 = base + warp * G::SLAB;
   const Rounds rounds(C, rank, G::R, p.T);
-  const int q = lane / CX, cx = lane % CX, d = d0 + cx * N, count = d0 < p.D ? rounds.n : 0;
+  const int q = lane / CX, cx = lane % CX, d = d0 + cx * N, count = rounds.n;
   const int sc = lane % G::ACROSS, sd = d0 + sc % CX * N + sc / CX;
   const int lo = p.starts ? max(0, p.starts[0]) : 0;
   const int hi = p.starts ? min(p.T, max(0, p.starts[p.B])) : p.T;
-  BackwardWarp<E> w{x, gate, dh, dx, dgate, p, sh, rounds, C, rank, lane, q, cx, d, sd, count, lo, hi, d < p.D, false};
-  w.fetch_xd(0);
-  w.fetch_gate(0);
+  BackwardWarp<E, WARPS> w{x, gate, dh, dx, dgate, p, cta, sh, rounds, C, rank, lane, q, cx, warp * CX + cx, base, d, sd, count, lo, hi, d < p.D, false};
+  w.fetch_tile(0);
   w.before = w.state_before(0);
   empty_sequences(p, p.dhT, p.dh0, d0, min(p.D, d0 + G::SLAB), rank, C);
   load_state(w.on ? p.bias : nullptr, 0, 0, d, w.bias);
@@ -869,14 +917,18 @@ recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, R
   if (C > 1) cluster_wait();
   Tile now, next;
   float2 c[G::S][N / 2], e[G::S][N / 2], cn[G::S][N / 2], en[G::S][N / 2];
-  for (int i = count > 0 ? -1 : 0; i < count; ++i) {
+  for (int i = -1; i < count; ++i) {
     const int j = i + 1;
     if (j < count) {
       next.r0 = w.first_row(j);
-      next.bits = row_bits<G::S>(p, sh.marks[j & 1], w.gap, next.r0, q, w.live_of(j));
-      next.plain = __all_sync(0xFFFFFFFFu, (next.bits.first | next.bits.last) == 0 && next.bits.live == G::ALL);
+      next.plain = plain_tile<G::R>(p, w.gap, next.r0, lo, hi);
+      if (!next.plain) {
+        next.bits = row_bits<G::S>(p, sh.marks[j & 1], w.gap, next.r0, q, w.live_of(j));
+        next.plain = (next.bits.first | next.bits.last) == 0 && next.bits.live == G::ALL;
+      }
+      next.plain = __all_sync(0xFFFFFFFFu, next.plain);
       asm volatile("cp.async.wait_all;" ::: "memory");
-      w.fetch_xd(j + 1);
+      cta_barrier<WARPS>();  // (the whole tile is there)
       if (next.plain) w.template first_half<true>(j, next, en, cn);
       else w.template first_half<false>(j, next, en, cn);
     }
@@ -994,7 +1046,7 @@ bool narrow(int D) { return (long long)((D + 63) / 64) * MAX_CLUSTER < num_sms()
 template <typename E, int WARPS>
 cudaError_t forward_w(const RecurArgs &a, cudaStream_t s) {
   using G = Fwd<E>;
-  constexpr int SMEM = WARPS * sizeof(FwdShared<E>);
+  constexpr int SMEM = sizeof(FwdCta<E, WARPS>);
   auto kern = recur_forward_kernel<E, WARPS>;
   static const Shape<decltype(kern)> shape(kern, 32 * WARPS, SMEM);
   if (shape.attr != cudaSuccess) return shape.attr;
@@ -1018,7 +1070,7 @@ cudaError_t forward_t(const RecurArgs &a, cudaStream_t s) {
 template <typename E, int WARPS>
 cudaError_t backward_w(const RecurArgs &a, cudaStream_t s) {
   using G = Bwd<E>;
-  constexpr int SMEM = WARPS * sizeof(BwdShared<E>);
+  constexpr int SMEM = sizeof(BwdCta<E, WARPS>);
   auto kern = recur_backward_kernel<E, WARPS>;
   static const Shape<decltype(kern)> shape(kern, 32 * WARPS, SMEM);
   if (shape.attr != cudaSuccess) return shape.attr;
