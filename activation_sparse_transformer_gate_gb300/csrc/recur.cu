@@ -29,10 +29,11 @@
 // HBM would bound it (3 values an element forward, 5 backward: 60 and 101 us at 16384 x
 // 4096 bf16), but what bounds it now is latency: the gates stay in registers from one
 // pass over a tile to the other, for two tiles, which leaves room for 8 warps an SM, and
-// a round takes a warp 4250 cycles alone and 5700 beside the others (107 and 186 us).
+// a round takes a warp 3700 cycles alone and 5100 beside the others (95 and 176 us).
 // Measured on the way: CTAs in step with barriers, 150 and 430 us; warps by themselves,
-// 120 and 187; gates computed again in the second pass (24 warps an SM, inputs of a
-// round from L2), 120 and 258.
+// 120 and 187; tile and tile overlapped, 107 and 186; two channels an instruction, 102 and
+// 183; rows copied in whole lines by the CTA, 95 and 176.  Gates computed again in the
+// second pass (24 warps an SM, a round's inputs from L2): 120 and 258.
 #include <cooperative_groups.h>
 #include <limits.h>
 
@@ -50,6 +51,7 @@ namespace {
 constexpr int SM_WARPS = 8;         // resident, by registers and shared memory
 constexpr int MAX_CLUSTER = 8;
 constexpr float LOG2E = 1.4426950408889634f;
+constexpr int FEW = 128;            // entries of starts that a CTA keeps at hand
 constexpr float CUT = 2.f;          // a C that stands for: nothing comes through
 
 struct RecurParams {
@@ -164,13 +166,13 @@ struct Marks {
 };
 
 // The first entry of starts[0 .. B] that is >= row (B + 1: none), by one warp.
-__device__ __forceinline__ int first_entry(const RecurParams &p, int row) {
+__device__ __forceinline__ int first_entry(const int32_t *starts, int B, int row) {
   const int lane = threadIdx.x & 31;
-  int lo = 0, hi = p.B + 1;     // the answer is in [lo, hi]
+  int lo = 0, hi = B + 1;     // the answer is in [lo, hi]
   while (lo < hi) {
     const int step = (hi - lo + 31) / 32;
     const long long at = (long long)lo + (long long)(lane + 1) * step - 1;
-    const bool before = at < hi && p.starts[at] < row;
+    const bool before = at < hi && starts[at] < row;
     const int n = __popc(__ballot_sync(0xFFFFFFFFu, before));
     const long long top = (long long)lo + (long long)(n + 1) * step - 1;
     lo += n * step;
@@ -188,23 +190,23 @@ struct Gap {
 // Marks a tile's rows; returns whether there are any.  Most tiles lie within a gap
 // that is known already, and cost no look at starts.
 template <int R>
-__device__ __forceinline__ bool mark(const RecurParams &p, Marks<R> &m, Gap &gap, int r0) {
+__device__ __forceinline__ bool mark(const int32_t *starts, int B, Marks<R> &m, Gap &gap, int r0) {
   if (gap.lo < r0 && gap.hi > r0 + R) return false;
   const int lane = threadIdx.x & 31;
-  const int from = first_entry(p, r0);
-  gap.lo = from > 0 ? p.starts[from - 1] : INT_MIN;
-  gap.hi = from <= p.B ? p.starts[from] : INT_MAX;
+  const int from = first_entry(starts, B, r0);
+  gap.lo = from > 0 ? starts[from - 1] : INT_MIN;
+  gap.hi = from <= B ? starts[from] : INT_MAX;
   __syncwarp();  // (the last tile's marks have been read)
   if (lane < R / 32) m.firsts[lane] = m.lasts[lane] = 0;
   __syncwarp();
-  for (int s = from + lane; s <= p.B; s += 32) {
-    const int v = p.starts[s], k = v - r0;
+  for (int s = from + lane; s <= B; s += 32) {
+    const int v = starts[s], k = v - r0;
     if (v > r0 + R || v < r0) break;  // (below: entries that descend)
-    if (s < p.B && k < R && p.starts[s + 1] > v) {
+    if (s < B && k < R && starts[s + 1] > v) {
       m.first[k] = s;
       atomicOr(&m.firsts[k / 32], 1u << (k & 31));
     }
-    if (s > 0 && k > 0 && p.starts[s - 1] < v) {
+    if (s > 0 && k > 0 && starts[s - 1] < v) {
       m.last[k - 1] = s - 1;
       atomicOr(&m.lasts[(k - 1) / 32], 1u << ((k - 1) & 31));
     }
@@ -226,12 +228,12 @@ __device__ __forceinline__ uint32_t live_rows(int row, int lo, int hi) {
   return (ALL << below) & ALL & ((1u << upto) - 1);
 }
 template <int S, int R>
-__device__ __forceinline__ RowBits row_bits(const RecurParams &p, Marks<R> &m, Gap &gap, int r0, int q,
-                                            uint32_t live) {
+__device__ __forceinline__ RowBits row_bits(const RecurParams &p, const int32_t *starts, Marks<R> &m,
+                                            Gap &gap, int r0, int q, uint32_t live) {
   constexpr uint32_t ALL = (1u << S) - 1;
   RowBits b{0, 0, live};
   if (p.starts) {
-    if (mark(p, m, gap, r0)) {
+    if (mark(starts, p.B, m, gap, r0)) {
       const int k = q * S;  // (S divides 32: a lane's rows are of one word)
       b.first = m.firsts[k / 32] >> (k & 31) & ALL;
       b.last = m.lasts[k / 32] >> (k & 31) & ALL;
@@ -330,6 +332,14 @@ struct Slot {
     return (k * G::GROUPS + q) * CH + (chunk ^ swap);
   }
 };
+
+// starts, in shared memory where there are few (from the CTA's next barrier on).
+template <int W>
+__device__ __forceinline__ const int32_t *keep_starts(const RecurParams &p, int32_t *few) {
+  if (!p.starts || p.B >= FEW) return p.starts;
+  for (int k = threadIdx.x; k <= p.B; k += 32 * W) few[k] = p.starts[k];
+  return few;
+}
 
 // Copies the rows in [lo, hi) of a tile from r0 on, asynchronously, by the whole CTA:
 // consecutive lanes take consecutive chunks of a row, so that rows go in whole lines
@@ -535,6 +545,7 @@ template <typename E, int W>
 struct FwdCta {
   Slot<Fwd<E>, W> x[3], gate;
   FwdShared<E> warps[W];
+  int32_t starts[FEW];
 };
 
 // A warp of the forward.
@@ -660,6 +671,7 @@ recur_forward_kernel(const E *x, const E *gate, E *h, RecurParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   FwdCta<E, WARPS> &cta = *(FwdCta<E, WARPS> *)shared;
   FwdShared<E> &sh = cta.warps[warp];
+  const int32_t *starts = keep_starts<WARPS>(p, cta.starts);
   open_exchange(sh.exchange, C);
   const int base = (int)(blockIdx.x / C) * WARPS * G::SLAB, d0 = base + warp * G::SLAB;
   const Rounds rounds(C, rank, G::R, p.T);
@@ -682,7 +694,7 @@ recur_forward_kernel(const E *x, const E *gate, E *h, RecurParams p) {
       next.r0 = rounds.row(j, p.T);
       next.plain = plain_tile<G::R>(p, w.gap, next.r0, lo, hi);
       if (!next.plain) {
-        next.bits = row_bits<G::S>(p, sh.marks[j & 1], w.gap, next.r0, q, w.live_of(j));
+        next.bits = row_bits<G::S>(p, starts, sh.marks[j & 1], w.gap, next.r0, q, w.live_of(j));
         next.plain = (next.bits.first | next.bits.last) == 0 && next.bits.live == G::ALL;
       }
       next.plain = __all_sync(0xFFFFFFFFu, next.plain);
@@ -723,6 +735,7 @@ template <typename E, int W>
 struct BwdCta {
   Slot<Bwd<E>, W> x[2], dh[3], gate;
   BwdShared<E> warps[W];
+  int32_t starts[FEW];
 };
 
 // A warp of the backward, which goes from the last tile to the first.
@@ -896,6 +909,7 @@ recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, R
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   BwdCta<E, WARPS> &cta = *(BwdCta<E, WARPS> *)shared;
   BwdShared<E> &sh = cta.warps[warp];
+  const int32_t *starts = keep_starts<WARPS>(p, cta.starts);
   open_exchange(sh.exchange, C);
   const int base = (int)(blockIdx.x / C) * WARPS * G::SLAB, d0 = base + warp * G::SLAB;
   const Rounds rounds(C, rank, G::R, p.T);
@@ -923,7 +937,7 @@ recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, R
       next.r0 = w.first_row(j);
       next.plain = plain_tile<G::R>(p, w.gap, next.r0, lo, hi);
       if (!next.plain) {
-        next.bits = row_bits<G::S>(p, sh.marks[j & 1], w.gap, next.r0, q, w.live_of(j));
+        next.bits = row_bits<G::S>(p, starts, sh.marks[j & 1], w.gap, next.r0, q, w.live_of(j));
         next.plain = (next.bits.first | next.bits.last) == 0 && next.bits.live == G::ALL;
       }
       next.plain = __all_sync(0xFFFFFFFFu, next.plain);
