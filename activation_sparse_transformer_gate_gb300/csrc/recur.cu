@@ -1053,8 +1053,8 @@ struct Shape {
 };
 
 // Four warps a CTA, or two where they leave SMs without one (us, forward and backward,
-// two | four: 2048 x 1024 fp32 13 + 21 | 15 + 24, 131072 x 1024 forward 270 | 354, 4096 x
-// 2048 34 + 40 | 25 + 37, 16384 x 4096 129 + 189 | 107 + 186).
+// two | four: 2048 x 1024 fp32 13 + 19 | 14 + 23, 131072 x 1024 forward 260 | 331, 4096 x
+// 2048 31 + 35 | 22 + 33, 16384 x 4096 118 + 179 | 94 + 177).
 bool narrow(int D) { return (long long)((D + 63) / 64) * MAX_CLUSTER < num_sms(); }
 
 template <typename E, int WARPS>
