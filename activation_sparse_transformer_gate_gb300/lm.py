@@ -142,8 +142,8 @@ class twell_adamw_tensor(ctypes.Structure):
 class AdamWTensors:
     """The tensors of a twell_adamw_step, kept by a program beside them: ``add`` each once, then
     step as often as wanted.  The tensors are held, and checked when they are added: types
-    (TWELL_ERR_DTYPE), elements, place and contiguity (TWELL_ERR_ARG), and that nothing that the
-    step writes overlaps with anything else (TWELL_ERR_ARG).  ``state_bits`` 8: m and v are float8_e4m3fn codes with
+    (TWELL_ERR_DTYPE), elements, place and contiguity (TWELL_ERR_ARG); before the first step, that
+    nothing that it writes overlaps with anything else (TWELL_ERR_ARG).  ``state_bits`` 8: m and v are float8_e4m3fn codes with
     fp32 scales for each 256 elements."""
 
     def __init__(self, state_bits: int = 32):
@@ -175,19 +175,11 @@ class AdamWTensors:
             raise TwellError(-3, "AdamWTensors.add")
         if any(t.numel() != k or not t.is_cuda or not t.is_contiguous() for t, _, k in every):
             raise TwellError(-1, "AdamWTensors.add")
-        # (a gradient may be shared, so it is compared with what is written alone)
         span = lambda t: (t.data_ptr(), t.data_ptr() + t.nbytes)  # noqa: E731
-        both = sorted(self.written + [span(t) for t, _, k in wanted if k])
-        read = self.read + ([span(grad)] if n else [])
-        ends = [b for _, b in both]
-        for lo, hi in read:
-            i = bisect.bisect_right(ends, lo)
-            if i < len(both) and both[i][0] < hi:
-                raise TwellError(-1, "AdamWTensors.add")
-        if any(a[1] > b[0] for a, b in zip(both, both[1:])):
-            raise TwellError(-1, "AdamWTensors.add")
-        self.read = read
-        self.written, self.grad_dtype, self.array = both, dtype, None
+        self.written += [span(t) for t, _, k in wanted if k]
+        if n:
+            self.read.append(span(grad))
+        self.grad_dtype, self.array = dtype, None
         self.held.append((param, grad, m, v, mscale, vscale, copy))
         self.rows.append([None if t is None else t.data_ptr() for t in self.held[-1]]
                          + [n, int(first), float(decay)])
@@ -195,6 +187,15 @@ class AdamWTensors:
     def table(self):
         """The address of the C array, and how many it has."""
         if self.array is None:
+            # (gradients may be shared: they are compared with what is written alone)
+            both = sorted(self.written)
+            ends = [b for _, b in both]
+            if any(a[1] > b[0] for a, b in zip(both, both[1:])):
+                raise TwellError(-1, "AdamWTensors")
+            for lo, hi in self.read:
+                i = bisect.bisect_right(ends, lo)
+                if i < len(both) and both[i][0] < hi:
+                    raise TwellError(-1, "AdamWTensors")
             self.array = (twell_adamw_tensor * max(1, len(self.rows)))(*map(tuple, self.rows))
             self.address = ctypes.addressof(self.array)
         return self.address, len(self.rows)

@@ -211,6 +211,30 @@ def test_rounding_goes_by_the_elements_number(n):
     whole.compare(*whole.step(3, 5))
 
 
+def test_overlaps_are_refused():
+    """What a step writes is written once, and is no gradient; gradients may be shared."""
+    x = torch.zeros(4096, device="cuda")
+    p, g, m, v = x[:512], x[512:1024], x[1024:1536], x[1536:2048]
+    half = torch.zeros(512, dtype=torch.bfloat16, device="cuda")
+
+    def code(*rows):
+        lst = tw.AdamWTensors(32)
+        for r in rows:
+            lst.add(*r[:4], copy=r[4] if len(r) > 4 else None)
+        try:
+            tw.twell_adamw_step(lst, 0.0, B1, B2, EPS, 1)
+        except tw.TwellError as e:
+            return e.code
+        return 0
+
+    other = (x[2048:2560], g, x[2560:3072], x[3072:3584])
+    assert code((p, g, m, v, half), other) == 0
+    for bad in ((p, g, m, v, half), (x[:512], g, *other[2:]), (other[0], g, other[2], x[1020:1532]),
+                (other[0], x[256:768], *other[2:]), (other[0], other[2], *other[2:]),
+                (*other, half)):
+        assert code((p, g, m, v, half), bad) == -1
+
+
 def test_rounding_is_unbiased():
     """The mean of many roundings of one value is the value: within 5 standard deviations, a
     rounding's being at most half a step."""
