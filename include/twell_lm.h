@@ -162,8 +162,8 @@ twell_status twell_distill_backward(const void *z, long long ldz, const int32_t 
  *   h0 [B][D] fp32: the states before the sequences (NULL: 0); hT [B][D] fp32 or
  *   NULL: the states behind them (of an empty sequence: h0).  hT may be h0.
  *   states [twell_recur_states(T)][D] fp32 or NULL: what the backward needs.
- * The state is held in fp32, h is its rounding.  B = T without starts is the step
- * of a decoded token for each of T sequences.
+ * The state is held in fp32, h is its rounding; h is a buffer of its own.  B = T
+ * without starts is the step of a decoded token for each of T sequences.
  * 1 <= T, 1 <= B, D <= 65536, ld >= D; D*elem_size and ld*elem_size multiples
  * of 16. */
 twell_status twell_recur_forward(const void *x, const void *gate, long long ld, const float *bias,
