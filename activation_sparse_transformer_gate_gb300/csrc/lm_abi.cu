@@ -248,7 +248,7 @@ static twell_status check_recur(const RecurArgs &a) {
   const twell_status st = check_dtype(a.dtype);
   if (st != TWELL_OK) return st;
   if (!a.x || !a.gate || !a.status || a.T < 1 || a.T > MAX_ROWS || a.B < 1 || a.B > MAX_ROWS ||
-      a.D < 1 || a.D > RECUR_MAX_D || a.ld < a.D || a.ld > (1ll << 40))
+      a.D < 1 || a.D > RECUR_MAX_D || a.ld < a.D || a.ld > (1ll << 34))
     return TWELL_ERR_ARG;
   if (!a.starts && a.T % a.B != 0) return TWELL_ERR_ARG;
   const size_t es = elem_size(a.dtype);

@@ -151,7 +151,7 @@ struct Geo {
   // columns are exchanged so that lanes that differ in q and cx do not meet in a bank
   // (nor do those of the scan, which differ in channel and part).
   __device__ static __forceinline__ int at(int q, int ch) {
-    return q * SLAB + (ch ^ (q % (SLAB / CX) * CX));
+    return q * SLAB + (ch ^ ((CX == 2 ? q : q << 1 | q >> 2) % (SLAB / CX) * CX));
   }
 };
 template <typename E> using Fwd = Geo<E, 8>;
@@ -320,18 +320,41 @@ __device__ __forceinline__ void cta_barrier() {
   asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory");
 }
 
-// A CTA's tile of one matrix in shared memory: the channels of W warps, 16-byte chunks.
-// The chunks of a group's rows are exchanged so that a warp's lanes, which read one row
-// of every group, do not meet in a bank.
+// A CTA's tile of one matrix in shared memory, the channels of W warps, as the copies of
+// a tensor leave it: boxes of up to 128 bytes of a row, whose 16-byte chunks are exchanged
+// by the address; the k-th rows of all groups stand together.
 template <typename G, int W>
-struct Slot {
-  static constexpr int CH = W * G::CX;  // chunks of a row
-  uint4 v[G::R * CH];
+struct alignas(1024) Slot {
+  static constexpr int CH = W * G::CX, BOX = CH < 8 ? CH : 8;  // chunks of a row, of a box's
+  static constexpr int BOXES = CH / BOX, LONG = G::R * BOX;
+  static constexpr uint32_t BYTES = BOXES * LONG * 16;
+  uint4 v[BOXES * LONG];
+  static_assert(G::GROUPS % 8 == 0 && (BOX == 8 || (BOX == 4 && G::CX == 2)), "see at, group");
   __device__ static __forceinline__ int at(int q, int k, int chunk) {
-    const int swap = CH >= 8 ? q * G::CX & 7 : (q >> 1) * G::CX & 3;
-    return (k * G::GROUPS + q) * CH + (chunk ^ swap);
+    return chunk / BOX * LONG + (k * G::GROUPS + q) * BOX + (chunk % BOX ^ (BOX == 8 ? q & 7 : q >> 1 & 3));
+  }
+  // A lane's group: eight lanes in a row read one row of 8 / CX groups at once, which are
+  // those that do not meet in a bank.
+  __device__ static __forceinline__ int group(int g) {
+    if (BOX == 4) return (g & 9) | (g << 1 & 4) | (g >> 1 & 2);
+    return (g & 8) | ((G::CX == 2 ? g << 1 | (g >> 2 & 1) : g << 2 | g >> 1) & 7);
   }
 };
+
+// The matrices of a call as tensors of (channel, group of S rows, row of the group).
+// What T leaves behind the last whole group is not a part of them.
+struct Maps {
+  CUtensorMap x, gate, dh;
+};
+
+__device__ __forceinline__ void load_box(void *dst, const CUtensorMap &map, int d, int group,
+                                         uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+      "l"((uint64_t)&map), "r"(d), "r"(group), "r"(0), "r"(bar), "l"(policy)
+      : "memory");
+}
 
 // starts, in shared memory where there are few (from the CTA's next barrier on).
 template <int W>
@@ -341,26 +364,25 @@ __device__ __forceinline__ const int32_t *keep_starts(const RecurParams &p, int3
   return few;
 }
 
-// Copies the rows in [lo, hi) of a tile from r0 on, asynchronously, by the whole CTA:
-// consecutive lanes take consecutive chunks of a row, so that rows go in whole lines
-// (lanes that copied what they read themselves, 32 bytes of each of 16 rows, kept the
-// load unit busy for half the time).
-template <typename G, int W, typename E>
-__device__ __forceinline__ void fetch(Slot<G, W> &slot, const E *src, long long pitch, int r0, int lo,
-                                      int hi, int d0, int D) {
-  constexpr int CH = Slot<G, W>::CH, STEP = 32 * W / CH, S = G::S;  // rows of a pass
-  static_assert(STEP % S == 0 && G::R % STEP == 0, "a pass is whole groups");
-  const int chunk = threadIdx.x % CH, first = threadIdx.x / CH, d = d0 + chunk * G::N;
-  if (d >= D) return;
+// Copies a tile from row r0 on, by one thread.
+template <typename G, int W>
+__device__ __forceinline__ void fetch(Slot<G, W> &slot, const CUtensorMap &map, int r0, int d0,
+                                      uint32_t bar) {
+  using Sl = Slot<G, W>;
   const uint64_t once = gather_policy<L2_FIRST>();
-  const E *at = src + (size_t)(r0 + first) * pitch + d;
-  const bool whole = r0 >= lo && r0 + G::R <= hi;
 #pragma unroll
-  for (int m = 0; m < G::R / STEP; ++m, at += STEP * pitch) {
-    const int row = r0 + first + m * STEP;
-    if (whole || (row >= lo && row < hi))
-      copy16_async(&slot.v[Slot<G, W>::at(first / S + m * (STEP / S), first % S, chunk)], at, once);
-  }
+  for (int b = 0; b < Sl::BOXES; ++b)
+    load_box(slot.v + b * Sl::LONG, map, d0 + b * Sl::BOX * G::N, r0 / G::S, bar, once);
+}
+// The rows of its last group where T cuts it, a warp's channels of them.
+template <typename G, int W, typename E>
+__device__ __forceinline__ void fetch_rest(Slot<G, W> &slot, const E *src, long long pitch, int r0,
+                                           int T, int d0, int D) {
+  const int lane = threadIdx.x & 31, k = lane / G::CX, cx = lane % G::CX, rest = T % G::S;
+  const int d = d0 + cx * G::N, whole = T - rest;
+  if (k < rest && d < D)
+    slot.v[Slot<G, W>::at((whole - r0) / G::S, k, (threadIdx.x >> 5) * G::CX + cx)] =
+        *(const uint4 *)(src + (size_t)(whole + k) * pitch + d);
 }
 
 // The scan over a tile's groups, from the tile's first row on (BACK: from its last).
@@ -438,14 +460,19 @@ __device__ __forceinline__ uint32_t peer(uint32_t addr, int rank) {
   return r;
 }
 
+// (OTHERS: what came in is from other CTAs of the cluster)
+template <bool OTHERS>
 __device__ __forceinline__ bool arrived(uint32_t bar, uint32_t parity, uint64_t limit) {
   uint64_t t0 = 0;
   for (;;) {
     uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    if (OTHERS)
+      asm volatile(
+          "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+          " selp.u32 %0, 1, 0, p;\n}\n"
+          : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    else
+      ok = mbar_try(bar, parity);
     if (ok) return true;
     const uint64_t now = global_timer();
     if (!t0) t0 = now;
@@ -480,10 +507,10 @@ __device__ __forceinline__ float receive_steps(Exchange &x, int n, int rank, int
   }
   if (!lost) {
     const uint32_t bar = smem_u32(&x.bar[i % ROOM]), parity = (uint32_t)i / ROOM & 1;
-    if (!arrived(bar, parity, WAIT_LIMIT_NS)) {
+    if (!arrived<true>(bar, parity, WAIT_LIMIT_NS)) {
       set_status(status, TWELL_ERR_TIMEOUT);
       // (what is on its way has to come in before the barrier is used again)
-      lost = !arrived(bar, parity, DRAIN_LIMIT_NS);
+      lost = !arrived<true>(bar, parity, DRAIN_LIMIT_NS);
     }
     lost = __any_sync(0xFFFFFFFFu, lost);
   }
@@ -492,6 +519,7 @@ __device__ __forceinline__ float receive_steps(Exchange &x, int n, int rank, int
 #pragma unroll
   for (int k = 0; k < MAX_CLUSTER; ++k) {
     const int r = BACK ? MAX_CLUSTER - 1 - k : k;
+    if (r >= MAX_CLUSTER / 2 && n <= MAX_CLUSTER / 2) continue;
     if (r == rank) in = carry;
     const float2 v = x.total[i % ROOM][r][ch];
     carry = apply(v.x, v.y, carry);
@@ -546,6 +574,7 @@ struct FwdCta {
   Slot<Fwd<E>, W> x[3], gate;
   FwdShared<E> warps[W];
   int32_t starts[FEW];
+  uint64_t bar[2];  // of the copies of the tiles, by the tile's parity
 };
 
 // A warp of the forward.
@@ -555,6 +584,7 @@ struct ForwardWarp {
   static constexpr int M = G::N / 2, S = G::S, CX = G::CX;  // M pairs of channels a lane
   const E *x, *gate;
   E *h;
+  const Maps &maps;
   const RecurParams &p;
   FwdCta<E, W> &cta;
   FwdShared<E> &sh;
@@ -569,10 +599,28 @@ struct ForwardWarp {
     return live_rows<S>(rounds.row(i, p.T) + q * S, lo, hi);
   }
   __device__ __forceinline__ void fetch_tile(int i) {
-    if (i >= count) return;
+    if (i >= count || threadIdx.x != 0) return;
     const int r0 = rounds.row(i, p.T);
-    fetch(cta.x[i % 3], x, p.ld, r0, lo, hi, d0, p.D);
-    fetch(cta.gate, gate, p.ld, r0, lo, hi, d0, p.D);
+    const bool any = r0 / S < p.T / S;
+    const uint32_t bar = smem_u32(&cta.bar[i & 1]);
+    mbar_expect_tx(bar, any ? 2 * Slot<G, W>::BYTES : 0);
+    if (!any) return;
+    fetch(cta.x[i % 3], maps.x, r0, d0, bar);
+    fetch(cta.gate, maps.gate, r0, d0, bar);
+  }
+  __device__ __forceinline__ void wait_tile(int i) {
+    const uint32_t bar = smem_u32(&cta.bar[i & 1]), parity = (uint32_t)i >> 1 & 1;
+    if (!arrived<false>(bar, parity, WAIT_LIMIT_NS)) {
+      set_status(p.status, TWELL_ERR_TIMEOUT);
+      arrived<false>(bar, parity, DRAIN_LIMIT_NS);  // (what is on its way has to come in)
+    }
+    const int r0 = rounds.row(i, p.T);
+    if (p.T % S == 0 || r0 >= p.T || r0 + G::R < p.T) return;
+    const int own = d - cx * G::N;
+    fetch_rest(cta.x[i % 3], x, p.ld, r0, p.T, own, p.D);
+    fetch_rest(cta.gate, gate, p.ld, r0, p.T, own, p.D);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
   }
   __device__ __forceinline__ int slot(int k) const { return Slot<G, W>::at(q, k, chunk); }
   // The first half of tile i: its rows as one step a lane, scanned and sent.
@@ -662,10 +710,10 @@ struct ForwardWarp {
 
 template <typename E, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, SM_WARPS / WARPS)
-recur_forward_kernel(const E *x, const E *gate, E *h, RecurParams p) {
+recur_forward_kernel(const E *x, const E *gate, E *h, const __grid_constant__ Maps maps, RecurParams p) {
   pdl_begin();
   using G = Fwd<E>;
-  extern __shared__ __align__(128) char shared[];
+  extern __shared__ __align__(1024) char shared[];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -675,10 +723,14 @@ recur_forward_kernel(const E *x, const E *gate, E *h, RecurParams p) {
   open_exchange(sh.exchange, C);
   const int base = (int)(blockIdx.x / C) * WARPS * G::SLAB, d0 = base + warp * G::SLAB;
   const Rounds rounds(C, rank, G::R, p.T);
-  const int q = lane / G::CX, cx = lane % G::CX, d = d0 + cx * G::N, count = rounds.n;
+  const int q = Slot<G, WARPS>::group(lane / G::CX), cx = lane % G::CX, d = d0 + cx * G::N, count = rounds.n;
   const int lo = p.starts ? max(0, p.starts[0]) : 0;
   const int hi = p.starts ? min(p.T, max(0, p.starts[p.B])) : p.T;
-  ForwardWarp<E, WARPS> w{x, gate, h, p, cta, sh, rounds, C, rank, lane, q, cx, warp * G::CX + cx, base, d, count, lo, hi, d < p.D, false};
+  ForwardWarp<E, WARPS> w{x, gate, h, maps, p, cta, sh, rounds, C, rank, lane, q, cx, warp * G::CX + cx, base, d, count, lo, hi, d < p.D, false};
+  if (threadIdx.x < 2) mbar_init(smem_u32(&cta.bar[threadIdx.x]), 1);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  cta_barrier<WARPS>();
   w.fetch_tile(0);
   empty_sequences(p, p.h0, p.hT, d0, min(p.D, d0 + G::SLAB), rank, C);
   load_state(w.on ? p.bias : nullptr, 0, 0, d, w.bias);
@@ -698,8 +750,7 @@ recur_forward_kernel(const E *x, const E *gate, E *h, RecurParams p) {
         next.plain = (next.bits.first | next.bits.last) == 0 && next.bits.live == G::ALL;
       }
       next.plain = __all_sync(0xFFFFFFFFu, next.plain);
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      cta_barrier<WARPS>();  // (the whole tile is there)
+      w.wait_tile(j);
       if (next.plain) w.template first_half<true>(j, next, cn);
       else w.template first_half<false>(j, next, cn);
     }
@@ -736,6 +787,7 @@ struct BwdCta {
   Slot<Bwd<E>, W> x[2], dh[3], gate;
   BwdShared<E> warps[W];
   int32_t starts[FEW];
+  uint64_t bar[2];  // of the copies of the tiles, by the tile's parity
 };
 
 // A warp of the backward, which goes from the last tile to the first.
@@ -745,6 +797,7 @@ struct BackwardWarp {
   static constexpr int M = G::N / 2, S = G::S, CX = G::CX;
   const E *x, *gate, *dh;
   E *dx, *dgate;
+  const Maps &maps;
   const RecurParams &p;
   BwdCta<E, W> &cta;
   BwdShared<E> &sh;
@@ -761,11 +814,30 @@ struct BackwardWarp {
     return live_rows<S>(first_row(i) + q * S, lo, hi);
   }
   __device__ __forceinline__ void fetch_tile(int i) {
-    if (i >= count) return;
+    if (i >= count || threadIdx.x != 0) return;
     const int r0 = first_row(i);
-    fetch(cta.x[i & 1], x, p.ld, r0, lo, hi, d0, p.D);
-    fetch(cta.gate, gate, p.ld, r0, lo, hi, d0, p.D);
-    fetch(cta.dh[i % 3], dh, (long long)p.D, r0, lo, hi, d0, p.D);
+    const bool any = r0 / S < p.T / S;
+    const uint32_t bar = smem_u32(&cta.bar[i & 1]);
+    mbar_expect_tx(bar, any ? 3 * Slot<G, W>::BYTES : 0);
+    if (!any) return;
+    fetch(cta.x[i & 1], maps.x, r0, d0, bar);
+    fetch(cta.gate, maps.gate, r0, d0, bar);
+    fetch(cta.dh[i % 3], maps.dh, r0, d0, bar);
+  }
+  __device__ __forceinline__ void wait_tile(int i) {
+    const uint32_t bar = smem_u32(&cta.bar[i & 1]), parity = (uint32_t)i >> 1 & 1;
+    if (!arrived<false>(bar, parity, WAIT_LIMIT_NS)) {
+      set_status(p.status, TWELL_ERR_TIMEOUT);
+      arrived<false>(bar, parity, DRAIN_LIMIT_NS);  // (what is on its way has to come in)
+    }
+    const int r0 = first_row(i);
+    if (p.T % S == 0 || r0 >= p.T || r0 + G::R < p.T) return;
+    const int own = d - cx * G::N;
+    fetch_rest(cta.x[i & 1], x, p.ld, r0, p.T, own, p.D);
+    fetch_rest(cta.gate, gate, p.ld, r0, p.T, own, p.D);
+    fetch_rest(cta.dh[i % 3], dh, (long long)p.D, r0, p.T, own, p.D);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
   }
   __device__ __forceinline__ int slot(int k) const { return Slot<G, W>::at(q, k, chunk); }
   // (where a tile's first row begins a sequence it is not used)
@@ -899,11 +971,11 @@ struct BackwardWarp {
 
 template <typename E, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, SM_WARPS / WARPS)
-recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, RecurParams p) {
+recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, const __grid_constant__ Maps maps, RecurParams p) {
   pdl_begin();
   using G = Bwd<E>;
   constexpr int N = G::N, CX = G::CX;
-  extern __shared__ __align__(128) char shared[];
+  extern __shared__ __align__(1024) char shared[];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -913,11 +985,15 @@ recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, R
   open_exchange(sh.exchange, C);
   const int base = (int)(blockIdx.x / C) * WARPS * G::SLAB, d0 = base + warp * G::SLAB;
   const Rounds rounds(C, rank, G::R, p.T);
-  const int q = lane / CX, cx = lane % CX, d = d0 + cx * N, count = rounds.n;
+  const int q = Slot<G, WARPS>::group(lane / CX), cx = lane % CX, d = d0 + cx * N, count = rounds.n;
   const int sc = lane % G::ACROSS, sd = d0 + sc % CX * N + sc / CX;
   const int lo = p.starts ? max(0, p.starts[0]) : 0;
   const int hi = p.starts ? min(p.T, max(0, p.starts[p.B])) : p.T;
-  BackwardWarp<E, WARPS> w{x, gate, dh, dx, dgate, p, cta, sh, rounds, C, rank, lane, q, cx, warp * CX + cx, base, d, sd, count, lo, hi, d < p.D, false};
+  BackwardWarp<E, WARPS> w{x, gate, dh, dx, dgate, maps, p, cta, sh, rounds, C, rank, lane, q, cx, warp * CX + cx, base, d, sd, count, lo, hi, d < p.D, false};
+  if (threadIdx.x < 2) mbar_init(smem_u32(&cta.bar[threadIdx.x]), 1);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  cta_barrier<WARPS>();
   w.fetch_tile(0);
   w.before = w.state_before(0);
   empty_sequences(p, p.dhT, p.dh0, d0, min(p.D, d0 + G::SLAB), rank, C);
@@ -941,8 +1017,7 @@ recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, R
         next.plain = (next.bits.first | next.bits.last) == 0 && next.bits.live == G::ALL;
       }
       next.plain = __all_sync(0xFFFFFFFFu, next.plain);
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      cta_barrier<WARPS>();  // (the whole tile is there)
+      w.wait_tile(j);
       if (next.plain) w.template first_half<true>(j, next, en, cn);
       else w.template first_half<false>(j, next, en, cn);
     }
@@ -1012,6 +1087,24 @@ RecurParams params_of(const RecurArgs &a) {
   return p;
 }
 
+// The matrix of pitch ld at v as tensor of (channel, group, row of the group), in tiles
+// of Slot<G, W>.
+template <typename G, int W>
+bool map_of(CUtensorMap &map, const void *v, long long ld, int T, int D) {
+  using Sl = Slot<G, W>;
+  const EncodeFn encode = encode_fn();
+  if (!encode) return false;
+  constexpr cuuint64_t SIZE = 16 / G::N;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)(T < G::S ? 1 : T / G::S), (cuuint64_t)G::S};
+  const cuuint64_t pitch[2] = {(cuuint64_t)ld * G::S * SIZE, (cuuint64_t)ld * SIZE};
+  const cuuint32_t box[3] = {(cuuint32_t)(Sl::BOX * G::N), (cuuint32_t)G::GROUPS, (cuuint32_t)G::S};
+  const cuuint32_t step[3] = {1, 1, 1};
+  return encode(&map, SIZE == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
+                const_cast<void *>(v), dims, pitch, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                Sl::BOX == 8 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Clusters of C CTAs of a kernel that are resident at once (0: cannot be told).
 template <typename K>
 int resident_clusters(K kern, int threads, size_t smem, int C) {
@@ -1066,8 +1159,13 @@ cudaError_t forward_w(const RecurArgs &a, cudaStream_t s) {
   if (shape.attr != cudaSuccess) return shape.attr;
   const int wide = WARPS * G::SLAB, ctas = (a.D + wide - 1) / wide;
   const int C = shape.cluster(ctas, (a.T + G::R - 1) / G::R);
+  Maps maps;
+  if (!map_of<G, WARPS>(maps.x, a.x, a.ld, a.T, a.D) ||
+      !map_of<G, WARPS>(maps.gate, a.gate, a.ld, a.T, a.D))
+    return cudaErrorNotSupported;
+  maps.dh = maps.x;
   return launch_clusters(kern, dim3((unsigned)(ctas * C)), dim3(32 * WARPS), SMEM, C, s,
-                         (const E *)a.x, (const E *)a.gate, (E *)a.h, params_of(a));
+                         (const E *)a.x, (const E *)a.gate, (E *)a.h, maps, params_of(a));
 }
 
 template <typename E>
@@ -1090,9 +1188,14 @@ cudaError_t backward_w(const RecurArgs &a, cudaStream_t s) {
   if (shape.attr != cudaSuccess) return shape.attr;
   const int wide = WARPS * G::SLAB, ctas = (a.D + wide - 1) / wide;
   const int C = shape.cluster(ctas, (a.T + G::R - 1) / G::R);
+  Maps maps;
+  if (!map_of<G, WARPS>(maps.x, a.x, a.ld, a.T, a.D) ||
+      !map_of<G, WARPS>(maps.gate, a.gate, a.ld, a.T, a.D) ||
+      !map_of<G, WARPS>(maps.dh, a.dh, a.D, a.T, a.D))
+    return cudaErrorNotSupported;
   return launch_clusters(kern, dim3((unsigned)(ctas * C)), dim3(32 * WARPS), SMEM, C, s,
                          (const E *)a.x, (const E *)a.gate, (const E *)a.dh, (E *)a.dx, (E *)a.dgate,
-                         params_of(a));
+                         maps, params_of(a));
 }
 
 template <typename E>

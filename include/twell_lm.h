@@ -164,7 +164,7 @@ twell_status twell_distill_backward(const void *z, long long ldz, const int32_t 
  *   states [twell_recur_states(T)][D] fp32 or NULL: what the backward needs.
  * The state is held in fp32, h is its rounding; h is a buffer of its own.  B = T
  * without starts is the step of a decoded token for each of T sequences.
- * 1 <= T, 1 <= B, D <= 65536, ld >= D; D*elem_size and ld*elem_size multiples
+ * 1 <= T, 1 <= B, D <= 65536, D <= ld <= 2^34; D*elem_size and ld*elem_size multiples
  * of 16. */
 twell_status twell_recur_forward(const void *x, const void *gate, long long ld, const float *bias,
                                  const int32_t *starts, int B, const float *h0, int T, int D,

@@ -44,6 +44,7 @@ def test_recurrence(lib):
         (7, None, ARG), (7, OFF, ALIGN), (8, None, ARG), (8, OFF, ALIGN), (9, OFF, ALIGN),
         (10, 0, ARG), (11, 4, ALIGN), (12, 9, DTYPE), (13, None, ARG), (13, OFF, ALIGN),
         (14, None, ARG), (14, OFF, ALIGN), (15, OFF, ALIGN), (16, OFF, ALIGN), (17, None, ARG)])
+    assert lib.twell_recur_forward(A, A, (1 << 34) + 64, A, A, 5, A, 64, 128, 1, A, A, A, A, None) == ARG
     assert [lib.twell_recur_states(t) for t in (0, -3, 1, 64, 65, (1 << 30) + 1)] == [0, 0, 1, 1, 2, 0]
 
 
