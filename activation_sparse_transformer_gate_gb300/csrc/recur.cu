@@ -11,8 +11,9 @@
 //
 // To read each value once without a wait of CTA on CTA through memory, a cluster of
 // up to 8 CTAs owns a slab of channels and goes through all rows in rounds.  A warp
-// has 16 channels and works by itself (lanes: 2 across, 16 groups of rows; fp32 4 and
-// 8): its tile of a round is 128 rows (backward 64; fp32 64), of which
+// has 16 channels, or 8, and works by itself (lanes: 2 across and 16 groups of rows,
+// or 1 and 32; fp32 has 8 channels on 2 lanes): its tile of a round is 8 rows a group,
+// in the backward 4, of which
 //   a lane composes its rows' steps, the warp its groups' (shared memory), the cluster
 //   its CTAs' (asynchronous stores to distributed shared memory, which an mbarrier
 //   counts),
@@ -28,14 +29,18 @@
 //
 // HBM would bound it (3 values an element forward, 5 backward: 60 and 101 us at 16384 x
 // 4096 bf16), but what bounds it now is latency: the gates stay in registers from one
-// pass over a tile to the other, for two tiles, which leaves room for 8 warps an SM, and
-// a round takes a warp 3700 cycles alone and 5100 beside the others (95 and 176 us).
-// Measured on the way: CTAs in step with barriers, 150 and 430 us; warps by themselves,
-// 120 and 187; tile and tile overlapped, 107 and 186; two channels an instruction, 102 and
-// 183; rows copied in whole lines by the CTA, 95 and 176.  Gates computed again in the
-// second pass (24 warps an SM, a round's inputs from L2): 120 and 258.
+// pass over a tile to the other, for two tiles, which leaves room for 8 warps an SM
+// (88 and 167 us).  Measured on the way: CTAs in step with barriers, 150 and 430 us; warps by
+// themselves, 120 and 187; tile and tile overlapped, 107 and 186; two channels an
+// instruction, 102 and 183; rows copied in whole lines by the CTA, 95 and 176; tiles copied
+// as boxes of a tensor, 88 and 167.  Gates computed again in the second pass (24 warps an
+// SM, a round's inputs from L2): 120 and 258.  Rows copied one by one in bulk: 233 and 251
+// (32 cycles of the SM each).  The loop over tiles unrolled, which would save its 64 moves:
+// 103 and 204 (it no longer fits the instruction cache).
 #include <cooperative_groups.h>
 #include <limits.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "lm_kernels.h"
@@ -137,33 +142,40 @@ __device__ __forceinline__ void then(float &C, float &H, float C2, float H2) {
   C = !CLEAN && (C == CUT || C2 == CUT) ? CUT : r;
 }
 
-// A warp's slab: 16 channels (32 or 64 bytes of a row), as CX lanes across; GROUPS of
-// lanes take S rows of a tile each.  In the scan over the groups a channel has PARTS
+// A warp's slab: 16 channels, or 8 (16 or 32 bytes of a row), as CX lanes across; GROUPS
+// of lanes take S rows of a tile each.  In the scan over the groups a channel has PARTS
 // lanes with N consecutive groups each.
-template <typename E, int S_>
+template <typename E, int SLAB_, int S_>
 struct Geo {
-  static constexpr int N = VEC16<E>, SLAB = 16, CX = SLAB / N, GROUPS = 32 / CX, S = S_, R = GROUPS * S;
+  static constexpr int N = VEC16<E>, SLAB = SLAB_, CX = SLAB / N, GROUPS = 32 / CX, S = S_, R = GROUPS * S;
   static constexpr int PARTS = 32 / SLAB, ACROSS = SLAB;
   static constexpr uint32_t ALL = (1u << S) - 1;
   static_assert(R % RECUR_KEEP == 0 && RECUR_KEEP % S == 0, "states stand at a group's first row");
   static_assert(PARTS * N == GROUPS && 32 % S == 0, "lanes hold a channel's groups");
+  static_assert(CX == 1 || CX == 2, "see at and the slots");
   // Where the step of group q's channel n * CX + cx stands: rows of SLAB pairs, whose
   // columns are exchanged so that lanes that differ in q and cx do not meet in a bank
   // (nor do those of the scan, which differ in channel and part).
   __device__ static __forceinline__ int at(int q, int ch) {
-    return q * SLAB + (ch ^ ((CX == 2 ? q : q << 1 | q >> 2) % (SLAB / CX) * CX));
+    const int row = SLAB == 8 ? q ^ (q / N & 1) : q, swap = SLAB == 8 ? row >> 1 : row;
+    return row * SLAB + (ch ^ swap % (SLAB / CX) * CX);
   }
 };
-template <typename E> using Fwd = Geo<E, 8>;
-template <typename E> using Bwd = Geo<E, sizeof(E) == 2 ? 4 : 8>;
+template <typename E, int SLAB> using Fwd = Geo<E, SLAB, 8>;
+template <typename E, int SLAB> using Bwd = Geo<E, SLAB, 4>;
+constexpr int WARPS = 4;  // a CTA's
 
 // Where sequences begin and end in a warp's tile, by rows.  (Without starts it
 // follows from the row.)
-template <int R>
+template <typename G>
 struct Marks {
+  static constexpr int R = G::R;
+  // (the longest tiles leave no room for more)
+  using Index = typename std::conditional<R == 256, uint16_t, int32_t>::type;
   uint32_t firsts[R / 32], lasts[R / 32];  // bits of the rows
-  int first[R], last[R];                   // the sequence that begins / ends with a marked row
+  Index first[R], last[R];                 // the sequence that begins / ends with a marked row
 };
+constexpr int MAX_SHORT_B = 65536;
 
 // The first entry of starts[0 .. B] that is >= row (B + 1: none), by one warp.
 __device__ __forceinline__ int first_entry(const int32_t *starts, int B, int row) {
@@ -189,8 +201,9 @@ struct Gap {
 
 // Marks a tile's rows; returns whether there are any.  Most tiles lie within a gap
 // that is known already, and cost no look at starts.
-template <int R>
-__device__ __forceinline__ bool mark(const int32_t *starts, int B, Marks<R> &m, Gap &gap, int r0) {
+template <typename G>
+__device__ __forceinline__ bool mark(const int32_t *starts, int B, Marks<G> &m, Gap &gap, int r0) {
+  constexpr int R = G::R;
   if (gap.lo < r0 && gap.hi > r0 + R) return false;
   const int lane = threadIdx.x & 31;
   const int from = first_entry(starts, B, r0);
@@ -203,11 +216,11 @@ __device__ __forceinline__ bool mark(const int32_t *starts, int B, Marks<R> &m, 
     const int v = starts[s], k = v - r0;
     if (v > r0 + R || v < r0) break;  // (below: entries that descend)
     if (s < B && k < R && starts[s + 1] > v) {
-      m.first[k] = s;
+      m.first[k] = (typename Marks<G>::Index)s;
       atomicOr(&m.firsts[k / 32], 1u << (k & 31));
     }
     if (s > 0 && k > 0 && starts[s - 1] < v) {
-      m.last[k - 1] = s - 1;
+      m.last[k - 1] = (typename Marks<G>::Index)(s - 1);
       atomicOr(&m.lasts[(k - 1) / 32], 1u << ((k - 1) & 31));
     }
   }
@@ -227,9 +240,10 @@ __device__ __forceinline__ uint32_t live_rows(int row, int lo, int hi) {
   const int below = min(max(lo - row, 0), S), upto = min(max(hi - row, 0), S);
   return (ALL << below) & ALL & ((1u << upto) - 1);
 }
-template <int S, int R>
-__device__ __forceinline__ RowBits row_bits(const RecurParams &p, const int32_t *starts, Marks<R> &m,
+template <typename G>
+__device__ __forceinline__ RowBits row_bits(const RecurParams &p, const int32_t *starts, Marks<G> &m,
                                             Gap &gap, int r0, int q, uint32_t live) {
+  constexpr int S = G::S;
   constexpr uint32_t ALL = (1u << S) - 1;
   RowBits b{0, 0, live};
   if (p.starts) {
@@ -264,12 +278,12 @@ __device__ __forceinline__ bool plain_tile(const RecurParams &p, const Gap &gap,
   if (!p.starts || r0 < lo || r0 + R > hi) return false;
   return gap.lo < r0 && gap.hi > r0 + R;
 }
-template <int R>
-__device__ __forceinline__ int first_of(const RecurParams &p, const Marks<R> &m, int r0, int k) {
+template <typename G>
+__device__ __forceinline__ int first_of(const RecurParams &p, const Marks<G> &m, int r0, int k) {
   return p.starts ? m.first[k] : (r0 + k) / p.len;
 }
-template <int R>
-__device__ __forceinline__ int last_of(const RecurParams &p, const Marks<R> &m, int r0, int k) {
+template <typename G>
+__device__ __forceinline__ int last_of(const RecurParams &p, const Marks<G> &m, int r0, int k) {
   return p.starts ? m.last[k] : (r0 + k) / p.len;
 }
 
@@ -315,29 +329,25 @@ __device__ __forceinline__ void cluster_wait() {
 }
 
 // All warps of the CTA, wherever each of them stands.
-template <int W>
 __device__ __forceinline__ void cta_barrier() {
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * WARPS) : "memory");
 }
 
-// A CTA's tile of one matrix in shared memory, the channels of W warps, as the copies of
-// a tensor leave it: boxes of up to 128 bytes of a row, whose 16-byte chunks are exchanged
+// A CTA's tile of one matrix in shared memory, the channels of its warps, as the copy of
+// a tensor's box leaves it: 64 or 128 bytes of a row, whose 16-byte chunks are exchanged
 // by the address; the k-th rows of all groups stand together.
-template <typename G, int W>
+template <typename G>
 struct alignas(1024) Slot {
-  static constexpr int CH = W * G::CX, BOX = CH < 8 ? CH : 8;  // chunks of a row, of a box's
-  static constexpr int BOXES = CH / BOX, LONG = G::R * BOX;
-  static constexpr uint32_t BYTES = BOXES * LONG * 16;
-  uint4 v[BOXES * LONG];
-  static_assert(G::GROUPS % 8 == 0 && (BOX == 8 || (BOX == 4 && G::CX == 2)), "see at, group");
+  static constexpr int CH = WARPS * G::CX;  // chunks of a row
+  uint4 v[G::R * CH];
+  static_assert(G::GROUPS % 8 == 0, "a chunk's place follows from q, not from k");
   __device__ static __forceinline__ int at(int q, int k, int chunk) {
-    return chunk / BOX * LONG + (k * G::GROUPS + q) * BOX + (chunk % BOX ^ (BOX == 8 ? q & 7 : q >> 1 & 3));
+    return (k * G::GROUPS + q) * CH + (chunk ^ (CH == 8 ? q & 7 : q >> 1 & 3));
   }
   // A lane's group: eight lanes in a row read one row of 8 / CX groups at once, which are
   // those that do not meet in a bank.
   __device__ static __forceinline__ int group(int g) {
-    if (BOX == 4) return (g & 9) | (g << 1 & 4) | (g >> 1 & 2);
-    return (g & 8) | ((G::CX == 2 ? g << 1 | (g >> 2 & 1) : g << 2 | g >> 1) & 7);
+    return G::CX == 1 ? g : (g & 8) | (g << 1 & 6) | (g >> 2 & 1);
   }
 };
 
@@ -347,41 +357,32 @@ struct Maps {
   CUtensorMap x, gate, dh;
 };
 
-__device__ __forceinline__ void load_box(void *dst, const CUtensorMap &map, int d, int group,
-                                         uint32_t bar, uint64_t policy) {
+// Copies a tile from row r0 on, by one thread.
+template <typename G>
+__device__ __forceinline__ void fetch(Slot<G> &slot, const CUtensorMap &map, int r0, int d0,
+                                      uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
-      "l"((uint64_t)&map), "r"(d), "r"(group), "r"(0), "r"(bar), "l"(policy)
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(slot.v)),
+      "l"((uint64_t)&map), "r"(d0), "r"(r0 / G::S), "r"(0), "r"(bar), "l"(gather_policy<L2_FIRST>())
       : "memory");
 }
 
 // starts, in shared memory where there are few (from the CTA's next barrier on).
-template <int W>
 __device__ __forceinline__ const int32_t *keep_starts(const RecurParams &p, int32_t *few) {
   if (!p.starts || p.B >= FEW) return p.starts;
-  for (int k = threadIdx.x; k <= p.B; k += 32 * W) few[k] = p.starts[k];
+  for (int k = threadIdx.x; k <= p.B; k += 32 * WARPS) few[k] = p.starts[k];
   return few;
 }
 
-// Copies a tile from row r0 on, by one thread.
-template <typename G, int W>
-__device__ __forceinline__ void fetch(Slot<G, W> &slot, const CUtensorMap &map, int r0, int d0,
-                                      uint32_t bar) {
-  using Sl = Slot<G, W>;
-  const uint64_t once = gather_policy<L2_FIRST>();
-#pragma unroll
-  for (int b = 0; b < Sl::BOXES; ++b)
-    load_box(slot.v + b * Sl::LONG, map, d0 + b * Sl::BOX * G::N, r0 / G::S, bar, once);
-}
-// The rows of its last group where T cuts it, a warp's channels of them.
-template <typename G, int W, typename E>
-__device__ __forceinline__ void fetch_rest(Slot<G, W> &slot, const E *src, long long pitch, int r0,
+// The rows of a tile's last group where T cuts it, a warp's channels of them.
+template <typename G, typename E>
+__device__ __forceinline__ void fetch_rest(Slot<G> &slot, const E *src, long long pitch, int r0,
                                            int T, int d0, int D) {
   const int lane = threadIdx.x & 31, k = lane / G::CX, cx = lane % G::CX, rest = T % G::S;
   const int d = d0 + cx * G::N, whole = T - rest;
   if (k < rest && d < D)
-    slot.v[Slot<G, W>::at((whole - r0) / G::S, k, (threadIdx.x >> 5) * G::CX + cx)] =
+    slot.v[Slot<G>::at((whole - r0) / G::S, k, (threadIdx.x >> 5) * G::CX + cx)] =
         *(const uint4 *)(src + (size_t)(whole + k) * pitch + d);
 }
 
@@ -449,8 +450,9 @@ __device__ __forceinline__ void scan_down(float2 *steps, const Scan &s, float h)
 // that they travel while it works.  It sends those of round i + 4 after all have
 // sent round i + 2's, and so have read round i's: four rounds' worth of room.
 constexpr int ROOM = 4;
+template <typename G>
 struct Exchange {
-  float2 total[ROOM][MAX_CLUSTER][16];  // (0, 0) for CTAs that the cluster does not have
+  float2 total[ROOM][MAX_CLUSTER][G::SLAB];  // (0, 0) for CTAs that the cluster does not have
   uint64_t bar[ROOM];
 };
 
@@ -481,7 +483,7 @@ __device__ __forceinline__ bool arrived(uint32_t bar, uint32_t parity, uint64_t 
 }
 
 template <typename G>
-__device__ __forceinline__ void send_step(Exchange &x, int n, int rank, int i, const Scan &s, bool lost) {
+__device__ __forceinline__ void send_step(Exchange<G> &x, int n, int rank, int i, const Scan &s, bool lost) {
   if (n == 1 || lost) return;
   const int lane = threadIdx.x & 31, ch = lane % G::ACROSS, part = lane / G::ACROSS;
   const uint32_t bar = smem_u32(&x.bar[i % ROOM]), mine = smem_u32(&x.total[i % ROOM][rank][ch]);
@@ -498,7 +500,7 @@ __device__ __forceinline__ void send_step(Exchange &x, int n, int rank, int i, c
 // order of the rows (BACK: against it); `carry` is what reaches the cluster's first
 // one, and then the first one of its next round.
 template <typename G, bool BACK>
-__device__ __forceinline__ float receive_steps(Exchange &x, int n, int rank, int i, const Scan &s,
+__device__ __forceinline__ float receive_steps(Exchange<G> &x, int n, int rank, int i, const Scan &s,
                                                float &carry, bool &lost, int32_t *status) {
   if (n == 1) {
     const float in = carry;
@@ -528,9 +530,10 @@ __device__ __forceinline__ float receive_steps(Exchange &x, int n, int rank, int
 }
 
 // Before the first exchange, by the whole cluster.
-__device__ __forceinline__ void open_exchange(Exchange &x, int C) {
+template <typename G>
+__device__ __forceinline__ void open_exchange(Exchange<G> &x, int C) {
   const int lane = threadIdx.x & 31;
-  for (int k = lane; k < ROOM * MAX_CLUSTER * 16; k += 32) (&x.total[0][0][0])[k] = make_float2(0.f, 0.f);
+  for (int k = lane; k < ROOM * MAX_CLUSTER * G::SLAB; k += 32) (&x.total[0][0][0])[k] = make_float2(0.f, 0.f);
   if (lane < ROOM) mbar_init(smem_u32(&x.bar[lane]), 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __syncwarp();
@@ -543,7 +546,7 @@ struct Rounds {
   __device__ __forceinline__ Rounds(int C_, int rank_, int R_, int T)
       : C(C_), rank(rank_), R(R_), n(((T + R_ - 1) / R_ + C_ - 1) / C_) {}
   // first row of this CTA's tile in the i-th of them (T where it has none)
-  // (T <= 2^30 and C R <= 1024: below T + C R, which fits)
+  // (T <= 2^30 and C R <= 2048: below T + C R, which fits)
   __device__ __forceinline__ int row(int i, int T) const { return min(T, (i * C + rank) * R); }
 };
 
@@ -557,37 +560,36 @@ struct Tile {
 };
 
 // What a warp of the forward has in shared memory.
-template <typename E>
+template <typename G>
 struct FwdShared {
-  using G = Fwd<E>;
   float2 steps[2][G::GROUPS * G::SLAB];  // the groups' steps, then what reaches them
-  Exchange exchange;
+  Exchange<G> exchange;
   // h0 of the last sequence that begins in each lane's rows: hT may be h0, and who
   // comes to that sequence's end first is open (the others end with the same lane)
   float4 held[2][G::N / 4][32];
-  Marks<G::R> marks[2];
+  Marks<G> marks[2];
 };
 
 // And a CTA: x of the tiles in both halves and the next one, gates of one.
-template <typename E, int W>
+template <typename G>
 struct FwdCta {
-  Slot<Fwd<E>, W> x[3], gate;
-  FwdShared<E> warps[W];
+  Slot<G> x[3], gate;
+  FwdShared<G> warps[WARPS];
   int32_t starts[FEW];
   uint64_t bar[2];  // of the copies of the tiles, by the tile's parity
 };
 
 // A warp of the forward.
-template <typename E, int W>
+template <typename E, int SLAB>
 struct ForwardWarp {
-  using G = Fwd<E>;
+  using G = Fwd<E, SLAB>;
   static constexpr int M = G::N / 2, S = G::S, CX = G::CX;  // M pairs of channels a lane
   const E *x, *gate;
   E *h;
   const Maps &maps;
   const RecurParams &p;
-  FwdCta<E, W> &cta;
-  FwdShared<E> &sh;
+  FwdCta<G> &cta;
+  FwdShared<G> &sh;
   Rounds rounds;
   int C, rank, lane, q, cx, chunk, d0, d, count, lo, hi;  // d0: the CTA's first channel
   bool on, lost;
@@ -603,7 +605,7 @@ struct ForwardWarp {
     const int r0 = rounds.row(i, p.T);
     const bool any = r0 / S < p.T / S;
     const uint32_t bar = smem_u32(&cta.bar[i & 1]);
-    mbar_expect_tx(bar, any ? 2 * Slot<G, W>::BYTES : 0);
+    mbar_expect_tx(bar, any ? 2 * (uint32_t)sizeof(Slot<G>) : 0);
     if (!any) return;
     fetch(cta.x[i % 3], maps.x, r0, d0, bar);
     fetch(cta.gate, maps.gate, r0, d0, bar);
@@ -622,7 +624,7 @@ struct ForwardWarp {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
   }
-  __device__ __forceinline__ int slot(int k) const { return Slot<G, W>::at(q, k, chunk); }
+  __device__ __forceinline__ int slot(int k) const { return Slot<G>::at(q, k, chunk); }
   // The first half of tile i: its rows as one step a lane, scanned and sent.
   template <bool PLAIN>
   __device__ __forceinline__ void first_half(int i, Tile &t, float2 (&mc)[S][M]) {
@@ -651,7 +653,7 @@ struct ForwardWarp {
         for (int n = 0; n < M; ++n) Hs[n] = both(0.f);
       }
     }
-    cta_barrier<W>();  // (all warps are done with the gates, and with tile i - 2)
+    cta_barrier();  // (all warps are done with the gates, and with tile i - 2)
     fetch_tile(i + 1);
     const bool cut = !PLAIN && (t.bits.first != 0 || t.bits.live != G::ALL);
 #pragma unroll
@@ -708,29 +710,29 @@ struct ForwardWarp {
   }
 };
 
-template <typename E, int WARPS>
+template <typename E, int SLAB>
 __global__ void __launch_bounds__(32 * WARPS, SM_WARPS / WARPS)
 recur_forward_kernel(const E *x, const E *gate, E *h, const __grid_constant__ Maps maps, RecurParams p) {
   pdl_begin();
-  using G = Fwd<E>;
+  using G = Fwd<E, SLAB>;
   extern __shared__ __align__(1024) char shared[];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  FwdCta<E, WARPS> &cta = *(FwdCta<E, WARPS> *)shared;
-  FwdShared<E> &sh = cta.warps[warp];
-  const int32_t *starts = keep_starts<WARPS>(p, cta.starts);
+  FwdCta<G> &cta = *(FwdCta<G> *)shared;
+  FwdShared<G> &sh = cta.warps[warp];
+  const int32_t *starts = keep_starts(p, cta.starts);
   open_exchange(sh.exchange, C);
   const int base = (int)(blockIdx.x / C) * WARPS * G::SLAB, d0 = base + warp * G::SLAB;
   const Rounds rounds(C, rank, G::R, p.T);
-  const int q = Slot<G, WARPS>::group(lane / G::CX), cx = lane % G::CX, d = d0 + cx * G::N, count = rounds.n;
+  const int q = Slot<G>::group(lane / G::CX), cx = lane % G::CX, d = d0 + cx * G::N, count = rounds.n;
   const int lo = p.starts ? max(0, p.starts[0]) : 0;
   const int hi = p.starts ? min(p.T, max(0, p.starts[p.B])) : p.T;
-  ForwardWarp<E, WARPS> w{x, gate, h, maps, p, cta, sh, rounds, C, rank, lane, q, cx, warp * G::CX + cx, base, d, count, lo, hi, d < p.D, false};
+  ForwardWarp<E, SLAB> w{x, gate, h, maps, p, cta, sh, rounds, C, rank, lane, q, cx, warp * G::CX + cx, base, d, count, lo, hi, d < p.D, false};
   if (threadIdx.x < 2) mbar_init(smem_u32(&cta.bar[threadIdx.x]), 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  cta_barrier<WARPS>();
+  cta_barrier();
   w.fetch_tile(0);
   empty_sequences(p, p.h0, p.hT, d0, min(p.D, d0 + G::SLAB), rank, C);
   load_state(w.on ? p.bias : nullptr, 0, 0, d, w.bias);
@@ -746,7 +748,7 @@ recur_forward_kernel(const E *x, const E *gate, E *h, const __grid_constant__ Ma
       next.r0 = rounds.row(j, p.T);
       next.plain = plain_tile<G::R>(p, w.gap, next.r0, lo, hi);
       if (!next.plain) {
-        next.bits = row_bits<G::S>(p, starts, sh.marks[j & 1], w.gap, next.r0, q, w.live_of(j));
+        next.bits = row_bits(p, starts, sh.marks[j & 1], w.gap, next.r0, q, w.live_of(j));
         next.plain = (next.bits.first | next.bits.last) == 0 && next.bits.live == G::ALL;
       }
       next.plain = __all_sync(0xFFFFFFFFu, next.plain);
@@ -772,35 +774,34 @@ recur_forward_kernel(const E *x, const E *gate, E *h, const __grid_constant__ Ma
 }
 
 // What a warp of the backward has in shared memory.
-template <typename E>
+template <typename G>
 struct BwdShared {
-  using G = Bwd<E>;
   float2 stepsF[G::GROUPS * G::SLAB];     // the groups' steps forward
   float2 stepsB[2][G::GROUPS * G::SLAB];  // and back, then what reaches them
-  Exchange exchange;
+  Exchange<G> exchange;
   float bias[MAX_CLUSTER][G::SLAB];       // the CTAs' sums of dgate
-  Marks<G::R> marks[2];
+  Marks<G> marks[2];
 };
 
-template <typename E, int W>
+template <typename G>
 struct BwdCta {
-  Slot<Bwd<E>, W> x[2], dh[3], gate;
-  BwdShared<E> warps[W];
+  Slot<G> x[2], dh[3], gate;
+  BwdShared<G> warps[WARPS];
   int32_t starts[FEW];
   uint64_t bar[2];  // of the copies of the tiles, by the tile's parity
 };
 
 // A warp of the backward, which goes from the last tile to the first.
-template <typename E, int W>
+template <typename E, int SLAB>
 struct BackwardWarp {
-  using G = Bwd<E>;
+  using G = Bwd<E, SLAB>;
   static constexpr int M = G::N / 2, S = G::S, CX = G::CX;
   const E *x, *gate, *dh;
   E *dx, *dgate;
   const Maps &maps;
   const RecurParams &p;
-  BwdCta<E, W> &cta;
-  BwdShared<E> &sh;
+  BwdCta<G> &cta;
+  BwdShared<G> &sh;
   Rounds rounds;
   int C, rank, lane, q, cx, chunk, d0, d, sd, count, lo, hi;  // d0: the CTA's first channel, sd: the scan's
   bool on, lost;
@@ -818,7 +819,7 @@ struct BackwardWarp {
     const int r0 = first_row(i);
     const bool any = r0 / S < p.T / S;
     const uint32_t bar = smem_u32(&cta.bar[i & 1]);
-    mbar_expect_tx(bar, any ? 3 * Slot<G, W>::BYTES : 0);
+    mbar_expect_tx(bar, any ? 3 * (uint32_t)sizeof(Slot<G>) : 0);
     if (!any) return;
     fetch(cta.x[i & 1], maps.x, r0, d0, bar);
     fetch(cta.gate, maps.gate, r0, d0, bar);
@@ -839,7 +840,7 @@ struct BackwardWarp {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
   }
-  __device__ __forceinline__ int slot(int k) const { return Slot<G, W>::at(q, k, chunk); }
+  __device__ __forceinline__ int slot(int k) const { return Slot<G>::at(q, k, chunk); }
   // (where a tile's first row begins a sequence it is not used)
   __device__ __forceinline__ float state_before(int i) const {
     const int r0 = i < count ? first_row(i) : p.T;
@@ -871,7 +872,7 @@ struct BackwardWarp {
         for (int n = 0; n < M; ++n) Hs[n] = both(0.f);
       }
     }
-    cta_barrier<W>();  // (all warps are done with the gates, and with what stood in the other slots)
+    cta_barrier();  // (all warps are done with the gates, and with what stood in the other slots)
     fetch_tile(i + 1);
     const bool dead = !PLAIN && t.bits.live != G::ALL;
     const bool cutF = !PLAIN && (dead || t.bits.first), cutB = !PLAIN && (dead || t.bits.last);
@@ -969,31 +970,31 @@ struct BackwardWarp {
   }
 };
 
-template <typename E, int WARPS>
+template <typename E, int SLAB>
 __global__ void __launch_bounds__(32 * WARPS, SM_WARPS / WARPS)
 recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, const __grid_constant__ Maps maps, RecurParams p) {
   pdl_begin();
-  using G = Bwd<E>;
+  using G = Bwd<E, SLAB>;
   constexpr int N = G::N, CX = G::CX;
   extern __shared__ __align__(1024) char shared[];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  BwdCta<E, WARPS> &cta = *(BwdCta<E, WARPS> *)shared;
-  BwdShared<E> &sh = cta.warps[warp];
-  const int32_t *starts = keep_starts<WARPS>(p, cta.starts);
+  BwdCta<G> &cta = *(BwdCta<G> *)shared;
+  BwdShared<G> &sh = cta.warps[warp];
+  const int32_t *starts = keep_starts(p, cta.starts);
   open_exchange(sh.exchange, C);
   const int base = (int)(blockIdx.x / C) * WARPS * G::SLAB, d0 = base + warp * G::SLAB;
   const Rounds rounds(C, rank, G::R, p.T);
-  const int q = Slot<G, WARPS>::group(lane / CX), cx = lane % CX, d = d0 + cx * N, count = rounds.n;
+  const int q = Slot<G>::group(lane / CX), cx = lane % CX, d = d0 + cx * N, count = rounds.n;
   const int sc = lane % G::ACROSS, sd = d0 + sc % CX * N + sc / CX;
   const int lo = p.starts ? max(0, p.starts[0]) : 0;
   const int hi = p.starts ? min(p.T, max(0, p.starts[p.B])) : p.T;
-  BackwardWarp<E, WARPS> w{x, gate, dh, dx, dgate, maps, p, cta, sh, rounds, C, rank, lane, q, cx, warp * CX + cx, base, d, sd, count, lo, hi, d < p.D, false};
+  BackwardWarp<E, SLAB> w{x, gate, dh, dx, dgate, maps, p, cta, sh, rounds, C, rank, lane, q, cx, warp * CX + cx, base, d, sd, count, lo, hi, d < p.D, false};
   if (threadIdx.x < 2) mbar_init(smem_u32(&cta.bar[threadIdx.x]), 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  cta_barrier<WARPS>();
+  cta_barrier();
   w.fetch_tile(0);
   w.before = w.state_before(0);
   empty_sequences(p, p.dhT, p.dh0, d0, min(p.D, d0 + G::SLAB), rank, C);
@@ -1013,7 +1014,7 @@ recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, c
       next.r0 = w.first_row(j);
       next.plain = plain_tile<G::R>(p, w.gap, next.r0, lo, hi);
       if (!next.plain) {
-        next.bits = row_bits<G::S>(p, starts, sh.marks[j & 1], w.gap, next.r0, q, w.live_of(j));
+        next.bits = row_bits(p, starts, sh.marks[j & 1], w.gap, next.r0, q, w.live_of(j));
         next.plain = (next.bits.first | next.bits.last) == 0 && next.bits.live == G::ALL;
       }
       next.plain = __all_sync(0xFFFFFFFFu, next.plain);
@@ -1088,20 +1089,20 @@ RecurParams params_of(const RecurArgs &a) {
 }
 
 // The matrix of pitch ld at v as tensor of (channel, group, row of the group), in tiles
-// of Slot<G, W>.
-template <typename G, int W>
+// of Slot<G>.
+template <typename G>
 bool map_of(CUtensorMap &map, const void *v, long long ld, int T, int D) {
-  using Sl = Slot<G, W>;
+  constexpr int CH = Slot<G>::CH;
   const EncodeFn encode = encode_fn();
   if (!encode) return false;
   constexpr cuuint64_t SIZE = 16 / G::N;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)(T < G::S ? 1 : T / G::S), (cuuint64_t)G::S};
   const cuuint64_t pitch[2] = {(cuuint64_t)ld * G::S * SIZE, (cuuint64_t)ld * SIZE};
-  const cuuint32_t box[3] = {(cuuint32_t)(Sl::BOX * G::N), (cuuint32_t)G::GROUPS, (cuuint32_t)G::S};
+  const cuuint32_t box[3] = {(cuuint32_t)CH * G::N, (cuuint32_t)G::GROUPS, (cuuint32_t)G::S};
   const cuuint32_t step[3] = {1, 1, 1};
   return encode(&map, SIZE == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
                 const_cast<void *>(v), dims, pitch, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                Sl::BOX == 8 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                CH == 8 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1145,23 +1146,28 @@ struct Shape {
   }
 };
 
-// Four warps a CTA, or two where they leave SMs without one (us, forward and backward,
-// two | four: 2048 x 1024 fp32 13 + 19 | 14 + 23, 131072 x 1024 forward 260 | 331, 4096 x
-// 2048 31 + 35 | 22 + 33, 16384 x 4096 118 + 179 | 94 + 177).
-bool narrow(int D) { return (long long)((D + 63) / 64) * MAX_CLUSTER < num_sms(); }
+// 16 channels a warp in bf16, unless three fifths of the CTAs that are resident at once
+// do not come together that way; 8 double them (us, 8 | 16: 16384 x 128 forward + backward
+// 33 + 61 | 53 + 101, 131072 x 1024 forward 200 | 309, 16384 x 1280 45 + 82 | 49 + 94,
+// 16384 x 1536 50 + 94 | 47 + 91, 16384 x 4096 106 + 198 | 89 + 167: 16 bytes of a row are
+// half a sector).  fp32 always 8 (8192 x 4096 79 + 138 | 77 + 148, 2048 x 1024 10 + 14 |
+// 14 + 22).
+bool wide(int D) {
+  return 5ll * ((D + 63) / 64) * MAX_CLUSTER >= 3ll * num_sms() * SM_WARPS / WARPS;
+}
 
-template <typename E, int WARPS>
+template <typename E, int SLAB>
 cudaError_t forward_w(const RecurArgs &a, cudaStream_t s) {
-  using G = Fwd<E>;
-  constexpr int SMEM = sizeof(FwdCta<E, WARPS>);
-  auto kern = recur_forward_kernel<E, WARPS>;
+  using G = Fwd<E, SLAB>;
+  constexpr int SMEM = sizeof(FwdCta<G>);
+  auto kern = recur_forward_kernel<E, SLAB>;
   static const Shape<decltype(kern)> shape(kern, 32 * WARPS, SMEM);
   if (shape.attr != cudaSuccess) return shape.attr;
-  const int wide = WARPS * G::SLAB, ctas = (a.D + wide - 1) / wide;
+  const int width = WARPS * G::SLAB, ctas = (a.D + width - 1) / width;
   const int C = shape.cluster(ctas, (a.T + G::R - 1) / G::R);
   Maps maps;
-  if (!map_of<G, WARPS>(maps.x, a.x, a.ld, a.T, a.D) ||
-      !map_of<G, WARPS>(maps.gate, a.gate, a.ld, a.T, a.D))
+  if (!map_of<G>(maps.x, a.x, a.ld, a.T, a.D) ||
+      !map_of<G>(maps.gate, a.gate, a.ld, a.T, a.D))
     return cudaErrorNotSupported;
   maps.dh = maps.x;
   return launch_clusters(kern, dim3((unsigned)(ctas * C)), dim3(32 * WARPS), SMEM, C, s,
@@ -1176,22 +1182,24 @@ cudaError_t forward_t(const RecurArgs &a, cudaStream_t s) {
                     dim3(STEP_THREADS), 0, s, (const E *)a.x, (const E *)a.gate, (E *)a.h,
                     params_of(a));
   }
-  return narrow(a.D) ? forward_w<E, 2>(a, s) : forward_w<E, 4>(a, s);
+  if constexpr (sizeof(E) == 2)
+    if (wide(a.D) || (a.starts && a.B > MAX_SHORT_B)) return forward_w<E, 16>(a, s);
+  return forward_w<E, 8>(a, s);
 }
 
-template <typename E, int WARPS>
+template <typename E, int SLAB>
 cudaError_t backward_w(const RecurArgs &a, cudaStream_t s) {
-  using G = Bwd<E>;
-  constexpr int SMEM = sizeof(BwdCta<E, WARPS>);
-  auto kern = recur_backward_kernel<E, WARPS>;
+  using G = Bwd<E, SLAB>;
+  constexpr int SMEM = sizeof(BwdCta<G>);
+  auto kern = recur_backward_kernel<E, SLAB>;
   static const Shape<decltype(kern)> shape(kern, 32 * WARPS, SMEM);
   if (shape.attr != cudaSuccess) return shape.attr;
-  const int wide = WARPS * G::SLAB, ctas = (a.D + wide - 1) / wide;
+  const int width = WARPS * G::SLAB, ctas = (a.D + width - 1) / width;
   const int C = shape.cluster(ctas, (a.T + G::R - 1) / G::R);
   Maps maps;
-  if (!map_of<G, WARPS>(maps.x, a.x, a.ld, a.T, a.D) ||
-      !map_of<G, WARPS>(maps.gate, a.gate, a.ld, a.T, a.D) ||
-      !map_of<G, WARPS>(maps.dh, a.dh, a.D, a.T, a.D))
+  if (!map_of<G>(maps.x, a.x, a.ld, a.T, a.D) ||
+      !map_of<G>(maps.gate, a.gate, a.ld, a.T, a.D) ||
+      !map_of<G>(maps.dh, a.dh, a.D, a.T, a.D))
     return cudaErrorNotSupported;
   return launch_clusters(kern, dim3((unsigned)(ctas * C)), dim3(32 * WARPS), SMEM, C, s,
                          (const E *)a.x, (const E *)a.gate, (const E *)a.dh, (E *)a.dx, (E *)a.dgate,
@@ -1200,7 +1208,9 @@ cudaError_t backward_w(const RecurArgs &a, cudaStream_t s) {
 
 template <typename E>
 cudaError_t backward_t(const RecurArgs &a, cudaStream_t s) {
-  return narrow(a.D) ? backward_w<E, 2>(a, s) : backward_w<E, 4>(a, s);
+  if constexpr (sizeof(E) == 2)
+    if (wide(a.D)) return backward_w<E, 16>(a, s);
+  return backward_w<E, 8>(a, s);
 }
 
 }  // namespace

@@ -142,6 +142,25 @@ def test_packed(T, D, starts, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,D,starts", [(5, 1544, [0, 5]), (7, 2000, [0, 3, 7]), (133, 2000, [2, 61, 131]),
+                                        (519, 1672, ragged(519, 9, 3)), (1285, 1536, [0, 700, 1285]),
+                                        (4099, 264, ragged(4099, 30, 4)), (2309, 1280, [0, 2309])])
+def test_packed_over_many_rounds(T, D, starts, dtype):
+    """Lengths that cut a group of rows in two, widths that cut a warp's channels, several
+    tiles a CTA."""
+    c = Case(T, D, starts, dtype)
+    c.compare(c.run())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_more_sequences_than_16_bits(dtype):
+    g = gen(11)
+    cuts = sorted(int(v) for v in torch.randint(0, 301, (66000,), generator=g))
+    c = Case(300, 16, [0] + cuts + [300], dtype)
+    c.compare(c.run())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T,D,B", [(5, 64, 5), (1, 8, 1), (64, 128, 4), (600, 40, 200), (640, 1024, 2),
                                    (37, 4096, 37), (515, 1000, 1), (513, 16, 513)])
 def test_sequences_of_one_length(T, D, B, dtype):
