@@ -10,17 +10,17 @@
 // rounding.  A sequence's first row forgets what stood before it ("cut").
 //
 // To read each value once without a wait of CTA on CTA through memory, a cluster of
-// up to 8 CTAs owns a slab of channels and goes through all rows in rounds.  A warp
+// up to 16 CTAs owns a slab of channels and goes through all rows in rounds.  A warp
 // has 16 channels, or 8, and works by itself (lanes: 2 across and 16 groups of rows,
-// or 1 and 32; fp32 has 8 channels on 2 lanes): its tile of a round is 8 rows a group,
-// in the backward 4, of which
+// or 1 and 32; fp32 has 8 channels on 2 lanes): its tile of a round is 8 rows a group
+// (a short backward: 4), of which
 //   a lane composes its rows' steps, the warp its groups' (shared memory), the cluster
 //   its CTAs' (asynchronous stores to distributed shared memory, which an mbarrier
 //   counts),
 // and with the state that comes in from the left the lanes go over their rows once
-// more, from shared memory and registers, and write them.  Tile and tile overlap: while a
-// tile's step is on its way to the other CTAs, the next one is composed.  The grouping
-// of the sums follows from the sizes alone.
+// more, from shared memory and registers, and write them.  While a tile's step is on its
+// way to the other CTAs, the SM's other CTAs work.  The grouping of the sums follows from
+// the sizes alone.
 //
 // The backward runs the same over the rows in reverse for G, and forward within a
 // tile for h, from the fp32 states that the forward kept every RECUR_KEEP rows: h
@@ -28,15 +28,18 @@
 // enter the gradient.
 //
 // HBM would bound it (3 values an element forward, 5 backward: 60 and 101 us at 16384 x
-// 4096 bf16), but what bounds it now is latency: the gates stay in registers from one
-// pass over a tile to the other, for two tiles, which leaves room for 8 warps an SM
-// (88 and 167 us).  Measured on the way: CTAs in step with barriers, 150 and 430 us; warps by
-// themselves, 120 and 187; tile and tile overlapped, 107 and 186; two channels an
-// instruction, 102 and 183; rows copied in whole lines by the CTA, 95 and 176; tiles copied
-// as boxes of a tensor, 88 and 167.  Gates computed again in the second pass (24 warps an
-// SM, a round's inputs from L2): 120 and 258.  Rows copied one by one in bulk: 233 and 251
-// (32 cycles of the SM each).  The loop over tiles unrolled, which would save its 64 moves:
-// 103 and 204 (it no longer fits the instruction cache).
+// 4096 bf16, which take 82 and 154).  What bounds it is latency, and next the issue slots:
+// the gates stay in registers from one pass over a tile to the other, which leaves room for
+// 12 warps an SM forward and 8 backward, and a round has its fixed part (two scans, the
+// exchange) of some 600 instructions.  Measured on the way: CTAs in step with barriers,
+// 150 and 430 us; warps by themselves, 120 and 187; two tiles at a time, one of them on its
+// way to the other CTAs, 107 and 186; two channels an instruction, 102 and 183; rows copied
+// in whole lines, 95 and 176; tiles copied as boxes of a tensor, 88 and 167; one tile at a
+// time again, with the registers spent on more warps and on longer tiles, 82 and 154.
+// Gates computed again in the second pass (24 warps an SM, a round's inputs from L2): 120
+// and 258.  Rows copied one by one in bulk: 233 and 251 (32 cycles of the SM each).  One
+// body for all tiles, with branches at the rows where sequences begin: 93 and 217; with
+// loops over the rows for the tiles that have such: 88 and 170.
 #include <cooperative_groups.h>
 #include <limits.h>
 
@@ -53,8 +56,6 @@ namespace twell {
 
 namespace {
 
-constexpr int SM_WARPS = 8;         // resident, by registers and shared memory
-constexpr int MAX_CLUSTER = 8;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr int FEW = 128;            // entries of starts that a CTA keeps at hand
 constexpr float CUT = 2.f;          // a C that stands for: nothing comes through
@@ -145,10 +146,11 @@ __device__ __forceinline__ void then(float &C, float &H, float C2, float H2) {
 // A warp's slab: 16 channels, or 8 (16 or 32 bytes of a row), as CX lanes across; GROUPS
 // of lanes take S rows of a tile each.  In the scan over the groups a channel has PARTS
 // lanes with N consecutive groups each.
-template <typename E, int SLAB_, int S_>
+template <typename E, int SLAB_, int S_, int CLUSTER_>
 struct Geo {
   static constexpr int N = VEC16<E>, SLAB = SLAB_, CX = SLAB / N, GROUPS = 32 / CX, S = S_, R = GROUPS * S;
   static constexpr int PARTS = 32 / SLAB, ACROSS = SLAB;
+  static constexpr int CLUSTER = CLUSTER_;  // CTAs at most
   static constexpr uint32_t ALL = (1u << S) - 1;
   static_assert(R % RECUR_KEEP == 0 && RECUR_KEEP % S == 0, "states stand at a group's first row");
   static_assert(PARTS * N == GROUPS && 32 % S == 0, "lanes hold a channel's groups");
@@ -161,8 +163,8 @@ struct Geo {
     return row * SLAB + (ch ^ swap % (SLAB / CX) * CX);
   }
 };
-template <typename E, int SLAB> using Fwd = Geo<E, SLAB, 8>;
-template <typename E, int SLAB> using Bwd = Geo<E, SLAB, 4>;
+template <typename E, int SLAB, int CLUSTER> using Fwd = Geo<E, SLAB, 8, CLUSTER>;
+template <typename E, int SLAB, int S> using Bwd = Geo<E, SLAB, S, 16>;
 constexpr int WARPS = 4;  // a CTA's
 
 // Where sequences begin and end in a warp's tile, by rows.  (Without starts it
@@ -231,6 +233,7 @@ __device__ __forceinline__ bool mark(const int32_t *starts, int B, Marks<G> &m, 
 // Bits of a thread's S rows of a tile.
 struct RowBits {
   uint32_t first, last, live;
+  uint32_t any_first, any_last;  // of the warp's lanes (a row that none has costs little)
 };
 // Those of rows row .. row + S - 1 that are in [lo, hi).
 template <int S>
@@ -245,7 +248,7 @@ __device__ __forceinline__ RowBits row_bits(const RecurParams &p, const int32_t 
                                             Gap &gap, int r0, int q, uint32_t live) {
   constexpr int S = G::S;
   constexpr uint32_t ALL = (1u << S) - 1;
-  RowBits b{0, 0, live};
+  RowBits b{0, 0, live, 0, 0};
   if (p.starts) {
     if (mark(starts, p.B, m, gap, r0)) {
       const int k = q * S;  // (S divides 32: a lane's rows are of one word)
@@ -269,6 +272,8 @@ __device__ __forceinline__ RowBits row_bits(const RecurParams &p, const int32_t 
   }
   b.first &= live;
   b.last &= live;
+  b.any_first = __reduce_or_sync(0xFFFFFFFFu, b.first);
+  b.any_last = __reduce_or_sync(0xFFFFFFFFu, b.last);
   return b;
 }
 // Whether no sequence begins or ends in the tile from r0 on and all of its rows are some
@@ -446,13 +451,12 @@ __device__ __forceinline__ void scan_down(float2 *steps, const Scan &s, float h)
 
 // The exchange of a slab's steps among the cluster's CTAs: in each round every warp
 // sends its tile's step to the warps of the CTAs that have the slab, whose barrier
-// counts the bytes.  A warp sends round i + 1's before it waits for round i's, so
-// that they travel while it works.  It sends those of round i + 4 after all have
-// sent round i + 2's, and so have read round i's: four rounds' worth of room.
-constexpr int ROOM = 4;
+// counts the bytes.  It sends those of round i + 2 after all have sent round i + 1's,
+// and so have read round i's: two rounds' worth of room.
+constexpr int ROOM = 2;
 template <typename G>
 struct Exchange {
-  float2 total[ROOM][MAX_CLUSTER][G::SLAB];  // (0, 0) for CTAs that the cluster does not have
+  float2 total[ROOM][G::CLUSTER][G::SLAB];  // (0, 0) for CTAs that the cluster does not have
   uint64_t bar[ROOM];
 };
 
@@ -519,9 +523,9 @@ __device__ __forceinline__ float receive_steps(Exchange<G> &x, int n, int rank, 
   const int ch = (threadIdx.x & 31) % G::ACROSS;
   float in = carry;
 #pragma unroll
-  for (int k = 0; k < MAX_CLUSTER; ++k) {
-    const int r = BACK ? MAX_CLUSTER - 1 - k : k;
-    if (r >= MAX_CLUSTER / 2 && n <= MAX_CLUSTER / 2) continue;
+  for (int k = 0; k < G::CLUSTER; ++k) {
+    const int r = BACK ? G::CLUSTER - 1 - k : k;
+    if (r / 4 * 4 >= n) continue;
     if (r == rank) in = carry;
     const float2 v = x.total[i % ROOM][r][ch];
     carry = apply(v.x, v.y, carry);
@@ -533,7 +537,7 @@ __device__ __forceinline__ float receive_steps(Exchange<G> &x, int n, int rank, 
 template <typename G>
 __device__ __forceinline__ void open_exchange(Exchange<G> &x, int C) {
   const int lane = threadIdx.x & 31;
-  for (int k = lane; k < ROOM * MAX_CLUSTER * G::SLAB; k += 32) (&x.total[0][0][0])[k] = make_float2(0.f, 0.f);
+  for (int k = lane; k < ROOM * G::CLUSTER * G::SLAB; k += 32) (&x.total[0][0][0])[k] = make_float2(0.f, 0.f);
   if (lane < ROOM) mbar_init(smem_u32(&x.bar[lane]), 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __syncwarp();
@@ -546,7 +550,7 @@ struct Rounds {
   __device__ __forceinline__ Rounds(int C_, int rank_, int R_, int T)
       : C(C_), rank(rank_), R(R_), n(((T + R_ - 1) / R_ + C_ - 1) / C_) {}
   // first row of this CTA's tile in the i-th of them (T where it has none)
-  // (T <= 2^30 and C R <= 2048: below T + C R, which fits)
+  // (T <= 2^30 and C R <= 4096: below T + C R, which fits)
   __device__ __forceinline__ int row(int i, int T) const { return min(T, (i * C + rank) * R); }
 };
 
@@ -562,27 +566,27 @@ struct Tile {
 // What a warp of the forward has in shared memory.
 template <typename G>
 struct FwdShared {
-  float2 steps[2][G::GROUPS * G::SLAB];  // the groups' steps, then what reaches them
+  float2 steps[G::GROUPS * G::SLAB];  // the groups' steps, then what reaches them
   Exchange<G> exchange;
   // h0 of the last sequence that begins in each lane's rows: hT may be h0, and who
   // comes to that sequence's end first is open (the others end with the same lane)
-  float4 held[2][G::N / 4][32];
-  Marks<G> marks[2];
+  float4 held[G::N / 4][32];
+  Marks<G> marks;
 };
 
-// And a CTA: x of the tiles in both halves and the next one, gates of one.
+// And a CTA: x of a tile and of the next one, gates of one.
 template <typename G>
 struct FwdCta {
-  Slot<G> x[3], gate;
+  Slot<G> x[2], gate;
   FwdShared<G> warps[WARPS];
   int32_t starts[FEW];
   uint64_t bar[2];  // of the copies of the tiles, by the tile's parity
 };
 
 // A warp of the forward.
-template <typename E, int SLAB>
+template <typename E, int SLAB, int CLUSTER>
 struct ForwardWarp {
-  using G = Fwd<E, SLAB>;
+  using G = Fwd<E, SLAB, CLUSTER>;
   static constexpr int M = G::N / 2, S = G::S, CX = G::CX;  // M pairs of channels a lane
   const E *x, *gate;
   E *h;
@@ -607,7 +611,7 @@ struct ForwardWarp {
     const uint32_t bar = smem_u32(&cta.bar[i & 1]);
     mbar_expect_tx(bar, any ? 2 * (uint32_t)sizeof(Slot<G>) : 0);
     if (!any) return;
-    fetch(cta.x[i % 3], maps.x, r0, d0, bar);
+    fetch(cta.x[i & 1], maps.x, r0, d0, bar);
     fetch(cta.gate, maps.gate, r0, d0, bar);
   }
   __device__ __forceinline__ void wait_tile(int i) {
@@ -619,7 +623,7 @@ struct ForwardWarp {
     const int r0 = rounds.row(i, p.T);
     if (p.T % S == 0 || r0 >= p.T || r0 + G::R < p.T) return;
     const int own = d - cx * G::N;
-    fetch_rest(cta.x[i % 3], x, p.ld, r0, p.T, own, p.D);
+    fetch_rest(cta.x[i & 1], x, p.ld, r0, p.T, own, p.D);
     fetch_rest(cta.gate, gate, p.ld, r0, p.T, own, p.D);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
@@ -633,14 +637,14 @@ struct ForwardWarp {
     for (int n = 0; n < M; ++n) Cs[n] = Hs[n] = both(0.f);
 #pragma unroll
     for (int k = 0; k < S; ++k) {
-      if (!PLAIN && (t.bits.first >> k & 1)) {
-        load_state(on ? p.h0 : nullptr, first_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, Hs);
+      if (!PLAIN && (t.bits.any_first >> k & 1) && (t.bits.first >> k & 1)) {
+        load_state(on ? p.h0 : nullptr, first_of(p, sh.marks, t.r0, q * S + k), p.D, d, Hs);
 #pragma unroll
         for (int n = 0; n < M; n += 2)
-          sh.held[i & 1][n / 2][lane] = make_float4(Hs[n].x, Hs[n].y, Hs[n + 1].x, Hs[n + 1].y);
+          sh.held[n / 2][lane] = make_float4(Hs[n].x, Hs[n].y, Hs[n + 1].x, Hs[n + 1].y);
       }
       float2 xv[M], gv[M];
-      pairs(cta.x[i % 3].v[slot(k)], xv, (E *)nullptr);
+      pairs(cta.x[i & 1].v[slot(k)], xv, (E *)nullptr);
       pairs(cta.gate.v[slot(k)], gv, (E *)nullptr);
 #pragma unroll
       for (int n = 0; n < M; ++n) {
@@ -648,34 +652,30 @@ struct ForwardWarp {
         Hs[n] = row_step(mc[k][n], xv[n], Hs[n]);
         Cs[n] = share(mc[k][n], Cs[n]);
       }
-      if (!PLAIN && !(t.bits.live >> k & 1)) {  // (what was not read may be anything)
-#pragma unroll
-        for (int n = 0; n < M; ++n) Hs[n] = both(0.f);
-      }
     }
-    cta_barrier();  // (all warps are done with the gates, and with tile i - 2)
+    cta_barrier();  // (all warps are done with the gates, and with tile i - 1)
     fetch_tile(i + 1);
     const bool cut = !PLAIN && (t.bits.first != 0 || t.bits.live != G::ALL);
 #pragma unroll
     for (int n = 0; n < M; ++n) {
-      sh.steps[i & 1][G::at(q, 2 * n * CX + cx)] = make_float2(cut ? CUT : Cs[n].x, Hs[n].x);
-      sh.steps[i & 1][G::at(q, (2 * n + 1) * CX + cx)] = make_float2(cut ? CUT : Cs[n].y, Hs[n].y);
+      sh.steps[G::at(q, 2 * n * CX + cx)] = make_float2(cut ? CUT : Cs[n].x, Hs[n].x);
+      sh.steps[G::at(q, (2 * n + 1) * CX + cx)] = make_float2(cut ? CUT : Cs[n].y, Hs[n].y);
     }
     __syncwarp();
-    t.scan = scan_up<G, false, PLAIN>(sh.steps[i & 1]);
+    t.scan = scan_up<G, false, PLAIN>(sh.steps);
     send_step<G>(sh.exchange, C, rank, i, t.scan, lost);
   }
   // The second half: the rows once more, from the state before them.
   template <bool PLAIN>
   __device__ __forceinline__ void second_half(int i, const Tile &t, const float2 (&mc)[S][M]) {
     const float in = receive_steps<G, false>(sh.exchange, C, rank, i, t.scan, carry, lost, p.status);
-    scan_down<G, false, PLAIN>(sh.steps[i & 1], t.scan, in);
+    scan_down<G, false, PLAIN>(sh.steps, t.scan, in);
     __syncwarp();
     float2 y[M];
 #pragma unroll
     for (int n = 0; n < M; ++n)
-      y[n] = make_float2(sh.steps[i & 1][G::at(q, 2 * n * CX + cx)].x,
-                         sh.steps[i & 1][G::at(q, (2 * n + 1) * CX + cx)].x);
+      y[n] = make_float2(sh.steps[G::at(q, 2 * n * CX + cx)].x,
+                         sh.steps[G::at(q, (2 * n + 1) * CX + cx)].x);
     if (!on) return;
     const int row = t.r0 + q * S;
     if (p.states && row % RECUR_KEEP == 0 && row < p.T)
@@ -683,38 +683,37 @@ struct ForwardWarp {
     E *out = h + (size_t)row * p.D + d;
     uint4 rows[S];  // (read before the first store, which the reads could not pass)
 #pragma unroll
-    for (int k = 0; k < S; ++k) rows[k] = cta.x[i % 3].v[slot(k)];
+    for (int k = 0; k < S; ++k) rows[k] = cta.x[i & 1].v[slot(k)];
 #pragma unroll
     for (int k = 0; k < S; ++k, out += p.D) {
       float2 xv[M];
       pairs(rows[k], xv, (E *)nullptr);
-      if (!PLAIN) {
-        if (!(t.bits.live >> k & 1)) continue;
+      if (!PLAIN && (t.bits.any_first >> k & 1)) {
         if (t.bits.first >> k == 1) {
 #pragma unroll
           for (int n = 0; n < M; n += 2) {
-            const float4 v = sh.held[i & 1][n / 2][lane];
+            const float4 v = sh.held[n / 2][lane];
             y[n] = make_float2(v.x, v.y);
             y[n + 1] = make_float2(v.z, v.w);
           }
         } else if (t.bits.first >> k & 1) {
-          load_state(p.h0, first_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, y);
+          load_state(p.h0, first_of(p, sh.marks, t.r0, q * S + k), p.D, d, y);
         }
       }
 #pragma unroll
       for (int n = 0; n < M; ++n) y[n] = row_step(mc[k][n], xv[n], y[n]);
-      *(uint4 *)out = packed(y, (E *)nullptr);
-      if (!PLAIN && (t.bits.last >> k & 1) && p.hT)
-        store_state(p.hT, last_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, y);
+      if (PLAIN || (t.bits.live >> k & 1)) *(uint4 *)out = packed(y, (E *)nullptr);
+      if (!PLAIN && (t.bits.any_last >> k & 1) && (t.bits.last >> k & 1) && p.hT)
+        store_state(p.hT, last_of(p, sh.marks, t.r0, q * S + k), p.D, d, y);
     }
   }
 };
 
-template <typename E, int SLAB>
-__global__ void __launch_bounds__(32 * WARPS, SM_WARPS / WARPS)
+template <typename E, int SLAB, int CLUSTER>
+__global__ void __launch_bounds__(32 * WARPS, CLUSTER == 8 ? 3 : 2)
 recur_forward_kernel(const E *x, const E *gate, E *h, const __grid_constant__ Maps maps, RecurParams p) {
   pdl_begin();
-  using G = Fwd<E, SLAB>;
+  using G = Fwd<E, SLAB, CLUSTER>;
   extern __shared__ __align__(1024) char shared[];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -728,7 +727,7 @@ recur_forward_kernel(const E *x, const E *gate, E *h, const __grid_constant__ Ma
   const int q = Slot<G>::group(lane / G::CX), cx = lane % G::CX, d = d0 + cx * G::N, count = rounds.n;
   const int lo = p.starts ? max(0, p.starts[0]) : 0;
   const int hi = p.starts ? min(p.T, max(0, p.starts[p.B])) : p.T;
-  ForwardWarp<E, SLAB> w{x, gate, h, maps, p, cta, sh, rounds, C, rank, lane, q, cx, warp * G::CX + cx, base, d, count, lo, hi, d < p.D, false};
+  ForwardWarp<E, SLAB, CLUSTER> w{x, gate, h, maps, p, cta, sh, rounds, C, rank, lane, q, cx, warp * G::CX + cx, base, d, count, lo, hi, d < p.D, false};
   if (threadIdx.x < 2) mbar_init(smem_u32(&cta.bar[threadIdx.x]), 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -740,31 +739,24 @@ recur_forward_kernel(const E *x, const E *gate, E *h, const __grid_constant__ Ma
   for (int n = 0; n < G::N / 2; ++n) w.bias[n] = mul2(w.bias[n], both(LOG2E));
   w.carry = 0.f;
   if (C > 1) cluster_wait();
-  Tile now, next;
-  float2 c[G::S][G::N / 2], cn[G::S][G::N / 2];
-  for (int i = -1; i < count; ++i) {
-    const int j = i + 1;
-    if (j < count) {
-      next.r0 = rounds.row(j, p.T);
-      next.plain = plain_tile<G::R>(p, w.gap, next.r0, lo, hi);
-      if (!next.plain) {
-        next.bits = row_bits(p, starts, sh.marks[j & 1], w.gap, next.r0, q, w.live_of(j));
-        next.plain = (next.bits.first | next.bits.last) == 0 && next.bits.live == G::ALL;
-      }
-      next.plain = __all_sync(0xFFFFFFFFu, next.plain);
-      w.wait_tile(j);
-      if (next.plain) w.template first_half<true>(j, next, cn);
-      else w.template first_half<false>(j, next, cn);
+  Tile t;
+  float2 c[G::S][G::N / 2];
+  for (int i = 0; i < count; ++i) {
+    t.r0 = rounds.row(i, p.T);
+    t.plain = plain_tile<G::R>(p, w.gap, t.r0, lo, hi);
+    if (!t.plain) {
+      t.bits = row_bits(p, starts, sh.marks, w.gap, t.r0, q, w.live_of(i));
+      t.plain = (t.bits.first | t.bits.last) == 0 && t.bits.live == G::ALL;
     }
-    if (i >= 0) {
-      if (now.plain) w.template second_half<true>(i, now, c);
-      else w.template second_half<false>(i, now, c);
+    t.plain = __all_sync(0xFFFFFFFFu, t.plain);
+    w.wait_tile(i);
+    if (t.plain) {
+      w.template first_half<true>(i, t, c);
+      w.template second_half<true>(i, t, c);
+    } else {
+      w.template first_half<false>(i, t, c);
+      w.template second_half<false>(i, t, c);
     }
-    now = next;
-#pragma unroll
-    for (int k = 0; k < G::S; ++k)
-#pragma unroll
-      for (int n = 0; n < G::N / 2; ++n) c[k][n] = cn[k][n];
   }
   // (nothing is on its way to this CTA any more, unless a wait has given up)
   if (C > 1) {
@@ -777,25 +769,25 @@ recur_forward_kernel(const E *x, const E *gate, E *h, const __grid_constant__ Ma
 template <typename G>
 struct BwdShared {
   float2 stepsF[G::GROUPS * G::SLAB];     // the groups' steps forward
-  float2 stepsB[2][G::GROUPS * G::SLAB];  // and back, then what reaches them
+  float2 stepsB[G::GROUPS * G::SLAB];  // and back, then what reaches them
   Exchange<G> exchange;
-  float bias[MAX_CLUSTER][G::SLAB];       // the CTAs' sums of dgate
-  Marks<G> marks[2];
+  float bias[G::CLUSTER][G::SLAB];       // the CTAs' sums of dgate
+  Marks<G> marks;
 };
 
 template <typename G>
 struct BwdCta {
-  Slot<G> x[2], dh[3], gate;
+  Slot<G> x, gate, dh[2];
   BwdShared<G> warps[WARPS];
   int32_t starts[FEW];
   uint64_t bar[2];  // of the copies of the tiles, by the tile's parity
 };
 
 // A warp of the backward, which goes from the last tile to the first.
-template <typename E, int SLAB>
+template <typename E, int SLAB, int S>
 struct BackwardWarp {
-  using G = Bwd<E, SLAB>;
-  static constexpr int M = G::N / 2, S = G::S, CX = G::CX;
+  using G = Bwd<E, SLAB, S>;
+  static constexpr int M = G::N / 2, CX = G::CX;
   const E *x, *gate, *dh;
   E *dx, *dgate;
   const Maps &maps;
@@ -821,9 +813,9 @@ struct BackwardWarp {
     const uint32_t bar = smem_u32(&cta.bar[i & 1]);
     mbar_expect_tx(bar, any ? 3 * (uint32_t)sizeof(Slot<G>) : 0);
     if (!any) return;
-    fetch(cta.x[i & 1], maps.x, r0, d0, bar);
+    fetch(cta.x, maps.x, r0, d0, bar);
     fetch(cta.gate, maps.gate, r0, d0, bar);
-    fetch(cta.dh[i % 3], maps.dh, r0, d0, bar);
+    fetch(cta.dh[i & 1], maps.dh, r0, d0, bar);
   }
   __device__ __forceinline__ void wait_tile(int i) {
     const uint32_t bar = smem_u32(&cta.bar[i & 1]), parity = (uint32_t)i >> 1 & 1;
@@ -834,9 +826,9 @@ struct BackwardWarp {
     const int r0 = first_row(i);
     if (p.T % S == 0 || r0 >= p.T || r0 + G::R < p.T) return;
     const int own = d - cx * G::N;
-    fetch_rest(cta.x[i & 1], x, p.ld, r0, p.T, own, p.D);
+    fetch_rest(cta.x, x, p.ld, r0, p.T, own, p.D);
     fetch_rest(cta.gate, gate, p.ld, r0, p.T, own, p.D);
-    fetch_rest(cta.dh[i % 3], dh, (long long)p.D, r0, p.T, own, p.D);
+    fetch_rest(cta.dh[i & 1], dh, (long long)p.D, r0, p.T, own, p.D);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
   }
@@ -855,10 +847,10 @@ struct BackwardWarp {
     for (int n = 0; n < M; ++n) Cs[n] = Hs[n] = both(0.f);
 #pragma unroll
     for (int k = 0; k < S; ++k) {
-      if (!PLAIN && (t.bits.first >> k & 1))
-        load_state(on ? p.h0 : nullptr, first_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, Hs);
+      if (!PLAIN && (t.bits.any_first >> k & 1) && (t.bits.first >> k & 1))
+        load_state(on ? p.h0 : nullptr, first_of(p, sh.marks, t.r0, q * S + k), p.D, d, Hs);
       float2 xv[M], gv[M];
-      pairs(cta.x[i & 1].v[slot(k)], xv, (E *)nullptr);
+      pairs(cta.x.v[slot(k)], xv, (E *)nullptr);
       pairs(cta.gate.v[slot(k)], gv, (E *)nullptr);
 #pragma unroll
       for (int n = 0; n < M; ++n) {
@@ -867,13 +859,7 @@ struct BackwardWarp {
         Hs[n] = row_step(mc[k][n], xv[n], Hs[n]);
         Cs[n] = share(mc[k][n], Cs[n]);
       }
-      if (!PLAIN && !(t.bits.live >> k & 1)) {
-#pragma unroll
-        for (int n = 0; n < M; ++n) Hs[n] = both(0.f);
-      }
     }
-    cta_barrier();  // (all warps are done with the gates, and with what stood in the other slots)
-    fetch_tile(i + 1);
     const bool dead = !PLAIN && t.bits.live != G::ALL;
     const bool cutF = !PLAIN && (dead || t.bits.first), cutB = !PLAIN && (dead || t.bits.last);
 #pragma unroll
@@ -884,27 +870,23 @@ struct BackwardWarp {
     }
 #pragma unroll
     for (int k = S - 1; k >= 0; --k) {
-      if (!PLAIN && (t.bits.last >> k & 1))
-        load_state(on ? p.dhT : nullptr, last_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, Hs);
+      if (!PLAIN && (t.bits.any_last >> k & 1) && (t.bits.last >> k & 1))
+        load_state(on ? p.dhT : nullptr, last_of(p, sh.marks, t.r0, q * S + k), p.D, d, Hs);
       float2 dv[M];
-      pairs(cta.dh[i % 3].v[slot(k)], dv, (E *)nullptr);
+      pairs(cta.dh[i & 1].v[slot(k)], dv, (E *)nullptr);
 #pragma unroll
       for (int n = 0; n < M; ++n) {
         const float2 g = add2(dv[n], Hs[n]);
         Hs[n] = fma2(mc[k][n], g, g);
       }
-      if (!PLAIN && !(t.bits.live >> k & 1)) {
-#pragma unroll
-        for (int n = 0; n < M; ++n) Hs[n] = both(0.f);
-      }
     }
 #pragma unroll
     for (int n = 0; n < M; ++n) {
-      sh.stepsB[i & 1][G::at(q, 2 * n * CX + cx)] = make_float2(cutB ? CUT : Cs[n].x, Hs[n].x);
-      sh.stepsB[i & 1][G::at(q, (2 * n + 1) * CX + cx)] = make_float2(cutB ? CUT : Cs[n].y, Hs[n].y);
+      sh.stepsB[G::at(q, 2 * n * CX + cx)] = make_float2(cutB ? CUT : Cs[n].x, Hs[n].x);
+      sh.stepsB[G::at(q, (2 * n + 1) * CX + cx)] = make_float2(cutB ? CUT : Cs[n].y, Hs[n].y);
     }
     __syncwarp();
-    t.scan = scan_up<G, true, PLAIN>(sh.stepsB[i & 1]);
+    t.scan = scan_up<G, true, PLAIN>(sh.stepsB);
     send_step<G>(sh.exchange, C, rank, i, t.scan, lost);
     scan_down<G, false, PLAIN>(sh.stepsF, scan_up<G, false, PLAIN>(sh.stepsF), before);
     before = state_before(i + 1);
@@ -915,10 +897,10 @@ struct BackwardWarp {
       y[n] = make_float2(sh.stepsF[G::at(q, 2 * n * CX + cx)].x, sh.stepsF[G::at(q, (2 * n + 1) * CX + cx)].x);
 #pragma unroll
     for (int k = 0; k < S; ++k) {
-      if (!PLAIN && on && (t.bits.first >> k & 1))
-        load_state(p.h0, first_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, y);
+      if (!PLAIN && (t.bits.any_first >> k & 1) && on && (t.bits.first >> k & 1))
+        load_state(p.h0, first_of(p, sh.marks, t.r0, q * S + k), p.D, d, y);
       float2 xv[M];
-      pairs(cta.x[i & 1].v[slot(k)], xv, (E *)nullptr);
+      pairs(cta.x.v[slot(k)], xv, (E *)nullptr);
 #pragma unroll
       for (int n = 0; n < M; ++n) {
         const float2 minus_took = mul2(less2(y[n], xv[n]), mc[k][n]);
@@ -926,55 +908,57 @@ struct BackwardWarp {
         e[k][n] = mul2(minus_took, mul2(e[k][n], mc[k][n]));
       }
     }
+    cta_barrier();  // (all warps are done with x and the gates, and with the last tile's dh)
+    fetch_tile(i + 1);
   }
   // The second half: G, from the last row on.
   template <bool PLAIN>
   __device__ __forceinline__ void second_half(int i, const Tile &t, const float2 (&e)[S][M],
                                               const float2 (&mc)[S][M]) {
     const float in = receive_steps<G, true>(sh.exchange, C, rank, i, t.scan, carry, lost, p.status);
-    scan_down<G, true, PLAIN>(sh.stepsB[i & 1], t.scan, in);
+    scan_down<G, true, PLAIN>(sh.stepsB, t.scan, in);
     __syncwarp();
     float2 y[M];
 #pragma unroll
     for (int n = 0; n < M; ++n)
-      y[n] = make_float2(sh.stepsB[i & 1][G::at(q, 2 * n * CX + cx)].x,
-                         sh.stepsB[i & 1][G::at(q, (2 * n + 1) * CX + cx)].x);
+      y[n] = make_float2(sh.stepsB[G::at(q, 2 * n * CX + cx)].x,
+                         sh.stepsB[G::at(q, (2 * n + 1) * CX + cx)].x);
     if (!on) return;
     const int row = t.r0 + q * S;
     E *px = dx + (size_t)row * p.ld + d, *pg = dgate + (size_t)row * p.ld + d;
     uint4 rows[S];
 #pragma unroll
-    for (int k = 0; k < S; ++k) rows[k] = cta.dh[i % 3].v[slot(k)];
+    for (int k = 0; k < S; ++k) rows[k] = cta.dh[i & 1].v[slot(k)];
 #pragma unroll
     for (int k = S - 1; k >= 0; --k) {
-      if (!PLAIN) {
-        if (!(t.bits.live >> k & 1)) continue;
-        if (t.bits.last >> k & 1)
-          load_state(p.dhT, last_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, y);
-      }
+      if (!PLAIN && (t.bits.any_last >> k & 1) && (t.bits.last >> k & 1))
+        load_state(p.dhT, last_of(p, sh.marks, t.r0, q * S + k), p.D, d, y);
+      const bool live = PLAIN || (t.bits.live >> k & 1);
       float2 dv[M], gv[M];
       pairs(rows[k], dv, (E *)nullptr);
 #pragma unroll
       for (int n = 0; n < M; ++n) {
         const float2 g = add2(dv[n], y[n]);
         gv[n] = mul2(g, e[k][n]);
-        db[n] = add2(db[n], gv[n]);
+        if (live) db[n] = add2(db[n], gv[n]);
         dv[n] = mul2(g, mc[k][n]);  // -dx
         y[n] = add2(g, dv[n]);
       }
-      *(uint4 *)(px + k * p.ld) = packed<true>(dv, (E *)nullptr);
-      *(uint4 *)(pg + k * p.ld) = packed(gv, (E *)nullptr);
-      if (!PLAIN && (t.bits.first >> k & 1) && p.dh0)
-        store_state(p.dh0, first_of(p, sh.marks[i & 1], t.r0, q * S + k), p.D, d, y);
+      if (live) {
+        *(uint4 *)(px + k * p.ld) = packed<true>(dv, (E *)nullptr);
+        *(uint4 *)(pg + k * p.ld) = packed(gv, (E *)nullptr);
+      }
+      if (!PLAIN && (t.bits.any_first >> k & 1) && (t.bits.first >> k & 1) && p.dh0)
+        store_state(p.dh0, first_of(p, sh.marks, t.r0, q * S + k), p.D, d, y);
     }
   }
 };
 
-template <typename E, int SLAB>
-__global__ void __launch_bounds__(32 * WARPS, SM_WARPS / WARPS)
+template <typename E, int SLAB, int S>
+__global__ void __launch_bounds__(32 * WARPS, S == 4 ? 3 : 2)
 recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, const __grid_constant__ Maps maps, RecurParams p) {
   pdl_begin();
-  using G = Bwd<E, SLAB>;
+  using G = Bwd<E, SLAB, S>;
   constexpr int N = G::N, CX = G::CX;
   extern __shared__ __align__(1024) char shared[];
   cg::cluster_group cluster = cg::this_cluster();
@@ -990,7 +974,7 @@ recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, c
   const int sc = lane % G::ACROSS, sd = d0 + sc % CX * N + sc / CX;
   const int lo = p.starts ? max(0, p.starts[0]) : 0;
   const int hi = p.starts ? min(p.T, max(0, p.starts[p.B])) : p.T;
-  BackwardWarp<E, SLAB> w{x, gate, dh, dx, dgate, maps, p, cta, sh, rounds, C, rank, lane, q, cx, warp * CX + cx, base, d, sd, count, lo, hi, d < p.D, false};
+  BackwardWarp<E, SLAB, S> w{x, gate, dh, dx, dgate, maps, p, cta, sh, rounds, C, rank, lane, q, cx, warp * CX + cx, base, d, sd, count, lo, hi, d < p.D, false};
   if (threadIdx.x < 2) mbar_init(smem_u32(&cta.bar[threadIdx.x]), 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -1006,34 +990,24 @@ recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, c
   }
   w.carry = 0.f;
   if (C > 1) cluster_wait();
-  Tile now, next;
-  float2 c[G::S][N / 2], e[G::S][N / 2], cn[G::S][N / 2], en[G::S][N / 2];
-  for (int i = -1; i < count; ++i) {
-    const int j = i + 1;
-    if (j < count) {
-      next.r0 = w.first_row(j);
-      next.plain = plain_tile<G::R>(p, w.gap, next.r0, lo, hi);
-      if (!next.plain) {
-        next.bits = row_bits(p, starts, sh.marks[j & 1], w.gap, next.r0, q, w.live_of(j));
-        next.plain = (next.bits.first | next.bits.last) == 0 && next.bits.live == G::ALL;
-      }
-      next.plain = __all_sync(0xFFFFFFFFu, next.plain);
-      w.wait_tile(j);
-      if (next.plain) w.template first_half<true>(j, next, en, cn);
-      else w.template first_half<false>(j, next, en, cn);
+  Tile t;
+  float2 c[G::S][N / 2], e[G::S][N / 2];
+  for (int i = 0; i < count; ++i) {
+    t.r0 = w.first_row(i);
+    t.plain = plain_tile<G::R>(p, w.gap, t.r0, lo, hi);
+    if (!t.plain) {
+      t.bits = row_bits(p, starts, sh.marks, w.gap, t.r0, q, w.live_of(i));
+      t.plain = (t.bits.first | t.bits.last) == 0 && t.bits.live == G::ALL;
     }
-    if (i >= 0) {
-      if (now.plain) w.template second_half<true>(i, now, e, c);
-      else w.template second_half<false>(i, now, e, c);
+    t.plain = __all_sync(0xFFFFFFFFu, t.plain);
+    w.wait_tile(i);
+    if (t.plain) {
+      w.template first_half<true>(i, t, e, c);
+      w.template second_half<true>(i, t, e, c);
+    } else {
+      w.template first_half<false>(i, t, e, c);
+      w.template second_half<false>(i, t, e, c);
     }
-    now = next;
-#pragma unroll
-    for (int k = 0; k < G::S; ++k)
-#pragma unroll
-      for (int n = 0; n < N / 2; ++n) {
-        c[k][n] = cn[k][n];
-        e[k][n] = en[k][n];
-      }
   }
   float db[N];
 #pragma unroll
@@ -1127,41 +1101,44 @@ int resident_clusters(K kern, int threads, size_t smem, int C) {
   return n;
 }
 
-// A kernel's clusters: as many CTAs as there are tiles, while all of them are
+// A kernel's clusters: as few CTAs as make the fewest rounds, while all of them are
 // resident at once.
-template <typename K>
+template <typename K, int MOST>
 struct Shape {
   cudaError_t attr;
-  int fit[MAX_CLUSTER + 1];  // clusters that are resident, by their CTAs
+  int fit[MOST + 1];  // clusters that are resident, by their CTAs
   Shape(K kern, int threads, size_t smem)
       : attr(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) {
-    for (int C = 1; C <= MAX_CLUSTER; ++C)
+    if (attr == cudaSuccess && MOST > 8)
+      attr = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    for (int C = 1; C <= MOST; ++C)
       fit[C] = attr == cudaSuccess ? resident_clusters(kern, threads, smem, C) : 0;
   }
   int cluster(int ctas, int tiles) const {
     int C = 1;
-    for (int k = 2; k <= MAX_CLUSTER && k <= tiles; ++k)
-      if (fit[k] >= ctas) C = k;
+    for (int k = 2; k <= MOST && k <= tiles; ++k)
+      if (fit[k] >= ctas && (tiles + k - 1) / k < (tiles + C - 1) / C) C = k;
     return C;
   }
 };
 
-// 16 channels a warp in bf16, unless three fifths of the CTAs that are resident at once
-// do not come together that way; 8 double them (us, 8 | 16: 16384 x 128 forward + backward
-// 33 + 61 | 53 + 101, 131072 x 1024 forward 200 | 309, 16384 x 1280 45 + 82 | 49 + 94,
-// 16384 x 1536 50 + 94 | 47 + 91, 16384 x 4096 106 + 198 | 89 + 167: 16 bytes of a row are
-// half a sector).  fp32 always 8 (8192 x 4096 79 + 138 | 77 + 148, 2048 x 1024 10 + 14 |
-// 14 + 22).
-bool wide(int D) {
-  return 5ll * ((D + 63) / 64) * MAX_CLUSTER >= 3ll * num_sms() * SM_WARPS / WARPS;
-}
+// bf16 takes 16 channels a warp where clusters of 16 CTAs of that width fill the SMs, two
+// CTAs each; else 8, which double the CTAs (us, 8 | 16: 16384 x 512 forward + backward
+// 22 + 36 | 28 + 44, 131072 x 1024 forward 195 | 221, 16384 x 1280 43 + 78 | 39 + 63, 16384 x
+// 4096 98 + 189 | 89 + 154: 16 bytes of a row are half a sector).  fp32 always 8 (8192 x
+// 4096 79 + 138 | 77 + 148, 2048 x 1024 10 + 14 | 14 + 22).
+int columns(int D) { return (D + 63) / 64; }
+bool wide(int D) { return columns(D) * 16 >= 2 * num_sms(); }
+// Clusters of 8 leave room in shared memory for a third CTA of the forward, where there
+// are the CTAs (8 | 16: 16384 x 4096 82 | 89, 16384 x 2048 49 | 49, 16384 x 1536 47 | 42).
+bool wider(int D) { return columns(D) * 8 > 2 * num_sms(); }
 
-template <typename E, int SLAB>
+template <typename E, int SLAB, int CLUSTER>
 cudaError_t forward_w(const RecurArgs &a, cudaStream_t s) {
-  using G = Fwd<E, SLAB>;
+  using G = Fwd<E, SLAB, CLUSTER>;
   constexpr int SMEM = sizeof(FwdCta<G>);
-  auto kern = recur_forward_kernel<E, SLAB>;
-  static const Shape<decltype(kern)> shape(kern, 32 * WARPS, SMEM);
+  auto kern = recur_forward_kernel<E, SLAB, CLUSTER>;
+  static const Shape<decltype(kern), G::CLUSTER> shape(kern, 32 * WARPS, SMEM);
   if (shape.attr != cudaSuccess) return shape.attr;
   const int width = WARPS * G::SLAB, ctas = (a.D + width - 1) / width;
   const int C = shape.cluster(ctas, (a.T + G::R - 1) / G::R);
@@ -1183,16 +1160,17 @@ cudaError_t forward_t(const RecurArgs &a, cudaStream_t s) {
                     params_of(a));
   }
   if constexpr (sizeof(E) == 2)
-    if (wide(a.D) || (a.starts && a.B > MAX_SHORT_B)) return forward_w<E, 16>(a, s);
-  return forward_w<E, 8>(a, s);
+    if (wide(a.D) || (a.starts && a.B > MAX_SHORT_B))
+      return wider(a.D) ? forward_w<E, 16, 8>(a, s) : forward_w<E, 16, 16>(a, s);
+  return forward_w<E, 8, 16>(a, s);
 }
 
-template <typename E, int SLAB>
-cudaError_t backward_w(const RecurArgs &a, cudaStream_t s) {
-  using G = Bwd<E, SLAB>;
+template <typename E, int SLAB, int S>
+cudaError_t backward_s(const RecurArgs &a, cudaStream_t s) {
+  using G = Bwd<E, SLAB, S>;
   constexpr int SMEM = sizeof(BwdCta<G>);
-  auto kern = recur_backward_kernel<E, SLAB>;
-  static const Shape<decltype(kern)> shape(kern, 32 * WARPS, SMEM);
+  auto kern = recur_backward_kernel<E, SLAB, S>;
+  static const Shape<decltype(kern), G::CLUSTER> shape(kern, 32 * WARPS, SMEM);
   if (shape.attr != cudaSuccess) return shape.attr;
   const int width = WARPS * G::SLAB, ctas = (a.D + width - 1) / width;
   const int C = shape.cluster(ctas, (a.T + G::R - 1) / G::R);
@@ -1206,10 +1184,22 @@ cudaError_t backward_w(const RecurArgs &a, cudaStream_t s) {
                          maps, params_of(a));
 }
 
+
+// Tiles of 4 rows a group leave registers for a third CTA, and a call of few rounds has
+// more CTAs at work; those of 8 have fewer rounds, each of a fixed cost (us, 4 | 8: 64 x 128
+// fp32 6.4 | 8.4, 4096 x 2048 of 9 sequences 32 | 37, of 1 28 | 27, 8192 x 1024 32 | 30, 16384
+// x 4096 164 | 154).
+constexpr int FEW_ROWS = 4096;
+
+template <typename E, int SLAB>
+cudaError_t backward_w(const RecurArgs &a, cudaStream_t s) {
+  return a.T <= FEW_ROWS ? backward_s<E, SLAB, 4>(a, s) : backward_s<E, SLAB, 8>(a, s);
+}
+
 template <typename E>
 cudaError_t backward_t(const RecurArgs &a, cudaStream_t s) {
   if constexpr (sizeof(E) == 2)
-    if (wide(a.D)) return backward_w<E, 16>(a, s);
+    if (wide(a.D) || (a.starts && a.B > MAX_SHORT_B)) return backward_w<E, 16>(a, s);
   return backward_w<E, 8>(a, s);
 }
 
