@@ -20,7 +20,7 @@
 // and with the state that comes in from the left the lanes go over their rows once
 // more, from shared memory and registers, and write them.  While a tile's step is on its
 // way to the other CTAs, the SM's other CTAs work.  The grouping of the sums follows from
-// the sizes alone.
+// the sizes and the device.
 //
 // The backward runs the same over the rows in reverse for G, and forward within a
 // tile for h, from the fp32 states that the forward kept every RECUR_KEEP rows: h
@@ -28,14 +28,15 @@
 // enter the gradient.
 //
 // HBM would bound it (3 values an element forward, 5 backward: 60 and 101 us at 16384 x
-// 4096 bf16, which take 82 and 154).  What bounds it is latency, and next the issue slots:
+// 4096 bf16, which take 84 and 142).  What bounds it is latency, and next the issue slots:
 // the gates stay in registers from one pass over a tile to the other, which leaves room for
 // 12 warps an SM forward and 8 backward, and a round has its fixed part (two scans, the
 // exchange) of some 600 instructions.  Measured on the way: CTAs in step with barriers,
 // 150 and 430 us; warps by themselves, 120 and 187; two tiles at a time, one of them on its
 // way to the other CTAs, 107 and 186; two channels an instruction, 102 and 183; rows copied
 // in whole lines, 95 and 176; tiles copied as boxes of a tensor, 88 and 167; one tile at a
-// time again, with the registers spent on more warps and on longer tiles, 82 and 154.
+// time again, with the registers spent on more warps and on longer tiles, 84 and 158; copies on
+// their way for a whole round, 84 and 142.
 // Gates computed again in the second pass (24 warps an SM, a round's inputs from L2): 120
 // and 258.  Rows copied one by one in bulk: 233 and 251 (32 cycles of the SM each).  One
 // body for all tiles, with branches at the rows where sequences begin: 93 and 217; with
@@ -164,7 +165,7 @@ struct Geo {
   }
 };
 template <typename E, int SLAB, int CLUSTER> using Fwd = Geo<E, SLAB, 8, CLUSTER>;
-template <typename E, int SLAB, int S> using Bwd = Geo<E, SLAB, S, 16>;
+template <typename E, int SLAB, int S, int CLUSTER> using Bwd = Geo<E, SLAB, S, CLUSTER>;
 constexpr int WARPS = 4;  // a CTA's
 
 // Where sequences begin and end in a warp's tile, by rows.  (Without starts it
@@ -777,17 +778,20 @@ struct BwdShared {
 
 template <typename G>
 struct BwdCta {
-  Slot<G> x, gate, dh[2];
+  // x of a tile and of the next one, where that costs no CTA of the SM (16384 x 4096: 142
+  // us, else 149; 4096 x 2048, with two CTAs where there were three: 35, else 32)
+  static constexpr int XS = G::SLAB == 16 && G::CLUSTER == 16 ? 1 : 2;
+  Slot<G> x[XS], gate, dh[2];
   BwdShared<G> warps[WARPS];
   int32_t starts[FEW];
   uint64_t bar[2];  // of the copies of the tiles, by the tile's parity
 };
 
 // A warp of the backward, which goes from the last tile to the first.
-template <typename E, int SLAB, int S>
+template <typename E, int SLAB, int S, int CLUSTER>
 struct BackwardWarp {
-  using G = Bwd<E, SLAB, S>;
-  static constexpr int M = G::N / 2, CX = G::CX;
+  using G = Bwd<E, SLAB, S, CLUSTER>;
+  static constexpr int M = G::N / 2, CX = G::CX, XS = BwdCta<G>::XS;
   const E *x, *gate, *dh;
   E *dx, *dgate;
   const Maps &maps;
@@ -806,6 +810,7 @@ struct BackwardWarp {
   __device__ __forceinline__ uint32_t live_of(int i) const {
     return live_rows<S>(first_row(i) + q * S, lo, hi);
   }
+  // A tile's copies; x's apart where its only slot is free later than the gates'.
   __device__ __forceinline__ void fetch_tile(int i) {
     if (i >= count || threadIdx.x != 0) return;
     const int r0 = first_row(i);
@@ -813,9 +818,14 @@ struct BackwardWarp {
     const uint32_t bar = smem_u32(&cta.bar[i & 1]);
     mbar_expect_tx(bar, any ? 3 * (uint32_t)sizeof(Slot<G>) : 0);
     if (!any) return;
-    fetch(cta.x, maps.x, r0, d0, bar);
     fetch(cta.gate, maps.gate, r0, d0, bar);
     fetch(cta.dh[i & 1], maps.dh, r0, d0, bar);
+    if (XS == 2) fetch(cta.x[i % XS], maps.x, r0, d0, bar);
+  }
+  __device__ __forceinline__ void fetch_x(int i) {
+    if (i >= count || threadIdx.x != 0) return;
+    const int r0 = first_row(i);
+    if (r0 / S < p.T / S) fetch(cta.x[i % XS], maps.x, r0, d0, smem_u32(&cta.bar[i & 1]));
   }
   __device__ __forceinline__ void wait_tile(int i) {
     const uint32_t bar = smem_u32(&cta.bar[i & 1]), parity = (uint32_t)i >> 1 & 1;
@@ -826,7 +836,7 @@ struct BackwardWarp {
     const int r0 = first_row(i);
     if (p.T % S == 0 || r0 >= p.T || r0 + G::R < p.T) return;
     const int own = d - cx * G::N;
-    fetch_rest(cta.x, x, p.ld, r0, p.T, own, p.D);
+    fetch_rest(cta.x[i % XS], x, p.ld, r0, p.T, own, p.D);
     fetch_rest(cta.gate, gate, p.ld, r0, p.T, own, p.D);
     fetch_rest(cta.dh[i & 1], dh, (long long)p.D, r0, p.T, own, p.D);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -850,7 +860,7 @@ struct BackwardWarp {
       if (!PLAIN && (t.bits.any_first >> k & 1) && (t.bits.first >> k & 1))
         load_state(on ? p.h0 : nullptr, first_of(p, sh.marks, t.r0, q * S + k), p.D, d, Hs);
       float2 xv[M], gv[M];
-      pairs(cta.x.v[slot(k)], xv, (E *)nullptr);
+      pairs(cta.x[i % XS].v[slot(k)], xv, (E *)nullptr);
       pairs(cta.gate.v[slot(k)], gv, (E *)nullptr);
 #pragma unroll
       for (int n = 0; n < M; ++n) {
@@ -860,6 +870,8 @@ struct BackwardWarp {
         Cs[n] = share(mc[k][n], Cs[n]);
       }
     }
+    cta_barrier();  // (all warps are done with the gates, and with the last tile's dh)
+    fetch_tile(i + 1);
     const bool dead = !PLAIN && t.bits.live != G::ALL;
     const bool cutF = !PLAIN && (dead || t.bits.first), cutB = !PLAIN && (dead || t.bits.last);
 #pragma unroll
@@ -900,7 +912,7 @@ struct BackwardWarp {
       if (!PLAIN && (t.bits.any_first >> k & 1) && on && (t.bits.first >> k & 1))
         load_state(p.h0, first_of(p, sh.marks, t.r0, q * S + k), p.D, d, y);
       float2 xv[M];
-      pairs(cta.x.v[slot(k)], xv, (E *)nullptr);
+      pairs(cta.x[i % XS].v[slot(k)], xv, (E *)nullptr);
 #pragma unroll
       for (int n = 0; n < M; ++n) {
         const float2 minus_took = mul2(less2(y[n], xv[n]), mc[k][n]);
@@ -908,8 +920,10 @@ struct BackwardWarp {
         e[k][n] = mul2(minus_took, mul2(e[k][n], mc[k][n]));
       }
     }
-    cta_barrier();  // (all warps are done with x and the gates, and with the last tile's dh)
-    fetch_tile(i + 1);
+    if constexpr (XS == 1) {
+      cta_barrier();  // (all warps are done with x)
+      fetch_x(i + 1);
+    }
   }
   // The second half: G, from the last row on.
   template <bool PLAIN>
@@ -954,11 +968,11 @@ struct BackwardWarp {
   }
 };
 
-template <typename E, int SLAB, int S>
+template <typename E, int SLAB, int S, int CLUSTER>
 __global__ void __launch_bounds__(32 * WARPS, S == 4 ? 3 : 2)
 recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, const __grid_constant__ Maps maps, RecurParams p) {
   pdl_begin();
-  using G = Bwd<E, SLAB, S>;
+  using G = Bwd<E, SLAB, S, CLUSTER>;
   constexpr int N = G::N, CX = G::CX;
   extern __shared__ __align__(1024) char shared[];
   cg::cluster_group cluster = cg::this_cluster();
@@ -974,12 +988,13 @@ recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, c
   const int sc = lane % G::ACROSS, sd = d0 + sc % CX * N + sc / CX;
   const int lo = p.starts ? max(0, p.starts[0]) : 0;
   const int hi = p.starts ? min(p.T, max(0, p.starts[p.B])) : p.T;
-  BackwardWarp<E, SLAB, S> w{x, gate, dh, dx, dgate, maps, p, cta, sh, rounds, C, rank, lane, q, cx, warp * CX + cx, base, d, sd, count, lo, hi, d < p.D, false};
+  BackwardWarp<E, SLAB, S, CLUSTER> w{x, gate, dh, dx, dgate, maps, p, cta, sh, rounds, C, rank, lane, q, cx, warp * CX + cx, base, d, sd, count, lo, hi, d < p.D, false};
   if (threadIdx.x < 2) mbar_init(smem_u32(&cta.bar[threadIdx.x]), 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   cta_barrier();
   w.fetch_tile(0);
+  if (BwdCta<G>::XS == 1) w.fetch_x(0);
   w.before = w.state_before(0);
   empty_sequences(p, p.dhT, p.dh0, d0, min(p.D, d0 + G::SLAB), rank, C);
   load_state(w.on ? p.bias : nullptr, 0, 0, d, w.bias);
@@ -1129,8 +1144,9 @@ struct Shape {
 // 4096 79 + 138 | 77 + 148, 2048 x 1024 10 + 14 | 14 + 22).
 int columns(int D) { return (D + 63) / 64; }
 bool wide(int D) { return columns(D) * 16 >= 2 * num_sms(); }
-// Clusters of 8 leave room in shared memory for a third CTA of the forward, where there
-// are the CTAs (8 | 16: 16384 x 4096 82 | 89, 16384 x 2048 49 | 49, 16384 x 1536 47 | 42).
+// Clusters of 8 leave room in shared memory for a third CTA of the forward and for more
+// copies on their way in the backward, where there are the CTAs (8 | 16: 16384 x 4096 82 +
+// 142 | 89 + 149, 16384 x 2048 49 + 81 | 49 + 78, 16384 x 1536 47 + 77 | 42 + 66).
 bool wider(int D) { return columns(D) * 8 > 2 * num_sms(); }
 
 template <typename E, int SLAB, int CLUSTER>
@@ -1165,11 +1181,11 @@ cudaError_t forward_t(const RecurArgs &a, cudaStream_t s) {
   return forward_w<E, 8, 16>(a, s);
 }
 
-template <typename E, int SLAB, int S>
+template <typename E, int SLAB, int S, int CLUSTER>
 cudaError_t backward_s(const RecurArgs &a, cudaStream_t s) {
-  using G = Bwd<E, SLAB, S>;
+  using G = Bwd<E, SLAB, S, CLUSTER>;
   constexpr int SMEM = sizeof(BwdCta<G>);
-  auto kern = recur_backward_kernel<E, SLAB, S>;
+  auto kern = recur_backward_kernel<E, SLAB, S, CLUSTER>;
   static const Shape<decltype(kern), G::CLUSTER> shape(kern, 32 * WARPS, SMEM);
   if (shape.attr != cudaSuccess) return shape.attr;
   const int width = WARPS * G::SLAB, ctas = (a.D + width - 1) / width;
@@ -1188,19 +1204,20 @@ cudaError_t backward_s(const RecurArgs &a, cudaStream_t s) {
 // Tiles of 4 rows a group leave registers for a third CTA, and a call of few rounds has
 // more CTAs at work; those of 8 have fewer rounds, each of a fixed cost (us, 4 | 8: 64 x 128
 // fp32 6.4 | 8.4, 4096 x 2048 of 9 sequences 32 | 37, of 1 28 | 27, 8192 x 1024 32 | 30, 16384
-// x 4096 164 | 154).
+// x 4096 164 | 154 before its copies began sooner).
 constexpr int FEW_ROWS = 4096;
 
-template <typename E, int SLAB>
+template <typename E, int SLAB, int CLUSTER>
 cudaError_t backward_w(const RecurArgs &a, cudaStream_t s) {
-  return a.T <= FEW_ROWS ? backward_s<E, SLAB, 4>(a, s) : backward_s<E, SLAB, 8>(a, s);
+  return a.T <= FEW_ROWS ? backward_s<E, SLAB, 4, CLUSTER>(a, s) : backward_s<E, SLAB, 8, CLUSTER>(a, s);
 }
 
 template <typename E>
 cudaError_t backward_t(const RecurArgs &a, cudaStream_t s) {
   if constexpr (sizeof(E) == 2)
-    if (wide(a.D) || (a.starts && a.B > MAX_SHORT_B)) return backward_w<E, 16>(a, s);
-  return backward_w<E, 8>(a, s);
+    if (wide(a.D) || (a.starts && a.B > MAX_SHORT_B))
+      return wider(a.D) ? backward_w<E, 16, 8>(a, s) : backward_w<E, 16, 16>(a, s);
+  return backward_w<E, 8, 16>(a, s);
 }
 
 }  // namespace
