@@ -1031,7 +1031,7 @@ struct BackwardWarp {
 };
 
 template <typename E, int SLAB, int S, int CLUSTER>
-__global__ void __launch_bounds__(32 * WARPS, S == 4 ? 3 : 2)
+__global__ void __launch_bounds__(32 * WARPS, S == 4 && sizeof(E) == 4 ? 3 : 2)
 recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, const __grid_constant__ Maps maps, RecurParams p) {
   pdl_begin();
   using G = Bwd<E, SLAB, S, CLUSTER>;
@@ -1067,8 +1067,9 @@ recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, c
   }
   w.carry = 0.f;
   if (C > 1) cluster_wait();
-  // (in bf16 a third body costs all of them registers: 16384 x 4096 142 us, with it 154)
-  constexpr bool EASY = sizeof(E) == 4;
+  // (with 8 rows of bf16 a third body costs all of them registers: 16384 x 4096 142 us, with
+  // it 154)
+  constexpr bool EASY = sizeof(E) == 4 || S == 4;
   Tile t;
   float2 c[G::S][N / 2], e[G::S][N / 2];
   for (int i = 0; i < count; ++i) {
@@ -1267,15 +1268,17 @@ cudaError_t backward_s(const RecurArgs &a, cudaStream_t s) {
 }
 
 
-// Tiles of 4 rows a group leave registers for a third CTA, and a call of few rounds has
-// more CTAs at work; those of 8 have fewer rounds, each of a fixed cost (us, 4 | 8: 64 x 128
-// fp32 6.4 | 8.4, 4096 x 2048 of 9 sequences 32 | 37, of 1 28 | 27, 8192 x 1024 32 | 30, 16384
-// x 4096 164 | 154 before its copies began sooner).
-constexpr int FEW_ROWS = 4096;
+// Tiles of 4 rows a group: a call of few rows has more CTAs at work, and easy tiles have
+// their registers.  Those of 8 have fewer rounds, each of a fixed cost (us, 4 | 8: 64 x 128
+// fp32 5.4 | 8.4, 4096 x 2048 of 9 sequences 32 | 37, of 1 28 | 27; 16384 x 2048 of 1 sequence
+// 89 | 76, of 9 97 | 91, of 17 101 | 105, of 65 123 | 155, of 257 149 | 150; 8 channels a warp,
+// 16384 x 128 of 50 34 | 31, 16384 x 512 of 65 fp32 73 | 59).
+constexpr int FEW_ROWS = 4096, SHORT = 1024;
 
 template <typename E, int SLAB, int CLUSTER>
 cudaError_t backward_w(const RecurArgs &a, cudaStream_t s) {
-  return a.T <= FEW_ROWS ? backward_s<E, SLAB, 4, CLUSTER>(a, s) : backward_s<E, SLAB, 8, CLUSTER>(a, s);
+  const bool four = a.T <= FEW_ROWS || (SLAB == 16 && a.T / a.B < SHORT);
+  return four ? backward_s<E, SLAB, 4, CLUSTER>(a, s) : backward_s<E, SLAB, 8, CLUSTER>(a, s);
 }
 
 template <typename E>

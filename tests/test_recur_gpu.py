@@ -146,7 +146,8 @@ def test_packed(T, D, starts, dtype):
                                         (519, 1672, ragged(519, 9, 3)), (1285, 1536, [0, 700, 1285]),
                                         (4099, 264, ragged(4099, 30, 4)), (2309, 1280, [0, 2309]),
                                         (700, 2504, ragged(700, 40, 6)), (4261, 1544, [1, 2000, 4260]),
-                                        (4261, 2504, ragged(4261, 20, 7)), (9000, 16, ragged(9000, 60, 8))])
+                                        (4261, 2504, ragged(4261, 20, 7)), (4205, 2504, [0, 1500, 4203]),
+                                        (9000, 16, ragged(9000, 60, 8))])
 def test_packed_over_many_rounds(T, D, starts, dtype):
     """Lengths that cut a group of rows in two, widths that cut a warp's channels, several
     tiles a CTA."""
