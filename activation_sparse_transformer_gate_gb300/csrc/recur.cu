@@ -3,11 +3,15 @@
 //   a = sigmoid(gate + bias), c = 1 - a,  h_t = h_{t-1} + c_t (x_t - h_{t-1})
 //   G_t = dh_t + a_{t+1} G_{t+1},  dx = c G,  dgate = G (h_{t-1} - x) a c
 //
-// A row's step is the map h -> (1 - C) h + H; maps compose,
-//   (C2, H2) after (C1, H1) = (C1 + C2 - C1 C2, H2 + H1 - C2 H1),
-// so time can be cut up.  The share that is taken, C, is kept instead of the one
-// that stays: where little is taken at each of many rows, 1 - C would lose it to
-// rounding.  A sequence's first row forgets what stood before it ("cut").
+// A row's step is the map h -> A h + H; maps compose,
+//   (A2, H2) after (A1, H1) = (A1 A2, H2 + A2 H1),
+// so time can be cut up.  Of the share that stays, A, and the one that is taken, 1 - A, the
+// smaller is kept: where little is taken at each of many rows, A would lose it to rounding;
+// where a gate closes behind a large state, 1 - A would leave that state's rounding in the
+// place of what stays of it.  A row's own gate likewise: it goes by c, of which h + c (x - h)
+// is one fma, and by a below 2^-6, from where on 1 - c has not the bits that a needs; only
+// tiles with such a gate look for it.  A sequence's first row forgets what stood before it
+// ("cut").
 //
 // To read each value once without a wait of CTA on CTA through memory, a cluster of
 // up to 16 CTAs owns a slab of channels and goes through all rows in rounds.  A warp
@@ -59,7 +63,8 @@ namespace {
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr int FEW = 128;            // entries of starts that a CTA keeps at hand
-constexpr float CUT = 2.f;          // a C that stands for: nothing comes through
+constexpr float CUT = 2.f;          // an m, or A, that stands for: nothing comes through
+constexpr float NOTHING = -0.f;     // the m of a step that takes nothing
 
 struct RecurParams {
   const int32_t *starts;
@@ -90,13 +95,21 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
 __device__ __forceinline__ float2 less2(float2 a, float2 b) { return fma2(b, both(-1.f), a); }  // a - b
 
-// exp(f), and -c = -1 / (1 + exp(f)) from it, to a few units of its own last place on
-// either side (0 where exp(f) has overflowed).
-__device__ __forceinline__ float2 exp2_of(float2 t) { return make_float2(ex2_approx(t.x), ex2_approx(t.y)); }
-__device__ __forceinline__ float2 minus_c(float2 e) {
+// A gate as m: -c, or below t = OPEN a, to a few units of its own last place on either side
+// (-0: all stays; 0: nothing does).  From OPEN on c's 3 units are 2^-16 of a at most.  What a
+// gate gives does not depend on what else is in its tile.
+constexpr float OPEN = -6.f;
+template <bool CLOSED>
+__device__ __forceinline__ float2 gate_of(float2 t, float2 e) {  // t = f log2(e), e = exp(f)
   const float2 u = fma2(e, both(-1.f), both(-1.f));
-  return make_float2(rcp_approx(u.x), rcp_approx(u.y));
+  float2 m = make_float2(rcp_approx(u.x), rcp_approx(u.y));
+  if (CLOSED) {
+    if (t.x < OPEN) m.x = e.x * -m.x;
+    if (t.y < OPEN) m.y = e.y * -m.y;
+  }
+  return m;
 }
+__device__ __forceinline__ float2 exp2_of(float2 t) { return make_float2(ex2_approx(t.x), ex2_approx(t.y)); }
 // exp(f) held below 2^127.5, where c has been flushed to 0 and e c is a number.
 __device__ __forceinline__ float2 exp2_held(float2 t) {
   float2 m;
@@ -104,9 +117,49 @@ __device__ __forceinline__ float2 exp2_held(float2 t) {
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(m.y) : "f"(t.y), "f"(127.5f));
   return exp2_of(m);
 }
-// h + c (x - h), and the share taken after c more is.
-__device__ __forceinline__ float2 row_step(float2 mc, float2 x, float2 h) { return fma2(mc, less2(h, x), h); }
-__device__ __forceinline__ float2 share(float2 mc, float2 C) { return fma2(mc, add2(C, both(-1.f)), C); }
+// a c, where a = e c has all its bits.
+template <bool CLOSED>
+__device__ __forceinline__ float2 both_shares(float2 t, float2 e, float2 m) {
+  float2 r = mul2(mul2(e, m), m);
+  if (CLOSED) {
+    if (t.x < OPEN) r.x = fmaf(-m.x, m.x, m.x);
+    if (t.y < OPEN) r.y = fmaf(-m.y, m.y, m.y);
+  }
+  return r;
+}
+__device__ __forceinline__ bool is_c(float m) { return __float_as_int(m) < 0; }
+// a where m is -c, else b.
+__device__ __forceinline__ float2 pick(float2 m, float2 a, float2 b) {
+  return make_float2(is_c(m.x) ? a.x : b.x, is_c(m.y) ? a.y : b.y);
+}
+// a v, and -c v (CLOSED: m may be either share, else it is -c).
+template <bool CLOSED>
+__device__ __forceinline__ float2 kept(float2 m, float2 v) {
+  return fma2(m, v, CLOSED ? pick(m, v, both(0.f)) : v);
+}
+template <bool CLOSED>
+__device__ __forceinline__ float2 minus_taken(float2 m, float2 v) {
+  return CLOSED ? fma2(m, v, pick(m, both(-0.f), make_float2(-v.x, -v.y))) : mul2(m, v);
+}
+// h + c (x - h), or x + a (h - x); off = h - x.
+template <bool CLOSED>
+__device__ __forceinline__ float2 row_step(float2 m, float2 x, float2 h, float2 off) {
+  return fma2(m, off, CLOSED ? pick(m, h, x) : h);
+}
+// The lower of two gates, in each place of 16 bytes.
+__device__ __forceinline__ uint32_t lower2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmin2(*(const __nv_bfloat162 *)&a, *(const __nv_bfloat162 *)&b);
+  return *(const uint32_t *)&r;
+}
+__device__ __forceinline__ uint4 lower(const uint4 &a, const uint4 &b, bf16 *) {
+  return make_uint4(lower2(a.x, b.x), lower2(a.y, b.y), lower2(a.z, b.z), lower2(a.w, b.w));
+}
+__device__ __forceinline__ uint32_t lower1(uint32_t a, uint32_t b) {
+  return __float_as_uint(fminf(__uint_as_float(a), __uint_as_float(b)));
+}
+__device__ __forceinline__ uint4 lower(const uint4 &a, const uint4 &b, float *) {
+  return make_uint4(lower1(a.x, b.x), lower1(a.y, b.y), lower1(a.z, b.z), lower1(a.w, b.w));
+}
 
 // 16 bytes of a row as pairs, and back (SIGN: negated).
 __device__ __forceinline__ void pairs(const uint4 &u, float2 (&f)[4], bf16 *) {
@@ -130,19 +183,37 @@ __device__ __forceinline__ uint4 packed(const float2 (&f)[2], float *) {
                     __float_as_uint(f[1].x) ^ s, __float_as_uint(f[1].y) ^ s);
 }
 
-// What a step (C, H) makes of h.  CLEAN: where no step is cut.
+// What a step stands as in the scan over a tile's groups: m, as a gate does, where the tile's
+// own step is asked for (the products of one tile after the other are long); A where it ends
+// with the tile.
+enum Share { AS_M, AS_A };
+// The share that stays (CUT: CUT).
+template <Share AS = AS_M>
+__device__ __forceinline__ float stays(float v) { return AS == AS_M && is_c(v) ? 1.f + v : v; }
+// The m of a share that stays, n: minus what is taken.
+__device__ __forceinline__ float smaller(float A, float n) { return A > 0.75f ? n : A; }
+// What a step (A, H) makes of h.  CLEAN: where no step is cut.
 template <bool CLEAN = false>
-__device__ __forceinline__ float apply(float C, float H, float h) {
-  const float r = fmaf(-C, h, h) + H;
-  return !CLEAN && C == CUT ? H : r;
+__device__ __forceinline__ float apply(float A, float H, float h) {
+  const float r = fmaf(A, h, H);
+  return !CLEAN && A == CUT ? H : r;
 }
-// (C, H) := (C2, H2) after it.
-template <bool CLEAN>
-__device__ __forceinline__ void then(float &C, float &H, float C2, float H2) {
-  H = apply<CLEAN>(C2, H2, H);
-  const float r = fmaf(-C, C2, C) + C2;
-  C = !CLEAN && (C == CUT || C2 == CUT) ? CUT : r;
-}
+// Steps on the way to one: A is what stays, n minus what is taken, each to its own last
+// place; n only where all of them are -c (it is asked for where little is taken).
+template <Share AS, bool CLEAN>
+struct Joint {
+  float A, n, H;
+  __device__ __forceinline__ Joint(float v, float H_) : A(stays<AS>(v)), n(v), H(H_) {}
+  // (v, H) after it
+  __device__ __forceinline__ void then(float v, float H2) {
+    const float A2 = stays<AS>(v);
+    H = apply<CLEAN>(A2, H2, H);
+    const bool cut = !CLEAN && (A == CUT || A2 == CUT);
+    n = cut ? CUT : fmaf(v, A, n);
+    A = cut ? CUT : A2 * A;
+  }
+  __device__ __forceinline__ float v() const { return AS == AS_M ? smaller(A, n) : A; }
+};
 
 // A warp's slab: 16 channels, or 8 (16 or 32 bytes of a row), as CX lanes across; GROUPS
 // of lanes take S rows of a tile each.  In the scan over the groups a channel has PARTS
@@ -396,9 +467,9 @@ __device__ __forceinline__ void fetch_rest(Slot<G> &slot, const E *src, long lon
 // What a lane keeps of it between its halves: the step of the parts before its own,
 // and the tile's.
 struct Scan {
-  float C, H, tileC, tileH;
+  float A, H, tileA, tileH;
 };
-template <typename G, bool BACK, bool CLEAN>
+template <typename G, Share AS, bool BACK, bool CLEAN>
 __device__ __forceinline__ Scan scan_up(const float2 *steps) {
   constexpr int N = G::N, P = G::PARTS, W = G::ACROSS;
   constexpr uint32_t FULL = 0xFFFFFFFFu;
@@ -406,47 +477,52 @@ __device__ __forceinline__ Scan scan_up(const float2 *steps) {
   float2 v[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) v[j] = steps[G::at(part * N + j, ch)];
-  float C = v[BACK ? N - 1 : 0].x, H = v[BACK ? N - 1 : 0].y;
+  Joint<AS, CLEAN> own(v[BACK ? N - 1 : 0].x, v[BACK ? N - 1 : 0].y);
 #pragma unroll
   for (int k = 1; k < N; ++k) {
     const int j = BACK ? N - 1 - k : k;
-    then<CLEAN>(C, H, v[j].x, v[j].y);
+    own.then(v[j].x, v[j].y);
   }
+  float share = own.v(), H = own.H;
   const int behind = BACK ? P - 1 - part : part;  // parts that come before this one
 #pragma unroll
   for (int o = 1; o < P; o *= 2) {
-    float C1 = BACK ? __shfl_down_sync(FULL, C, o * W) : __shfl_up_sync(FULL, C, o * W);
-    float H1 = BACK ? __shfl_down_sync(FULL, H, o * W) : __shfl_up_sync(FULL, H, o * W);
+    const float v1 = BACK ? __shfl_down_sync(FULL, share, o * W) : __shfl_up_sync(FULL, share, o * W);
+    const float H1 = BACK ? __shfl_down_sync(FULL, H, o * W) : __shfl_up_sync(FULL, H, o * W);
     if (behind >= o) {
-      then<CLEAN>(C1, H1, C, H);
-      C = C1;
-      H = H1;
+      Joint<AS, CLEAN> two(v1, H1);
+      two.then(share, H);
+      share = two.v();
+      H = two.H;
     }
   }
   const int whole = (BACK ? 0 : 32 - W) + lane % W;  // the lane that has the tile's step
   Scan s;
-  s.tileC = __shfl_sync(FULL, C, whole);
+  s.tileA = stays<AS>(__shfl_sync(FULL, share, whole));
   s.tileH = __shfl_sync(FULL, H, whole);
-  s.C = BACK ? __shfl_down_sync(FULL, C, W) : __shfl_up_sync(FULL, C, W);
+  s.A = stays<AS>(BACK ? __shfl_down_sync(FULL, share, W) : __shfl_up_sync(FULL, share, W));
   s.H = BACK ? __shfl_down_sync(FULL, H, W) : __shfl_up_sync(FULL, H, W);
-  if (behind == 0) s.C = s.H = 0.f;
+  if (behind == 0) {
+    s.A = 1.f;
+    s.H = 0.f;
+  }
   return s;
 }
 // Replaces each group's step by the value that reaches the group, from the one that
 // reaches the tile.
-template <typename G, bool BACK, bool CLEAN>
+template <typename G, Share AS, bool BACK, bool CLEAN>
 __device__ __forceinline__ void scan_down(float2 *steps, const Scan &s, float h) {
   constexpr int N = G::N, W = G::ACROSS;
   const int lane = threadIdx.x & 31, part = lane / W, ch = lane % W;
   float2 v[N];  // (all read before any is written: the compiler would keep the order)
 #pragma unroll
   for (int j = 0; j < N; ++j) v[j] = steps[G::at(part * N + j, ch)];
-  h = apply<CLEAN>(s.C, s.H, h);
+  h = apply<CLEAN>(s.A, s.H, h);
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     const int j = BACK ? N - 1 - k : k;
     steps[G::at(part * N + j, ch)].x = h;
-    h = apply<CLEAN>(v[j].x, v[j].y, h);
+    h = apply<CLEAN>(stays<AS>(v[j].x), v[j].y, h);
   }
 }
 
@@ -457,7 +533,7 @@ __device__ __forceinline__ void scan_down(float2 *steps, const Scan &s, float h)
 constexpr int ROOM = 2;
 template <typename G>
 struct Exchange {
-  float2 total[ROOM][G::CLUSTER][G::SLAB];  // (0, 0) for CTAs that the cluster does not have
+  float2 total[ROOM][G::CLUSTER][G::SLAB];  // (1, 0) for CTAs that the cluster does not have
   uint64_t bar[ROOM];
 };
 
@@ -497,7 +573,7 @@ __device__ __forceinline__ void send_step(Exchange<G> &x, int n, int rank, int i
     asm volatile(
         "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
             peer(mine, r)),
-        "f"(s.tileC), "f"(s.tileH), "r"(peer(bar, r))
+        "f"(s.tileA), "f"(s.tileH), "r"(peer(bar, r))
         : "memory");
 }
 
@@ -509,7 +585,7 @@ __device__ __forceinline__ float receive_steps(Exchange<G> &x, int n, int rank, 
                                                float &carry, bool &lost, int32_t *status) {
   if (n == 1) {
     const float in = carry;
-    carry = apply(s.tileC, s.tileH, carry);
+    carry = apply(s.tileA, s.tileH, carry);
     return in;
   }
   if (!lost) {
@@ -538,7 +614,7 @@ __device__ __forceinline__ float receive_steps(Exchange<G> &x, int n, int rank, 
 template <typename G>
 __device__ __forceinline__ void open_exchange(Exchange<G> &x, int C) {
   const int lane = threadIdx.x & 31;
-  for (int k = lane; k < ROOM * G::CLUSTER * G::SLAB; k += 32) (&x.total[0][0][0])[k] = make_float2(0.f, 0.f);
+  for (int k = lane; k < ROOM * G::CLUSTER * G::SLAB; k += 32) (&x.total[0][0][0])[k] = make_float2(1.f, 0.f);
   if (lane < ROOM) mbar_init(smem_u32(&x.bar[lane]), 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __syncwarp();
@@ -556,15 +632,26 @@ struct Rounds {
 };
 
 // What can be in a warp's tile: no sequence begins or ends there and all of its rows are
-// some sequence's; one at most begins and one ends in each lane's rows, and all are some
-// sequence's; anything.  Branches at the rows keep the rows' arithmetic from overlapping
-// (16384 x 2048 of 9 sequences forward 55 us, of 257 80), so what is easy has a selection
-// a row instead (50 and 72).
-enum Kind { PLAIN_TILE, EASY_TILE, ANY_TILE };
+// some sequence's (PLAIN); one at most begins and one ends in each lane's rows, and all are
+// some sequence's (EASY); anything; no row of a sequence (DEAD).  Branches at the rows keep the
+// rows' arithmetic from overlapping (16384 x 2048 of 9 sequences forward 55 us, of 257 80), so
+// what is easy has a selection a row instead (50 and 72).  With a gate below OPEN, which shows
+// when the gates are read, a tile begins again as CLOSED: two or three selections a value.  Its
+// rows are a loop that is hardly unrolled, with the gates in local memory: one more unrolled
+// body slows the others down (16384 x 4096 backward 152 us, else 164; with closed gates in
+// every tile 317, else 378; forward 82 and 136, else 88 and 180).
+enum Kind { PLAIN_TILE, PLAIN_CLOSED, EASY_TILE, ANY_TILE, ANY_CLOSED, DEAD_TILE };
+template <int S>
+constexpr int unroll_of(int kind) {
+  return kind == PLAIN_CLOSED ? 2 : kind == ANY_CLOSED ? 1 : S;
+}
 template <typename G>
 __device__ __forceinline__ int kind_of(const RowBits &b) {
+  if (!__any_sync(0xFFFFFFFFu, b.live != 0)) return DEAD_TILE;
   const uint32_t more = (b.first & (b.first - 1)) | (b.last & (b.last - 1));
-  return b.live != G::ALL || more != 0 ? ANY_TILE : (b.first | b.last) != 0 ? EASY_TILE : PLAIN_TILE;
+  return __reduce_max_sync(0xFFFFFFFFu, b.live != G::ALL || more != 0 ? ANY_TILE
+                                        : (b.first | b.last) != 0    ? EASY_TILE
+                                                                     : PLAIN_TILE);
 }
 // The last row of those marked (-1: none).
 __device__ __forceinline__ int last_row(uint32_t bits) { return 31 - __clz(bits); }
@@ -662,51 +749,87 @@ struct ForwardWarp {
     }
   }
   // The first half of tile i: its rows as one step a lane, scanned and sent.
+  // Returns false, with nothing sent, where it finds a closed gate.
   template <int KIND>
-  __device__ __forceinline__ void first_half(int i, Tile &t, float2 (&mc)[S][M]) {
-    float2 Cs[M], Hs[M];
+  __device__ __forceinline__ bool first_half(int i, Tile &t, float2 (&m)[S][M]) {
+    constexpr bool CLOSED = KIND == PLAIN_CLOSED || KIND == ANY_CLOSED;
+    constexpr int UNROLL = unroll_of<S>(KIND);
+    uint4 lowest;
+    float2 As[M], ns[M], Hs[M];  // the rows so far, see Joint
 #pragma unroll
-    for (int n = 0; n < M; ++n) Cs[n] = Hs[n] = both(0.f);
+    for (int n = 0; n < M; ++n) {
+      As[n] = both(1.f);
+      ns[n] = both(NOTHING);
+      Hs[n] = both(0.f);
+    }
     float2 start[M] = {};
     const int begin = KIND == EASY_TILE ? last_row(t.bits.first) : -1;
     if (KIND == EASY_TILE && begin >= 0) {
       load_state(on ? p.h0 : nullptr, first_of(p, sh.marks, t.r0, q * S + begin), p.D, d, start);
       hold(start);
     }
-#pragma unroll
+#pragma unroll UNROLL
     for (int k = 0; k < S; ++k) {
       if (KIND == EASY_TILE) select(Hs, start, k == begin);
-      if (KIND == ANY_TILE && (t.bits.any_first >> k & 1) && (t.bits.first >> k & 1)) {
+      if (KIND >= ANY_TILE && (t.bits.any_first >> k & 1) && (t.bits.first >> k & 1)) {
         load_state(on ? p.h0 : nullptr, first_of(p, sh.marks, t.r0, q * S + k), p.D, d, Hs);
         hold(Hs);
       }
       float2 xv[M], gv[M];
       pairs(cta.x[i & 1].v[slot(k)], xv, (E *)nullptr);
-      pairs(cta.gate.v[slot(k)], gv, (E *)nullptr);
+      const uint4 gates = cta.gate.v[slot(k)];
+      if (!CLOSED) lowest = k == 0 ? gates : lower(lowest, gates, (E *)nullptr);
+      pairs(gates, gv, (E *)nullptr);
 #pragma unroll
       for (int n = 0; n < M; ++n) {
-        mc[k][n] = minus_c(exp2_of(fma2(gv[n], both(LOG2E), bias[n])));
-        Hs[n] = row_step(mc[k][n], xv[n], Hs[n]);
-        Cs[n] = share(mc[k][n], Cs[n]);
+        const float2 g = fma2(gv[n], both(LOG2E), bias[n]);
+        m[k][n] = gate_of<CLOSED>(g, exp2_of(g));
+        Hs[n] = row_step<CLOSED>(m[k][n], xv[n], Hs[n], less2(Hs[n], xv[n]));
+        ns[n] = fma2(m[k][n], As[n], ns[n]);
+        As[n] = kept<CLOSED>(m[k][n], As[n]);
       }
+    }
+    if (!CLOSED) {
+      float2 gv[M];
+      pairs(lowest, gv, (E *)nullptr);
+      bool closed = false;
+#pragma unroll
+      for (int n = 0; n < M; ++n) {
+        const float2 t = fma2(gv[n], both(LOG2E), bias[n]);
+        closed |= fminf(t.x, t.y) < OPEN;
+      }
+      if (__any_sync(0xFFFFFFFFu, closed)) return false;
     }
     cta_barrier();  // (all warps are done with the gates, and with tile i - 1)
     fetch_tile(i + 1);
-    const bool cut = KIND != PLAIN_TILE && (t.bits.first != 0 || t.bits.live != G::ALL);
+    const bool cut = KIND > PLAIN_CLOSED && (t.bits.first != 0 || t.bits.live != G::ALL);
 #pragma unroll
     for (int n = 0; n < M; ++n) {
-      sh.steps[G::at(q, 2 * n * CX + cx)] = make_float2(cut ? CUT : Cs[n].x, Hs[n].x);
-      sh.steps[G::at(q, (2 * n + 1) * CX + cx)] = make_float2(cut ? CUT : Cs[n].y, Hs[n].y);
+      const float2 all = make_float2(smaller(As[n].x, ns[n].x), smaller(As[n].y, ns[n].y));
+      sh.steps[G::at(q, 2 * n * CX + cx)] = make_float2(cut ? CUT : all.x, Hs[n].x);
+      sh.steps[G::at(q, (2 * n + 1) * CX + cx)] = make_float2(cut ? CUT : all.y, Hs[n].y);
     }
     __syncwarp();
-    t.scan = scan_up<G, false, KIND == PLAIN_TILE>(sh.steps);
+    t.scan = scan_up<G, AS_M, false, KIND <= PLAIN_CLOSED>(sh.steps);
     send_step<G>(sh.exchange, C, rank, i, t.scan, lost);
+    return true;
+  }
+  // A tile without a row of any sequence.
+  __device__ __forceinline__ void skip(int i, Tile &t) {
+    cta_barrier();
+    fetch_tile(i + 1);
+    t.scan.tileA = CUT;
+    t.scan.tileH = 0.f;
+    send_step<G>(sh.exchange, C, rank, i, t.scan, lost);
+    receive_steps<G, false>(sh.exchange, C, rank, i, t.scan, carry, lost, p.status);
   }
   // The second half: the rows once more, from the state before them.
   template <int KIND>
-  __device__ __forceinline__ void second_half(int i, const Tile &t, const float2 (&mc)[S][M]) {
+  __device__ __forceinline__ void second_half(int i, const Tile &t, const float2 (&m)[S][M]) {
+    constexpr bool CLOSED = KIND == PLAIN_CLOSED || KIND == ANY_CLOSED;
+    constexpr int UNROLL = unroll_of<S>(KIND);
     const float in = receive_steps<G, false>(sh.exchange, C, rank, i, t.scan, carry, lost, p.status);
-    scan_down<G, false, KIND == PLAIN_TILE>(sh.steps, t.scan, in);
+    scan_down<G, AS_M, false, KIND <= PLAIN_CLOSED>(sh.steps, t.scan, in);
     __syncwarp();
     float2 y[M];
 #pragma unroll
@@ -722,23 +845,23 @@ struct ForwardWarp {
     const int begin = KIND == EASY_TILE ? last_row(t.bits.first) : -1;
     const int end = KIND == EASY_TILE ? last_row(t.bits.last) : -1;
     if (KIND == EASY_TILE) held(start);
-    uint4 rows[S];  // (read before the first store, which the reads could not pass)
+    uint4 rows[CLOSED ? 1 : S];  // (read before the first store, which the reads could not pass)
 #pragma unroll
-    for (int k = 0; k < S; ++k) rows[k] = cta.x[i & 1].v[slot(k)];
-#pragma unroll
+    for (int k = 0; !CLOSED && k < S; ++k) rows[CLOSED ? 0 : k] = cta.x[i & 1].v[slot(k)];
+#pragma unroll UNROLL
     for (int k = 0; k < S; ++k, out += p.D) {
       float2 xv[M];
-      pairs(rows[k], xv, (E *)nullptr);
+      pairs(CLOSED ? cta.x[i & 1].v[slot(k)] : rows[CLOSED ? 0 : k], xv, (E *)nullptr);
       if (KIND == EASY_TILE) select(y, start, k == begin);
-      if (KIND == ANY_TILE && (t.bits.any_first >> k & 1)) {
+      if (KIND >= ANY_TILE && (t.bits.any_first >> k & 1)) {
         if (t.bits.first >> k == 1) held(y);
         else if (t.bits.first >> k & 1) load_state(p.h0, first_of(p, sh.marks, t.r0, q * S + k), p.D, d, y);
       }
 #pragma unroll
-      for (int n = 0; n < M; ++n) y[n] = row_step(mc[k][n], xv[n], y[n]);
-      if (KIND != ANY_TILE || (t.bits.live >> k & 1)) *(uint4 *)out = packed(y, (E *)nullptr);
+      for (int n = 0; n < M; ++n) y[n] = row_step<CLOSED>(m[k][n], xv[n], y[n], less2(y[n], xv[n]));
+      if (KIND < ANY_TILE || (t.bits.live >> k & 1)) *(uint4 *)out = packed(y, (E *)nullptr);
       if (KIND == EASY_TILE) select(behind, y, k == end);
-      if (KIND == ANY_TILE && (t.bits.any_last >> k & 1) && (t.bits.last >> k & 1) && p.hT)
+      if (KIND >= ANY_TILE && (t.bits.any_last >> k & 1) && (t.bits.last >> k & 1) && p.hT)
         store_state(p.hT, last_of(p, sh.marks, t.r0, q * S + k), p.D, d, y);
     }
     if (KIND == EASY_TILE && end >= 0 && p.hT)
@@ -747,7 +870,7 @@ struct ForwardWarp {
 };
 
 template <typename E, int SLAB, int CLUSTER>
-__global__ void __launch_bounds__(32 * WARPS, CLUSTER == 8 ? 3 : 2)
+__global__ void __launch_bounds__(32 * WARPS, CLUSTER == 8 || sizeof(E) == 4 ? 3 : 2)
 recur_forward_kernel(const E *x, const E *gate, E *h, const __grid_constant__ Maps maps, RecurParams p) {
   pdl_begin();
   using G = Fwd<E, SLAB, CLUSTER>;
@@ -781,20 +904,29 @@ recur_forward_kernel(const E *x, const E *gate, E *h, const __grid_constant__ Ma
   for (int i = 0; i < count; ++i) {
     t.r0 = rounds.row(i, p.T);
     t.kind = PLAIN_TILE;
+    t.bits = RowBits{0, 0, G::ALL, 0, 0};
     if (!plain_tile<G::R>(p, w.gap, t.r0, lo, hi)) {
       t.bits = row_bits(p, starts, sh.marks, w.gap, t.r0, q, w.live_of(i));
-      t.kind = __reduce_max_sync(0xFFFFFFFFu, kind_of<G>(t.bits));
+      t.kind = kind_of<G>(t.bits);
     }
     w.wait_tile(i);
-    if (t.kind == PLAIN_TILE) {
-      w.template first_half<PLAIN_TILE>(i, t, c);
+    if (t.kind == PLAIN_TILE && w.template first_half<PLAIN_TILE>(i, t, c)) {
       w.template second_half<PLAIN_TILE>(i, t, c);
-    } else if (t.kind == EASY_TILE) {
-      w.template first_half<EASY_TILE>(i, t, c);
+    } else if (t.kind == EASY_TILE && w.template first_half<EASY_TILE>(i, t, c)) {
       w.template second_half<EASY_TILE>(i, t, c);
-    } else {
-      w.template first_half<ANY_TILE>(i, t, c);
+    } else if (t.kind == ANY_TILE && w.template first_half<ANY_TILE>(i, t, c)) {
       w.template second_half<ANY_TILE>(i, t, c);
+    } else if (t.kind == DEAD_TILE) {
+      w.skip(i, t);
+    } else {
+      float2 cc[G::S][G::N / 2];
+      if (t.kind == PLAIN_TILE) {
+        w.template first_half<PLAIN_CLOSED>(i, t, cc);
+        w.template second_half<PLAIN_CLOSED>(i, t, cc);
+      } else {
+        w.template first_half<ANY_CLOSED>(i, t, cc);
+        w.template second_half<ANY_CLOSED>(i, t, cc);
+      }
     }
   }
   // (nothing is on its way to this CTA any more, unless a wait has given up)
@@ -887,12 +1019,19 @@ struct BackwardWarp {
     return sd < p.D && r0 > 0 && r0 < p.T ? p.states[(size_t)(r0 / RECUR_KEEP) * p.D + sd] : 0.f;
   }
   // The first half of tile i: its rows as one step forward and one back; h within the
-  // tile needs no other, and of the gates there stay -c and e := (h_{t-1} - x_t) a c.
+  // tile needs no other, and of the gates there stay m and e := (h_{t-1} - x_t) a c.
   template <int KIND>
-  __device__ __forceinline__ void first_half(int i, Tile &t, float2 (&e)[S][M], float2 (&mc)[S][M]) {
-    float2 Cs[M], Hs[M];
+  __device__ __forceinline__ bool first_half(int i, Tile &t, float2 (&e)[S][M], float2 (&m)[S][M]) {
+    constexpr bool CLOSED = KIND == PLAIN_CLOSED || KIND == ANY_CLOSED;
+    constexpr int UNROLL = unroll_of<S>(KIND);
+    uint4 lowest;
+    float2 As[M], ns[M], Hs[M];  // the rows so far, see Joint
 #pragma unroll
-    for (int n = 0; n < M; ++n) Cs[n] = Hs[n] = both(0.f);
+    for (int n = 0; n < M; ++n) {
+      As[n] = both(1.f);
+      ns[n] = both(NOTHING);
+      Hs[n] = both(0.f);
+    }
     float2 start[M] = {};
     const int begin = KIND == EASY_TILE ? last_row(t.bits.first) : -1;
     const int end = KIND == EASY_TILE ? last_row(t.bits.last) : -1;
@@ -901,57 +1040,73 @@ struct BackwardWarp {
         load_state(on ? p.h0 : nullptr, first_of(p, sh.marks, t.r0, q * S + begin), p.D, d, v);
     };
     at_begin(start);
-#pragma unroll
+#pragma unroll UNROLL
     for (int k = 0; k < S; ++k) {
       if (KIND == EASY_TILE) select(Hs, start, k == begin);
-      if (KIND == ANY_TILE && (t.bits.any_first >> k & 1) && (t.bits.first >> k & 1))
+      if (KIND >= ANY_TILE && (t.bits.any_first >> k & 1) && (t.bits.first >> k & 1))
         load_state(on ? p.h0 : nullptr, first_of(p, sh.marks, t.r0, q * S + k), p.D, d, Hs);
       float2 xv[M], gv[M];
       pairs(cta.x[i % XS].v[slot(k)], xv, (E *)nullptr);
-      pairs(cta.gate.v[slot(k)], gv, (E *)nullptr);
+      const uint4 gates = cta.gate.v[slot(k)];
+      if (!CLOSED) lowest = k == 0 ? gates : lower(lowest, gates, (E *)nullptr);
+      pairs(gates, gv, (E *)nullptr);
 #pragma unroll
       for (int n = 0; n < M; ++n) {
-        e[k][n] = exp2_held(fma2(gv[n], both(LOG2E), bias[n]));
-        mc[k][n] = minus_c(e[k][n]);
-        Hs[n] = row_step(mc[k][n], xv[n], Hs[n]);
-        Cs[n] = share(mc[k][n], Cs[n]);
+        const float2 g = fma2(gv[n], both(LOG2E), bias[n]), eg = exp2_held(g);
+        m[k][n] = gate_of<CLOSED>(g, eg);
+        e[k][n] = both_shares<CLOSED>(g, eg, m[k][n]);
+        Hs[n] = row_step<CLOSED>(m[k][n], xv[n], Hs[n], less2(Hs[n], xv[n]));
+        ns[n] = fma2(m[k][n], As[n], ns[n]);
+        As[n] = kept<CLOSED>(m[k][n], As[n]);
       }
+    }
+    if (!CLOSED) {
+      float2 gv[M];
+      pairs(lowest, gv, (E *)nullptr);
+      bool closed = false;
+#pragma unroll
+      for (int n = 0; n < M; ++n) {
+        const float2 t = fma2(gv[n], both(LOG2E), bias[n]);
+        closed |= fminf(t.x, t.y) < OPEN;
+      }
+      if (__any_sync(0xFFFFFFFFu, closed)) return false;
     }
     cta_barrier();  // (all warps are done with the gates, and with the last tile's dh)
     fetch_tile(i + 1);
-    const bool dead = KIND == ANY_TILE && t.bits.live != G::ALL;
-    const bool cutF = KIND != PLAIN_TILE && (dead || t.bits.first),
-               cutB = KIND != PLAIN_TILE && (dead || t.bits.last);
+    const bool dead = KIND >= ANY_TILE && t.bits.live != G::ALL;
+    const bool cutF = KIND > PLAIN_CLOSED && (dead || t.bits.first),
+               cutB = KIND > PLAIN_CLOSED && (dead || t.bits.last);
 #pragma unroll
     for (int n = 0; n < M; ++n) {
-      sh.stepsF[G::at(q, 2 * n * CX + cx)] = make_float2(cutF ? CUT : Cs[n].x, Hs[n].x);
-      sh.stepsF[G::at(q, (2 * n + 1) * CX + cx)] = make_float2(cutF ? CUT : Cs[n].y, Hs[n].y);
+      sh.stepsF[G::at(q, 2 * n * CX + cx)] = make_float2(cutF ? CUT : As[n].x, Hs[n].x);
+      sh.stepsF[G::at(q, (2 * n + 1) * CX + cx)] = make_float2(cutF ? CUT : As[n].y, Hs[n].y);
+      As[n] = make_float2(smaller(As[n].x, ns[n].x), smaller(As[n].y, ns[n].y));
       Hs[n] = both(0.f);
     }
     if (KIND == EASY_TILE && end >= 0)
       load_state(on ? p.dhT : nullptr, last_of(p, sh.marks, t.r0, q * S + end), p.D, d, start);
-#pragma unroll
+#pragma unroll UNROLL
     for (int k = S - 1; k >= 0; --k) {
       if (KIND == EASY_TILE) select(Hs, start, k == end);
-      if (KIND == ANY_TILE && (t.bits.any_last >> k & 1) && (t.bits.last >> k & 1))
+      if (KIND >= ANY_TILE && (t.bits.any_last >> k & 1) && (t.bits.last >> k & 1))
         load_state(on ? p.dhT : nullptr, last_of(p, sh.marks, t.r0, q * S + k), p.D, d, Hs);
       float2 dv[M];
       pairs(cta.dh[i & 1].v[slot(k)], dv, (E *)nullptr);
 #pragma unroll
       for (int n = 0; n < M; ++n) {
-        const float2 g = add2(dv[n], Hs[n]);
-        Hs[n] = fma2(mc[k][n], g, g);
+        Hs[n] = kept<CLOSED>(m[k][n], add2(dv[n], Hs[n]));
       }
     }
 #pragma unroll
     for (int n = 0; n < M; ++n) {
-      sh.stepsB[G::at(q, 2 * n * CX + cx)] = make_float2(cutB ? CUT : Cs[n].x, Hs[n].x);
-      sh.stepsB[G::at(q, (2 * n + 1) * CX + cx)] = make_float2(cutB ? CUT : Cs[n].y, Hs[n].y);
+      sh.stepsB[G::at(q, 2 * n * CX + cx)] = make_float2(cutB ? CUT : As[n].x, Hs[n].x);
+      sh.stepsB[G::at(q, (2 * n + 1) * CX + cx)] = make_float2(cutB ? CUT : As[n].y, Hs[n].y);
     }
     __syncwarp();
-    t.scan = scan_up<G, true, KIND == PLAIN_TILE>(sh.stepsB);
+    t.scan = scan_up<G, AS_M, true, KIND <= PLAIN_CLOSED>(sh.stepsB);
     send_step<G>(sh.exchange, C, rank, i, t.scan, lost);
-    scan_down<G, false, KIND == PLAIN_TILE>(sh.stepsF, scan_up<G, false, KIND == PLAIN_TILE>(sh.stepsF), before);
+    scan_down<G, AS_A, false, KIND <= PLAIN_CLOSED>(
+        sh.stepsF, scan_up<G, AS_A, false, KIND <= PLAIN_CLOSED>(sh.stepsF), before);
     before = state_before(i + 1);
     __syncwarp();
     float2 y[M];
@@ -959,31 +1114,45 @@ struct BackwardWarp {
     for (int n = 0; n < M; ++n)
       y[n] = make_float2(sh.stepsF[G::at(q, 2 * n * CX + cx)].x, sh.stepsF[G::at(q, (2 * n + 1) * CX + cx)].x);
     at_begin(start);
-#pragma unroll
+#pragma unroll UNROLL
     for (int k = 0; k < S; ++k) {
       if (KIND == EASY_TILE) select(y, start, k == begin);
-      if (KIND == ANY_TILE && (t.bits.any_first >> k & 1) && on && (t.bits.first >> k & 1))
+      if (KIND >= ANY_TILE && (t.bits.any_first >> k & 1) && on && (t.bits.first >> k & 1))
         load_state(p.h0, first_of(p, sh.marks, t.r0, q * S + k), p.D, d, y);
       float2 xv[M];
       pairs(cta.x[i % XS].v[slot(k)], xv, (E *)nullptr);
 #pragma unroll
       for (int n = 0; n < M; ++n) {
-        const float2 minus_took = mul2(less2(y[n], xv[n]), mc[k][n]);
-        y[n] = add2(y[n], minus_took);
-        e[k][n] = mul2(minus_took, mul2(e[k][n], mc[k][n]));
+        const float2 off = less2(y[n], xv[n]);
+        y[n] = row_step<CLOSED>(m[k][n], xv[n], y[n], off);
+        e[k][n] = mul2(off, e[k][n]);
       }
     }
     if constexpr (XS == 1) {
       cta_barrier();  // (all warps are done with x)
       fetch_x(i + 1);
     }
+    return true;
+  }
+  // A tile without a row of any sequence.
+  __device__ __forceinline__ void skip(int i, Tile &t) {
+    cta_barrier();
+    fetch_tile(i + 1);
+    if (XS == 1) fetch_x(i + 1);  // (which no warp reads here)
+    before = state_before(i + 1);
+    t.scan.tileA = CUT;
+    t.scan.tileH = 0.f;
+    send_step<G>(sh.exchange, C, rank, i, t.scan, lost);
+    receive_steps<G, true>(sh.exchange, C, rank, i, t.scan, carry, lost, p.status);
   }
   // The second half: G, from the last row on.
   template <int KIND>
   __device__ __forceinline__ void second_half(int i, const Tile &t, const float2 (&e)[S][M],
-                                              const float2 (&mc)[S][M]) {
+                                              const float2 (&m)[S][M]) {
+    constexpr bool CLOSED = KIND == PLAIN_CLOSED || KIND == ANY_CLOSED;
+    constexpr int UNROLL = unroll_of<S>(KIND);
     const float in = receive_steps<G, true>(sh.exchange, C, rank, i, t.scan, carry, lost, p.status);
-    scan_down<G, true, KIND == PLAIN_TILE>(sh.stepsB, t.scan, in);
+    scan_down<G, AS_M, true, KIND <= PLAIN_CLOSED>(sh.stepsB, t.scan, in);
     __syncwarp();
     float2 y[M];
 #pragma unroll
@@ -993,36 +1162,36 @@ struct BackwardWarp {
     if (!on) return;
     const int row = t.r0 + q * S;
     E *px = dx + (size_t)row * p.ld + d, *pg = dgate + (size_t)row * p.ld + d;
-    uint4 rows[S];
+    uint4 rows[CLOSED ? 1 : S];
 #pragma unroll
-    for (int k = 0; k < S; ++k) rows[k] = cta.dh[i & 1].v[slot(k)];
+    for (int k = 0; !CLOSED && k < S; ++k) rows[CLOSED ? 0 : k] = cta.dh[i & 1].v[slot(k)];
     float2 start[M] = {}, ahead[M] = {};
     const int begin = KIND == EASY_TILE ? last_row(t.bits.first) : -1;
     const int end = KIND == EASY_TILE ? last_row(t.bits.last) : -1;
     if (KIND == EASY_TILE && end >= 0)
       load_state(p.dhT, last_of(p, sh.marks, t.r0, q * S + end), p.D, d, start);
-#pragma unroll
+#pragma unroll UNROLL
     for (int k = S - 1; k >= 0; --k) {
       if (KIND == EASY_TILE) select(y, start, k == end);
-      if (KIND == ANY_TILE && (t.bits.any_last >> k & 1) && (t.bits.last >> k & 1))
+      if (KIND >= ANY_TILE && (t.bits.any_last >> k & 1) && (t.bits.last >> k & 1))
         load_state(p.dhT, last_of(p, sh.marks, t.r0, q * S + k), p.D, d, y);
-      const bool live = KIND != ANY_TILE || (t.bits.live >> k & 1);
+      const bool live = KIND < ANY_TILE || (t.bits.live >> k & 1);
       float2 dv[M], gv[M];
-      pairs(rows[k], dv, (E *)nullptr);
+      pairs(CLOSED ? cta.dh[i & 1].v[slot(k)] : rows[CLOSED ? 0 : k], dv, (E *)nullptr);
 #pragma unroll
       for (int n = 0; n < M; ++n) {
         const float2 g = add2(dv[n], y[n]);
         gv[n] = mul2(g, e[k][n]);
         if (live) db[n] = add2(db[n], gv[n]);
-        dv[n] = mul2(g, mc[k][n]);  // -dx
-        y[n] = add2(g, dv[n]);
+        dv[n] = minus_taken<CLOSED>(m[k][n], g);
+        y[n] = kept<CLOSED>(m[k][n], g);
       }
       if (live) {
         *(uint4 *)(px + k * p.ld) = packed<true>(dv, (E *)nullptr);
         *(uint4 *)(pg + k * p.ld) = packed(gv, (E *)nullptr);
       }
       if (KIND == EASY_TILE) select(ahead, y, k == begin);
-      if (KIND == ANY_TILE && (t.bits.any_first >> k & 1) && (t.bits.first >> k & 1) && p.dh0)
+      if (KIND >= ANY_TILE && (t.bits.any_first >> k & 1) && (t.bits.first >> k & 1) && p.dh0)
         store_state(p.dh0, first_of(p, sh.marks, t.r0, q * S + k), p.D, d, y);
     }
     if (KIND == EASY_TILE && begin >= 0 && p.dh0)
@@ -1031,7 +1200,7 @@ struct BackwardWarp {
 };
 
 template <typename E, int SLAB, int S, int CLUSTER>
-__global__ void __launch_bounds__(32 * WARPS, S == 4 && sizeof(E) == 4 ? 3 : 2)
+__global__ void __launch_bounds__(32 * WARPS, S == 4 ? 3 : 2)
 recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, const __grid_constant__ Maps maps, RecurParams p) {
   pdl_begin();
   using G = Bwd<E, SLAB, S, CLUSTER>;
@@ -1075,20 +1244,31 @@ recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, c
   for (int i = 0; i < count; ++i) {
     t.r0 = w.first_row(i);
     t.kind = PLAIN_TILE;
+    t.bits = RowBits{0, 0, G::ALL, 0, 0};
     if (!plain_tile<G::R>(p, w.gap, t.r0, lo, hi)) {
       t.bits = row_bits(p, starts, sh.marks, w.gap, t.r0, q, w.live_of(i));
-      t.kind = __reduce_max_sync(0xFFFFFFFFu, kind_of<G>(t.bits));
+      t.kind = kind_of<G>(t.bits);
     }
     w.wait_tile(i);
-    if (t.kind == PLAIN_TILE) {
-      w.template first_half<PLAIN_TILE>(i, t, e, c);
+    if (t.kind == PLAIN_TILE && w.template first_half<PLAIN_TILE>(i, t, e, c)) {
       w.template second_half<PLAIN_TILE>(i, t, e, c);
-    } else if (EASY && t.kind == EASY_TILE) {
-      w.template first_half<EASY ? EASY_TILE : ANY_TILE>(i, t, e, c);
+    } else if (EASY && t.kind == EASY_TILE &&
+               w.template first_half<EASY ? EASY_TILE : ANY_TILE>(i, t, e, c)) {
       w.template second_half<EASY ? EASY_TILE : ANY_TILE>(i, t, e, c);
-    } else {
-      w.template first_half<ANY_TILE>(i, t, e, c);
+    } else if (t.kind == DEAD_TILE) {
+      w.skip(i, t);
+    } else if ((t.kind == ANY_TILE || (!EASY && t.kind == EASY_TILE)) &&
+               w.template first_half<ANY_TILE>(i, t, e, c)) {
       w.template second_half<ANY_TILE>(i, t, e, c);
+    } else {
+      float2 cc[G::S][N / 2], ce[G::S][N / 2];
+      if (t.kind == PLAIN_TILE) {
+        w.template first_half<PLAIN_CLOSED>(i, t, ce, cc);
+        w.template second_half<PLAIN_CLOSED>(i, t, ce, cc);
+      } else {
+        w.template first_half<ANY_CLOSED>(i, t, ce, cc);
+        w.template second_half<ANY_CLOSED>(i, t, ce, cc);
+      }
     }
   }
   float db[N];
@@ -1130,7 +1310,7 @@ recur_step_kernel(const E *x, const E *gate, E *h, RecurParams p) {
 #pragma unroll
   for (int n = 0; n < M; ++n) {
     const float2 t = fma2(gv[n], both(LOG2E), mul2(bias[n], both(LOG2E)));
-    y[n] = row_step(minus_c(exp2_of(t)), xv[n], y[n]);
+    y[n] = row_step<true>(gate_of<true>(t, exp2_of(t)), xv[n], y[n], less2(y[n], xv[n]));
   }
   *(uint4 *)(h + (size_t)row * p.D + d) = packed(y, (E *)nullptr);
   if (p.hT) store_state(p.hT, row, p.D, d, y);
