@@ -632,26 +632,23 @@ struct Rounds {
 };
 
 // What can be in a warp's tile: no sequence begins or ends there and all of its rows are
-// some sequence's (PLAIN); one at most begins and one ends in each lane's rows, and all are
-// some sequence's (EASY); anything; no row of a sequence (DEAD).  Branches at the rows keep the
-// rows' arithmetic from overlapping (16384 x 2048 of 9 sequences forward 55 us, of 257 80), so
-// what is easy has a selection a row instead (50 and 72).  With a gate below OPEN, which shows
-// when the gates are read, a tile begins again as CLOSED: two or three selections a value.  Its
-// rows are a loop that is hardly unrolled, with the gates in local memory: one more unrolled
-// body slows the others down (16384 x 4096 backward 152 us, else 164; with closed gates in
-// every tile 317, else 378; forward 82 and 136, else 88 and 180).
-enum Kind { PLAIN_TILE, PLAIN_CLOSED, EASY_TILE, ANY_TILE, ANY_CLOSED, DEAD_TILE };
-template <int S>
-constexpr int unroll_of(int kind) {
-  return kind == PLAIN_CLOSED ? 2 : kind == ANY_CLOSED ? 1 : S;
-}
+// some sequence's (PLAIN); one at most begins and one ends in each lane's rows (EASY); anything;
+// no row of a sequence (DEAD).  Branches at the rows keep the rows' arithmetic from overlapping
+// (16384 x 2048 of 9 sequences forward 55 us, of 257 80), so what is easy has a selection a row
+// instead (50 and 72).  With a gate below OPEN, which shows when the gates are read, a tile
+// begins again as CLOSED: two or three selections a value, and branches at the rows.  This is a
+// loop over the rows, with their gates in local memory: one more unrolled body slows the others
+// down (16384 x 4096 backward 151 us, else 164; 64 x 128 fp32, where the code's way from L2
+// counts, both directions 10 and 12), although closed gates in every tile take twice a tile's
+// time (156 and 365 us).  Where there is an EASY body, ANY goes by that loop too (sequences of
+// 8 rows, 16384 x 2048 forward 191 us, else 177).
+enum Kind { PLAIN_TILE, EASY_TILE, ANY_TILE, CLOSED_TILE, DEAD_TILE };
 template <typename G>
 __device__ __forceinline__ int kind_of(const RowBits &b) {
   if (!__any_sync(0xFFFFFFFFu, b.live != 0)) return DEAD_TILE;
   const uint32_t more = (b.first & (b.first - 1)) | (b.last & (b.last - 1));
-  return __reduce_max_sync(0xFFFFFFFFu, b.live != G::ALL || more != 0 ? ANY_TILE
-                                        : (b.first | b.last) != 0    ? EASY_TILE
-                                                                     : PLAIN_TILE);
+  const bool marked = (b.first | b.last) != 0 || b.live != G::ALL;
+  return __reduce_max_sync(0xFFFFFFFFu, more != 0 ? ANY_TILE : marked ? EASY_TILE : PLAIN_TILE);
 }
 // The last row of those marked (-1: none).
 __device__ __forceinline__ int last_row(uint32_t bits) { return 31 - __clz(bits); }
@@ -752,8 +749,7 @@ struct ForwardWarp {
   // Returns false, with nothing sent, where it finds a closed gate.
   template <int KIND>
   __device__ __forceinline__ bool first_half(int i, Tile &t, float2 (&m)[S][M]) {
-    constexpr bool CLOSED = KIND == PLAIN_CLOSED || KIND == ANY_CLOSED;
-    constexpr int UNROLL = unroll_of<S>(KIND);
+    constexpr bool CLOSED = KIND == CLOSED_TILE;
     uint4 lowest;
     float2 As[M], ns[M], Hs[M];  // the rows so far, see Joint
 #pragma unroll
@@ -768,7 +764,7 @@ struct ForwardWarp {
       load_state(on ? p.h0 : nullptr, first_of(p, sh.marks, t.r0, q * S + begin), p.D, d, start);
       hold(start);
     }
-#pragma unroll UNROLL
+#pragma unroll(CLOSED ? 1 : S)
     for (int k = 0; k < S; ++k) {
       if (KIND == EASY_TILE) select(Hs, start, k == begin);
       if (KIND >= ANY_TILE && (t.bits.any_first >> k & 1) && (t.bits.first >> k & 1)) {
@@ -802,7 +798,7 @@ struct ForwardWarp {
     }
     cta_barrier();  // (all warps are done with the gates, and with tile i - 1)
     fetch_tile(i + 1);
-    const bool cut = KIND > PLAIN_CLOSED && (t.bits.first != 0 || t.bits.live != G::ALL);
+    const bool cut = KIND != PLAIN_TILE && (t.bits.first != 0 || t.bits.live != G::ALL);
 #pragma unroll
     for (int n = 0; n < M; ++n) {
       const float2 all = make_float2(smaller(As[n].x, ns[n].x), smaller(As[n].y, ns[n].y));
@@ -810,7 +806,7 @@ struct ForwardWarp {
       sh.steps[G::at(q, (2 * n + 1) * CX + cx)] = make_float2(cut ? CUT : all.y, Hs[n].y);
     }
     __syncwarp();
-    t.scan = scan_up<G, AS_M, false, KIND <= PLAIN_CLOSED>(sh.steps);
+    t.scan = scan_up<G, AS_M, false, KIND == PLAIN_TILE>(sh.steps);
     send_step<G>(sh.exchange, C, rank, i, t.scan, lost);
     return true;
   }
@@ -826,10 +822,9 @@ struct ForwardWarp {
   // The second half: the rows once more, from the state before them.
   template <int KIND>
   __device__ __forceinline__ void second_half(int i, const Tile &t, const float2 (&m)[S][M]) {
-    constexpr bool CLOSED = KIND == PLAIN_CLOSED || KIND == ANY_CLOSED;
-    constexpr int UNROLL = unroll_of<S>(KIND);
+    constexpr bool CLOSED = KIND == CLOSED_TILE;
     const float in = receive_steps<G, false>(sh.exchange, C, rank, i, t.scan, carry, lost, p.status);
-    scan_down<G, AS_M, false, KIND <= PLAIN_CLOSED>(sh.steps, t.scan, in);
+    scan_down<G, AS_M, false, KIND == PLAIN_TILE>(sh.steps, t.scan, in);
     __syncwarp();
     float2 y[M];
 #pragma unroll
@@ -848,7 +843,7 @@ struct ForwardWarp {
     uint4 rows[CLOSED ? 1 : S];  // (read before the first store, which the reads could not pass)
 #pragma unroll
     for (int k = 0; !CLOSED && k < S; ++k) rows[CLOSED ? 0 : k] = cta.x[i & 1].v[slot(k)];
-#pragma unroll UNROLL
+#pragma unroll(CLOSED ? 1 : S)
     for (int k = 0; k < S; ++k, out += p.D) {
       float2 xv[M];
       pairs(CLOSED ? cta.x[i & 1].v[slot(k)] : rows[CLOSED ? 0 : k], xv, (E *)nullptr);
@@ -859,7 +854,7 @@ struct ForwardWarp {
       }
 #pragma unroll
       for (int n = 0; n < M; ++n) y[n] = row_step<CLOSED>(m[k][n], xv[n], y[n], less2(y[n], xv[n]));
-      if (KIND < ANY_TILE || (t.bits.live >> k & 1)) *(uint4 *)out = packed(y, (E *)nullptr);
+      if (KIND == PLAIN_TILE || (t.bits.live >> k & 1)) *(uint4 *)out = packed(y, (E *)nullptr);
       if (KIND == EASY_TILE) select(behind, y, k == end);
       if (KIND >= ANY_TILE && (t.bits.any_last >> k & 1) && (t.bits.last >> k & 1) && p.hT)
         store_state(p.hT, last_of(p, sh.marks, t.r0, q * S + k), p.D, d, y);
@@ -914,19 +909,12 @@ recur_forward_kernel(const E *x, const E *gate, E *h, const __grid_constant__ Ma
       w.template second_half<PLAIN_TILE>(i, t, c);
     } else if (t.kind == EASY_TILE && w.template first_half<EASY_TILE>(i, t, c)) {
       w.template second_half<EASY_TILE>(i, t, c);
-    } else if (t.kind == ANY_TILE && w.template first_half<ANY_TILE>(i, t, c)) {
-      w.template second_half<ANY_TILE>(i, t, c);
     } else if (t.kind == DEAD_TILE) {
       w.skip(i, t);
     } else {
       float2 cc[G::S][G::N / 2];
-      if (t.kind == PLAIN_TILE) {
-        w.template first_half<PLAIN_CLOSED>(i, t, cc);
-        w.template second_half<PLAIN_CLOSED>(i, t, cc);
-      } else {
-        w.template first_half<ANY_CLOSED>(i, t, cc);
-        w.template second_half<ANY_CLOSED>(i, t, cc);
-      }
+      w.template first_half<CLOSED_TILE>(i, t, cc);
+      w.template second_half<CLOSED_TILE>(i, t, cc);
     }
   }
   // (nothing is on its way to this CTA any more, unless a wait has given up)
@@ -1022,8 +1010,7 @@ struct BackwardWarp {
   // tile needs no other, and of the gates there stay m and e := (h_{t-1} - x_t) a c.
   template <int KIND>
   __device__ __forceinline__ bool first_half(int i, Tile &t, float2 (&e)[S][M], float2 (&m)[S][M]) {
-    constexpr bool CLOSED = KIND == PLAIN_CLOSED || KIND == ANY_CLOSED;
-    constexpr int UNROLL = unroll_of<S>(KIND);
+    constexpr bool CLOSED = KIND == CLOSED_TILE;
     uint4 lowest;
     float2 As[M], ns[M], Hs[M];  // the rows so far, see Joint
 #pragma unroll
@@ -1040,7 +1027,7 @@ struct BackwardWarp {
         load_state(on ? p.h0 : nullptr, first_of(p, sh.marks, t.r0, q * S + begin), p.D, d, v);
     };
     at_begin(start);
-#pragma unroll UNROLL
+#pragma unroll(CLOSED ? 1 : S)
     for (int k = 0; k < S; ++k) {
       if (KIND == EASY_TILE) select(Hs, start, k == begin);
       if (KIND >= ANY_TILE && (t.bits.any_first >> k & 1) && (t.bits.first >> k & 1))
@@ -1073,9 +1060,9 @@ struct BackwardWarp {
     }
     cta_barrier();  // (all warps are done with the gates, and with the last tile's dh)
     fetch_tile(i + 1);
-    const bool dead = KIND >= ANY_TILE && t.bits.live != G::ALL;
-    const bool cutF = KIND > PLAIN_CLOSED && (dead || t.bits.first),
-               cutB = KIND > PLAIN_CLOSED && (dead || t.bits.last);
+    const bool dead = KIND != PLAIN_TILE && t.bits.live != G::ALL;
+    const bool cutF = KIND != PLAIN_TILE && (dead || t.bits.first),
+               cutB = KIND != PLAIN_TILE && (dead || t.bits.last);
 #pragma unroll
     for (int n = 0; n < M; ++n) {
       sh.stepsF[G::at(q, 2 * n * CX + cx)] = make_float2(cutF ? CUT : As[n].x, Hs[n].x);
@@ -1085,7 +1072,7 @@ struct BackwardWarp {
     }
     if (KIND == EASY_TILE && end >= 0)
       load_state(on ? p.dhT : nullptr, last_of(p, sh.marks, t.r0, q * S + end), p.D, d, start);
-#pragma unroll UNROLL
+#pragma unroll(CLOSED ? 1 : S)
     for (int k = S - 1; k >= 0; --k) {
       if (KIND == EASY_TILE) select(Hs, start, k == end);
       if (KIND >= ANY_TILE && (t.bits.any_last >> k & 1) && (t.bits.last >> k & 1))
@@ -1103,10 +1090,10 @@ struct BackwardWarp {
       sh.stepsB[G::at(q, (2 * n + 1) * CX + cx)] = make_float2(cutB ? CUT : As[n].y, Hs[n].y);
     }
     __syncwarp();
-    t.scan = scan_up<G, AS_M, true, KIND <= PLAIN_CLOSED>(sh.stepsB);
+    t.scan = scan_up<G, AS_M, true, KIND == PLAIN_TILE>(sh.stepsB);
     send_step<G>(sh.exchange, C, rank, i, t.scan, lost);
-    scan_down<G, AS_A, false, KIND <= PLAIN_CLOSED>(
-        sh.stepsF, scan_up<G, AS_A, false, KIND <= PLAIN_CLOSED>(sh.stepsF), before);
+    scan_down<G, AS_A, false, KIND == PLAIN_TILE>(
+        sh.stepsF, scan_up<G, AS_A, false, KIND == PLAIN_TILE>(sh.stepsF), before);
     before = state_before(i + 1);
     __syncwarp();
     float2 y[M];
@@ -1114,7 +1101,7 @@ struct BackwardWarp {
     for (int n = 0; n < M; ++n)
       y[n] = make_float2(sh.stepsF[G::at(q, 2 * n * CX + cx)].x, sh.stepsF[G::at(q, (2 * n + 1) * CX + cx)].x);
     at_begin(start);
-#pragma unroll UNROLL
+#pragma unroll(CLOSED ? 1 : S)
     for (int k = 0; k < S; ++k) {
       if (KIND == EASY_TILE) select(y, start, k == begin);
       if (KIND >= ANY_TILE && (t.bits.any_first >> k & 1) && on && (t.bits.first >> k & 1))
@@ -1149,10 +1136,9 @@ struct BackwardWarp {
   template <int KIND>
   __device__ __forceinline__ void second_half(int i, const Tile &t, const float2 (&e)[S][M],
                                               const float2 (&m)[S][M]) {
-    constexpr bool CLOSED = KIND == PLAIN_CLOSED || KIND == ANY_CLOSED;
-    constexpr int UNROLL = unroll_of<S>(KIND);
+    constexpr bool CLOSED = KIND == CLOSED_TILE;
     const float in = receive_steps<G, true>(sh.exchange, C, rank, i, t.scan, carry, lost, p.status);
-    scan_down<G, AS_M, true, KIND <= PLAIN_CLOSED>(sh.stepsB, t.scan, in);
+    scan_down<G, AS_M, true, KIND == PLAIN_TILE>(sh.stepsB, t.scan, in);
     __syncwarp();
     float2 y[M];
 #pragma unroll
@@ -1170,12 +1156,12 @@ struct BackwardWarp {
     const int end = KIND == EASY_TILE ? last_row(t.bits.last) : -1;
     if (KIND == EASY_TILE && end >= 0)
       load_state(p.dhT, last_of(p, sh.marks, t.r0, q * S + end), p.D, d, start);
-#pragma unroll UNROLL
+#pragma unroll(CLOSED ? 1 : S)
     for (int k = S - 1; k >= 0; --k) {
       if (KIND == EASY_TILE) select(y, start, k == end);
       if (KIND >= ANY_TILE && (t.bits.any_last >> k & 1) && (t.bits.last >> k & 1))
         load_state(p.dhT, last_of(p, sh.marks, t.r0, q * S + k), p.D, d, y);
-      const bool live = KIND < ANY_TILE || (t.bits.live >> k & 1);
+      const bool live = KIND == PLAIN_TILE || (t.bits.live >> k & 1);
       float2 dv[M], gv[M];
       pairs(CLOSED ? cta.dh[i & 1].v[slot(k)] : rows[CLOSED ? 0 : k], dv, (E *)nullptr);
 #pragma unroll
@@ -1236,9 +1222,10 @@ recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, c
   }
   w.carry = 0.f;
   if (C > 1) cluster_wait();
-  // (with 8 rows of bf16 a third body costs all of them registers: 16384 x 4096 142 us, with
-  // it 154)
+  // (with 8 rows of bf16 an easy body costs all of them registers: 16384 x 4096 151 us, with
+  // it 166)
   constexpr bool EASY = sizeof(E) == 4 || S == 4;
+  constexpr int MARKED = EASY ? EASY_TILE : ANY_TILE;
   Tile t;
   float2 c[G::S][N / 2], e[G::S][N / 2];
   for (int i = 0; i < count; ++i) {
@@ -1252,23 +1239,15 @@ recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, c
     w.wait_tile(i);
     if (t.kind == PLAIN_TILE && w.template first_half<PLAIN_TILE>(i, t, e, c)) {
       w.template second_half<PLAIN_TILE>(i, t, e, c);
-    } else if (EASY && t.kind == EASY_TILE &&
-               w.template first_half<EASY ? EASY_TILE : ANY_TILE>(i, t, e, c)) {
-      w.template second_half<EASY ? EASY_TILE : ANY_TILE>(i, t, e, c);
     } else if (t.kind == DEAD_TILE) {
       w.skip(i, t);
-    } else if ((t.kind == ANY_TILE || (!EASY && t.kind == EASY_TILE)) &&
-               w.template first_half<ANY_TILE>(i, t, e, c)) {
-      w.template second_half<ANY_TILE>(i, t, e, c);
+    } else if (t.kind != PLAIN_TILE && !(EASY && t.kind == ANY_TILE) &&
+               w.template first_half<MARKED>(i, t, e, c)) {
+      w.template second_half<MARKED>(i, t, e, c);
     } else {
       float2 cc[G::S][N / 2], ce[G::S][N / 2];
-      if (t.kind == PLAIN_TILE) {
-        w.template first_half<PLAIN_CLOSED>(i, t, ce, cc);
-        w.template second_half<PLAIN_CLOSED>(i, t, ce, cc);
-      } else {
-        w.template first_half<ANY_CLOSED>(i, t, ce, cc);
-        w.template second_half<ANY_CLOSED>(i, t, ce, cc);
-      }
+      w.template first_half<CLOSED_TILE>(i, t, ce, cc);
+      w.template second_half<CLOSED_TILE>(i, t, ce, cc);
     }
   }
   float db[N];
