@@ -58,7 +58,15 @@ __device__ __forceinline__ float log_prob(float z, float m, float l, float c) {
   return (Ref(m, c)(z, c) - log2f(l)) * LN2;
 }
 
-// The row's loss over its weight, and its slope over its weight.
+// A factor of the gradient, held where its products with exponentials up to 2^(1/2), over sums
+// of them from 2^(-1/2) on, are finite: an infinite one would make NaN of the elements of
+// probability 0.
+__device__ __forceinline__ float held(float v) {
+  return v == v ? fminf(fmaxf(v, -0x1p126f), 0x1p126f) : v;
+}
+
+// The row's loss over its weight, and its slope over its weight.  Where exp(d) leaves fp32's
+// range, so does the KL term (d, which may be infinite too, is not taken from it then).
 __device__ __forceinline__ void row_loss(const PolicyParams &p, size_t t, float logp, float *loss,
                                          float *slope) {
   const float A = p.advantage[t];
@@ -68,14 +76,19 @@ __device__ __forceinline__ void row_loss(const PolicyParams &p, size_t t, float 
   const float gain = A == 0.f && r == INFINITY ? 0.f : r * A;
   const float kept = fminf(fmaxf(r, p.low), p.high) * A;
   const bool clipped = kept < gain;
-  float l = -(clipped ? kept : gain), s = clipped ? 0.f : -gain;
+  float l = -(clipped ? kept : gain), s = clipped ? 0.f : -held(gain);
   if (p.ref_logp && p.beta != 0.f) {
     const float d = p.ref_logp[t] - logp, e = expm1f(d);
-    l += p.beta * (e - d);
-    s -= p.beta * e;
+    l += p.beta * (e == INFINITY ? e : e - d);
+    s -= held(p.beta * e);
   }
   *loss = l;
   *slope = s;
+}
+
+// The gradient's factor of (onehot - softmax).
+__device__ __forceinline__ float coef_of(const PolicyParams &p, const Token &tk, float slope) {
+  return held(tk.w * slope * p.inv_tau);
 }
 
 // The row's outputs, by one thread; m, l: maximum and sum of exponentials.
@@ -91,7 +104,7 @@ __device__ __forceinline__ float finish_row(const PolicyParams &p, size_t t, con
     p.logp[t] = *logp;
     p.stats[t] = make_float2(m, logf(l) - (ref.wide ? 0.f : LN2 * fmaf(m, p.c, -ref.mc)));
   }
-  return tk.w * slope * p.inv_tau;
+  return coef_of(p, tk, slope);
 }
 
 __device__ __forceinline__ void store_nothing(const PolicyParams &p, size_t t) {
@@ -251,12 +264,12 @@ policy_row_kernel(const E *z, E *dz, PolicyParams p) {
 // a CTA.
 constexpr int BWD_THREADS = 256;
 
-// The factor of the softmax's exponentials in the gradient, from the statistics.
+// The same from the statistics, and that of the exponentials.
 __device__ __forceinline__ float coef_of(const PolicyParams &p, size_t t, const Token &tk,
                                          float logp) {
   float loss, slope;
   row_loss(p, t, logp, &loss, &slope);
-  return tk.w * slope * p.inv_tau;
+  return coef_of(p, tk, slope);
 }
 __device__ __forceinline__ float gl_of(float coef, const float2 &st, const Ref &ref, float c) {
   return -coef * ex2(-st.y * LOG2E - (ref.wide ? 0.f : fmaf(st.x, c, -ref.mc)));

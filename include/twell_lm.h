@@ -209,7 +209,11 @@ int twell_recur_states(int T);
  * A row of weight 0 or with a token < 0 is not read: its loss, logp, stats and dz
  * are 0.  A token >= V records TWELL_ERR_INDEX, and its row is treated the same.
  * Logits of -inf have probability 0; a row with NaN, +inf or nothing but -inf has
- * loss, logp and dz NaN (with advantage 0 and no KL term: loss and dz 0 or NaN).
+ * loss, logp and dz NaN (with advantage 0 and no KL term: loss and dz 0 or NaN).  A
+ * token of probability 0 has logp -inf: r is 0 and, with beta > 0, the loss infinite
+ * (old_logp and ref_logp finite).  The terms of the slope, and row_weight * slope / tau,
+ * are held within +-2^126, which exp(d) reaches near d = 87, so that dz is finite there
+ * too, and 0 at other elements of probability 0.
  * advantage NULL: the log-probabilities alone (loss and dz NULL), as for old_logp
  * and ref_logp themselves.  dz (else NULL: not computed) has z's type and pitch and
  * may be z itself.
