@@ -143,8 +143,12 @@ class AdamWTensors:
     """The tensors of a twell_adamw_step, kept by a program beside them: ``add`` each once, then
     step as often as wanted.  The tensors are held, and checked when they are added: types
     (TWELL_ERR_DTYPE), elements, place and contiguity (TWELL_ERR_ARG); before the first step, that
-    nothing that it writes overlaps with anything else (TWELL_ERR_ARG).  ``state_bits`` 8: m and v are float8_e4m3fn codes with
-    fp32 scales for each 256 elements."""
+    nothing that it writes overlaps with anything else (TWELL_ERR_ARG).  A step goes to the memory
+    that they had then: it is refused (the same codes) once one of them has been given other memory
+    or another shape or type, as by ``p.data = ...``; a list is then built anew.  A gradient is the
+    tensor that was added, not what ``p.grad`` is later; a captured step has its addresses, and
+    needs the list to be kept.  ``state_bits`` 8: m and v are float8_e4m3fn codes with fp32 scales
+    for each 256 elements."""
 
     def __init__(self, state_bits: int = 32):
         if state_bits not in (8, 32):
@@ -196,8 +200,13 @@ class AdamWTensors:
                 i = bisect.bisect_right(ends, lo)
                 if i < len(both) and both[i][0] < hi:
                     raise TwellError(-1, "AdamWTensors")
-            self.array = (twell_adamw_tensor * max(1, len(self.rows)))(*map(tuple, self.rows))
-            self.address = ctypes.addressof(self.array)
+            array = (twell_adamw_tensor * max(1, len(self.rows)))(*map(tuple, self.rows))
+            self.address = ctypes.addressof(array)
+            self.list = _lm.adamw_list(tuple(t for row in self.held for t in row), self.address,
+                                       len(self.rows))
+            if self.list is None:   # (a tensor has got other memory since it was added)
+                raise TwellError(-1, "AdamWTensors")
+            self.array = array
         return self.address, len(self.rows)
 
 
@@ -211,6 +220,8 @@ def adamw_dynamic(lr: float, beta1: float, beta2: float, step: int, seed: int = 
 
 def twell_adamw_step(tensors: AdamWTensors, lr: float, beta1: float, beta2: float, eps: float,
                      step: int, seed: int = 0, grad_scale=None, dynamic=None, stream=None) -> None:
-    address, count = tensors.table()
-    _check(_lm.adamw_step(address, count, tensors.grad_dtype or 0, tensors.state_bits, lr, beta1,
-                          beta2, eps, step, seed, grad_scale, dynamic, stream), "twell_adamw_step")
+    if tensors.array is None:
+        tensors.table()
+    _check(_lm.adamw_step(tensors.list, tensors.address, len(tensors.rows), tensors.grad_dtype or 0,
+                          tensors.state_bits, lr, beta1, beta2, eps, step, seed, grad_scale, dynamic,
+                          stream), "twell_adamw_step")
