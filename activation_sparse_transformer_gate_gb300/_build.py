@@ -12,7 +12,7 @@ entry points):
   the tensor-core GEMM engine with a plain fp32 epilogue, and the random-row
   gather probe that the benchmark reads the gather kernels against; and a count
   of CTA pairs that end before their last commits have arrived.
-* ``libtwell_timeout.so`` -- the same hooks of the kernels, and the pipeline waits of the tensor-core kernels
+* ``libtwell_timeout.so`` -- the same hooks of the kernels, and the waits of the tensor-core kernels and the recurrence
   limited to 1 ns, so that every wait that is not satisfied at once runs out
   on a sane input and the timeout path (status, drain, exit) can be tested
   without a fault.

@@ -543,20 +543,36 @@ __device__ __forceinline__ uint32_t peer(uint32_t addr, int rank) {
   return r;
 }
 
+// mbar_try and mbar_test for what came in from other CTAs of the cluster.
+__device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+
 // (OTHERS: what came in is from other CTAs of the cluster)
 template <bool OTHERS>
 __device__ __forceinline__ bool arrived(uint32_t bar, uint32_t parity, uint64_t limit) {
+  // A limit below a microsecond is a build's that tests it.  A try holds the thread until what
+  // it waits for has come, if that takes no longer than a few of them: such a limit would never
+  // run out.
+  const bool look = limit < 1000;
   uint64_t t0 = 0;
   for (;;) {
-    uint32_t ok;
-    if (OTHERS)
-      asm volatile(
-          "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-          " selp.u32 %0, 1, 0, p;\n}\n"
-          : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    else
-      ok = mbar_try(bar, parity);
-    if (ok) return true;
+    if (OTHERS ? (look ? mbar_test_cluster(bar, parity) : mbar_try_cluster(bar, parity))
+               : (look ? mbar_test(bar, parity) : mbar_try(bar, parity)))
+      return true;
     const uint64_t now = global_timer();
     if (!t0) t0 = now;
     else if (now - t0 > limit) return false;
