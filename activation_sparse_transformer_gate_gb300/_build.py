@@ -34,9 +34,11 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 
-SOURCES = ["twell_abi.cu", "pack.cu", "simt_gemm.cu", "updown.cu", "tc_gemm.cu", "backward.cu",
-           "rowell.cu", "static_split.cu", "lm_abi.cu", "embed.cu", "rmsnorm.cu", "distill.cu",
-           "q8.cu", "recur.cu", "policy.cu", "adamw.cu"]
+# the FFN's, and those of the operators around it
+FFN_SOURCES = ["twell_abi.cu", "pack.cu", "simt_gemm.cu", "updown.cu", "tc_gemm.cu", "backward.cu",
+               "rowell.cu", "static_split.cu"]
+SOURCES = FFN_SOURCES + ["lm_abi.cu", "embed.cu", "rmsnorm.cu", "distill.cu", "q8.cu", "recur.cu",
+                         "policy.cu", "adamw.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 # variant -> (library file, extra sources, extra nvcc flags)

@@ -662,23 +662,30 @@ def kernel_rooflines(kern, w, nnz, train, rows_f=0, rows_b=0, dh_gemm=False):
     return out
 
 
-def kernel_source_hash() -> str:
-    """Hash of the FFN's sources with comments and blank space removed, so that
-    a capture stays matched to its kernels across comment edits and changes of
-    the operators around the FFN (which no captured kernel is built from)."""
+def kernel_source_hash(csrc=None) -> str:
+    """Hash of what the FFN's kernels are built from: its sources and the
+    headers that these include, without comments, blank space and the names of
+    the timing events, so that a capture stays matched to its kernels across
+    comment edits and changes of the operators around the FFN (which no
+    captured kernel is built from)."""
     import re
-    around = ("lm_abi.cu", "lm_kernels.h", "vec16.cuh", "embed.cu", "rmsnorm.cu", "distill.cu",
-              "q8.cu", "lm_bind.cpp")
-    h = hashlib.sha256()
-    csrc = os.path.join(ROOT, "activation_sparse_transformer_gate_gb300", "csrc")
-    for f in sorted(os.listdir(csrc)):
-        if f in around:
+    from activation_sparse_transformer_gate_gb300 import _build
+    csrc = csrc or _build.CSRC
+    todo, texts = list(_build.FFN_SOURCES), {}
+    while todo:
+        f = todo.pop()
+        path = os.path.join(csrc, f)
+        if f in texts or not os.path.exists(path):  # (a header of another folder)
             continue
-        text = open(os.path.join(csrc, f), encoding="utf-8").read()
+        text = open(path, encoding="utf-8").read()
+        todo += re.findall(r'^\s*#include "([^"]+)"', text, flags=re.M)
         text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
         text = re.sub(r"//[^\n]*", "", text)
-        text = re.sub(r"\s+", " ", text)
-        h.update(f.encode() + b"\0" + text.encode())
+        text = re.sub(r"enum KernelId \{.*?\};|kKernelNames\[KID_COUNT\] = \{.*?\};", "", text, flags=re.S)
+        texts[f] = re.sub(r"\s+", " ", text)
+    h = hashlib.sha256()
+    for f in sorted(texts):
+        h.update(f.encode() + b"\0" + texts[f].encode())
     return h.hexdigest()[:16]
 
 
