@@ -7,12 +7,12 @@ distillation and served with an 8-bit output product.
               -> gradients -> AdamW
 
 Every step of it is a call of the library but the matrix multiplications of the
-output product and of the recurrence's inputs (torch).  Without --mix the student
+output product and of the recurrence's inputs, and the sampling of --tune (torch).  Without --mix the student
 sees one token at a time, so what it can learn is a table of next-token
 distributions: the teacher here is such a table, of which each token gives its
 largest logits.  With it a gated recurrence carries a state along each sequence.
 --tune goes on with the policy loss: tokens are sampled, and a reward for even ones
-moves the distribution, held by the KL term to where it was.
+moves the distribution, held by the KL term to the weights that it began with.
 
     python examples/distill_student.py [--steps N] [--mix] [--tune N] [--bits 8]
 """
@@ -115,9 +115,14 @@ class Student:
         """bf16 copies of the matrices (norm weights and biases stay fp32)."""
         self.p = {n: p.bfloat16() if p.dim() == 2 else p for n, p in self.master.items()}
 
-    def forward(self, tokens):
-        """The final norm's rows; the residual stream and its norms stay in self.s, self.n."""
-        T, D, p = self.T, self.D, self.p
+    def frozen(self):
+        """The weights as they are, for ``forward`` once they have moved on."""
+        return {n: p.clone() for n, p in self.p.items()}
+
+    def forward(self, tokens, p=None):
+        """The final norm's rows; the residual stream and its norms stay in self.s, self.n.  ``p``:
+        other weights than the present ones."""
+        T, D, p = self.T, self.D, p or self.p
         tw.twell_embed_forward(tokens, p["embed"], T, self.V, D, BF16, self.scale, self.pad_id,
                                self.x0, self.status)
         for i in range(self.L + 1):
@@ -151,9 +156,10 @@ class Student:
         self.backward(tokens, n, z)
         return self.loss
 
-    def log_probabilities(self, tokens, sampled, row_weight):
-        """Of the sampled tokens, as the old and the reference policy's are taken."""
-        z, logp = self.forward(tokens) @ self.p["out"].t(), torch.empty_like(self.loss)
+    def log_probabilities(self, tokens, sampled, row_weight, p=None):
+        """Of the sampled tokens, as the old and (of frozen weights) the reference policy's are
+        taken."""
+        z, logp = self.forward(tokens, p) @ (p or self.p)["out"].t(), torch.empty_like(self.loss)
         tw.twell_policy_forward(z, self.V, sampled, None, None, None, row_weight, self.T, self.V,
                                 BF16, self.tau, 0.2, 0.2, 0.0, None, logp, self.stats, None,
                                 self.status)
@@ -261,7 +267,9 @@ class Server:
 
 
 def tune(student, steps, weight, g):
-    """Policy steps, two on each batch of sampled tokens; a reward for the even ones."""
+    """Policy steps, two on each batch of sampled tokens; a reward for the even ones.  The policy
+    that sampled is the batch's, the reference the one that tuning began with."""
+    reference = student.frozen()
     for step in range(0, steps, 2):
         tokens = torch.randint(0, student.V, (student.T,), generator=g, device="cuda")
         z = student.forward(tokens) @ student.p["out"].t()
@@ -269,8 +277,9 @@ def tune(student, steps, weight, g):
         reward = (sampled % 2 == 0).float()
         advantage = reward - reward.mean()
         old = student.log_probabilities(tokens, sampled, weight)
+        ref = student.log_probabilities(tokens, sampled, weight, reference)
         for _ in range(min(2, steps - step)):
-            student.policy_and_gradients(tokens, sampled, old, old, advantage, weight)
+            student.policy_and_gradients(tokens, sampled, old, ref, advantage, weight)
             student.update(lr=5e-4)
         student.check()
         print(f"tuned {step + 2:4d}  even tokens {100 * reward.mean().item():.0f}%", flush=True)
