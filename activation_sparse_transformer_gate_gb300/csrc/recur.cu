@@ -1443,17 +1443,18 @@ cudaError_t backward_s(const RecurArgs &a, cudaStream_t s) {
 }
 
 
-// Tiles of 4 rows a group: a call of few rows has more CTAs at work, and easy tiles have
-// their registers.  Those of 8 have fewer rounds, each of a fixed cost (us, 4 | 8: 64 x 128
-// fp32 5.4 | 8.4, 4096 x 2048 of 9 sequences 32 | 37, of 1 28 | 27; 16384 x 2048 of 1 sequence
-// 89 | 76, of 9 97 | 91, of 17 101 | 105, of 65 123 | 155, of 257 149 | 150; 8 channels a warp,
-// 16384 x 128 of 50 34 | 31, 16384 x 512 of 65 fp32 73 | 59).
-constexpr int FEW_ROWS = 4096, SHORT = 1024;
+// Tiles of 4 rows a group leave room for a third CTA; those of 8 have fewer rounds, each of a
+// fixed cost.  With 16 channels a warp 4 rows win at every number of sequences; with 8 in
+// calls of few rows (us, 4 | 8: 64 x 128 fp32 5.8 | 11, 16384 x 2048 of 1 sequence 84 | 85, of 9
+// 93 | 106, of 65 124 | 178, 16384 x 4096 149 | 151; 8 channels, 16384 x 512 46 | 45, 16384 x 128
+// of 50 36 | 34, 16384 x 512 of 65 fp32 75 | 61).
+constexpr int FEW_ROWS = 4096;
 
 template <typename E, int SLAB, int CLUSTER>
 cudaError_t backward_w(const RecurArgs &a, cudaStream_t s) {
-  const bool four = a.T <= FEW_ROWS || (SLAB == 16 && a.T / a.B < SHORT);
-  return four ? backward_s<E, SLAB, 4, CLUSTER>(a, s) : backward_s<E, SLAB, 8, CLUSTER>(a, s);
+  if constexpr (SLAB == 8)
+    if (a.T > FEW_ROWS) return backward_s<E, SLAB, 8, CLUSTER>(a, s);
+  return backward_s<E, SLAB, 4, CLUSTER>(a, s);
 }
 
 template <typename E>
