@@ -130,7 +130,8 @@ inline cudaError_t launch_k(void (*kern)(KArgs...), dim3 grid, dim3 block, size_
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-// The same for a kernel whose CTAs form clusters of `cluster` (at most 8).
+// The same for a kernel whose CTAs form clusters of `cluster` (above 8: a kernel that has
+// cudaFuncAttributeNonPortableClusterSizeAllowed).
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_clusters(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
                                    int cluster, cudaStream_t s, Args... args) {

@@ -17,7 +17,7 @@
 // up to 16 CTAs owns a slab of channels and goes through all rows in rounds.  A warp
 // has 16 channels, or 8, and works by itself (lanes: 2 across and 16 groups of rows,
 // or 1 and 32; fp32 has 8 channels on 2 lanes): its tile of a round is 8 rows a group
-// (a short backward: 4), of which
+// (a backward of 16 channels, or of few rows: 4), of which
 //   a lane composes its rows' steps, the warp its groups' (shared memory), the cluster
 //   its CTAs' (asynchronous stores to distributed shared memory, which an mbarrier
 //   counts),
@@ -32,15 +32,17 @@
 // enter the gradient.
 //
 // HBM would bound it (3 values an element forward, 5 backward: 60 and 101 us at 16384 x
-// 4096 bf16, which take 84 and 142).  What bounds it is latency, and next the issue slots:
-// the gates stay in registers from one pass over a tile to the other, which leaves room for
-// 12 warps an SM forward and 8 backward, and a round has its fixed part (two scans, the
-// exchange) of some 600 instructions.  Measured on the way: CTAs in step with barriers,
+// 4096 bf16, which take 81 and 150).  What bounds it is latency, and next the issue slots (41
+// and 45%): the gates stay in registers from one pass over a tile to the other, which leaves
+// room for 12 warps an SM (8 with 8 rows of bf16 a group and fewer clusters), and a round has
+// its fixed part (two scans, the exchange).  Measured on the way: CTAs in step with barriers,
 // 150 and 430 us; warps by themselves, 120 and 187; two tiles at a time, one of them on its
 // way to the other CTAs, 107 and 186; two channels an instruction, 102 and 183; rows copied
 // in whole lines, 95 and 176; tiles copied as boxes of a tensor, 88 and 167; one tile at a
 // time again, with the registers spent on more warps and on longer tiles, 84 and 158; copies on
-// their way for a whole round, 84 and 142.
+// their way for a whole round, 84 and 142; the smaller share at every joint, 81 and 151; 4 rows
+// a group and a third CTA in the backward, 81 and 150 (of 65 sequences 105 and 208, before 104
+// and 248).
 // Gates computed again in the second pass (24 warps an SM, a round's inputs from L2): 120
 // and 258.  Rows copied one by one in bulk: 233 and 251 (32 cycles of the SM each).  One
 // body for all tiles, with branches at the rows where sequences begin: 93 and 217; with
@@ -653,11 +655,12 @@ struct Rounds {
 // (16384 x 2048 of 9 sequences forward 55 us, of 257 80), so what is easy has a selection a row
 // instead (50 and 72).  With a gate below OPEN, which shows when the gates are read, a tile
 // begins again as CLOSED: two or three selections a value, and branches at the rows.  This is a
-// loop over the rows, with their gates in local memory: one more unrolled body slows the others
-// down (16384 x 4096 backward 151 us, else 164; 64 x 128 fp32, where the code's way from L2
-// counts, both directions 10 and 12), although closed gates in every tile take twice a tile's
-// time (156 and 365 us).  Where there is an EASY body, ANY goes by that loop too (sequences of
-// 8 rows, 16384 x 2048 forward 191 us, else 177).
+// loop over the rows, with their gates in local memory: as much code unrolled slows the others
+// down, whose own has to come from L2 when forward and backward alternate (us, loop | unrolled:
+// 64 x 128 fp32 10 | 12, 4096 x 2048 of 9 sequences 49 | 63, 16384 x 4096 233 | 245).  Closed gates
+// in every tile take twice a tile's time (16384 x 4096 156 + 320 | 168 + 290).  Where there is an
+// EASY body, ANY goes by that loop too (sequences of 8 rows, 16384 x 2048 forward 191 us, else
+// 177).
 enum Kind { PLAIN_TILE, EASY_TILE, ANY_TILE, CLOSED_TILE, DEAD_TILE };
 template <typename G>
 __device__ __forceinline__ int kind_of(const RowBits &b) {
@@ -952,8 +955,9 @@ struct BwdShared {
 
 template <typename G>
 struct BwdCta {
-  // x of a tile and of the next one, where that costs no CTA of the SM (16384 x 4096: 142
-  // us, else 149; 4096 x 2048, with two CTAs where there were three: 35, else 32)
+  // x of a tile and of the next one, where that costs no CTA of the SM (16384 x 4096: 150
+  // us, else 156; 16384 x 2048 of 65 sequences, with two CTAs where there were three: 142, else
+  // 124)
   static constexpr int XS = G::SLAB == 16 && G::CLUSTER == 16 ? 1 : 2;
   Slot<G> x[XS], gate, dh[2];
   BwdShared<G> warps[WARPS];
@@ -1238,8 +1242,8 @@ recur_backward_kernel(const E *x, const E *gate, const E *dh, E *dx, E *dgate, c
   }
   w.carry = 0.f;
   if (C > 1) cluster_wait();
-  // (with 8 rows of bf16 an easy body costs all of them registers: 16384 x 4096 151 us, with
-  // it 166)
+  // (with 8 rows of bf16 an easy body costs all of them registers: 16384 x 512 43 us, with it
+  // 46)
   constexpr bool EASY = sizeof(E) == 4 || S == 4;
   constexpr int MARKED = EASY ? EASY_TILE : ANY_TILE;
   Tile t;
@@ -1381,14 +1385,14 @@ struct Shape {
 
 // bf16 takes 16 channels a warp where clusters of 16 CTAs of that width fill the SMs, two
 // CTAs each; else 8, which double the CTAs (us, 8 | 16: 16384 x 512 forward + backward
-// 22 + 36 | 28 + 44, 131072 x 1024 forward 195 | 221, 16384 x 1280 43 + 78 | 39 + 63, 16384 x
-// 4096 98 + 189 | 89 + 154: 16 bytes of a row are half a sector).  fp32 always 8 (8192 x
-// 4096 79 + 138 | 77 + 148, 2048 x 1024 10 + 14 | 14 + 22).
+// 24 + 45 | 30 + 60, 131072 x 1024 forward 193 | 214, 16384 x 1280 49 + 93 | 42 + 78, 16384 x
+// 4096 100 + 203 | 81 + 150: 16 bytes of a row are half a sector).  fp32 always 8 (in an earlier
+// form 8192 x 4096 79 + 138 | 77 + 148, 2048 x 1024 10 + 14 | 14 + 22).
 int columns(int D) { return (D + 63) / 64; }
 bool wide(int D) { return columns(D) * 16 >= 2 * num_sms(); }
 // Clusters of 8 leave room in shared memory for a third CTA of the forward and for more
-// copies on their way in the backward, where there are the CTAs (8 | 16: 16384 x 4096 82 +
-// 142 | 89 + 149, 16384 x 2048 49 + 81 | 49 + 78, 16384 x 1536 47 + 77 | 42 + 66).
+// copies on their way in the backward, where there are the CTAs (8 | 16: 16384 x 4096 81 +
+// 150 | 89 + 158, 16384 x 2048 of 9 sequences 55 + 100 | 54 + 94, 16384 x 1536 55 + 99 | 47 + 81).
 bool wider(int D) { return columns(D) * 8 > 2 * num_sms(); }
 
 template <typename E, int SLAB, int CLUSTER>

@@ -1,5 +1,5 @@
-"""A batch padded with empty sequences: the bits of the batch without them, whatever their number and
-place (how a call is cut up goes by its rows and channels alone)."""
+"""A batch padded with a few hundred empty sequences: the bits of the batch without them, wherever
+they stand."""
 import pytest
 import torch
 
