@@ -165,9 +165,9 @@ twell_status twell_distill_backward(const void *z, long long ldz, const int32_t 
  * The state is held in fp32, h is its rounding; h is a buffer of its own.  B = T
  * without starts is the step of a decoded token for each of T sequences.
  * a and c are each right to 2^-15 of themselves, the small one beside 1 included: a
- * state that gates have forgotten leaves nothing.  An infinity, a NaN or a difference
- * h - x beyond fp32's range reaches nothing outside its sequence (but dbias); in it, the
- * states from that row on and the gradients are infinite or NaN.
+ * state that gates have forgotten leaves nothing.  Where x, h0, dh or dhT is infinite
+ * or NaN, or h - x beyond fp32's range, what depends on it by these formulas is infinite
+ * or NaN (h from that row of its sequence on, G up to it), and nothing else.
  * 1 <= T, 1 <= B, D <= 65536, D <= ld <= 2^34; D*elem_size and ld*elem_size multiples
  * of 16. */
 twell_status twell_recur_forward(const void *x, const void *gate, long long ld, const float *bias,

@@ -169,3 +169,34 @@ def test_a_closed_gate_changes_no_other_sequence(T, D, starts, dtype):
     for n in ("hT", "dh0"):
         v, w = got[n].cpu(), want[n].cpu()
         assert torch.equal(v[other], w[other]) and torch.equal(v[:, channels], w[:, channels]), n
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("T,D,starts", [(300, 72, [0, 100, 290]), (5000, 1544, [0, 777, 4100, 5000]),
+                                        (700, 16, [0, 350, 700])])
+def test_infinities_reach_what_depends_on_them(T, D, starts, bad, dtype):
+    """x: the states from its row on, and their gates' gradients; dh: G up to its row.  The rest has
+    the bits that it has without."""
+    s = 1
+    lo, hi = starts[s], starts[s + 1]
+    at = (lo + hi) // 2
+    rows = torch.arange(T)
+    c = Case(T, D, starts, dtype)
+    want = {n: v.cpu() for n, v in c.run().items()}
+
+    def compare(got, reached):
+        for n, r in reached.items():
+            r = r[:len(got[n])]
+            v, w = got[n].cpu(), want[n]
+            assert not v[r].isfinite().any(), n
+            assert torch.equal(torch.nan_to_num(v[~r]), torch.nan_to_num(w[~r])), n
+
+    nothing, mine = rows < 0, torch.arange(len(starts) - 1) == s
+    after, upto = (rows >= at) & (rows < hi), (rows >= lo) & (rows <= at)
+    whole, none = c.x.clone(), torch.zeros_like(mine)
+    c.x[at] = bad
+    compare(c.run(), {"h": after, "hT": mine, "dx": nothing, "dgate": after, "dh0": none})
+    c.x = whole
+    c.dh[at] = bad
+    compare(c.run(), {"h": nothing, "hT": none, "dx": upto, "dgate": upto, "dh0": mine})
