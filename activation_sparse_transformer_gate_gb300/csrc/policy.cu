@@ -414,6 +414,16 @@ cudaError_t row_t(const PolicyArgs &a, cudaStream_t s) {
 //   64         3.6|3.3|2.8|2.8  5.6|8.1|6.0|5.4   8.4|16|11|8.6
 // (With few rows, a row's latency counts; with many, that the rows in flight fit into L2
 // and the warps into the SMs.)
+// fp32 goes by the same vectors: with the gradient at 6000, 12000, 50001 and 131072 logits
+//   8192 rows   91|67|84|137    137|129|134|171    614|748|678|551   1532|1851|1824|1770
+//   304        6.7|5.3|5.0|5.4   10|9.4|8.6|8.4     31|32|30|29       66|79|72|70
+//   64         4.7|4.4|3.7|3.8  5.2|6.2|4.9|4.5    9.9|20|16|14       22|41|29|22
+// and alone
+//   8192        60|30|36|60      76|57|56|72       229|234|230|223    570|587|579|566
+//   304        4.5|3.6|3.3|3.5  6.3|5.3|5.0|5.0     14|14|13|13       26|29|24|25
+//   64         3.4|2.9|2.5|2.5  3.6|4.1|3.1|2.8    6.6|12|7.7|6.2    9.5|26|15|10
+// so the rule's choice is the best or within a tenth of it, but for many rows of 512 KB with
+// the gradient, where clusters would read less from HBM twice.
 int row_warps(long long rows, int nvec, bool grad) {
   const int sms = num_sms();
   const bool short_ = nvec <= 2048;  // 32 KB
