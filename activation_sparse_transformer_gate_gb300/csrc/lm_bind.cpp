@@ -395,7 +395,7 @@ int same_tensors(const List &list) {
     const c10::TensorImpl *i = h.t.unsafeGetTensorImpl();
     if (i->dtype() != h.type) return TWELL_ERR_DTYPE;
     if (i->numel() != h.n || i->storage_offset() != h.offset || !i->is_contiguous() ||
-        i->unsafe_storage().data() != h.memory)
+        !i->has_storage() || i->unsafe_storage().data() != h.memory)
       return TWELL_ERR_ARG;
   }
   return TWELL_OK;

@@ -652,8 +652,8 @@ struct Rounds {
 // What can be in a warp's tile: no sequence begins or ends there and all of its rows are
 // some sequence's (PLAIN); one at most begins and one ends in each lane's rows (EASY); anything;
 // no row of a sequence (DEAD).  Branches at the rows keep the rows' arithmetic from overlapping
-// (16384 x 2048 of 9 sequences forward 55 us, of 257 80), so what is easy has a selection a row
-// instead (50 and 72).  With a gate below OPEN, which shows when the gates are read, a tile
+// (in an earlier form 16384 x 2048 of 9 sequences forward 55 us, of 257 80), so what is easy has
+// a selection a row instead (50 and 72).  With a gate below OPEN, which shows when the gates are read, a tile
 // begins again as CLOSED: two or three selections a value, and branches at the rows.  This is a
 // loop over the rows, with their gates in local memory: as much code unrolled slows the others
 // down, whose own has to come from L2 when forward and backward alternate (us, loop | unrolled:
